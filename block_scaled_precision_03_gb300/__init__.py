@@ -12,6 +12,9 @@ Names follow the C ABI in ``include/bsq.h``:
     grouped_gemm(A, offsets, B, dtype)-> torch.Tensor  per-group A_g @ B_g^T
     mxfp4_to_mxfp8(q)                 -> QTensor
     sync_status()                     -> raises BsqError on a recorded device fault
+
+The operators around the layer (expert sort, layer norm, linear cross
+entropy, gradient clipping) are bound in ``ops.py`` and exported here.
 """
 from __future__ import annotations
 
@@ -77,6 +80,7 @@ def lib():
         "bsq_status_string": (ctypes.c_char_p, [i32]),
         "bsq_version": (ctypes.c_char_p, []),
     }
+    sig.update(_signatures())
     for name, (res, args) in sig.items():
         f = getattr(L, name)
         f.restype = res
@@ -350,3 +354,11 @@ def debug_gemm_timeout_into(A: QTensor, B: QTensor, C, timeout_ns: int, kernel: 
 
 def version() -> str:
     return lib().bsq_version().decode()
+
+
+from .ops import (GradList, MoePlan, _signatures, clip_grad_norm, clip_grad_norm_into, grad_norm,  # noqa: E402
+                  layer_norm, layer_norm_backward, layer_norm_backward_into, layer_norm_into, linear_cross_entropy,
+                  linear_cross_entropy_backward, linear_cross_entropy_backward_into, linear_cross_entropy_into,
+                  moe_combine, moe_combine_backward, moe_combine_backward_into, moe_combine_into, moe_dispatch,
+                  moe_dispatch_backward, moe_dispatch_into, moe_gather, moe_gather_into, moe_plan, moe_sort,
+                  moe_sort_into)

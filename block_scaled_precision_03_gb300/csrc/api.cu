@@ -134,6 +134,11 @@ bsq_status quantize_common(const void* src_bf16, int64_t rows, int64_t cols, int
 
 }  // namespace
 
+namespace bsq {
+int device_sms() { return num_sms(); }
+unsigned* device_status() { return status_ptr(); }
+}  // namespace bsq
+
 extern "C" {
 
 size_t bsq_codes_bytes(int32_t fmt, int64_t rows, int64_t cols) {

@@ -79,6 +79,100 @@ cudaError_t run_gemm(const GemmArgs& a, cudaStream_t st);
 cudaError_t run_gemm_pair(const GemmArgs& a, cudaStream_t st);
 bool gemm_pair_grouped_ok(const GemmArgs& a);
 
+// ---- tokens sorted by expert and back (moe.cu)
+struct MoePlanArgs {
+    int64_t tokens;
+    int k, num_experts;
+    int64_t* offsets;
+    int32_t* slot_row;
+    int32_t* row_slot;
+    int num_sms;
+};
+constexpr int kMoeMaxK = 256, kMoeMaxExperts = 1024;
+size_t moe_sort_workspace(int64_t tokens, int k, int num_experts);
+cudaError_t run_moe_sort(const MoePlanArgs& p, const void* ids, bool ids64, void* ws, cudaStream_t st);
+struct MoeRowsArgs {
+    const void* src;               // gather: x or dout [tokens, cols]; combine: rows [tokens * k, cols]
+    int64_t ld_src;
+    void* dst;
+    int64_t ld_dst;
+    int64_t cols;
+    int bf16;
+    const float* weights;          // nullptr: 1
+    const void* rows;              // combine gradient: the expert rows (nullptr: no dweights)
+    int64_t ld_rows;
+    float* dweights;
+};
+cudaError_t run_moe_gather(const MoePlanArgs& p, const MoeRowsArgs& a, cudaStream_t st);
+cudaError_t run_moe_combine(const MoePlanArgs& p, const MoeRowsArgs& a, cudaStream_t st);
+cudaError_t run_moe_combine_backward(const MoePlanArgs& p, const MoeRowsArgs& a, cudaStream_t st);
+
+// ---- layer norm (norm.cu)
+struct NormArgs {
+    const void* x;
+    int64_t ldx;
+    int bf16;
+    int64_t rows, cols;
+    const void* weight;
+    const void* bias;
+    int param_bf16;
+    float eps;
+    void* y;                       // forward: y; backward: dx
+    int64_t ldy;
+    float* mean;
+    float* rstd;
+    const void* dy;                // backward
+    int64_t ld_dy;
+    float* dweight;
+    float* dbias;
+    float* ws;
+    int num_sms;
+};
+size_t norm_workspace(int64_t rows, int64_t cols, int num_sms);
+cudaError_t run_layer_norm(const NormArgs& a, cudaStream_t st);
+cudaError_t run_layer_norm_backward(const NormArgs& a, cudaStream_t st);
+
+// ---- linear cross entropy (head.cu)
+struct HeadArgs {
+    const void* h;
+    int64_t ldh;
+    const void* w;
+    int64_t ldw;
+    const int64_t* targets;
+    int64_t tokens, vocab, cols;
+    float* loss;
+    float* lse;
+    const float* dloss;            // backward
+    void* dh;
+    int64_t ld_dh;
+    void* dw;
+    int64_t ld_dw;
+    void* ws;
+    int num_sms;
+    unsigned* status;
+    uint64_t timeout_ns;
+};
+size_t head_workspace(int64_t tokens, int64_t vocab, int64_t cols, bool backward, int num_sms);
+cudaError_t run_head(const HeadArgs& a, cudaStream_t st);
+cudaError_t run_head_backward(const HeadArgs& a, cudaStream_t st);
+
+// ---- global gradient norm and clipping (clip.cu)
+struct ClipArgs {
+    const void* grads;             // host array of bsq_grad
+    int count;
+    bool scale;                    // false: the norm only
+    float max_norm, eps;
+    float* norm;
+    double* ws;
+    int num_sms;
+};
+size_t clip_workspace(int count, int num_sms);
+cudaError_t run_clip(const ClipArgs& a, cudaStream_t st);
+
+// this device's SM count and status word (api.cu)
+int device_sms();
+unsigned* device_status();
+
 cudaError_t run_timeout_probe(unsigned* status, uint64_t limit_ns, cudaStream_t st);
 
 }  // namespace bsq

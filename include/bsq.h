@@ -21,6 +21,9 @@
  *    Hopper FP8 block of the same section), NVFP4 with delayed scaling
  *    from an amax history (FP8 page, "Estrategias de escalonamento"), and
  *    the GEMM on MXFP4 x MXFP4 operands natively.
+ *  - What a mixture-of-experts step runs next to it: tokens sorted by expert
+ *    and back, layer norm, the softmax cross entropy of a linear head and
+ *    the global gradient norm with clipping, each with its gradient.
  *
  * Conventions shared by every entry point
  *  - Matrices are row-major.  A GEMM computes C[M,N] = A[M,K] * B[N,K]^T:
@@ -254,6 +257,174 @@ bsq_status bsq_mxfp4_to_mxfp8_col(const bsq_tensor* in_mxfp4, bsq_tensor* out_e4
  * de Conversao Direta" (FP8 blocks of 128, the largest of four FP4 block
  * scales, exponents adjusted locally). */
 bsq_status bsq_mxfp4_to_fp8_1x128(const bsq_tensor* in_mxfp4, void* out_codes, void* out_scales, void* stream);
+
+/* ======================================================================
+ * Operators around the layer: what a mixture-of-experts training or serving
+ * step runs next to the GEMMs.  Conventions as above, and:
+ *  - A matrix is given by its first element, its type (bsq_out: FP32 or
+ *    BF16), its shape and `ld`, the distance between two rows in ELEMENTS
+ *    (ld >= cols; the last axis is contiguous).  Any ld and any address that
+ *    is a multiple of the element size is valid; rows that start on 16-byte
+ *    boundaries are faster.  The linear cross entropy asks for 16-byte rows.
+ *  - Inputs and outputs may not overlap unless a call says so.
+ *  - Sums, statistics and softmax terms are held in FP32 (the global norm in
+ *    FP64); a BF16 result is rounded once, at its store.  No result depends
+ *    on the order in which thread blocks run: the same inputs give the same
+ *    bits.
+ *  - A workspace is device memory, 16-byte aligned, of at least the size the
+ *    *_workspace_bytes function gives (0: none needed, NULL is valid).  Its
+ *    contents need no preparation and mean nothing after the call; two calls
+ *    that may run at the same time need one each.
+ * ====================================================================== */
+
+/* -- tokens sorted by expert and back --------------------------------- */
+
+typedef enum { BSQ_ID_I32 = 0, BSQ_ID_I64 = 1 } bsq_id_type;
+
+/* Where the k slots of each token go.  Slot i = t * k + j is token t's j-th
+ * expert; a slot whose id lies outside [0, num_experts) is left out (a
+ * padding token, or a token over its expert's capacity).  The others are
+ * sorted by expert, slots of one expert in slot order:
+ *   offsets[e]  = number of slots with an expert before e (DEVICE
+ *                 int64[num_experts + 1]; what bsq_grouped_gemm takes)
+ *   slot_row[i] = slot i's row in that order, -1 for a slot left out
+ *                 (DEVICE int32[tokens * k])
+ *   row_slot[r] = the slot in row r, -1 from row offsets[num_experts] on
+ *                 (DEVICE int32[tokens * k])
+ * All three arrays are the caller's.  1 <= k <= 256, 1 <= num_experts <=
+ * 1024, tokens * k < 2^31 - 256. */
+typedef struct {
+    int64_t tokens;
+    int32_t k;
+    int32_t num_experts;
+    int64_t* offsets;
+    int32_t* slot_row;
+    int32_t* row_slot;
+} bsq_moe_plan;
+
+/* Workspace of bsq_moe_sort and bsq_moe_dispatch (0 on bad sizes too). */
+size_t bsq_moe_workspace_bytes(int64_t tokens, int32_t k, int32_t num_experts);
+
+/* Fill `plan` from the expert ids [tokens, k] (DEVICE, contiguous). */
+bsq_status bsq_moe_sort(const void* expert_ids, int32_t id_type, const bsq_moe_plan* plan, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* bsq_moe_sort, then rows[r, :] = x[row_slot[r] / k, :] for every row of
+ * rows[tokens * k, cols]; rows that hold no slot are written as zeros. */
+bsq_status bsq_moe_dispatch(const void* x, int64_t ldx, int32_t type, int64_t cols, const void* expert_ids,
+                            int32_t id_type, const bsq_moe_plan* plan, void* rows, int64_t ld_rows, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* The gather of bsq_moe_dispatch with a plan that is already filled. */
+bsq_status bsq_moe_gather(const void* x, int64_t ldx, int32_t type, int64_t cols, const bsq_moe_plan* plan,
+                          void* rows, int64_t ld_rows, void* stream);
+
+/* out[t, :] = sum_j weights[t, j] * rows[slot_row[t, j], :], the sum over the
+ * slots that are not left out, in the order of j; 0 for a token that has
+ * none.  weights: DEVICE float[tokens, k], contiguous; NULL takes 1, which is
+ * the gradient of bsq_moe_dispatch and bsq_moe_gather.  A slot left out
+ * contributes nothing, whatever its weight. */
+bsq_status bsq_moe_combine(const void* rows, int64_t ld_rows, int32_t type, int64_t cols, const float* weights,
+                           const bsq_moe_plan* plan, void* out, int64_t ldo, void* stream);
+
+/* Gradient of bsq_moe_combine for dout[tokens, cols]:
+ *   drows[r, :]   = weights[slot] * dout[slot / k, :] with slot = row_slot[r]
+ *                   (0 in rows that hold no slot)
+ *   dweights[t,j] = dout[t, :] . rows[slot_row[t, j], :] (0 for a slot left
+ *                   out)
+ * dweights may be NULL (then rows is not read and may be NULL too). */
+bsq_status bsq_moe_combine_backward(const void* dout, int64_t ldd, const void* rows, int64_t ld_rows, int32_t type,
+                                    int64_t cols, const float* weights, const bsq_moe_plan* plan, void* drows,
+                                    int64_t ld_drows, float* dweights, void* stream);
+
+/* -- layer norm --------------------------------------------------------- */
+
+/* Per row of x[rows, cols]: mean = sum x / cols, var = sum (x - mean)^2 /
+ * cols, rstd = 1 / sqrt(var + eps), y = (x - mean) * rstd * weight + bias.
+ * weight, bias: DEVICE [cols] of `param_type` (bsq_out), either may be NULL
+ * (1, 0).  mean, rstd: DEVICE float[rows] for the backward pass, either may
+ * be NULL.  y has x's type and may be x itself (same pointer and ld).
+ * eps >= 0. */
+bsq_status bsq_layer_norm(const void* x, int64_t ldx, int32_t type, int64_t rows, int64_t cols, const void* weight,
+                          const void* bias, int32_t param_type, float eps, void* y, int64_t ldy, float* mean,
+                          float* rstd, void* stream);
+
+/* Workspace of bsq_layer_norm_backward (0 on bad sizes too). */
+size_t bsq_layer_norm_workspace_bytes(int64_t rows, int64_t cols);
+
+/* Gradient of bsq_layer_norm for dy[rows, cols] (dy, x and dx of one type),
+ * with xh = (x - mean) * rstd and g = dy * weight:
+ *   dx      = rstd * (g - sum(g) / cols - xh * sum(g * xh) / cols)
+ *   dweight = sum over the rows of dy * xh   (DEVICE float[cols])
+ *   dbias   = sum over the rows of dy        (DEVICE float[cols])
+ * dweight and dbias may each be NULL.  dx may be dy itself. */
+bsq_status bsq_layer_norm_backward(const void* dy, int64_t ld_dy, const void* x, int64_t ldx, int32_t type,
+                                   int64_t rows, int64_t cols, const void* weight, int32_t param_type,
+                                   const float* mean, const float* rstd, void* dx, int64_t ld_dx, float* dweight,
+                                   float* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
+/* -- softmax cross entropy of a linear head ----------------------------- */
+
+/* Workspace of bsq_linear_cross_entropy (backward = 0) and of
+ * bsq_linear_cross_entropy_backward (backward = 1); 0 on bad sizes. */
+size_t bsq_linear_cross_entropy_workspace_bytes(int64_t tokens, int64_t vocab, int64_t cols, int32_t backward);
+
+/* With logits z[t, v] = h[t, :] . w[v, :], which are never stored:
+ *   lse[t]  = log(sum_v exp(z[t, v]))
+ *   loss[t] = lse[t] - z[t, targets[t]], 0 where targets[t] lies outside
+ *             [0, vocab) (a token that does not count)
+ * h: BF16 [tokens, cols], w: BF16 [vocab, cols], both on 16-byte boundaries
+ * with cols, ldh and ldw multiples of 8 (BSQ_ERR_ALIGNMENT otherwise);
+ * targets: DEVICE int64[tokens]; loss, lse: DEVICE float[tokens].
+ * FP32 accumulation on the tensor cores.  tokens, vocab, cols up to
+ * 2^31 - 256. */
+bsq_status bsq_linear_cross_entropy(const void* h, int64_t ldh, const void* w, int64_t ldw, const int64_t* targets,
+                                    int64_t tokens, int64_t vocab, int64_t cols, float* loss, float* lse,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of sum_t dloss[t] * loss[t], with lse from the forward call and
+ * g[t, v] = dloss[t] * (exp(z[t, v] - lse[t]) - [v == targets[t]]), 0 for a
+ * token that does not count:
+ *   dh = g w  (BF16 [tokens, cols]),  dw = g^T h  (BF16 [vocab, cols])
+ * Either of dh, dw may be NULL (a frozen head, or frozen states).  The logits
+ * are computed again, a piece of the vocabulary at a time.  g enters the two
+ * products in BF16, with the largest |dloss| taken out of it and put back in
+ * FP32.  dh, dw on 16-byte boundaries, ld_dh and ld_dw multiples of 8;
+ * dloss: DEVICE float[tokens], finite. */
+bsq_status bsq_linear_cross_entropy_backward(const void* h, int64_t ldh, const void* w, int64_t ldw,
+                                             const int64_t* targets, int64_t tokens, int64_t vocab, int64_t cols,
+                                             const float* lse, const float* dloss, void* dh, int64_t ld_dh, void* dw,
+                                             int64_t ld_dw, void* workspace, size_t workspace_bytes, void* stream);
+
+/* -- global norm and clipping ------------------------------------------- */
+
+/* One gradient: n contiguous elements (0 is valid) of `type` (bsq_out) at
+ * `grad`, and where its clipped copy goes (`out`: same type and length; may
+ * be `grad` itself; ignored by bsq_grad_norm). */
+typedef struct {
+    const void* grad;
+    void* out;
+    int64_t n;
+    int32_t type;
+    int32_t reserved;          /* must be 0 */
+} bsq_grad;
+
+/* Workspace of the two calls below for `count` gradients. */
+size_t bsq_grad_workspace_bytes(int32_t count);
+
+/* norm[0] = sqrt(sum of the squares of all elements) (DEVICE float): squares
+ * and runs of at most 128 of them in FP32, the sum of the runs in FP64 (an
+ * element beyond 1.8e19 makes the norm infinite).  `grads` is a HOST array,
+ * read before the call returns; count <= 2^20, and at most 2^40 elements. */
+bsq_status bsq_grad_norm(const bsq_grad* grads, int32_t count, float* norm, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* bsq_grad_norm, then out = grad * min(1, max_norm / (norm + eps)) for every
+ * element, the factor and the product in FP32.  An infinite norm gives the
+ * factor 0 and a NaN norm makes every output NaN, as the formula says.
+ * max_norm >= 0, eps >= 0. */
+bsq_status bsq_clip_grad_norm(const bsq_grad* grads, int32_t count, float max_norm, float eps, float* norm,
+                              void* workspace, size_t workspace_bytes, void* stream);
 
 /* Take and clear the device status word (one atomic exchange on the
  * device, ordered after the work already on `stream`), synchronize
