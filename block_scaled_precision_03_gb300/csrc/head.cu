@@ -1,136 +1,508 @@
 // Softmax cross entropy of a linear head, without keeping the logits.
 //
 // z = h w^T (BF16 operands, FP32 accumulation).  Forward: each output tile
-// leaves, per row, its maximum m and s = sum exp(z - m) over its columns (the
-// target's logit beside it); a second kernel joins the tiles of a row,
+// leaves, per row and 128 columns, the maximum m and s = sum exp(z - m) (the
+// target's logit beside it); a second kernel joins a row's parts,
 //   lse = M + log sum_i s_i exp(m_i - M),  M = max_i m_i,
 // and loss = lse - z[target].  Backward, a piece of the vocabulary at a time:
 // the logits' tile again, g = ratio (exp(z - lse) - [v = target]) in BF16 with
 // ratio = dloss / max |dloss|, then dh += g w (FP32 between pieces) and
-// dw = g^T h, both times max |dloss| in FP32.
+// dw = g^T h, both times max |dloss| in FP32.  With the usual dloss (one value
+// for every token that counts) ratio is 1, so the one large entry of a row of
+// g, the target's, loses nothing to BF16.
+//
+// All four products run in one kernel on CTA pairs (tcgen05 cta_group::2,
+// M = N = 256, K = 16 per MMA): each CTA stages its own 128 rows of A and of
+// B by TMA (128-byte swizzle), the even CTA issues the MMAs, and two
+// accumulators of 256 tensor-memory columns let the epilogue of one tile run
+// under the MMAs of the next.  An operand is read in the layout it has in
+// memory: K-major (h and w for the logits, g for dh) or MN-major (w for dh; g
+// and h for dw), so nothing is transposed on the way.
 #include <algorithm>
+#include <cuda.h>
 #include "common.cuh"
+#include "epilogue.cuh"
 #include "internal.h"
+#include "tcgen05.cuh"
+#include "tmap.h"
 
 namespace bsq {
 namespace {
 
-constexpr int BM = 128, BN = 128, BK = 16, kThreads = 256;
 constexpr int64_t kPieceBytes = 256ll << 20;       // of g
 constexpr float kNegInf = -INFINITY;
+constexpr float kLog2e = 1.44269504088896340736f;
 
 enum { kStats, kGrad, kDh, kDw };
 
-// C(m, n) = sum_k A(m, k) B(n, k): an operand is K-major (k contiguous, ld
-// between rows) or MN-major (m or n contiguous, ld between k).
-struct TileArgs {
-    const __nv_bfloat16 *a, *b;
-    int64_t lda, ldb;
-    int64_t M, N, K;
+// ------------------------------------------------------------ the products
+constexpr int kTile = 256;                          // output rows and columns of a pair
+constexpr int kSubK = 64;                           // K of one 128-byte sub-step
+constexpr int kSub = 2;                             // sub-steps per stage
+constexpr int kStages = 3;
+constexpr int kSubBytes = 128 * kSubK * 2;          // one CTA's 128 rows of an operand, one sub-step
+constexpr int kOpBytes = kSub * kSubBytes;
+constexpr int kMmas = 4 * kSub;                     // per stage
+constexpr uint32_t kTx = 2 * kOpBytes;              // bytes one CTA loads per stage
+constexpr int kEpiWarps = 8;
+constexpr int kGemmThreads = 32 * (2 + kEpiWarps);
+constexpr uint32_t kTmemCols = 512;
+constexpr int kSmem = 1024 + kStages * 2 * kOpBytes + kEpiWarps * 2048 + 256;
+static_assert(kSmem <= 232448, "shared memory per block");
+constexpr int kRasterGroup = 8;
+constexpr int64_t kL2Resident = 48ll << 20;
+
+// MODE's operand layouts: K-major (false) or MN-major (true)
+__host__ __device__ constexpr bool a_mn(int mode) { return mode == kDw; }
+__host__ __device__ constexpr bool b_mn(int mode) { return mode == kDh || mode == kDw; }
+
+struct GemmParams {
+    int64_t M, N;                  // output
+    int32_t k_stages, mma_last;    // K stages in all; MMAs of the last one
+    int32_t m_tiles, n_tiles, splits, split_stages, total;
+    int32_t raster, raster_n;
     const int64_t* targets;
     int64_t vocab;
     int64_t col0;                  // first vocabulary column of the piece
-    float2* part;                  // kStats: [n tile][M] (max, sum)
-    float* hit;                    // kStats: target's logit
+    float2* part;                  // kStats: [128 columns][M] (max, sum)
+    float* hit;                    // kStats: the target's logit
     const float* lse;
     const float* dloss;
     const float* smax;
-    __nv_bfloat16* out;            // kGrad: g; kDw: dw
-    int64_t ldo;
-    float* acc;                    // kDh: [M][N]
-    int first;
+    int32_t add;                   // kDh: add to what is there
+    unsigned* status;
+    uint64_t timeout_ns;
 };
 
-template <int MODE, bool A_MN, bool B_MN>
-__global__ void __launch_bounds__(kThreads) head_tile_kernel(const TileArgs p) {
-    __shared__ float sa[BK][BM + 4], sb[BK][BN + 4];
-    const int64_t m0 = (int64_t)blockIdx.y * BM, n0 = (int64_t)blockIdx.x * BN;
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    float c[8][8] = {};
-    for (int64_t k0 = 0; k0 < p.K; k0 += BK) {
-        for (int i = tid; i < BM * BK; i += kThreads) {
-            const int k = A_MN ? i / BM : i % BK, m = A_MN ? i % BM : i / BK;
-            const bool in = m0 + m < p.M && k0 + k < p.K;
-            sa[k][m] = in ? __bfloat162float(A_MN ? p.a[(k0 + k) * p.lda + m0 + m] : p.a[(m0 + m) * p.lda + k0 + k]) : 0.0f;
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+// tcgen05 instruction descriptor of kind::f16: bits 4-5 FP32 accumulator,
+// 7-9 and 10-12 BF16 operands, 15 and 16 MN-major A and B, 17-22 N>>3,
+// 24-28 M>>4.
+__host__ __device__ constexpr uint32_t idesc_bf16(bool amn, bool bmn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((amn ? 1u : 0u) << 15) | ((bmn ? 1u : 0u) << 16) |
+           ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+}
+// Descriptor of an MN-major operand tile with 128-byte swizzle: rows of 64
+// contiguous M (or N) elements, one per k; 8 of them 1024 bytes apart, the
+// next 64 elements a box of 64 rows (8192 bytes) further.
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(8192 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+template <bool ADD>
+__device__ __forceinline__ void tma_store_3d(const void* tmap, int32_t x, int32_t y, int32_t z, uint32_t src) {
+    if (ADD)
+        asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
+                     :: "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(src) : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];"
+                     :: "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(src) : "memory");
+}
+
+// A warp's 32 rows x 128 FP32 columns into (or added to) the [split][M][N]
+// accumulator, 16 columns at a time through its 64-byte-swizzled staging
+// buffer (the layout of store_tile_tma).
+__device__ __forceinline__ void store_acc(const uint32_t (&r)[4][32], uint32_t buf, const void* tmap, int col0, int row0,
+                                          int split, bool add, int lane) {
+    const uint32_t row_base = buf + (uint32_t)lane * 64u;
+    const uint32_t sw = (uint32_t)((lane >> 1) & 3);
+#pragma unroll
+    for (int ch = 0; ch < 8; ch++) {
+        if (lane == 0) tc::bulk_wait_read();
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+            const int c = ch * 16 + u * 4;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                         :: "r"(row_base + ((u ^ sw) << 4)), "r"(r[c >> 5][c & 31]), "r"(r[c >> 5][(c & 31) + 1]),
+                            "r"(r[c >> 5][(c & 31) + 2]), "r"(r[c >> 5][(c & 31) + 3]) : "memory");
         }
-        for (int i = tid; i < BN * BK; i += kThreads) {
-            const int k = B_MN ? i / BN : i % BK, n = B_MN ? i % BN : i / BK;
-            const bool in = n0 + n < p.N && k0 + k < p.K;
-            sb[k][n] = in ? __bfloat162float(B_MN ? p.b[(k0 + k) * p.ldb + n0 + n] : p.b[(n0 + n) * p.ldb + k0 + k]) : 0.0f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < BK; k++) {
-            float x[8], y[8];
-#pragma unroll
-            for (int i = 0; i < 8; i++) x[i] = sa[k][ty * 8 + i];
-#pragma unroll
-            for (int j = 0; j < 8; j++) y[j] = sb[k][tx * 8 + j];
-#pragma unroll
-            for (int i = 0; i < 8; i++)
-#pragma unroll
-                for (int j = 0; j < 8; j++) c[i][j] = fmaf(x[i], y[j], c[i][j]);
-        }
-        __syncthreads();
-    }
-    const float smax = MODE == kStats ? 0.0f : *p.smax;
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const int64_t m = m0 + ty * 8 + i;
-        if (MODE == kStats) {
-            const int64_t target = m < p.M ? p.targets[m] : -1;
-            float mx = kNegInf;
-#pragma unroll
-            for (int j = 0; j < 8; j++) {
-                const int64_t n = n0 + tx * 8 + j;
-                if (n >= p.N) c[i][j] = kNegInf;
-                else if (n == target) p.hit[m] = c[i][j];
-                mx = fmaxf(mx, c[i][j]);
-            }
-#pragma unroll
-            for (int d = 8; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-            float s = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 8; j++) s += mx == kNegInf ? 0.0f : expf(c[i][j] - mx);
-#pragma unroll
-            for (int d = 8; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-            if (tx == 0 && m < p.M) p.part[(int64_t)blockIdx.x * p.M + m] = make_float2(mx, s);
-        } else if (m < p.M) {
-            float ratio = 0.0f, lse = 0.0f;
-            int64_t target = -1;
-            if (MODE == kGrad) {
-                target = p.targets[m];
-                lse = p.lse[m];
-                ratio = target >= 0 && target < p.vocab && smax > 0.0f ? p.dloss[m] / smax : 0.0f;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; j++) {
-                const int64_t n = n0 + tx * 8 + j;
-                if (n >= p.N) continue;
-                if (MODE == kGrad) {
-                    const float g = expf(c[i][j] - lse) - (p.col0 + n == target ? 1.0f : 0.0f);
-                    p.out[m * p.ldo + n] = __float2bfloat16_rn(ratio == 0.0f ? 0.0f : ratio * g);
-                } else if (MODE == kDh) {
-                    float* a = p.acc + m * p.N + n;
-                    *a = p.first ? c[i][j] : *a + c[i][j];
-                } else {
-                    p.out[m * p.ldo + n] = __float2bfloat16_rn(c[i][j] * smax);
-                }
-            }
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            if (add) tma_store_3d<true>(tmap, col0 + ch * 16, row0, split, buf);
+            else tma_store_3d<false>(tmap, col0 + ch * 16, row0, split, buf);
+            tc::bulk_commit();
         }
     }
 }
 
-__global__ void __launch_bounds__(256) head_join_kernel(const float2* part, int64_t parts, int64_t T, int64_t V,
+struct TileAt {
+    int mt, nt, split, k0, k1;
+};
+__device__ __forceinline__ TileAt tile_at(const GemmParams& p, int t) {
+    TileAt a;
+    const int per = p.m_tiles * p.n_tiles;
+    a.split = p.splits > 1 ? t / per : 0;
+    t -= a.split * per;
+    const int MT = p.raster_n ? p.n_tiles : p.m_tiles, NT = p.raster_n ? p.m_tiles : p.n_tiles;
+    const int g = t / (p.raster * NT);
+    const int first = g * p.raster;
+    const int gm = min(p.raster, MT - first);
+    const int local = t - g * p.raster * NT;
+    const int x = first + local % gm, y = local / gm;
+    a.mt = p.raster_n ? y : x;
+    a.nt = p.raster_n ? x : y;
+    a.k0 = a.split * p.split_stages;
+    a.k1 = min(p.k_stages, a.k0 + p.split_stages);
+    return a;
+}
+
+// After an abort: every stage load in flight lands before the pair exits.
+// Load k goes to stage k % kStages, phase (k / kStages) & 1, on the even CTA,
+// which arms each load with both CTAs' bytes; a load that only one CTA issued
+// gets the missing half of that accounting here.
+__device__ __noinline__ void drain_loads(uint32_t full0, int n_own, int n_peer) {
+    const int n = max(n_own, n_peer);
+    for (int k = max(0, n - kStages); k < n; k++) {
+        const uint32_t bar = full0 + 8 * (uint32_t)(k % kStages);
+        if (k < n_own && k >= n_peer) tc::mbar_complete_tx(bar, kTx);
+        if (k < n_peer && k >= n_own) tc::mbar_expect_tx(bar, kTx);
+        volatile int no_abort = 0;
+        tc::mbar_wait(bar, (uint32_t)((k / kStages) & 1), &no_abort, nullptr, 100000000ull);
+    }
+}
+
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
+head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                 const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ GemmParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* smA = base;
+    uint8_t* smB = smA + kStages * kOpBytes;
+    uint8_t* smOut = smB + kStages * kOpBytes;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smOut + kEpiWarps * 2048);
+    // full[S], empty[S], tfull[2], tempty[2], drain
+    const uint32_t full0 = tc::smem_u32(bars), empty0 = tc::smem_u32(bars + kStages);
+    const uint32_t tfull0 = tc::smem_u32(bars + 2 * kStages), tempty0 = tc::smem_u32(bars + 2 * kStages + 2);
+    const uint32_t drain = tc::smem_u32(bars + 2 * kStages + 4);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 5);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* issued_slot = reinterpret_cast<volatile int*>(tmem_slot + 2);
+    static_assert(8 * (2 * kStages + 5) + 12 <= 256, "barrier area");
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = tc::cluster_rank();
+    const bool leader = rank == 0;
+    const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < kStages; s++) {
+            tc::mbar_init(full0 + 8 * s, 1);
+            tc::mbar_init(empty0 + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; b++) {
+            tc::mbar_init(tfull0 + 8 * b, 1);
+            tc::mbar_init(tempty0 + 8 * b, 2 * kEpiWarps);
+        }
+        tc::mbar_init(drain, 1);
+        *abort_flag = 0;
+        *issued_slot = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        tc::prefetch_tmap(&tmA);
+        tc::prefetch_tmap(&tmB);
+    }
+    if (warp == 1) tc::tmem_alloc<2>(tc::smem_u32(tmem_slot), kTmemCols);
+    tc::fence_before();
+    __syncthreads();
+    tc::cluster_sync();
+    tc::fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer (both CTAs)
+        if (lane == 0) {
+            const uint32_t full_c0 = tc::mapa(full0, 0);
+            int stage = 0, issued = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int t = cid; t < p.total && ok; t += ncl) {
+                const TileAt ti = tile_at(p, t);
+                const int am = ti.mt * kTile + (int)rank * 128, bn = ti.nt * kTile + (int)rank * 128;
+                for (int kb = ti.k0; kb < ti.k1; kb++) {
+                    if (!tc::mbar_wait(empty0 + 8 * stage, phase ^ 1, abort_flag, p.status, p.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb = full_c0 + 8 * stage;
+                    if (leader) tc::mbar_expect_tx(full0 + 8 * stage, 2 * kTx);
+#pragma unroll
+                    for (int j = 0; j < kSub; j++) {
+                        const int k = (kb * kSub + j) * kSubK;
+                        const uint32_t da = tc::smem_u32(smA + stage * kOpBytes + j * kSubBytes);
+                        const uint32_t db = tc::smem_u32(smB + stage * kOpBytes + j * kSubBytes);
+                        if (a_mn(MODE)) {
+                            tc::tma_load_2d_pair(da, &tmA, am, k, fb);
+                            tc::tma_load_2d_pair(da + 8192, &tmA, am + 64, k, fb);
+                        } else {
+                            tc::tma_load_2d_pair(da, &tmA, k, am, fb);
+                        }
+                        if (b_mn(MODE)) {
+                            tc::tma_load_2d_pair(db, &tmB, bn, k, fb);
+                            tc::tma_load_2d_pair(db + 8192, &tmB, bn + 64, k, fb);
+                        } else {
+                            tc::tma_load_2d_pair(db, &tmB, k, bn, fb);
+                        }
+                    }
+                    ++issued;
+                    if (++stage == kStages) { stage = 0; phase ^= 1; }
+                }
+            }
+            *issued_slot = issued;
+            if (!ok) *abort_flag = 1;
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer (even CTA)
+        if (lane == 0 && leader) {
+            constexpr uint32_t idesc = idesc_bf16(a_mn(MODE), b_mn(MODE));
+            // 16 k further: 32 bytes of a K-major row, 16 rows of an MN-major tile
+            constexpr uint32_t a_step = a_mn(MODE) ? 2048 >> 4 : 2, b_step = b_mn(MODE) ? 2048 >> 4 : 2;
+            const uint64_t ad0 = a_mn(MODE) ? desc_mn_sw128(tc::smem_u32(smA)) : tc::desc_sw128(tc::smem_u32(smA));
+            const uint64_t bd0 = b_mn(MODE) ? desc_mn_sw128(tc::smem_u32(smB)) : tc::desc_sw128(tc::smem_u32(smB));
+            int stage = 0, iter = 0;
+            uint32_t phase = 0;
+            bool ok = true, any = false;
+            for (int t = cid; t < p.total && ok; t += ncl, ++iter) {
+                const TileAt ti = tile_at(p, t);
+                const int buf = iter & 1;
+                if (!tc::mbar_wait(tempty0 + 8 * buf, ((iter >> 1) & 1) ^ 1, abort_flag, p.status, p.timeout_ns)) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after();
+                const uint32_t d = tmem + (uint32_t)buf * kTile;
+                for (int kb = ti.k0; kb < ti.k1; kb++) {
+                    if (!tc::mbar_wait(full0 + 8 * stage, phase, abort_flag, p.status, p.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after();
+                    const uint64_t ad = ad0 + (uint64_t)(stage * (kOpBytes >> 4));
+                    const uint64_t bd = bd0 + (uint64_t)(stage * (kOpBytes >> 4));
+                    const int nk = kb == p.k_stages - 1 ? p.mma_last : kMmas;
+#pragma unroll
+                    for (int m = 0; m < kMmas; m++)
+                        if (m < nk)
+                            mma_bf16(d, ad + (m >> 2) * (kSubBytes >> 4) + (m & 3) * a_step,
+                                     bd + (m >> 2) * (kSubBytes >> 4) + (m & 3) * b_step, idesc, (kb != ti.k0) | (m != 0));
+                    any = true;
+                    tc::commit<2>(empty0 + 8 * stage, 3);
+                    if (kb == ti.k1 - 1) tc::commit<2>(tfull0 + 8 * buf, 3);
+                    if (++stage == kStages) { stage = 0; phase ^= 1; }
+                }
+            }
+            if (!ok) *abort_flag = 1;
+            if (any) {
+                // every MMA issued finishes before tensor memory is released
+                tc::commit<2>(drain, 1);
+                volatile int no_abort = 0;
+                tc::mbar_wait(drain, 0, &no_abort, nullptr, 100000000ull);
+            }
+        }
+    } else {
+        // ------------------------------------------------ epilogue (both CTAs)
+        // A thread owns one row and 128 of the tile's columns.
+        const int q = warp & 3, half = (warp - 2) >> 2;
+        const uint32_t tempty_c0 = tc::mapa(tempty0, 0);
+        const uint32_t stage_buf = tc::smem_u32(smOut + (warp - 2) * 2048);
+        const float smax = MODE == kGrad || MODE == kDw ? *p.smax : 1.0f;
+        int iter = 0;
+        for (int t = cid; t < p.total; t += ncl, ++iter) {
+            const TileAt ti = tile_at(p, t);
+            const int buf = iter & 1;
+            const int64_t row0 = (int64_t)ti.mt * kTile + rank * 128 + q * 32, row = row0 + lane;
+            const int64_t col0 = (int64_t)ti.nt * kTile + half * 128;
+            // what the row needs, read while the tile is computed
+            int64_t target = -1;
+            float lse = 0.0f, ratio = 0.0f;
+            if ((MODE == kStats || MODE == kGrad) && row < p.M) {
+                target = p.targets[row];
+                if (MODE == kGrad && target >= 0 && target < p.vocab && smax > 0.0f) {
+                    lse = p.lse[row];
+                    ratio = p.dloss[row] / smax;
+                }
+                target -= p.col0 + col0;
+            }
+            if (!tc::mbar_wait(tfull0 + 8 * buf, (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns)) break;
+            tc::fence_after();
+            uint32_t r[4][32];
+            const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kTile + half * 128);
+            BSQ_TMEM_LD32(r[0], ta);
+            BSQ_TMEM_LD32(r[1], ta + 32);
+            BSQ_TMEM_LD32(r[2], ta + 64);
+            BSQ_TMEM_LD32(r[3], ta + 96);
+            tc::tmem_wait_ld();
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_cluster(tempty_c0 + 8 * buf);
+            if (row0 >= p.M || col0 >= p.N) continue;
+            const bool here = target >= 0 && target < 128;
+            if (MODE == kStats) {
+                const int live = (int)min((int64_t)128, p.N - col0);
+                if (live < 128)
+#pragma unroll
+                    for (int j = 0; j < 128; j++)
+                        if (j >= live) r[j >> 5][j & 31] = __float_as_uint(kNegInf);
+                float m = kNegInf;
+#pragma unroll
+                for (int j = 0; j < 128; j++) m = fmaxf(m, __uint_as_float(r[j >> 5][j & 31]));
+                if (__any_sync(0xffffffffu, here)) {
+                    float hit = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 128; j++)
+                        if ((int)target == j) hit = __uint_as_float(r[j >> 5][j & 31]);
+                    if (here && row < p.M && target < live) p.hit[row] = hit;
+                }
+                // z - m is formed first: a product with log2(e) before it would round away the
+                // difference of large logits
+                const float m0 = m == kNegInf ? 0.0f : m;
+                float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int j = 0; j < 128; j++)
+                    s[j & 3] += exp2_fast((__uint_as_float(r[j >> 5][j & 31]) - m0) * kLog2e);
+                if (row < p.M) p.part[(col0 >> 7) * p.M + row] = make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
+            } else if (MODE == kGrad) {
+                // ratio 0 (a token that does not count) gives 0 whatever its logits
+                const bool zero = ratio == 0.0f;
+#pragma unroll
+                for (int j = 0; j < 128; j++) {
+                    float g = exp2_fast((__uint_as_float(r[j >> 5][j & 31]) - lse) * kLog2e);
+                    if ((int)target == j && here) g -= 1.0f;
+                    r[j >> 5][j & 31] = zero ? 0u : __float_as_uint(g);
+                }
+                store_tile_tma<true>(r, stage_buf, &tmOut, (int)col0, (int)row0, ratio, 1.0f, lane);
+            } else if (MODE == kDh) {
+                store_acc(r, stage_buf, &tmOut, (int)col0, (int)row0, ti.split, p.add != 0, lane);
+            } else {
+                store_tile_tma<true>(r, stage_buf, &tmOut, (int)col0, (int)row0, smax, 1.0f, lane);
+            }
+        }
+        if (lane == 0) tc::bulk_wait_all();
+    }
+
+    // Both CTAs have stopped issuing; if either gave up, the even CTA waits
+    // (bounded) for the loads still in flight before either may exit.
+    tc::fence_before();
+    __syncthreads();
+    tc::cluster_sync();
+    if (leader && warp == 0 && lane == 0) {
+        const int peer_abort = tc::ld_cluster_s32(tc::mapa(tc::smem_u32((const void*)abort_flag), 1));
+        if (*abort_flag || peer_abort)
+            drain_loads(full0, *issued_slot, tc::ld_cluster_s32(tc::mapa(tc::smem_u32((const void*)issued_slot), 1)));
+    }
+    tc::cluster_sync();
+    if (warp == 1) {
+        tc::fence_after();
+        tc::tmem_dealloc<2>(tmem, kTmemCols);
+    }
+}
+
+// BF16 matrix [rows, cols] with pitch ld, box 64 columns x box_rows, 128-byte
+// swizzle; elements outside read as zero.
+bool map_operand(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t ld, uint32_t box_rows) {
+    tmap::EncodeTiledFn enc = tmap::encoder();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)(ld * 2)};
+    cuuint32_t box[2] = {64u, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// FP32 accumulator [splits][rows][cols], box 16 columns x 32 rows, 64-byte swizzle
+bool map_acc(CUtensorMap* m, float* p, int64_t splits, int64_t rows, int64_t cols) {
+    tmap::EncodeTiledFn enc = tmap::encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)splits};
+    cuuint64_t strides[2] = {(cuuint64_t)(cols * 4), (cuuint64_t)(rows * cols * 4)};
+    cuuint32_t box[3] = {16u, 32u, 1u};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// One operand of a product: its matrix in memory ([rows, cols], pitch ld)
+struct Operand {
+    const void* p;
+    int64_t rows, cols, ld;
+};
+
+template <int MODE>
+cudaError_t gemm(GemmParams p, const Operand& a, const Operand& b, const CUtensorMap* out, int64_t K, int splits,
+                 const HeadArgs& args, cudaStream_t st) {
+    CUtensorMap ta, tb;
+    if (!map_operand(&ta, a.p, a.rows, a.cols, a.ld, a_mn(MODE) ? kSubK : 128) ||
+        !map_operand(&tb, b.p, b.rows, b.cols, b.ld, b_mn(MODE) ? kSubK : 128))
+        return cudaErrorInvalidValue;
+    p.k_stages = (int32_t)((K + kSub * kSubK - 1) / (kSub * kSubK));
+    p.mma_last = (int32_t)((K - (int64_t)(p.k_stages - 1) * kSub * kSubK + 15) / 16);
+    p.m_tiles = (int32_t)((p.M + kTile - 1) / kTile);
+    p.n_tiles = (int32_t)((p.N + kTile - 1) / kTile);
+    p.split_stages = (p.k_stages + splits - 1) / splits;
+    p.splits = (p.k_stages + p.split_stages - 1) / p.split_stages;
+    const int64_t total = (int64_t)p.m_tiles * p.n_tiles * p.splits;
+    if (total > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    p.total = (int32_t)total;
+    // one operand stays in L2 while the other streams past it once, where it fits
+    p.raster = kRasterGroup;
+    p.raster_n = 0;
+    const int64_t a_bytes = p.M * K * 2, b_bytes = p.N * K * 2;
+    if (std::min(a_bytes, b_bytes) <= kL2Resident) {
+        p.raster_n = b_bytes < a_bytes;
+        p.raster = p.raster_n ? p.n_tiles : p.m_tiles;
+    }
+    p.status = args.status;
+    p.timeout_ns = args.timeout_ns;
+    static bool attr_done = false;
+    if (!attr_done) {
+        cudaError_t e = cudaFuncSetAttribute(head_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        attr_done = true;
+    }
+    const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(args.num_sms / 2, total));
+    head_gemm_kernel<MODE><<<2 * pairs, kGemmThreads, kSmem, st>>>(ta, tb, out ? *out : ta, p);
+    return cudaGetLastError();
+}
+
+// ------------------------------------------------------- around the products
+// Joins a row's parts: TT tokens a CTA, the parts dealt to 512 / TT threads
+// each, whose results meet in shared memory in a fixed order.
+template <int TT>
+__global__ void __launch_bounds__(512) head_join_kernel(const float2* part, int64_t parts, int64_t T, int64_t V,
                                                         const float* hit, const int64_t* targets, float* loss,
                                                         float* lse) {
-    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (t >= T) return;
+    constexpr int G = 512 / TT;
+    __shared__ float2 joined[G][TT];
+    const int tt = threadIdx.x % TT, g = threadIdx.x / TT;
+    const int64_t t = (int64_t)blockIdx.x * TT + tt;
     float m = kNegInf, s = 0.0f;
-    for (int64_t i = 0; i < parts; i++) {
-        const float2 v = part[i * T + t];
+    if (t < T) {
+#pragma unroll 4
+        for (int64_t i = g; i < parts; i += G) {
+            const float2 v = part[i * T + t];
+            const float n = fmaxf(m, v.x);
+            if (n != kNegInf) s = s * exp2_fast((m - n) * kLog2e) + v.y * exp2_fast((v.x - n) * kLog2e);
+            m = n;
+        }
+    }
+    joined[g][tt] = make_float2(m, s);
+    __syncthreads();
+    if (g != 0 || t >= T) return;
+    for (int i = 1; i < G; i++) {
+        const float2 v = joined[i][tt];
         const float n = fmaxf(m, v.x);
-        if (n != kNegInf) s = s * expf(m - n) + v.y * expf(v.x - n);
+        if (n != kNegInf) s = s * exp2_fast((m - n) * kLog2e) + v.y * exp2_fast((v.x - n) * kLog2e);
         m = n;
     }
     const float l = m + logf(s);
@@ -156,104 +528,119 @@ __global__ void __launch_bounds__(1024) head_scale_kernel(const float* dloss, co
     }
 }
 
-__global__ void __launch_bounds__(256) head_dh_kernel(const float* acc, int64_t T, int64_t D, const float* smax,
-                                                      __nv_bfloat16* dh, int64_t ld) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i < T * D) dh[i / D * ld + i % D] = __float2bfloat16_rn(acc[i] * *smax);
+// dh = smax * the sum of the splits' accumulators, 8 columns a thread
+__global__ void __launch_bounds__(256) head_dh_kernel(const float* acc, int splits, int64_t T, int64_t D,
+                                                      const float* smax, __nv_bfloat16* dh, int64_t ld) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, per = D / 8;
+    if (i >= T * per) return;
+    const int64_t t = i / per, c = (i - t * per) * 8;
+    float v[8] = {};
+    for (int s = 0; s < splits; s++) {
+        const float4* a = reinterpret_cast<const float4*>(acc + ((int64_t)s * T + t) * D + c);
+        const float4 x = a[0], y = a[1];
+        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+    }
+    const float f = *smax;
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+        w[j] = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(v[2 * j] * f)) |
+               ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(v[2 * j + 1] * f)) << 16);
+    *reinterpret_cast<uint4*>(dh + t * ld + c) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
 // columns of one piece of the vocabulary
 int64_t piece_cols(int64_t tokens, int64_t vocab) {
-    const int64_t most = std::max<int64_t>(2048, kPieceBytes / (2 * tokens) / 256 * 256);
-    return std::min(round_up(vocab, 256), most);
+    const int64_t most = std::max<int64_t>(2048, kPieceBytes / (2 * tokens) / kTile * kTile);
+    return std::min(round_up(vocab, kTile), most);
+}
+// dh has few tiles when there are few tokens: its sum over the vocabulary is
+// then split over the idle pairs, at least 8 stages each
+int dh_splits(int64_t tokens, int64_t cols, int64_t piece, int num_sms) {
+    const int64_t tiles = (tokens + kTile - 1) / kTile * ((cols + kTile - 1) / kTile);
+    const int64_t stages = (piece + kSub * kSubK - 1) / (kSub * kSubK);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(num_sms / 2 / tiles, stages / 8));
 }
 
 }  // namespace
 
-size_t head_workspace(int64_t tokens, int64_t vocab, int64_t cols, bool backward, int) {
-    if (!backward) return (size_t)(round_up(vocab, BN) / BN * tokens * 8 + round_up(tokens * 4, 16));
-    return (size_t)(16 + round_up(tokens * piece_cols(tokens, vocab) * 2, 16) + tokens * cols * 4);
+size_t head_workspace(int64_t tokens, int64_t vocab, int64_t cols, bool backward, int num_sms) {
+    if (!backward) return (size_t)((vocab + 127) / 128 * tokens * 8 + round_up(tokens * 4, 16));
+    const int64_t piece = piece_cols(tokens, vocab);
+    return (size_t)(256 + tokens * piece * 2 + dh_splits(tokens, cols, piece, num_sms) * tokens * cols * 4);
 }
 
 cudaError_t run_head(const HeadArgs& a, cudaStream_t st) {
-    const int64_t parts = round_up(a.vocab, BN) / BN;
-    TileArgs p{};
-    p.a = static_cast<const __nv_bfloat16*>(a.h);
-    p.b = static_cast<const __nv_bfloat16*>(a.w);
-    p.lda = a.ldh;
-    p.ldb = a.ldw;
-    p.M = a.tokens;
+    const int64_t T = a.tokens, parts = (a.vocab + 127) / 128;
+    GemmParams p{};
+    p.M = T;
     p.N = a.vocab;
-    p.K = a.cols;
     p.targets = a.targets;
+    p.vocab = a.vocab;
     p.part = static_cast<float2*>(a.ws);
-    p.hit = reinterpret_cast<float*>(p.part + parts * a.tokens);
-    const dim3 grid((unsigned)parts, (unsigned)((a.tokens + BM - 1) / BM));
-    head_tile_kernel<kStats, false, false><<<grid, kThreads, 0, st>>>(p);
-    head_join_kernel<<<(unsigned)((a.tokens + 255) / 256), 256, 0, st>>>(p.part, parts, a.tokens, a.vocab, p.hit,
-                                                                         a.targets, a.loss, a.lse);
+    p.hit = reinterpret_cast<float*>(p.part + parts * T);
+    cudaError_t e = gemm<kStats>(p, {a.h, T, a.cols, a.ldh}, {a.w, a.vocab, a.cols, a.ldw}, nullptr, a.cols, 1, a, st);
+    if (e != cudaSuccess) return e;
+    if (T >= 4096)
+        head_join_kernel<32><<<(unsigned)((T + 31) / 32), 512, 0, st>>>(p.part, parts, T, a.vocab, p.hit, a.targets,
+                                                                       a.loss, a.lse);
+    else
+        head_join_kernel<8><<<(unsigned)((T + 7) / 8), 512, 0, st>>>(p.part, parts, T, a.vocab, p.hit, a.targets,
+                                                                     a.loss, a.lse);
     return cudaGetLastError();
 }
 
 cudaError_t run_head_backward(const HeadArgs& a, cudaStream_t st) {
     const int64_t T = a.tokens, V = a.vocab, D = a.cols, piece = piece_cols(T, V);
+    const int splits = dh_splits(T, D, piece, a.num_sms);
     uint8_t* ws = static_cast<uint8_t*>(a.ws);
     float* smax = reinterpret_cast<float*>(ws);
-    __nv_bfloat16* g = reinterpret_cast<__nv_bfloat16*>(ws + 16);
-    float* acc = reinterpret_cast<float*>(ws + 16 + round_up(T * piece * 2, 16));
+    uint8_t* g = ws + 256;
+    float* acc = reinterpret_cast<float*>(g + T * piece * 2);
     head_scale_kernel<<<1, 1024, 0, st>>>(a.dloss, a.targets, T, V, smax);
-    const __nv_bfloat16* h = static_cast<const __nv_bfloat16*>(a.h);
-    const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(a.w);
-    const unsigned mt = (unsigned)((T + BM - 1) / BM), dt = (unsigned)((D + BN - 1) / BN);
-    for (int64_t v0 = 0; v0 < V; v0 += piece) {
+    cudaError_t e = cudaGetLastError();
+    int used = 1;
+    for (int64_t v0 = 0; v0 < V && e == cudaSuccess; v0 += piece) {
         const int64_t n = std::min(piece, V - v0);
-        TileArgs p{};
+        const uint8_t* w = static_cast<const uint8_t*>(a.w) + v0 * a.ldw * 2;
+        GemmParams p{};
         p.targets = a.targets;
         p.vocab = V;
+        p.col0 = v0;
         p.lse = a.lse;
         p.dloss = a.dloss;
         p.smax = smax;
-        p.col0 = v0;
-        p.a = h;
-        p.lda = a.ldh;
-        p.b = w + v0 * a.ldw;
-        p.ldb = a.ldw;
         p.M = T;
         p.N = n;
-        p.K = D;
-        p.out = g;
-        p.ldo = piece;
-        head_tile_kernel<kGrad, false, false><<<dim3((unsigned)((n + BN - 1) / BN), mt), kThreads, 0, st>>>(p);
-        if (a.dh) {
-            TileArgs q = p;
-            q.a = g;
-            q.lda = piece;
-            q.N = D;
-            q.K = n;
-            q.acc = acc;
-            q.first = v0 == 0;
-            head_tile_kernel<kDh, false, true><<<dim3(dt, mt), kThreads, 0, st>>>(q);
+        CUtensorMap out;
+        if (!tmap::out_2d(&out, g, T, n, piece, true)) return cudaErrorInvalidValue;
+        e = gemm<kGrad>(p, {a.h, T, D, a.ldh}, {w, n, D, a.ldw}, &out, D, 1, a, st);
+        if (e == cudaSuccess && a.dh) {
+            p.M = T;
+            p.N = D;
+            p.add = v0 > 0;
+            if (!map_acc(&out, acc, splits, T, D)) return cudaErrorInvalidValue;
+            e = gemm<kDh>(p, {g, T, n, piece}, {w, n, D, a.ldw}, &out, n, splits, a, st);
+            const int stages = (int)((n + kSub * kSubK - 1) / (kSub * kSubK)), per = (stages + splits - 1) / splits;
+            if (v0 == 0) used = (stages + per - 1) / per;          // the splits that the first piece wrote
         }
-        if (a.dw) {
-            TileArgs q = p;
-            q.a = g;
-            q.lda = piece;
-            q.b = h;
-            q.ldb = a.ldh;
-            q.M = n;
-            q.N = D;
-            q.K = T;
-            q.out = static_cast<__nv_bfloat16*>(a.dw) + v0 * a.ld_dw;
-            q.ldo = a.ld_dw;
-            head_tile_kernel<kDw, true, true><<<dim3(dt, (unsigned)((n + BM - 1) / BM)), kThreads, 0, st>>>(q);
+        if (e == cudaSuccess && a.dw) {
+            p.M = n;
+            p.N = D;
+            if (!tmap::out_2d(&out, static_cast<uint8_t*>(a.dw) + v0 * a.ld_dw * 2, n, D, a.ld_dw, true))
+                return cudaErrorInvalidValue;
+            e = gemm<kDw>(p, {g, T, n, piece}, {a.h, T, D, a.ldh}, &out, T, 1, a, st);
         }
     }
-    if (a.dh)
-        head_dh_kernel<<<(unsigned)((T * D + 255) / 256), 256, 0, st>>>(acc, T, D, smax,
-                                                                         static_cast<__nv_bfloat16*>(a.dh), a.ld_dh);
-    return cudaGetLastError();
+    if (e == cudaSuccess && a.dh) {
+        head_dh_kernel<<<(unsigned)((T * (D / 8) + 255) / 256), 256, 0, st>>>(acc, used, T, D, smax,
+                                                                              static_cast<__nv_bfloat16*>(a.dh), a.ld_dh);
+        e = cudaGetLastError();
+    }
+    return e;
 }
 
 }  // namespace bsq
