@@ -157,9 +157,8 @@ bsq_status bsq_moe_dispatch(const void* x, int64_t ldx, int32_t type, int64_t co
     if ((s = check_plan(plan, p)) != BSQ_OK) return s;
     s = check_workspace(workspace, workspace_bytes, bsq::moe_sort_workspace(p.tokens, p.k, p.num_experts));
     if (s != BSQ_OK) return s;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    s = from_cuda(bsq::run_moe_sort(p, expert_ids, id_type == BSQ_ID_I64, workspace, st));
-    return s != BSQ_OK ? s : from_cuda(bsq::run_moe_gather(p, r, st));
+    return from_cuda(bsq::run_moe_dispatch(p, r, expert_ids, id_type == BSQ_ID_I64, workspace,
+                                           static_cast<cudaStream_t>(stream)));
 }
 
 bsq_status bsq_moe_gather(const void* x, int64_t ldx, int32_t type, int64_t cols, const bsq_moe_plan* plan,

@@ -103,6 +103,8 @@ struct MoeRowsArgs {
     int64_t ld_rows;
     float* dweights;
 };
+cudaError_t run_moe_dispatch(const MoePlanArgs& p, const MoeRowsArgs& a, const void* ids, bool ids64, void* ws,
+                             cudaStream_t st);
 cudaError_t run_moe_gather(const MoePlanArgs& p, const MoeRowsArgs& a, cudaStream_t st);
 cudaError_t run_moe_combine(const MoePlanArgs& p, const MoeRowsArgs& a, cudaStream_t st);
 cudaError_t run_moe_combine_backward(const MoePlanArgs& p, const MoeRowsArgs& a, cudaStream_t st);

@@ -1,0 +1,95 @@
+// Programmatic dependent launch and 16-byte vector access, shared by the
+// operators around the layer.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+namespace bsq {
+
+// A kernel launched with launch_k(true, ...) may start while the kernel before
+// it on the stream still runs.  Such a kernel calls pdl_wait() before its
+// first access to global memory; the kernel before it may let it start early
+// with pdl_launch_dependents().
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+inline cudaError_t launch_k(bool dependent, void (*k)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st,
+                            A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = dependent ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, k, static_cast<P>(args)...);
+}
+
+// N elements of T held packed, as they lie in memory (16 bytes, or one element)
+template <typename T, int N>
+struct Pack;
+template <>
+struct Pack<__nv_bfloat16, 8> {
+    uint4 v;
+    __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = v; }
+    __device__ __forceinline__ void unpack(float (&f)[8]) const {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+    __device__ __forceinline__ void pack(const float (&f)[8]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        v = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+template <>
+struct Pack<float, 4> {
+    float4 v;
+    __device__ __forceinline__ void zero() { v = make_float4(0, 0, 0, 0); }
+    __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
+    __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float4*>(p) = v; }
+    __device__ __forceinline__ void unpack(float (&f)[4]) const { f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w; }
+    __device__ __forceinline__ void pack(const float (&f)[4]) { v = make_float4(f[0], f[1], f[2], f[3]); }
+};
+template <>
+struct Pack<__nv_bfloat16, 1> {
+    __nv_bfloat16 v;
+    __device__ __forceinline__ void zero() { v = __ushort_as_bfloat16(0); }
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *p; }
+    __device__ __forceinline__ void store(__nv_bfloat16* p) const { *p = v; }
+    __device__ __forceinline__ void unpack(float (&f)[1]) const { f[0] = __bfloat162float(v); }
+    __device__ __forceinline__ void pack(const float (&f)[1]) { v = __float2bfloat16_rn(f[0]); }
+};
+template <>
+struct Pack<float, 1> {
+    float v;
+    __device__ __forceinline__ void zero() { v = 0.0f; }
+    __device__ __forceinline__ void load(const float* p) { v = *p; }
+    __device__ __forceinline__ void store(float* p) const { *p = v; }
+    __device__ __forceinline__ void unpack(float (&f)[1]) const { f[0] = v; }
+    __device__ __forceinline__ void pack(const float (&f)[1]) { v = f[0]; }
+};
+template <typename T>
+constexpr int kVec = 16 / (int)sizeof(T);
+
+// rows of a matrix start on 16-byte boundaries and hold whole vectors
+inline bool rows_vec(const void* p, int64_t ld, int64_t cols, int bytes) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld * bytes % 16 == 0 && cols * bytes % 16 == 0;
+}
+
+}  // namespace bsq

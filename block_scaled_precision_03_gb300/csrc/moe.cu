@@ -5,12 +5,22 @@
 //   offsets[e]  = number of valid slots with an id below e
 //   slot_row[i] = offsets[id_i] + number of valid slots before i with id_i
 //   row_slot    = its inverse, -1 past the last row that holds a slot
-// The gather copies each token's row to its slots' rows; the combine sums a
-// token's expert rows with its routing weights (the gather's gradient with
-// weights 1); the combine's gradient scales dout into the expert rows and
-// takes one dot product per slot.
+// Slots are placed kSortThreads at a time: lanes of a warp with the same id
+// find their rank with one match, the warps' counts per expert are summed in
+// warp order, so no atomic decides an order.  Up to kSortThreads slots (a
+// decoding step) every CTA of the gather sorts them by itself and the whole
+// dispatch is one launch; above that a count kernel and a place kernel run
+// first, each the programmatic dependent of the one before.
+//
+// The row movements are bound by memory: the gather reads a token's row once
+// and writes it to its k rows, the combine reads the k rows and writes one,
+// the combine's gradient reads dout and the k rows and writes k rows and k dot
+// products.  A group of 1 to 8 warps owns a token; rows on 16-byte boundaries
+// move in 16-byte vectors, others element by element, several in flight.
+#include <algorithm>
 #include "common.cuh"
 #include "internal.h"
+#include "launch.cuh"
 
 namespace bsq {
 namespace {
@@ -19,228 +29,556 @@ constexpr int kSortThreads = 1024;     // slots per step: one per thread
 
 // Slots of one CTA: whole steps, so that at most kSortCtas CTAs cover them.
 constexpr int kSortCtas = 128;
-__host__ __device__ inline int64_t sort_chunk(int64_t slots) {
+inline int64_t sort_chunk(int64_t slots) {
     const int64_t steps = (slots + kSortThreads - 1) / kSortThreads;
     return (steps + kSortCtas - 1) / kSortCtas * kSortThreads;
 }
 
-__device__ __forceinline__ int load_id(const void* ids, bool ids64, int64_t i, int experts) {
-    const int64_t id = ids64 ? static_cast<const int64_t*>(ids)[i] : static_cast<const int32_t*>(ids)[i];
-    return id >= 0 && id < experts ? (int)id : -1;
+struct SortArgs {
+    const void* ids;
+    int64_t slots, chunk;
+    int ids64, experts, chunks;
+    int32_t* counts;               // [chunks][experts]
+    int64_t* offsets;
+    int32_t* slot_row;
+    int32_t* row_slot;
+};
+
+__device__ __forceinline__ int load_id(const SortArgs& a, int64_t i) {
+    const int64_t id = a.ids64 ? static_cast<const int64_t*>(a.ids)[i] : static_cast<const int32_t*>(a.ids)[i];
+    return id >= 0 && id < a.experts ? (int)id : -1;
+}
+
+// Exclusive scan over the threads of a CTA of kSortThreads; `all` is the sum.
+__device__ __forceinline__ int32_t block_scan(int32_t v, int32_t& all) {
+    __shared__ int32_t warp_sum[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int32_t s = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int32_t u = __shfl_up_sync(0xffffffffu, s, d);
+        if (lane >= d) s += u;
+    }
+    if (lane == 31) warp_sum[warp] = s;
+    __syncthreads();
+    int32_t w = warp_sum[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int32_t u = __shfl_up_sync(0xffffffffu, w, d);
+        if (lane >= d) w += u;
+    }
+    all = __shfl_sync(0xffffffffu, w, 31);
+    const int32_t before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+    return s - v + (warp > 0 ? before : 0);
+}
+
+// One step: this thread's slot (expert e, -1 for none).  wcount[warps][experts]
+// receives, per warp, the slots of each expert in the warps before it; returns
+// the slot's rank in its warp.  `sum` (thread x < experts): the step's slots of
+// expert x.  Ends with the counts visible to the CTA.
+__device__ __forceinline__ int step_ranks(int e, int experts, int warps, uint16_t* wcount, int32_t& sum) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int x = tid; x < warps * experts; x += kSortThreads) wcount[x] = 0;
+    __syncthreads();
+    const unsigned same = __match_any_sync(0xffffffffu, e);
+    const int rank = __popc(same & ((1u << lane) - 1));
+    if (e >= 0 && rank == 0) wcount[warp * experts + e] = (uint16_t)__popc(same);
+    __syncthreads();
+    sum = 0;
+    if (tid < experts)
+        for (int w = 0; w < warps; w++) {
+            const int n = wcount[w * experts + tid];
+            wcount[w * experts + tid] = (uint16_t)sum;
+            sum += n;
+        }
+    return rank;
 }
 
 // counts[b][e]: valid slots of chunk b with expert e
-__global__ void __launch_bounds__(kSortThreads) moe_count_kernel(const void* ids, bool ids64, int64_t slots,
-                                                                 int64_t chunk, int experts, int32_t* counts) {
-    extern __shared__ int32_t hist[];
-    for (int e = threadIdx.x; e < experts; e += kSortThreads) hist[e] = 0;
-    __syncthreads();
-    const int64_t lo = blockIdx.x * chunk, hi = min(slots, lo + chunk);
-    for (int64_t i = lo + threadIdx.x; i < hi; i += kSortThreads) {
-        const int e = load_id(ids, ids64, i, experts);
-        if (e >= 0) atomicAdd(&hist[e], 1);
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e < experts; e += kSortThreads) counts[(int64_t)blockIdx.x * experts + e] = hist[e];
-}
-
-// Places the slots of one chunk.  Shared memory: base[experts + 1] (the next
-// free row of each expert for this chunk; its last entry the total) and
-// wcount[32][experts], the slots of each expert in each warp of a step.
-__global__ void __launch_bounds__(kSortThreads) moe_place_kernel(const void* ids, bool ids64, int64_t slots,
-                                                                 int64_t chunk, int experts, const int32_t* counts,
-                                                                 int chunks, int64_t* offsets, int32_t* slot_row,
-                                                                 int32_t* row_slot) {
+__global__ void __launch_bounds__(kSortThreads) moe_count_kernel(const SortArgs a) {
     extern __shared__ int32_t sm[];
-    int32_t* base = sm;
-    uint16_t* wcount = reinterpret_cast<uint16_t*>(sm + experts + 1);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    __shared__ int32_t carry[33];
-    // totals and this chunk's start within each expert, then an exclusive scan over the experts
-    int32_t total = 0, before = 0;
-    if (tid < experts)
-        for (int b = 0; b < chunks; b++) {
-            const int32_t c = counts[(int64_t)b * experts + tid];
-            if (b < (int)blockIdx.x) before += c;
-            total += c;
+    for (int e = threadIdx.x; e < a.experts; e += kSortThreads) sm[e] = 0;
+    __syncthreads();
+    pdl_launch_dependents();
+    const int64_t lo = blockIdx.x * a.chunk, hi = min(a.slots, lo + a.chunk);
+    for (int64_t i = lo + threadIdx.x; i < hi; i += kSortThreads) {
+        const int e = load_id(a, i);
+        if (e >= 0) atomicAdd(&sm[e], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.experts; e += kSortThreads)
+        a.counts[(int64_t)blockIdx.x * a.experts + e] = sm[e];
+}
+
+// Places the slots of one chunk.  Shared memory: total[experts], base[experts]
+// (the next free row of each expert for this chunk) and wcount[32][experts].
+__global__ void __launch_bounds__(kSortThreads) moe_place_kernel(const SortArgs a) {
+    extern __shared__ int32_t sm[];
+    const int E = a.experts, tid = threadIdx.x;
+    int32_t* total = sm;
+    int32_t* base = sm + E;
+    uint16_t* wcount = reinterpret_cast<uint16_t*>(sm + 2 * E);
+    for (int e = tid; e < 2 * E; e += kSortThreads) sm[e] = 0;
+    const int64_t lo = blockIdx.x * a.chunk, hi = min(a.slots, lo + a.chunk);
+    int e = lo + tid < hi ? load_id(a, lo + tid) : -1;         // ids are inputs: read before the counts are done
+    __syncthreads();
+    pdl_wait();
+    pdl_launch_dependents();
+    // totals and this chunk's start within each expert: integer sums, any order
+    for (int i = tid; i < a.chunks * E; i += kSortThreads) {
+        const int b = i / E, x = i - b * E;
+        const int32_t c = a.counts[i];
+        if (c) {
+            atomicAdd(&total[x], c);
+            if (b < (int)blockIdx.x) atomicAdd(&base[x], c);
         }
-    int32_t scan = total;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int32_t u = __shfl_up_sync(0xffffffffu, scan, d);
-        if (lane >= d) scan += u;
     }
-    if (lane == 31) carry[warp + 1] = scan;
-    if (tid == 0) carry[0] = 0;
     __syncthreads();
-    if (tid == 0)
-        for (int w = 1; w <= 32; w++) carry[w] += carry[w - 1];
-    __syncthreads();
-    const int32_t first = carry[warp] + scan - total;      // rows of the experts before this one
-    if (tid < experts) {
-        base[tid] = first + before;
-        if (blockIdx.x == 0) offsets[tid] = first;
+    int32_t all;
+    const int32_t first = block_scan(tid < E ? total[tid] : 0, all);
+    if (tid < E) {
+        base[tid] += first;
+        if (blockIdx.x == 0) a.offsets[tid] = first;
     }
-    const int32_t all = carry[32];
-    if (blockIdx.x == 0 && tid == 0) offsets[experts] = all;
-    const int64_t lo = blockIdx.x * chunk, hi = min(slots, lo + chunk);
-    for (int64_t i = max(lo, (int64_t)all) + tid; i < hi; i += kSortThreads) row_slot[i] = -1;
+    if (blockIdx.x == 0 && tid == 0) a.offsets[E] = all;
+    for (int64_t i = max(lo, (int64_t)all) + tid; i < hi; i += kSortThreads) a.row_slot[i] = -1;
     for (int64_t s = lo; s < hi; s += kSortThreads) {
-        for (int x = tid; x < 32 * experts; x += kSortThreads) wcount[x] = 0;
-        __syncthreads();
         const int64_t i = s + tid;
-        const int e = i < hi ? load_id(ids, ids64, i, experts) : -1;
-        // slots of the same expert in this warp: the lanes before this one give its rank
-        const unsigned same = __match_any_sync(0xffffffffu, e);
-        const int rank = __popc(same & ((1u << lane) - 1));
-        if (e >= 0 && rank == 0) wcount[warp * experts + e] = (uint16_t)__popc(same);
+        if (s > lo) e = i < hi ? load_id(a, i) : -1;
+        int32_t sum;
+        const int rank = step_ranks(e, E, 32, wcount, sum);
         __syncthreads();
-        int32_t row = -1;
-        if (e >= 0) {
-            row = base[e] + rank;
-            for (int w = 0; w < warp; w++) row += wcount[w * experts + e];
-        }
+        const int32_t row = e >= 0 ? base[e] + wcount[(tid >> 5) * E + e] + rank : -1;
         __syncthreads();
-        if (tid < experts) {
-            int32_t n = 0;
-            for (int w = 0; w < 32; w++) n += wcount[w * experts + tid];
-            base[tid] += n;
-        }
+        if (tid < E) base[tid] += sum;
         if (i < hi) {
-            slot_row[i] = row;
-            if (row >= 0) row_slot[row] = (int32_t)i;
+            a.slot_row[i] = row;
+            if (row >= 0) a.row_slot[row] = (int32_t)i;
         }
-        __syncthreads();
     }
 }
 
-template <typename T>
-__device__ __forceinline__ float to_float(T v);
-template <>
-__device__ __forceinline__ float to_float(float v) { return v; }
-template <>
-__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <typename T>
-__device__ __forceinline__ T from_float(float v);
-template <>
-__device__ __forceinline__ float from_float(float v) { return v; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_float(float v) { return __float2bfloat16_rn(v); }
+struct RowArgs {
+    const void* src;
+    int64_t ld_src;
+    void* dst;
+    int64_t ld_dst;
+    int64_t tokens;
+    int32_t nvec;                  // vectors (or elements) of a row
+    int32_t k;
+    const int32_t* slot_row;
+    const int64_t* total;          // offsets[num_experts]: rows that hold a slot
+    const float* weights;
+    const void* rows;              // combine gradient
+    int64_t ld_rows;
+    float* dweights;
+};
+
+// The rows from `total` on hold no slot: token t's group clears those among
+// rows t k .. t k + k - 1.
+template <typename T, int VEC>
+__device__ __forceinline__ void clear_rows(const RowArgs& a, int64_t t, int64_t total, int v0, int step) {
+    Pack<T, VEC> z;
+    z.zero();
+    for (int64_t r = max(t * a.k, total); r < (t + 1) * a.k; r++) {
+        T* out = static_cast<T*>(a.dst) + r * a.ld_dst;
+        for (int v = v0; v < a.nvec; v += step) z.store(out + (int64_t)v * VEC);
+    }
+}
+
+// Copies token t's row to its rows; rows_of(j) is slot j's row.
+template <typename T, int VEC, typename F>
+__device__ __forceinline__ void copy_row(const RowArgs& a, int64_t t, F rows_of, int v0, int step) {
+    constexpr int UN = 4;
+    const T* in = static_cast<const T*>(a.src) + t * a.ld_src;
+    for (int v = v0; v < a.nvec; v += UN * step) {
+        Pack<T, VEC> p[UN];
+#pragma unroll
+        for (int u = 0; u < UN; u++)
+            if (v + u * step < a.nvec) p[u].load(in + (int64_t)(v + u * step) * VEC);
+        for (int j = 0; j < a.k; j++) {
+            const int32_t r = rows_of(j);
+            if (r < 0) continue;
+            T* out = static_cast<T*>(a.dst) + r * a.ld_dst;
+#pragma unroll
+            for (int u = 0; u < UN; u++)
+                if (v + u * step < a.nvec) p[u].store(out + (int64_t)(v + u * step) * VEC);
+        }
+    }
+}
 
 constexpr int kRowThreads = 256;
 
-// rows[r] = src[slot / k] (times weights[slot]), 0 where row r holds no slot
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads) moe_gather_kernel(const T* src, int64_t ld_src, T* dst, int64_t ld_dst,
-                                                                 int64_t cols, int k, const float* weights,
-                                                                 const int32_t* row_slot) {
-    const int64_t r = blockIdx.x;
-    const int32_t slot = row_slot[r];
-    T* out = dst + r * ld_dst;
-    if (slot < 0) {
-        for (int64_t c = threadIdx.x; c < cols; c += kRowThreads) out[c] = from_float<T>(0.0f);
-        return;
-    }
-    const T* in = src + (int64_t)(slot / k) * ld_src;
-    if (weights) {
-        const float w = weights[slot];
-        for (int64_t c = threadIdx.x; c < cols; c += kRowThreads) out[c] = from_float<T>(w * to_float(in[c]));
-    } else {
-        for (int64_t c = threadIdx.x; c < cols; c += kRowThreads) out[c] = in[c];
-    }
+// Token of this thread's group of WPT warps, its first vector and its step
+struct Place {
+    int64_t t;
+    int v0, step;
+};
+template <int WPT>
+__device__ __forceinline__ Place place() {
+    constexpr int PER = kRowThreads / 32 / WPT;
+    const int g = threadIdx.x / (32 * WPT), at = threadIdx.x % (32 * WPT);
+    return {(int64_t)blockIdx.x * PER + g, at + (int)blockIdx.y * 32 * WPT, 32 * WPT * (int)gridDim.y};
 }
 
-// out[t] = sum_j weights[t, j] rows[slot_row[t, j]]
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads) moe_combine_kernel(const T* rows, int64_t ld_rows, T* dst,
-                                                                  int64_t ld_dst, int64_t cols, int k,
-                                                                  const float* weights, const int32_t* slot_row) {
-    const int64_t t = blockIdx.x;
-    for (int64_t c = threadIdx.x; c < cols; c += kRowThreads) {
-        float acc = 0.0f;
-        for (int j = 0; j < k; j++) {
-            const int32_t r = slot_row[t * k + j];
-            if (r < 0) continue;
-            const float v = to_float(rows[r * ld_rows + c]);
-            acc = weights ? fmaf(weights[t * k + j], v, acc) : acc + v;
+template <typename T, int VEC, int WPT>
+__global__ void __launch_bounds__(kRowThreads) moe_gather_kernel(const RowArgs a) {
+    const Place at = place<WPT>();
+    pdl_wait();
+    if (at.t >= a.tokens) return;
+    const int32_t* rows = a.slot_row + at.t * a.k;
+    copy_row<T, VEC>(a, at.t, [&](int j) { return rows[j]; }, at.v0, at.step);
+    clear_rows<T, VEC>(a, at.t, *a.total, at.v0, at.step);
+}
+
+// Sort and gather of at most kSortThreads slots in one launch: every CTA sorts
+// all slots in shared memory (they are few) and moves its own pieces of rows;
+// CTA 0 writes the plan.  With a.src null it only sorts.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kSortThreads) moe_small_kernel(const SortArgs s, const RowArgs a, int pieces) {
+    extern __shared__ int32_t sm[];
+    const int E = s.experts, n = (int)s.slots, tid = threadIdx.x, warps = (n + 31) >> 5;
+    int32_t* row_of = sm;                                        // [kSortThreads]
+    int32_t* base = sm + kSortThreads;                           // [E]
+    uint16_t* wcount = reinterpret_cast<uint16_t*>(base + E);    // [warps][E]
+    const int e = tid < n ? load_id(s, tid) : -1;
+    int32_t sum, all;
+    const int rank = step_ranks(e, E, warps, wcount, sum);
+    const int32_t first = block_scan(sum, all);
+    if (tid < E) base[tid] = first;
+    __syncthreads();
+    const int32_t row = e >= 0 ? base[e] + wcount[(tid >> 5) * E + e] + rank : -1;
+    row_of[tid] = row;
+    if (blockIdx.x == 0) {
+        if (tid < E) s.offsets[tid] = first;
+        if (tid == 0) s.offsets[E] = all;
+        if (tid < n) {
+            s.slot_row[tid] = row;
+            if (row >= 0) s.row_slot[row] = tid;
+            if (tid >= all) s.row_slot[tid] = -1;
         }
-        dst[t * ld_dst + c] = from_float<T>(acc);
+    }
+    if (!a.src) return;
+    __syncthreads();
+    // a piece: 128 threads' share of one token's row
+    const int g = tid >> 7, at = tid & 127;
+    for (int64_t w = (int64_t)blockIdx.x * (kSortThreads / 128) + g; w < a.tokens * pieces;
+         w += (int64_t)gridDim.x * (kSortThreads / 128)) {
+        const int64_t t = w / pieces;
+        const int v0 = (int)(w - t * pieces) * 128 + at, step = pieces * 128;
+        copy_row<T, VEC>(a, t, [&](int j) { return row_of[t * a.k + j]; }, v0, step);
+        clear_rows<T, VEC>(a, t, all, v0, step);
     }
 }
 
-// dweights[slot] = dout[slot / k] . rows[slot_row[slot]], one warp per slot
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads) moe_dweights_kernel(const T* dout, int64_t ldd, const T* rows,
-                                                                   int64_t ld_rows, int64_t cols, int64_t slots, int k,
-                                                                   const int32_t* slot_row, float* dweights) {
-    const int64_t i = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (i >= slots) return;
-    const int32_t r = slot_row[i];
-    float acc = 0.0f;
-    if (r >= 0) {
-        const T* a = dout + i / k * ldd;
-        const T* b = rows + r * ld_rows;
-        for (int64_t c = lane; c < cols; c += 32) acc = fmaf(to_float(a[c]), to_float(b[c]), acc);
-    }
+constexpr int kSlots = 8;              // slots of a token handled together
+
+// out[t] = sum_j weights[t, j] rows[slot_row[t, j]], in the order of j
+template <typename T, int VEC, int WPT, bool WEIGHTED>
+__global__ void __launch_bounds__(kRowThreads) moe_combine_kernel(const RowArgs a) {
+    constexpr int UN = VEC == 1 ? 4 : 1;
+    const Place at = place<WPT>();
+    if (at.t >= a.tokens) return;
+    const T* src = static_cast<const T*>(a.src);
+    T* out = static_cast<T*>(a.dst) + at.t * a.ld_dst;
+    int32_t row[kSlots];
+    float w[kSlots];
+    auto slots = [&](int j0) {
 #pragma unroll
-    for (int d = 16; d; d >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, d);
-    if (lane == 0) dweights[i] = acc;
+        for (int j = 0; j < kSlots; j++) {
+            row[j] = j0 + j < a.k ? a.slot_row[at.t * a.k + j0 + j] : -1;
+            w[j] = WEIGHTED && row[j] >= 0 ? a.weights[at.t * a.k + j0 + j] : 1.0f;
+        }
+    };
+    slots(0);
+    for (int v = at.v0; v < a.nvec; v += UN * at.step) {
+        float acc[UN][VEC] = {};
+        for (int j0 = 0; j0 < a.k; j0 += kSlots) {
+            if (a.k > kSlots) slots(j0);
+            Pack<T, VEC> p[UN][kSlots];
+#pragma unroll
+            for (int j = 0; j < kSlots; j++)
+#pragma unroll
+                for (int u = 0; u < UN; u++)
+                    if (row[j] >= 0 && v + u * at.step < a.nvec)
+                        p[u][j].load(src + row[j] * a.ld_src + (int64_t)(v + u * at.step) * VEC);
+#pragma unroll
+            for (int j = 0; j < kSlots; j++)
+                if (row[j] >= 0)
+#pragma unroll
+                    for (int u = 0; u < UN; u++) {
+                        float f[VEC];
+                        p[u][j].unpack(f);
+#pragma unroll
+                        for (int i = 0; i < VEC; i++)
+                            acc[u][i] = WEIGHTED ? fmaf(w[j], f[i], acc[u][i]) : acc[u][i] + f[i];
+                    }
+        }
+#pragma unroll
+        for (int u = 0; u < UN; u++)
+            if (v + u * at.step < a.nvec) {
+                Pack<T, VEC> o;
+                o.pack(acc[u]);
+                o.store(out + (int64_t)(v + u * at.step) * VEC);
+            }
+    }
 }
 
-template <typename T>
-cudaError_t gather(const MoePlanArgs& p, const MoeRowsArgs& a, cudaStream_t st) {
-    moe_gather_kernel<T><<<(unsigned)(p.tokens * p.k), kRowThreads, 0, st>>>(
-        static_cast<const T*>(a.src), a.ld_src, static_cast<T*>(a.dst), a.ld_dst, a.cols, p.k, a.weights, p.row_slot);
+// drows[row] = weights[slot] dout[t], dweights[slot] = dout[t] . rows[row]
+template <typename T, int VEC, int WPT, bool DOT>
+__global__ void __launch_bounds__(kRowThreads) moe_combine_backward_kernel(const RowArgs a) {
+    constexpr int UN = VEC == 1 ? 4 : 1;
+    __shared__ float part[kRowThreads / 32][kSlots];
+    const Place at = place<WPT>();
+    const bool live = at.t < a.tokens;
+    const T* dout = static_cast<const T*>(a.src) + (live ? at.t : 0) * a.ld_src;
+    const T* rows = static_cast<const T*>(a.rows);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int j0 = 0; j0 < a.k; j0 += kSlots) {
+        int32_t row[kSlots];
+        float w[kSlots], dot[kSlots];
+#pragma unroll
+        for (int j = 0; j < kSlots; j++) {
+            row[j] = live && j0 + j < a.k ? a.slot_row[at.t * a.k + j0 + j] : -1;
+            w[j] = row[j] >= 0 ? a.weights[at.t * a.k + j0 + j] : 0.0f;
+            dot[j] = 0.0f;
+        }
+        for (int v = live ? at.v0 : a.nvec; v < a.nvec; v += UN * at.step) {
+            Pack<T, VEC> d[UN], p[UN][kSlots];
+#pragma unroll
+            for (int u = 0; u < UN; u++) {
+                if (v + u * at.step >= a.nvec) continue;
+                d[u].load(dout + (int64_t)(v + u * at.step) * VEC);
+                if (DOT)
+#pragma unroll
+                    for (int j = 0; j < kSlots; j++)
+                        if (row[j] >= 0) p[u][j].load(rows + row[j] * a.ld_rows + (int64_t)(v + u * at.step) * VEC);
+            }
+#pragma unroll
+            for (int u = 0; u < UN; u++) {
+                if (v + u * at.step >= a.nvec) continue;
+                float f[VEC];
+                d[u].unpack(f);
+#pragma unroll
+                for (int j = 0; j < kSlots; j++) {
+                    if (row[j] < 0) continue;
+                    float o[VEC];
+                    if (DOT) {
+                        p[u][j].unpack(o);
+#pragma unroll
+                        for (int i = 0; i < VEC; i++) dot[j] = fmaf(f[i], o[i], dot[j]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < VEC; i++) o[i] = w[j] * f[i];
+                    Pack<T, VEC> g;
+                    g.pack(o);
+                    g.store(static_cast<T*>(a.dst) + row[j] * a.ld_dst + (int64_t)(v + u * at.step) * VEC);
+                }
+            }
+        }
+        if (DOT) {
+#pragma unroll
+            for (int j = 0; j < kSlots; j++)
+#pragma unroll
+                for (int d = 16; d; d >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], d);
+            __syncthreads();
+            if (lane == 0)
+#pragma unroll
+                for (int j = 0; j < kSlots; j++) part[warp][j] = dot[j];
+            __syncthreads();
+            const int j = threadIdx.x % (32 * WPT);
+            if (live && j < kSlots && j0 + j < a.k) {
+                float s = 0.0f;
+#pragma unroll
+                for (int x = 0; x < WPT; x++) s += part[warp / WPT * WPT + x][j];
+                a.dweights[at.t * a.k + j0 + j] = s;
+            }
+        }
+    }
+    if (live) clear_rows<T, VEC>(a, at.t, *a.total, at.v0, at.step);
+}
+
+// ------------------------------------------------------------------- launches
+SortArgs sort_args(const MoePlanArgs& p, const void* ids, bool ids64, void* ws) {
+    SortArgs a{};
+    a.ids = ids;
+    a.slots = p.tokens * p.k;
+    a.chunk = sort_chunk(a.slots);
+    a.chunks = (int)((a.slots + a.chunk - 1) / a.chunk);
+    a.ids64 = ids64;
+    a.experts = p.num_experts;
+    a.counts = static_cast<int32_t*>(ws);
+    a.offsets = p.offsets;
+    a.slot_row = p.slot_row;
+    a.row_slot = p.row_slot;
+    return a;
+}
+
+RowArgs row_args(const MoePlanArgs& p, const MoeRowsArgs& m, int vec) {
+    RowArgs a{};
+    a.src = m.src;
+    a.ld_src = m.ld_src;
+    a.dst = m.dst;
+    a.ld_dst = m.ld_dst;
+    a.tokens = p.tokens;
+    a.nvec = (int32_t)(m.cols / vec);
+    a.k = p.k;
+    a.slot_row = p.slot_row;
+    a.total = p.offsets + p.num_experts;
+    a.weights = m.weights;
+    a.rows = m.rows;
+    a.ld_rows = m.ld_rows;
+    a.dweights = m.dweights;
+    return a;
+}
+
+// vectors only where every matrix of the call allows them
+bool vectors(const MoeRowsArgs& m) {
+    const int e = m.bf16 ? 2 : 4;
+    return rows_vec(m.src, m.ld_src, m.cols, e) && rows_vec(m.dst, m.ld_dst, m.cols, e) &&
+           (!m.rows || rows_vec(m.rows, m.ld_rows, m.cols, e));
+}
+
+// warps per token: about 64 vectors each, so that a warp has several in flight
+int warps_per_token(int nvec) {
+    int w = 1;
+    while (w < 8 && nvec > 64 * w) w *= 2;
+    return w;
+}
+
+// Tokens along x; with few tokens their rows are cut along y as well (where
+// the kernel allows it), until two CTAs per SM have work.
+dim3 row_grid(const RowArgs& a, int wpt, bool split, int num_sms) {
+    const int per = kRowThreads / 32 / wpt;
+    const int64_t x = (a.tokens + per - 1) / per;
+    const int64_t most = (a.nvec + 32 * wpt - 1) / (32 * wpt);
+    const int64_t y = split ? std::min(most, std::max<int64_t>(1, 2 * num_sms / x)) : 1;
+    return dim3((unsigned)x, (unsigned)y);
+}
+
+template <typename T, int VEC>
+cudaError_t gather_t(const MoePlanArgs& p, const MoeRowsArgs& m, bool dependent, cudaStream_t st) {
+    const RowArgs a = row_args(p, m, VEC);
+    const int w = warps_per_token(a.nvec);
+    const dim3 g = row_grid(a, w, true, p.num_sms);
+    switch (w) {
+    case 1: return launch_k(dependent, moe_gather_kernel<T, VEC, 1>, g, kRowThreads, 0, st, a);
+    case 2: return launch_k(dependent, moe_gather_kernel<T, VEC, 2>, g, kRowThreads, 0, st, a);
+    case 4: return launch_k(dependent, moe_gather_kernel<T, VEC, 4>, g, kRowThreads, 0, st, a);
+    default: return launch_k(dependent, moe_gather_kernel<T, VEC, 8>, g, kRowThreads, 0, st, a);
+    }
+}
+
+template <typename T, int VEC, bool WEIGHTED>
+cudaError_t combine_w(const MoePlanArgs& p, const RowArgs& a, cudaStream_t st) {
+    const int w = warps_per_token(a.nvec);
+    const dim3 g = row_grid(a, w, true, p.num_sms);
+    switch (w) {
+    case 1: moe_combine_kernel<T, VEC, 1, WEIGHTED><<<g, kRowThreads, 0, st>>>(a); break;
+    case 2: moe_combine_kernel<T, VEC, 2, WEIGHTED><<<g, kRowThreads, 0, st>>>(a); break;
+    case 4: moe_combine_kernel<T, VEC, 4, WEIGHTED><<<g, kRowThreads, 0, st>>>(a); break;
+    default: moe_combine_kernel<T, VEC, 8, WEIGHTED><<<g, kRowThreads, 0, st>>>(a);
+    }
+    return cudaGetLastError();
+}
+template <typename T, int VEC>
+cudaError_t combine_t(const MoePlanArgs& p, const MoeRowsArgs& m, cudaStream_t st) {
+    const RowArgs a = row_args(p, m, VEC);
+    return m.weights ? combine_w<T, VEC, true>(p, a, st) : combine_w<T, VEC, false>(p, a, st);
+}
+
+template <typename T, int VEC, bool DOT>
+cudaError_t backward_d(const MoePlanArgs& p, const RowArgs& a, cudaStream_t st) {
+    const int w = warps_per_token(a.nvec);
+    const dim3 g = row_grid(a, w, !DOT, p.num_sms);         // a dot product stays in one CTA
+    switch (w) {
+    case 1: moe_combine_backward_kernel<T, VEC, 1, DOT><<<g, kRowThreads, 0, st>>>(a); break;
+    case 2: moe_combine_backward_kernel<T, VEC, 2, DOT><<<g, kRowThreads, 0, st>>>(a); break;
+    case 4: moe_combine_backward_kernel<T, VEC, 4, DOT><<<g, kRowThreads, 0, st>>>(a); break;
+    default: moe_combine_backward_kernel<T, VEC, 8, DOT><<<g, kRowThreads, 0, st>>>(a);
+    }
+    return cudaGetLastError();
+}
+template <typename T, int VEC>
+cudaError_t backward_t(const MoePlanArgs& p, const MoeRowsArgs& m, cudaStream_t st) {
+    const RowArgs a = row_args(p, m, VEC);
+    return m.dweights ? backward_d<T, VEC, true>(p, a, st) : backward_d<T, VEC, false>(p, a, st);
+}
+
+template <typename T, int VEC>
+cudaError_t small_t(const MoePlanArgs& p, const SortArgs& s, const MoeRowsArgs* m, cudaStream_t st) {
+    RowArgs a{};
+    int pieces = 1;
+    int64_t ctas = 1;
+    if (m) {
+        a = row_args(p, *m, VEC);
+        // a token's row in pieces of at least 128 vectors, about as many pieces as there is room for
+        const int64_t room = (int64_t)p.num_sms * (kSortThreads / 128);
+        pieces = (int)std::max<int64_t>(1, std::min<int64_t>((a.nvec + 127) / 128, room / p.tokens));
+        ctas = std::min<int64_t>(p.num_sms, (p.tokens * pieces + kSortThreads / 128 - 1) / (kSortThreads / 128));
+    }
+    const size_t smem = (kSortThreads + s.experts) * sizeof(int32_t) +
+                        (size_t)((s.slots + 31) / 32) * s.experts * sizeof(uint16_t);
+    if (smem > 40 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(moe_small_kernel<T, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             80 * 1024);
+        if (e != cudaSuccess) return e;
+    }
+    moe_small_kernel<T, VEC><<<(unsigned)ctas, kSortThreads, smem, st>>>(s, a, pieces);
     return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t combine(const MoePlanArgs& p, const MoeRowsArgs& a, cudaStream_t st) {
-    moe_combine_kernel<T><<<(unsigned)p.tokens, kRowThreads, 0, st>>>(
-        static_cast<const T*>(a.src), a.ld_src, static_cast<T*>(a.dst), a.ld_dst, a.cols, p.k, a.weights, p.slot_row);
-    return cudaGetLastError();
-}
-
-template <typename T>
-cudaError_t combine_backward(const MoePlanArgs& p, const MoeRowsArgs& a, cudaStream_t st) {
-    cudaError_t e = gather<T>(p, a, st);
-    if (e != cudaSuccess || !a.dweights) return e;
-    const int64_t slots = p.tokens * p.k, per = kRowThreads / 32;
-    moe_dweights_kernel<T><<<(unsigned)((slots + per - 1) / per), kRowThreads, 0, st>>>(
-        static_cast<const T*>(a.src), a.ld_src, static_cast<const T*>(a.rows), a.ld_rows, a.cols, slots, p.k,
-        p.slot_row, a.dweights);
-    return cudaGetLastError();
+// more than kSortThreads slots: the plan in two launches
+cudaError_t sort_large(const SortArgs& s, cudaStream_t st) {
+    moe_count_kernel<<<s.chunks, kSortThreads, s.experts * sizeof(int32_t), st>>>(s);
+    const size_t smem = 2 * s.experts * sizeof(int32_t) + (size_t)32 * s.experts * sizeof(uint16_t);
+    if (smem > 40 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(moe_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 80 * 1024);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_k(true, moe_place_kernel, dim3(s.chunks), kSortThreads, smem, st, s);
 }
 
 }  // namespace
 
 size_t moe_sort_workspace(int64_t tokens, int k, int num_experts) {
     const int64_t slots = tokens * k, chunk = sort_chunk(slots);
-    return (size_t)((slots + chunk - 1) / chunk) * num_experts * sizeof(int32_t);
+    return slots <= kSortThreads ? 0 : (size_t)((slots + chunk - 1) / chunk) * num_experts * sizeof(int32_t);
 }
 
 cudaError_t run_moe_sort(const MoePlanArgs& p, const void* ids, bool ids64, void* ws, cudaStream_t st) {
-    const int64_t slots = p.tokens * p.k, chunk = sort_chunk(slots);
-    const int chunks = (int)((slots + chunk - 1) / chunk), E = p.num_experts;
-    int32_t* counts = static_cast<int32_t*>(ws);
-    moe_count_kernel<<<chunks, kSortThreads, E * sizeof(int32_t), st>>>(ids, ids64, slots, chunk, E, counts);
-    const size_t smem = (E + 1) * sizeof(int32_t) + (size_t)32 * E * sizeof(uint16_t);
-    cudaError_t e = cudaFuncSetAttribute(moe_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 80 * 1024);
-    if (e != cudaSuccess) return e;
-    moe_place_kernel<<<chunks, kSortThreads, smem, st>>>(ids, ids64, slots, chunk, E, counts, chunks, p.offsets,
-                                                         p.slot_row, p.row_slot);
-    return cudaGetLastError();
+    const SortArgs s = sort_args(p, ids, ids64, ws);
+    return s.slots <= kSortThreads ? small_t<float, 4>(p, s, nullptr, st) : sort_large(s, st);
 }
 
-cudaError_t run_moe_gather(const MoePlanArgs& p, const MoeRowsArgs& a, cudaStream_t st) {
-    return a.bf16 ? gather<__nv_bfloat16>(p, a, st) : gather<float>(p, a, st);
+cudaError_t run_moe_dispatch(const MoePlanArgs& p, const MoeRowsArgs& m, const void* ids, bool ids64, void* ws,
+                             cudaStream_t st) {
+    const SortArgs s = sort_args(p, ids, ids64, ws);
+    const bool v = vectors(m);
+    if (s.slots <= kSortThreads) {
+        if (m.bf16) return v ? small_t<__nv_bfloat16, 8>(p, s, &m, st) : small_t<__nv_bfloat16, 1>(p, s, &m, st);
+        return v ? small_t<float, 4>(p, s, &m, st) : small_t<float, 1>(p, s, &m, st);
+    }
+    cudaError_t e = sort_large(s, st);
+    if (e != cudaSuccess) return e;
+    if (m.bf16) return v ? gather_t<__nv_bfloat16, 8>(p, m, true, st) : gather_t<__nv_bfloat16, 1>(p, m, true, st);
+    return v ? gather_t<float, 4>(p, m, true, st) : gather_t<float, 1>(p, m, true, st);
 }
-cudaError_t run_moe_combine(const MoePlanArgs& p, const MoeRowsArgs& a, cudaStream_t st) {
-    return a.bf16 ? combine<__nv_bfloat16>(p, a, st) : combine<float>(p, a, st);
+
+cudaError_t run_moe_gather(const MoePlanArgs& p, const MoeRowsArgs& m, cudaStream_t st) {
+    const bool v = vectors(m);
+    if (m.bf16) return v ? gather_t<__nv_bfloat16, 8>(p, m, false, st) : gather_t<__nv_bfloat16, 1>(p, m, false, st);
+    return v ? gather_t<float, 4>(p, m, false, st) : gather_t<float, 1>(p, m, false, st);
 }
-cudaError_t run_moe_combine_backward(const MoePlanArgs& p, const MoeRowsArgs& a, cudaStream_t st) {
-    return a.bf16 ? combine_backward<__nv_bfloat16>(p, a, st) : combine_backward<float>(p, a, st);
+cudaError_t run_moe_combine(const MoePlanArgs& p, const MoeRowsArgs& m, cudaStream_t st) {
+    const bool v = vectors(m);
+    if (m.bf16) return v ? combine_t<__nv_bfloat16, 8>(p, m, st) : combine_t<__nv_bfloat16, 1>(p, m, st);
+    return v ? combine_t<float, 4>(p, m, st) : combine_t<float, 1>(p, m, st);
+}
+cudaError_t run_moe_combine_backward(const MoePlanArgs& p, const MoeRowsArgs& m, cudaStream_t st) {
+    const bool v = vectors(m);
+    if (m.bf16) return v ? backward_t<__nv_bfloat16, 8>(p, m, st) : backward_t<__nv_bfloat16, 1>(p, m, st);
+    return v ? backward_t<float, 4>(p, m, st) : backward_t<float, 1>(p, m, st);
 }
 
 }  // namespace bsq
