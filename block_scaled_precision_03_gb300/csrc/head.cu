@@ -47,9 +47,10 @@ constexpr uint32_t kTx = 2 * kOpBytes;              // bytes one CTA loads per s
 constexpr int kEpiWarps = 8;
 constexpr int kGemmThreads = 32 * (2 + kEpiWarps);
 constexpr uint32_t kTmemCols = 512;
-constexpr int kSmem = 1024 + kStages * 2 * kOpBytes + kEpiWarps * 2048 + 256;
+constexpr int kStage = 4096;                        // a warp's staging: two chunks of 32 rows x 64 bytes
+constexpr int kSmem = 1024 + kStages * 2 * kOpBytes + kEpiWarps * kStage + 256;
 static_assert(kSmem <= 232448, "shared memory per block");
-constexpr int kRasterGroup = 8;
+constexpr int kRasterGroup = 16;
 constexpr int64_t kL2Resident = 48ll << 20;
 
 // MODE's operand layouts: K-major (false) or MN-major (true)
@@ -108,32 +109,64 @@ __device__ __forceinline__ void tma_store_3d(const void* tmap, int32_t x, int32_
                      :: "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(src) : "memory");
 }
 
-// A warp's 32 rows x 128 FP32 columns into (or added to) the [split][M][N]
-// accumulator, 16 columns at a time through its 64-byte-swizzled staging
-// buffer (the layout of store_tile_tma).
-__device__ __forceinline__ void store_acc(const uint32_t (&r)[4][32], uint32_t buf, const void* tmap, int col0, int row0,
-                                          int split, bool add, int lane) {
-    const uint32_t row_base = buf + (uint32_t)lane * 64u;
-    const uint32_t sw = (uint32_t)((lane >> 1) & 3);
+// Epilogue stores.  A warp's 32 rows leave in chunks of 64 bytes a row (32
+// BF16 or 16 FP32 columns) through two 2 KB staging buffers laid out with the
+// 64-byte swizzle (16-byte unit u of row r at unit u ^ ((r >> 1) & 3)), one
+// TMA tile store each; `n` counts the warp's chunks.
+__device__ __forceinline__ void stage_chunk(const uint32_t (&w)[16], uint32_t buf, int lane) {
+    const uint32_t row = buf + (uint32_t)lane * 64u, sw = (uint32_t)((lane >> 1) & 3);
 #pragma unroll
-    for (int ch = 0; ch < 8; ch++) {
-        if (lane == 0) tc::bulk_wait_read();
-        __syncwarp();
+    for (int u = 0; u < 4; u++)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                     :: "r"(row + ((u ^ sw) << 4)), "r"(w[4 * u]), "r"(w[4 * u + 1]), "r"(w[4 * u + 2]), "r"(w[4 * u + 3])
+                     : "memory");
+    tc::fence_async_smem();
+    __syncwarp();
+}
+// the buffer of chunk n may be written again: at most one store still reads its own
+__device__ __forceinline__ uint32_t chunk_buffer(uint32_t base, int n, int lane) {
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    __syncwarp();
+    return base + (uint32_t)(n & 1) * 2048u;
+}
+__device__ __forceinline__ void store_bf16(const float (&v)[32], float alpha, uint32_t base, const void* tmap, int col,
+                                           int row, int& n, int lane) {
+    uint32_t w[16];
 #pragma unroll
-        for (int u = 0; u < 4; u++) {
-            const int c = ch * 16 + u * 4;
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                         :: "r"(row_base + ((u ^ sw) << 4)), "r"(r[c >> 5][c & 31]), "r"(r[c >> 5][(c & 31) + 1]),
-                            "r"(r[c >> 5][(c & 31) + 2]), "r"(r[c >> 5][(c & 31) + 3]) : "memory");
-        }
-        tc::fence_async_smem();
-        __syncwarp();
+    for (int j = 0; j < 16; j++) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j] * alpha, v[2 * j + 1] * alpha);
+        w[j] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    const uint32_t buf = chunk_buffer(base, n++, lane);
+    stage_chunk(w, buf, lane);
+    if (lane == 0) {
+        tc::tma_store_2d(tmap, col, row, buf);
+        tc::bulk_commit();
+    }
+}
+__device__ __forceinline__ void store_acc(const float (&v)[32], uint32_t base, const void* tmap, int col, int row, int split,
+                                          bool add, int& n, int lane) {
+#pragma unroll
+    for (int c = 0; c < 2; c++) {
+        uint32_t w[16];
+#pragma unroll
+        for (int j = 0; j < 16; j++) w[j] = __float_as_uint(v[16 * c + j]);
+        const uint32_t buf = chunk_buffer(base, n++, lane);
+        stage_chunk(w, buf, lane);
         if (lane == 0) {
-            if (add) tma_store_3d<true>(tmap, col0 + ch * 16, row0, split, buf);
-            else tma_store_3d<false>(tmap, col0 + ch * 16, row0, split, buf);
+            if (add) tma_store_3d<true>(tmap, col + 16 * c, row, split, buf);
+            else tma_store_3d<false>(tmap, col + 16 * c, row, split, buf);
             tc::bulk_commit();
         }
     }
+}
+// 32 columns of the accumulator at `taddr`
+__device__ __forceinline__ void load_acc(float (&v)[32], uint32_t taddr) {
+    uint32_t r[32];
+    BSQ_TMEM_LD32(r, taddr);
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 32; j++) v[j] = __uint_as_float(r[j]);
 }
 
 struct TileAt {
@@ -181,7 +214,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     uint8_t* smA = base;
     uint8_t* smB = smA + kStages * kOpBytes;
     uint8_t* smOut = smB + kStages * kOpBytes;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smOut + kEpiWarps * 2048);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smOut + kEpiWarps * kStage);
     // full[S], empty[S], tfull[2], tempty[2], drain
     const uint32_t full0 = tc::smem_u32(bars), empty0 = tc::smem_u32(bars + kStages);
     const uint32_t tfull0 = tc::smem_u32(bars + 2 * kStages), tempty0 = tc::smem_u32(bars + 2 * kStages + 2);
@@ -271,7 +304,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             const uint64_t bd0 = b_mn(MODE) ? desc_mn_sw128(tc::smem_u32(smB)) : tc::desc_sw128(tc::smem_u32(smB));
             int stage = 0, iter = 0;
             uint32_t phase = 0;
-            bool ok = true, any = false;
+            bool ok = true, any = false, ready = false;
             for (int t = cid; t < p.total && ok; t += ncl, ++iter) {
                 const TileAt ti = tile_at(p, t);
                 const int buf = iter & 1;
@@ -279,26 +312,36 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     ok = false;
                     break;
                 }
-                tc::fence_after();
                 const uint32_t d = tmem + (uint32_t)buf * kTile;
                 for (int kb = ti.k0; kb < ti.k1; kb++) {
-                    if (!tc::mbar_wait(full0 + 8 * stage, phase, abort_flag, p.status, p.timeout_ns)) {
+                    if (!ready && !tc::mbar_wait(full0 + 8 * stage, phase, abort_flag, p.status, p.timeout_ns)) {
                         ok = false;
                         break;
                     }
                     tc::fence_after();
                     const uint64_t ad = ad0 + (uint64_t)(stage * (kOpBytes >> 4));
                     const uint64_t bd = bd0 + (uint64_t)(stage * (kOpBytes >> 4));
-                    const int nk = kb == p.k_stages - 1 ? p.mma_last : kMmas;
+                    const int next = stage + 1 == kStages ? 0 : stage + 1;
+                    const uint32_t next_phase = next == 0 ? phase ^ 1 : phase;
+                    if (kb != p.k_stages - 1 || p.mma_last == kMmas) {
+                        // the next stage's barrier is tested while this stage's MMAs run
 #pragma unroll
-                    for (int m = 0; m < kMmas; m++)
-                        if (m < nk)
+                        for (int m = 0; m < kMmas; m++) {
+                            if (m == kMmas - 1) ready = tc::mbar_test(full0 + 8 * next, next_phase);
                             mma_bf16(d, ad + (m >> 2) * (kSubBytes >> 4) + (m & 3) * a_step,
                                      bd + (m >> 2) * (kSubBytes >> 4) + (m & 3) * b_step, idesc, (kb != ti.k0) | (m != 0));
+                        }
+                    } else {
+                        for (int m = 0; m < p.mma_last; m++)
+                            mma_bf16(d, ad + (m >> 2) * (kSubBytes >> 4) + (m & 3) * a_step,
+                                     bd + (m >> 2) * (kSubBytes >> 4) + (m & 3) * b_step, idesc, (kb != ti.k0) | (m != 0));
+                        ready = false;
+                    }
                     any = true;
                     tc::commit<2>(empty0 + 8 * stage, 3);
                     if (kb == ti.k1 - 1) tc::commit<2>(tfull0 + 8 * buf, 3);
-                    if (++stage == kStages) { stage = 0; phase ^= 1; }
+                    stage = next;
+                    phase = next_phase;
                 }
             }
             if (!ok) *abort_flag = 1;
@@ -314,78 +357,92 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         // A thread owns one row and 128 of the tile's columns.
         const int q = warp & 3, half = (warp - 2) >> 2;
         const uint32_t tempty_c0 = tc::mapa(tempty0, 0);
-        const uint32_t stage_buf = tc::smem_u32(smOut + (warp - 2) * 2048);
+        const uint32_t stage_buf = tc::smem_u32(smOut + (warp - 2) * kStage);
         const float smax = MODE == kGrad || MODE == kDw ? *p.smax : 1.0f;
-        int iter = 0;
+        int iter = 0, n = 0;
         for (int t = cid; t < p.total; t += ncl, ++iter) {
             const TileAt ti = tile_at(p, t);
             const int buf = iter & 1;
             const int64_t row0 = (int64_t)ti.mt * kTile + rank * 128 + q * 32, row = row0 + lane;
             const int64_t col0 = (int64_t)ti.nt * kTile + half * 128;
             // what the row needs, read while the tile is computed
-            int64_t target = -1;
+            int target = -1;                       // the target's column among this thread's 128
             float lse = 0.0f, ratio = 0.0f;
             if ((MODE == kStats || MODE == kGrad) && row < p.M) {
-                target = p.targets[row];
-                if (MODE == kGrad && target >= 0 && target < p.vocab && smax > 0.0f) {
-                    lse = p.lse[row];
-                    ratio = p.dloss[row] / smax;
+                const int64_t id = p.targets[row];
+                if (id >= 0 && id < p.vocab) {
+                    if (MODE == kGrad && smax > 0.0f) {
+                        lse = p.lse[row];
+                        ratio = p.dloss[row] / smax;
+                    }
+                    const int64_t at = id - p.col0 - col0;
+                    if (at >= 0 && at < 128) target = (int)at;
                 }
-                target -= p.col0 + col0;
             }
             if (!tc::mbar_wait(tfull0 + 8 * buf, (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns)) break;
             tc::fence_after();
-            uint32_t r[4][32];
             const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kTile + half * 128);
-            BSQ_TMEM_LD32(r[0], ta);
-            BSQ_TMEM_LD32(r[1], ta + 32);
-            BSQ_TMEM_LD32(r[2], ta + 64);
-            BSQ_TMEM_LD32(r[3], ta + 96);
-            tc::tmem_wait_ld();
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive_cluster(tempty_c0 + 8 * buf);
-            if (row0 >= p.M || col0 >= p.N) continue;
-            const bool here = target >= 0 && target < 128;
-            if (MODE == kStats) {
-                const int live = (int)min((int64_t)128, p.N - col0);
-                if (live < 128)
+            const bool live = row0 < p.M && col0 < p.N;
+            float v[32];
+            if (MODE == kStats && live) {
+                // two passes over the accumulator: it is read from tensor memory again
+                // rather than held in 128 registers
+                const int cols = (int)min((int64_t)128, p.N - col0);
+                const bool hits = __any_sync(0xffffffffu, target >= 0 && target < cols);
+                float m = kNegInf, hit = 0.0f;
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 32) {
+                    load_acc(v, ta + c);
 #pragma unroll
-                    for (int j = 0; j < 128; j++)
-                        if (j >= live) r[j >> 5][j & 31] = __float_as_uint(kNegInf);
-                float m = kNegInf;
+                    for (int j = 0; j < 32; j++) {
+                        if (cols < 128 && c + j >= cols) v[j] = kNegInf;
+                        m = fmaxf(m, v[j]);
+                    }
+                    if (hits)
 #pragma unroll
-                for (int j = 0; j < 128; j++) m = fmaxf(m, __uint_as_float(r[j >> 5][j & 31]));
-                if (__any_sync(0xffffffffu, here)) {
-                    float hit = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < 128; j++)
-                        if ((int)target == j) hit = __uint_as_float(r[j >> 5][j & 31]);
-                    if (here && row < p.M && target < live) p.hit[row] = hit;
+                        for (int j = 0; j < 32; j++)
+                            if (target == c + j) hit = v[j];
                 }
                 // z - m is formed first: a product with log2(e) before it would round away the
                 // difference of large logits
                 const float m0 = m == kNegInf ? 0.0f : m;
                 float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 32) {
+                    load_acc(v, ta + c);
 #pragma unroll
-                for (int j = 0; j < 128; j++)
-                    s[j & 3] += exp2_fast((__uint_as_float(r[j >> 5][j & 31]) - m0) * kLog2e);
-                if (row < p.M) p.part[(col0 >> 7) * p.M + row] = make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
-            } else if (MODE == kGrad) {
-                // ratio 0 (a token that does not count) gives 0 whatever its logits
-                const bool zero = ratio == 0.0f;
-#pragma unroll
-                for (int j = 0; j < 128; j++) {
-                    float g = exp2_fast((__uint_as_float(r[j >> 5][j & 31]) - lse) * kLog2e);
-                    if ((int)target == j && here) g -= 1.0f;
-                    r[j >> 5][j & 31] = zero ? 0u : __float_as_uint(g);
+                    for (int j = 0; j < 32; j++) {
+                        if (cols < 128 && c + j >= cols) v[j] = kNegInf;
+                        s[j & 3] += exp2_fast((v[j] - m0) * kLog2e);
+                    }
                 }
-                store_tile_tma<true>(r, stage_buf, &tmOut, (int)col0, (int)row0, ratio, 1.0f, lane);
-            } else if (MODE == kDh) {
-                store_acc(r, stage_buf, &tmOut, (int)col0, (int)row0, ti.split, p.add != 0, lane);
-            } else {
-                store_tile_tma<true>(r, stage_buf, &tmOut, (int)col0, (int)row0, smax, 1.0f, lane);
+                if (row < p.M) {
+                    if (target >= 0 && target < cols) p.hit[row] = hit;
+                    p.part[(col0 >> 7) * p.M + row] = make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
+                }
+            } else if (live) {
+                // ratio 0 (a token that does not count) gives 0 whatever its logits
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 32) {
+                    load_acc(v, ta + c);
+                    const int col = (int)col0 + c;
+                    if (MODE == kDh) {
+                        store_acc(v, stage_buf, &tmOut, col, (int)row0, ti.split, p.add != 0, n, lane);
+                        continue;
+                    }
+                    if (MODE == kGrad) {
+#pragma unroll
+                        for (int j = 0; j < 32; j++) {
+                            const float g = exp2_fast((v[j] - lse) * kLog2e) - (target == c + j ? 1.0f : 0.0f);
+                            v[j] = ratio == 0.0f ? 0.0f : g;
+                        }
+                    }
+                    store_bf16(v, MODE == kGrad ? ratio : smax, stage_buf, &tmOut, col, (int)row0, n, lane);
+                }
             }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_cluster(tempty_c0 + 8 * buf);
         }
         if (lane == 0) tc::bulk_wait_all();
     }
