@@ -23,6 +23,7 @@
 #include "common.cuh"
 #include "epilogue.cuh"
 #include "internal.h"
+#include "launch.cuh"
 #include "tcgen05.cuh"
 #include "tmap.h"
 
@@ -43,15 +44,13 @@ constexpr int kStages = 3;
 constexpr int kSubBytes = 128 * kSubK * 2;          // one CTA's 128 rows of an operand, one sub-step
 constexpr int kOpBytes = kSub * kSubBytes;
 constexpr int kMmas = 4 * kSub;                     // per stage
-constexpr uint32_t kTx = 2 * kOpBytes;              // bytes one CTA loads per stage
 constexpr int kEpiWarps = 8;
 constexpr int kGemmThreads = 32 * (2 + kEpiWarps);
 constexpr uint32_t kTmemCols = 512;
 constexpr int kStage = 4096;                        // a warp's staging: two chunks of 32 rows x 64 bytes
 constexpr int kSmem = 1024 + kStages * 2 * kOpBytes + kEpiWarps * kStage + 256;
 static_assert(kSmem <= 232448, "shared memory per block");
-constexpr int kRasterGroup = 16;
-constexpr int64_t kL2Resident = 48ll << 20;
+constexpr int64_t kL2Resident = 40ll << 20;         // operand bytes that stay in L2 while others stream past
 
 // MODE's operand layouts: K-major (false) or MN-major (true)
 __host__ __device__ constexpr bool a_mn(int mode) { return mode == kDw; }
@@ -62,10 +61,13 @@ struct GemmParams {
     int32_t k_stages, mma_last;    // K stages in all; MMAs of the last one
     int32_t m_tiles, n_tiles, splits, split_stages, total;
     int32_t raster, raster_n;
+    int32_t tile_n;                // output columns of a pair: 256, or fewer where that balances few rows
+    uint32_t tx;                   // bytes one CTA loads per stage
+    int32_t wait_end;              // a programmatic dependent that needs nothing of the kernel before it
     const int64_t* targets;
     int64_t vocab;
     int64_t col0;                  // first vocabulary column of the piece
-    float2* part;                  // kStats: [128 columns][M] (max, sum)
+    float2* part;                  // kStats: [part][M] (max, sum), a part per tile and 128 columns
     float* hit;                    // kStats: the target's logit
     const float* lse;
     const float* dloss;
@@ -81,11 +83,11 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
                  :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
 }
 // tcgen05 instruction descriptor of kind::f16: bits 4-5 FP32 accumulator,
-// 7-9 and 10-12 BF16 operands, 15 and 16 MN-major A and B, 17-22 N>>3,
-// 24-28 M>>4.
+// 7-9 and 10-12 BF16 operands, 15 and 16 MN-major A and B, 17-22 N>>3 (left
+// 0 here), 24-28 M>>4.
 __host__ __device__ constexpr uint32_t idesc_bf16(bool amn, bool bmn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((amn ? 1u : 0u) << 15) | ((bmn ? 1u : 0u) << 16) |
-           ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+           ((uint32_t)(kTile >> 4) << 24);
 }
 // Descriptor of an MN-major operand tile with 128-byte swizzle: rows of 64
 // contiguous M (or N) elements, one per k; 8 of them 1024 bytes apart, the
@@ -194,12 +196,12 @@ __device__ __forceinline__ TileAt tile_at(const GemmParams& p, int t) {
 // Load k goes to stage k % kStages, phase (k / kStages) & 1, on the even CTA,
 // which arms each load with both CTAs' bytes; a load that only one CTA issued
 // gets the missing half of that accounting here.
-__device__ __noinline__ void drain_loads(uint32_t full0, int n_own, int n_peer) {
+__device__ __noinline__ void drain_loads(uint32_t full0, int n_own, int n_peer, uint32_t tx) {
     const int n = max(n_own, n_peer);
     for (int k = max(0, n - kStages); k < n; k++) {
         const uint32_t bar = full0 + 8 * (uint32_t)(k % kStages);
-        if (k < n_own && k >= n_peer) tc::mbar_complete_tx(bar, kTx);
-        if (k < n_peer && k >= n_own) tc::mbar_expect_tx(bar, kTx);
+        if (k < n_own && k >= n_peer) tc::mbar_complete_tx(bar, tx);
+        if (k < n_peer && k >= n_own) tc::mbar_expect_tx(bar, tx);
         volatile int no_abort = 0;
         tc::mbar_wait(bar, (uint32_t)((k / kStages) & 1), &no_abort, nullptr, 100000000ull);
     }
@@ -224,6 +226,8 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     volatile int* issued_slot = reinterpret_cast<volatile int*>(tmem_slot + 2);
     static_assert(8 * (2 * kStages + 5) + 12 <= 256, "barrier area");
 
+    // a kernel that may run beside this one starts as soon as SMs are free
+    pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_rank();
     const bool leader = rank == 0;
@@ -261,14 +265,14 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             bool ok = true;
             for (int t = cid; t < p.total && ok; t += ncl) {
                 const TileAt ti = tile_at(p, t);
-                const int am = ti.mt * kTile + (int)rank * 128, bn = ti.nt * kTile + (int)rank * 128;
+                const int am = ti.mt * kTile + (int)rank * 128, bn = ti.nt * p.tile_n + (int)rank * (p.tile_n / 2);
                 for (int kb = ti.k0; kb < ti.k1; kb++) {
                     if (!tc::mbar_wait(empty0 + 8 * stage, phase ^ 1, abort_flag, p.status, p.timeout_ns)) {
                         ok = false;
                         break;
                     }
                     const uint32_t fb = full_c0 + 8 * stage;
-                    if (leader) tc::mbar_expect_tx(full0 + 8 * stage, 2 * kTx);
+                    if (leader) tc::mbar_expect_tx(full0 + 8 * stage, 2 * p.tx);
 #pragma unroll
                     for (int j = 0; j < kSub; j++) {
                         const int k = (kb * kSub + j) * kSubK;
@@ -297,7 +301,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer (even CTA)
         if (lane == 0 && leader) {
-            constexpr uint32_t idesc = idesc_bf16(a_mn(MODE), b_mn(MODE));
+            const uint32_t idesc = idesc_bf16(a_mn(MODE), b_mn(MODE)) | ((uint32_t)(p.tile_n >> 3) << 17);
             // 16 k further: 32 bytes of a K-major row, 16 rows of an MN-major tile
             constexpr uint32_t a_step = a_mn(MODE) ? 2048 >> 4 : 2, b_step = b_mn(MODE) ? 2048 >> 4 : 2;
             const uint64_t ad0 = a_mn(MODE) ? desc_mn_sw128(tc::smem_u32(smA)) : tc::desc_sw128(tc::smem_u32(smA));
@@ -364,7 +368,8 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             const TileAt ti = tile_at(p, t);
             const int buf = iter & 1;
             const int64_t row0 = (int64_t)ti.mt * kTile + rank * 128 + q * 32, row = row0 + lane;
-            const int64_t col0 = (int64_t)ti.nt * kTile + half * 128;
+            const int64_t col0 = (int64_t)ti.nt * p.tile_n + half * 128;
+            const int width = min(128, p.tile_n - half * 128);       // of the tile's columns, this thread's
             // what the row needs, read while the tile is computed
             int target = -1;                       // the target's column among this thread's 128
             float lse = 0.0f, ratio = 0.0f;
@@ -376,26 +381,26 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                         ratio = p.dloss[row] / smax;
                     }
                     const int64_t at = id - p.col0 - col0;
-                    if (at >= 0 && at < 128) target = (int)at;
+                    if (at >= 0 && at < width) target = (int)at;
                 }
             }
             if (!tc::mbar_wait(tfull0 + 8 * buf, (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns)) break;
             tc::fence_after();
             const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kTile + half * 128);
-            const bool live = row0 < p.M && col0 < p.N;
+            const bool live = row0 < p.M && (MODE == kStats ? width > 0 : col0 < p.N && width > 0);
             float v[32];
             if (MODE == kStats && live) {
                 // two passes over the accumulator: it is read from tensor memory again
                 // rather than held in 128 registers
-                const int cols = (int)min((int64_t)128, p.N - col0);
+                const int cols = (int)min((int64_t)width, p.N - col0);       // 0 or less: an empty part
                 const bool hits = __any_sync(0xffffffffu, target >= 0 && target < cols);
                 float m = kNegInf, hit = 0.0f;
 #pragma unroll 1
-                for (int c = 0; c < 128; c += 32) {
+                for (int c = 0; c < cols; c += 32) {
                     load_acc(v, ta + c);
 #pragma unroll
                     for (int j = 0; j < 32; j++) {
-                        if (cols < 128 && c + j >= cols) v[j] = kNegInf;
+                        if (c + j >= cols) v[j] = kNegInf;
                         m = fmaxf(m, v[j]);
                     }
                     if (hits)
@@ -408,22 +413,22 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 const float m0 = m == kNegInf ? 0.0f : m;
                 float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
-                for (int c = 0; c < 128; c += 32) {
+                for (int c = 0; c < cols; c += 32) {
                     load_acc(v, ta + c);
 #pragma unroll
                     for (int j = 0; j < 32; j++) {
-                        if (cols < 128 && c + j >= cols) v[j] = kNegInf;
+                        if (c + j >= cols) v[j] = kNegInf;
                         s[j & 3] += exp2_fast((v[j] - m0) * kLog2e);
                     }
                 }
                 if (row < p.M) {
                     if (target >= 0 && target < cols) p.hit[row] = hit;
-                    p.part[(col0 >> 7) * p.M + row] = make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
+                    p.part[(int64_t)(p.tile_n > 128 ? 2 * ti.nt + half : ti.nt) * p.M + row] = make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
                 }
             } else if (live) {
                 // ratio 0 (a token that does not count) gives 0 whatever its logits
 #pragma unroll 1
-                for (int c = 0; c < 128; c += 32) {
+                for (int c = 0; c < width; c += 32) {
                     load_acc(v, ta + c);
                     const int col = (int)col0 + c;
                     if (MODE == kDh) {
@@ -447,6 +452,8 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         if (lane == 0) tc::bulk_wait_all();
     }
 
+    // what was launched before this kernel is done when this kernel is
+    if (p.wait_end) pdl_wait();
     // Both CTAs have stopped issuing; if either gave up, the even CTA waits
     // (bounded) for the loads still in flight before either may exit.
     tc::fence_before();
@@ -455,7 +462,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     if (leader && warp == 0 && lane == 0) {
         const int peer_abort = tc::ld_cluster_s32(tc::mapa(tc::smem_u32((const void*)abort_flag), 1));
         if (*abort_flag || peer_abort)
-            drain_loads(full0, *issued_slot, tc::ld_cluster_s32(tc::mapa(tc::smem_u32((const void*)issued_slot), 1)));
+            drain_loads(full0, *issued_slot, tc::ld_cluster_s32(tc::mapa(tc::smem_u32((const void*)issued_slot), 1)), p.tx);
     }
     tc::cluster_sync();
     if (warp == 1) {
@@ -495,30 +502,76 @@ struct Operand {
     int64_t rows, cols, ld;
 };
 
+// Order of the tiles: groups of `raster` tiles along m (or n), swept along the
+// other dimension.  A group's strips (a strip: 256 rows of an operand, all of
+// K) that fit in L2 are read from memory once, the other operand once per
+// group; where they do not, each wave of tiles reads the strips it touches.
+// The order with the fewest bytes is taken.  Measured (8192 x 65536 x 4096):
+// 16 row tiles 2.451 ms, 12 2.481, 24 2.458, and 8 or 32 (67 MB, which do not
+// stay) 4 to 6% slower.
+void choose_raster(GemmParams& p, int64_t K, int pairs) {
+    const double strip_a = 512.0 * K, strip_b = 2.0 * p.tile_n * K;
+    const double a_bytes = strip_a * p.m_tiles, b_bytes = strip_b * p.n_tiles;
+    const double waves = (double)p.m_tiles * p.n_tiles / pairs;
+    double best = 0.0;
+    for (int along_n = 0; along_n < 2; along_n++) {
+        const int tiles = along_n ? p.n_tiles : p.m_tiles, others = along_n ? p.m_tiles : p.n_tiles;
+        const double own = along_n ? strip_b : strip_a, other = along_n ? strip_a : strip_b;
+        for (int most = 1; most <= std::min(tiles, 2 * pairs); most++) {
+            const int groups = (tiles + most - 1) / most, g = (tiles + groups - 1) / groups;
+            const double across = std::min<double>(others, std::max(1.0, (double)pairs / g));
+            const double bytes = g * own <= (double)kL2Resident
+                                     ? (along_n ? b_bytes : a_bytes) + groups * (along_n ? a_bytes : b_bytes)
+                                     : waves * (std::min(g, pairs) * own + across * other);
+            if (best == 0.0 || bytes < best) {
+                best = bytes;
+                p.raster = g;
+                p.raster_n = along_n;
+            }
+        }
+    }
+}
+
+// Columns of a pair's tile.  With one or two row tiles the time goes to
+// streaming w, so the pairs should get equally many of its rows: the width
+// that gives the busiest pair the fewest.  (7 tokens x 50021: 196 tiles of 256
+// leave 76 pairs 2 or 3 each, 224 of 224 nearly always 3.)
+int tile_columns(int64_t M, int64_t N, int num_sms) {
+    const int64_t m_tiles = (M + kTile - 1) / kTile, pairs = std::max(1, num_sms / 2);
+    if (m_tiles > 2) return kTile;
+    int best = kTile;
+    int64_t least = INT64_MAX;
+    for (int tn = kTile; tn >= 96; tn -= 32) {
+        const int64_t tiles = m_tiles * ((N + tn - 1) / tn), load = (tiles + pairs - 1) / pairs * tn;
+        if (load < least) {
+            least = load;
+            best = tn;
+        }
+    }
+    return best;
+}
+
+// `beside`: launched so that it may run while the kernel before it on the
+// stream still does (of which it needs nothing); it ends after that kernel.
 template <int MODE>
 cudaError_t gemm(GemmParams p, const Operand& a, const Operand& b, const CUtensorMap* out, int64_t K, int splits,
-                 const HeadArgs& args, cudaStream_t st) {
+                 int tile_n, bool beside, const HeadArgs& args, cudaStream_t st) {
     CUtensorMap ta, tb;
     if (!map_operand(&ta, a.p, a.rows, a.cols, a.ld, a_mn(MODE) ? kSubK : 128) ||
-        !map_operand(&tb, b.p, b.rows, b.cols, b.ld, b_mn(MODE) ? kSubK : 128))
+        !map_operand(&tb, b.p, b.rows, b.cols, b.ld, b_mn(MODE) ? kSubK : tile_n / 2))
         return cudaErrorInvalidValue;
+    p.tile_n = tile_n;
+    p.tx = (uint32_t)(kOpBytes + kSub * (tile_n / 2) * kSubK * 2);
     p.k_stages = (int32_t)((K + kSub * kSubK - 1) / (kSub * kSubK));
     p.mma_last = (int32_t)((K - (int64_t)(p.k_stages - 1) * kSub * kSubK + 15) / 16);
     p.m_tiles = (int32_t)((p.M + kTile - 1) / kTile);
-    p.n_tiles = (int32_t)((p.N + kTile - 1) / kTile);
+    p.n_tiles = (int32_t)((p.N + tile_n - 1) / tile_n);
     p.split_stages = (p.k_stages + splits - 1) / splits;
     p.splits = (p.k_stages + p.split_stages - 1) / p.split_stages;
     const int64_t total = (int64_t)p.m_tiles * p.n_tiles * p.splits;
     if (total > 0x7FFFFFFF) return cudaErrorInvalidValue;
     p.total = (int32_t)total;
-    // one operand stays in L2 while the other streams past it once, where it fits
-    p.raster = kRasterGroup;
-    p.raster_n = 0;
-    const int64_t a_bytes = p.M * K * 2, b_bytes = p.N * K * 2;
-    if (std::min(a_bytes, b_bytes) <= kL2Resident) {
-        p.raster_n = b_bytes < a_bytes;
-        p.raster = p.raster_n ? p.n_tiles : p.m_tiles;
-    }
+    p.wait_end = beside;
     p.status = args.status;
     p.timeout_ns = args.timeout_ns;
     static bool attr_done = false;
@@ -528,8 +581,8 @@ cudaError_t gemm(GemmParams p, const Operand& a, const Operand& b, const CUtenso
         attr_done = true;
     }
     const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(args.num_sms / 2, total));
-    head_gemm_kernel<MODE><<<2 * pairs, kGemmThreads, kSmem, st>>>(ta, tb, out ? *out : ta, p);
-    return cudaGetLastError();
+    choose_raster(p, K, pairs);
+    return launch_k(beside, head_gemm_kernel<MODE>, dim3(2 * pairs), kGemmThreads, kSmem, st, ta, tb, out ? *out : ta, p);
 }
 
 // ------------------------------------------------------- around the products
@@ -543,6 +596,7 @@ __global__ void __launch_bounds__(512) head_join_kernel(const float2* part, int6
     __shared__ float2 joined[G][TT];
     const int tt = threadIdx.x % TT, g = threadIdx.x / TT;
     const int64_t t = (int64_t)blockIdx.x * TT + tt;
+    pdl_wait();
     float m = kNegInf, s = 0.0f;
     if (t < T) {
 #pragma unroll 4
@@ -622,16 +676,23 @@ int dh_splits(int64_t tokens, int64_t cols, int64_t piece, int num_sms) {
     return (int)std::max<int64_t>(1, std::min<int64_t>(num_sms / 2 / tiles, stages / 8));
 }
 
+// parts of a row's statistics
+int64_t head_parts(int64_t tokens, int64_t vocab, int num_sms) {
+    const int tn = tile_columns(tokens, vocab, num_sms);
+    return (vocab + tn - 1) / tn * (tn > 128 ? 2 : 1);
+}
+
 }  // namespace
 
 size_t head_workspace(int64_t tokens, int64_t vocab, int64_t cols, bool backward, int num_sms) {
-    if (!backward) return (size_t)((vocab + 127) / 128 * tokens * 8 + round_up(tokens * 4, 16));
+    if (!backward) return (size_t)(head_parts(tokens, vocab, num_sms) * tokens * 8 + round_up(tokens * 4, 16));
     const int64_t piece = piece_cols(tokens, vocab);
-    return (size_t)(256 + tokens * piece * 2 + dh_splits(tokens, cols, piece, num_sms) * tokens * cols * 4);
+    return (size_t)(256 + (piece < vocab ? 2 : 1) * tokens * piece * 2 +
+                    dh_splits(tokens, cols, piece, num_sms) * tokens * cols * 4);
 }
 
 cudaError_t run_head(const HeadArgs& a, cudaStream_t st) {
-    const int64_t T = a.tokens, parts = (a.vocab + 127) / 128;
+    const int64_t T = a.tokens, parts = head_parts(T, a.vocab, a.num_sms);
     GemmParams p{};
     p.M = T;
     p.N = a.vocab;
@@ -639,30 +700,35 @@ cudaError_t run_head(const HeadArgs& a, cudaStream_t st) {
     p.vocab = a.vocab;
     p.part = static_cast<float2*>(a.ws);
     p.hit = reinterpret_cast<float*>(p.part + parts * T);
-    cudaError_t e = gemm<kStats>(p, {a.h, T, a.cols, a.ldh}, {a.w, a.vocab, a.cols, a.ldw}, nullptr, a.cols, 1, a, st);
+    cudaError_t e = gemm<kStats>(p, {a.h, T, a.cols, a.ldh}, {a.w, a.vocab, a.cols, a.ldw}, nullptr, a.cols, 1,
+                                 tile_columns(T, a.vocab, a.num_sms), false, a, st);
     if (e != cudaSuccess) return e;
-    if (T >= 4096)
-        head_join_kernel<32><<<(unsigned)((T + 31) / 32), 512, 0, st>>>(p.part, parts, T, a.vocab, p.hit, a.targets,
-                                                                       a.loss, a.lse);
-    else
-        head_join_kernel<8><<<(unsigned)((T + 7) / 8), 512, 0, st>>>(p.part, parts, T, a.vocab, p.hit, a.targets,
-                                                                     a.loss, a.lse);
-    return cudaGetLastError();
+    // tokens a CTA: few where there are few, so that more threads share a token's parts
+    const auto k = T >= 4096 ? head_join_kernel<32> : head_join_kernel<8>;
+    const int tt = T >= 4096 ? 32 : 8;
+    return launch_k(true, k, dim3((unsigned)((T + tt - 1) / tt)), 512, 0, st, p.part, parts, T, a.vocab, p.hit, a.targets,
+                    a.loss, a.lse);
 }
 
+// Per piece: g, then dh and dw from it.  dw runs beside dh's last tiles, and
+// the next piece's g (in the other of two buffers) beside dw's: each kernel is
+// launched while the one before it drains, so that no SM waits for the end of
+// a wave.  dh starts only when everything before it is done: it needs g, and
+// its accumulator takes the pieces in order.
 cudaError_t run_head_backward(const HeadArgs& a, cudaStream_t st) {
     const int64_t T = a.tokens, V = a.vocab, D = a.cols, piece = piece_cols(T, V);
     const int splits = dh_splits(T, D, piece, a.num_sms);
     uint8_t* ws = static_cast<uint8_t*>(a.ws);
     float* smax = reinterpret_cast<float*>(ws);
-    uint8_t* g = ws + 256;
-    float* acc = reinterpret_cast<float*>(g + T * piece * 2);
+    uint8_t* g0 = ws + 256;
+    float* acc = reinterpret_cast<float*>(g0 + (piece < V ? 2 : 1) * T * piece * 2);
     head_scale_kernel<<<1, 1024, 0, st>>>(a.dloss, a.targets, T, V, smax);
     cudaError_t e = cudaGetLastError();
     int used = 1;
-    for (int64_t v0 = 0; v0 < V && e == cudaSuccess; v0 += piece) {
+    for (int64_t v0 = 0, i = 0; v0 < V && e == cudaSuccess; v0 += piece, i++) {
         const int64_t n = std::min(piece, V - v0);
         const uint8_t* w = static_cast<const uint8_t*>(a.w) + v0 * a.ldw * 2;
+        uint8_t* g = g0 + (i & 1) * T * piece * 2;
         GemmParams p{};
         p.targets = a.targets;
         p.vocab = V;
@@ -674,13 +740,15 @@ cudaError_t run_head_backward(const HeadArgs& a, cudaStream_t st) {
         p.N = n;
         CUtensorMap out;
         if (!tmap::out_2d(&out, g, T, n, piece, true)) return cudaErrorInvalidValue;
-        e = gemm<kGrad>(p, {a.h, T, D, a.ldh}, {w, n, D, a.ldw}, &out, D, 1, a, st);
+        // without dw in between, the kernel before may be the dh of the piece that this buffer held
+        e = gemm<kGrad>(p, {a.h, T, D, a.ldh}, {w, n, D, a.ldw}, &out, D, 1, tile_columns(T, n, a.num_sms),
+                        i > 0 && a.dh && a.dw, a, st);
         if (e == cudaSuccess && a.dh) {
             p.M = T;
             p.N = D;
             p.add = v0 > 0;
             if (!map_acc(&out, acc, splits, T, D)) return cudaErrorInvalidValue;
-            e = gemm<kDh>(p, {g, T, n, piece}, {w, n, D, a.ldw}, &out, n, splits, a, st);
+            e = gemm<kDh>(p, {g, T, n, piece}, {w, n, D, a.ldw}, &out, n, splits, kTile, false, a, st);
             const int stages = (int)((n + kSub * kSubK - 1) / (kSub * kSubK)), per = (stages + splits - 1) / splits;
             if (v0 == 0) used = (stages + per - 1) / per;          // the splits that the first piece wrote
         }
@@ -689,7 +757,7 @@ cudaError_t run_head_backward(const HeadArgs& a, cudaStream_t st) {
             p.N = D;
             if (!tmap::out_2d(&out, static_cast<uint8_t*>(a.dw) + v0 * a.ld_dw * 2, n, D, a.ld_dw, true))
                 return cudaErrorInvalidValue;
-            e = gemm<kDw>(p, {g, T, n, piece}, {a.h, T, D, a.ldh}, &out, T, 1, a, st);
+            e = gemm<kDw>(p, {g, T, n, piece}, {a.h, T, D, a.ldh}, &out, T, 1, kTile, a.dh != nullptr, a, st);
         }
     }
     if (e == cudaSuccess && a.dh) {

@@ -11,11 +11,14 @@
 // registers as packed 16-byte vectors (elements where rows are not aligned),
 // so the input is read once; the grid is persistent, so weight, bias and the
 // column sums of the backward pass stay in registers over all rows of a
-// group, and the next row is loaded before the current one is worked on.
+// group.  The rows ahead are copied into shared memory (cp.async, each thread
+// its own vectors, so no barrier): DEPTH rows of every group in flight, about
+// 100 KB per SM, what the memory's latency asks for at its rate.
 // The column sums leave as one partial row per CTA, which a second kernel
 // (its programmatic dependent) adds up in a fixed order.  Rows too wide for a
 // group's registers take kernels that read them again from cache.
 #include <algorithm>
+#include <atomic>
 #include "common.cuh"
 #include "internal.h"
 #include "launch.cuh"
@@ -68,6 +71,51 @@ struct Row {
     }
 };
 
+// The rows ahead of a group: a ring of DEPTH slots in shared memory that each
+// thread fills and reads by itself (DEPTH 0: rows whose vectors are single
+// elements; the next row waits in registers instead).
+template <typename T, int VEC, int NV, int DEPTH>
+struct Ahead {
+    Row<T, VEC, NV> next;
+    uint32_t slot0;                // this thread's first vector of slot 0
+    int32_t pitch;                 // bytes between its vectors
+    __device__ __forceinline__ void init(void* ring) {
+        slot0 = (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16;
+        pitch = blockDim.x * 16;
+    }
+    __device__ __forceinline__ void issue(const T* row, bool there, int slot, int at, int tpr, int nvec) {
+        if (DEPTH == 0) {
+            if (there) next.load(row, at, tpr, nvec);
+        } else if (there) {
+#pragma unroll
+            for (int i = 0; i < NV; i++)
+                if (at + i * tpr < nvec)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                                 :: "r"(slot0 + (slot * NV + i) * pitch), "l"(row + (int64_t)(at + i * tpr) * VEC) : "memory");
+        }
+    }
+    __device__ __forceinline__ void read(Row<T, VEC, NV>& r, int slot, int at, int tpr, int nvec) {
+        if (DEPTH == 0) {
+            r = next;
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            r.p[i].zero();
+            if (at + i * tpr < nvec) {
+                uint4 u;
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(slot0 + (slot * NV + i) * pitch) : "memory");
+                if constexpr (VEC > 1) r.p[i].v = *reinterpret_cast<const decltype(r.p[i].v)*>(&u);
+            }
+        }
+    }
+};
+__device__ __forceinline__ void ahead_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all but the youngest N groups of this thread have landed
+template <int N>
+__device__ __forceinline__ void ahead_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+
 template <int VEC, int NV>
 __device__ __forceinline__ void load_params(float (&f)[NV][VEC], const void* p, int bf16, float none, int at, int tpr,
                                             int nvec) {
@@ -78,22 +126,31 @@ __device__ __forceinline__ void load_params(float (&f)[NV][VEC], const void* p, 
             f[i][e] = p && at + i * tpr < nvec ? param(p, bf16, (int64_t)(at + i * tpr) * VEC + e) : none;
 }
 
-template <typename T, int VEC, int NV>
+template <typename T, int VEC, int NV, int DEPTH>
 __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a, int tpr) {
+    extern __shared__ uint4 ring[];                // [DEPTH][NV][threads]
     __shared__ float2 part[2][kMaxThreads / 32];
+    constexpr int AHEAD = DEPTH == 0 ? 1 : DEPTH;
     const int g = threadIdx.x / tpr, at = threadIdx.x % tpr, nvec = (int)(a.cols / VEC);
     const int64_t step = (int64_t)gridDim.x * (blockDim.x / tpr);
     int64_t r = (int64_t)blockIdx.x * (blockDim.x / tpr) + g;
     if (r >= a.rows) return;
     const float C = (float)a.cols;
-    Row<T, VEC, NV> next;
-    next.load(static_cast<const T*>(a.x) + r * a.ldx, at, tpr, nvec);
+    const T* X = static_cast<const T*>(a.x);
+    Ahead<T, VEC, NV, DEPTH> ahead;
+    ahead.init(ring);
+#pragma unroll
+    for (int d = 0; d < AHEAD; d++) {
+        ahead.issue(X + (r + d * step) * a.ldx, r + d * step < a.rows, d, at, tpr, nvec);
+        ahead_commit();
+    }
     float w[NV][VEC], b[NV][VEC];
     load_params<VEC, NV>(w, a.weight, a.param_bf16, 1.0f, at, tpr, nvec);
     load_params<VEC, NV>(b, a.bias, a.param_bf16, 0.0f, at, tpr, nvec);
-    for (; r < a.rows; r += step) {
-        const Row<T, VEC, NV> x = next;
-        if (r + step < a.rows) next.load(static_cast<const T*>(a.x) + (r + step) * a.ldx, at, tpr, nvec);
+    for (int slot = 0; r < a.rows; r += step, slot = slot + 1 == AHEAD ? 0 : slot + 1) {
+        Row<T, VEC, NV> x;
+        ahead_wait<AHEAD - 1>();
+        ahead.read(x, slot, at, tpr, nvec);
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; i++) {
@@ -103,6 +160,9 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a, int
             for (int e = 0; e < VEC; e++) s += f[e];
         }
         const float mean = group_sum(make_float2(s, 0.0f), tpr, part[0]).x / C;
+        // the slot has been read (its values are summed): the row AHEAD steps on takes it
+        ahead.issue(X + (r + AHEAD * step) * a.ldx, r + AHEAD * step < a.rows, slot, at, tpr, nvec);
+        ahead_commit();
         s = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; i++) {
@@ -133,33 +193,41 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a, int
 }
 
 // COLS: also the column sums, one partial row [2][cols] per CTA
-template <typename T, int VEC, int NV, bool PREFETCH, bool COLS>
+template <typename T, int VEC, int NV, int DEPTH, bool COLS>
 __global__ void __launch_bounds__(kMaxThreads) norm_backward_kernel(const NormArgs a, int tpr) {
+    extern __shared__ uint4 ring[];                // x and dy [DEPTH][NV][threads] each; then the sums' meeting
     __shared__ float2 part[2][kMaxThreads / 32];
-    extern __shared__ float merged[];              // [groups - 1][2][cols]
+    constexpr int AHEAD = DEPTH == 0 ? 1 : DEPTH;
     const int groups = blockDim.x / tpr, g = threadIdx.x / tpr, at = threadIdx.x % tpr, nvec = (int)(a.cols / VEC);
     const int64_t step = (int64_t)gridDim.x * groups;
     int64_t r = (int64_t)blockIdx.x * groups + g;
     const float C = (float)a.cols;
     const T* X = static_cast<const T*>(a.x);
     const T* DY = static_cast<const T*>(a.dy);
-    Row<T, VEC, NV> nx, nd;
-    float nmean = 0.0f, nrstd = 0.0f;
-    auto fetch = [&](int64_t row) {
-        nx.load(X + row * a.ldx, at, tpr, nvec);
-        nd.load(DY + row * a.ld_dy, at, tpr, nvec);
-        nmean = a.mean[row];
-        nrstd = a.rstd[row];
+    Ahead<T, VEC, NV, DEPTH> ax, ad;
+    ax.init(ring);
+    ad.init(ring + (size_t)DEPTH * NV * blockDim.x);
+    auto issue = [&](int64_t row, int slot) {
+        ax.issue(X + row * a.ldx, row < a.rows, slot, at, tpr, nvec);
+        ad.issue(DY + row * a.ld_dy, row < a.rows, slot, at, tpr, nvec);
+        ahead_commit();
     };
-    if (PREFETCH && r < a.rows) fetch(r);
+#pragma unroll
+    for (int d = 0; d < AHEAD; d++) issue(r + d * step, d);
+    float nmean = r < a.rows ? a.mean[r] : 0.0f, nrstd = r < a.rows ? a.rstd[r] : 0.0f;
     float w[NV][VEC];
     load_params<VEC, NV>(w, a.weight, a.param_bf16, 1.0f, at, tpr, nvec);
     float dw[NV][VEC] = {}, db[NV][VEC] = {};
-    for (int n = 0; r < a.rows; r += step, n ^= 1) {
-        if (!PREFETCH) fetch(r);
-        const Row<T, VEC, NV> x = nx, d = nd;
+    for (int n = 0, slot = 0; r < a.rows; r += step, n ^= 1, slot = slot + 1 == AHEAD ? 0 : slot + 1) {
+        Row<T, VEC, NV> x, d;
+        ahead_wait<AHEAD - 1>();
+        ax.read(x, slot, at, tpr, nvec);
+        ad.read(d, slot, at, tpr, nvec);
         const float mean = nmean, rstd = nrstd;
-        if (PREFETCH && r + step < a.rows) fetch(r + step);
+        if (r + step < a.rows) {
+            nmean = a.mean[r + step];
+            nrstd = a.rstd[r + step];
+        }
         float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < NV; i++) {
@@ -179,6 +247,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_backward_kernel(const NormAr
             }
         }
         s = group_sum(s, tpr, part[n]);
+        issue(r + AHEAD * step, slot);                     // the slot has been read
         s.x /= C;
         s.y /= C;
         T* dx = static_cast<T*>(a.y) + r * a.ldy;
@@ -200,8 +269,12 @@ __global__ void __launch_bounds__(kMaxThreads) norm_backward_kernel(const NormAr
     }
     if (!COLS) return;
     pdl_launch_dependents();
-    // the CTA's groups meet in shared memory; group 0 adds them in order and writes the partial row
+    // the CTA's groups meet in shared memory, [groups - 1][2][cols]; group 0 adds them in order and
+    // writes the partial row
     const int64_t c0 = a.cols;
+    float* merged = reinterpret_cast<float*>(ring);
+    ahead_wait<0>();
+    if (groups > 1) __syncthreads();
     if (g > 0) {
 #pragma unroll
         for (int i = 0; i < NV; i++)
@@ -385,15 +458,15 @@ __global__ void __launch_bounds__(kWide) norm_wide_dx_kernel(const NormArgs a) {
 }
 
 // ------------------------------------------------------------------- launches
-// Threads of a row's group, of a CTA, and CTAs, for NV vectors a thread.
+// Threads of a row's group, of a CTA, CTAs and shared memory
 struct Shape {
     int tpr, threads, groups;
+    size_t smem;
     unsigned ctas;
 };
 template <typename K>
-Shape shape(K kernel, const NormArgs& a, int vec, int nv, size_t smem_per_group, int per_sm) {
+cudaError_t shape(Shape& s, K kernel, const NormArgs& a, int vec, int nv, int slots, bool cols, int per_sm) {
     const int64_t nvec = a.cols / vec;
-    Shape s;
     s.tpr = (int)((nvec + 32 * nv - 1) / (32 * nv)) * 32;
     if (s.tpr < kMinThreads) {                     // several rows a CTA
         int t = 32;
@@ -404,33 +477,48 @@ Shape shape(K kernel, const NormArgs& a, int vec, int nv, size_t smem_per_group,
         s.threads = s.tpr;
     }
     s.groups = s.threads / s.tpr;
-    int occ = 1;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, s.threads, smem_per_group * (s.groups - 1)) !=
-            cudaSuccess || occ < 1)
-        occ = 1;
+    s.smem = (size_t)slots * nv * s.threads * 16;
+    if (cols) s.smem = std::max(s.smem, (size_t)(s.groups - 1) * 2 * a.cols * sizeof(float));
+    if (s.smem > 40 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+        if (e != cudaSuccess) return e;
+    }
+    // resident CTAs, asked once per kernel and size
+    static std::atomic<uint64_t> known[kMaxThreads / 32 + 1];
+    const uint64_t key = known[s.threads / 32].load(std::memory_order_relaxed);
+    int occ = (int)(key >> 32);
+    if (occ == 0 || (uint32_t)key != (uint32_t)s.smem) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, s.threads, s.smem) != cudaSuccess || occ < 1)
+            occ = 1;
+        known[s.threads / 32].store((uint64_t)occ << 32 | (uint32_t)s.smem, std::memory_order_relaxed);
+    }
     const int64_t most = (int64_t)a.num_sms * std::min(occ, per_sm), want = (a.rows + s.groups - 1) / s.groups;
     s.ctas = (unsigned)std::min(most, want);
-    return s;
+    return cudaSuccess;
 }
 
-template <typename T, int VEC, int NV>
+template <typename T, int VEC, int NV, int DEPTH>
 cudaError_t forward(const NormArgs& a, cudaStream_t st) {
-    const Shape s = shape(norm_kernel<T, VEC, NV>, a, VEC, NV, 0, 16);
-    norm_kernel<T, VEC, NV><<<s.ctas, s.threads, 0, st>>>(a, s.tpr);
+    Shape s;
+    cudaError_t e = shape(s, norm_kernel<T, VEC, NV, DEPTH>, a, VEC, NV, DEPTH, false, 16);
+    if (e != cudaSuccess) return e;
+    norm_kernel<T, VEC, NV, DEPTH><<<s.ctas, s.threads, s.smem, st>>>(a, s.tpr);
     return cudaGetLastError();
 }
 
-template <typename T, int VEC, int NV, bool PREFETCH>
+template <typename T, int VEC, int NV, int DEPTH>
 cudaError_t backward(const NormArgs& a, cudaStream_t st) {
+    Shape s;
     if (!a.dweight && !a.dbias) {
-        const Shape s = shape(norm_backward_kernel<T, VEC, NV, PREFETCH, false>, a, VEC, NV, 0, 16);
-        norm_backward_kernel<T, VEC, NV, PREFETCH, false><<<s.ctas, s.threads, 0, st>>>(a, s.tpr);
+        cudaError_t e = shape(s, norm_backward_kernel<T, VEC, NV, DEPTH, false>, a, VEC, NV, 2 * DEPTH, false, 16);
+        if (e != cudaSuccess) return e;
+        norm_backward_kernel<T, VEC, NV, DEPTH, false><<<s.ctas, s.threads, s.smem, st>>>(a, s.tpr);
         return cudaGetLastError();
     }
-    const size_t per = 2 * a.cols * sizeof(float);
-    Shape s = shape(norm_backward_kernel<T, VEC, NV, PREFETCH, true>, a, VEC, NV, per, 4);
+    cudaError_t e = shape(s, norm_backward_kernel<T, VEC, NV, DEPTH, true>, a, VEC, NV, 2 * DEPTH, true, 4);
+    if (e != cudaSuccess) return e;
     s.ctas = std::min<unsigned>(s.ctas, kMaxParts);
-    norm_backward_kernel<T, VEC, NV, PREFETCH, true><<<s.ctas, s.threads, per * (s.groups - 1), st>>>(a, s.tpr);
+    norm_backward_kernel<T, VEC, NV, DEPTH, true><<<s.ctas, s.threads, s.smem, st>>>(a, s.tpr);
     return launch_k(true, norm_reduce_kernel, dim3((unsigned)((a.cols + 31) / 32), 2), 1024, 0, st, a.ws, (int)s.ctas,
                     a.cols, a.dweight, a.dbias);
 }
@@ -466,13 +554,13 @@ cudaError_t forward_t(const NormArgs& a, cudaStream_t st) {
     constexpr int VEC = kVec<T>;
     if (vectors(a)) {
         const int64_t n = a.cols / VEC;
-        if (n <= kMaxThreads && a.rows <= 2 * a.num_sms) return forward<T, VEC, 1>(a, st);
-        if (n <= 2 * kMaxThreads) return forward<T, VEC, 2>(a, st);
-        if (n <= 4 * kMaxThreads) return forward<T, VEC, 4>(a, st);
+        if (n <= kMaxThreads && a.rows <= 2 * a.num_sms) return forward<T, VEC, 1, 2>(a, st);
+        if (n <= 2 * kMaxThreads) return forward<T, VEC, 2, 4>(a, st);
+        if (n <= 4 * kMaxThreads) return forward<T, VEC, 4, 2>(a, st);
         return forward_wide<T, VEC>(a, st);
     }
-    if (a.cols <= 4 * kMaxThreads) return forward<T, 1, 4>(a, st);
-    if (a.cols <= 16 * kMaxThreads) return forward<T, 1, 16>(a, st);
+    if (a.cols <= 4 * kMaxThreads) return forward<T, 1, 4, 0>(a, st);
+    if (a.cols <= 16 * kMaxThreads) return forward<T, 1, 16, 0>(a, st);
     return forward_wide<T, 1>(a, st);
 }
 
@@ -481,12 +569,12 @@ cudaError_t backward_t(const NormArgs& a, cudaStream_t st) {
     constexpr int VEC = kVec<T>;
     if (vectors(a)) {
         const int64_t n = a.cols / VEC;
-        if (n <= kMaxThreads && a.rows <= 2 * a.num_sms) return backward<T, VEC, 1, true>(a, st);
-        if (n <= 2 * kMaxThreads) return backward<T, VEC, 2, true>(a, st);
+        if (n <= kMaxThreads && a.rows <= 2 * a.num_sms) return backward<T, VEC, 1, 2>(a, st);
+        if (n <= 2 * kMaxThreads) return backward<T, VEC, 2, 3>(a, st);
         return backward_wide<T, VEC>(a, st);
     }
-    if (a.cols <= 4 * kMaxThreads) return backward<T, 1, 4, true>(a, st);
-    if (a.cols <= 16 * kMaxThreads) return backward<T, 1, 16, false>(a, st);
+    if (a.cols <= 4 * kMaxThreads) return backward<T, 1, 4, 0>(a, st);
+    if (a.cols <= 12 * kMaxThreads) return backward<T, 1, 12, 0>(a, st);
     return backward_wide<T, 1>(a, st);
 }
 

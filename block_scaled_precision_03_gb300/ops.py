@@ -24,7 +24,7 @@ from __future__ import annotations
 import ctypes
 from dataclasses import dataclass
 
-from . import OUT_BF16, OUT_F32, BsqError, _check, _stream, lib
+from . import OUT_BF16, OUT_F32, BsqError, _check, lib
 
 ID_I32, ID_I64 = 0, 1
 
@@ -61,6 +61,23 @@ def _signatures():
         "bsq_grad_norm": (i32, [PG, i32, vp, vp, sz, vp]),
         "bsq_clip_grad_norm": (i32, [PG, i32, f32, f32, vp, vp, sz, vp]),
     }
+
+
+_raw_stream = None
+
+
+def _stream(stream, like) -> int:
+    """Handle of the stream to launch on: the given one, or the current one of
+    the tensor's device (by the call behind torch.cuda.current_stream, which
+    costs more than a small kernel here)."""
+    global _raw_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda device: torch.cuda.current_stream(device).cuda_stream)
+    return _raw_stream(like.get_device())
 
 
 # ------------------------------------------------------------- argument checks
@@ -176,7 +193,7 @@ def moe_sort_into(expert_ids, plan: MoePlan, stream=None) -> MoePlan:
     ids, id_type = _ids(expert_ids, p)
     n = lib().bsq_moe_workspace_bytes(p.tokens, p.k, p.num_experts)
     keep, ws = _workspace(n, stream, expert_ids)
-    _check(lib().bsq_moe_sort(ids, id_type, ctypes.byref(p), ws, n, _stream(stream)), "bsq_moe_sort")
+    _check(lib().bsq_moe_sort(ids, id_type, ctypes.byref(p), ws, n, _stream(stream, expert_ids)), "bsq_moe_sort")
     return plan
 
 
@@ -193,7 +210,7 @@ def moe_dispatch_into(x, expert_ids, plan: MoePlan, rows, stream=None):
     n = lib().bsq_moe_workspace_bytes(p.tokens, p.k, p.num_experts)
     keep, ws = _workspace(n, stream, x)
     _check(lib().bsq_moe_dispatch(px, ldx, _type(x, "x"), x.shape[1], ids, id_type, ctypes.byref(p), pr, ldr, ws, n,
-                                  _stream(stream)), "bsq_moe_dispatch")
+                                  _stream(stream, x)), "bsq_moe_dispatch")
     return rows
 
 
@@ -208,7 +225,7 @@ def moe_gather_into(x, plan: MoePlan, rows, stream=None):
     p = plan.c()
     px, ldx = _matrix(x, "x", p.tokens)
     pr, ldr = _matrix(rows, "rows", p.tokens * p.k, x.shape[1], x.dtype)
-    _check(lib().bsq_moe_gather(px, ldx, _type(x, "x"), x.shape[1], ctypes.byref(p), pr, ldr, _stream(stream)),
+    _check(lib().bsq_moe_gather(px, ldx, _type(x, "x"), x.shape[1], ctypes.byref(p), pr, ldr, _stream(stream, x)),
            "bsq_moe_gather")
     return rows
 
@@ -224,7 +241,7 @@ def moe_combine_into(rows, weights, plan: MoePlan, out, stream=None):
     po, ldo = _matrix(out, "out", p.tokens, rows.shape[1], rows.dtype)
     pw = _vector(weights, "weights", p.tokens * p.k, torch.float32)
     _check(lib().bsq_moe_combine(pr, ldr, _type(rows, "rows"), rows.shape[1], pw, ctypes.byref(p), po, ldo,
-                                 _stream(stream)), "bsq_moe_combine")
+                                 _stream(stream, rows)), "bsq_moe_combine")
     return out
 
 
@@ -250,7 +267,7 @@ def moe_combine_backward_into(dout, rows, weights, plan: MoePlan, drows, dweight
     pw = _vector(weights, "weights", p.tokens * p.k, torch.float32)
     pdw = _vector(dweights, "dweights", p.tokens * p.k, torch.float32)
     _check(lib().bsq_moe_combine_backward(pd, ldd, pr, ldr, _type(dout, "dout"), C, pw, ctypes.byref(p), pg, ldg, pdw,
-                                          _stream(stream)), "bsq_moe_combine_backward")
+                                          _stream(stream, dout)), "bsq_moe_combine_backward")
     return drows, dweights
 
 
@@ -279,7 +296,7 @@ def layer_norm_into(x, weight, bias, eps: float, y, mean=None, rstd=None, stream
     pw, pb, pt = _params(weight, bias, C)
     _check(lib().bsq_layer_norm(px, ldx, _type(x, "x"), R, C, pw, pb, pt, eps, py, ldy,
                                 _vector(mean, "mean", R, torch.float32), _vector(rstd, "rstd", R, torch.float32),
-                                _stream(stream)), "bsq_layer_norm")
+                                _stream(stream, x)), "bsq_layer_norm")
     return y, mean, rstd
 
 
@@ -304,7 +321,7 @@ def layer_norm_backward_into(dy, x, weight, mean, rstd, dx, dweight=None, dbias=
     _check(lib().bsq_layer_norm_backward(pdy, ld_dy, px, ldx, _type(x, "x"), R, C, pw, pt,
                                          _vector(mean, "mean", R, f32), _vector(rstd, "rstd", R, f32), pdx, ld_dx,
                                          _vector(dweight, "dweight", C, f32), _vector(dbias, "dbias", C, f32), ws, n,
-                                         _stream(stream)), "bsq_layer_norm_backward")
+                                         _stream(stream, x)), "bsq_layer_norm_backward")
     return dx, dweight, dbias
 
 
@@ -335,7 +352,7 @@ def linear_cross_entropy_into(h, w, targets, loss, lse, stream=None):
     n = lib().bsq_linear_cross_entropy_workspace_bytes(T, V, D, 0)
     keep, ws = _workspace(n, stream, h)
     _check(lib().bsq_linear_cross_entropy(ph, ldh, pw, ldw, pt, T, V, D, _vector(loss, "loss", T, torch.float32),
-                                          _vector(lse, "lse", T, torch.float32), ws, n, _stream(stream)),
+                                          _vector(lse, "lse", T, torch.float32), ws, n, _stream(stream, h)),
            "bsq_linear_cross_entropy")
     return loss, lse
 
@@ -360,7 +377,7 @@ def linear_cross_entropy_backward_into(h, w, targets, lse, dloss, dh, dw, stream
     _check(lib().bsq_linear_cross_entropy_backward(ph, ldh, pw, ldw, pt, T, V, D,
                                                    _vector(lse, "lse", T, torch.float32),
                                                    _vector(dloss, "dloss", T, torch.float32), pdh, ld_dh, pdw, ld_dw,
-                                                   ws, n, _stream(stream)), "bsq_linear_cross_entropy_backward")
+                                                   ws, n, _stream(stream, h)), "bsq_linear_cross_entropy_backward")
     return dh, dw
 
 
@@ -389,6 +406,21 @@ class GradList:
                               _vector(o, f"output {i}", g.numel(), g.dtype), g.numel(), t, 0)
         self.grads, self.outs, self.array = grads, outs, arr
         self.workspace_bytes = int(lib().bsq_grad_workspace_bytes(len(grads)))
+        self._workspaces, self._captured = {}, []
+
+    def workspace(self, stream):
+        """(handle of the launching stream, scratch kept for it): calls on one
+        stream run in order, calls on two get one each.  A call captured in a
+        graph gets its own: the graph may replay beside later calls."""
+        import torch
+        raw = _stream(stream, self.grads[0])
+        if torch.cuda.is_current_stream_capturing():
+            self._captured.append(_workspace(self.workspace_bytes, stream, self.grads[0]))
+            return raw, self._captured[-1][1]
+        ws = self._workspaces.get(raw)
+        if ws is None:
+            ws = self._workspaces[raw] = _workspace(self.workspace_bytes, stream, self.grads[0])
+        return raw, ws[1]
 
 
 def _grad_list(grads) -> GradList:
@@ -400,9 +432,8 @@ def grad_norm(grads, stream=None):
     import torch
     g = _grad_list(grads)
     norm = _new(1, torch.float32, stream, g.grads[0])
-    keep, ws = _workspace(g.workspace_bytes, stream, g.grads[0])
-    _check(lib().bsq_grad_norm(g.array, len(g.grads), norm.data_ptr(), ws, g.workspace_bytes, _stream(stream)),
-           "bsq_grad_norm")
+    raw, ws = g.workspace(stream)
+    _check(lib().bsq_grad_norm(g.array, len(g.grads), norm.data_ptr(), ws, g.workspace_bytes, raw), "bsq_grad_norm")
     return norm
 
 
@@ -410,8 +441,8 @@ def clip_grad_norm_into(grads, max_norm: float, norm, eps: float = 1e-6, stream=
     import torch
     g = _grad_list(grads)
     pn = _vector(norm, "norm", 1, torch.float32)
-    keep, ws = _workspace(g.workspace_bytes, stream, g.grads[0])
-    _check(lib().bsq_clip_grad_norm(g.array, len(g.grads), max_norm, eps, pn, ws, g.workspace_bytes, _stream(stream)),
+    raw, ws = g.workspace(stream)
+    _check(lib().bsq_clip_grad_norm(g.array, len(g.grads), max_norm, eps, pn, ws, g.workspace_bytes, raw),
            "bsq_clip_grad_norm")
     return norm
 
