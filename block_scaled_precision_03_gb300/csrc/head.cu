@@ -18,6 +18,11 @@
 // under the MMAs of the next.  An operand is read in the layout it has in
 // memory: K-major (h and w for the logits, g for dh) or MN-major (w for dh; g
 // and h for dw), so nothing is transposed on the way.
+//
+// Up to kFewTokens tokens the logits' product is bound by streaming w, and runs
+// the other way round, z^T = w h^T: w's rows are the tile's 256 rows and the
+// tokens its 16 to 128 columns, so that a stage is nearly all w and six of them
+// (192 KB per SM) are in flight instead of three half-filled ones.
 #include <algorithm>
 #include <cuda.h>
 #include "common.cuh"
@@ -34,13 +39,15 @@ constexpr int64_t kPieceBytes = 256ll << 20;       // of g
 constexpr float kNegInf = -INFINITY;
 constexpr float kLog2e = 1.44269504088896340736f;
 
-enum { kStats, kGrad, kDh, kDw };
+enum { kStats, kGrad, kDh, kDw, kFewStats, kFewGrad };
 
 // ------------------------------------------------------------ the products
 constexpr int kTile = 256;                          // output rows and columns of a pair
 constexpr int kSubK = 64;                           // K of one 128-byte sub-step
 constexpr int kSub = 2;                             // sub-steps per stage
 constexpr int kStages = 3;
+constexpr int kMaxStages = 6;                       // few tokens: as many as fit
+constexpr int kFewTokens = 128;
 constexpr int kSubBytes = 128 * kSubK * 2;          // one CTA's 128 rows of an operand, one sub-step
 constexpr int kOpBytes = kSub * kSubBytes;
 constexpr int kMmas = 4 * kSub;                     // per stage
@@ -50,6 +57,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kStage = 4096;                        // a warp's staging: two chunks of 32 rows x 64 bytes
 constexpr int kSmem = 1024 + kStages * 2 * kOpBytes + kEpiWarps * kStage + 256;
 static_assert(kSmem <= 232448, "shared memory per block");
+__host__ __device__ constexpr bool is_few(int mode) { return mode == kFewStats || mode == kFewGrad; }
 constexpr int64_t kL2Resident = 40ll << 20;         // operand bytes that stay in L2 while others stream past
 
 // MODE's operand layouts: K-major (false) or MN-major (true)
@@ -62,6 +70,8 @@ struct GemmParams {
     int32_t m_tiles, n_tiles, splits, split_stages, total;
     int32_t raster, raster_n;
     int32_t tile_n;                // output columns of a pair: 256, or fewer where that balances few rows
+    int32_t tile_m;                // rows of a pair: 256, or fewer (few tokens) for balance
+    int32_t stages, b_bytes;       // few tokens: stages, and one CTA's bytes of B per stage
     uint32_t tx;                   // bytes one CTA loads per stage
     int32_t wait_end;              // a programmatic dependent that needs nothing of the kernel before it
     const int64_t* targets;
@@ -69,6 +79,8 @@ struct GemmParams {
     int64_t col0;                  // first vocabulary column of the piece
     float2* part;                  // kStats: [part][M] (max, sum), a part per tile and 128 columns
     float* hit;                    // kStats: the target's logit
+    __nv_bfloat16* g;              // kFewGrad: g [tokens][ld_g]
+    int64_t ld_g;
     const float* lse;
     const float* dloss;
     const float* smax;
@@ -193,17 +205,17 @@ __device__ __forceinline__ TileAt tile_at(const GemmParams& p, int t) {
 }
 
 // After an abort: every stage load in flight lands before the pair exits.
-// Load k goes to stage k % kStages, phase (k / kStages) & 1, on the even CTA,
+// Load k goes to stage k % stages, phase (k / stages) & 1, on the even CTA,
 // which arms each load with both CTAs' bytes; a load that only one CTA issued
 // gets the missing half of that accounting here.
-__device__ __noinline__ void drain_loads(uint32_t full0, int n_own, int n_peer, uint32_t tx) {
+__device__ __noinline__ void drain_loads(uint32_t full0, int stages, int n_own, int n_peer, uint32_t tx) {
     const int n = max(n_own, n_peer);
-    for (int k = max(0, n - kStages); k < n; k++) {
-        const uint32_t bar = full0 + 8 * (uint32_t)(k % kStages);
+    for (int k = max(0, n - stages); k < n; k++) {
+        const uint32_t bar = full0 + 8 * (uint32_t)(k % stages);
         if (k < n_own && k >= n_peer) tc::mbar_complete_tx(bar, tx);
         if (k < n_peer && k >= n_own) tc::mbar_expect_tx(bar, tx);
         volatile int no_abort = 0;
-        tc::mbar_wait(bar, (uint32_t)((k / kStages) & 1), &no_abort, nullptr, 100000000ull);
+        tc::mbar_wait(bar, (uint32_t)((k / stages) & 1), &no_abort, nullptr, 100000000ull);
     }
 }
 
@@ -213,18 +225,22 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                  const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ GemmParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // [stages] of A, [stages] of B, then the epilogue's staging (few tokens: the
+    // tokens' lse, ratio and target); the barriers come last
+    constexpr bool FEW = is_few(MODE);
+    const int S = FEW ? p.stages : kStages, b_bytes = FEW ? p.b_bytes : kOpBytes, sub_b = b_bytes / kSub;
     uint8_t* smA = base;
-    uint8_t* smB = smA + kStages * kOpBytes;
-    uint8_t* smOut = smB + kStages * kOpBytes;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smOut + kEpiWarps * kStage);
+    uint8_t* smB = smA + S * kOpBytes;
+    uint8_t* smOut = smB + S * b_bytes;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(base + (kSmem - 1024 - 256));
     // full[S], empty[S], tfull[2], tempty[2], drain
-    const uint32_t full0 = tc::smem_u32(bars), empty0 = tc::smem_u32(bars + kStages);
-    const uint32_t tfull0 = tc::smem_u32(bars + 2 * kStages), tempty0 = tc::smem_u32(bars + 2 * kStages + 2);
-    const uint32_t drain = tc::smem_u32(bars + 2 * kStages + 4);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 5);
+    const uint32_t full0 = tc::smem_u32(bars), empty0 = tc::smem_u32(bars + kMaxStages);
+    const uint32_t tfull0 = tc::smem_u32(bars + 2 * kMaxStages), tempty0 = tc::smem_u32(bars + 2 * kMaxStages + 2);
+    const uint32_t drain = tc::smem_u32(bars + 2 * kMaxStages + 4);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 5);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     volatile int* issued_slot = reinterpret_cast<volatile int*>(tmem_slot + 2);
-    static_assert(8 * (2 * kStages + 5) + 12 <= 256, "barrier area");
+    static_assert(8 * (2 * kMaxStages + 5) + 12 <= 256, "barrier area");
 
     // a kernel that may run beside this one starts as soon as SMs are free
     pdl_launch_dependents();
@@ -234,7 +250,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
 
     if (warp == 0 && lane == 0) {
-        for (int s = 0; s < kStages; s++) {
+        for (int s = 0; s < S; s++) {
             tc::mbar_init(full0 + 8 * s, 1);
             tc::mbar_init(empty0 + 8 * s, 1);
         }
@@ -250,6 +266,26 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         tc::prefetch_tmap(&tmB);
     }
     if (warp == 1) tc::tmem_alloc<2>(tc::smem_u32(tmem_slot), kTmemCols);
+    float* few_lse = reinterpret_cast<float*>(smOut);
+    float* few_ratio = few_lse + kFewTokens;
+    int64_t* few_target = reinterpret_cast<int64_t*>(few_ratio + kFewTokens);
+    if (FEW) {
+        // rows of A that no load fills (tile_m below 256) are read by the MMAs all the same
+        const int rows = p.tile_m / 2;
+        for (int i = threadIdx.x; i < S * kSub * (128 - rows) * 8; i += kGemmThreads) {
+            const int block = i / ((128 - rows) * 8), at = i - block * ((128 - rows) * 8);
+            reinterpret_cast<uint4*>(smA + block * kSubBytes + rows * 128)[at] = make_uint4(0, 0, 0, 0);
+        }
+        tc::fence_async_smem();
+        for (int t = threadIdx.x; t < kFewTokens; t += kGemmThreads) {
+            const int64_t id = t < p.N ? p.targets[t] : -1;
+            const bool counts = id >= 0 && id < p.vocab;
+            few_target[t] = counts ? id - p.col0 : -1;
+            const float smax = MODE == kFewGrad ? *p.smax : 0.0f;
+            few_lse[t] = MODE == kFewGrad && counts ? p.lse[t] : 0.0f;
+            few_ratio[t] = MODE == kFewGrad && counts && smax > 0.0f ? p.dloss[t] / smax : 0.0f;
+        }
+    }
     tc::fence_before();
     __syncthreads();
     tc::cluster_sync();
@@ -265,7 +301,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             bool ok = true;
             for (int t = cid; t < p.total && ok; t += ncl) {
                 const TileAt ti = tile_at(p, t);
-                const int am = ti.mt * kTile + (int)rank * 128, bn = ti.nt * p.tile_n + (int)rank * (p.tile_n / 2);
+                const int am = ti.mt * p.tile_m + (int)rank * (p.tile_m / 2), bn = ti.nt * p.tile_n + (int)rank * (p.tile_n / 2);
                 for (int kb = ti.k0; kb < ti.k1; kb++) {
                     if (!tc::mbar_wait(empty0 + 8 * stage, phase ^ 1, abort_flag, p.status, p.timeout_ns)) {
                         ok = false;
@@ -277,7 +313,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     for (int j = 0; j < kSub; j++) {
                         const int k = (kb * kSub + j) * kSubK;
                         const uint32_t da = tc::smem_u32(smA + stage * kOpBytes + j * kSubBytes);
-                        const uint32_t db = tc::smem_u32(smB + stage * kOpBytes + j * kSubBytes);
+                        const uint32_t db = tc::smem_u32(smB + stage * b_bytes + j * sub_b);
                         if (a_mn(MODE)) {
                             tc::tma_load_2d_pair(da, &tmA, am, k, fb);
                             tc::tma_load_2d_pair(da + 8192, &tmA, am + 64, k, fb);
@@ -292,7 +328,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                         }
                     }
                     ++issued;
-                    if (++stage == kStages) { stage = 0; phase ^= 1; }
+                    if (++stage == S) { stage = 0; phase ^= 1; }
                 }
             }
             *issued_slot = issued;
@@ -324,8 +360,8 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     }
                     tc::fence_after();
                     const uint64_t ad = ad0 + (uint64_t)(stage * (kOpBytes >> 4));
-                    const uint64_t bd = bd0 + (uint64_t)(stage * (kOpBytes >> 4));
-                    const int next = stage + 1 == kStages ? 0 : stage + 1;
+                    const uint64_t bd = bd0 + (uint64_t)(stage * (b_bytes >> 4));
+                    const int next = stage + 1 == S ? 0 : stage + 1;
                     const uint32_t next_phase = next == 0 ? phase ^ 1 : phase;
                     if (kb != p.k_stages - 1 || p.mma_last == kMmas) {
                         // the next stage's barrier is tested while this stage's MMAs run
@@ -333,12 +369,12 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                         for (int m = 0; m < kMmas; m++) {
                             if (m == kMmas - 1) ready = tc::mbar_test(full0 + 8 * next, next_phase);
                             mma_bf16(d, ad + (m >> 2) * (kSubBytes >> 4) + (m & 3) * a_step,
-                                     bd + (m >> 2) * (kSubBytes >> 4) + (m & 3) * b_step, idesc, (kb != ti.k0) | (m != 0));
+                                     bd + (m >> 2) * (sub_b >> 4) + (m & 3) * b_step, idesc, (kb != ti.k0) | (m != 0));
                         }
                     } else {
                         for (int m = 0; m < p.mma_last; m++)
                             mma_bf16(d, ad + (m >> 2) * (kSubBytes >> 4) + (m & 3) * a_step,
-                                     bd + (m >> 2) * (kSubBytes >> 4) + (m & 3) * b_step, idesc, (kb != ti.k0) | (m != 0));
+                                     bd + (m >> 2) * (sub_b >> 4) + (m & 3) * b_step, idesc, (kb != ti.k0) | (m != 0));
                         ready = false;
                     }
                     any = true;
@@ -364,10 +400,55 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         const uint32_t stage_buf = tc::smem_u32(smOut + (warp - 2) * kStage);
         const float smax = MODE == kGrad || MODE == kDw ? *p.smax : 1.0f;
         int iter = 0, n = 0;
+        if (FEW) {
+            // A thread owns one row of w and the tokens 64 half ... 64 half + 63.
+            for (int t = cid; t < p.total; t += ncl, ++iter) {
+                const int buf = iter & 1, local = (int)rank * (p.tile_m / 2) + q * 32 + lane;
+                const int64_t row = (int64_t)tile_at(p, t).mt * p.tile_m + local;      // vocabulary row of the piece
+                const bool in = q * 32 + lane < p.tile_m / 2 && row < p.M;
+                const int64_t part = ((int64_t)tile_at(p, t).mt * 2 + rank) * 4 + q;
+                if (!tc::mbar_wait(tfull0 + 8 * buf, (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns)) break;
+                tc::fence_after();
+                const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kTile);
+#pragma unroll 1
+                for (int c = 64 * half; c < 64 * half + 64 && c < p.N; c += 32) {
+                    float v[32];
+                    load_acc(v, ta + c);
+                    float mine_m = kNegInf, mine_s = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 32; j++) {
+                        if (c + j >= p.N) break;
+                        const bool hit = in && row == few_target[c + j];
+                        if (MODE == kFewStats) {
+                            if (hit) p.hit[c + j] = v[j];
+                            const float z = in ? v[j] : kNegInf;
+                            float m = z;
+#pragma unroll
+                            for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+                            float e = exp2_fast((z - (m == kNegInf ? 0.0f : m)) * kLog2e);
+#pragma unroll
+                            for (int d = 16; d; d >>= 1) e += __shfl_xor_sync(0xffffffffu, e, d);
+                            if (lane == j) {
+                                mine_m = m;
+                                mine_s = e;
+                            }
+                        } else if (in) {
+                            const float ratio = few_ratio[c + j];
+                            const float g = exp2_fast((v[j] - few_lse[c + j]) * kLog2e) - (hit ? 1.0f : 0.0f);
+                            p.g[(int64_t)(c + j) * p.ld_g + row] = __float2bfloat16_rn(ratio == 0.0f ? 0.0f : g * ratio);
+                        }
+                    }
+                    if (MODE == kFewStats && c + lane < p.N) p.part[part * p.N + c + lane] = make_float2(mine_m, mine_s);
+                }
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_cluster(tempty_c0 + 8 * buf);
+            }
+        } else
         for (int t = cid; t < p.total; t += ncl, ++iter) {
             const TileAt ti = tile_at(p, t);
             const int buf = iter & 1;
-            const int64_t row0 = (int64_t)ti.mt * kTile + rank * 128 + q * 32, row = row0 + lane;
+            const int64_t row0 = (int64_t)ti.mt * kTile + rank * 128 + q * 32, row = row0 + lane;       // tile_m is 256
             const int64_t col0 = (int64_t)ti.nt * p.tile_n + half * 128;
             const int width = min(128, p.tile_n - half * 128);       // of the tile's columns, this thread's
             // what the row needs, read while the tile is computed
@@ -462,7 +543,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     if (leader && warp == 0 && lane == 0) {
         const int peer_abort = tc::ld_cluster_s32(tc::mapa(tc::smem_u32((const void*)abort_flag), 1));
         if (*abort_flag || peer_abort)
-            drain_loads(full0, *issued_slot, tc::ld_cluster_s32(tc::mapa(tc::smem_u32((const void*)issued_slot), 1)), p.tx);
+            drain_loads(full0, S, *issued_slot, tc::ld_cluster_s32(tc::mapa(tc::smem_u32((const void*)issued_slot), 1)), p.tx);
     }
     tc::cluster_sync();
     if (warp == 1) {
@@ -532,39 +613,46 @@ void choose_raster(GemmParams& p, int64_t K, int pairs) {
     }
 }
 
-// Columns of a pair's tile.  With one or two row tiles the time goes to
-// streaming w, so the pairs should get equally many of its rows: the width
-// that gives the busiest pair the fewest.  (7 tokens x 50021: 196 tiles of 256
-// leave 76 pairs 2 or 3 each, 224 of 224 nearly always 3.)
-int tile_columns(int64_t M, int64_t N, int num_sms) {
-    const int64_t m_tiles = (M + kTile - 1) / kTile, pairs = std::max(1, num_sms / 2);
-    if (m_tiles > 2) return kTile;
+// Rows of w that a pair takes at a time when the time goes to streaming w (few
+// tokens): the pairs should get equally many, so the size that gives the
+// busiest pair the fewest.  (50021 rows: 196 tiles of 256 leave 76 pairs 2 or 3
+// each, 224 of 224 nearly always 3.)
+int stream_rows(int64_t vocab, int num_sms, int step) {
+    const int64_t pairs = std::max(1, num_sms / 2);
     int best = kTile;
     int64_t least = INT64_MAX;
-    for (int tn = kTile; tn >= 96; tn -= 32) {
-        const int64_t tiles = m_tiles * ((N + tn - 1) / tn), load = (tiles + pairs - 1) / pairs * tn;
+    for (int t = kTile; t >= 96; t -= step) {
+        const int64_t load = ((vocab + t - 1) / t + pairs - 1) / pairs * t;
         if (load < least) {
             least = load;
-            best = tn;
+            best = t;
         }
     }
     return best;
+}
+// Columns of a pair's tile in the token-major products: as above with one row
+// tile, else 256 (a tile's MMAs then hide the loads).
+int tile_columns(int64_t tokens, int64_t vocab, int num_sms) {
+    return tokens <= kTile ? stream_rows(vocab, num_sms, 32) : kTile;
 }
 
 // `beside`: launched so that it may run while the kernel before it on the
 // stream still does (of which it needs nothing); it ends after that kernel.
 template <int MODE>
 cudaError_t gemm(GemmParams p, const Operand& a, const Operand& b, const CUtensorMap* out, int64_t K, int splits,
-                 int tile_n, bool beside, const HeadArgs& args, cudaStream_t st) {
+                 int tile_m, int tile_n, bool beside, const HeadArgs& args, cudaStream_t st) {
     CUtensorMap ta, tb;
-    if (!map_operand(&ta, a.p, a.rows, a.cols, a.ld, a_mn(MODE) ? kSubK : 128) ||
+    if (!map_operand(&ta, a.p, a.rows, a.cols, a.ld, a_mn(MODE) ? kSubK : tile_m / 2) ||
         !map_operand(&tb, b.p, b.rows, b.cols, b.ld, b_mn(MODE) ? kSubK : tile_n / 2))
         return cudaErrorInvalidValue;
     p.tile_n = tile_n;
-    p.tx = (uint32_t)(kOpBytes + kSub * (tile_n / 2) * kSubK * 2);
     p.k_stages = (int32_t)((K + kSub * kSubK - 1) / (kSub * kSubK));
     p.mma_last = (int32_t)((K - (int64_t)(p.k_stages - 1) * kSub * kSubK + 15) / 16);
-    p.m_tiles = (int32_t)((p.M + kTile - 1) / kTile);
+    p.tile_m = tile_m;
+    p.b_bytes = kSub * (tile_n / 2) * kSubK * 2;
+    p.stages = std::min(kMaxStages, (kSmem - 1024 - 256 - 4096) / (kOpBytes + p.b_bytes));
+    p.tx = (uint32_t)(kSub * (tile_m / 2) * kSubK * 2 + p.b_bytes);
+    p.m_tiles = (int32_t)((p.M + tile_m - 1) / tile_m);
     p.n_tiles = (int32_t)((p.N + tile_n - 1) / tile_n);
     p.split_stages = (p.k_stages + splits - 1) / splits;
     p.splits = (p.k_stages + p.split_stages - 1) / p.split_stages;
@@ -678,6 +766,10 @@ int dh_splits(int64_t tokens, int64_t cols, int64_t piece, int num_sms) {
 
 // parts of a row's statistics
 int64_t head_parts(int64_t tokens, int64_t vocab, int num_sms) {
+    if (tokens <= kFewTokens) {
+        const int tm = stream_rows(vocab, num_sms, 16);
+        return (vocab + tm - 1) / tm * 8;
+    }
     const int tn = tile_columns(tokens, vocab, num_sms);
     return (vocab + tn - 1) / tn * (tn > 128 ? 2 : 1);
 }
@@ -700,8 +792,14 @@ cudaError_t run_head(const HeadArgs& a, cudaStream_t st) {
     p.vocab = a.vocab;
     p.part = static_cast<float2*>(a.ws);
     p.hit = reinterpret_cast<float*>(p.part + parts * T);
-    cudaError_t e = gemm<kStats>(p, {a.h, T, a.cols, a.ldh}, {a.w, a.vocab, a.cols, a.ldw}, nullptr, a.cols, 1,
-                                 tile_columns(T, a.vocab, a.num_sms), false, a, st);
+    const Operand h{a.h, T, a.cols, a.ldh}, w{a.w, a.vocab, a.cols, a.ldw};
+    cudaError_t e;
+    if (T <= kFewTokens) {
+        std::swap(p.M, p.N);
+        e = gemm<kFewStats>(p, w, h, nullptr, a.cols, 1, stream_rows(a.vocab, a.num_sms, 16), (int)round_up(T, 16), false, a, st);
+    } else {
+        e = gemm<kStats>(p, h, w, nullptr, a.cols, 1, kTile, tile_columns(T, a.vocab, a.num_sms), false, a, st);
+    }
     if (e != cudaSuccess) return e;
     // tokens a CTA: few where there are few, so that more threads share a token's parts
     const auto k = T >= 4096 ? head_join_kernel<32> : head_join_kernel<8>;
@@ -739,16 +837,25 @@ cudaError_t run_head_backward(const HeadArgs& a, cudaStream_t st) {
         p.M = T;
         p.N = n;
         CUtensorMap out;
-        if (!tmap::out_2d(&out, g, T, n, piece, true)) return cudaErrorInvalidValue;
+        const Operand h{a.h, T, D, a.ldh}, wp{w, n, D, a.ldw}, gp{g, T, n, piece};
         // without dw in between, the kernel before may be the dh of the piece that this buffer held
-        e = gemm<kGrad>(p, {a.h, T, D, a.ldh}, {w, n, D, a.ldw}, &out, D, 1, tile_columns(T, n, a.num_sms),
-                        i > 0 && a.dh && a.dw, a, st);
+        const bool beside = i > 0 && a.dh && a.dw;
+        if (T <= kFewTokens) {
+            p.M = n;
+            p.N = T;
+            p.g = reinterpret_cast<__nv_bfloat16*>(g);
+            p.ld_g = piece;
+            e = gemm<kFewGrad>(p, wp, h, nullptr, D, 1, stream_rows(n, a.num_sms, 16), (int)round_up(T, 16), beside, a, st);
+        } else {
+            if (!tmap::out_2d(&out, g, T, n, piece, true)) return cudaErrorInvalidValue;
+            e = gemm<kGrad>(p, h, wp, &out, D, 1, kTile, tile_columns(T, n, a.num_sms), beside, a, st);
+        }
         if (e == cudaSuccess && a.dh) {
             p.M = T;
             p.N = D;
             p.add = v0 > 0;
             if (!map_acc(&out, acc, splits, T, D)) return cudaErrorInvalidValue;
-            e = gemm<kDh>(p, {g, T, n, piece}, {w, n, D, a.ldw}, &out, n, splits, kTile, false, a, st);
+            e = gemm<kDh>(p, gp, wp, &out, n, splits, kTile, kTile, false, a, st);
             const int stages = (int)((n + kSub * kSubK - 1) / (kSub * kSubK)), per = (stages + splits - 1) / splits;
             if (v0 == 0) used = (stages + per - 1) / per;          // the splits that the first piece wrote
         }
@@ -757,7 +864,7 @@ cudaError_t run_head_backward(const HeadArgs& a, cudaStream_t st) {
             p.N = D;
             if (!tmap::out_2d(&out, static_cast<uint8_t*>(a.dw) + v0 * a.ld_dw * 2, n, D, a.ld_dw, true))
                 return cudaErrorInvalidValue;
-            e = gemm<kDw>(p, {g, T, n, piece}, {a.h, T, D, a.ldh}, &out, T, 1, kTile, a.dh != nullptr, a, st);
+            e = gemm<kDw>(p, gp, h, &out, T, 1, kTile, kTile, a.dh != nullptr, a, st);
         }
     }
     if (e == cudaSuccess && a.dh) {

@@ -84,6 +84,58 @@ struct Pack<float, 1> {
     __device__ __forceinline__ void unpack(float (&f)[1]) const { f[0] = v; }
     __device__ __forceinline__ void pack(const float (&f)[1]) { v = f[0]; }
 };
+// Two FP32 values in a register pair, for the packed FP32 instructions (two
+// IEEE operations each)
+struct F2 {
+    unsigned long long v;
+    __device__ __forceinline__ F2() {}
+    __device__ __forceinline__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+    __device__ __forceinline__ explicit F2(float a) : F2(a, a) {}
+    __device__ __forceinline__ float2 get() const {
+        float2 f;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+        return f;
+    }
+};
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ void unpack2(const Pack<__nv_bfloat16, 8>& p, F2 (&f)[4]) {
+    const uint32_t w[4] = {p.v.x, p.v.y, p.v.z, p.v.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) f[i] = F2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+__device__ __forceinline__ void unpack2(const Pack<float, 4>& p, F2 (&f)[2]) {
+    f[0] = F2(p.v.x, p.v.y);
+    f[1] = F2(p.v.z, p.v.w);
+}
+__device__ __forceinline__ void pack2(Pack<__nv_bfloat16, 8>& p, const F2 (&f)[4]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const float2 x = f[i].get();
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    p.v = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void pack2(Pack<float, 4>& p, const F2 (&f)[2]) {
+    const float2 a = f[0].get(), b = f[1].get();
+    p.v = make_float4(a.x, a.y, b.x, b.y);
+}
+
 template <typename T>
 constexpr int kVec = 16 / (int)sizeof(T);
 

@@ -271,21 +271,25 @@ __global__ void __launch_bounds__(kSortThreads) moe_small_kernel(const SortArgs 
     }
 }
 
-constexpr int kSlots = 8;              // slots of a token handled together
+// Slots of a token handled together: 8 vectors (the usual k in one pass), or 4
+// single elements of 4 columns each.  (Odd combine of 1021 x 3 x 2047: 9.3 us
+// with 4, 12.3 with 8.)
+template <int VEC>
+constexpr int kSlots = VEC == 1 ? 4 : 8;
 
 // out[t] = sum_j weights[t, j] rows[slot_row[t, j]], in the order of j
 template <typename T, int VEC, int WPT, bool WEIGHTED>
 __global__ void __launch_bounds__(kRowThreads) moe_combine_kernel(const RowArgs a) {
-    constexpr int UN = VEC == 1 ? 4 : 1;
+    constexpr int UN = VEC == 1 ? 4 : 1, S = kSlots<VEC>;
     const Place at = place<WPT>();
     if (at.t >= a.tokens) return;
     const T* src = static_cast<const T*>(a.src);
     T* out = static_cast<T*>(a.dst) + at.t * a.ld_dst;
-    int32_t row[kSlots];
-    float w[kSlots];
+    int32_t row[S];
+    float w[S];
     auto slots = [&](int j0) {
 #pragma unroll
-        for (int j = 0; j < kSlots; j++) {
+        for (int j = 0; j < S; j++) {
             row[j] = j0 + j < a.k ? a.slot_row[at.t * a.k + j0 + j] : -1;
             w[j] = WEIGHTED && row[j] >= 0 ? a.weights[at.t * a.k + j0 + j] : 1.0f;
         }
@@ -293,17 +297,17 @@ __global__ void __launch_bounds__(kRowThreads) moe_combine_kernel(const RowArgs 
     slots(0);
     for (int v = at.v0; v < a.nvec; v += UN * at.step) {
         float acc[UN][VEC] = {};
-        for (int j0 = 0; j0 < a.k; j0 += kSlots) {
-            if (a.k > kSlots) slots(j0);
-            Pack<T, VEC> p[UN][kSlots];
+        for (int j0 = 0; j0 < a.k; j0 += S) {
+            if (a.k > S) slots(j0);
+            Pack<T, VEC> p[UN][S];
 #pragma unroll
-            for (int j = 0; j < kSlots; j++)
+            for (int j = 0; j < S; j++)
 #pragma unroll
                 for (int u = 0; u < UN; u++)
                     if (row[j] >= 0 && v + u * at.step < a.nvec)
                         p[u][j].load(src + row[j] * a.ld_src + (int64_t)(v + u * at.step) * VEC);
 #pragma unroll
-            for (int j = 0; j < kSlots; j++)
+            for (int j = 0; j < S; j++)
                 if (row[j] >= 0)
 #pragma unroll
                     for (int u = 0; u < UN; u++) {
@@ -324,34 +328,36 @@ __global__ void __launch_bounds__(kRowThreads) moe_combine_kernel(const RowArgs 
     }
 }
 
-// drows[row] = weights[slot] dout[t], dweights[slot] = dout[t] . rows[row]
+// drows[row] = weights[slot] dout[t], dweights[slot] = dout[t] . rows[row].
+// Three CTAs per SM (80 registers): the batch of 32768 x 7168 takes 156 us,
+// with two (98 registers) 209, with four (spills) 176.
 template <typename T, int VEC, int WPT, bool DOT>
-__global__ void __launch_bounds__(kRowThreads) moe_combine_backward_kernel(const RowArgs a) {
-    constexpr int UN = VEC == 1 ? 4 : 1;
-    __shared__ float part[kRowThreads / 32][kSlots];
+__global__ void __launch_bounds__(kRowThreads, 3) moe_combine_backward_kernel(const RowArgs a) {
+    constexpr int UN = VEC == 1 ? 4 : 1, S = kSlots<VEC>;
+    __shared__ float part[kRowThreads / 32][S];
     const Place at = place<WPT>();
     const bool live = at.t < a.tokens;
     const T* dout = static_cast<const T*>(a.src) + (live ? at.t : 0) * a.ld_src;
     const T* rows = static_cast<const T*>(a.rows);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int j0 = 0; j0 < a.k; j0 += kSlots) {
-        int32_t row[kSlots];
-        float w[kSlots], dot[kSlots];
+    for (int j0 = 0; j0 < a.k; j0 += S) {
+        int32_t row[S];
+        float w[S], dot[S];
 #pragma unroll
-        for (int j = 0; j < kSlots; j++) {
+        for (int j = 0; j < S; j++) {
             row[j] = live && j0 + j < a.k ? a.slot_row[at.t * a.k + j0 + j] : -1;
             w[j] = row[j] >= 0 ? a.weights[at.t * a.k + j0 + j] : 0.0f;
             dot[j] = 0.0f;
         }
         for (int v = live ? at.v0 : a.nvec; v < a.nvec; v += UN * at.step) {
-            Pack<T, VEC> d[UN], p[UN][kSlots];
+            Pack<T, VEC> d[UN], p[UN][S];
 #pragma unroll
             for (int u = 0; u < UN; u++) {
                 if (v + u * at.step >= a.nvec) continue;
                 d[u].load(dout + (int64_t)(v + u * at.step) * VEC);
                 if (DOT)
 #pragma unroll
-                    for (int j = 0; j < kSlots; j++)
+                    for (int j = 0; j < S; j++)
                         if (row[j] >= 0) p[u][j].load(rows + row[j] * a.ld_rows + (int64_t)(v + u * at.step) * VEC);
             }
 #pragma unroll
@@ -360,7 +366,7 @@ __global__ void __launch_bounds__(kRowThreads) moe_combine_backward_kernel(const
                 float f[VEC];
                 d[u].unpack(f);
 #pragma unroll
-                for (int j = 0; j < kSlots; j++) {
+                for (int j = 0; j < S; j++) {
                     if (row[j] < 0) continue;
                     float o[VEC];
                     if (DOT) {
@@ -378,16 +384,16 @@ __global__ void __launch_bounds__(kRowThreads) moe_combine_backward_kernel(const
         }
         if (DOT) {
 #pragma unroll
-            for (int j = 0; j < kSlots; j++)
+            for (int j = 0; j < S; j++)
 #pragma unroll
                 for (int d = 16; d; d >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], d);
             __syncthreads();
             if (lane == 0)
 #pragma unroll
-                for (int j = 0; j < kSlots; j++) part[warp][j] = dot[j];
+                for (int j = 0; j < S; j++) part[warp][j] = dot[j];
             __syncthreads();
             const int j = threadIdx.x % (32 * WPT);
-            if (live && j < kSlots && j0 + j < a.k) {
+            if (live && j < S && j0 + j < a.k) {
                 float s = 0.0f;
 #pragma unroll
                 for (int x = 0; x < WPT; x++) s += part[warp / WPT * WPT + x][j];

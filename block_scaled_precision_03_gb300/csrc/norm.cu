@@ -7,18 +7,25 @@
 //   dx = rstd (g - sum(g) / C - xh sum(g xh) / C),
 //   dw = sum over the rows of dy xh, db = sum over the rows of dy.
 //
-// Both are bound by memory.  A group of threads owns a row and holds it in
-// registers as packed 16-byte vectors (elements where rows are not aligned),
-// so the input is read once; the grid is persistent, so weight, bias and the
-// column sums of the backward pass stay in registers over all rows of a
-// group.  The rows ahead are copied into shared memory (cp.async, each thread
-// its own vectors, so no barrier): DEPTH rows of every group in flight, about
-// 100 KB per SM, what the memory's latency asks for at its rate.
-// The column sums leave as one partial row per CTA, which a second kernel
-// (its programmatic dependent) adds up in a fixed order.  Rows too wide for a
-// group's registers take kernels that read them again from cache.
+// Both are bound by memory; a row is read once and held in registers as packed
+// 16-byte vectors.  The vectors lie on 16-byte boundaries of memory, so rows
+// that start elsewhere (odd widths) take a vector at either end that is only
+// partly theirs, moved element by element.
+//
+// Forward: a group of lanes owns a row, one warp up to 512 vectors, so most
+// rows need no barrier at all; many independent rows per SM hide the latency
+// of their two sums.  (A block of 256 threads per row, two barriers each, took
+// 46 us on 8192 x 4096 whatever was prefetched: the barriers, not the loads,
+// held it.)
+//
+// Backward with column sums: a thread keeps its columns' weight and sums in
+// registers over all rows of a persistent CTA; the rows ahead are copied into shared memory
+// (cp.async, each thread its own vectors, so no barrier there).  Each CTA
+// leaves one partial row, and a second kernel (its programmatic dependent)
+// adds them up in a fixed order.  Where columns and threads do not line up
+// (rows that start off 16-byte boundaries) or are too many for the registers,
+// the column sums take a pass of their own.
 #include <algorithm>
-#include <atomic>
 #include "common.cuh"
 #include "internal.h"
 #include "launch.cuh"
@@ -26,164 +33,243 @@
 namespace bsq {
 namespace {
 
-constexpr int kMaxThreads = 512;       // of a row's group: 128 registers each
-constexpr int kMinThreads = 128;       // of a CTA
+constexpr int kMaxThreads = 512;       // of a CTA: 128 registers each
+constexpr int kCta = 128;              // of a CTA of several rows
 constexpr int kMaxParts = 608;         // partial rows of the column sums: 4 CTAs on each of 152 SMs
 constexpr int kWide = 512;             // threads of the kernels for wide rows
 constexpr int kWideParts = 128;
+constexpr int kMaxOddCols = 16384;     // weight and bias in shared memory
 
 __device__ __forceinline__ float param(const void* p, int bf16, int64_t c) {
     return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[c]) : static_cast<const float*>(p)[c];
 }
-
-// Sum over a row's group of `tpr` threads, the same bits in every thread.
-// part: one float2 per warp of the CTA, not the one of the group's previous
-// sum (its readers may still be at it).
-__device__ __forceinline__ float2 group_sum(float2 v, int tpr, float2* part) {
+// VEC parameters from column c.  The loads are volatile: they do not change
+// from row to row, and the compiler would otherwise keep a whole row's worth of
+// them in registers (NV 16 spilled 1.3 KB); they come from L1.
+template <int VEC>
+__device__ __forceinline__ void params(float (&f)[VEC], const void* p, int bf16, float none, int64_t c) {
+    if (!p) {
 #pragma unroll
-    for (int d = 16; d; d >>= 1) {
-        v.x += __shfl_xor_sync(0xffffffffu, v.x, d);
-        v.y += __shfl_xor_sync(0xffffffffu, v.y, d);
+        for (int e = 0; e < VEC; e++) f[e] = none;
+    } else if (!bf16 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 4)
+            asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(f[e]), "=f"(f[e + 1]), "=f"(f[e + 2]), "=f"(f[e + 3])
+                         : "l"(static_cast<const float*>(p) + c + e));
+    } else if (VEC == 8 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+        uint32_t w[4];
+        asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(static_cast<const __nv_bfloat16*>(p) + c));
+#pragma unroll
+        for (int e = 0; e < VEC; e++) f[e] = e & 1 ? bf16hi(w[(e >> 1) & 3]) : bf16lo(w[(e >> 1) & 3]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; e++) f[e] = param(p, bf16, c + e);
     }
-    if (tpr == 32) return v;
-    const int warp = threadIdx.x >> 5, wpr = tpr >> 5, g = warp / wpr;
-    if ((threadIdx.x & 31) == 0) part[warp] = v;
-    asm volatile("bar.sync %0, %1;" :: "r"(g + 1), "r"(tpr) : "memory");
-    float2 s = make_float2(0.0f, 0.0f);
-    for (int w = 0; w < wpr; w++) {
-        const float2 u = part[g * wpr + w];
-        s.x += u.x;
-        s.y += u.y;
-    }
-    return s;
 }
 
-// A row's vectors of one thread: v = at + i * tpr
-template <typename T, int VEC, int NV>
-struct Row {
-    Pack<T, VEC> p[NV];
-    __device__ __forceinline__ void load(const T* row, int at, int tpr, int nvec) {
-#pragma unroll
-        for (int i = 0; i < NV; i++) {
-            p[i].zero();
-            if (at + i * tpr < nvec) p[i].load(row + (int64_t)(at + i * tpr) * VEC);
-        }
+// A row's group of `tpr` threads (a power of two below 32, or whole warps) and
+// where its warps' sums meet in shared memory: `part` holds [2][N][16] floats,
+// a group's warps side by side from a multiple of 4, zero where it has none.
+struct Group {
+    int tpr, g, at, slot, base, quads;
+    __device__ __forceinline__ Group(int lanes_per_row, float* part, int floats) : tpr(lanes_per_row) {
+        g = threadIdx.x / tpr;
+        at = threadIdx.x - g * tpr;
+        const int wpr = tpr >> 5;
+        quads = (wpr + 3) >> 2;
+        base = g * quads * 4;
+        slot = base + (at >> 5);
+        for (int i = threadIdx.x; i < floats; i += blockDim.x) part[i] = 0.0f;
+        __syncthreads();
     }
 };
-
-// The rows ahead of a group: a ring of DEPTH slots in shared memory that each
-// thread fills and reads by itself (DEPTH 0: rows whose vectors are single
-// elements; the next row waits in registers instead).
-template <typename T, int VEC, int NV, int DEPTH>
-struct Ahead {
-    Row<T, VEC, NV> next;
-    uint32_t slot0;                // this thread's first vector of slot 0
-    int32_t pitch;                 // bytes between its vectors
-    __device__ __forceinline__ void init(void* ring) {
-        slot0 = (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16;
-        pitch = blockDim.x * 16;
-    }
-    __device__ __forceinline__ void issue(const T* row, bool there, int slot, int at, int tpr, int nvec) {
-        if (DEPTH == 0) {
-            if (there) next.load(row, at, tpr, nvec);
-        } else if (there) {
+// Sums over the group, the same bits in every thread.  `turn` alternates: the
+// readers of the sum before may still be at its half of `part`.
+// WARPS: the group is known to be whole warps.
+template <bool WARPS = false, int N>
+__device__ __forceinline__ void group_sum(float (&v)[N], const Group& q, float* part, int turn) {
 #pragma unroll
-            for (int i = 0; i < NV; i++)
-                if (at + i * tpr < nvec)
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
-                                 :: "r"(slot0 + (slot * NV + i) * pitch), "l"(row + (int64_t)(at + i * tpr) * VEC) : "memory");
+    for (int d = 16; d; d >>= 1)
+        if (WARPS || d < q.tpr)
+#pragma unroll
+            for (int i = 0; i < N; i++) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
+    if (q.tpr <= 32) return;
+    float* mine = part + turn * N * 16;
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+        for (int i = 0; i < N; i++) mine[i * 16 + q.slot] = v[i];
+    asm volatile("bar.sync %0, %1;" :: "r"(q.g + 1), "r"(q.tpr) : "memory");
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        v[i] = 0.0f;
+        for (int k = 0; k < q.quads; k++) {
+            const float4 t = *reinterpret_cast<const float4*>(mine + i * 16 + q.base + 4 * k);
+            v[i] += (t.x + t.y) + (t.z + t.w);
         }
     }
-    __device__ __forceinline__ void read(Row<T, VEC, NV>& r, int slot, int at, int tpr, int nvec) {
-        if (DEPTH == 0) {
-            r = next;
-            return;
-        }
+}
+
+// A row's vectors of one thread, v = at + i * tpr.  Vector v holds the columns
+// v * VEC - shift ... (shift: elements between the 16-byte boundary at or
+// before the row's start and that start; 0 for EVEN rows, which also hold
+// whole vectors only); columns outside [0, cols) are zero here and not stored.
+// The grid of vectors is x's; a matrix whose row lies otherwise (`alike` false)
+// is moved element by element.
+template <typename T, int NV, bool EVEN>
+struct Row {
+    static constexpr int VEC = kVec<T>;
+    Pack<T, VEC> p[NV];
+    __device__ __forceinline__ static int shift_of(const T* row) {
+        return EVEN ? 0 : (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+    }
+    __device__ __forceinline__ static bool whole(int c, int cols) { return EVEN ? c < cols : c >= 0 && c + VEC <= cols; }
+    __device__ __forceinline__ void load(const T* row, int shift, bool alike, int at, int tpr, int cols) {
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            r.p[i].zero();
-            if (at + i * tpr < nvec) {
-                uint4 u;
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(slot0 + (slot * NV + i) * pitch) : "memory");
-                if constexpr (VEC > 1) r.p[i].v = *reinterpret_cast<const decltype(r.p[i].v)*>(&u);
+            const int c = (at + i * tpr) * VEC - shift;
+            p[i].zero();
+            if (whole(c, cols) && (EVEN || alike)) {
+                p[i].load(row + c);
+            } else if (!EVEN && c < cols) {
+                float f[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; e++) {
+                    Pack<T, 1> one;
+                    float x[1] = {0.0f};
+                    if (c + e >= 0 && c + e < cols) {
+                        one.load(row + c + e);
+                        one.unpack(x);
+                    }
+                    f[e] = x[0];
+                }
+                p[i].pack(f);
             }
         }
     }
-};
-__device__ __forceinline__ void ahead_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// all but the youngest N groups of this thread have landed
-template <int N>
-__device__ __forceinline__ void ahead_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
-
-template <int VEC, int NV>
-__device__ __forceinline__ void load_params(float (&f)[NV][VEC], const void* p, int bf16, float none, int at, int tpr,
-                                            int nvec) {
-#pragma unroll
-    for (int i = 0; i < NV; i++)
-#pragma unroll
-        for (int e = 0; e < VEC; e++)
-            f[i][e] = p && at + i * tpr < nvec ? param(p, bf16, (int64_t)(at + i * tpr) * VEC + e) : none;
-}
-
-template <typename T, int VEC, int NV, int DEPTH>
-__global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a, int tpr) {
-    extern __shared__ uint4 ring[];                // [DEPTH][NV][threads]
-    __shared__ float2 part[2][kMaxThreads / 32];
-    constexpr int AHEAD = DEPTH == 0 ? 1 : DEPTH;
-    const int g = threadIdx.x / tpr, at = threadIdx.x % tpr, nvec = (int)(a.cols / VEC);
-    const int64_t step = (int64_t)gridDim.x * (blockDim.x / tpr);
-    int64_t r = (int64_t)blockIdx.x * (blockDim.x / tpr) + g;
-    if (r >= a.rows) return;
-    const float C = (float)a.cols;
-    const T* X = static_cast<const T*>(a.x);
-    Ahead<T, VEC, NV, DEPTH> ahead;
-    ahead.init(ring);
-#pragma unroll
-    for (int d = 0; d < AHEAD; d++) {
-        ahead.issue(X + (r + d * step) * a.ldx, r + d * step < a.rows, d, at, tpr, nvec);
-        ahead_commit();
-    }
-    float w[NV][VEC], b[NV][VEC];
-    load_params<VEC, NV>(w, a.weight, a.param_bf16, 1.0f, at, tpr, nvec);
-    load_params<VEC, NV>(b, a.bias, a.param_bf16, 0.0f, at, tpr, nvec);
-    for (int slot = 0; r < a.rows; r += step, slot = slot + 1 == AHEAD ? 0 : slot + 1) {
-        Row<T, VEC, NV> x;
-        ahead_wait<AHEAD - 1>();
-        ahead.read(x, slot, at, tpr, nvec);
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NV; i++) {
-            float f[VEC];
-            x.p[i].unpack(f);
-#pragma unroll
-            for (int e = 0; e < VEC; e++) s += f[e];
-        }
-        const float mean = group_sum(make_float2(s, 0.0f), tpr, part[0]).x / C;
-        // the slot has been read (its values are summed): the row AHEAD steps on takes it
-        ahead.issue(X + (r + AHEAD * step) * a.ldx, r + AHEAD * step < a.rows, slot, at, tpr, nvec);
-        ahead_commit();
-        s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NV; i++) {
-            if (at + i * tpr >= nvec) continue;
-            float f[VEC];
-            x.p[i].unpack(f);
-#pragma unroll
-            for (int e = 0; e < VEC; e++) s = fmaf(f[e] - mean, f[e] - mean, s);
-        }
-        const float rstd = 1.0f / sqrtf(group_sum(make_float2(s, 0.0f), tpr, part[1]).x / C + a.eps);
-        T* y = static_cast<T*>(a.y) + r * a.ldy;
-#pragma unroll
-        for (int i = 0; i < NV; i++) {
-            if (at + i * tpr >= nvec) continue;
-            float f[VEC];
-            x.p[i].unpack(f);
-#pragma unroll
-            for (int e = 0; e < VEC; e++) f[e] = (f[e] - mean) * rstd * w[i][e] + b[i][e];
+    __device__ __forceinline__ static void store(T* row, int c, bool alike, int cols, const float (&f)[VEC]) {
+        if (whole(c, cols) && (EVEN || alike)) {
             Pack<T, VEC> o;
             o.pack(f);
-            o.store(y + (int64_t)(at + i * tpr) * VEC);
+            o.store(row + c);
+        } else if (!EVEN && c < cols) {
+#pragma unroll
+            for (int e = 0; e < VEC; e++)
+                if (c + e >= 0 && c + e < cols) {
+                    Pack<T, 1> one;
+                    const float x[1] = {f[e]};
+                    one.pack(x);
+                    one.store(row + c + e);
+                }
+        }
+    }
+    // Between two passes over the row: the compiler may not keep the unpacked
+    // values of the first for the second (twice the registers).
+    __device__ __forceinline__ void again() {
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            uint32_t* u = reinterpret_cast<uint32_t*>(&p[i].v);
+            asm volatile("" : "+r"(u[0]), "+r"(u[1]), "+r"(u[2]), "+r"(u[3]));
+        }
+    }
+    // zero outside the row (EVEN: the vector is the row's or is skipped as a whole)
+    __device__ __forceinline__ static float keep(float x, int c, int cols) {
+        return EVEN || (c >= 0 && c < cols) ? x : 0.0f;
+    }
+};
+
+// Weight and bias of odd rows: column c at [c % VEC][c / VEC], so that lanes
+// whose columns lie VEC apart read neighbouring words.
+template <int VEC>
+struct OddParams {
+    float *w, *b;
+    int pitch;
+    __device__ __forceinline__ void fill(float* smem, const NormArgs& a) {
+        pitch = (int)((a.cols + VEC - 1) / VEC);
+        w = smem;
+        b = smem + VEC * pitch;
+        for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+            w[c % VEC * pitch + c / VEC] = a.weight ? param(a.weight, a.param_bf16, c) : 1.0f;
+            b[c % VEC * pitch + c / VEC] = a.bias ? param(a.bias, a.param_bf16, c) : 0.0f;
+        }
+        __syncthreads();
+    }
+    __device__ __forceinline__ float at(const float* f, int c, int cols) const {
+        return c >= 0 && c < cols ? f[c % VEC * pitch + c / VEC] : 0.0f;
+    }
+};
+
+template <typename T, int NV, bool EVEN>
+__global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a, int tpr) {
+    constexpr int VEC = kVec<T>;
+    using R = Row<T, NV, EVEN>;
+    extern __shared__ float odd_smem[];
+    __shared__ __align__(16) float part[2 * 16];
+    const Group q(tpr, part, 2 * 16);
+    const int groups = blockDim.x / tpr, g = q.g, at = q.at, cols = (int)a.cols;
+    const float per_col = 1.0f / (float)cols;
+    OddParams<VEC> odd;
+    if (!EVEN) odd.fill(odd_smem, a);
+    for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < a.rows; r0 += (int64_t)gridDim.x * groups) {
+        const int64_t r = r0 + g;
+        const bool live = r < a.rows;              // lanes of a warp stay together for the sums
+        const T* row = static_cast<const T*>(a.x) + (live ? r : 0) * a.ldx;
+        const int shift = R::shift_of(row);
+        R x;
+        if (live) x.load(row, shift, true, at, tpr, cols);
+        else
+#pragma unroll
+            for (int i = 0; i < NV; i++) x.p[i].zero();
+        float s[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            float f[VEC];
+            x.p[i].unpack(f);
+#pragma unroll
+            for (int e = 0; e < VEC; e++) s[0] += f[e];
+        }
+        group_sum(s, q, part, 0);
+        const float mean = s[0] * per_col;
+        s[0] = 0.0f;
+        x.again();
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int c = (at + i * tpr) * VEC - shift;
+            if (c >= cols) continue;
+            float f[VEC];
+            x.p[i].unpack(f);
+#pragma unroll
+            for (int e = 0; e < VEC; e++) {
+                const float d = R::keep(f[e] - mean, c + e, cols);
+                s[0] = fmaf(d, d, s[0]);
+            }
+        }
+        group_sum(s, q, part, 1);
+        const float rstd = rsqrtf(fmaf(s[0], per_col, a.eps));
+        if (!live) continue;
+        T* y = static_cast<T*>(a.y) + r * a.ldy;
+        const bool alike = R::shift_of(y) == shift;
+        x.again();
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int c = (at + i * tpr) * VEC - shift;
+            if (c >= cols) continue;
+            float f[VEC], w[VEC], b[VEC];
+            x.p[i].unpack(f);
+            if (EVEN) {
+                params<VEC>(w, a.weight, a.param_bf16, 1.0f, c);
+                params<VEC>(b, a.bias, a.param_bf16, 0.0f, c);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; e++) {
+                    w[e] = odd.at(odd.w, c + e, cols);
+                    b[e] = odd.at(odd.b, c + e, cols);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < VEC; e++) f[e] = (f[e] - mean) * rstd * w[e] + b[e];
+            R::store(y, c, alike, cols, f);
         }
         if (at == 0) {
             if (a.mean) a.mean[r] = mean;
@@ -192,98 +278,328 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a, int
     }
 }
 
-// COLS: also the column sums, one partial row [2][cols] per CTA
-template <typename T, int VEC, int NV, int DEPTH, bool COLS>
-__global__ void __launch_bounds__(kMaxThreads) norm_backward_kernel(const NormArgs a, int tpr) {
-    extern __shared__ uint4 ring[];                // x and dy [DEPTH][NV][threads] each; then the sums' meeting
-    __shared__ float2 part[2][kMaxThreads / 32];
-    constexpr int AHEAD = DEPTH == 0 ? 1 : DEPTH;
-    const int groups = blockDim.x / tpr, g = threadIdx.x / tpr, at = threadIdx.x % tpr, nvec = (int)(a.cols / VEC);
-    const int64_t step = (int64_t)gridDim.x * groups;
-    int64_t r = (int64_t)blockIdx.x * groups + g;
-    const float C = (float)a.cols;
-    const T* X = static_cast<const T*>(a.x);
-    const T* DY = static_cast<const T*>(a.dy);
-    Ahead<T, VEC, NV, DEPTH> ax, ad;
-    ax.init(ring);
-    ad.init(ring + (size_t)DEPTH * NV * blockDim.x);
-    auto issue = [&](int64_t row, int slot) {
-        ax.issue(X + row * a.ldx, row < a.rows, slot, at, tpr, nvec);
-        ad.issue(DY + row * a.ld_dy, row < a.rows, slot, at, tpr, nvec);
-        ahead_commit();
-    };
+// dx alone, a group of lanes per row as above
+template <typename T, int NV, bool EVEN>
+__global__ void __launch_bounds__(kMaxThreads) norm_dx_kernel(const NormArgs a, int tpr) {
+    constexpr int VEC = kVec<T>;
+    using R = Row<T, NV, EVEN>;
+    extern __shared__ float odd_smem[];
+    __shared__ __align__(16) float part[2 * 2 * 16];
+    const Group q(tpr, part, 2 * 2 * 16);
+    const int groups = blockDim.x / tpr, g = q.g, at = q.at, cols = (int)a.cols;
+    const float per_col = 1.0f / (float)cols;
+    OddParams<VEC> odd;
+    if (!EVEN) odd.fill(odd_smem, a);
+    int n = 0;
+    for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < a.rows; r0 += (int64_t)gridDim.x * groups, n ^= 1) {
+        const int64_t r = r0 + g;
+        const bool live = r < a.rows;
+        const T* row = static_cast<const T*>(a.x) + (live ? r : 0) * a.ldx;
+        const int shift = R::shift_of(row);
+        R x, d;
+        float mean = 0.0f, rstd = 0.0f;
+        if (live) {
+            const T* dy = static_cast<const T*>(a.dy) + r * a.ld_dy;
+            x.load(row, shift, true, at, tpr, cols);
+            d.load(dy, shift, R::shift_of(dy) == shift, at, tpr, cols);
+            mean = a.mean[r];
+            rstd = a.rstd[r];
+        } else {
 #pragma unroll
-    for (int d = 0; d < AHEAD; d++) issue(r + d * step, d);
-    float nmean = r < a.rows ? a.mean[r] : 0.0f, nrstd = r < a.rows ? a.rstd[r] : 0.0f;
-    float w[NV][VEC];
-    load_params<VEC, NV>(w, a.weight, a.param_bf16, 1.0f, at, tpr, nvec);
-    float dw[NV][VEC] = {}, db[NV][VEC] = {};
-    for (int n = 0, slot = 0; r < a.rows; r += step, n ^= 1, slot = slot + 1 == AHEAD ? 0 : slot + 1) {
-        Row<T, VEC, NV> x, d;
-        ahead_wait<AHEAD - 1>();
-        ax.read(x, slot, at, tpr, nvec);
-        ad.read(d, slot, at, tpr, nvec);
-        const float mean = nmean, rstd = nrstd;
-        if (r + step < a.rows) {
-            nmean = a.mean[r + step];
-            nrstd = a.rstd[r + step];
+            for (int i = 0; i < NV; i++) {
+                x.p[i].zero();
+                d.p[i].zero();
+            }
         }
-        float2 s = make_float2(0.0f, 0.0f);
+        float s[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            if (at + i * tpr >= nvec) continue;
-            float fx[VEC], fd[VEC];
+            const int c = (at + i * tpr) * VEC - shift;
+            if (c >= cols) continue;
+            float fx[VEC], fd[VEC], w[VEC];
             x.p[i].unpack(fx);
             d.p[i].unpack(fd);
+            if (EVEN) params<VEC>(w, a.weight, a.param_bf16, 1.0f, c);
 #pragma unroll
             for (int e = 0; e < VEC; e++) {
-                const float xh = (fx[e] - mean) * rstd, gr = fd[e] * w[i][e];
-                s.x += gr;
-                s.y = fmaf(gr, xh, s.y);
-                if (COLS) {
-                    dw[i][e] = fmaf(fd[e], xh, dw[i][e]);
-                    db[i][e] += fd[e];
+                // outside the row dy and the weight are zero here
+                const float gr = fd[e] * (EVEN ? w[e] : odd.at(odd.w, c + e, cols));
+                s[0] += gr;
+                s[1] = fmaf(gr, (fx[e] - mean) * rstd, s[1]);
+            }
+        }
+        group_sum(s, q, part, n);
+        if (!live) continue;
+        T* dx = static_cast<T*>(a.y) + r * a.ldy;
+        const float s0 = s[0] * per_col, s1 = s[1] * per_col;
+        const bool alike = R::shift_of(dx) == shift;
+        x.again();
+        d.again();
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int c = (at + i * tpr) * VEC - shift;
+            if (c >= cols) continue;
+            float fx[VEC], fd[VEC], w[VEC];
+            x.p[i].unpack(fx);
+            d.p[i].unpack(fd);
+            if (EVEN) params<VEC>(w, a.weight, a.param_bf16, 1.0f, c);
+#pragma unroll
+            for (int e = 0; e < VEC; e++)
+                fd[e] = rstd * (fd[e] * (EVEN ? w[e] : odd.at(odd.w, c + e, cols)) - s0 - (fx[e] - mean) * rstd * s1);
+            R::store(dx, c, alike, cols, fd);
+        }
+    }
+}
+
+__device__ __forceinline__ void ahead_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all but the youngest N groups of this thread have landed
+template <int N>
+__device__ __forceinline__ void ahead_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+
+// Rows ahead of a CTA's groups in shared memory: a ring of slots, each
+// [MATS matrices][NV][threads] of 16 bytes, that every thread fills and reads
+// by itself.
+template <int NV, int MATS>
+struct Ring {
+    uint32_t mine, pitch;
+    __device__ __forceinline__ Ring(void* base)
+        : mine((uint32_t)__cvta_generic_to_shared(base) + threadIdx.x * 16), pitch(blockDim.x * 16) {}
+    __device__ __forceinline__ uint32_t slot(int s) const { return mine + (uint32_t)(s * MATS * NV) * pitch; }
+    template <typename T>
+    __device__ __forceinline__ void copy(uint32_t slot, int mat, int i, const T* src) const {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(slot + (mat * NV + i) * pitch), "l"(src) : "memory");
+    }
+    template <typename P>
+    __device__ __forceinline__ void read(P& p, uint32_t slot, int mat, int i) const {
+        uint4 u;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(slot + (mat * NV + i) * pitch) : "memory");
+        p.v = *reinterpret_cast<const decltype(p.v)*>(&u);
+    }
+};
+
+// A thread's parameters as pairs; `none` where it has no columns or there is no parameter
+template <int VEC, int NV>
+__device__ __forceinline__ void pair_params(F2 (&f)[NV][VEC / 2], const void* p, int bf16, float none, int at, int tpr,
+                                            int nvec) {
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+        float x[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; e++) x[e] = none;
+        if (at + i * tpr < nvec) params<VEC>(x, p, bf16, none, (int64_t)(at + i * tpr) * VEC);
+#pragma unroll
+        for (int e = 0; e < VEC / 2; e++) f[i][e] = F2(x[2 * e], x[2 * e + 1]);
+    }
+}
+
+// The two kernels below are bound by the instructions they issue, so the usual
+// widths get a version without tests: FULL says that every lane of every group
+// has all its NV vectors and that groups are whole warps (each then leaves the
+// loop by itself).
+
+// Forward of EVEN rows where many stream through: weight and bias stay in
+// registers.
+template <typename T, int NV, int DEPTH, bool FULL>
+__global__ void __launch_bounds__(kMaxThreads) norm_stream_kernel(const NormArgs a, int tpr) {
+    constexpr int VEC = kVec<T>, H = VEC / 2;
+    extern __shared__ uint4 ring_smem[];
+    __shared__ __align__(16) float part[2 * 16];
+    const Group q(tpr, part, 2 * 16);
+    const int groups = blockDim.x / tpr, at = q.at, nvec = (int)(a.cols / VEC);
+    const float per_col = 1.0f / (float)a.cols;
+    const int64_t step = (int64_t)gridDim.x * groups;
+    const Ring<NV, 1> ring(ring_smem);
+    int64_t r = (int64_t)blockIdx.x * groups + q.g;
+    const int64_t end = FULL ? a.rows : a.rows + q.g;      // not FULL: the CTA's groups make the same steps
+    // the next row to be copied, and where this thread's part of it lies
+    int64_t ra = r;
+    const T* xa = static_cast<const T*>(a.x) + r * a.ldx + at * VEC;
+    T* y = static_cast<T*>(a.y) + r * a.ldy + at * VEC;
+    const int64_t x_step = step * a.ldx, y_step = step * a.ldy;
+    const auto issue = [&](int slot) {
+        const uint32_t to = ring.slot(slot);
+        if (ra < a.rows)
+#pragma unroll
+            for (int i = 0; i < NV; i++)
+                if (FULL || at + i * tpr < nvec) ring.copy(to, 0, i, xa + i * tpr * VEC);
+        ahead_commit();
+        ra += step;
+        xa += x_step;
+    };
+#pragma unroll
+    for (int d = 0; d < DEPTH; d++) issue(d);
+    F2 w[NV][H], b[NV][H];
+    pair_params<VEC, NV>(w, a.weight, a.param_bf16, 1.0f, at, tpr, nvec);
+    pair_params<VEC, NV>(b, a.bias, a.param_bf16, 0.0f, at, tpr, nvec);
+    for (int slot = 0; r < end; r += step, y += y_step, slot = slot + 1 == DEPTH ? 0 : slot + 1) {
+        const bool live = FULL || r < a.rows;
+        ahead_wait<DEPTH - 1>();
+        F2 x[NV][H], sum(0.0f);
+        const uint32_t from = ring.slot(slot);
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            Pack<T, VEC> p;
+            if (!FULL) p.zero();
+            if (FULL || (live && at + i * tpr < nvec)) ring.read(p, from, 0, i);
+            unpack2(p, x[i]);
+#pragma unroll
+            for (int e = 0; e < H; e++) sum = sum + x[i][e];
+        }
+        float s[1] = {sum.get().x + sum.get().y};
+        group_sum<FULL>(s, q, part, 0);
+        issue(slot);                                       // the slot's values have been summed
+        const float mean = s[0] * per_col;
+        const F2 minus(-mean);
+        F2 sq(0.0f);
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+            if (FULL || at + i * tpr < nvec)
+#pragma unroll
+                for (int e = 0; e < H; e++) {
+                    x[i][e] = x[i][e] + minus;
+                    sq = fma2(x[i][e], x[i][e], sq);
+                }
+        s[0] = sq.get().x + sq.get().y;
+        group_sum<FULL>(s, q, part, 1);
+        const float rstd = rsqrtf(fmaf(s[0], per_col, a.eps));
+        if (!live) continue;
+        const F2 scale(rstd);
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+            if (FULL || at + i * tpr < nvec) {
+                F2 o[H];
+#pragma unroll
+                for (int e = 0; e < H; e++) o[e] = fma2(x[i][e] * scale, w[i][e], b[i][e]);
+                Pack<T, VEC> p;
+                pack2(p, o);
+                p.store(y + i * tpr * VEC);
+            }
+        if (at == 0) {
+            if (a.mean) a.mean[r] = mean;
+            if (a.rstd) a.rstd[r] = rstd;
+        }
+    }
+}
+
+// dx and the column sums of EVEN rows.  COLS: one partial row [2][cols] per CTA.
+template <typename T, int NV, int DEPTH, bool COLS, bool FULL>
+__global__ void __launch_bounds__(kMaxThreads) norm_backward_kernel(const NormArgs a, int tpr) {
+    constexpr int VEC = kVec<T>, H = VEC / 2;
+    extern __shared__ uint4 ring_smem[];           // the ring; then the sums' meeting
+    __shared__ __align__(16) float part[2 * 2 * 16];
+    const Group q(tpr, part, 2 * 2 * 16);
+    const int groups = blockDim.x / tpr, g = q.g, at = q.at, nvec = (int)(a.cols / VEC);
+    const float per_col = 1.0f / (float)a.cols;
+    const int64_t step = (int64_t)gridDim.x * groups, last = a.rows - 1;
+    const Ring<NV, 2> ring(ring_smem);
+    int64_t r = (int64_t)blockIdx.x * groups + g;
+    const int64_t end = FULL ? a.rows : a.rows + g;
+    int64_t ra = r;
+    const T* xa = static_cast<const T*>(a.x) + r * a.ldx + at * VEC;
+    const T* da = static_cast<const T*>(a.dy) + r * a.ld_dy + at * VEC;
+    T* dx = static_cast<T*>(a.y) + r * a.ldy + at * VEC;
+    const int64_t x_step = step * a.ldx, d_step = step * a.ld_dy, y_step = step * a.ldy;
+    const auto issue = [&](int slot) {
+        const uint32_t to = ring.slot(slot);
+        if (ra < a.rows)
+#pragma unroll
+            for (int i = 0; i < NV; i++)
+                if (FULL || at + i * tpr < nvec) {
+                    ring.copy(to, 0, i, xa + i * tpr * VEC);
+                    ring.copy(to, 1, i, da + i * tpr * VEC);
+                }
+        ahead_commit();
+        ra += step;
+        xa += x_step;
+        da += d_step;
+    };
+#pragma unroll
+    for (int d = 0; d < DEPTH; d++) issue(d);
+    // the next row's statistics; volatile, so that they are loaded a whole step ahead of their use
+    float nmean, nrstd;
+    const auto statistics = [&](int64_t row) {
+        row = min(row, last);
+        asm volatile("ld.global.f32 %0, [%1];" : "=f"(nmean) : "l"(a.mean + row));
+        asm volatile("ld.global.f32 %0, [%1];" : "=f"(nrstd) : "l"(a.rstd + row));
+    };
+    statistics(r);
+    F2 w[NV][H], dw[NV][H], db[NV][H];
+    pair_params<VEC, NV>(w, a.weight, a.param_bf16, 1.0f, at, tpr, nvec);
+#pragma unroll
+    for (int i = 0; i < NV; i++)
+#pragma unroll
+        for (int e = 0; e < H; e++) dw[i][e] = db[i][e] = F2(0.0f);
+    for (int n = 0, slot = 0; r < end; r += step, dx += y_step, n ^= 1, slot = slot + 1 == DEPTH ? 0 : slot + 1) {
+        const bool live = FULL || r < a.rows;
+        ahead_wait<DEPTH - 1>();
+        F2 xh[NV][H], s0(0.0f), s1(0.0f);
+        Pack<T, VEC> d[NV];
+        const float mean = nmean, rstd = nrstd;
+        statistics(r + step);
+        const F2 minus(-mean), scale(rstd);
+        const uint32_t from = ring.slot(slot);
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            Pack<T, VEC> x;
+            if (!FULL) {
+                x.zero();
+                d[i].zero();                       // dy is zero outside the rows and columns
+            }
+            if (FULL || (live && at + i * tpr < nvec)) {
+                ring.read(x, from, 0, i);
+                ring.read(d[i], from, 1, i);
+            }
+            F2 dy[H];
+            unpack2(x, xh[i]);
+            unpack2(d[i], dy);
+#pragma unroll
+            for (int e = 0; e < H; e++) {
+                xh[i][e] = (xh[i][e] + minus) * scale;
+                const F2 gr = dy[e] * w[i][e];
+                s0 = s0 + gr;
+                s1 = fma2(gr, xh[i][e], s1);
+                if (COLS && live) {
+                    dw[i][e] = fma2(dy[e], xh[i][e], dw[i][e]);
+                    db[i][e] = db[i][e] + dy[e];
                 }
             }
         }
-        s = group_sum(s, tpr, part[n]);
-        issue(r + AHEAD * step, slot);                     // the slot has been read
-        s.x /= C;
-        s.y /= C;
-        T* dx = static_cast<T*>(a.y) + r * a.ldy;
+        float s[2] = {s0.get().x + s0.get().y, s1.get().x + s1.get().y};
+        group_sum<FULL>(s, q, part, n);
+        issue(slot);                                       // the slot's values have been summed
+        if (!live) continue;
+        const F2 m0(-(s[0] * per_col)), m1(-(s[1] * per_col));
 #pragma unroll
-        for (int i = 0; i < NV; i++) {
-            if (at + i * tpr >= nvec) continue;
-            float fx[VEC], fd[VEC];
-            x.p[i].unpack(fx);
-            d.p[i].unpack(fd);
+        for (int i = 0; i < NV; i++)
+            if (FULL || at + i * tpr < nvec) {
+                F2 dy[H];
+                unpack2(d[i], dy);
 #pragma unroll
-            for (int e = 0; e < VEC; e++) {
-                const float xh = (fx[e] - mean) * rstd;
-                fd[e] = rstd * (fd[e] * w[i][e] - s.x - xh * s.y);
+                for (int e = 0; e < H; e++) dy[e] = fma2(dy[e], w[i][e], fma2(xh[i][e], m1, m0)) * scale;
+                Pack<T, VEC> o;
+                pack2(o, dy);
+                o.store(dx + i * tpr * VEC);
             }
-            Pack<T, VEC> o;
-            o.pack(fd);
-            o.store(dx + (int64_t)(at + i * tpr) * VEC);
-        }
     }
     if (!COLS) return;
     pdl_launch_dependents();
     // the CTA's groups meet in shared memory, [groups - 1][2][cols]; group 0 adds them in order and
     // writes the partial row
     const int64_t c0 = a.cols;
-    float* merged = reinterpret_cast<float*>(ring);
+    float* merged = reinterpret_cast<float*>(ring_smem);
     ahead_wait<0>();
     if (groups > 1) __syncthreads();
+    const auto column = [&](float* f, int i, int e) { return f + (at + i * tpr) * VEC + 2 * e; };
     if (g > 0) {
+        float* mine = merged + (int64_t)(g - 1) * 2 * c0;
 #pragma unroll
         for (int i = 0; i < NV; i++)
             if (at + i * tpr < nvec)
 #pragma unroll
-                for (int e = 0; e < VEC; e++) {
-                    const int64_t c = (int64_t)(at + i * tpr) * VEC + e;
-                    merged[(g - 1) * 2 * c0 + c] = dw[i][e];
-                    merged[((g - 1) * 2 + 1) * c0 + c] = db[i][e];
+                for (int e = 0; e < H; e++) {
+                    *reinterpret_cast<float2*>(column(mine, i, e)) = dw[i][e].get();
+                    *reinterpret_cast<float2*>(column(mine + c0, i, e)) = db[i][e].get();
                 }
     }
     if (groups > 1) __syncthreads();
@@ -291,17 +607,24 @@ __global__ void __launch_bounds__(kMaxThreads) norm_backward_kernel(const NormAr
     float* out = a.ws + (int64_t)blockIdx.x * 2 * c0;
 #pragma unroll
     for (int i = 0; i < NV; i++)
-        if (at + i * tpr < nvec)
+        if (at + i * tpr < nvec) {
+            for (int k = 0; k < groups - 1; k++) {
+                float* other = merged + (int64_t)k * 2 * c0;
 #pragma unroll
-            for (int e = 0; e < VEC; e++) {
-                const int64_t c = (int64_t)(at + i * tpr) * VEC + e;
-                for (int k = 1; k < groups; k++) {
-                    dw[i][e] += merged[(k - 1) * 2 * c0 + c];
-                    db[i][e] += merged[((k - 1) * 2 + 1) * c0 + c];
+                for (int e = 0; e < H; e++) {
+                    const float2 x = *reinterpret_cast<const float2*>(column(other, i, e));
+                    const float2 y = *reinterpret_cast<const float2*>(column(other + c0, i, e));
+                    dw[i][e] = dw[i][e] + F2(x.x, x.y);
+                    db[i][e] = db[i][e] + F2(y.x, y.y);
                 }
-                out[c] = dw[i][e];
-                out[c0 + c] = db[i][e];
             }
+#pragma unroll
+            for (int e = 0; e < H; e += 2) {
+                const float2 x = dw[i][e].get(), x1 = dw[i][e + 1].get(), y = db[i][e].get(), y1 = db[i][e + 1].get();
+                *reinterpret_cast<float4*>(column(out, i, e)) = make_float4(x.x, x.y, x1.x, x1.y);
+                *reinterpret_cast<float4*>(column(out + c0, i, e)) = make_float4(y.x, y.y, y1.x, y1.y);
+            }
+        }
 }
 
 // Adds the partial rows: 32 columns a CTA, the parts dealt to 32 threads each
@@ -329,9 +652,12 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* ws, int 
 
 // ------------------------------------------------------------------ wide rows
 __device__ __forceinline__ float2 block_sum(float2 v) {
-    __shared__ float2 part[kWide / 32];
+    __shared__ __align__(16) float part[2 * 2 * 16];
     __syncthreads();
-    return group_sum(v, kWide, part);
+    const Group q(kWide, part, 2 * 2 * 16);
+    float s[2] = {v.x, v.y};
+    group_sum(s, q, part, 0);
+    return make_float2(s[0], s[1]);
 }
 
 template <typename T, int VEC>
@@ -391,7 +717,7 @@ __global__ void __launch_bounds__(128) norm_columns_kernel(const NormArgs a) {
     const int64_t per = (a.rows + gridDim.y - 1) / gridDim.y;
     const int64_t lo = blockIdx.y * per, hi = min(a.rows, lo + per);
     float dw[VEC] = {}, db[VEC] = {};
-#pragma unroll 4
+#pragma unroll 8
     for (int64_t r = lo; r < hi; r++) {
         Pack<T, VEC> d, x;
         float fd[VEC], fx[VEC];
@@ -464,118 +790,171 @@ struct Shape {
     size_t smem;
     unsigned ctas;
 };
-template <typename K>
-cudaError_t shape(Shape& s, K kernel, const NormArgs& a, int vec, int nv, int slots, bool cols, int per_sm) {
-    const int64_t nvec = a.cols / vec;
-    s.tpr = (int)((nvec + 32 * nv - 1) / (32 * nv)) * 32;
-    if (s.tpr < kMinThreads) {                     // several rows a CTA
-        int t = 32;
-        while (t < s.tpr) t *= 2;
-        s.tpr = t;
-        s.threads = kMinThreads;
-    } else {
-        s.threads = s.tpr;
-    }
-    s.groups = s.threads / s.tpr;
-    s.smem = (size_t)slots * nv * s.threads * 16;
-    if (cols) s.smem = std::max(s.smem, (size_t)(s.groups - 1) * 2 * a.cols * sizeof(float));
+// `tpr` lanes a row; CTAs of about kCta threads unless one row takes more.
+// smem(s): bytes that a CTA of s.threads needs.
+template <typename K, typename S>
+cudaError_t shape(Shape& s, K kernel, const NormArgs& a, int tpr, S smem, int per_sm) {
+    s.tpr = tpr;
+    s.threads = tpr >= kCta ? tpr : kCta / tpr * tpr;
+    s.groups = s.threads / tpr;
+    s.smem = smem(s);
     if (s.smem > 40 * 1024) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
         if (e != cudaSuccess) return e;
     }
-    // resident CTAs, asked once per kernel and size
-    static std::atomic<uint64_t> known[kMaxThreads / 32 + 1];
-    const uint64_t key = known[s.threads / 32].load(std::memory_order_relaxed);
-    int occ = (int)(key >> 32);
-    if (occ == 0 || (uint32_t)key != (uint32_t)s.smem) {
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, s.threads, s.smem) != cudaSuccess || occ < 1)
-            occ = 1;
-        known[s.threads / 32].store((uint64_t)occ << 32 | (uint32_t)s.smem, std::memory_order_relaxed);
+    int occ = 1;
+    if (a.rows > (int64_t)a.num_sms * s.groups) {
+        cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, s.threads, s.smem);
+        if (e != cudaSuccess) return e;
+        occ = std::max(1, std::min(occ, per_sm));
     }
-    const int64_t most = (int64_t)a.num_sms * std::min(occ, per_sm), want = (a.rows + s.groups - 1) / s.groups;
-    s.ctas = (unsigned)std::min(most, want);
+    s.ctas = (unsigned)std::min((int64_t)a.num_sms * occ, (a.rows + s.groups - 1) / s.groups);
     return cudaSuccess;
 }
 
-template <typename T, int VEC, int NV, int DEPTH>
-cudaError_t forward(const NormArgs& a, cudaStream_t st) {
+// Lanes for n vectors, at most nv each: a power of two below a warp, else whole warps.
+int lanes(int64_t n, int nv) {
+    const int64_t want = (n + nv - 1) / nv;
+    if (want > 32) return (int)((want + 31) / 32 * 32);
+    int t = 4;
+    while (t < want) t *= 2;
+    return t;
+}
+
+size_t odd_bytes(const NormArgs& a, bool even) {
+    const int64_t vec = a.bf16 ? 8 : 4;
+    return even ? 0 : (size_t)(2 * vec * ((a.cols + vec - 1) / vec)) * sizeof(float);
+}
+
+template <typename T, int NV, bool EVEN>
+cudaError_t forward(const NormArgs& a, int64_t n, cudaStream_t st) {
     Shape s;
-    cudaError_t e = shape(s, norm_kernel<T, VEC, NV, DEPTH>, a, VEC, NV, DEPTH, false, 16);
+    cudaError_t e = shape(s, norm_kernel<T, NV, EVEN>, a, lanes(n, NV), [&](const Shape&) { return odd_bytes(a, EVEN); }, 16);
     if (e != cudaSuccess) return e;
-    norm_kernel<T, VEC, NV, DEPTH><<<s.ctas, s.threads, s.smem, st>>>(a, s.tpr);
+    norm_kernel<T, NV, EVEN><<<s.ctas, s.threads, s.smem, st>>>(a, s.tpr);
     return cudaGetLastError();
 }
 
-template <typename T, int VEC, int NV, int DEPTH>
-cudaError_t backward(const NormArgs& a, cudaStream_t st) {
+// every lane has nv vectors, and a row takes whole warps
+bool full(int64_t n, int nv) { return n % (32 * nv) == 0; }
+
+template <typename T, int NV, int DEPTH, bool FULL>
+cudaError_t stream_f(const NormArgs& a, cudaStream_t st) {
+    Shape s;
+    const auto ring = [](const Shape& x) { return (size_t)DEPTH * NV * x.threads * 16; };
+    cudaError_t e = shape(s, norm_stream_kernel<T, NV, DEPTH, FULL>, a, lanes(a.cols / kVec<T>, NV), ring, 16);
+    if (e != cudaSuccess) return e;
+    norm_stream_kernel<T, NV, DEPTH, FULL><<<s.ctas, s.threads, s.smem, st>>>(a, s.tpr);
+    return cudaGetLastError();
+}
+template <typename T, int NV, int DEPTH>
+cudaError_t stream(const NormArgs& a, cudaStream_t st) {
+    return full(a.cols / kVec<T>, NV) ? stream_f<T, NV, DEPTH, true>(a, st) : stream_f<T, NV, DEPTH, false>(a, st);
+}
+
+template <typename T, int NV, bool EVEN>
+cudaError_t dx_only(const NormArgs& a, int64_t n, cudaStream_t st) {
+    Shape s;
+    cudaError_t e = shape(s, norm_dx_kernel<T, NV, EVEN>, a, lanes(n, NV), [&](const Shape&) { return odd_bytes(a, EVEN); }, 16);
+    if (e != cudaSuccess) return e;
+    norm_dx_kernel<T, NV, EVEN><<<s.ctas, s.threads, s.smem, st>>>(a, s.tpr);
+    return cudaGetLastError();
+}
+
+template <typename T, int NV, int DEPTH, bool FULL>
+cudaError_t backward_f(const NormArgs& a, cudaStream_t st) {
+    const int tpr = lanes(a.cols / kVec<T>, NV);
+    const auto ring = [](const Shape& s) { return (size_t)DEPTH * 2 * NV * s.threads * 16; };
     Shape s;
     if (!a.dweight && !a.dbias) {
-        cudaError_t e = shape(s, norm_backward_kernel<T, VEC, NV, DEPTH, false>, a, VEC, NV, 2 * DEPTH, false, 16);
+        cudaError_t e = shape(s, norm_backward_kernel<T, NV, DEPTH, false, FULL>, a, tpr, ring, 16);
         if (e != cudaSuccess) return e;
-        norm_backward_kernel<T, VEC, NV, DEPTH, false><<<s.ctas, s.threads, s.smem, st>>>(a, s.tpr);
+        norm_backward_kernel<T, NV, DEPTH, false, FULL><<<s.ctas, s.threads, s.smem, st>>>(a, s.tpr);
         return cudaGetLastError();
     }
-    cudaError_t e = shape(s, norm_backward_kernel<T, VEC, NV, DEPTH, true>, a, VEC, NV, 2 * DEPTH, true, 4);
+    cudaError_t e = shape(s, norm_backward_kernel<T, NV, DEPTH, true, FULL>, a, tpr, [&](const Shape& x) {
+        return std::max(ring(x), (size_t)(x.groups - 1) * 2 * a.cols * sizeof(float));
+    }, 4);
     if (e != cudaSuccess) return e;
     s.ctas = std::min<unsigned>(s.ctas, kMaxParts);
-    norm_backward_kernel<T, VEC, NV, DEPTH, true><<<s.ctas, s.threads, s.smem, st>>>(a, s.tpr);
+    norm_backward_kernel<T, NV, DEPTH, true, FULL><<<s.ctas, s.threads, s.smem, st>>>(a, s.tpr);
     return launch_k(true, norm_reduce_kernel, dim3((unsigned)((a.cols + 31) / 32), 2), 1024, 0, st, a.ws, (int)s.ctas,
                     a.cols, a.dweight, a.dbias);
 }
-
-template <typename T, int VEC>
-cudaError_t forward_wide(const NormArgs& a, cudaStream_t st) {
-    norm_wide_kernel<T, VEC><<<(unsigned)a.rows, kWide, 0, st>>>(a);
-    return cudaGetLastError();
+template <typename T, int NV, int DEPTH>
+cudaError_t backward(const NormArgs& a, cudaStream_t st) {
+    return full(a.cols / kVec<T>, NV) ? backward_f<T, NV, DEPTH, true>(a, st) : backward_f<T, NV, DEPTH, false>(a, st);
 }
 
 template <typename T, int VEC>
-cudaError_t backward_wide(const NormArgs& a, cudaStream_t st) {
-    if (a.dweight || a.dbias) {
-        const int groups = (int)std::min<int64_t>(a.rows, kWideParts);
-        norm_columns_kernel<T, VEC><<<dim3((unsigned)((a.cols / VEC + 127) / 128), groups), 128, 0, st>>>(a);
-        norm_reduce_kernel<<<dim3((unsigned)((a.cols + 31) / 32), 2), 1024, 0, st>>>(a.ws, groups, a.cols, a.dweight,
-                                                                                   a.dbias);
-    }
-    norm_wide_dx_kernel<T, VEC><<<(unsigned)a.rows, kWide, 0, st>>>(a);
-    return cudaGetLastError();
+cudaError_t columns(const NormArgs& a, cudaStream_t st) {
+    const int groups = (int)std::min<int64_t>(a.rows, kWideParts);
+    norm_columns_kernel<T, VEC><<<dim3((unsigned)((a.cols / VEC + 127) / 128), groups), 128, 0, st>>>(a);
+    return launch_k(true, norm_reduce_kernel, dim3((unsigned)((a.cols + 31) / 32), 2), 1024, 0, st, a.ws, groups, a.cols,
+                    a.dweight, a.dbias);
 }
 
-bool vectors(const NormArgs& a) {
+// rows on 16-byte boundaries that hold whole vectors, in every matrix of the call
+bool even_rows(const NormArgs& a) {
     const int e = a.bf16 ? 2 : 4;
     return rows_vec(a.x, a.ldx, a.cols, e) && rows_vec(a.y, a.ldy, a.cols, e) &&
            (!a.dy || rows_vec(a.dy, a.ld_dy, a.cols, e));
 }
 
-// Vectors a thread: one where few rows leave SMs idle (a row's latency counts),
-// two where many rows stream through (fewer threads share a row's sums).
+// Vectors a lane: few where few rows leave SMs idle (a row's latency counts),
+// else as many as keep a row inside one warp.
+template <typename T, bool EVEN>
+cudaError_t forward_e(const NormArgs& a, cudaStream_t st) {
+    const int64_t n = a.cols / kVec<T> + (EVEN ? 0 : 2);
+    if (a.rows <= 2 * a.num_sms) {
+        if (n <= kMaxThreads) return forward<T, 1, EVEN>(a, n, st);
+        if (n <= 2 * kMaxThreads) return forward<T, 2, EVEN>(a, n, st);
+    }
+    if (n <= 4 * 32) return forward<T, 4, EVEN>(a, n, st);
+    // 16 vectors of BF16 fit the registers; of FP32, and with shifted columns, they spill
+    if (n <= 8 * 32 || !EVEN || (sizeof(T) == 4 && n <= 8 * kMaxThreads)) return forward<T, 8, EVEN>(a, n, st);
+    return forward<T, EVEN ? 16 : 8, EVEN>(a, n, st);
+}
 template <typename T>
 cudaError_t forward_t(const NormArgs& a, cudaStream_t st) {
-    constexpr int VEC = kVec<T>;
-    if (vectors(a)) {
-        const int64_t n = a.cols / VEC;
-        if (n <= kMaxThreads && a.rows <= 2 * a.num_sms) return forward<T, VEC, 1, 2>(a, st);
-        if (n <= 2 * kMaxThreads) return forward<T, VEC, 2, 4>(a, st);
-        if (n <= 4 * kMaxThreads) return forward<T, VEC, 4, 2>(a, st);
-        return forward_wide<T, VEC>(a, st);
-    }
-    if (a.cols <= 4 * kMaxThreads) return forward<T, 1, 4, 0>(a, st);
-    if (a.cols <= 16 * kMaxThreads) return forward<T, 1, 16, 0>(a, st);
-    return forward_wide<T, 1>(a, st);
+    const bool even = even_rows(a);
+    const int64_t n = a.cols / kVec<T>;
+    if (even && a.rows > 2 * a.num_sms && n <= 4 * kMaxThreads) return stream<T, 4, 2>(a, st);
+    if (even && n <= 16 * kMaxThreads) return forward_e<T, true>(a, st);
+    if (!even && a.cols <= kMaxOddCols) return forward_e<T, false>(a, st);
+    if (even) norm_wide_kernel<T, kVec<T>><<<(unsigned)a.rows, kWide, 0, st>>>(a);
+    else norm_wide_kernel<T, 1><<<(unsigned)a.rows, kWide, 0, st>>>(a);
+    return cudaGetLastError();
 }
 
+template <typename T, bool EVEN>
+cudaError_t dx_e(const NormArgs& a, cudaStream_t st) {
+    const int64_t n = a.cols / kVec<T> + (EVEN ? 0 : 2);
+    if (a.rows <= 2 * a.num_sms && n <= 2 * kMaxThreads) return dx_only<T, 2, EVEN>(a, n, st);
+    if (n <= 4 * 32) return dx_only<T, 4, EVEN>(a, n, st);
+    return dx_only<T, 8, EVEN>(a, n, st);
+}
 template <typename T>
 cudaError_t backward_t(const NormArgs& a, cudaStream_t st) {
     constexpr int VEC = kVec<T>;
-    if (vectors(a)) {
-        const int64_t n = a.cols / VEC;
-        if (n <= kMaxThreads && a.rows <= 2 * a.num_sms) return backward<T, VEC, 1, 2>(a, st);
-        if (n <= 2 * kMaxThreads) return backward<T, VEC, 2, 3>(a, st);
-        return backward_wide<T, VEC>(a, st);
+    const bool even = even_rows(a);
+    const int64_t n = a.cols / VEC;
+    if (even) {
+        if (n <= kMaxThreads && a.rows <= 2 * a.num_sms) return backward<T, 1, 2>(a, st);
+        // 16 columns a thread: more would not leave room for their sums
+        constexpr int NV = 16 / VEC, DEPTH = sizeof(T) == 2 ? 3 : 2;
+        if (n <= NV * kMaxThreads) return backward<T, NV, DEPTH>(a, st);
     }
-    if (a.cols <= 4 * kMaxThreads) return backward<T, 1, 4, 0>(a, st);
-    if (a.cols <= 12 * kMaxThreads) return backward<T, 1, 12, 0>(a, st);
-    return backward_wide<T, 1>(a, st);
+    // the column sums first: dx may be written over dy
+    if (a.dweight || a.dbias) {
+        cudaError_t e = even ? columns<T, kVec<T>>(a, st) : columns<T, 1>(a, st);
+        if (e != cudaSuccess) return e;
+    }
+    if (even && n <= 8 * kMaxThreads) return dx_e<T, true>(a, st);
+    if (!even && a.cols <= kMaxOddCols) return dx_e<T, false>(a, st);
+    if (even) norm_wide_dx_kernel<T, kVec<T>><<<(unsigned)a.rows, kWide, 0, st>>>(a);
+    else norm_wide_dx_kernel<T, 1><<<(unsigned)a.rows, kWide, 0, st>>>(a);
+    return cudaGetLastError();
 }
 
 }  // namespace

@@ -62,6 +62,28 @@ def test_forward_and_gradient(bsq, T, V, D, pad):
     assert torch.equal(one, dh) and torch.equal(two, dw)
 
 
+@pytest.mark.parametrize("T", [15, 16, 17, 63, 64, 65, 100, 127, 255, 256, 257])
+def test_token_counts_around_the_tiles(bsq, T):
+    # the token counts at which a tile's shape or the products' order changes, over vocabularies
+    # that end inside a tile
+    for V, D in ((1, 8), (333, 200), (4501, 136)):
+        h, w, targets, g = make(T, V, D, T + V)
+        targets[T // 2] = -1
+        loss, lse = bsq.linear_cross_entropy(h, w, targets)
+        rl, rz, tl, tz = head_ref(h, w, targets)
+        assert_close(lse, rz, tz, "lse")
+        assert_close(loss, rl, tl, "loss")
+        dloss = torch.rand(T, generator=g, device="cuda")
+        dh, hbuf = strided((T, D), BF, 8, 8, fill=float("nan"))
+        dw, wbuf = strided((V, D), BF, 8, 8, fill=float("nan"))
+        bsq.linear_cross_entropy_backward_into(h, w, targets, lse, dloss, dh, dw)
+        rh, th, rw, tw = head_grad_ref(h, w, targets, lse, dloss)
+        assert_close(dh, rh, th, "dh")
+        assert_close(dw, rw, tw, "dw")
+        Guard(dh, hbuf).check()
+        Guard(dw, wbuf).check()
+
+
 def test_several_pieces_of_the_vocabulary(bsq):
     # more tokens than one 256 MB piece of the whole vocabulary holds: 3 pieces
     T, V, D = 70001, 5003, 16
