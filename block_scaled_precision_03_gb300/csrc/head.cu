@@ -69,7 +69,7 @@ struct GemmParams {
     int32_t k_stages, mma_last;    // K stages in all; MMAs of the last one
     int32_t m_tiles, n_tiles, splits, split_stages, total;
     int32_t raster, raster_n;
-    int32_t tile_n;                // output columns of a pair: 256, or fewer where that balances few rows
+    int32_t tile_n;                // output columns of a pair: 256; few tokens: the tokens in sixteens
     int32_t tile_m;                // rows of a pair: 256, or fewer (few tokens) for balance
     int32_t stages, b_bytes;       // few tokens: stages, and one CTA's bytes of B per stage
     uint32_t tx;                   // bytes one CTA loads per stage
@@ -449,8 +449,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             const TileAt ti = tile_at(p, t);
             const int buf = iter & 1;
             const int64_t row0 = (int64_t)ti.mt * kTile + rank * 128 + q * 32, row = row0 + lane;       // tile_m is 256
-            const int64_t col0 = (int64_t)ti.nt * p.tile_n + half * 128;
-            const int width = min(128, p.tile_n - half * 128);       // of the tile's columns, this thread's
+            const int64_t col0 = (int64_t)ti.nt * kTile + half * 128;
             // what the row needs, read while the tile is computed
             int target = -1;                       // the target's column among this thread's 128
             float lse = 0.0f, ratio = 0.0f;
@@ -462,18 +461,18 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                         ratio = p.dloss[row] / smax;
                     }
                     const int64_t at = id - p.col0 - col0;
-                    if (at >= 0 && at < width) target = (int)at;
+                    if (at >= 0 && at < 128) target = (int)at;
                 }
             }
             if (!tc::mbar_wait(tfull0 + 8 * buf, (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns)) break;
             tc::fence_after();
             const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kTile + half * 128);
-            const bool live = row0 < p.M && (MODE == kStats ? width > 0 : col0 < p.N && width > 0);
+            const bool live = row0 < p.M && (MODE == kStats || col0 < p.N);
             float v[32];
             if (MODE == kStats && live) {
                 // two passes over the accumulator: it is read from tensor memory again
                 // rather than held in 128 registers
-                const int cols = (int)min((int64_t)width, p.N - col0);       // 0 or less: an empty part
+                const int cols = (int)min((int64_t)128, p.N - col0);       // 0 or less: an empty part
                 const bool hits = __any_sync(0xffffffffu, target >= 0 && target < cols);
                 float m = kNegInf, hit = 0.0f;
 #pragma unroll 1
@@ -504,12 +503,12 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 }
                 if (row < p.M) {
                     if (target >= 0 && target < cols) p.hit[row] = hit;
-                    p.part[(int64_t)(p.tile_n > 128 ? 2 * ti.nt + half : ti.nt) * p.M + row] = make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
+                    p.part[((int64_t)2 * ti.nt + half) * p.M + row] = make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
                 }
             } else if (live) {
                 // ratio 0 (a token that does not count) gives 0 whatever its logits
 #pragma unroll 1
-                for (int c = 0; c < width; c += 32) {
+                for (int c = 0; c < 128; c += 32) {
                     load_acc(v, ta + c);
                     const int col = (int)col0 + c;
                     if (MODE == kDh) {
@@ -617,11 +616,11 @@ void choose_raster(GemmParams& p, int64_t K, int pairs) {
 // tokens): the pairs should get equally many, so the size that gives the
 // busiest pair the fewest.  (50021 rows: 196 tiles of 256 leave 76 pairs 2 or 3
 // each, 224 of 224 nearly always 3.)
-int stream_rows(int64_t vocab, int num_sms, int step) {
+int stream_rows(int64_t vocab, int num_sms) {
     const int64_t pairs = std::max(1, num_sms / 2);
     int best = kTile;
     int64_t least = INT64_MAX;
-    for (int t = kTile; t >= 96; t -= step) {
+    for (int t = kTile; t >= 96; t -= 16) {
         const int64_t load = ((vocab + t - 1) / t + pairs - 1) / pairs * t;
         if (load < least) {
             least = load;
@@ -630,12 +629,6 @@ int stream_rows(int64_t vocab, int num_sms, int step) {
     }
     return best;
 }
-// Columns of a pair's tile in the token-major products: as above with one row
-// tile, else 256 (a tile's MMAs then hide the loads).
-int tile_columns(int64_t tokens, int64_t vocab, int num_sms) {
-    return tokens <= kTile ? stream_rows(vocab, num_sms, 32) : kTile;
-}
-
 // `beside`: launched so that it may run while the kernel before it on the
 // stream still does (of which it needs nothing); it ends after that kernel.
 template <int MODE>
@@ -767,11 +760,10 @@ int dh_splits(int64_t tokens, int64_t cols, int64_t piece, int num_sms) {
 // parts of a row's statistics
 int64_t head_parts(int64_t tokens, int64_t vocab, int num_sms) {
     if (tokens <= kFewTokens) {
-        const int tm = stream_rows(vocab, num_sms, 16);
+        const int tm = stream_rows(vocab, num_sms);
         return (vocab + tm - 1) / tm * 8;
     }
-    const int tn = tile_columns(tokens, vocab, num_sms);
-    return (vocab + tn - 1) / tn * (tn > 128 ? 2 : 1);
+    return (vocab + kTile - 1) / kTile * 2;
 }
 
 }  // namespace
@@ -796,9 +788,9 @@ cudaError_t run_head(const HeadArgs& a, cudaStream_t st) {
     cudaError_t e;
     if (T <= kFewTokens) {
         std::swap(p.M, p.N);
-        e = gemm<kFewStats>(p, w, h, nullptr, a.cols, 1, stream_rows(a.vocab, a.num_sms, 16), (int)round_up(T, 16), false, a, st);
+        e = gemm<kFewStats>(p, w, h, nullptr, a.cols, 1, stream_rows(a.vocab, a.num_sms), (int)round_up(T, 16), false, a, st);
     } else {
-        e = gemm<kStats>(p, h, w, nullptr, a.cols, 1, kTile, tile_columns(T, a.vocab, a.num_sms), false, a, st);
+        e = gemm<kStats>(p, h, w, nullptr, a.cols, 1, kTile, kTile, false, a, st);
     }
     if (e != cudaSuccess) return e;
     // tokens a CTA: few where there are few, so that more threads share a token's parts
@@ -845,10 +837,10 @@ cudaError_t run_head_backward(const HeadArgs& a, cudaStream_t st) {
             p.N = T;
             p.g = reinterpret_cast<__nv_bfloat16*>(g);
             p.ld_g = piece;
-            e = gemm<kFewGrad>(p, wp, h, nullptr, D, 1, stream_rows(n, a.num_sms, 16), (int)round_up(T, 16), beside, a, st);
+            e = gemm<kFewGrad>(p, wp, h, nullptr, D, 1, stream_rows(n, a.num_sms), (int)round_up(T, 16), beside, a, st);
         } else {
             if (!tmap::out_2d(&out, g, T, n, piece, true)) return cudaErrorInvalidValue;
-            e = gemm<kGrad>(p, h, wp, &out, D, 1, kTile, tile_columns(T, n, a.num_sms), beside, a, st);
+            e = gemm<kGrad>(p, h, wp, &out, D, 1, kTile, kTile, beside, a, st);
         }
         if (e == cudaSuccess && a.dh) {
             p.M = T;
