@@ -23,6 +23,13 @@
 // the other way round, z^T = w h^T: w's rows are the tile's 256 rows and the
 // tokens its 16 to 128 columns, so that a stage is nearly all w and six of them
 // (192 KB per SM) are in flight instead of three half-filled ones.
+//
+// The tensor cores' FP32 sums are not rounded to nearest: over K = 4096 the
+// logits came out up to 3e-6 to 6e-6 (relative) too small in magnitude, ten
+// times an FP32 product's error.  For the loss the accumulators are therefore
+// read out every kChunk of K and added up in registers, rounded to nearest
+// (3e-6 -> 4e-7); the gradient's logits, whose g is rounded to BF16, keep one
+// accumulator for all of K.
 #include <algorithm>
 #include <cuda.h>
 #include "common.cuh"
@@ -48,6 +55,10 @@ constexpr int kSub = 2;                             // sub-steps per stage
 constexpr int kStages = 3;
 constexpr int kMaxStages = 6;                       // few tokens: as many as fit
 constexpr int kFewTokens = 128;
+// Stages (K = 512) that one accumulator sums for the loss.  Against 64 bits, 1024
+// x 20000 x 4096: 3.2e-7 (2 stages 1.6e-7, 8 6.7e-7; a plain FP32 product
+// 6.8e-7); the batch takes 2.46 ms with 4 or 8, 2.59 with 2.
+constexpr int kChunk = 4;
 constexpr int kSubBytes = 128 * kSubK * 2;          // one CTA's 128 rows of an operand, one sub-step
 constexpr int kOpBytes = kSub * kSubBytes;
 constexpr int kMmas = 4 * kSub;                     // per stage
@@ -67,6 +78,7 @@ __host__ __device__ constexpr bool b_mn(int mode) { return mode == kDh || mode =
 struct GemmParams {
     int64_t M, N;                  // output
     int32_t k_stages, mma_last;    // K stages in all; MMAs of the last one
+    int32_t chunk;                 // stages per accumulator
     int32_t m_tiles, n_tiles, splits, split_stages, total;
     int32_t raster, raster_n;
     int32_t tile_n;                // output columns of a pair: 256; few tokens: the tokens in sixteens
@@ -173,6 +185,17 @@ __device__ __forceinline__ void store_acc(const float (&v)[32], uint32_t base, c
             tc::bulk_commit();
         }
     }
+}
+// 16 more columns of a chunk's accumulator onto a running sum
+__device__ __forceinline__ void add_acc(float* sum, uint32_t taddr) {
+    uint32_t r[16];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 16; j++) sum[j] += __uint_as_float(r[j]);
 }
 // 32 columns of the accumulator at `taddr`
 __device__ __forceinline__ void load_acc(float (&v)[32], uint32_t taddr) {
@@ -345,43 +368,45 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             int stage = 0, iter = 0;
             uint32_t phase = 0;
             bool ok = true, any = false, ready = false;
-            for (int t = cid; t < p.total && ok; t += ncl, ++iter) {
+            for (int t = cid; t < p.total && ok; t += ncl) {
                 const TileAt ti = tile_at(p, t);
-                const int buf = iter & 1;
-                if (!tc::mbar_wait(tempty0 + 8 * buf, ((iter >> 1) & 1) ^ 1, abort_flag, p.status, p.timeout_ns)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t d = tmem + (uint32_t)buf * kTile;
-                for (int kb = ti.k0; kb < ti.k1; kb++) {
-                    if (!ready && !tc::mbar_wait(full0 + 8 * stage, phase, abort_flag, p.status, p.timeout_ns)) {
+                for (int c0 = ti.k0; c0 < ti.k1 && ok; c0 += p.chunk, ++iter) {
+                    const int c1 = min(ti.k1, c0 + p.chunk), buf = iter & 1;
+                    if (!tc::mbar_wait(tempty0 + 8 * buf, ((iter >> 1) & 1) ^ 1, abort_flag, p.status, p.timeout_ns)) {
                         ok = false;
                         break;
                     }
-                    tc::fence_after();
-                    const uint64_t ad = ad0 + (uint64_t)(stage * (kOpBytes >> 4));
-                    const uint64_t bd = bd0 + (uint64_t)(stage * (b_bytes >> 4));
-                    const int next = stage + 1 == S ? 0 : stage + 1;
-                    const uint32_t next_phase = next == 0 ? phase ^ 1 : phase;
-                    if (kb != p.k_stages - 1 || p.mma_last == kMmas) {
-                        // the next stage's barrier is tested while this stage's MMAs run
-#pragma unroll
-                        for (int m = 0; m < kMmas; m++) {
-                            if (m == kMmas - 1) ready = tc::mbar_test(full0 + 8 * next, next_phase);
-                            mma_bf16(d, ad + (m >> 2) * (kSubBytes >> 4) + (m & 3) * a_step,
-                                     bd + (m >> 2) * (sub_b >> 4) + (m & 3) * b_step, idesc, (kb != ti.k0) | (m != 0));
+                    const uint32_t d = tmem + (uint32_t)buf * kTile;
+                    for (int kb = c0; kb < c1; kb++) {
+                        if (!ready && !tc::mbar_wait(full0 + 8 * stage, phase, abort_flag, p.status, p.timeout_ns)) {
+                            ok = false;
+                            break;
                         }
-                    } else {
-                        for (int m = 0; m < p.mma_last; m++)
-                            mma_bf16(d, ad + (m >> 2) * (kSubBytes >> 4) + (m & 3) * a_step,
-                                     bd + (m >> 2) * (sub_b >> 4) + (m & 3) * b_step, idesc, (kb != ti.k0) | (m != 0));
-                        ready = false;
+                        tc::fence_after();
+                        const uint64_t ad = ad0 + (uint64_t)(stage * (kOpBytes >> 4));
+                        const uint64_t bd = bd0 + (uint64_t)(stage * (b_bytes >> 4));
+                        const int next = stage + 1 == S ? 0 : stage + 1;
+                        const uint32_t next_phase = next == 0 ? phase ^ 1 : phase;
+                        if (kb != p.k_stages - 1 || p.mma_last == kMmas) {
+                            // the next stage's barrier is tested while this stage's MMAs run
+#pragma unroll
+                            for (int m = 0; m < kMmas; m++) {
+                                if (m == kMmas - 1) ready = tc::mbar_test(full0 + 8 * next, next_phase);
+                                mma_bf16(d, ad + (m >> 2) * (kSubBytes >> 4) + (m & 3) * a_step,
+                                         bd + (m >> 2) * (sub_b >> 4) + (m & 3) * b_step, idesc, (kb != c0) | (m != 0));
+                            }
+                        } else {
+                            for (int m = 0; m < p.mma_last; m++)
+                                mma_bf16(d, ad + (m >> 2) * (kSubBytes >> 4) + (m & 3) * a_step,
+                                         bd + (m >> 2) * (sub_b >> 4) + (m & 3) * b_step, idesc, (kb != c0) | (m != 0));
+                            ready = false;
+                        }
+                        any = true;
+                        tc::commit<2>(empty0 + 8 * stage, 3);
+                        if (kb == c1 - 1) tc::commit<2>(tfull0 + 8 * buf, 3);
+                        stage = next;
+                        phase = next_phase;
                     }
-                    any = true;
-                    tc::commit<2>(empty0 + 8 * stage, 3);
-                    if (kb == ti.k1 - 1) tc::commit<2>(tfull0 + 8 * buf, 3);
-                    stage = next;
-                    phase = next_phase;
                 }
             }
             if (!ok) *abort_flag = 1;
@@ -402,52 +427,62 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         int iter = 0, n = 0;
         if (FEW) {
             // A thread owns one row of w and the tokens 64 half ... 64 half + 63.
-            for (int t = cid; t < p.total; t += ncl, ++iter) {
-                const int buf = iter & 1, local = (int)rank * (p.tile_m / 2) + q * 32 + lane;
-                const int64_t row = (int64_t)tile_at(p, t).mt * p.tile_m + local;      // vocabulary row of the piece
+            for (int t = cid; t < p.total; t += ncl) {
+                const int mt = tile_at(p, t).mt;
+                const int64_t row = (int64_t)mt * p.tile_m + rank * (p.tile_m / 2) + q * 32 + lane;     // of the piece
                 const bool in = q * 32 + lane < p.tile_m / 2 && row < p.M;
-                const int64_t part = ((int64_t)tile_at(p, t).mt * 2 + rank) * 4 + q;
-                if (!tc::mbar_wait(tfull0 + 8 * buf, (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns)) break;
-                tc::fence_after();
-                const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kTile);
-#pragma unroll 1
-                for (int c = 64 * half; c < 64 * half + 64 && c < p.N; c += 32) {
-                    float v[32];
-                    load_acc(v, ta + c);
-                    float mine_m = kNegInf, mine_s = 0.0f;
+                const int64_t part = ((int64_t)mt * 2 + rank) * 4 + q;
+                const int tokens = (int)p.N - 64 * half;       // of this warp, at most 64
+                float z[64] = {};
+                bool ok = true;
+                for (int c0 = 0; c0 < p.k_stages && ok; c0 += p.chunk, ++iter) {
+                    const int buf = iter & 1;
+                    ok = tc::mbar_wait(tfull0 + 8 * buf, (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns);
+                    if (!ok) break;
+                    tc::fence_after();
+                    const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kTile + 64 * half);
 #pragma unroll
-                    for (int j = 0; j < 32; j++) {
-                        if (c + j >= p.N) break;
-                        const bool hit = in && row == few_target[c + j];
-                        if (MODE == kFewStats) {
-                            if (hit) p.hit[c + j] = v[j];
-                            const float z = in ? v[j] : kNegInf;
-                            float m = z;
-#pragma unroll
-                            for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-                            float e = exp2_fast((z - (m == kNegInf ? 0.0f : m)) * kLog2e);
-#pragma unroll
-                            for (int d = 16; d; d >>= 1) e += __shfl_xor_sync(0xffffffffu, e, d);
-                            if (lane == j) {
-                                mine_m = m;
-                                mine_s = e;
-                            }
-                        } else if (in) {
-                            const float ratio = few_ratio[c + j];
-                            const float g = exp2_fast((v[j] - few_lse[c + j]) * kLog2e) - (hit ? 1.0f : 0.0f);
-                            p.g[(int64_t)(c + j) * p.ld_g + row] = __float2bfloat16_rn(ratio == 0.0f ? 0.0f : g * ratio);
-                        }
-                    }
-                    if (MODE == kFewStats && c + lane < p.N) p.part[part * p.N + c + lane] = make_float2(mine_m, mine_s);
+                    for (int c = 0; c < 64; c += 16)
+                        if (c < tokens) add_acc(z + c, ta + c);
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive_cluster(tempty_c0 + 8 * buf);
                 }
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive_cluster(tempty_c0 + 8 * buf);
+                if (!ok) break;
+                float mine_m[2] = {kNegInf, kNegInf}, mine_s[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int j = 0; j < 64; j++) {
+                    if (j >= tokens) continue;
+                    const int token = 64 * half + j;
+                    const bool hit = in && row == few_target[token];
+                    if (MODE == kFewStats) {
+                        if (hit) p.hit[token] = z[j];
+                        const float x = in ? z[j] : kNegInf;
+                        float m = x;
+#pragma unroll
+                        for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+                        float e = exp2_fast((x - (m == kNegInf ? 0.0f : m)) * kLog2e);
+#pragma unroll
+                        for (int d = 16; d; d >>= 1) e += __shfl_xor_sync(0xffffffffu, e, d);
+                        if (lane == (j & 31)) {
+                            mine_m[j >> 5] = m;
+                            mine_s[j >> 5] = e;
+                        }
+                    } else if (in) {
+                        const float ratio = few_ratio[token];
+                        const float g = exp2_fast((z[j] - few_lse[token]) * kLog2e) - (hit ? 1.0f : 0.0f);
+                        p.g[(int64_t)token * p.ld_g + row] = __float2bfloat16_rn(ratio == 0.0f ? 0.0f : g * ratio);
+                    }
+                }
+                if (MODE == kFewStats)
+#pragma unroll
+                    for (int j = 0; j < 2; j++)
+                        if (32 * j + lane < tokens)
+                            p.part[part * p.N + 64 * half + 32 * j + lane] = make_float2(mine_m[j], mine_s[j]);
             }
         } else
-        for (int t = cid; t < p.total; t += ncl, ++iter) {
+        for (int t = cid; t < p.total; t += ncl) {
             const TileAt ti = tile_at(p, t);
-            const int buf = iter & 1;
             const int64_t row0 = (int64_t)ti.mt * kTile + rank * 128 + q * 32, row = row0 + lane;       // tile_m is 256
             const int64_t col0 = (int64_t)ti.nt * kTile + half * 128;
             // what the row needs, read while the tile is computed
@@ -464,48 +499,52 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     if (at >= 0 && at < 128) target = (int)at;
                 }
             }
-            if (!tc::mbar_wait(tfull0 + 8 * buf, (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns)) break;
-            tc::fence_after();
-            const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kTile + half * 128);
             const bool live = row0 < p.M && (MODE == kStats || col0 < p.N);
-            float v[32];
-            if (MODE == kStats && live) {
-                // two passes over the accumulator: it is read from tensor memory again
-                // rather than held in 128 registers
-                const int cols = (int)min((int64_t)128, p.N - col0);       // 0 or less: an empty part
-                const bool hits = __any_sync(0xffffffffu, target >= 0 && target < cols);
-                float m = kNegInf, hit = 0.0f;
-#pragma unroll 1
-                for (int c = 0; c < cols; c += 32) {
-                    load_acc(v, ta + c);
+            const uint32_t ta0 = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * 128);
+            if (MODE == kStats) {
+                float z[128] = {};
+                bool ok = true;
+                for (int c0 = ti.k0; c0 < ti.k1; c0 += p.chunk, ++iter) {
+                    ok = tc::mbar_wait(tfull0 + 8 * (iter & 1), (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns);
+                    if (!ok) break;
+                    tc::fence_after();
 #pragma unroll
-                    for (int j = 0; j < 32; j++) {
-                        if (c + j >= cols) v[j] = kNegInf;
-                        m = fmaxf(m, v[j]);
-                    }
-                    if (hits)
-#pragma unroll
-                        for (int j = 0; j < 32; j++)
-                            if (target == c + j) hit = v[j];
+                    for (int c = 0; c < 128; c += 16) add_acc(z + c, ta0 + (uint32_t)((iter & 1) * kTile + c));
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive_cluster(tempty_c0 + 8 * (iter & 1));
                 }
+                if (!ok) break;
+                if (!live) continue;
+                const int cols = (int)min((int64_t)128, p.N - col0);       // 0 or less: an empty part
+                if (cols < 128)
+#pragma unroll
+                    for (int j = 0; j < 128; j++) z[j] = j < cols ? z[j] : kNegInf;
+                if (__any_sync(0xffffffffu, target >= 0)) {
+#pragma unroll
+                    for (int j = 0; j < 128; j++)
+                        if (target == j && j < cols) p.hit[row] = z[j];
+                }
+                float m4[4] = {z[0], z[1], z[2], z[3]};
+#pragma unroll
+                for (int j = 4; j < 128; j++) m4[j & 3] = fmaxf(m4[j & 3], z[j]);
+                const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 // z - m is formed first: a product with log2(e) before it would round away the
                 // difference of large logits
                 const float m0 = m == kNegInf ? 0.0f : m;
                 float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 1
-                for (int c = 0; c < cols; c += 32) {
-                    load_acc(v, ta + c);
 #pragma unroll
-                    for (int j = 0; j < 32; j++) {
-                        if (c + j >= cols) v[j] = kNegInf;
-                        s[j & 3] += exp2_fast((v[j] - m0) * kLog2e);
-                    }
-                }
-                if (row < p.M) {
-                    if (target >= 0 && target < cols) p.hit[row] = hit;
-                    p.part[((int64_t)2 * ti.nt + half) * p.M + row] = make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
-                }
-            } else if (live) {
+                for (int j = 0; j < 128; j++) s[j & 3] += exp2_fast((z[j] - m0) * kLog2e);
+                if (row < p.M) p.part[((int64_t)2 * ti.nt + half) * p.M + row] = make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
+                continue;
+            }
+            const int buf = iter & 1;
+            if (!tc::mbar_wait(tfull0 + 8 * buf, (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns)) break;
+            tc::fence_after();
+            ++iter;
+            const uint32_t ta = ta0 + (uint32_t)(buf * kTile);
+            float v[32];
+            if (live) {
                 // ratio 0 (a token that does not count) gives 0 whatever its logits
 #pragma unroll 1
                 for (int c = 0; c < 128; c += 32) {
@@ -640,6 +679,7 @@ cudaError_t gemm(GemmParams p, const Operand& a, const Operand& b, const CUtenso
         return cudaErrorInvalidValue;
     p.tile_n = tile_n;
     p.k_stages = (int32_t)((K + kSub * kSubK - 1) / (kSub * kSubK));
+    p.chunk = MODE == kStats || MODE == kFewStats ? kChunk : p.k_stages;
     p.mma_last = (int32_t)((K - (int64_t)(p.k_stages - 1) * kSub * kSubK + 15) / 16);
     p.tile_m = tile_m;
     p.b_bytes = kSub * (tile_n / 2) * kSubK * 2;

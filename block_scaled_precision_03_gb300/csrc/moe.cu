@@ -9,18 +9,25 @@
 // find their rank with one match, the warps' counts per expert are summed in
 // warp order, so no atomic decides an order.  Up to kSortThreads slots (a
 // decoding step) every CTA of the gather sorts them by itself and the whole
-// dispatch is one launch; above that a count kernel and a place kernel run
-// first, each the programmatic dependent of the one before.
+// dispatch is one launch.  Up to kClusterSlots one cluster of 8 CTAs sorts them
+// (their counts meet through distributed shared memory), above that a count
+// kernel and a place kernel; the gather follows as their programmatic
+// dependent.
 //
 // The row movements are bound by memory: the gather reads a token's row once
 // and writes it to its k rows, the combine reads the k rows and writes one,
 // the combine's gradient reads dout and the k rows and writes k rows and k dot
 // products.  A group of 1 to 8 warps owns a token; rows on 16-byte boundaries
-// move in 16-byte vectors, others element by element, several in flight.
+// move in 16-byte vectors, others element by element, several in flight.  (Such
+// rows read as two aligned vectors and a shift along the boundaries of the row
+// that is written were slower: 4096 x 8 x 2047 combined in 70 us instead of 53,
+// its gradient with k = 4 in 92 instead of 49, because the warps that hold a
+// row's ends go both ways.)
 #include <algorithm>
 #include "common.cuh"
 #include "internal.h"
 #include "launch.cuh"
+#include "tcgen05.cuh"
 
 namespace bsq {
 namespace {
@@ -72,6 +79,23 @@ __device__ __forceinline__ int32_t block_scan(int32_t v, int32_t& all) {
     return s - v + (warp > 0 ? before : 0);
 }
 
+// counts[w] of `warps` warps, `pitch` apart: each becomes the sum of those
+// before it; returns the sum of all.
+__device__ __forceinline__ int32_t scan_warps(uint16_t* counts, int pitch, int warps) {
+    int32_t sum = 0;
+    for (int w0 = 0; w0 < warps; w0 += 8) {
+        int n[8];
+#pragma unroll
+        for (int w = 0; w < 8; w++) n[w] = w0 + w < warps ? counts[(w0 + w) * pitch] : 0;
+#pragma unroll
+        for (int w = 0; w < 8; w++) {
+            if (w0 + w < warps) counts[(w0 + w) * pitch] = (uint16_t)sum;
+            sum += n[w];
+        }
+    }
+    return sum;
+}
+
 // One step: this thread's slot (expert e, -1 for none).  wcount[warps][experts]
 // receives, per warp, the slots of each expert in the warps before it; returns
 // the slot's rank in its warp.  `sum` (thread x < experts): the step's slots of
@@ -84,13 +108,7 @@ __device__ __forceinline__ int step_ranks(int e, int experts, int warps, uint16_
     const int rank = __popc(same & ((1u << lane) - 1));
     if (e >= 0 && rank == 0) wcount[warp * experts + e] = (uint16_t)__popc(same);
     __syncthreads();
-    sum = 0;
-    if (tid < experts)
-        for (int w = 0; w < warps; w++) {
-            const int n = wcount[w * experts + tid];
-            wcount[w * experts + tid] = (uint16_t)sum;
-            sum += n;
-        }
+    sum = tid < experts ? scan_warps(wcount + tid, experts, warps) : 0;
     return rank;
 }
 
@@ -156,6 +174,54 @@ __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(const SortArgs 
             if (row >= 0) a.row_slot[row] = (int32_t)i;
         }
     }
+}
+
+// One cluster sorts up to kClusterSlots slots, one a thread: a CTA's counts per
+// expert meet the other CTAs' through distributed shared memory.  (With 2 to 8
+// slots a thread it also sorted 65536, but 8 SMs write the plan too slowly then:
+// 32768 slots took 4 us longer than the two launches below.)
+constexpr int kCluster = 8;
+constexpr int64_t kClusterSlots = (int64_t)kCluster * kSortThreads;
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads) moe_cluster_sort_kernel(const SortArgs a) {
+    extern __shared__ int32_t sm[];
+    const int E = a.experts, tid = threadIdx.x;
+    int32_t* mine = sm;                                     // [E] this CTA's slots of each expert
+    int32_t* base = sm + E;                                 // [E] first row of each expert for this CTA
+    uint16_t* wcount = reinterpret_cast<uint16_t*>(sm + 2 * E);    // [32][E]
+    const int64_t slot = (int64_t)blockIdx.x * kSortThreads + tid;
+    pdl_launch_dependents();
+    const int e = slot < a.slots ? load_id(a, slot) : -1;
+    int32_t sum;
+    const int rank = step_ranks(e, E, 32, wcount, sum);
+    if (tid < E) mine[tid] = sum;
+    tc::cluster_sync();
+    int32_t total = 0, before = 0;
+    if (tid < E) {
+        const uint32_t at = tc::smem_u32(mine + tid);
+#pragma unroll
+        for (int c = 0; c < kCluster; c++) {
+            const int32_t n = tc::ld_cluster_s32(tc::mapa(at, c));
+            if (c < (int)blockIdx.x) before += n;
+            total += n;
+        }
+    }
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");      // done with the other CTAs' counts
+    int32_t all;
+    const int32_t first = block_scan(total, all);
+    if (tid < E) {
+        base[tid] = first + before;
+        if (blockIdx.x == 0) a.offsets[tid] = first;
+    }
+    if (blockIdx.x == 0 && tid == 0) a.offsets[E] = all;
+    __syncthreads();
+    const int32_t row = e >= 0 ? base[e] + wcount[(tid >> 5) * E + e] + rank : -1;
+    if (slot < a.slots) {
+        a.slot_row[slot] = row;
+        if (row >= 0) a.row_slot[row] = (int32_t)slot;
+        if (slot >= all) a.row_slot[slot] = -1;
+    }
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");        // a CTA's counts outlive their readers
 }
 
 struct RowArgs {
@@ -534,14 +600,22 @@ cudaError_t small_t(const MoePlanArgs& p, const SortArgs& s, const MoeRowsArgs* 
     return cudaGetLastError();
 }
 
-// more than kSortThreads slots: the plan in two launches
+// more than kSortThreads slots: the plan by one cluster, or in two launches
 cudaError_t sort_large(const SortArgs& s, cudaStream_t st) {
-    moe_count_kernel<<<s.chunks, kSortThreads, s.experts * sizeof(int32_t), st>>>(s);
     const size_t smem = 2 * s.experts * sizeof(int32_t) + (size_t)32 * s.experts * sizeof(uint16_t);
-    if (smem > 40 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(moe_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 80 * 1024);
+    const auto allow = [&](const void* k) {
+        return smem > 40 * 1024 ? cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 80 * 1024)
+                                : cudaSuccess;
+    };
+    if (s.slots <= kClusterSlots) {
+        cudaError_t e = allow(reinterpret_cast<const void*>(moe_cluster_sort_kernel));
         if (e != cudaSuccess) return e;
+        moe_cluster_sort_kernel<<<kCluster, kSortThreads, smem, st>>>(s);
+        return cudaGetLastError();
     }
+    cudaError_t e = allow(reinterpret_cast<const void*>(moe_place_kernel));
+    if (e != cudaSuccess) return e;
+    moe_count_kernel<<<s.chunks, kSortThreads, s.experts * sizeof(int32_t), st>>>(s);
     return launch_k(true, moe_place_kernel, dim3(s.chunks), kSortThreads, smem, st, s);
 }
 

@@ -8,9 +8,11 @@
 //   dw = sum over the rows of dy xh, db = sum over the rows of dy.
 //
 // Both are bound by memory; a row is read once and held in registers as packed
-// 16-byte vectors.  The vectors lie on 16-byte boundaries of memory, so rows
-// that start elsewhere (odd widths) take a vector at either end that is only
-// partly theirs, moved element by element.
+// 16-byte vectors.  The vectors lie on 16-byte boundaries of x; where rows start
+// off those boundaries (odd widths) their first and last vectors move element
+// by element, dy is read by two aligned loads and a shift where it lies
+// otherwise than x, and an output that lies otherwise is written element by
+// element.
 //
 // Forward: a group of lanes owns a row, one warp up to 512 vectors, so most
 // rows need no barrier at all; many independent rows per SM hide the latency
@@ -112,57 +114,38 @@ __device__ __forceinline__ void group_sum(float (&v)[N], const Group& q, float* 
 }
 
 // A row's vectors of one thread, v = at + i * tpr.  Vector v holds the columns
-// v * VEC - shift ... (shift: elements between the 16-byte boundary at or
-// before the row's start and that start; 0 for EVEN rows, which also hold
-// whole vectors only); columns outside [0, cols) are zero here and not stored.
-// The grid of vectors is x's; a matrix whose row lies otherwise (`alike` false)
-// is moved element by element.
+// v * VEC - shift ... (shift: where x's row starts behind a 16-byte boundary,
+// whatever the other matrices do, so that the sums do not depend on them; 0 for
+// EVEN calls, whose rows all start on one and hold whole vectors); columns
+// outside [0, cols) are zero here and not stored.
 template <typename T, int NV, bool EVEN>
 struct Row {
     static constexpr int VEC = kVec<T>;
     Pack<T, VEC> p[NV];
-    __device__ __forceinline__ static int shift_of(const T* row) {
-        return EVEN ? 0 : (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
-    }
-    __device__ __forceinline__ static bool whole(int c, int cols) { return EVEN ? c < cols : c >= 0 && c + VEC <= cols; }
-    __device__ __forceinline__ void load(const T* row, int shift, bool alike, int at, int tpr, int cols) {
+    // `alike`: the row lies to 16-byte boundaries as the vectors do
+    __device__ __forceinline__ void load(const T* row, bool alike, int shift, int at, int tpr, int cols) {
 #pragma unroll
         for (int i = 0; i < NV; i++) {
             const int c = (at + i * tpr) * VEC - shift;
             p[i].zero();
-            if (whole(c, cols) && (EVEN || alike)) {
-                p[i].load(row + c);
-            } else if (!EVEN && c < cols) {
-                float f[VEC];
+            if (EVEN ? c < cols : alike && c >= 0 && c + VEC <= cols) p[i].load(row + c);
+        }
+        // the rest after all of those: the branches would keep them apart
+        if constexpr (!EVEN)
 #pragma unroll
-                for (int e = 0; e < VEC; e++) {
-                    Pack<T, 1> one;
-                    float x[1] = {0.0f};
-                    if (c + e >= 0 && c + e < cols) {
-                        one.load(row + c + e);
-                        one.unpack(x);
-                    }
-                    f[e] = x[0];
-                }
-                p[i].pack(f);
+            for (int i = 0; i < NV; i++) {
+                const int c = (at + i * tpr) * VEC - shift;
+                if (c >= cols || (alike && c >= 0 && c + VEC <= cols)) continue;
+                if (is_inside<T>(c, cols)) load_inside(p[i], row, c);
+                else load_elements(p[i], row, c, cols);
             }
-        }
     }
-    __device__ __forceinline__ static void store(T* row, int c, bool alike, int cols, const float (&f)[VEC]) {
-        if (whole(c, cols) && (EVEN || alike)) {
-            Pack<T, VEC> o;
-            o.pack(f);
-            o.store(row + c);
-        } else if (!EVEN && c < cols) {
-#pragma unroll
-            for (int e = 0; e < VEC; e++)
-                if (c + e >= 0 && c + e < cols) {
-                    Pack<T, 1> one;
-                    const float x[1] = {f[e]};
-                    one.pack(x);
-                    one.store(row + c + e);
-                }
-        }
+    __device__ __forceinline__ static void store(T* row, bool alike, int c, int cols, const float (&f)[VEC]) {
+        Pack<T, VEC> o;
+        o.pack(f);
+        if (EVEN) o.store(row + c);
+        else if (alike) store_edge(o, row, c, cols);
+        else store_elements(o, row, c, cols);
     }
     // Between two passes over the row: the compiler may not keep the unpacked
     // values of the first for the second (twice the registers).
@@ -173,30 +156,39 @@ struct Row {
             asm volatile("" : "+r"(u[0]), "+r"(u[1]), "+r"(u[2]), "+r"(u[3]));
         }
     }
-    // zero outside the row (EVEN: the vector is the row's or is skipped as a whole)
-    __device__ __forceinline__ static float keep(float x, int c, int cols) {
-        return EVEN || (c >= 0 && c < cols) ? x : 0.0f;
-    }
 };
 
 // Weight and bias of odd rows: column c at [c % VEC][c / VEC], so that lanes
-// whose columns lie VEC apart read neighbouring words.
+// whose columns lie VEC apart read neighbouring words.  The last word of every
+// line is zero, and so is what columns outside the row find there.
 template <int VEC>
 struct OddParams {
-    float *w, *b;
-    int pitch;
-    __device__ __forceinline__ void fill(float* smem, const NormArgs& a) {
-        pitch = (int)((a.cols + VEC - 1) / VEC);
+    float* w;
+    int pitch, off[VEC];
+    __device__ __forceinline__ void fill(float* smem, const NormArgs& a, bool bias) {
+        pitch = (int)((a.cols + VEC - 1) / VEC) + 1;
         w = smem;
-        b = smem + VEC * pitch;
+        for (int i = threadIdx.x; i < (bias ? 2 : 1) * VEC * pitch; i += blockDim.x) w[i] = 0.0f;
+        __syncthreads();
         for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
-            w[c % VEC * pitch + c / VEC] = a.weight ? param(a.weight, a.param_bf16, c) : 1.0f;
-            b[c % VEC * pitch + c / VEC] = a.bias ? param(a.bias, a.param_bf16, c) : 0.0f;
+            float* at = w + c % VEC * pitch + c / VEC;
+            at[0] = a.weight ? param(a.weight, a.param_bf16, c) : 1.0f;
+            if (bias) at[VEC * pitch] = a.bias ? param(a.bias, a.param_bf16, c) : 0.0f;
         }
         __syncthreads();
     }
-    __device__ __forceinline__ float at(const float* f, int c, int cols) const {
-        return c >= 0 && c < cols ? f[c % VEC * pitch + c / VEC] : 0.0f;
+    // for a row whose vectors are shifted: where element e of vector v is, off[e] + v
+    __device__ __forceinline__ void row(int shift) {
+#pragma unroll
+        for (int e = 0; e < VEC; e++) off[e] = ((e - shift) & (VEC - 1)) * pitch + ((e - shift) >> (VEC == 8 ? 3 : 2));
+    }
+    __device__ __forceinline__ void weights(float (&f)[VEC], int v) const {
+#pragma unroll
+        for (int e = 0; e < VEC; e++) f[e] = w[off[e] + v];
+    }
+    __device__ __forceinline__ void biases(float (&f)[VEC], int v) const {
+#pragma unroll
+        for (int e = 0; e < VEC; e++) f[e] = w[VEC * pitch + off[e] + v];
     }
 };
 
@@ -210,14 +202,17 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a, int
     const int groups = blockDim.x / tpr, g = q.g, at = q.at, cols = (int)a.cols;
     const float per_col = 1.0f / (float)cols;
     OddParams<VEC> odd;
-    if (!EVEN) odd.fill(odd_smem, a);
+    if (!EVEN) odd.fill(odd_smem, a, true);
     for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < a.rows; r0 += (int64_t)gridDim.x * groups) {
         const int64_t r = r0 + g;
         const bool live = r < a.rows;              // lanes of a warp stay together for the sums
+        T* y = static_cast<T*>(a.y) + (live ? r : 0) * a.ldy;
         const T* row = static_cast<const T*>(a.x) + (live ? r : 0) * a.ldx;
-        const int shift = R::shift_of(row);
+        const int shift = EVEN ? 0 : row_shift(row);
+        const bool alike = EVEN || row_shift(y) == shift;
+        if (!EVEN) odd.row(shift);
         R x;
-        if (live) x.load(row, shift, true, at, tpr, cols);
+        if (live) x.load(row, true, shift, at, tpr, cols);
         else
 #pragma unroll
             for (int i = 0; i < NV; i++) x.p[i].zero();
@@ -239,17 +234,16 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a, int
             if (c >= cols) continue;
             float f[VEC];
             x.p[i].unpack(f);
+            const bool whole = EVEN || (c >= 0 && c + VEC <= cols);
 #pragma unroll
             for (int e = 0; e < VEC; e++) {
-                const float d = R::keep(f[e] - mean, c + e, cols);
-                s[0] = fmaf(d, d, s[0]);
+                const float d = f[e] - mean;
+                if (whole || (c + e >= 0 && c + e < cols)) s[0] = fmaf(d, d, s[0]);
             }
         }
         group_sum(s, q, part, 1);
         const float rstd = rsqrtf(fmaf(s[0], per_col, a.eps));
         if (!live) continue;
-        T* y = static_cast<T*>(a.y) + r * a.ldy;
-        const bool alike = R::shift_of(y) == shift;
         x.again();
 #pragma unroll
         for (int i = 0; i < NV; i++) {
@@ -261,15 +255,12 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a, int
                 params<VEC>(w, a.weight, a.param_bf16, 1.0f, c);
                 params<VEC>(b, a.bias, a.param_bf16, 0.0f, c);
             } else {
-#pragma unroll
-                for (int e = 0; e < VEC; e++) {
-                    w[e] = odd.at(odd.w, c + e, cols);
-                    b[e] = odd.at(odd.b, c + e, cols);
-                }
+                odd.weights(w, at + i * tpr);
+                odd.biases(b, at + i * tpr);
             }
 #pragma unroll
             for (int e = 0; e < VEC; e++) f[e] = (f[e] - mean) * rstd * w[e] + b[e];
-            R::store(y, c, alike, cols, f);
+            R::store(y, alike, c, cols, f);
         }
         if (at == 0) {
             if (a.mean) a.mean[r] = mean;
@@ -289,19 +280,22 @@ __global__ void __launch_bounds__(kMaxThreads) norm_dx_kernel(const NormArgs a, 
     const int groups = blockDim.x / tpr, g = q.g, at = q.at, cols = (int)a.cols;
     const float per_col = 1.0f / (float)cols;
     OddParams<VEC> odd;
-    if (!EVEN) odd.fill(odd_smem, a);
+    if (!EVEN) odd.fill(odd_smem, a, false);
     int n = 0;
     for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < a.rows; r0 += (int64_t)gridDim.x * groups, n ^= 1) {
         const int64_t r = r0 + g;
         const bool live = r < a.rows;
+        T* dx = static_cast<T*>(a.y) + (live ? r : 0) * a.ldy;
         const T* row = static_cast<const T*>(a.x) + (live ? r : 0) * a.ldx;
-        const int shift = R::shift_of(row);
+        const int shift = EVEN ? 0 : row_shift(row);
+        const bool alike = EVEN || row_shift(dx) == shift;
+        if (!EVEN) odd.row(shift);
         R x, d;
         float mean = 0.0f, rstd = 0.0f;
         if (live) {
             const T* dy = static_cast<const T*>(a.dy) + r * a.ld_dy;
-            x.load(row, shift, true, at, tpr, cols);
-            d.load(dy, shift, R::shift_of(dy) == shift, at, tpr, cols);
+            x.load(row, true, shift, at, tpr, cols);
+            d.load(dy, EVEN || row_shift(dy) == shift, shift, at, tpr, cols);
             mean = a.mean[r];
             rstd = a.rstd[r];
         } else {
@@ -320,19 +314,17 @@ __global__ void __launch_bounds__(kMaxThreads) norm_dx_kernel(const NormArgs a, 
             x.p[i].unpack(fx);
             d.p[i].unpack(fd);
             if (EVEN) params<VEC>(w, a.weight, a.param_bf16, 1.0f, c);
+            else odd.weights(w, at + i * tpr);
 #pragma unroll
             for (int e = 0; e < VEC; e++) {
-                // outside the row dy and the weight are zero here
-                const float gr = fd[e] * (EVEN ? w[e] : odd.at(odd.w, c + e, cols));
+                const float gr = fd[e] * w[e];         // outside the row both are zero
                 s[0] += gr;
                 s[1] = fmaf(gr, (fx[e] - mean) * rstd, s[1]);
             }
         }
         group_sum(s, q, part, n);
         if (!live) continue;
-        T* dx = static_cast<T*>(a.y) + r * a.ldy;
         const float s0 = s[0] * per_col, s1 = s[1] * per_col;
-        const bool alike = R::shift_of(dx) == shift;
         x.again();
         d.again();
 #pragma unroll
@@ -343,10 +335,10 @@ __global__ void __launch_bounds__(kMaxThreads) norm_dx_kernel(const NormArgs a, 
             x.p[i].unpack(fx);
             d.p[i].unpack(fd);
             if (EVEN) params<VEC>(w, a.weight, a.param_bf16, 1.0f, c);
+            else odd.weights(w, at + i * tpr);
 #pragma unroll
-            for (int e = 0; e < VEC; e++)
-                fd[e] = rstd * (fd[e] * (EVEN ? w[e] : odd.at(odd.w, c + e, cols)) - s0 - (fx[e] - mean) * rstd * s1);
-            R::store(dx, c, alike, cols, fd);
+            for (int e = 0; e < VEC; e++) fd[e] = rstd * (fd[e] * w[e] - s0 - (fx[e] - mean) * rstd * s1);
+            R::store(dx, alike, c, cols, fd);
         }
     }
 }
@@ -823,7 +815,7 @@ int lanes(int64_t n, int nv) {
 
 size_t odd_bytes(const NormArgs& a, bool even) {
     const int64_t vec = a.bf16 ? 8 : 4;
-    return even ? 0 : (size_t)(2 * vec * ((a.cols + vec - 1) / vec)) * sizeof(float);
+    return even ? 0 : (size_t)(2 * vec * ((a.cols + vec - 1) / vec + 1)) * sizeof(float);
 }
 
 template <typename T, int NV, bool EVEN>
@@ -888,8 +880,11 @@ cudaError_t backward(const NormArgs& a, cudaStream_t st) {
 
 template <typename T, int VEC>
 cudaError_t columns(const NormArgs& a, cudaStream_t st) {
-    const int groups = (int)std::min<int64_t>(a.rows, kWideParts);
-    norm_columns_kernel<T, VEC><<<dim3((unsigned)((a.cols / VEC + 127) / 128), groups), 128, 0, st>>>(a);
+    // row groups: enough CTAs for every SM to hold several, at least 8 rows each
+    const int64_t blocks = (a.cols + 128 * VEC - 1) / (128 * VEC);
+    const int64_t want = std::max<int64_t>(kWideParts, (int64_t)a.num_sms * 8 / blocks);
+    const int groups = (int)std::max<int64_t>(1, std::min<int64_t>({want, (a.rows + 7) / 8, kMaxParts}));
+    norm_columns_kernel<T, VEC><<<dim3((unsigned)blocks, groups), 128, 0, st>>>(a);
     return launch_k(true, norm_reduce_kernel, dim3((unsigned)((a.cols + 31) / 32), 2), 1024, 0, st, a.ws, groups, a.cols,
                     a.dweight, a.dbias);
 }
@@ -905,7 +900,7 @@ bool even_rows(const NormArgs& a) {
 // else as many as keep a row inside one warp.
 template <typename T, bool EVEN>
 cudaError_t forward_e(const NormArgs& a, cudaStream_t st) {
-    const int64_t n = a.cols / kVec<T> + (EVEN ? 0 : 2);
+    const int64_t n = EVEN ? a.cols / kVec<T> : (a.cols + 2 * kVec<T> - 2) / kVec<T>;
     if (a.rows <= 2 * a.num_sms) {
         if (n <= kMaxThreads) return forward<T, 1, EVEN>(a, n, st);
         if (n <= 2 * kMaxThreads) return forward<T, 2, EVEN>(a, n, st);
@@ -929,7 +924,7 @@ cudaError_t forward_t(const NormArgs& a, cudaStream_t st) {
 
 template <typename T, bool EVEN>
 cudaError_t dx_e(const NormArgs& a, cudaStream_t st) {
-    const int64_t n = a.cols / kVec<T> + (EVEN ? 0 : 2);
+    const int64_t n = EVEN ? a.cols / kVec<T> : (a.cols + 2 * kVec<T> - 2) / kVec<T>;
     if (a.rows <= 2 * a.num_sms && n <= 2 * kMaxThreads) return dx_only<T, 2, EVEN>(a, n, st);
     if (n <= 4 * 32) return dx_only<T, 4, EVEN>(a, n, st);
     return dx_only<T, 8, EVEN>(a, n, st);
@@ -947,7 +942,7 @@ cudaError_t backward_t(const NormArgs& a, cudaStream_t st) {
     }
     // the column sums first: dx may be written over dy
     if (a.dweight || a.dbias) {
-        cudaError_t e = even ? columns<T, kVec<T>>(a, st) : columns<T, 1>(a, st);
+        cudaError_t e = even ? columns<T, VEC>(a, st) : columns<T, 1>(a, st);
         if (e != cudaSuccess) return e;
     }
     if (even && n <= 8 * kMaxThreads) return dx_e<T, true>(a, st);
