@@ -1,8 +1,10 @@
-"""Build libbsq.so in-tree with nvcc for sm_103a.
+"""Build libbsq.so in-tree with nvcc for sm_103a, and the native Python
+binding _binding.so with the host compiler.
 
 Each .cu file is compiled in parallel into _build/, then linked into
 block_scaled_precision_03_gb300/libbsq.so (CUDA runtime linked statically,
-driver entry points resolved at run time).  Usage:
+driver entry points resolved at run time); binding.cpp is compiled against the
+installed PyTorch beside them.  Usage:
 
     python -m block_scaled_precision_03_gb300._build [--force] [-v]
 """
@@ -17,6 +19,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libbsq.so")
+BINDING = os.path.join(HERE, "_binding.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["api.cu", "quantize.cu", "convert.cu", "gemm.cu", "gemm2.cu", "api_ops.cu", "moe.cu",
            "norm.cu", "head.cu", "clip.cu"]
@@ -37,8 +40,26 @@ def _deps():
     return max(os.path.getmtime(f) for f in files)
 
 
+def _compile_binding():
+    import sysconfig
+    import torch
+    root = os.path.dirname(torch.__file__)
+    tmp = BINDING + f".{os.getpid()}.tmp"
+    abi = f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", abi,
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(root, "include"),
+           "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"),
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", os.path.join(root, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{os.path.join(root, 'lib')}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps():
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps() for f in (LIB, BINDING)):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     flags = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE] + ARCH
@@ -55,8 +76,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
-    with ThreadPoolExecutor(len(SOURCES)) as ex:
+    with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
+        binding.result()
     tmp = LIB + f".{os.getpid()}.tmp"
     r = subprocess.run([nvcc(), "-shared", *ARCH, "-o", tmp, *objs, "-cudart", "static"],
                        capture_output=True, text=True)
