@@ -56,9 +56,10 @@ __device__ __forceinline__ int load_id(const SortArgs& a, int64_t i) {
     return id >= 0 && id < a.experts ? (int)id : -1;
 }
 
-// Exclusive scan over the threads of a CTA of kSortThreads; `all` is the sum.
+// Exclusive scan over the threads of a CTA; `all` is the sum.
+template <int THREADS>
 __device__ __forceinline__ int32_t block_scan(int32_t v, int32_t& all) {
-    __shared__ int32_t warp_sum[32];
+    __shared__ int32_t warp_sum[THREADS / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int32_t s = v;
 #pragma unroll
@@ -68,13 +69,13 @@ __device__ __forceinline__ int32_t block_scan(int32_t v, int32_t& all) {
     }
     if (lane == 31) warp_sum[warp] = s;
     __syncthreads();
-    int32_t w = warp_sum[lane];
+    int32_t w = lane < THREADS / 32 ? warp_sum[lane] : 0;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
+    for (int d = 1; d < THREADS / 32; d <<= 1) {
         const int32_t u = __shfl_up_sync(0xffffffffu, w, d);
         if (lane >= d) w += u;
     }
-    all = __shfl_sync(0xffffffffu, w, 31);
+    all = __shfl_sync(0xffffffffu, w, THREADS / 32 - 1);
     const int32_t before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
     return s - v + (warp > 0 ? before : 0);
 }
@@ -100,9 +101,10 @@ __device__ __forceinline__ int32_t scan_warps(uint16_t* counts, int pitch, int w
 // receives, per warp, the slots of each expert in the warps before it; returns
 // the slot's rank in its warp.  `sum` (thread x < experts): the step's slots of
 // expert x.  Ends with the counts visible to the CTA.
+template <int THREADS>
 __device__ __forceinline__ int step_ranks(int e, int experts, int warps, uint16_t* wcount, int32_t& sum) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int x = tid; x < warps * experts; x += kSortThreads) wcount[x] = 0;
+    for (int x = tid; x < warps * experts; x += THREADS) wcount[x] = 0;
     __syncthreads();
     const unsigned same = __match_any_sync(0xffffffffu, e);
     const int rank = __popc(same & ((1u << lane) - 1));
@@ -153,7 +155,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(const SortArgs 
     }
     __syncthreads();
     int32_t all;
-    const int32_t first = block_scan(tid < E ? total[tid] : 0, all);
+    const int32_t first = block_scan<kSortThreads>(tid < E ? total[tid] : 0, all);
     if (tid < E) {
         base[tid] += first;
         if (blockIdx.x == 0) a.offsets[tid] = first;
@@ -164,7 +166,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(const SortArgs 
         const int64_t i = s + tid;
         if (s > lo) e = i < hi ? load_id(a, i) : -1;
         int32_t sum;
-        const int rank = step_ranks(e, E, 32, wcount, sum);
+        const int rank = step_ranks<kSortThreads>(e, E, 32, wcount, sum);
         __syncthreads();
         const int32_t row = e >= 0 ? base[e] + wcount[(tid >> 5) * E + e] + rank : -1;
         __syncthreads();
@@ -193,7 +195,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads)
     pdl_launch_dependents();
     const int e = slot < a.slots ? load_id(a, slot) : -1;
     int32_t sum;
-    const int rank = step_ranks(e, E, 32, wcount, sum);
+    const int rank = step_ranks<kSortThreads>(e, E, 32, wcount, sum);
     if (tid < E) mine[tid] = sum;
     tc::cluster_sync();
     int32_t total = 0, before = 0;
@@ -208,7 +210,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads)
     }
     asm volatile("barrier.cluster.arrive.release;" ::: "memory");      // done with the other CTAs' counts
     int32_t all;
-    const int32_t first = block_scan(total, all);
+    const int32_t first = block_scan<kSortThreads>(total, all);
     if (tid < E) {
         base[tid] = first + before;
         if (blockIdx.x == 0) a.offsets[tid] = first;
@@ -252,23 +254,33 @@ __device__ __forceinline__ void clear_rows(const RowArgs& a, int64_t t, int64_t 
     }
 }
 
-// Copies token t's row to its rows; rows_of(j) is slot j's row.
-template <typename T, int VEC, typename F>
-__device__ __forceinline__ void copy_row(const RowArgs& a, int64_t t, F rows_of, int v0, int step) {
-    constexpr int UN = 4;
-    const T* in = static_cast<const T*>(a.src) + t * a.ld_src;
-    for (int v = v0; v < a.nvec; v += UN * step) {
-        Pack<T, VEC> p[UN];
+// The vectors of a row that a thread copies at a time
+template <typename T, int VEC>
+struct Copied {
+    static constexpr int UN = 4;
+    Pack<T, VEC> p[UN];
+    __device__ __forceinline__ void load(const RowArgs& a, int64_t t, int v, int step) {
+        const T* in = static_cast<const T*>(a.src) + t * a.ld_src;
 #pragma unroll
         for (int u = 0; u < UN; u++)
             if (v + u * step < a.nvec) p[u].load(in + (int64_t)(v + u * step) * VEC);
+    }
+};
+// Copies token t's row to its rows; rows_of(j) is slot j's row.  `loaded`: the
+// first vectors are in `held` already.
+template <typename T, int VEC, typename F>
+__device__ __forceinline__ void copy_row(const RowArgs& a, int64_t t, F rows_of, int v0, int step, Copied<T, VEC>& held,
+                                         bool loaded) {
+    constexpr int UN = Copied<T, VEC>::UN;
+    for (int v = v0; v < a.nvec; v += UN * step, loaded = false) {
+        if (!loaded) held.load(a, t, v, step);
         for (int j = 0; j < a.k; j++) {
             const int32_t r = rows_of(j);
             if (r < 0) continue;
             T* out = static_cast<T*>(a.dst) + r * a.ld_dst;
 #pragma unroll
             for (int u = 0; u < UN; u++)
-                if (v + u * step < a.nvec) p[u].store(out + (int64_t)(v + u * step) * VEC);
+                if (v + u * step < a.nvec) held.p[u].store(out + (int64_t)(v + u * step) * VEC);
         }
     }
 }
@@ -293,24 +305,35 @@ __global__ void __launch_bounds__(kRowThreads) moe_gather_kernel(const RowArgs a
     pdl_wait();
     if (at.t >= a.tokens) return;
     const int32_t* rows = a.slot_row + at.t * a.k;
-    copy_row<T, VEC>(a, at.t, [&](int j) { return rows[j]; }, at.v0, at.step);
+    Copied<T, VEC> held;
+    copy_row<T, VEC>(a, at.t, [&](int j) { return rows[j]; }, at.v0, at.step, held, false);
     clear_rows<T, VEC>(a, at.t, *a.total, at.v0, at.step);
 }
 
-// Sort and gather of at most kSortThreads slots in one launch: every CTA sorts
-// all slots in shared memory (they are few) and moves its own pieces of rows;
-// CTA 0 writes the plan.  With a.src null it only sorts.
-template <typename T, int VEC>
-__global__ void __launch_bounds__(kSortThreads) moe_small_kernel(const SortArgs s, const RowArgs a, int pieces) {
+// Sort and gather of at most THREADS slots over at most THREADS experts in one
+// launch: every CTA sorts all slots in shared memory (they are few) and moves
+// its own pieces of rows; CTA 0 writes the plan.  The first piece of a row is
+// read before the sort, so the two wait for memory together.  With a.src null
+// it only sorts.
+template <typename T, int VEC, int THREADS>
+__global__ void __launch_bounds__(THREADS) moe_small_kernel(const SortArgs s, const RowArgs a, int pieces) {
     extern __shared__ int32_t sm[];
     const int E = s.experts, n = (int)s.slots, tid = threadIdx.x, warps = (n + 31) >> 5;
-    int32_t* row_of = sm;                                        // [kSortThreads]
-    int32_t* base = sm + kSortThreads;                           // [E]
+    int32_t* row_of = sm;                                        // [THREADS]
+    int32_t* base = sm + THREADS;                                // [E]
     uint16_t* wcount = reinterpret_cast<uint16_t*>(base + E);    // [warps][E]
     const int e = tid < n ? load_id(s, tid) : -1;
+    // a piece: 128 threads' share of one token's row
+    const int at = tid & 127, step = pieces * 128;
+    const int64_t all_pieces = a.tokens * pieces, ahead = (int64_t)gridDim.x * (THREADS / 128);
+    int64_t w = (int64_t)blockIdx.x * (THREADS / 128) + (tid >> 7);
+    const auto token = [&] { return w / pieces; };
+    const auto first_vec = [&] { return (int)(w - token() * pieces) * 128 + at; };
+    Copied<T, VEC> held;
+    if (a.src && w < all_pieces) held.load(a, token(), first_vec(), step);
     int32_t sum, all;
-    const int rank = step_ranks(e, E, warps, wcount, sum);
-    const int32_t first = block_scan(sum, all);
+    const int rank = step_ranks<THREADS>(e, E, warps, wcount, sum);
+    const int32_t first = block_scan<THREADS>(sum, all);
     if (tid < E) base[tid] = first;
     __syncthreads();
     const int32_t row = e >= 0 ? base[e] + wcount[(tid >> 5) * E + e] + rank : -1;
@@ -326,14 +349,10 @@ __global__ void __launch_bounds__(kSortThreads) moe_small_kernel(const SortArgs 
     }
     if (!a.src) return;
     __syncthreads();
-    // a piece: 128 threads' share of one token's row
-    const int g = tid >> 7, at = tid & 127;
-    for (int64_t w = (int64_t)blockIdx.x * (kSortThreads / 128) + g; w < a.tokens * pieces;
-         w += (int64_t)gridDim.x * (kSortThreads / 128)) {
-        const int64_t t = w / pieces;
-        const int v0 = (int)(w - t * pieces) * 128 + at, step = pieces * 128;
-        copy_row<T, VEC>(a, t, [&](int j) { return row_of[t * a.k + j]; }, v0, step);
-        clear_rows<T, VEC>(a, t, all, v0, step);
+    for (bool loaded = true; w < all_pieces; w += ahead, loaded = false) {
+        const int64_t t = token();
+        copy_row<T, VEC>(a, t, [&](int j) { return row_of[t * a.k + j]; }, first_vec(), step, held, loaded);
+        clear_rows<T, VEC>(a, t, all, first_vec(), step);
     }
 }
 
@@ -577,27 +596,33 @@ cudaError_t backward_t(const MoePlanArgs& p, const MoeRowsArgs& m, cudaStream_t 
     return m.dweights ? backward_d<T, VEC, true>(p, a, st) : backward_d<T, VEC, false>(p, a, st);
 }
 
-template <typename T, int VEC>
-cudaError_t small_t(const MoePlanArgs& p, const SortArgs& s, const MoeRowsArgs* m, cudaStream_t st) {
+template <typename T, int VEC, int THREADS>
+cudaError_t small_n(const MoePlanArgs& p, const SortArgs& s, const MoeRowsArgs* m, cudaStream_t st) {
     RowArgs a{};
     int pieces = 1;
     int64_t ctas = 1;
     if (m) {
         a = row_args(p, *m, VEC);
         // a token's row in pieces of at least 128 vectors, about as many pieces as there is room for
-        const int64_t room = (int64_t)p.num_sms * (kSortThreads / 128);
+        constexpr int PER = THREADS / 128;
+        const int64_t room = (int64_t)p.num_sms * PER;
         pieces = (int)std::max<int64_t>(1, std::min<int64_t>((a.nvec + 127) / 128, room / p.tokens));
-        ctas = std::min<int64_t>(p.num_sms, (p.tokens * pieces + kSortThreads / 128 - 1) / (kSortThreads / 128));
+        ctas = std::min<int64_t>(p.num_sms, (p.tokens * pieces + PER - 1) / PER);
     }
-    const size_t smem = (kSortThreads + s.experts) * sizeof(int32_t) +
+    const size_t smem = (THREADS + s.experts) * sizeof(int32_t) +
                         (size_t)((s.slots + 31) / 32) * s.experts * sizeof(uint16_t);
     if (smem > 40 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(moe_small_kernel<T, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(moe_small_kernel<T, VEC, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              80 * 1024);
         if (e != cudaSuccess) return e;
     }
-    moe_small_kernel<T, VEC><<<(unsigned)ctas, kSortThreads, smem, st>>>(s, a, pieces);
+    moe_small_kernel<T, VEC, THREADS><<<(unsigned)ctas, THREADS, smem, st>>>(s, a, pieces);
     return cudaGetLastError();
+}
+template <typename T, int VEC>
+cudaError_t small_t(const MoePlanArgs& p, const SortArgs& s, const MoeRowsArgs* m, cudaStream_t st) {
+    constexpr int FEW = 256;           // a smaller CTA starts and synchronizes sooner
+    return s.slots <= FEW && s.experts <= FEW ? small_n<T, VEC, FEW>(p, s, m, st) : small_n<T, VEC, kSortThreads>(p, s, m, st);
 }
 
 // more than kSortThreads slots: the plan by one cluster, or in two launches

@@ -896,29 +896,26 @@ bool even_rows(const NormArgs& a) {
            (!a.dy || rows_vec(a.dy, a.ld_dy, a.cols, e));
 }
 
-// Vectors a lane: few where few rows leave SMs idle (a row's latency counts),
-// else as many as keep a row inside one warp.
-template <typename T, bool EVEN>
-cudaError_t forward_e(const NormArgs& a, cudaStream_t st) {
-    const int64_t n = EVEN ? a.cols / kVec<T> : (a.cols + 2 * kVec<T> - 2) / kVec<T>;
-    if (a.rows <= 2 * a.num_sms) {
-        if (n <= kMaxThreads) return forward<T, 1, EVEN>(a, n, st);
-        if (n <= 2 * kMaxThreads) return forward<T, 2, EVEN>(a, n, st);
-    }
-    if (n <= 4 * 32) return forward<T, 4, EVEN>(a, n, st);
-    // 16 vectors of BF16 fit the registers; of FP32, and with shifted columns, they spill
-    if (n <= 8 * 32 || !EVEN || (sizeof(T) == 4 && n <= 8 * kMaxThreads)) return forward<T, 8, EVEN>(a, n, st);
-    return forward<T, EVEN ? 16 : 8, EVEN>(a, n, st);
-}
 template <typename T>
 cudaError_t forward_t(const NormArgs& a, cudaStream_t st) {
-    const bool even = even_rows(a);
     const int64_t n = a.cols / kVec<T>;
-    if (even && a.rows > 2 * a.num_sms && n <= 4 * kMaxThreads) return stream<T, 4, 2>(a, st);
-    if (even && n <= 16 * kMaxThreads) return forward_e<T, true>(a, st);
-    if (!even && a.cols <= kMaxOddCols) return forward_e<T, false>(a, st);
-    if (even) norm_wide_kernel<T, kVec<T>><<<(unsigned)a.rows, kWide, 0, st>>>(a);
-    else norm_wide_kernel<T, 1><<<(unsigned)a.rows, kWide, 0, st>>>(a);
+    if (even_rows(a)) {
+        // few rows: one or two vectors a thread and one slot ahead, for the latency of a row; many:
+        // as few threads share a row's sums as the registers allow
+        if (a.rows <= a.num_sms && n <= kMaxThreads) return stream<T, 1, 1>(a, st);
+        if (a.rows <= a.num_sms && n <= 2 * kMaxThreads) return stream<T, 2, 1>(a, st);
+        if (n <= 4 * kMaxThreads) return stream<T, 4, 2>(a, st);
+        if (n <= 16 * kMaxThreads) return forward<T, 16, true>(a, n, st);
+        norm_wide_kernel<T, kVec<T>><<<(unsigned)a.rows, kWide, 0, st>>>(a);
+        return cudaGetLastError();
+    }
+    if (a.cols <= kMaxOddCols) {
+        const int64_t odd = (a.cols + 2 * kVec<T> - 2) / kVec<T>;      // vectors, wherever the row starts
+        if (a.rows <= 2 * a.num_sms && odd <= kMaxThreads) return forward<T, 1, false>(a, odd, st);
+        if (a.rows <= 2 * a.num_sms && odd <= 2 * kMaxThreads) return forward<T, 2, false>(a, odd, st);
+        return odd <= 4 * 32 ? forward<T, 4, false>(a, odd, st) : forward<T, 8, false>(a, odd, st);
+    }
+    norm_wide_kernel<T, 1><<<(unsigned)a.rows, kWide, 0, st>>>(a);
     return cudaGetLastError();
 }
 
