@@ -72,8 +72,10 @@ __device__ __forceinline__ void params(float (&f)[VEC], const void* p, int bf16,
 }
 
 // A row's group of `tpr` threads (a power of two below 32, or whole warps) and
-// where its warps' sums meet in shared memory: `part` holds [2][N][16] floats,
-// a group's warps side by side from a multiple of 4, zero where it has none.
+// where its warps' sums meet in shared memory: `part` holds [2][N][kPart]
+// floats, a group's warps side by side from a multiple of 4, zero where it has
+// none.  (At most 16: a CTA is one group of up to 16 warps, or two of 2 warps.)
+constexpr int kPart = 16;
 struct Group {
     int tpr, g, at, slot, base, quads;
     __device__ __forceinline__ Group(int lanes_per_row, float* part, int floats) : tpr(lanes_per_row) {
@@ -98,16 +100,16 @@ __device__ __forceinline__ void group_sum(float (&v)[N], const Group& q, float* 
 #pragma unroll
             for (int i = 0; i < N; i++) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
     if (q.tpr <= 32) return;
-    float* mine = part + turn * N * 16;
+    float* mine = part + turn * N * kPart;
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
-        for (int i = 0; i < N; i++) mine[i * 16 + q.slot] = v[i];
+        for (int i = 0; i < N; i++) mine[i * kPart + q.slot] = v[i];
     asm volatile("bar.sync %0, %1;" :: "r"(q.g + 1), "r"(q.tpr) : "memory");
 #pragma unroll
     for (int i = 0; i < N; i++) {
         v[i] = 0.0f;
         for (int k = 0; k < q.quads; k++) {
-            const float4 t = *reinterpret_cast<const float4*>(mine + i * 16 + q.base + 4 * k);
+            const float4 t = *reinterpret_cast<const float4*>(mine + i * kPart + q.base + 4 * k);
             v[i] += (t.x + t.y) + (t.z + t.w);
         }
     }
@@ -197,8 +199,8 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a, int
     constexpr int VEC = kVec<T>;
     using R = Row<T, NV, EVEN>;
     extern __shared__ float odd_smem[];
-    __shared__ __align__(16) float part[2 * 16];
-    const Group q(tpr, part, 2 * 16);
+    __shared__ __align__(16) float part[2 * kPart];
+    const Group q(tpr, part, 2 * kPart);
     const int groups = blockDim.x / tpr, g = q.g, at = q.at, cols = (int)a.cols;
     const float per_col = 1.0f / (float)cols;
     OddParams<VEC> odd;
@@ -275,8 +277,8 @@ __global__ void __launch_bounds__(kMaxThreads) norm_dx_kernel(const NormArgs a, 
     constexpr int VEC = kVec<T>;
     using R = Row<T, NV, EVEN>;
     extern __shared__ float odd_smem[];
-    __shared__ __align__(16) float part[2 * 2 * 16];
-    const Group q(tpr, part, 2 * 2 * 16);
+    __shared__ __align__(16) float part[2 * 2 * kPart];
+    const Group q(tpr, part, 2 * 2 * kPart);
     const int groups = blockDim.x / tpr, g = q.g, at = q.at, cols = (int)a.cols;
     const float per_col = 1.0f / (float)cols;
     OddParams<VEC> odd;
@@ -396,8 +398,8 @@ template <typename T, int NV, int DEPTH, bool FULL>
 __global__ void __launch_bounds__(kMaxThreads) norm_stream_kernel(const NormArgs a, int tpr) {
     constexpr int VEC = kVec<T>, H = VEC / 2;
     extern __shared__ uint4 ring_smem[];
-    __shared__ __align__(16) float part[2 * 16];
-    const Group q(tpr, part, 2 * 16);
+    __shared__ __align__(16) float part[2 * kPart];
+    const Group q(tpr, part, 2 * kPart);
     const int groups = blockDim.x / tpr, at = q.at, nvec = (int)(a.cols / VEC);
     const float per_col = 1.0f / (float)a.cols;
     const int64_t step = (int64_t)gridDim.x * groups;
@@ -479,8 +481,8 @@ template <typename T, int NV, int DEPTH, bool COLS, bool FULL>
 __global__ void __launch_bounds__(kMaxThreads) norm_backward_kernel(const NormArgs a, int tpr) {
     constexpr int VEC = kVec<T>, H = VEC / 2;
     extern __shared__ uint4 ring_smem[];           // the ring; then the sums' meeting
-    __shared__ __align__(16) float part[2 * 2 * 16];
-    const Group q(tpr, part, 2 * 2 * 16);
+    __shared__ __align__(16) float part[2 * 2 * kPart];
+    const Group q(tpr, part, 2 * 2 * kPart);
     const int groups = blockDim.x / tpr, g = q.g, at = q.at, nvec = (int)(a.cols / VEC);
     const float per_col = 1.0f / (float)a.cols;
     const int64_t step = (int64_t)gridDim.x * groups, last = a.rows - 1;
@@ -644,9 +646,9 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* ws, int 
 
 // ------------------------------------------------------------------ wide rows
 __device__ __forceinline__ float2 block_sum(float2 v) {
-    __shared__ __align__(16) float part[2 * 2 * 16];
+    __shared__ __align__(16) float part[2 * 2 * kPart];
     __syncthreads();
-    const Group q(kWide, part, 2 * 2 * 16);
+    const Group q(kWide, part, 2 * 2 * kPart);
     float s[2] = {v.x, v.y};
     group_sum(s, q, part, 0);
     return make_float2(s[0], s[1]);
@@ -934,8 +936,8 @@ cudaError_t backward_t(const NormArgs& a, cudaStream_t st) {
     if (even) {
         if (n <= kMaxThreads && a.rows <= 2 * a.num_sms) return backward<T, 1, 2>(a, st);
         // 16 columns a thread: more would not leave room for their sums
-        constexpr int NV = 16 / VEC, DEPTH = sizeof(T) == 2 ? 3 : 2;
-        if (n <= NV * kMaxThreads) return backward<T, NV, DEPTH>(a, st);
+        constexpr int NV = 16 / VEC;
+        if (n <= NV * kMaxThreads) return backward<T, NV, 2>(a, st);
     }
     // the column sums first: dx may be written over dy
     if (a.dweight || a.dbias) {
