@@ -47,6 +47,11 @@ constexpr float kNegInf = -INFINITY;
 constexpr float kLog2e = 1.44269504088896340736f;
 
 enum { kStats, kGrad, kDh, kDw, kFewStats, kFewGrad };
+// When a product waits for the kernel before it on the stream: that kernel is done
+// when it is launched; before it reads or writes anything (its set-up runs
+// earlier); before its epilogue (only the epilogue needs that kernel); at its end
+// (it needs nothing of that kernel, and runs beside it).
+enum { kWaitLaunch, kWaitStart, kWaitEpilogue, kWaitEnd };
 
 // ------------------------------------------------------------ the products
 constexpr int kTile = 256;                          // output rows and columns of a pair
@@ -85,7 +90,7 @@ struct GemmParams {
     int32_t tile_m;                // rows of a pair: 256, or fewer (few tokens) for balance
     int32_t stages, b_bytes;       // few tokens: stages, and one CTA's bytes of B per stage
     uint32_t tx;                   // bytes one CTA loads per stage
-    int32_t wait_end;              // a programmatic dependent that needs nothing of the kernel before it
+    int32_t wait;                  // kWait...: when it waits for the kernel before it
     const int64_t* targets;
     int64_t vocab;
     int64_t col0;                  // first vocabulary column of the piece
@@ -95,8 +100,10 @@ struct GemmParams {
     int64_t ld_g;
     const float* lse;
     const float* dloss;
-    const float* smax;
+    float* smax;
+    int32_t put_smax;              // kFewGrad: leave max |dloss| there
     int32_t add;                   // kDh: add to what is there
+    int32_t direct;                // kDh: the only piece and split, so dh itself leaves
     unsigned* status;
     uint64_t timeout_ns;
 };
@@ -119,6 +126,27 @@ __host__ __device__ constexpr uint32_t idesc_bf16(bool amn, bool bmn) {
 __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr) {
     return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(8192 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// N reductions over the warp at once: lane l has that of v[l N / 32].  Each step
+// sends the half of the values that the other lane keeps.
+template <int N, typename Op>
+__device__ __forceinline__ float warp_each(float (&v)[N], Op op) {
+    int n = N;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+        if (n > 1) {
+            n >>= 1;
+            const bool upper = threadIdx.x & d;
+#pragma unroll
+            for (int i = 0; i < n; i++) {
+                const float keep = upper ? v[i + n] : v[i], send = upper ? v[i] : v[i + n];
+                v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, d));
+            }
+        } else {
+            v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], d));
+        }
+    }
+    return v[0];
 }
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
@@ -242,6 +270,40 @@ __device__ __noinline__ void drain_loads(uint32_t full0, int stages, int n_own, 
     }
 }
 
+// max |dloss| over the tokens that count, of this warp's lanes' tokens lane, lane + step, ...
+__device__ __forceinline__ float largest_dloss(const float* dloss, const int64_t* targets, int64_t T, int64_t V, int64_t first,
+                                               int step) {
+    float m = 0.0f;
+#pragma unroll 4
+    for (int64_t t = first; t < T; t += step) {
+        const int64_t id = targets[t];
+        const float d = fabsf(dloss[t]);
+        if (id >= 0 && id < V) m = fmaxf(m, d);
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    return m;
+}
+
+// The tokens' table of the few-token kernels, filled by the epilogue's warps
+template <int MODE>
+__device__ __forceinline__ void few_tokens(const GemmParams& p, float* lse, float* ratio, int64_t* target) {
+    const int t = threadIdx.x - 64;
+    float smax = 0.0f;
+    if (MODE == kFewGrad) {
+        smax = largest_dloss(p.dloss, p.targets, p.N, p.vocab, t & 31, 32);
+        if (p.put_smax && blockIdx.x == 0 && t == 0) *p.smax = smax;
+    }
+    if (t < kFewTokens) {
+        const int64_t id = t < p.N ? p.targets[t] : -1;
+        const bool counts = id >= 0 && id < p.vocab;
+        target[t] = counts ? id - p.col0 : -1;
+        lse[t] = MODE == kFewGrad && counts ? p.lse[t] : 0.0f;
+        ratio[t] = MODE == kFewGrad && counts && smax > 0.0f ? p.dloss[t] / smax : 0.0f;
+    }
+    asm volatile("bar.sync 1, %0;" :: "n"(32 * kEpiWarps) : "memory");
+}
+
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -265,8 +327,9 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     volatile int* issued_slot = reinterpret_cast<volatile int*>(tmem_slot + 2);
     static_assert(8 * (2 * kMaxStages + 5) + 12 <= 256, "barrier area");
 
-    // a kernel that may run beside this one starts as soon as SMs are free
-    pdl_launch_dependents();
+    // a kernel that may run beside this one starts as soon as SMs are free, but not before what
+    // this one waits for is done
+    if (p.wait != kWaitStart) pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_rank();
     const bool leader = rank == 0;
@@ -292,23 +355,6 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     float* few_lse = reinterpret_cast<float*>(smOut);
     float* few_ratio = few_lse + kFewTokens;
     int64_t* few_target = reinterpret_cast<int64_t*>(few_ratio + kFewTokens);
-    if (FEW) {
-        // rows of A that no load fills (tile_m below 256) are read by the MMAs all the same
-        const int rows = p.tile_m / 2;
-        for (int i = threadIdx.x; i < S * kSub * (128 - rows) * 8; i += kGemmThreads) {
-            const int block = i / ((128 - rows) * 8), at = i - block * ((128 - rows) * 8);
-            reinterpret_cast<uint4*>(smA + block * kSubBytes + rows * 128)[at] = make_uint4(0, 0, 0, 0);
-        }
-        tc::fence_async_smem();
-        for (int t = threadIdx.x; t < kFewTokens; t += kGemmThreads) {
-            const int64_t id = t < p.N ? p.targets[t] : -1;
-            const bool counts = id >= 0 && id < p.vocab;
-            few_target[t] = counts ? id - p.col0 : -1;
-            const float smax = MODE == kFewGrad ? *p.smax : 0.0f;
-            few_lse[t] = MODE == kFewGrad && counts ? p.lse[t] : 0.0f;
-            few_ratio[t] = MODE == kFewGrad && counts && smax > 0.0f ? p.dloss[t] / smax : 0.0f;
-        }
-    }
     tc::fence_before();
     __syncthreads();
     tc::cluster_sync();
@@ -322,6 +368,10 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             int stage = 0, issued = 0;
             uint32_t phase = 0;
             bool ok = true;
+            if (p.wait == kWaitStart) {
+                pdl_wait();
+                pdl_launch_dependents();
+            }
             for (int t = cid; t < p.total && ok; t += ncl) {
                 const TileAt ti = tile_at(p, t);
                 const int am = ti.mt * p.tile_m + (int)rank * (p.tile_m / 2), bn = ti.nt * p.tile_n + (int)rank * (p.tile_n / 2);
@@ -368,6 +418,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             int stage = 0, iter = 0;
             uint32_t phase = 0;
             bool ok = true, any = false, ready = false;
+            if (p.wait == kWaitStart) pdl_wait();          // the limit of its waits counts from there
             for (int t = cid; t < p.total && ok; t += ncl) {
                 const TileAt ti = tile_at(p, t);
                 for (int c0 = ti.k0; c0 < ti.k1 && ok; c0 += p.chunk, ++iter) {
@@ -423,10 +474,13 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         const int q = warp & 3, half = (warp - 2) >> 2;
         const uint32_t tempty_c0 = tc::mapa(tempty0, 0);
         const uint32_t stage_buf = tc::smem_u32(smOut + (warp - 2) * kStage);
-        const float smax = MODE == kGrad || MODE == kDw ? *p.smax : 1.0f;
+        if (p.wait == kWaitStart || p.wait == kWaitEpilogue) pdl_wait();
+        const float smax = MODE == kGrad || MODE == kDw || MODE == kDh ? __ldcg(p.smax) : 1.0f;
         int iter = 0, n = 0;
         if (FEW) {
-            // A thread owns one row of w and the tokens 64 half ... 64 half + 63.
+            few_tokens<MODE>(p, few_lse, few_ratio, few_target);
+            // A thread owns one row of w (rows past the tile's are whatever shared memory held: they
+            // stay in their rows) and the tokens 64 half ... 64 half + 63.
             for (int t = cid; t < p.total; t += ncl) {
                 const int mt = tile_at(p, t).mt;
                 const int64_t row = (int64_t)mt * p.tile_m + rank * (p.tile_m / 2) + q * 32 + lane;     // of the piece
@@ -449,36 +503,37 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     if (lane == 0) tc::mbar_arrive_cluster(tempty_c0 + 8 * buf);
                 }
                 if (!ok) break;
-                float mine_m[2] = {kNegInf, kNegInf}, mine_s[2] = {0.0f, 0.0f};
 #pragma unroll
-                for (int j = 0; j < 64; j++) {
-                    if (j >= tokens) continue;
-                    const int token = 64 * half + j;
-                    const bool hit = in && row == few_target[token];
+                for (int c = 0; c < 64; c += 16) {
+                    if (c >= tokens) continue;
+                    const int token0 = 64 * half + c;
                     if (MODE == kFewStats) {
-                        if (hit) p.hit[token] = z[j];
-                        const float x = in ? z[j] : kNegInf;
-                        float m = x;
+                        float m[16], e[16];
 #pragma unroll
-                        for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-                        float e = exp2_fast((x - (m == kNegInf ? 0.0f : m)) * kLog2e);
-#pragma unroll
-                        for (int d = 16; d; d >>= 1) e += __shfl_xor_sync(0xffffffffu, e, d);
-                        if (lane == (j & 31)) {
-                            mine_m[j >> 5] = m;
-                            mine_s[j >> 5] = e;
+                        for (int j = 0; j < 16; j++) {
+                            if (in && row == few_target[token0 + j]) p.hit[token0 + j] = z[c + j];
+                            m[j] = e[j] = in ? z[c + j] : kNegInf;
                         }
+                        const float most = warp_each(m, [](float a, float b) { return fmaxf(a, b); });
+#pragma unroll
+                        for (int j = 0; j < 16; j++) {
+                            const float mj = __shfl_sync(0xffffffffu, most, 2 * j);
+                            e[j] = exp2_fast((e[j] - (mj == kNegInf ? 0.0f : mj)) * kLog2e);
+                        }
+                        const float sum = warp_each(e, [](float a, float b) { return a + b; });
+                        if ((lane & 1) == 0 && c + (lane >> 1) < tokens)
+                            p.part[part * p.N + token0 + (lane >> 1)] = make_float2(most, sum);
                     } else if (in) {
-                        const float ratio = few_ratio[token];
-                        const float g = exp2_fast((z[j] - few_lse[token]) * kLog2e) - (hit ? 1.0f : 0.0f);
-                        p.g[(int64_t)token * p.ld_g + row] = __float2bfloat16_rn(ratio == 0.0f ? 0.0f : g * ratio);
+#pragma unroll
+                        for (int j = 0; j < 16; j++) {
+                            const int token = token0 + j;
+                            const float ratio = few_ratio[token];
+                            const float g = exp2_fast((z[c + j] - few_lse[token]) * kLog2e) - (row == few_target[token] ? 1.0f : 0.0f);
+                            if (c + j < tokens)
+                                p.g[(int64_t)token * p.ld_g + row] = __float2bfloat16_rn(ratio == 0.0f ? 0.0f : g * ratio);
+                        }
                     }
                 }
-                if (MODE == kFewStats)
-#pragma unroll
-                    for (int j = 0; j < 2; j++)
-                        if (32 * j + lane < tokens)
-                            p.part[part * p.N + 64 * half + 32 * j + lane] = make_float2(mine_m[j], mine_s[j]);
             }
         } else
         for (int t = cid; t < p.total; t += ncl) {
@@ -550,7 +605,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 for (int c = 0; c < 128; c += 32) {
                     load_acc(v, ta + c);
                     const int col = (int)col0 + c;
-                    if (MODE == kDh) {
+                    if (MODE == kDh && !p.direct) {
                         store_acc(v, stage_buf, &tmOut, col, (int)row0, ti.split, p.add != 0, n, lane);
                         continue;
                     }
@@ -572,7 +627,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     }
 
     // what was launched before this kernel is done when this kernel is
-    if (p.wait_end) pdl_wait();
+    if (p.wait == kWaitEnd) pdl_wait();
     // Both CTAs have stopped issuing; if either gave up, the even CTA waits
     // (bounded) for the loads still in flight before either may exit.
     tc::fence_before();
@@ -668,11 +723,9 @@ int stream_rows(int64_t vocab, int num_sms) {
     }
     return best;
 }
-// `beside`: launched so that it may run while the kernel before it on the
-// stream still does (of which it needs nothing); it ends after that kernel.
 template <int MODE>
 cudaError_t gemm(GemmParams p, const Operand& a, const Operand& b, const CUtensorMap* out, int64_t K, int splits,
-                 int tile_m, int tile_n, bool beside, const HeadArgs& args, cudaStream_t st) {
+                 int tile_m, int tile_n, int wait, const HeadArgs& args, cudaStream_t st) {
     CUtensorMap ta, tb;
     if (!map_operand(&ta, a.p, a.rows, a.cols, a.ld, a_mn(MODE) ? kSubK : tile_m / 2) ||
         !map_operand(&tb, b.p, b.rows, b.cols, b.ld, b_mn(MODE) ? kSubK : tile_n / 2))
@@ -692,7 +745,7 @@ cudaError_t gemm(GemmParams p, const Operand& a, const Operand& b, const CUtenso
     const int64_t total = (int64_t)p.m_tiles * p.n_tiles * p.splits;
     if (total > 0x7FFFFFFF) return cudaErrorInvalidValue;
     p.total = (int32_t)total;
-    p.wait_end = beside;
+    p.wait = wait;
     p.status = args.status;
     p.timeout_ns = args.timeout_ns;
     static bool attr_done = false;
@@ -703,7 +756,7 @@ cudaError_t gemm(GemmParams p, const Operand& a, const Operand& b, const CUtenso
     }
     const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(args.num_sms / 2, total));
     choose_raster(p, K, pairs);
-    return launch_k(beside, head_gemm_kernel<MODE>, dim3(2 * pairs), kGemmThreads, kSmem, st, ta, tb, out ? *out : ta, p);
+    return launch_k(wait != kWaitLaunch, head_gemm_kernel<MODE>, dim3(2 * pairs), kGemmThreads, kSmem, st, ta, tb, out ? *out : ta, p);
 }
 
 // ------------------------------------------------------- around the products
@@ -747,11 +800,8 @@ __global__ void __launch_bounds__(512) head_join_kernel(const float2* part, int6
 __global__ void __launch_bounds__(1024) head_scale_kernel(const float* dloss, const int64_t* targets, int64_t T, int64_t V,
                                                           float* smax) {
     __shared__ float part[32];
-    float m = 0.0f;
-    for (int64_t t = threadIdx.x; t < T; t += 1024)
-        if (targets[t] >= 0 && targets[t] < V) m = fmaxf(m, fabsf(dloss[t]));
-#pragma unroll
-    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    pdl_launch_dependents();
+    float m = largest_dloss(dloss, targets, T, V, threadIdx.x, 1024);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -765,6 +815,7 @@ __global__ void __launch_bounds__(256) head_dh_kernel(const float* acc, int spli
                                                       const float* smax, __nv_bfloat16* dh, int64_t ld) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, per = D / 8;
     if (i >= T * per) return;
+    pdl_wait();
     const int64_t t = i / per, c = (i - t * per) * 8;
     float v[8] = {};
     for (int s = 0; s < splits; s++) {
@@ -797,6 +848,9 @@ int dh_splits(int64_t tokens, int64_t cols, int64_t piece, int num_sms) {
     return (int)std::max<int64_t>(1, std::min<int64_t>(num_sms / 2 / tiles, stages / 8));
 }
 
+// dh comes out of one product as it is
+bool dh_direct(int splits, int64_t piece, int64_t vocab) { return splits == 1 && piece >= vocab; }
+
 // parts of a row's statistics
 int64_t head_parts(int64_t tokens, int64_t vocab, int num_sms) {
     if (tokens <= kFewTokens) {
@@ -811,8 +865,9 @@ int64_t head_parts(int64_t tokens, int64_t vocab, int num_sms) {
 size_t head_workspace(int64_t tokens, int64_t vocab, int64_t cols, bool backward, int num_sms) {
     if (!backward) return (size_t)(head_parts(tokens, vocab, num_sms) * tokens * 8 + round_up(tokens * 4, 16));
     const int64_t piece = piece_cols(tokens, vocab);
+    const int splits = dh_splits(tokens, cols, piece, num_sms);
     return (size_t)(256 + (piece < vocab ? 2 : 1) * tokens * piece * 2 +
-                    dh_splits(tokens, cols, piece, num_sms) * tokens * cols * 4);
+                    (dh_direct(splits, piece, vocab) ? 0 : splits * tokens * cols * 4));
 }
 
 cudaError_t run_head(const HeadArgs& a, cudaStream_t st) {
@@ -828,9 +883,9 @@ cudaError_t run_head(const HeadArgs& a, cudaStream_t st) {
     cudaError_t e;
     if (T <= kFewTokens) {
         std::swap(p.M, p.N);
-        e = gemm<kFewStats>(p, w, h, nullptr, a.cols, 1, stream_rows(a.vocab, a.num_sms), (int)round_up(T, 16), false, a, st);
+        e = gemm<kFewStats>(p, w, h, nullptr, a.cols, 1, stream_rows(a.vocab, a.num_sms), (int)round_up(T, 16), kWaitLaunch, a, st);
     } else {
-        e = gemm<kStats>(p, h, w, nullptr, a.cols, 1, kTile, kTile, false, a, st);
+        e = gemm<kStats>(p, h, w, nullptr, a.cols, 1, kTile, kTile, kWaitLaunch, a, st);
     }
     if (e != cudaSuccess) return e;
     // tokens a CTA: few where there are few, so that more threads share a token's parts
@@ -843,17 +898,23 @@ cudaError_t run_head(const HeadArgs& a, cudaStream_t st) {
 // Per piece: g, then dh and dw from it.  dw runs beside dh's last tiles, and
 // the next piece's g (in the other of two buffers) beside dw's: each kernel is
 // launched while the one before it drains, so that no SM waits for the end of
-// a wave.  dh starts only when everything before it is done: it needs g, and
-// its accumulator takes the pieces in order.
+// a wave.  dh waits until everything before it is done: it needs g, and its
+// accumulator takes the pieces in order; dw and the next g start after dh has
+// waited.  max |dloss| is needed by the first g's epilogue only; few tokens
+// find it themselves.
 cudaError_t run_head_backward(const HeadArgs& a, cudaStream_t st) {
     const int64_t T = a.tokens, V = a.vocab, D = a.cols, piece = piece_cols(T, V);
     const int splits = dh_splits(T, D, piece, a.num_sms);
+    const bool few = T <= kFewTokens, direct = dh_direct(splits, piece, V);
     uint8_t* ws = static_cast<uint8_t*>(a.ws);
     float* smax = reinterpret_cast<float*>(ws);
     uint8_t* g0 = ws + 256;
     float* acc = reinterpret_cast<float*>(g0 + (piece < V ? 2 : 1) * T * piece * 2);
-    head_scale_kernel<<<1, 1024, 0, st>>>(a.dloss, a.targets, T, V, smax);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = cudaSuccess;
+    if (!few) {
+        head_scale_kernel<<<1, 1024, 0, st>>>(a.dloss, a.targets, T, V, smax);
+        e = cudaGetLastError();
+    }
     int used = 1;
     for (int64_t v0 = 0, i = 0; v0 < V && e == cudaSuccess; v0 += piece, i++) {
         const int64_t n = std::min(piece, V - v0);
@@ -866,28 +927,31 @@ cudaError_t run_head_backward(const HeadArgs& a, cudaStream_t st) {
         p.lse = a.lse;
         p.dloss = a.dloss;
         p.smax = smax;
+        p.put_smax = i == 0;
         p.M = T;
         p.N = n;
         CUtensorMap out;
         const Operand h{a.h, T, D, a.ldh}, wp{w, n, D, a.ldw}, gp{g, T, n, piece};
         // without dw in between, the kernel before may be the dh of the piece that this buffer held
-        const bool beside = i > 0 && a.dh && a.dw;
-        if (T <= kFewTokens) {
+        const int wait = i == 0 ? (few ? kWaitLaunch : kWaitEpilogue) : a.dh && a.dw ? kWaitEnd : kWaitStart;
+        if (few) {
             p.M = n;
             p.N = T;
             p.g = reinterpret_cast<__nv_bfloat16*>(g);
             p.ld_g = piece;
-            e = gemm<kFewGrad>(p, wp, h, nullptr, D, 1, stream_rows(n, a.num_sms), (int)round_up(T, 16), beside, a, st);
+            e = gemm<kFewGrad>(p, wp, h, nullptr, D, 1, stream_rows(n, a.num_sms), (int)round_up(T, 16), wait, a, st);
         } else {
             if (!tmap::out_2d(&out, g, T, n, piece, true)) return cudaErrorInvalidValue;
-            e = gemm<kGrad>(p, h, wp, &out, D, 1, kTile, kTile, beside, a, st);
+            e = gemm<kGrad>(p, h, wp, &out, D, 1, kTile, kTile, wait, a, st);
         }
         if (e == cudaSuccess && a.dh) {
             p.M = T;
             p.N = D;
             p.add = v0 > 0;
-            if (!map_acc(&out, acc, splits, T, D)) return cudaErrorInvalidValue;
-            e = gemm<kDh>(p, gp, wp, &out, n, splits, kTile, kTile, false, a, st);
+            p.direct = direct;
+            if (!(direct ? tmap::out_2d(&out, a.dh, T, D, a.ld_dh, true) : map_acc(&out, acc, splits, T, D)))
+                return cudaErrorInvalidValue;
+            e = gemm<kDh>(p, gp, wp, &out, n, splits, kTile, kTile, kWaitStart, a, st);
             const int stages = (int)((n + kSub * kSubK - 1) / (kSub * kSubK)), per = (stages + splits - 1) / splits;
             if (v0 == 0) used = (stages + per - 1) / per;          // the splits that the first piece wrote
         }
@@ -896,14 +960,12 @@ cudaError_t run_head_backward(const HeadArgs& a, cudaStream_t st) {
             p.N = D;
             if (!tmap::out_2d(&out, static_cast<uint8_t*>(a.dw) + v0 * a.ld_dw * 2, n, D, a.ld_dw, true))
                 return cudaErrorInvalidValue;
-            e = gemm<kDw>(p, gp, h, &out, T, 1, kTile, kTile, a.dh != nullptr, a, st);
+            e = gemm<kDw>(p, gp, h, &out, T, 1, kTile, kTile, a.dh ? kWaitEnd : kWaitStart, a, st);
         }
     }
-    if (e == cudaSuccess && a.dh) {
-        head_dh_kernel<<<(unsigned)((T * (D / 8) + 255) / 256), 256, 0, st>>>(acc, used, T, D, smax,
-                                                                              static_cast<__nv_bfloat16*>(a.dh), a.ld_dh);
-        e = cudaGetLastError();
-    }
+    if (e == cudaSuccess && a.dh && !direct)
+        e = launch_k(true, head_dh_kernel, dim3((unsigned)((T * (D / 8) + 255) / 256)), 256, 0, st, acc, used, T, D, smax,
+                     static_cast<__nv_bfloat16*>(a.dh), a.ld_dh);
     return e;
 }
 
