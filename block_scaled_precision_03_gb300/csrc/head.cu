@@ -60,6 +60,8 @@ constexpr int kSub = 2;                             // sub-steps per stage
 constexpr int kStages = 3;
 constexpr int kMaxStages = 6;                       // few tokens: as many as fit
 constexpr int kFewTokens = 128;
+constexpr int kFewTable = kFewTokens * 12;          // their lse, ratio and target
+constexpr int kFewOut = kFewTable + 8 * 2048;       // and 32 rows by 16 tokens for each warp of the epilogue
 // Stages (K = 512) that one accumulator sums for the loss.  Against 64 bits, 1024
 // x 20000 x 4096: 3.2e-7 (2 stages 1.6e-7, 8 6.7e-7; a plain FP32 product
 // 6.8e-7); the batch takes 2.46 ms with 4 or 8, 2.59 with 2.
@@ -127,26 +129,8 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr) {
     return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(8192 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
-// N reductions over the warp at once: lane l has that of v[l N / 32].  Each step
-// sends the half of the values that the other lane keeps.
-template <int N, typename Op>
-__device__ __forceinline__ float warp_each(float (&v)[N], Op op) {
-    int n = N;
-#pragma unroll
-    for (int d = 16; d; d >>= 1) {
-        if (n > 1) {
-            n >>= 1;
-            const bool upper = threadIdx.x & d;
-#pragma unroll
-            for (int i = 0; i < n; i++) {
-                const float keep = upper ? v[i + n] : v[i], send = upper ? v[i] : v[i + n];
-                v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, d));
-            }
-        } else {
-            v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], d));
-        }
-    }
-    return v[0];
+__device__ __forceinline__ void st_cluster(uint32_t addr, int v) {
+    asm volatile("st.shared::cluster.s32 [%0], %1;" :: "r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
@@ -234,6 +218,16 @@ __device__ __forceinline__ void load_acc(float (&v)[32], uint32_t taddr) {
     for (int j = 0; j < 32; j++) v[j] = __uint_as_float(r[j]);
 }
 
+// A bounded wait that polls for a while (some 2000 cycles) before it suspends the
+// thread: waking up again costs more than most of these waits last.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* status,
+                                     uint64_t limit_ns) {
+#pragma unroll 1
+    for (int i = 0; i < 64; i++)
+        if (tc::mbar_test(bar, parity)) return true;
+    return tc::mbar_wait_slow(bar, parity, abort_flag, status, limit_ns);
+}
+
 struct TileAt {
     int mt, nt, split, k0, k1;
 };
@@ -287,7 +281,7 @@ __device__ __forceinline__ float largest_dloss(const float* dloss, const int64_t
 
 // The tokens' table of the few-token kernels, filled by the epilogue's warps
 template <int MODE>
-__device__ __forceinline__ void few_tokens(const GemmParams& p, float* lse, float* ratio, int64_t* target) {
+__device__ __forceinline__ void few_tokens(const GemmParams& p, float* lse, float* ratio, int* target) {
     const int t = threadIdx.x - 64;
     float smax = 0.0f;
     if (MODE == kFewGrad) {
@@ -297,7 +291,7 @@ __device__ __forceinline__ void few_tokens(const GemmParams& p, float* lse, floa
     if (t < kFewTokens) {
         const int64_t id = t < p.N ? p.targets[t] : -1;
         const bool counts = id >= 0 && id < p.vocab;
-        target[t] = counts ? id - p.col0 : -1;
+        target[t] = counts && id >= p.col0 && id - p.col0 < p.M ? (int)(id - p.col0) : -1;
         lse[t] = MODE == kFewGrad && counts ? p.lse[t] : 0.0f;
         ratio[t] = MODE == kFewGrad && counts && smax > 0.0f ? p.dloss[t] / smax : 0.0f;
     }
@@ -310,8 +304,8 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                  const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ GemmParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    // [stages] of A, [stages] of B, then the epilogue's staging (few tokens: the
-    // tokens' lse, ratio and target); the barriers come last
+    // [stages] of A, [stages] of B, then the epilogue's staging (few tokens: their
+    // table, then the warps' turned rows); the barriers come last
     constexpr bool FEW = is_few(MODE);
     const int S = FEW ? p.stages : kStages, b_bytes = FEW ? p.b_bytes : kOpBytes, sub_b = b_bytes / kSub;
     uint8_t* smA = base;
@@ -325,7 +319,8 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 5);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     volatile int* issued_slot = reinterpret_cast<volatile int*>(tmem_slot + 2);
-    static_assert(8 * (2 * kMaxStages + 5) + 12 <= 256, "barrier area");
+    volatile int* peer_abort = reinterpret_cast<volatile int*>(tmem_slot + 3);
+    static_assert(8 * (2 * kMaxStages + 5) + 16 <= 256, "barrier area");
 
     // a kernel that may run beside this one starts as soon as SMs are free, but not before what
     // this one waits for is done
@@ -347,6 +342,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         tc::mbar_init(drain, 1);
         *abort_flag = 0;
         *issued_slot = 0;
+        *peer_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         tc::prefetch_tmap(&tmA);
         tc::prefetch_tmap(&tmB);
@@ -354,7 +350,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     if (warp == 1) tc::tmem_alloc<2>(tc::smem_u32(tmem_slot), kTmemCols);
     float* few_lse = reinterpret_cast<float*>(smOut);
     float* few_ratio = few_lse + kFewTokens;
-    int64_t* few_target = reinterpret_cast<int64_t*>(few_ratio + kFewTokens);
+    int* few_target = reinterpret_cast<int*>(few_ratio + kFewTokens);
     tc::fence_before();
     __syncthreads();
     tc::cluster_sync();
@@ -376,7 +372,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 const TileAt ti = tile_at(p, t);
                 const int am = ti.mt * p.tile_m + (int)rank * (p.tile_m / 2), bn = ti.nt * p.tile_n + (int)rank * (p.tile_n / 2);
                 for (int kb = ti.k0; kb < ti.k1; kb++) {
-                    if (!tc::mbar_wait(empty0 + 8 * stage, phase ^ 1, abort_flag, p.status, p.timeout_ns)) {
+                    if (!wait(empty0 + 8 * stage, phase ^ 1, abort_flag, p.status, p.timeout_ns)) {
                         ok = false;
                         break;
                     }
@@ -423,13 +419,13 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 const TileAt ti = tile_at(p, t);
                 for (int c0 = ti.k0; c0 < ti.k1 && ok; c0 += p.chunk, ++iter) {
                     const int c1 = min(ti.k1, c0 + p.chunk), buf = iter & 1;
-                    if (!tc::mbar_wait(tempty0 + 8 * buf, ((iter >> 1) & 1) ^ 1, abort_flag, p.status, p.timeout_ns)) {
+                    if (!wait(tempty0 + 8 * buf, ((iter >> 1) & 1) ^ 1, abort_flag, p.status, p.timeout_ns)) {
                         ok = false;
                         break;
                     }
                     const uint32_t d = tmem + (uint32_t)buf * kTile;
                     for (int kb = c0; kb < c1; kb++) {
-                        if (!ready && !tc::mbar_wait(full0 + 8 * stage, phase, abort_flag, p.status, p.timeout_ns)) {
+                        if (!ready && !wait(full0 + 8 * stage, phase, abort_flag, p.status, p.timeout_ns)) {
                             ok = false;
                             break;
                         }
@@ -480,21 +476,23 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         if (FEW) {
             few_tokens<MODE>(p, few_lse, few_ratio, few_target);
             // A thread owns one row of w (rows past the tile's are whatever shared memory held: they
-            // stay in their rows) and the tokens 64 half ... 64 half + 63.
+            // stay in their rows) and half of the tokens, in sixteens.
+            const int share = ((int)p.N + 31) / 32 * 16, own = half * share;
+            float* turned = reinterpret_cast<float*>(smOut + kFewTable) + (warp - 2) * 512;
             for (int t = cid; t < p.total; t += ncl) {
                 const int mt = tile_at(p, t).mt;
-                const int64_t row = (int64_t)mt * p.tile_m + rank * (p.tile_m / 2) + q * 32 + lane;     // of the piece
+                const int row = mt * p.tile_m + (int)rank * (p.tile_m / 2) + q * 32 + lane;     // of the piece
                 const bool in = q * 32 + lane < p.tile_m / 2 && row < p.M;
                 const int64_t part = ((int64_t)mt * 2 + rank) * 4 + q;
-                const int tokens = (int)p.N - 64 * half;       // of this warp, at most 64
+                const int tokens = min(share, (int)p.N - own);         // of this warp, at most 64; 0 or less: none
                 float z[64] = {};
                 bool ok = true;
                 for (int c0 = 0; c0 < p.k_stages && ok; c0 += p.chunk, ++iter) {
                     const int buf = iter & 1;
-                    ok = tc::mbar_wait(tfull0 + 8 * buf, (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns);
+                    ok = wait(tfull0 + 8 * buf, (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns);
                     if (!ok) break;
                     tc::fence_after();
-                    const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kTile + 64 * half);
+                    const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kTile + own);
 #pragma unroll
                     for (int c = 0; c < 64; c += 16)
                         if (c < tokens) add_acc(z + c, ta + c);
@@ -503,36 +501,56 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     if (lane == 0) tc::mbar_arrive_cluster(tempty_c0 + 8 * buf);
                 }
                 if (!ok) break;
-#pragma unroll
-                for (int c = 0; c < 64; c += 16) {
-                    if (c >= tokens) continue;
-                    const int token0 = 64 * half + c;
+                // sixteen tokens at a time; the loop stays one, and z moves on: this code is mostly run
+                // once per call, and fetching it four times over took longer than running it
+#pragma unroll 1
+                for (int c = 0; c < tokens; c += 16) {
+                    const int token0 = own + c;
                     if (MODE == kFewStats) {
-                        float m[16], e[16];
+                        // the 32 rows by 16 tokens turn in shared memory: two lanes a token, 16 rows each.  (Sums
+                        // across the lanes took three times the instructions, and with one or two warps a
+                        // scheduler an instruction costs its latency.)
+                        __syncwarp();
 #pragma unroll
-                        for (int j = 0; j < 16; j++) {
-                            if (in && row == few_target[token0 + j]) p.hit[token0 + j] = z[c + j];
-                            m[j] = e[j] = in ? z[c + j] : kNegInf;
-                        }
-                        const float most = warp_each(m, [](float a, float b) { return fmaxf(a, b); });
+                        for (int j = 0; j < 16; j++) turned[32 * j + lane] = in ? z[j] : kNegInf;
+                        __syncwarp();
+                        const int j = lane >> 1;
+                        const float* mine = turned + 32 * j;
+                        float x[16];
 #pragma unroll
-                        for (int j = 0; j < 16; j++) {
-                            const float mj = __shfl_sync(0xffffffffu, most, 2 * j);
-                            e[j] = exp2_fast((e[j] - (mj == kNegInf ? 0.0f : mj)) * kLog2e);
+                        for (int i = 0; i < 4; i++)            // four tokens read four different sets of banks
+                            *reinterpret_cast<float4*>(x + 4 * i) =
+                                *reinterpret_cast<const float4*>(mine + 16 * (lane & 1) + 4 * ((i + j) & 3));
+                        float m4[4] = {x[0], x[1], x[2], x[3]}, s4[4] = {};
+#pragma unroll
+                        for (int i = 4; i < 16; i++) m4[i & 3] = fmaxf(m4[i & 3], x[i]);
+                        float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                        const float m0 = m == kNegInf ? 0.0f : m;
+#pragma unroll
+                        for (int i = 0; i < 16; i++) s4[i & 3] += exp2_fast((x[i] - m0) * kLog2e);
+                        float sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                        if ((lane & 1) == 0 && c + j < tokens) {
+                            p.part[part * p.N + token0 + j] = make_float2(m, sum);
+                            const int at = few_target[token0 + j] - (row - lane);      // the target's row, if it is one of these
+                            if (at >= 0 && at < 32) {
+                                const float hit = mine[at];
+                                if (row - lane + at < p.M && q * 32 + at < p.tile_m / 2) p.hit[token0 + j] = hit;
+                            }
                         }
-                        const float sum = warp_each(e, [](float a, float b) { return a + b; });
-                        if ((lane & 1) == 0 && c + (lane >> 1) < tokens)
-                            p.part[part * p.N + token0 + (lane >> 1)] = make_float2(most, sum);
                     } else if (in) {
 #pragma unroll
                         for (int j = 0; j < 16; j++) {
                             const int token = token0 + j;
                             const float ratio = few_ratio[token];
-                            const float g = exp2_fast((z[c + j] - few_lse[token]) * kLog2e) - (row == few_target[token] ? 1.0f : 0.0f);
+                            const float g = exp2_fast((z[j] - few_lse[token]) * kLog2e) - (row == few_target[token] ? 1.0f : 0.0f);
                             if (c + j < tokens)
                                 p.g[(int64_t)token * p.ld_g + row] = __float2bfloat16_rn(ratio == 0.0f ? 0.0f : g * ratio);
                         }
                     }
+#pragma unroll
+                    for (int j = 0; j < 48; j++) z[j] = z[j + 16];
                 }
             }
         } else
@@ -560,7 +578,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 float z[128] = {};
                 bool ok = true;
                 for (int c0 = ti.k0; c0 < ti.k1; c0 += p.chunk, ++iter) {
-                    ok = tc::mbar_wait(tfull0 + 8 * (iter & 1), (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns);
+                    ok = wait(tfull0 + 8 * (iter & 1), (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns);
                     if (!ok) break;
                     tc::fence_after();
 #pragma unroll
@@ -576,9 +594,10 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 #pragma unroll
                     for (int j = 0; j < 128; j++) z[j] = j < cols ? z[j] : kNegInf;
                 if (__any_sync(0xffffffffu, target >= 0)) {
+                    float hit = 0.0f;
 #pragma unroll
-                    for (int j = 0; j < 128; j++)
-                        if (target == j && j < cols) p.hit[row] = z[j];
+                    for (int j = 0; j < 128; j++) hit = target == j ? z[j] : hit;
+                    if (target >= 0) p.hit[row] = hit;         // a target is below the vocabulary's end
                 }
                 float m4[4] = {z[0], z[1], z[2], z[3]};
 #pragma unroll
@@ -594,7 +613,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 continue;
             }
             const int buf = iter & 1;
-            if (!tc::mbar_wait(tfull0 + 8 * buf, (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns)) break;
+            if (!wait(tfull0 + 8 * buf, (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns)) break;
             tc::fence_after();
             ++iter;
             const uint32_t ta = ta0 + (uint32_t)(buf * kTile);
@@ -628,17 +647,17 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 
     // what was launched before this kernel is done when this kernel is
     if (p.wait == kWaitEnd) pdl_wait();
-    // Both CTAs have stopped issuing; if either gave up, the even CTA waits
-    // (bounded) for the loads still in flight before either may exit.
+    // Both CTAs have stopped issuing.  If either gave up, both know after the barrier, and the even CTA
+    // waits (bounded) for the loads still in flight before either may exit.
     tc::fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && *abort_flag) st_cluster(tc::mapa(tc::smem_u32((const void*)peer_abort), rank ^ 1), 1);
     tc::cluster_sync();
-    if (leader && warp == 0 && lane == 0) {
-        const int peer_abort = tc::ld_cluster_s32(tc::mapa(tc::smem_u32((const void*)abort_flag), 1));
-        if (*abort_flag || peer_abort)
+    if (*abort_flag || *peer_abort) {
+        if (leader && warp == 0 && lane == 0)
             drain_loads(full0, S, *issued_slot, tc::ld_cluster_s32(tc::mapa(tc::smem_u32((const void*)issued_slot), 1)), p.tx);
+        tc::cluster_sync();
     }
-    tc::cluster_sync();
     if (warp == 1) {
         tc::fence_after();
         tc::tmem_dealloc<2>(tmem, kTmemCols);
@@ -736,7 +755,7 @@ cudaError_t gemm(GemmParams p, const Operand& a, const Operand& b, const CUtenso
     p.mma_last = (int32_t)((K - (int64_t)(p.k_stages - 1) * kSub * kSubK + 15) / 16);
     p.tile_m = tile_m;
     p.b_bytes = kSub * (tile_n / 2) * kSubK * 2;
-    p.stages = std::min(kMaxStages, (kSmem - 1024 - 256 - 4096) / (kOpBytes + p.b_bytes));
+    p.stages = std::min(kMaxStages, (kSmem - 1024 - 256 - kFewOut) / (kOpBytes + p.b_bytes));
     p.tx = (uint32_t)(kSub * (tile_m / 2) * kSubK * 2 + p.b_bytes);
     p.m_tiles = (int32_t)((p.M + tile_m - 1) / tile_m);
     p.n_tiles = (int32_t)((p.N + tile_n - 1) / tile_n);
