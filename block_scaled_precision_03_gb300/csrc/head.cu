@@ -137,6 +137,14 @@ __device__ __forceinline__ float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// An element of g; ratio 0 (a token that does not count) gives 0 whatever its logits
+__device__ __forceinline__ float few_g(float z, float lse, float ratio, bool target) {
+    const float g = exp2_fast((z - lse) * kLog2e) - (target ? 1.0f : 0.0f);
+    return ratio == 0.0f ? 0.0f : g * ratio;
+}
+// Where lane l's i-th group of four rows starts: its 16 rows, begun at another
+// place for each of four neighbouring tokens
+__device__ __forceinline__ int turn(int lane, int i) { return 16 * (lane & 1) + ((i + 2 * (lane & ~1)) & 15); }
 template <bool ADD>
 __device__ __forceinline__ void tma_store_3d(const void* tmap, int32_t x, int32_t y, int32_t z, uint32_t src) {
     if (ADD)
@@ -505,25 +513,25 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 // once per call, and fetching it four times over took longer than running it
 #pragma unroll 1
                 for (int c = 0; c < tokens; c += 16) {
-                    const int token0 = own + c;
+                    // the 32 rows by 16 tokens turn in shared memory: two lanes a token, 16 rows each.  (Sums
+                    // across the lanes and stores of single elements took three times the instructions, and
+                    // with one or two warps a scheduler an instruction costs its latency.)
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 16; j++) turned[32 * j + lane] = MODE == kFewGrad || in ? z[j] : kNegInf;
+                    __syncwarp();
+                    const int j = lane >> 1, token = own + c + j, row0 = row - lane;
+                    const bool live = c + j < tokens;
+                    const float* mine = turned + 32 * j;
+                    const int at = few_target[token] - row0;       // the target's row, if it is one of these 32
                     if (MODE == kFewStats) {
-                        // the 32 rows by 16 tokens turn in shared memory: two lanes a token, 16 rows each.  (Sums
-                        // across the lanes took three times the instructions, and with one or two warps a
-                        // scheduler an instruction costs its latency.)
-                        __syncwarp();
+                        float x[16], m4[4] = {kNegInf, kNegInf, kNegInf, kNegInf}, s4[4] = {};
 #pragma unroll
-                        for (int j = 0; j < 16; j++) turned[32 * j + lane] = in ? z[j] : kNegInf;
-                        __syncwarp();
-                        const int j = lane >> 1;
-                        const float* mine = turned + 32 * j;
-                        float x[16];
+                        for (int i = 0; i < 16; i += 4) {          // four tokens read four different sets of banks
+                            *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(mine + turn(lane, i));
 #pragma unroll
-                        for (int i = 0; i < 4; i++)            // four tokens read four different sets of banks
-                            *reinterpret_cast<float4*>(x + 4 * i) =
-                                *reinterpret_cast<const float4*>(mine + 16 * (lane & 1) + 4 * ((i + j) & 3));
-                        float m4[4] = {x[0], x[1], x[2], x[3]}, s4[4] = {};
-#pragma unroll
-                        for (int i = 4; i < 16; i++) m4[i & 3] = fmaxf(m4[i & 3], x[i]);
+                            for (int k = 0; k < 4; k++) m4[k] = fmaxf(m4[k], x[i + k]);
+                        }
                         float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
                         const float m0 = m == kNegInf ? 0.0f : m;
@@ -531,22 +539,24 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                         for (int i = 0; i < 16; i++) s4[i & 3] += exp2_fast((x[i] - m0) * kLog2e);
                         float sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
                         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                        if ((lane & 1) == 0 && c + j < tokens) {
-                            p.part[part * p.N + token0 + j] = make_float2(m, sum);
-                            const int at = few_target[token0 + j] - (row - lane);      // the target's row, if it is one of these
-                            if (at >= 0 && at < 32) {
-                                const float hit = mine[at];
-                                if (row - lane + at < p.M && q * 32 + at < p.tile_m / 2) p.hit[token0 + j] = hit;
-                            }
+                        if ((lane & 1) == 0 && live) {
+                            p.part[part * p.N + token] = make_float2(m, sum);
+                            if (at >= 0 && at < 32 && row0 + at < p.M && q * 32 + at < p.tile_m / 2) p.hit[token] = mine[at];
                         }
-                    } else if (in) {
+                    } else if (live) {
+                        const float ratio = few_ratio[token], lse = few_lse[token];
+                        __nv_bfloat16* g = p.g + (int64_t)token * p.ld_g + row0;
 #pragma unroll
-                        for (int j = 0; j < 16; j++) {
-                            const int token = token0 + j;
-                            const float ratio = few_ratio[token];
-                            const float g = exp2_fast((z[j] - few_lse[token]) * kLog2e) - (row == few_target[token] ? 1.0f : 0.0f);
-                            if (c + j < tokens)
-                                p.g[(int64_t)token * p.ld_g + row] = __float2bfloat16_rn(ratio == 0.0f ? 0.0f : g * ratio);
+                        for (int i = 0; i < 16; i += 4) {
+                            // (tile_m / 2 is a multiple of 8, and a row of g has room for whole tiles of 256)
+                            const int r = turn(lane, i);
+                            if (q * 32 + r >= p.tile_m / 2 || row0 + r >= p.M) continue;
+                            const float4 x = *reinterpret_cast<const float4*>(mine + r);
+                            const float v[4] = {few_g(x.x, lse, ratio, at == r), few_g(x.y, lse, ratio, at == r + 1),
+                                                few_g(x.z, lse, ratio, at == r + 2), few_g(x.w, lse, ratio, at == r + 3)};
+                            const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
+                            *reinterpret_cast<uint2*>(g + r) =
+                                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
                         }
                     }
 #pragma unroll
