@@ -621,6 +621,121 @@ __global__ void __launch_bounds__(kMaxThreads) norm_backward_kernel(const NormAr
         }
 }
 
+// The same for rows of up to 32 columns a thread (BF16, kLongCols): the column
+// sums alone are 64 registers, so nothing else stays in them.  The weight lies in
+// shared memory as FP32, and dx's pass reads x and dy from the ring again, whose
+// slot is free only after it.  One row at a time and CTA.
+constexpr int kLongVecs = 4, kLongDepth = 2;
+constexpr int64_t kLongCols = 8 * kLongVecs * kMaxThreads;
+template <bool COLS>
+__global__ void __launch_bounds__(kMaxThreads) norm_backward_long_kernel(const NormArgs a) {
+    using T = __nv_bfloat16;
+    constexpr int NV = kLongVecs, VEC = 8, H = 4;
+    extern __shared__ uint4 ring_smem[];           // the ring, then the weight: [2][nvec] of four columns
+    __shared__ __align__(16) float part[2 * 2 * kPart];
+    const int tpr = blockDim.x, at = threadIdx.x, nvec = (int)(a.cols / VEC);
+    const Group q(tpr, part, 2 * 2 * kPart);
+    const float per_col = 1.0f / (float)a.cols;
+    const Ring<NV, 2> ring(ring_smem);
+    float4* weight = reinterpret_cast<float4*>(ring_smem + kLongDepth * 2 * NV * tpr);
+    int64_t ra = blockIdx.x;
+    const auto issue = [&](int slot) {
+        const uint32_t to = ring.slot(slot);
+        if (ra < a.rows) {
+            const T* x = static_cast<const T*>(a.x) + ra * a.ldx + at * VEC;
+            const T* d = static_cast<const T*>(a.dy) + ra * a.ld_dy + at * VEC;
+#pragma unroll
+            for (int i = 0; i < NV; i++)
+                if (at + i * tpr < nvec) {
+                    ring.copy(to, 0, i, x + i * tpr * VEC);
+                    ring.copy(to, 1, i, d + i * tpr * VEC);
+                }
+        }
+        ahead_commit();
+        ra += gridDim.x;
+    };
+#pragma unroll
+    for (int d = 0; d < kLongDepth; d++) issue(d);
+    for (int v = at; v < nvec; v += tpr) {         // each thread its own columns: no barrier
+        float f[VEC];
+        params<VEC>(f, a.weight, a.param_bf16, 1.0f, (int64_t)v * VEC);
+        weight[v] = make_float4(f[0], f[1], f[2], f[3]);
+        weight[nvec + v] = make_float4(f[4], f[5], f[6], f[7]);
+    }
+    F2 dw[NV][H], db[NV][H];
+#pragma unroll
+    for (int i = 0; i < NV; i++)
+#pragma unroll
+        for (int e = 0; e < H; e++) dw[i][e] = db[i][e] = F2(0.0f);
+    int n = 0, slot = 0;
+    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, n ^= 1, slot = slot + 1 == kLongDepth ? 0 : slot + 1) {
+        const float mean = a.mean[r], rstd = a.rstd[r];
+        const F2 minus(-mean), scale(rstd);
+        const uint32_t from = ring.slot(slot);
+        F2 x[H], dy[H], w[H], s0(0.0f), s1(0.0f);
+        const auto read = [&](int i) {
+            Pack<T, VEC> px, pd;
+            ring.read(px, from, 0, i);
+            ring.read(pd, from, 1, i);
+            const float4 w0 = weight[at + i * tpr], w1 = weight[nvec + at + i * tpr];
+            unpack2(px, x);
+            unpack2(pd, dy);
+            w[0] = F2(w0.x, w0.y);
+            w[1] = F2(w0.z, w0.w);
+            w[2] = F2(w1.x, w1.y);
+            w[3] = F2(w1.z, w1.w);
+#pragma unroll
+            for (int e = 0; e < H; e++) x[e] = (x[e] + minus) * scale;
+        };
+        ahead_wait<kLongDepth - 1>();
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            if (at + i * tpr >= nvec) continue;
+            read(i);
+#pragma unroll
+            for (int e = 0; e < H; e++) {
+                const F2 gr = dy[e] * w[e];
+                s0 = s0 + gr;
+                s1 = fma2(gr, x[e], s1);
+                if (COLS) {
+                    dw[i][e] = fma2(dy[e], x[e], dw[i][e]);
+                    db[i][e] = db[i][e] + dy[e];
+                }
+            }
+        }
+        float s[2] = {s0.get().x + s0.get().y, s1.get().x + s1.get().y};
+        group_sum<true>(s, q, part, n);
+        const F2 m0(-(s[0] * per_col)), m1(-(s[1] * per_col));
+        T* dx = static_cast<T*>(a.y) + r * a.ldy + at * VEC;
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            if (at + i * tpr >= nvec) continue;
+            read(i);
+#pragma unroll
+            for (int e = 0; e < H; e++) dy[e] = fma2(dy[e], w[e], fma2(x[e], m1, m0)) * scale;
+            Pack<T, VEC> o;
+            pack2(o, dy);
+            o.store(dx + i * tpr * VEC);
+        }
+        issue(slot);                               // this thread has read the slot twice
+    }
+    ahead_wait<0>();
+    if (!COLS) return;
+    pdl_launch_dependents();
+    float* out = a.ws + (int64_t)blockIdx.x * 2 * a.cols;
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+        if (at + i * tpr >= nvec) continue;
+#pragma unroll
+        for (int e = 0; e < H; e += 2) {
+            const float2 u = dw[i][e].get(), u1 = dw[i][e + 1].get(), v = db[i][e].get(), v1 = db[i][e + 1].get();
+            float* to = out + (at + i * tpr) * VEC + 2 * e;
+            *reinterpret_cast<float4*>(to) = make_float4(u.x, u.y, u1.x, u1.y);
+            *reinterpret_cast<float4*>(to + a.cols) = make_float4(v.x, v.y, v1.x, v1.y);
+        }
+    }
+}
+
 // Adds the partial rows: 32 columns a CTA, the parts dealt to 32 threads each
 // (blockIdx.y: 0 dweight, 1 dbias).
 __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* ws, int parts, int64_t cols, float* dweight,
@@ -880,6 +995,21 @@ cudaError_t backward(const NormArgs& a, cudaStream_t st) {
     return full(a.cols / kVec<T>, NV) ? backward_f<T, NV, DEPTH, true>(a, st) : backward_f<T, NV, DEPTH, false>(a, st);
 }
 
+template <bool COLS>
+cudaError_t backward_long_c(const NormArgs& a, cudaStream_t st) {
+    const int64_t nvec = a.cols / 8;
+    const int threads = lanes(nvec, kLongVecs);
+    const size_t smem = (size_t)kLongDepth * 2 * kLongVecs * threads * 16 + (size_t)a.cols * 4;
+    cudaError_t e = cudaFuncSetAttribute(norm_backward_long_kernel<COLS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         200 * 1024);
+    if (e != cudaSuccess) return e;
+    const unsigned ctas = (unsigned)std::min<int64_t>({a.num_sms, a.rows, kMaxParts});
+    norm_backward_long_kernel<COLS><<<ctas, threads, smem, st>>>(a);
+    if (!COLS) return cudaGetLastError();
+    return launch_k(true, norm_reduce_kernel, dim3((unsigned)((a.cols + 31) / 32), 2), 1024, 0, st, a.ws, (int)ctas,
+                    a.cols, a.dweight, a.dbias);
+}
+
 template <typename T, int VEC>
 cudaError_t columns(const NormArgs& a, cudaStream_t st) {
     // row groups: enough CTAs for every SM to hold several, at least 8 rows each
@@ -938,6 +1068,9 @@ cudaError_t backward_t(const NormArgs& a, cudaStream_t st) {
         // 16 columns a thread: more would not leave room for their sums
         constexpr int NV = 16 / VEC;
         if (n <= NV * kMaxThreads) return backward<T, NV, 2>(a, st);
+        if constexpr (VEC == 8)
+            if (a.cols <= kLongCols)
+                return a.dweight || a.dbias ? backward_long_c<true>(a, st) : backward_long_c<false>(a, st);
     }
     // the column sums first: dx may be written over dy
     if (a.dweight || a.dbias) {

@@ -83,6 +83,13 @@ def test_backward(bsq, R, C, dtype, pad, offset, kind):
     assert torch.equal(d2, dx)
 
 
+@pytest.mark.parametrize("R,C,kind", [(400, 9000, "f32"), (350, 16384, "bf16"), (2, 8200, "none"), (1, 12288, "f32"),
+                                      (311, 14336, "f32")])
+def test_backward_of_long_rows(bsq, R, C, kind):
+    test_backward(bsq, R, C, torch.bfloat16, 0, 0, kind)
+    test_backward(bsq, R, C, torch.bfloat16, 8, 8, kind)
+
+
 def test_large_mean_keeps_the_variance(bsq):
     # values 1000 +- 2^-9 (exact in FP32): a variance by differences of squares would be lost
     x = torch.full((4, 4096), 1000.0, device="cuda")
