@@ -147,53 +147,20 @@ template <typename T>
 __device__ __forceinline__ int row_shift(const T* row) {
     return (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
 }
-// VEC elements from column c of a row whose neighbours within a vector on
-// either side are the row's too: two aligned loads and a shift by whole words
-// (and half a word for BF16), without a branch, so that many can be in flight.
+// A vector's elements one by one, for a row that lies to 16-byte boundaries otherwise than the vectors
 template <typename T>
-__device__ __forceinline__ bool is_inside(int c, int cols) { return c >= kVec<T> - 1 && c + 2 * kVec<T> - 1 <= cols; }
-template <typename T>
-__device__ __forceinline__ void load_inside(Pack<T, kVec<T>>& p, const T* row, int c) {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);
-    const int sh = (int)(at & 15);
-    const uint4* q = reinterpret_cast<const uint4*>(at - sh);
-    const uint4 lo = q[0], hi = q[1];
-    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-    uint32_t u[6], t[5];
+__device__ __forceinline__ void load_each(Pack<T, kVec<T>>& p, const T* at) {
+    T e[kVec<T>];
 #pragma unroll
-    for (int i = 0; i < 6; i++) u[i] = sh & 8 ? w[i + 2] : w[i];
-#pragma unroll
-    for (int i = 0; i < 5; i++) t[i] = sh & 4 ? u[i + 1] : u[i];
-    uint32_t* out = reinterpret_cast<uint32_t*>(&p.v);
-#pragma unroll
-    for (int i = 0; i < 4; i++) out[i] = sizeof(T) == 2 ? __funnelshift_r(t[i], t[i + 1], (sh & 2) * 8) : t[i];
-}
-// the same from any column, element by element, zero outside [0, cols)
-template <typename T>
-__device__ __forceinline__ void load_elements(Pack<T, kVec<T>>& p, const T* row, int c, int cols) {
-    T* out = reinterpret_cast<T*>(&p.v);
-#pragma unroll
-    for (int e = 0; e < kVec<T>; e++) {
-        Pack<T, 1> one;
-        one.zero();
-        if (c + e >= 0 && c + e < cols) one.load(row + c + e);
-        out[e] = one.v;
-    }
+    for (int i = 0; i < kVec<T>; i++) e[i] = at[i];
+    memcpy(&p.v, e, 16);
 }
 template <typename T>
-__device__ __forceinline__ void store_elements(const Pack<T, kVec<T>>& p, T* row, int c, int cols) {
-    const T* in = reinterpret_cast<const T*>(&p.v);
+__device__ __forceinline__ void store_each(const Pack<T, kVec<T>>& p, T* at) {
+    T e[kVec<T>];
+    memcpy(e, &p.v, 16);
 #pragma unroll
-    for (int e = 0; e < kVec<T>; e++)
-        if (c + e >= 0 && c + e < cols) row[c + e] = in[e];
-}
-// Vector at column c of a row whose grid of vectors is its own (row + c on a
-// 16-byte boundary); columns outside [0, cols) are not written.
-template <typename T>
-__device__ __forceinline__ void store_edge(const Pack<T, kVec<T>>& p, T* row, int c, int cols) {
-    constexpr int VEC = kVec<T>;
-    if (c >= 0 && c + VEC <= cols) p.store(row + c);
-    else store_elements(p, row, c, cols);
+    for (int i = 0; i < kVec<T>; i++) at[i] = e[i];
 }
 
 // rows of a matrix start on 16-byte boundaries and hold whole vectors

@@ -115,39 +115,77 @@ __device__ __forceinline__ void group_sum(float (&v)[N], const Group& q, float* 
     }
 }
 
-// A row's vectors of one thread, v = at + i * tpr.  Vector v holds the columns
-// v * VEC - shift ... (shift: where x's row starts behind a 16-byte boundary,
-// whatever the other matrices do, so that the sums do not depend on them; 0 for
-// EVEN calls, whose rows all start on one and hold whole vectors); columns
-// outside [0, cols) are zero here and not stored.
+// Where a thread's part of a row lies.  Its vectors lie on 16-byte boundaries of x
+// (whatever the other matrices do, so that the sums do not depend on them), the
+// first at column `c0`, the next `step` columns further, all of them whole; the
+// up to 2 VEC - 2 elements of the row outside whole vectors go to the group's
+// first lanes, one each (column `edge`, -1 for none).  EVEN calls, whose rows
+// start on a boundary and hold whole vectors, have none.
+template <typename T, bool EVEN>
+struct Part {
+    static constexpr int VEC = kVec<T>;
+    int shift, first, c0, step, edge;
+    __device__ __forceinline__ Part(const T* row, int at, int tpr, int cols) {
+        shift = EVEN ? 0 : row_shift(row);
+        first = shift ? 1 : 0;                     // vector 0 holds columns -shift ...
+        c0 = (first + at) * VEC - shift;
+        step = tpr * VEC;
+        edge = -1;
+        if (!EVEN) {
+            const int head = min(cols, first * VEC - shift), tail = cols - (cols - head) % VEC;
+            edge = at < head ? at : tail + at - head < cols ? tail + at - head : -1;
+        }
+    }
+    __device__ __forceinline__ int column(int i) const { return c0 + i * step; }
+};
+
 template <typename T, int NV, bool EVEN>
 struct Row {
     static constexpr int VEC = kVec<T>;
     Pack<T, VEC> p[NV];
+    float edge;
     // `alike`: the row lies to 16-byte boundaries as the vectors do
-    __device__ __forceinline__ void load(const T* row, bool alike, int shift, int at, int tpr, int cols) {
+    __device__ __forceinline__ void load(const T* row, bool alike, const Part<T, EVEN>& at, int cols) {
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            const int c = (at + i * tpr) * VEC - shift;
             p[i].zero();
-            if (EVEN ? c < cols : alike && c >= 0 && c + VEC <= cols) p[i].load(row + c);
+            if (alike && at.column(i) + VEC <= cols) p[i].load(row + at.column(i));
         }
-        // the rest after all of those: the branches would keep them apart
-        if constexpr (!EVEN)
+        if (!alike)
+#pragma unroll 1
+            for (int i = 0; i < NV; i++)
+                if (at.column(i) + VEC <= cols) {
+                    Pack<T, VEC> q;
+                    load_each(q, row + at.column(i));
 #pragma unroll
-            for (int i = 0; i < NV; i++) {
-                const int c = (at + i * tpr) * VEC - shift;
-                if (c >= cols || (alike && c >= 0 && c + VEC <= cols)) continue;
-                if (is_inside<T>(c, cols)) load_inside(p[i], row, c);
-                else load_elements(p[i], row, c, cols);
-            }
+                    for (int k = 0; k < NV; k++)
+                        if (k == i) p[k] = q;
+                }
+        edge = at.edge < 0 ? 0.0f : element(row, at.edge);
     }
-    __device__ __forceinline__ static void store(T* row, bool alike, int c, int cols, const float (&f)[VEC]) {
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < NV; i++) p[i].zero();
+        edge = 0.0f;
+    }
+    __device__ __forceinline__ static float element(const T* row, int c) {
+        Pack<T, 1> e;
+        float f[1];
+        e.load(row + c);
+        e.unpack(f);
+        return f[0];
+    }
+    __device__ __forceinline__ static void put(T* row, int c, float v) {
+        Pack<T, 1> e;
+        const float f[1] = {v};
+        e.pack(f);
+        e.store(row + c);
+    }
+    __device__ __forceinline__ static void store(T* row, bool alike, int c, const F2 (&f)[VEC / 2]) {
         Pack<T, VEC> o;
-        o.pack(f);
-        if (EVEN) o.store(row + c);
-        else if (alike) store_edge(o, row, c, cols);
-        else store_elements(o, row, c, cols);
+        pack2(o, f);
+        if (alike) o.store(row + c);
+        else store_each(o, row + c);
     }
     // Between two passes over the row: the compiler may not keep the unpacked
     // values of the first for the second (twice the registers).
@@ -184,19 +222,30 @@ struct OddParams {
 #pragma unroll
         for (int e = 0; e < VEC; e++) off[e] = ((e - shift) & (VEC - 1)) * pitch + ((e - shift) >> (VEC == 8 ? 3 : 2));
     }
-    __device__ __forceinline__ void weights(float (&f)[VEC], int v) const {
+    __device__ __forceinline__ void weights(F2 (&f)[VEC / 2], int v) const {
 #pragma unroll
-        for (int e = 0; e < VEC; e++) f[e] = w[off[e] + v];
+        for (int e = 0; e < VEC; e += 2) f[e / 2] = F2(w[off[e] + v], w[off[e + 1] + v]);
     }
-    __device__ __forceinline__ void biases(float (&f)[VEC], int v) const {
+    __device__ __forceinline__ void biases(F2 (&f)[VEC / 2], int v) const {
 #pragma unroll
-        for (int e = 0; e < VEC; e++) f[e] = w[VEC * pitch + off[e] + v];
+        for (int e = 0; e < VEC; e += 2) f[e / 2] = F2(w[VEC * pitch + off[e] + v], w[VEC * pitch + off[e + 1] + v]);
     }
+    __device__ __forceinline__ float weight(int c) const { return w[c % VEC * pitch + c / VEC]; }
+    __device__ __forceinline__ float bias(int c) const { return w[VEC * pitch + c % VEC * pitch + c / VEC]; }
 };
+
+// VEC parameters from column c as pairs
+template <int VEC>
+__device__ __forceinline__ void params2(F2 (&f)[VEC / 2], const void* p, int bf16, float none, int64_t c) {
+    float x[VEC];
+    params<VEC>(x, p, bf16, none, c);
+#pragma unroll
+    for (int e = 0; e < VEC / 2; e++) f[e] = F2(x[2 * e], x[2 * e + 1]);
+}
 
 template <typename T, int NV, bool EVEN>
 __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a, int tpr) {
-    constexpr int VEC = kVec<T>;
+    constexpr int VEC = kVec<T>, H = VEC / 2;
     using R = Row<T, NV, EVEN>;
     extern __shared__ float odd_smem[];
     __shared__ __align__(16) float part[2 * kPart];
@@ -210,60 +259,63 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a, int
         const bool live = r < a.rows;              // lanes of a warp stay together for the sums
         T* y = static_cast<T*>(a.y) + (live ? r : 0) * a.ldy;
         const T* row = static_cast<const T*>(a.x) + (live ? r : 0) * a.ldx;
-        const int shift = EVEN ? 0 : row_shift(row);
-        const bool alike = EVEN || row_shift(y) == shift;
-        if (!EVEN) odd.row(shift);
+        const Part<T, EVEN> mine(row, at, tpr, cols);
+        const bool alike = EVEN || row_shift(y) == mine.shift;
+        if (!EVEN) odd.row(mine.shift);
         R x;
-        if (live) x.load(row, true, shift, at, tpr, cols);
-        else
-#pragma unroll
-            for (int i = 0; i < NV; i++) x.p[i].zero();
-        float s[1] = {0.0f};
+        if (live) x.load(row, true, mine, cols);
+        else x.zero();
+        F2 sum(0.0f);
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            float f[VEC];
-            x.p[i].unpack(f);
+            F2 f[H];
+            unpack2(x.p[i], f);
 #pragma unroll
-            for (int e = 0; e < VEC; e++) s[0] += f[e];
+            for (int e = 0; e < H; e++) sum = sum + f[e];
         }
+        float s[1] = {sum.get().x + sum.get().y + x.edge};
         group_sum(s, q, part, 0);
         const float mean = s[0] * per_col;
-        s[0] = 0.0f;
+        const F2 minus(-mean);
+        F2 sq(0.0f);
         x.again();
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            const int c = (at + i * tpr) * VEC - shift;
-            if (c >= cols) continue;
-            float f[VEC];
-            x.p[i].unpack(f);
-            const bool whole = EVEN || (c >= 0 && c + VEC <= cols);
+            if (mine.column(i) + VEC > cols) continue;
+            F2 f[H];
+            unpack2(x.p[i], f);
 #pragma unroll
-            for (int e = 0; e < VEC; e++) {
-                const float d = f[e] - mean;
-                if (whole || (c + e >= 0 && c + e < cols)) s[0] = fmaf(d, d, s[0]);
+            for (int e = 0; e < H; e++) {
+                f[e] = f[e] + minus;
+                sq = fma2(f[e], f[e], sq);
             }
         }
+        s[0] = sq.get().x + sq.get().y;
+        if (!EVEN && mine.edge >= 0) s[0] = fmaf(x.edge - mean, x.edge - mean, s[0]);
         group_sum(s, q, part, 1);
         const float rstd = rsqrtf(fmaf(s[0], per_col, a.eps));
         if (!live) continue;
+        const F2 scale(rstd);
         x.again();
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            const int c = (at + i * tpr) * VEC - shift;
-            if (c >= cols) continue;
-            float f[VEC], w[VEC], b[VEC];
-            x.p[i].unpack(f);
+            const int c = mine.column(i);
+            if (c + VEC > cols) continue;
+            F2 f[H], w[H], b[H];
+            unpack2(x.p[i], f);
             if (EVEN) {
-                params<VEC>(w, a.weight, a.param_bf16, 1.0f, c);
-                params<VEC>(b, a.bias, a.param_bf16, 0.0f, c);
+                params2<VEC>(w, a.weight, a.param_bf16, 1.0f, c);
+                params2<VEC>(b, a.bias, a.param_bf16, 0.0f, c);
             } else {
-                odd.weights(w, at + i * tpr);
-                odd.biases(b, at + i * tpr);
+                odd.weights(w, mine.first + at + i * tpr);
+                odd.biases(b, mine.first + at + i * tpr);
             }
 #pragma unroll
-            for (int e = 0; e < VEC; e++) f[e] = (f[e] - mean) * rstd * w[e] + b[e];
-            R::store(y, alike, c, cols, f);
+            for (int e = 0; e < H; e++) f[e] = fma2((f[e] + minus) * scale, w[e], b[e]);
+            R::store(y, alike, c, f);
         }
+        if (!EVEN && mine.edge >= 0)
+            R::put(y, mine.edge, fmaf((x.edge - mean) * rstd, odd.weight(mine.edge), odd.bias(mine.edge)));
         if (at == 0) {
             if (a.mean) a.mean[r] = mean;
             if (a.rstd) a.rstd[r] = rstd;
@@ -274,7 +326,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a, int
 // dx alone, a group of lanes per row as above
 template <typename T, int NV, bool EVEN>
 __global__ void __launch_bounds__(kMaxThreads) norm_dx_kernel(const NormArgs a, int tpr) {
-    constexpr int VEC = kVec<T>;
+    constexpr int VEC = kVec<T>, H = VEC / 2;
     using R = Row<T, NV, EVEN>;
     extern __shared__ float odd_smem[];
     __shared__ __align__(16) float part[2 * 2 * kPart];
@@ -289,59 +341,68 @@ __global__ void __launch_bounds__(kMaxThreads) norm_dx_kernel(const NormArgs a, 
         const bool live = r < a.rows;
         T* dx = static_cast<T*>(a.y) + (live ? r : 0) * a.ldy;
         const T* row = static_cast<const T*>(a.x) + (live ? r : 0) * a.ldx;
-        const int shift = EVEN ? 0 : row_shift(row);
-        const bool alike = EVEN || row_shift(dx) == shift;
-        if (!EVEN) odd.row(shift);
+        const Part<T, EVEN> mine(row, at, tpr, cols);
+        const bool alike = EVEN || row_shift(dx) == mine.shift;
+        if (!EVEN) odd.row(mine.shift);
         R x, d;
         float mean = 0.0f, rstd = 0.0f;
         if (live) {
             const T* dy = static_cast<const T*>(a.dy) + r * a.ld_dy;
-            x.load(row, true, shift, at, tpr, cols);
-            d.load(dy, EVEN || row_shift(dy) == shift, shift, at, tpr, cols);
+            x.load(row, true, mine, cols);
+            d.load(dy, EVEN || row_shift(dy) == mine.shift, mine, cols);
             mean = a.mean[r];
             rstd = a.rstd[r];
         } else {
-#pragma unroll
-            for (int i = 0; i < NV; i++) {
-                x.p[i].zero();
-                d.p[i].zero();
-            }
+            x.zero();
+            d.zero();
         }
-        float s[2] = {0.0f, 0.0f};
+        const F2 minus(-mean), scale(rstd);
+        const auto weights = [&](F2 (&w)[H], int i) {
+            if (EVEN) params2<VEC>(w, a.weight, a.param_bf16, 1.0f, mine.column(i));
+            else odd.weights(w, mine.first + at + i * tpr);
+        };
+        F2 s0(0.0f), s1(0.0f);
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            const int c = (at + i * tpr) * VEC - shift;
-            if (c >= cols) continue;
-            float fx[VEC], fd[VEC], w[VEC];
-            x.p[i].unpack(fx);
-            d.p[i].unpack(fd);
-            if (EVEN) params<VEC>(w, a.weight, a.param_bf16, 1.0f, c);
-            else odd.weights(w, at + i * tpr);
+            if (mine.column(i) + VEC > cols) continue;
+            F2 fx[H], fd[H], w[H];
+            unpack2(x.p[i], fx);
+            unpack2(d.p[i], fd);
+            weights(w, i);
 #pragma unroll
-            for (int e = 0; e < VEC; e++) {
-                const float gr = fd[e] * w[e];         // outside the row both are zero
-                s[0] += gr;
-                s[1] = fmaf(gr, (fx[e] - mean) * rstd, s[1]);
+            for (int e = 0; e < H; e++) {
+                const F2 gr = fd[e] * w[e];
+                s0 = s0 + gr;
+                s1 = fma2(gr, (fx[e] + minus) * scale, s1);
             }
+        }
+        float s[2] = {s0.get().x + s0.get().y, s1.get().x + s1.get().y};
+        float we = 0.0f;
+        if (!EVEN && mine.edge >= 0) {
+            we = odd.weight(mine.edge);
+            s[0] = fmaf(d.edge, we, s[0]);
+            s[1] = fmaf(d.edge * we, (x.edge - mean) * rstd, s[1]);
         }
         group_sum(s, q, part, n);
         if (!live) continue;
-        const float s0 = s[0] * per_col, s1 = s[1] * per_col;
+        const float t0 = -(s[0] * per_col), t1 = -(s[1] * per_col);
+        const F2 m0(t0), m1(t1);
         x.again();
         d.again();
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            const int c = (at + i * tpr) * VEC - shift;
-            if (c >= cols) continue;
-            float fx[VEC], fd[VEC], w[VEC];
-            x.p[i].unpack(fx);
-            d.p[i].unpack(fd);
-            if (EVEN) params<VEC>(w, a.weight, a.param_bf16, 1.0f, c);
-            else odd.weights(w, at + i * tpr);
+            const int c = mine.column(i);
+            if (c + VEC > cols) continue;
+            F2 fx[H], fd[H], w[H];
+            unpack2(x.p[i], fx);
+            unpack2(d.p[i], fd);
+            weights(w, i);
 #pragma unroll
-            for (int e = 0; e < VEC; e++) fd[e] = rstd * (fd[e] * w[e] - s0 - (fx[e] - mean) * rstd * s1);
-            R::store(dx, alike, c, cols, fd);
+            for (int e = 0; e < H; e++) fd[e] = fma2(fd[e], w[e], fma2((fx[e] + minus) * scale, m1, m0)) * scale;
+            R::store(dx, alike, c, fd);
         }
+        if (!EVEN && mine.edge >= 0)
+            R::put(dx, mine.edge, fmaf(d.edge, we, fmaf((x.edge - mean) * rstd, t1, t0)) * rstd);
     }
 }
 
@@ -921,11 +982,11 @@ cudaError_t shape(Shape& s, K kernel, const NormArgs& a, int tpr, S smem, int pe
     return cudaSuccess;
 }
 
-// Lanes for n vectors, at most nv each: a power of two below a warp, else whole warps.
-int lanes(int64_t n, int nv) {
+// Lanes for n vectors, at most nv each: a power of two (`least` or more) below a warp, else whole warps.
+int lanes(int64_t n, int nv, int least = 4) {
     const int64_t want = (n + nv - 1) / nv;
     if (want > 32) return (int)((want + 31) / 32 * 32);
-    int t = 4;
+    int t = least;
     while (t < want) t *= 2;
     return t;
 }
@@ -938,7 +999,7 @@ size_t odd_bytes(const NormArgs& a, bool even) {
 template <typename T, int NV, bool EVEN>
 cudaError_t forward(const NormArgs& a, int64_t n, cudaStream_t st) {
     Shape s;
-    cudaError_t e = shape(s, norm_kernel<T, NV, EVEN>, a, lanes(n, NV), [&](const Shape&) { return odd_bytes(a, EVEN); }, 16);
+    cudaError_t e = shape(s, norm_kernel<T, NV, EVEN>, a, lanes(n, NV, EVEN ? 4 : 16), [&](const Shape&) { return odd_bytes(a, EVEN); }, 16);
     if (e != cudaSuccess) return e;
     norm_kernel<T, NV, EVEN><<<s.ctas, s.threads, s.smem, st>>>(a, s.tpr);
     return cudaGetLastError();
@@ -964,7 +1025,7 @@ cudaError_t stream(const NormArgs& a, cudaStream_t st) {
 template <typename T, int NV, bool EVEN>
 cudaError_t dx_only(const NormArgs& a, int64_t n, cudaStream_t st) {
     Shape s;
-    cudaError_t e = shape(s, norm_dx_kernel<T, NV, EVEN>, a, lanes(n, NV), [&](const Shape&) { return odd_bytes(a, EVEN); }, 16);
+    cudaError_t e = shape(s, norm_dx_kernel<T, NV, EVEN>, a, lanes(n, NV, EVEN ? 4 : 16), [&](const Shape&) { return odd_bytes(a, EVEN); }, 16);
     if (e != cudaSuccess) return e;
     norm_dx_kernel<T, NV, EVEN><<<s.ctas, s.threads, s.smem, st>>>(a, s.tpr);
     return cudaGetLastError();
@@ -1042,7 +1103,7 @@ cudaError_t forward_t(const NormArgs& a, cudaStream_t st) {
         return cudaGetLastError();
     }
     if (a.cols <= kMaxOddCols) {
-        const int64_t odd = (a.cols + 2 * kVec<T> - 2) / kVec<T>;      // vectors, wherever the row starts
+        const int64_t odd = a.cols / kVec<T>;                          // whole vectors, at most
         if (a.rows <= 2 * a.num_sms && odd <= kMaxThreads) return forward<T, 1, false>(a, odd, st);
         if (a.rows <= 2 * a.num_sms && odd <= 2 * kMaxThreads) return forward<T, 2, false>(a, odd, st);
         return odd <= 4 * 32 ? forward<T, 4, false>(a, odd, st) : forward<T, 8, false>(a, odd, st);
@@ -1053,7 +1114,7 @@ cudaError_t forward_t(const NormArgs& a, cudaStream_t st) {
 
 template <typename T, bool EVEN>
 cudaError_t dx_e(const NormArgs& a, cudaStream_t st) {
-    const int64_t n = EVEN ? a.cols / kVec<T> : (a.cols + 2 * kVec<T> - 2) / kVec<T>;
+    const int64_t n = a.cols / kVec<T>;
     if (a.rows <= 2 * a.num_sms && n <= 2 * kMaxThreads) return dx_only<T, 2, EVEN>(a, n, st);
     if (n <= 4 * 32) return dx_only<T, 4, EVEN>(a, n, st);
     return dx_only<T, 8, EVEN>(a, n, st);
