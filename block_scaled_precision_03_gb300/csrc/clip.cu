@@ -48,16 +48,20 @@ __device__ __forceinline__ int find(const Table<CAP>& t, int chunk) {
     return lo;
 }
 
+// Sum over the CTA, known to warp 0.  The SM has few FP64 lanes (a warp's
+// addition takes some 16 cycles of them), so one warp adds: 13 additions
+// instead of the 104 of a tree in every warp.  Once per CTA.
 __device__ __forceinline__ double block_sum(double v) {
-    __shared__ double part[kThreads / 32];
-#pragma unroll
-    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __shared__ double all[kThreads];
+    all[threadIdx.x] = v;
     __syncthreads();
     double s = 0.0;
+    if (threadIdx.x < 32) {
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; w++) s += part[w];
+        for (int w = 0; w < kThreads / 32; w++) s += all[w * 32 + threadIdx.x];
+#pragma unroll
+        for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    }
     return s;
 }
 
@@ -119,8 +123,12 @@ __global__ void __launch_bounds__(kThreads) square_sum_kernel(const __grid_const
 
 __device__ __forceinline__ float total_norm(const double* partial, int parts) {
     double s = 0.0;
+    __shared__ float norm;
     for (int i = threadIdx.x; i < parts; i += kThreads) s += partial[i];
-    return (float)sqrt(block_sum(s));
+    s = block_sum(s);
+    if (threadIdx.x == 0) norm = (float)sqrt(s);
+    __syncthreads();
+    return norm;
 }
 
 __global__ void __launch_bounds__(kThreads) norm_out_kernel(const double* partial, int parts, float* norm) {
