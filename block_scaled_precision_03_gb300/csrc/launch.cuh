@@ -67,6 +67,21 @@ struct Pack<float, 4> {
     __device__ __forceinline__ void pack(const float (&f)[4]) { v = make_float4(f[0], f[1], f[2], f[3]); }
 };
 template <>
+struct Pack<__nv_bfloat16, 2> {
+    uint32_t v;
+    __device__ __forceinline__ void zero() { v = 0; }
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint32_t*>(p); }
+    __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint32_t*>(p) = v; }
+    __device__ __forceinline__ void unpack(float (&f)[2]) const {
+        f[0] = __uint_as_float(v << 16);
+        f[1] = __uint_as_float(v & 0xFFFF0000u);
+    }
+    __device__ __forceinline__ void pack(const float (&f)[2]) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[0], f[1]);
+        v = *reinterpret_cast<const uint32_t*>(&h);
+    }
+};
+template <>
 struct Pack<__nv_bfloat16, 1> {
     __nv_bfloat16 v;
     __device__ __forceinline__ void zero() { v = __ushort_as_bfloat16(0); }
@@ -163,9 +178,9 @@ __device__ __forceinline__ void store_each(const Pack<T, kVec<T>>& p, T* at) {
     for (int i = 0; i < kVec<T>; i++) at[i] = e[i];
 }
 
-// rows of a matrix start on 16-byte boundaries and hold whole vectors
-inline bool rows_vec(const void* p, int64_t ld, int64_t cols, int bytes) {
-    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld * bytes % 16 == 0 && cols * bytes % 16 == 0;
+// rows of a matrix start on boundaries of `vector` bytes and hold whole vectors
+inline bool rows_vec(const void* p, int64_t ld, int64_t cols, int bytes, int vector = 16) {
+    return reinterpret_cast<uintptr_t>(p) % vector == 0 && ld * bytes % vector == 0 && cols * bytes % vector == 0;
 }
 
 }  // namespace bsq

@@ -24,6 +24,7 @@
 // its gradient with k = 4 in 92 instead of 49, because the warps that hold a
 // row's ends go both ways.)
 #include <algorithm>
+#include <type_traits>
 #include "common.cuh"
 #include "internal.h"
 #include "launch.cuh"
@@ -360,12 +361,12 @@ __global__ void __launch_bounds__(THREADS) moe_small_kernel(const SortArgs s, co
 // single elements of 4 columns each.  (Odd combine of 1021 x 3 x 2047: 9.3 us
 // with 4, 12.3 with 8.)
 template <int VEC>
-constexpr int kSlots = VEC == 1 ? 4 : 8;
+constexpr int kSlots = VEC <= 2 ? 4 : 8;
 
 // out[t] = sum_j weights[t, j] rows[slot_row[t, j]], in the order of j
 template <typename T, int VEC, int WPT, bool WEIGHTED>
 __global__ void __launch_bounds__(kRowThreads) moe_combine_kernel(const RowArgs a) {
-    constexpr int UN = VEC == 1 ? 4 : 1, S = kSlots<VEC>;
+    constexpr int UN = VEC <= 2 ? 4 : 1, S = kSlots<VEC>;
     const Place at = place<WPT>();
     if (at.t >= a.tokens) return;
     const T* src = static_cast<const T*>(a.src);
@@ -418,7 +419,7 @@ __global__ void __launch_bounds__(kRowThreads) moe_combine_kernel(const RowArgs 
 // with two (98 registers) 209, with four (spills) 176.
 template <typename T, int VEC, int WPT, bool DOT>
 __global__ void __launch_bounds__(kRowThreads, 3) moe_combine_backward_kernel(const RowArgs a) {
-    constexpr int UN = VEC == 1 ? 4 : 1, S = kSlots<VEC>;
+    constexpr int UN = VEC <= 2 ? 4 : 1, S = kSlots<VEC>;
     __shared__ float part[kRowThreads / 32][S];
     const Place at = place<WPT>();
     const bool live = at.t < a.tokens;
@@ -523,11 +524,19 @@ RowArgs row_args(const MoePlanArgs& p, const MoeRowsArgs& m, int vec) {
     return a;
 }
 
-// vectors only where every matrix of the call allows them
-bool vectors(const MoeRowsArgs& m) {
+// vectors of so many bytes only where every matrix of the call allows them
+bool vectors(const MoeRowsArgs& m, int bytes) {
     const int e = m.bf16 ? 2 : 4;
-    return rows_vec(m.src, m.ld_src, m.cols, e) && rows_vec(m.dst, m.ld_dst, m.cols, e) &&
-           (!m.rows || rows_vec(m.rows, m.ld_rows, m.cols, e));
+    return rows_vec(m.src, m.ld_src, m.cols, e, bytes) && rows_vec(m.dst, m.ld_dst, m.cols, e, bytes) &&
+           (!m.rows || rows_vec(m.rows, m.ld_rows, m.cols, e, bytes));
+}
+// f(element, vector length): 16 bytes, else pairs of BF16, else single elements
+template <typename F>
+cudaError_t by_vector(const MoeRowsArgs& m, F f) {
+    using std::integral_constant;
+    if (!m.bf16) return vectors(m, 16) ? f(0.0f, integral_constant<int, 4>()) : f(0.0f, integral_constant<int, 1>());
+    if (vectors(m, 16)) return f(__nv_bfloat16(), integral_constant<int, 8>());
+    return vectors(m, 4) ? f(__nv_bfloat16(), integral_constant<int, 2>()) : f(__nv_bfloat16(), integral_constant<int, 1>());
 }
 
 // warps per token: about 64 vectors each, so that a warp has several in flight
@@ -659,31 +668,21 @@ cudaError_t run_moe_sort(const MoePlanArgs& p, const void* ids, bool ids64, void
 cudaError_t run_moe_dispatch(const MoePlanArgs& p, const MoeRowsArgs& m, const void* ids, bool ids64, void* ws,
                              cudaStream_t st) {
     const SortArgs s = sort_args(p, ids, ids64, ws);
-    const bool v = vectors(m);
-    if (s.slots <= kSortThreads) {
-        if (m.bf16) return v ? small_t<__nv_bfloat16, 8>(p, s, &m, st) : small_t<__nv_bfloat16, 1>(p, s, &m, st);
-        return v ? small_t<float, 4>(p, s, &m, st) : small_t<float, 1>(p, s, &m, st);
-    }
+    if (s.slots <= kSortThreads)
+        return by_vector(m, [&](auto t, auto v) { return small_t<decltype(t), decltype(v)::value>(p, s, &m, st); });
     cudaError_t e = sort_large(s, st);
     if (e != cudaSuccess) return e;
-    if (m.bf16) return v ? gather_t<__nv_bfloat16, 8>(p, m, true, st) : gather_t<__nv_bfloat16, 1>(p, m, true, st);
-    return v ? gather_t<float, 4>(p, m, true, st) : gather_t<float, 1>(p, m, true, st);
+    return by_vector(m, [&](auto t, auto v) { return gather_t<decltype(t), decltype(v)::value>(p, m, true, st); });
 }
 
 cudaError_t run_moe_gather(const MoePlanArgs& p, const MoeRowsArgs& m, cudaStream_t st) {
-    const bool v = vectors(m);
-    if (m.bf16) return v ? gather_t<__nv_bfloat16, 8>(p, m, false, st) : gather_t<__nv_bfloat16, 1>(p, m, false, st);
-    return v ? gather_t<float, 4>(p, m, false, st) : gather_t<float, 1>(p, m, false, st);
+    return by_vector(m, [&](auto t, auto v) { return gather_t<decltype(t), decltype(v)::value>(p, m, false, st); });
 }
 cudaError_t run_moe_combine(const MoePlanArgs& p, const MoeRowsArgs& m, cudaStream_t st) {
-    const bool v = vectors(m);
-    if (m.bf16) return v ? combine_t<__nv_bfloat16, 8>(p, m, st) : combine_t<__nv_bfloat16, 1>(p, m, st);
-    return v ? combine_t<float, 4>(p, m, st) : combine_t<float, 1>(p, m, st);
+    return by_vector(m, [&](auto t, auto v) { return combine_t<decltype(t), decltype(v)::value>(p, m, st); });
 }
 cudaError_t run_moe_combine_backward(const MoePlanArgs& p, const MoeRowsArgs& m, cudaStream_t st) {
-    const bool v = vectors(m);
-    if (m.bf16) return v ? backward_t<__nv_bfloat16, 8>(p, m, st) : backward_t<__nv_bfloat16, 1>(p, m, st);
-    return v ? backward_t<float, 4>(p, m, st) : backward_t<float, 1>(p, m, st);
+    return by_vector(m, [&](auto t, auto v) { return backward_t<decltype(t), decltype(v)::value>(p, m, st); });
 }
 
 }  // namespace bsq

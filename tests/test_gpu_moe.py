@@ -91,6 +91,17 @@ def test_dispatch_gather_combine(bsq, T, k, E, C, dropped, dtype, pad, offset):
     assert torch.equal(bsq.moe_dispatch_backward(y, plan), out)
 
 
+# even widths that are not whole 16-byte vectors, and rows that start between them
+PAIRS = [(70, 4, 9, 1030, 0.1), (3, 2, 4, 2, 0.0), (300, 9, 20, 62, 0.2), (2000, 3, 8, 1764, 0.5)]
+
+
+@pytest.mark.parametrize("T,k,E,C,dropped", PAIRS)
+@pytest.mark.parametrize("pad,offset", [(0, 0), (2, 2), (6, 4)])
+def test_pairs(bsq, T, k, E, C, dropped, pad, offset):
+    test_dispatch_gather_combine(bsq, T, k, E, C, dropped, torch.bfloat16, pad, offset)
+    test_combine_backward(bsq, T, k, E, C, dropped, torch.bfloat16, pad, offset)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("T,k,E,C,dropped", CASES)
 @pytest.mark.parametrize("pad,offset", [(0, 0), (8, 0), (3, 1)])
