@@ -37,6 +37,9 @@ namespace {
 
 constexpr int kMaxThreads = 512;       // of a CTA: 128 registers each
 constexpr int kCta = 128;              // of a CTA of several rows
+// of many odd rows, whose weight and bias are in shared memory once a CTA: the more rows share
+// them, the less a CTA spends on filling it (1704 x 5746: 24.6 us, 42.9 with 128)
+constexpr int kOddCta = 512;
 constexpr int kMaxParts = 608;         // partial rows of the column sums: 4 CTAs on each of 152 SMs
 constexpr int kWide = 512;             // threads of the kernels for wide rows
 constexpr int kWideParts = 128;
@@ -74,8 +77,9 @@ __device__ __forceinline__ void params(float (&f)[VEC], const void* p, int bf16,
 // A row's group of `tpr` threads (a power of two below 32, or whole warps) and
 // where its warps' sums meet in shared memory: `part` holds [2][N][kPart]
 // floats, a group's warps side by side from a multiple of 4, zero where it has
-// none.  (At most 16: a CTA is one group of up to 16 warps, or two of 2 warps.)
-constexpr int kPart = 16;
+// none.  (At most 32: a CTA is one group of up to 16 warps, or 512 threads in
+// groups of 2 warps or more.)
+constexpr int kPart = 32;
 struct Group {
     int tpr, g, at, slot, base, quads;
     __device__ __forceinline__ Group(int lanes_per_row, float* part, int floats) : tpr(lanes_per_row) {
@@ -198,18 +202,24 @@ struct Row {
     }
 };
 
+// Kernels of up to 2 vectors a thread run where rows are few
+__host__ __device__ constexpr bool staged(int nv) { return nv > 2; }
+
 // Weight and bias of odd rows: column c at [c % VEC][c / VEC], so that lanes
 // whose columns lie VEC apart read neighbouring words.  The last word of every
 // line is zero, and so is what columns outside the row find there.
-template <int VEC>
+// Not STAGED (a CTA has one or two rows): they are read from global memory (7 x 4692 in 8.2 us, 8.9 staged).
+template <int VEC, bool STAGED>
 struct OddParams {
     float* w;
     int pitch, off[VEC];
     __device__ __forceinline__ void fill(float* smem, const NormArgs& a, bool bias) {
+        if (!STAGED) return;
         pitch = (int)((a.cols + VEC - 1) / VEC) + 1;
         w = smem;
         for (int i = threadIdx.x; i < (bias ? 2 : 1) * VEC * pitch; i += blockDim.x) w[i] = 0.0f;
         __syncthreads();
+#pragma unroll 8
         for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
             float* at = w + c % VEC * pitch + c / VEC;
             at[0] = a.weight ? param(a.weight, a.param_bf16, c) : 1.0f;
@@ -222,16 +232,25 @@ struct OddParams {
 #pragma unroll
         for (int e = 0; e < VEC; e++) off[e] = ((e - shift) & (VEC - 1)) * pitch + ((e - shift) >> (VEC == 8 ? 3 : 2));
     }
-    __device__ __forceinline__ void weights(F2 (&f)[VEC / 2], int v) const {
+    // of vector v, whose first column is c
+    __device__ __forceinline__ void get(F2 (&f)[VEC / 2], const float* from, const void* p, int bf16, float none, int v, int c) const {
 #pragma unroll
-        for (int e = 0; e < VEC; e += 2) f[e / 2] = F2(w[off[e] + v], w[off[e + 1] + v]);
+        for (int e = 0; e < VEC; e += 2)
+            f[e / 2] = STAGED ? F2(from[off[e] + v], from[off[e + 1] + v])
+                         : p ? F2(param(p, bf16, c + e), param(p, bf16, c + e + 1)) : F2(none);
     }
-    __device__ __forceinline__ void biases(F2 (&f)[VEC / 2], int v) const {
-#pragma unroll
-        for (int e = 0; e < VEC; e += 2) f[e / 2] = F2(w[VEC * pitch + off[e] + v], w[VEC * pitch + off[e + 1] + v]);
+    __device__ __forceinline__ void weights(F2 (&f)[VEC / 2], const NormArgs& a, int v, int c) const {
+        get(f, w, a.weight, a.param_bf16, 1.0f, v, c);
     }
-    __device__ __forceinline__ float weight(int c) const { return w[c % VEC * pitch + c / VEC]; }
-    __device__ __forceinline__ float bias(int c) const { return w[VEC * pitch + c % VEC * pitch + c / VEC]; }
+    __device__ __forceinline__ void biases(F2 (&f)[VEC / 2], const NormArgs& a, int v, int c) const {
+        get(f, w + VEC * pitch, a.bias, a.param_bf16, 0.0f, v, c);
+    }
+    __device__ __forceinline__ static float weight(const NormArgs& a, int c) {
+        return a.weight ? param(a.weight, a.param_bf16, c) : 1.0f;
+    }
+    __device__ __forceinline__ static float bias(const NormArgs& a, int c) {
+        return a.bias ? param(a.bias, a.param_bf16, c) : 0.0f;
+    }
 };
 
 // VEC parameters from column c as pairs
@@ -252,7 +271,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a, int
     const Group q(tpr, part, 2 * kPart);
     const int groups = blockDim.x / tpr, g = q.g, at = q.at, cols = (int)a.cols;
     const float per_col = 1.0f / (float)cols;
-    OddParams<VEC> odd;
+    OddParams<VEC, staged(NV)> odd;
     if (!EVEN) odd.fill(odd_smem, a, true);
     for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < a.rows; r0 += (int64_t)gridDim.x * groups) {
         const int64_t r = r0 + g;
@@ -307,15 +326,15 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a, int
                 params2<VEC>(w, a.weight, a.param_bf16, 1.0f, c);
                 params2<VEC>(b, a.bias, a.param_bf16, 0.0f, c);
             } else {
-                odd.weights(w, mine.first + at + i * tpr);
-                odd.biases(b, mine.first + at + i * tpr);
+                odd.weights(w, a, mine.first + at + i * tpr, c);
+                odd.biases(b, a, mine.first + at + i * tpr, c);
             }
 #pragma unroll
             for (int e = 0; e < H; e++) f[e] = fma2((f[e] + minus) * scale, w[e], b[e]);
             R::store(y, alike, c, f);
         }
         if (!EVEN && mine.edge >= 0)
-            R::put(y, mine.edge, fmaf((x.edge - mean) * rstd, odd.weight(mine.edge), odd.bias(mine.edge)));
+            R::put(y, mine.edge, fmaf((x.edge - mean) * rstd, odd.weight(a, mine.edge), odd.bias(a, mine.edge)));
         if (at == 0) {
             if (a.mean) a.mean[r] = mean;
             if (a.rstd) a.rstd[r] = rstd;
@@ -333,7 +352,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_dx_kernel(const NormArgs a, 
     const Group q(tpr, part, 2 * 2 * kPart);
     const int groups = blockDim.x / tpr, g = q.g, at = q.at, cols = (int)a.cols;
     const float per_col = 1.0f / (float)cols;
-    OddParams<VEC> odd;
+    OddParams<VEC, staged(NV)> odd;
     if (!EVEN) odd.fill(odd_smem, a, false);
     int n = 0;
     for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < a.rows; r0 += (int64_t)gridDim.x * groups, n ^= 1) {
@@ -359,7 +378,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_dx_kernel(const NormArgs a, 
         const F2 minus(-mean), scale(rstd);
         const auto weights = [&](F2 (&w)[H], int i) {
             if (EVEN) params2<VEC>(w, a.weight, a.param_bf16, 1.0f, mine.column(i));
-            else odd.weights(w, mine.first + at + i * tpr);
+            else odd.weights(w, a, mine.first + at + i * tpr, mine.column(i));
         };
         F2 s0(0.0f), s1(0.0f);
 #pragma unroll
@@ -379,7 +398,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_dx_kernel(const NormArgs a, 
         float s[2] = {s0.get().x + s0.get().y, s1.get().x + s1.get().y};
         float we = 0.0f;
         if (!EVEN && mine.edge >= 0) {
-            we = odd.weight(mine.edge);
+            we = odd.weight(a, mine.edge);
             s[0] = fmaf(d.edge, we, s[0]);
             s[1] = fmaf(d.edge * we, (x.edge - mean) * rstd, s[1]);
         }
@@ -960,12 +979,12 @@ struct Shape {
     size_t smem;
     unsigned ctas;
 };
-// `tpr` lanes a row; CTAs of about kCta threads unless one row takes more.
+// `tpr` lanes a row; CTAs of about `cta` threads unless one row takes more.
 // smem(s): bytes that a CTA of s.threads needs.
 template <typename K, typename S>
-cudaError_t shape(Shape& s, K kernel, const NormArgs& a, int tpr, S smem, int per_sm) {
+cudaError_t shape(Shape& s, K kernel, const NormArgs& a, int tpr, S smem, int per_sm, int cta = kCta) {
     s.tpr = tpr;
-    s.threads = tpr >= kCta ? tpr : kCta / tpr * tpr;
+    s.threads = tpr >= cta ? tpr : cta / tpr * tpr;
     s.groups = s.threads / tpr;
     s.smem = smem(s);
     if (s.smem > 40 * 1024) {
@@ -991,15 +1010,16 @@ int lanes(int64_t n, int nv, int least = 4) {
     return t;
 }
 
-size_t odd_bytes(const NormArgs& a, bool even) {
+int row_cta(const NormArgs& a, bool even) { return even || a.rows < 4 * (int64_t)a.num_sms ? kCta : kOddCta; }
+size_t odd_bytes(const NormArgs& a, int nv, bool even) {
     const int64_t vec = a.bf16 ? 8 : 4;
-    return even ? 0 : (size_t)(2 * vec * ((a.cols + vec - 1) / vec + 1)) * sizeof(float);
+    return even || !staged(nv) ? 0 : (size_t)(2 * vec * ((a.cols + vec - 1) / vec + 1)) * sizeof(float);
 }
 
 template <typename T, int NV, bool EVEN>
 cudaError_t forward(const NormArgs& a, int64_t n, cudaStream_t st) {
     Shape s;
-    cudaError_t e = shape(s, norm_kernel<T, NV, EVEN>, a, lanes(n, NV, EVEN ? 4 : 16), [&](const Shape&) { return odd_bytes(a, EVEN); }, 16);
+    cudaError_t e = shape(s, norm_kernel<T, NV, EVEN>, a, lanes(n, NV, EVEN ? 4 : 16), [&](const Shape&) { return odd_bytes(a, NV, EVEN); }, 16, row_cta(a, EVEN));
     if (e != cudaSuccess) return e;
     norm_kernel<T, NV, EVEN><<<s.ctas, s.threads, s.smem, st>>>(a, s.tpr);
     return cudaGetLastError();
@@ -1025,7 +1045,7 @@ cudaError_t stream(const NormArgs& a, cudaStream_t st) {
 template <typename T, int NV, bool EVEN>
 cudaError_t dx_only(const NormArgs& a, int64_t n, cudaStream_t st) {
     Shape s;
-    cudaError_t e = shape(s, norm_dx_kernel<T, NV, EVEN>, a, lanes(n, NV, EVEN ? 4 : 16), [&](const Shape&) { return odd_bytes(a, EVEN); }, 16);
+    cudaError_t e = shape(s, norm_dx_kernel<T, NV, EVEN>, a, lanes(n, NV, EVEN ? 4 : 16), [&](const Shape&) { return odd_bytes(a, NV, EVEN); }, 16, row_cta(a, EVEN));
     if (e != cudaSuccess) return e;
     norm_dx_kernel<T, NV, EVEN><<<s.ctas, s.threads, s.smem, st>>>(a, s.tpr);
     return cudaGetLastError();
