@@ -105,7 +105,7 @@ struct GemmParams {
     float* smax;
     int32_t put_smax;              // kFewGrad: leave max |dloss| there
     int32_t add;                   // kDh: add to what is there
-    int32_t direct;                // kDh: the only piece and split, so dh itself leaves
+    int32_t direct;                // kDh, kDw: the only piece and split, so dh or dw itself leaves
     unsigned* status;
     uint64_t timeout_ns;
 };
@@ -634,7 +634,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 for (int c = 0; c < 128; c += 32) {
                     load_acc(v, ta + c);
                     const int col = (int)col0 + c;
-                    if (MODE == kDh && !p.direct) {
+                    if ((MODE == kDh || MODE == kDw) && !p.direct) {
                         store_acc(v, stage_buf, &tmOut, col, (int)row0, ti.split, p.add != 0, n, lane);
                         continue;
                     }
@@ -839,9 +839,9 @@ __global__ void __launch_bounds__(1024) head_scale_kernel(const float* dloss, co
     }
 }
 
-// dh = smax * the sum of the splits' accumulators, 8 columns a thread
-__global__ void __launch_bounds__(256) head_dh_kernel(const float* acc, int splits, int64_t T, int64_t D,
-                                                      const float* smax, __nv_bfloat16* dh, int64_t ld) {
+// dh (or dw) = smax * the sum of the splits' accumulators [splits][T][D], 8 columns a thread
+__global__ void __launch_bounds__(256) head_sum_kernel(const float* acc, int splits, int64_t T, int64_t D,
+                                                      const float* smax, __nv_bfloat16* out, int64_t ld) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, per = D / 8;
     if (i >= T * per) return;
     pdl_wait();
@@ -859,7 +859,7 @@ __global__ void __launch_bounds__(256) head_dh_kernel(const float* acc, int spli
     for (int j = 0; j < 4; j++)
         w[j] = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(v[2 * j] * f)) |
                ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(v[2 * j + 1] * f)) << 16);
-    *reinterpret_cast<uint4*>(dh + t * ld + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(out + t * ld + c) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
@@ -869,14 +869,20 @@ int64_t piece_cols(int64_t tokens, int64_t vocab) {
     const int64_t most = std::max<int64_t>(2048, kPieceBytes / (2 * tokens) / kTile * kTile);
     return std::min(round_up(vocab, kTile), most);
 }
-// dh has few tiles when there are few tokens: its sum over the vocabulary is
-// then split over the idle pairs, at least 8 stages each
-int dh_splits(int64_t tokens, int64_t cols, int64_t piece, int num_sms) {
-    const int64_t tiles = (tokens + kTile - 1) / kTile * ((cols + kTile - 1) / kTile);
-    const int64_t stages = (piece + kSub * kSubK - 1) / (kSub * kSubK);
-    return (int)std::max<int64_t>(1, std::min<int64_t>(num_sms / 2 / tiles, stages / 8));
+// dh has few tiles when there are few tokens, and dw when the vocabulary is
+// small: the sum over K is then split over the idle pairs, at least 8 stages
+// each.  (5180 tokens, 596 x 72: dw in one split kept 3 pairs busy for 24 us.)
+int splits_of(int64_t rows, int64_t cols, int64_t k, int num_sms) {
+    const int64_t tiles = (rows + kTile - 1) / kTile * ((cols + kTile - 1) / kTile);
+    const int64_t stages = (k + kSub * kSubK - 1) / (kSub * kSubK);
+    const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(num_sms / 2 / tiles, stages / 8));
+    const int64_t per = (stages + splits - 1) / splits;
+    return (int)((stages + per - 1) / per);        // those that get any
 }
-
+// of dw: only where the vocabulary is one piece
+int dw_splits(int64_t tokens, int64_t vocab, int64_t cols, int64_t piece, int num_sms) {
+    return piece < vocab ? 1 : splits_of(vocab, cols, tokens, num_sms);
+}
 // dh comes out of one product as it is
 bool dh_direct(int splits, int64_t piece, int64_t vocab) { return splits == 1 && piece >= vocab; }
 
@@ -894,9 +900,9 @@ int64_t head_parts(int64_t tokens, int64_t vocab, int num_sms) {
 size_t head_workspace(int64_t tokens, int64_t vocab, int64_t cols, bool backward, int num_sms) {
     if (!backward) return (size_t)(head_parts(tokens, vocab, num_sms) * tokens * 8 + round_up(tokens * 4, 16));
     const int64_t piece = piece_cols(tokens, vocab);
-    const int splits = dh_splits(tokens, cols, piece, num_sms);
+    const int splits = splits_of(tokens, cols, std::min(piece, vocab), num_sms), dw = dw_splits(tokens, vocab, cols, piece, num_sms);
     return (size_t)(256 + (piece < vocab ? 2 : 1) * tokens * piece * 2 +
-                    (dh_direct(splits, piece, vocab) ? 0 : splits * tokens * cols * 4));
+                    (dh_direct(splits, piece, vocab) ? 0 : splits * tokens * cols * 4) + (dw > 1 ? dw * vocab * cols * 4 : 0));
 }
 
 cudaError_t run_head(const HeadArgs& a, cudaStream_t st) {
@@ -933,18 +939,18 @@ cudaError_t run_head(const HeadArgs& a, cudaStream_t st) {
 // find it themselves.
 cudaError_t run_head_backward(const HeadArgs& a, cudaStream_t st) {
     const int64_t T = a.tokens, V = a.vocab, D = a.cols, piece = piece_cols(T, V);
-    const int splits = dh_splits(T, D, piece, a.num_sms);
+    const int splits = splits_of(T, D, std::min(piece, V), a.num_sms), dw_split = dw_splits(T, V, D, piece, a.num_sms);
     const bool few = T <= kFewTokens, direct = dh_direct(splits, piece, V);
     uint8_t* ws = static_cast<uint8_t*>(a.ws);
     float* smax = reinterpret_cast<float*>(ws);
     uint8_t* g0 = ws + 256;
     float* acc = reinterpret_cast<float*>(g0 + (piece < V ? 2 : 1) * T * piece * 2);
+    float* dw_acc = acc + (direct ? 0 : splits * T * D);
     cudaError_t e = cudaSuccess;
     if (!few) {
         head_scale_kernel<<<1, 1024, 0, st>>>(a.dloss, a.targets, T, V, smax);
         e = cudaGetLastError();
     }
-    int used = 1;
     for (int64_t v0 = 0, i = 0; v0 < V && e == cudaSuccess; v0 += piece, i++) {
         const int64_t n = std::min(piece, V - v0);
         const uint8_t* w = static_cast<const uint8_t*>(a.w) + v0 * a.ldw * 2;
@@ -981,20 +987,24 @@ cudaError_t run_head_backward(const HeadArgs& a, cudaStream_t st) {
             if (!(direct ? tmap::out_2d(&out, a.dh, T, D, a.ld_dh, true) : map_acc(&out, acc, splits, T, D)))
                 return cudaErrorInvalidValue;
             e = gemm<kDh>(p, gp, wp, &out, n, splits, kTile, kTile, kWaitStart, a, st);
-            const int stages = (int)((n + kSub * kSubK - 1) / (kSub * kSubK)), per = (stages + splits - 1) / splits;
-            if (v0 == 0) used = (stages + per - 1) / per;          // the splits that the first piece wrote
         }
         if (e == cudaSuccess && a.dw) {
             p.M = n;
             p.N = D;
-            if (!tmap::out_2d(&out, static_cast<uint8_t*>(a.dw) + v0 * a.ld_dw * 2, n, D, a.ld_dw, true))
+            p.add = 0;
+            p.direct = dw_split == 1;
+            if (!(p.direct ? tmap::out_2d(&out, static_cast<uint8_t*>(a.dw) + v0 * a.ld_dw * 2, n, D, a.ld_dw, true)
+                           : map_acc(&out, dw_acc, dw_split, V, D)))
                 return cudaErrorInvalidValue;
-            e = gemm<kDw>(p, gp, h, &out, T, 1, kTile, kTile, a.dh ? kWaitEnd : kWaitStart, a, st);
+            e = gemm<kDw>(p, gp, h, &out, T, dw_split, kTile, kTile, a.dh ? kWaitEnd : kWaitStart, a, st);
         }
     }
-    if (e == cudaSuccess && a.dh && !direct)
-        e = launch_k(true, head_dh_kernel, dim3((unsigned)((T * (D / 8) + 255) / 256)), 256, 0, st, acc, used, T, D, smax,
-                     static_cast<__nv_bfloat16*>(a.dh), a.ld_dh);
+    const auto sum = [&](const float* from, int n, int64_t rows, void* to, int64_t ld) {
+        return launch_k(true, head_sum_kernel, dim3((unsigned)((rows * (D / 8) + 255) / 256)), 256, 0, st, from, n, rows, D, smax,
+                        static_cast<__nv_bfloat16*>(to), ld);
+    };
+    if (e == cudaSuccess && a.dh && !direct) e = sum(acc, splits, T, a.dh, a.ld_dh);
+    if (e == cudaSuccess && a.dw && dw_split > 1) e = sum(dw_acc, dw_split, V, a.dw, a.ld_dw);
     return e;
 }
 

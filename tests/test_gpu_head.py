@@ -84,6 +84,12 @@ def test_token_counts_around_the_tiles(bsq, T):
         Guard(dw, wbuf).check()
 
 
+@pytest.mark.parametrize("T,V,D", [(5180, 300, 72), (2304, 257, 600), (2048, 2049, 8), (130, 9001, 64)])
+def test_sums_split_over_the_tokens_or_the_vocabulary(bsq, T, V, D):
+    for pad in (0, 8):
+        test_forward_and_gradient(bsq, T, V, D, pad)
+
+
 def test_several_pieces_of_the_vocabulary(bsq):
     # more tokens than one 256 MB piece of the whole vocabulary holds: 3 pieces
     T, V, D = 70001, 5003, 16
