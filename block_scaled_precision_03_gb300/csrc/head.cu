@@ -789,40 +789,62 @@ cudaError_t gemm(GemmParams p, const Operand& a, const Operand& b, const CUtenso
 }
 
 // ------------------------------------------------------- around the products
+// A part of a row's statistics: the maximum m and sum exp(z - m).  NaN sums stay
+// NaN, also beside parts without a number (m = -inf).
+struct Stat {
+    float m, s;
+};
+__device__ __forceinline__ float finite_or_zero(float m) { return m == kNegInf ? 0.0f : m; }
+__device__ __forceinline__ Stat join(Stat a, Stat b) {
+    const float m = fmaxf(a.m, b.m), m0 = finite_or_zero(m);
+    return {m, a.s * exp2_fast((a.m - m0) * kLog2e) + b.s * exp2_fast((b.m - m0) * kLog2e)};
+}
+
 // Joins a row's parts: TT tokens a CTA, the parts dealt to 512 / TT threads
-// each, whose results meet in shared memory in a fixed order.
+// each, eight at a time (one rescaling for the eight), whose results one warp
+// joins.  Bound by latency: what 7 tokens of 50021 columns (1792 parts) wait for.
 template <int TT>
 __global__ void __launch_bounds__(512) head_join_kernel(const float2* part, int64_t parts, int64_t T, int64_t V,
                                                         const float* hit, const int64_t* targets, float* loss,
                                                         float* lse) {
     constexpr int G = 512 / TT;
-    __shared__ float2 joined[G][TT];
+    __shared__ Stat joined[TT][G + 1];
     const int tt = threadIdx.x % TT, g = threadIdx.x / TT;
-    const int64_t t = (int64_t)blockIdx.x * TT + tt;
+    const int64_t first = (int64_t)blockIdx.x * TT;
     pdl_wait();
-    float m = kNegInf, s = 0.0f;
-    if (t < T) {
-#pragma unroll 4
-        for (int64_t i = g; i < parts; i += G) {
-            const float2 v = part[i * T + t];
-            const float n = fmaxf(m, v.x);
-            if (n != kNegInf) s = s * exp2_fast((m - n) * kLog2e) + v.y * exp2_fast((v.x - n) * kLog2e);
-            m = n;
+    Stat own = {kNegInf, 0.0f};
+    if (first + tt < T) {
+        for (int64_t i = g; i < parts; i += 8 * G) {
+            float2 v[8];
+            float m = own.m;
+#pragma unroll
+            for (int u = 0; u < 8; u++)
+                v[u] = i + u * G < parts ? part[(i + u * G) * T + first + tt] : make_float2(kNegInf, 0.0f);
+#pragma unroll
+            for (int u = 0; u < 8; u++) m = fmaxf(m, v[u].x);
+            const float m0 = finite_or_zero(m);
+            float s = own.s * exp2_fast((own.m - m0) * kLog2e);
+#pragma unroll
+            for (int u = 0; u < 8; u++) s += v[u].y * exp2_fast((v[u].x - m0) * kLog2e);
+            own = {m, s};
         }
     }
-    joined[g][tt] = make_float2(m, s);
+    joined[tt][g] = own;
     __syncthreads();
-    if (g != 0 || t >= T) return;
-    for (int i = 1; i < G; i++) {
-        const float2 v = joined[i][tt];
-        const float n = fmaxf(m, v.x);
-        if (n != kNegInf) s = s * exp2_fast((m - n) * kLog2e) + v.y * exp2_fast((v.x - n) * kLog2e);
-        m = n;
+    const int lane = threadIdx.x & 31;
+    for (int k = threadIdx.x >> 5; k < TT && first + k < T; k += 16) {
+        Stat a = {kNegInf, 0.0f};
+        for (int i = lane; i < G; i += 32) a = join(a, joined[k][i]);
+#pragma unroll
+        for (int d = 16; d; d >>= 1)
+            a = join(a, {__shfl_xor_sync(0xffffffffu, a.m, d), __shfl_xor_sync(0xffffffffu, a.s, d)});
+        if (lane == 0) {
+            const float l = a.m + logf(a.s);
+            const int64_t t = first + k, target = targets[t];
+            lse[t] = l;
+            loss[t] = target >= 0 && target < V ? l - hit[t] : 0.0f;
+        }
     }
-    const float l = m + logf(s);
-    lse[t] = l;
-    const int64_t target = targets[t];
-    loss[t] = target >= 0 && target < V ? l - hit[t] : 0.0f;
 }
 
 // max |dloss| over the tokens that count
@@ -924,8 +946,8 @@ cudaError_t run_head(const HeadArgs& a, cudaStream_t st) {
     }
     if (e != cudaSuccess) return e;
     // tokens a CTA: few where there are few, so that more threads share a token's parts
-    const auto k = T >= 4096 ? head_join_kernel<32> : head_join_kernel<8>;
-    const int tt = T >= 4096 ? 32 : 8;
+    const auto k = T >= 4096 ? head_join_kernel<32> : T > kFewTokens ? head_join_kernel<8> : head_join_kernel<2>;
+    const int tt = T >= 4096 ? 32 : T > kFewTokens ? 8 : 2;
     return launch_k(true, k, dim3((unsigned)((T + tt - 1) / tt)), 512, 0, st, p.part, parts, T, a.vocab, p.hit, a.targets,
                     a.loss, a.lse);
 }

@@ -17,12 +17,13 @@
 // The row movements are bound by memory: the gather reads a token's row once
 // and writes it to its k rows, the combine reads the k rows and writes one,
 // the combine's gradient reads dout and the k rows and writes k rows and k dot
-// products.  A group of 1 to 8 warps owns a token; rows on 16-byte boundaries
-// move in 16-byte vectors, others element by element, several in flight.  (Such
-// rows read as two aligned vectors and a shift along the boundaries of the row
-// that is written were slower: 4096 x 8 x 2047 combined in 70 us instead of 53,
-// its gradient with k = 4 in 92 instead of 49, because the warps that hold a
-// row's ends go both ways.)
+// products.  A group of 1 to 8 warps owns a token.  Rows on 16-byte boundaries
+// move in 16-byte vectors, BF16 rows of even widths in pairs, others element by
+// element, several in flight: 4096 x 8 rows of 2046 BF16 are combined in 36.9 us
+// by pairs, 53.4 by elements.  (Odd rows read as two aligned vectors and a shift
+// along the boundaries of the row that is written were slower than elements:
+// 4096 x 8 x 2047 combined in 70 us instead of 53, its gradient with k = 4 in 92
+// instead of 49, because the warps that hold a row's ends go both ways.)
 #include <algorithm>
 #include <type_traits>
 #include "common.cuh"
@@ -300,6 +301,8 @@ __device__ __forceinline__ Place place() {
     return {(int64_t)blockIdx.x * PER + g, at + (int)blockIdx.y * 32 * WPT, 32 * WPT * (int)gridDim.y};
 }
 
+// Bound by the writes: 32768 rows of 7168 BF16 from 4096 in 80 us, 6.6 TB/s; with
+// the sort before it the dispatch takes 88.4 us (0.89 of a copy's rate).
 template <typename T, int VEC, int WPT>
 __global__ void __launch_bounds__(kRowThreads) moe_gather_kernel(const RowArgs a) {
     const Place at = place<WPT>();
@@ -315,7 +318,8 @@ __global__ void __launch_bounds__(kRowThreads) moe_gather_kernel(const RowArgs a
 // launch: every CTA sorts all slots in shared memory (they are few) and moves
 // its own pieces of rows; CTA 0 writes the plan.  The first piece of a row is
 // read before the sort, so the two wait for memory together.  With a.src null
-// it only sorts.
+// it only sorts.  Bound by latency: one token to 8 of 64 experts, 7168 BF16, in
+// 4.1 us, which is what a launch takes.
 template <typename T, int VEC, int THREADS>
 __global__ void __launch_bounds__(THREADS) moe_small_kernel(const SortArgs s, const RowArgs a, int pieces) {
     extern __shared__ int32_t sm[];
@@ -363,7 +367,9 @@ __global__ void __launch_bounds__(THREADS) moe_small_kernel(const SortArgs s, co
 template <int VEC>
 constexpr int kSlots = VEC <= 2 ? 4 : 8;
 
-// out[t] = sum_j weights[t, j] rows[slot_row[t, j]], in the order of j
+// out[t] = sum_j weights[t, j] rows[slot_row[t, j]], in the order of j.  Bound by
+// reading the rows: 4096 x 8 x 7168 BF16 in 85.3 us, 6.2 TB/s (0.93 of a copy's
+// rate); 1021 x 3 x 2047 element by element in 8.2 us, two thirds of it latency.
 template <typename T, int VEC, int WPT, bool WEIGHTED>
 __global__ void __launch_bounds__(kRowThreads) moe_combine_kernel(const RowArgs a) {
     constexpr int UN = VEC <= 2 ? 4 : 1, S = kSlots<VEC>;
@@ -414,7 +420,8 @@ __global__ void __launch_bounds__(kRowThreads) moe_combine_kernel(const RowArgs 
     }
 }
 
-// drows[row] = weights[slot] dout[t], dweights[slot] = dout[t] . rows[row].
+// drows[row] = weights[slot] dout[t], dweights[slot] = dout[t] . rows[row].  Bound
+// by memory: 4096 x 8 x 7168 BF16 in 155 us, 6.4 TB/s (0.95 of a copy's rate).
 // Three CTAs per SM (80 registers): the batch of 32768 x 7168 takes 156 us,
 // with two (98 registers) 209, with four (spills) 176.
 template <typename T, int VEC, int WPT, bool DOT>

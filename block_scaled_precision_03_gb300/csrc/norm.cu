@@ -7,18 +7,22 @@
 //   dx = rstd (g - sum(g) / C - xh sum(g xh) / C),
 //   dw = sum over the rows of dy xh, db = sum over the rows of dy.
 //
-// Both are bound by memory; a row is read once and held in registers as packed
-// 16-byte vectors.  The vectors lie on 16-byte boundaries of x; where rows start
-// off those boundaries (odd widths) their first and last vectors move element
-// by element, dy is read by two aligned loads and a shift where it lies
-// otherwise than x, and an output that lies otherwise is written element by
-// element.
+// Both read a row once and hold it in registers as packed 16-byte vectors; the
+// floor is memory: two passes of the matrix forward, three backward.  With one
+// to four warps per scheduler, what holds the kernels above it is the
+// instructions per row and the latency of its two sums, so most of the choices
+// below save instructions: packed FP32 (two elements an instruction), kernels
+// without tests for the usual widths, and as few threads to a row as its
+// registers allow.
 //
-// Forward: a group of lanes owns a row, one warp up to 512 vectors, so most
-// rows need no barrier at all; many independent rows per SM hide the latency
-// of their two sums.  (A block of 256 threads per row, two barriers each, took
-// 46 us on 8192 x 4096 whatever was prefetched: the barriers, not the loads,
-// held it.)
+// EVEN rows start on 16-byte boundaries and hold whole vectors, in every matrix
+// of the call.  Other rows are walked along the boundaries of x: whole vectors,
+// and the few elements outside them one by one.
+//
+// Forward: a group of lanes owns a row, as few as its registers allow, and many
+// independent rows per SM hide the latency of their sums.  (A block of 256
+// threads per row, two barriers each, took 46 us on 8192 x 4096 whatever was
+// prefetched.)
 //
 // Backward with column sums: a thread keeps its columns' weight and sums in
 // registers over all rows of a persistent CTA; the rows ahead are copied into shared memory
@@ -26,7 +30,13 @@
 // leaves one partial row, and a second kernel (its programmatic dependent)
 // adds them up in a fixed order.  Where columns and threads do not line up
 // (rows that start off 16-byte boundaries) or are too many for the registers,
-// the column sums take a pass of their own.
+// the column sums take a pass of their own.  (Whole blocks of rows for one
+// CTA of 1024 threads, copied in bulk and reduced together, took 49 us instead
+// of 45 on 8192 x 4096: its warps add, reduce and wait all at the same time.)
+//
+// Measured, BF16, of the copy rate: 8192 x 4096 forward 25.2 us (0.80), backward
+// 44.0 us (0.68); FP32 8192 x 2048 26.4 and 39.4 us; 8192 x 2047 24.7 and 54.3;
+// 2048 x 14336 28.7 and 59.3; one row of 7168 4.1 us (a launch).
 #include <algorithm>
 #include "common.cuh"
 #include "internal.h"
@@ -262,6 +272,10 @@ __device__ __forceinline__ void params2(F2 (&f)[VEC / 2], const void* p, int bf1
     for (int e = 0; e < VEC / 2; e++) f[e] = F2(x[2 * e], x[2 * e + 1]);
 }
 
+// Forward of odd rows and of very wide ones.  8192 x 2047 BF16: 24.7 us, 2.7 TB/s,
+// of which the weight and bias, read from shared memory element by element
+// because their place shifts from row to row, are the larger part.  (With a test
+// per element it was 46.5 us and four times the instructions of even rows.)
 template <typename T, int NV, bool EVEN>
 __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a, int tpr) {
     constexpr int VEC = kVec<T>, H = VEC / 2;
@@ -342,7 +356,8 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a, int
     }
 }
 
-// dx alone, a group of lanes per row as above
+// dx alone, a group of lanes per row as above: odd rows, after the pass for the
+// column sums (8192 x 2047 BF16, both: 54.3 us; x and dy are read twice)
 template <typename T, int NV, bool EVEN>
 __global__ void __launch_bounds__(kMaxThreads) norm_dx_kernel(const NormArgs a, int tpr) {
     constexpr int VEC = kVec<T>, H = VEC / 2;
@@ -467,13 +482,14 @@ __device__ __forceinline__ void pair_params(F2 (&f)[NV][VEC / 2], const void* p,
     }
 }
 
-// The two kernels below are bound by the instructions they issue, so the usual
+// The two kernels below are bound by the instructions they issue and their
+// latency (issue slots 47 and 50% busy with 4 warps a scheduler), so the usual
 // widths get a version without tests: FULL says that every lane of every group
 // has all its NV vectors and that groups are whole warps (each then leaves the
 // loop by itself).
 
 // Forward of EVEN rows where many stream through: weight and bias stay in
-// registers.
+// registers.  8192 x 4096 BF16: 25.2 us, 5.3 TB/s (0.80 of a copy's rate).
 template <typename T, int NV, int DEPTH, bool FULL>
 __global__ void __launch_bounds__(kMaxThreads) norm_stream_kernel(const NormArgs a, int tpr) {
     constexpr int VEC = kVec<T>, H = VEC / 2;
@@ -557,6 +573,10 @@ __global__ void __launch_bounds__(kMaxThreads) norm_stream_kernel(const NormArgs
 }
 
 // dx and the column sums of EVEN rows.  COLS: one partial row [2][cols] per CTA.
+// 8192 x 4096 BF16: 44.0 us with the sum of the partial rows (about 5 of them),
+// 4.6 TB/s (0.68).  The registers of the column sums allow 16 warps per SM, and
+// a row's instructions (339 per warp and 16 columns) take most of their time.
+// Two rows ahead: three left room for one CTA fewer per SM.
 template <typename T, int NV, int DEPTH, bool COLS, bool FULL>
 __global__ void __launch_bounds__(kMaxThreads) norm_backward_kernel(const NormArgs a, int tpr) {
     constexpr int VEC = kVec<T>, H = VEC / 2;
@@ -704,7 +724,8 @@ __global__ void __launch_bounds__(kMaxThreads) norm_backward_kernel(const NormAr
 // The same for rows of up to 32 columns a thread (BF16, kLongCols): the column
 // sums alone are 64 registers, so nothing else stays in them.  The weight lies in
 // shared memory as FP32, and dx's pass reads x and dy from the ring again, whose
-// slot is free only after it.  One row at a time and CTA.
+// slot is free only after it.  One row at a time and CTA.  2048 x 14336: 59.3 us
+// (3.0 TB/s; 99.0 with the column sums in a pass of their own).
 constexpr int kLongVecs = 4, kLongDepth = 2;
 constexpr int64_t kLongCols = 8 * kLongVecs * kMaxThreads;
 template <bool COLS>
@@ -816,7 +837,8 @@ __global__ void __launch_bounds__(kMaxThreads) norm_backward_long_kernel(const N
     }
 }
 
-// Adds the partial rows: 32 columns a CTA, the parts dealt to 32 threads each
+// Adds the partial rows (10 MB of 304 CTAs at 4096 columns: about 5 us from L2):
+// 32 columns a CTA, the parts dealt to 32 threads each
 // (blockIdx.y: 0 dweight, 1 dbias).
 __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* ws, int parts, int64_t cols, float* dweight,
                                                            float* dbias) {
@@ -840,6 +862,8 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* ws, int 
 }
 
 // ------------------------------------------------------------------ wide rows
+// Rows that no group of 512 threads holds in registers: a CTA per row, read again
+// for each pass (from L2, mostly).
 __device__ __forceinline__ float2 block_sum(float2 v) {
     __shared__ __align__(16) float part[2 * 2 * kPart];
     __syncthreads();
@@ -898,7 +922,9 @@ __global__ void __launch_bounds__(kWide) norm_wide_kernel(const NormArgs a) {
     }
 }
 
-// column sums of one group of rows (blockIdx.y), VEC columns a thread
+// Column sums of one group of rows (blockIdx.y), VEC columns a thread, where the
+// kernels above cannot keep them: x and dy are read once more (8192 x 2047 BF16:
+// 22 us of the 54.3)
 template <typename T, int VEC>
 __global__ void __launch_bounds__(128) norm_columns_kernel(const NormArgs a) {
     const int64_t c = ((int64_t)blockIdx.x * 128 + threadIdx.x) * VEC;
@@ -1132,12 +1158,12 @@ cudaError_t forward_t(const NormArgs& a, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-template <typename T, bool EVEN>
-cudaError_t dx_e(const NormArgs& a, cudaStream_t st) {
+template <typename T>
+cudaError_t dx_odd(const NormArgs& a, cudaStream_t st) {
     const int64_t n = a.cols / kVec<T>;
-    if (a.rows <= 2 * a.num_sms && n <= 2 * kMaxThreads) return dx_only<T, 2, EVEN>(a, n, st);
-    if (n <= 4 * 32) return dx_only<T, 4, EVEN>(a, n, st);
-    return dx_only<T, 8, EVEN>(a, n, st);
+    if (a.rows <= 2 * a.num_sms && n <= 2 * kMaxThreads) return dx_only<T, 2, false>(a, n, st);
+    if (n <= 4 * 32) return dx_only<T, 4, false>(a, n, st);
+    return dx_only<T, 8, false>(a, n, st);
 }
 template <typename T>
 cudaError_t backward_t(const NormArgs& a, cudaStream_t st) {
@@ -1158,8 +1184,8 @@ cudaError_t backward_t(const NormArgs& a, cudaStream_t st) {
         cudaError_t e = even ? columns<T, VEC>(a, st) : columns<T, 1>(a, st);
         if (e != cudaSuccess) return e;
     }
-    if (even && n <= 8 * kMaxThreads) return dx_e<T, true>(a, st);
-    if (!even && a.cols <= kMaxOddCols) return dx_e<T, false>(a, st);
+    if (even && n <= 8 * kMaxThreads) return dx_only<T, 8, true>(a, n, st);
+    if (!even && a.cols <= kMaxOddCols) return dx_odd<T>(a, st);
     if (even) norm_wide_dx_kernel<T, kVec<T>><<<(unsigned)a.rows, kWide, 0, st>>>(a);
     else norm_wide_dx_kernel<T, 1><<<(unsigned)a.rows, kWide, 0, st>>>(a);
     return cudaGetLastError();

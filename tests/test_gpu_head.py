@@ -159,6 +159,16 @@ def test_nan_and_inf_stay_in_their_rows(bsq):
     assert torch.equal(dh, want)
 
 
+@pytest.mark.parametrize("T", [5, 200])
+@pytest.mark.parametrize("where", [0, 256, 700])
+def test_columns_of_nan_reach_every_loss(bsq, T, where):
+    # whole tiles of logits without a number beside tiles with some
+    h, w, targets, _ = make(T, 1000, 64, 8)
+    w[where:where + 256] = float("nan")
+    loss, lse = bsq.linear_cross_entropy(h, w, targets)
+    assert torch.isnan(lse).all() and torch.isnan(loss).all()
+
+
 def test_gradient_against_differences(bsq):
     T, V, D, step = 19, 101, 40, 1e-4
     h, w, targets, g = make(T, V, D, 7)
