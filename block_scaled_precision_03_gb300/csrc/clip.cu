@@ -102,8 +102,7 @@ __device__ __forceinline__ float squares(const T* g, int64_t n) {
     return s[0] + s[1];
 }
 
-// One read of the gradients: 0.61 GB of one layer in 95 us, 6.4 TB/s (0.96 of a
-// copy's rate).
+// One read of the gradients: 480 MB in 71 us, 6.8 TB/s (a copy's rate).
 template <int CAP>
 __global__ void __launch_bounds__(kThreads) square_sum_kernel(const __grid_constant__ Table<CAP> t, double* partial) {
     double sum = 0.0;
@@ -207,10 +206,10 @@ __device__ __forceinline__ void scale_chunk(const T* g, T* o, int64_t n, Factor&
     }
 }
 
-// A second read and the write: 0.61 GB of one layer in 186 us, 6.5 TB/s (0.98 of a
-// copy's rate); both kernels 282 us.  Of 129 MB of L2 the second read finds next
-// to nothing: reading forwards took 284 us, and keeping the first read's lines with
-// an evict-last policy 278.  Short lists are bound by the two launches (61 tensors,
+// A second read and the write: 480 MB in 146 us, 6.6 TB/s (0.98 of a copy's rate);
+// both kernels on one layer's 610 MB 281 us.  The second read finds next to nothing
+// in the 129 MB of L2: there, reading forwards took 284 us, and keeping the first
+// read's lines with an evict-last policy 278.  Short lists are bound by the two launches (61 tensors,
 // 200003 elements: 8.2 us; one cluster that does it all in one launch took 18).
 template <int CAP>
 __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ Table<CAP> t, Factor factor) {
