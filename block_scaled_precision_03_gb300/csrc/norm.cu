@@ -108,24 +108,45 @@ struct Group {
 // WARPS: the group is known to be whole warps.
 template <bool WARPS = false, int N>
 __device__ __forceinline__ void group_sum(float (&v)[N], const Group& q, float* part, int turn) {
-#pragma unroll
-    for (int d = 16; d; d >>= 1)
-        if (WARPS || d < q.tpr)
-#pragma unroll
-            for (int i = 0; i < N; i++) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
-    if (q.tpr <= 32) return;
     float* mine = part + turn * N * kPart;
-    if ((threadIdx.x & 31) == 0)
+    if (WARPS && N == 2 && q.tpr > 32) {
+        // the lanes' halves take one sum each: 5 shuffles for the two
+        const bool upper = threadIdx.x & 16;
+        float s = upper ? v[N - 1] : v[0];
+        s += __shfl_xor_sync(0xffffffffu, upper ? v[0] : v[N - 1], 16);
 #pragma unroll
-        for (int i = 0; i < N; i++) mine[i * kPart + q.slot] = v[i];
+        for (int d = 8; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+        if ((threadIdx.x & 15) == 0) mine[(upper ? kPart : 0) + q.slot] = s;
+    } else {
+#pragma unroll
+        for (int d = 16; d; d >>= 1)
+            if (WARPS || d < q.tpr)
+#pragma unroll
+                for (int i = 0; i < N; i++) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
+        if (q.tpr <= 32) return;
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int i = 0; i < N; i++) mine[i * kPart + q.slot] = v[i];
+    }
     asm volatile("bar.sync %0, %1;" :: "r"(q.g + 1), "r"(q.tpr) : "memory");
+    mine += q.base;
 #pragma unroll
     for (int i = 0; i < N; i++) {
-        v[i] = 0.0f;
-        for (int k = 0; k < q.quads; k++) {
-            const float4 t = *reinterpret_cast<const float4*>(mine + i * kPart + q.base + 4 * k);
+        const float4 t = *reinterpret_cast<const float4*>(mine + i * kPart);
+        v[i] = (t.x + t.y) + (t.z + t.w);
+    }
+    if (q.quads > 1) {
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const float4 t = *reinterpret_cast<const float4*>(mine + i * kPart + 4);
             v[i] += (t.x + t.y) + (t.z + t.w);
         }
+        for (int k = 2; k < q.quads; k++)
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+                const float4 t = *reinterpret_cast<const float4*>(mine + i * kPart + 4 * k);
+                v[i] += (t.x + t.y) + (t.z + t.w);
+            }
     }
 }
 
