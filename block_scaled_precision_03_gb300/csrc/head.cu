@@ -906,13 +906,25 @@ int64_t piece_cols(int64_t tokens, int64_t vocab) {
     return std::min(round_up(vocab, kTile), most);
 }
 // dh has few tiles when there are few tokens, and dw when the vocabulary is
-// small: the sum over K is then split over the idle pairs, at least 8 stages
-// each.  (5180 tokens, 596 x 72: dw in one split kept 3 pairs busy for 24 us.)
+// small: the sum over K is then split, so that the pairs get equally much.  The
+// estimate: a stage takes 0.55 us, and a split's FP32 tile is written and read.
+// (526 tokens, 35368 x 3656: 45 tiles of dh on 76 pairs, 458 us for the gradient
+// in one split, 418 in 5; 5180 tokens, 596 x 72: dw in one split kept 3 pairs
+// busy for 24 us.)
 int splits_of(int64_t rows, int64_t cols, int64_t k, int num_sms) {
-    const int64_t tiles = (rows + kTile - 1) / kTile * ((cols + kTile - 1) / kTile);
+    const int64_t tiles = (rows + kTile - 1) / kTile * ((cols + kTile - 1) / kTile), pairs = std::max(1, num_sms / 2);
     const int64_t stages = (k + kSub * kSubK - 1) / (kSub * kSubK);
-    const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(num_sms / 2 / tiles, stages / 8));
-    const int64_t per = (stages + splits - 1) / splits;
+    const double split_us = (double)rows * cols * 8 / 6.7e6;
+    int64_t best = 1;
+    double least = 0.0;
+    for (int64_t n = 1; n == 1 || (n * 8 <= stages && n * tiles <= 8 * pairs); n++) {
+        const double us = (double)((tiles * n + pairs - 1) / pairs) * ((stages + n - 1) / n) * 0.55 + (n > 1 ? n * split_us : 0.0);
+        if (n == 1 || us < least) {
+            least = us;
+            best = n;
+        }
+    }
+    const int64_t per = (stages + best - 1) / best;
     return (int)((stages + per - 1) / per);        // those that get any
 }
 // of dw: only where the vocabulary is one piece
