@@ -35,8 +35,8 @@
 // of 45 on 8192 x 4096: its warps add, reduce and wait all at the same time.)
 //
 // Measured, BF16, of the copy rate: 8192 x 4096 forward 25.2 us (0.80), backward
-// 44.0 us (0.68); FP32 8192 x 2048 26.4 and 39.4 us; 8192 x 2047 24.7 and 54.3;
-// 2048 x 14336 28.7 and 59.3; one row of 7168 4.1 us (a launch).
+// 44.0 us (0.68); FP32 8192 x 2048 26.4 and 39.4 us; 8192 x 2047 24.7 and 50.9;
+// 2048 x 14336 28.7 and 57.5; one row of 7168 4.1 us (a launch).
 #include <algorithm>
 #include "common.cuh"
 #include "internal.h"
@@ -378,7 +378,9 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a, int
 }
 
 // dx alone, a group of lanes per row as above: odd rows, after the pass for the
-// column sums (8192 x 2047 BF16, both: 54.3 us; x and dy are read twice)
+// column sums (8192 x 2047 BF16, both: 50.9 us; x and dy are read twice).  It runs
+// beside the sum of the partial rows, which lets it start once the column pass is
+// done: dx may be written over dy.
 template <typename T, int NV, bool EVEN>
 __global__ void __launch_bounds__(kMaxThreads) norm_dx_kernel(const NormArgs a, int tpr) {
     constexpr int VEC = kVec<T>, H = VEC / 2;
@@ -459,6 +461,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_dx_kernel(const NormArgs a, 
         if (!EVEN && mine.edge >= 0)
             R::put(dx, mine.edge, fmaf(d.edge, we, fmaf((x.edge - mean) * rstd, t1, t0)) * rstd);
     }
+    pdl_wait();                                    // the kernel beside which this one ran is done, too
 }
 
 __device__ __forceinline__ void ahead_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -745,7 +748,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_backward_kernel(const NormAr
 // The same for rows of up to 32 columns a thread (BF16, kLongCols): the column
 // sums alone are 64 registers, so nothing else stays in them.  The weight lies in
 // shared memory as FP32, and dx's pass reads x and dy from the ring again, whose
-// slot is free only after it.  One row at a time and CTA.  2048 x 14336: 59.3 us
+// slot is free only after it.  One row at a time and CTA.  2048 x 14336: 57.5 us
 // (3.0 TB/s; 99.0 with the column sums in a pass of their own).
 constexpr int kLongVecs = 4, kLongDepth = 2;
 constexpr int64_t kLongCols = 8 * kLongVecs * kMaxThreads;
@@ -868,6 +871,7 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* ws, int 
     const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     pdl_wait();
+    pdl_launch_dependents();                       // only now: see norm_dx_kernel
     if (!out) return;
     float s = 0.0f;
     if (c < cols)
@@ -945,7 +949,7 @@ __global__ void __launch_bounds__(kWide) norm_wide_kernel(const NormArgs a) {
 
 // Column sums of one group of rows (blockIdx.y), VEC columns a thread, where the
 // kernels above cannot keep them: x and dy are read once more (8192 x 2047 BF16:
-// 22 us of the 54.3)
+// 22 us of the 50.9)
 template <typename T, int VEC>
 __global__ void __launch_bounds__(128) norm_columns_kernel(const NormArgs a) {
     const int64_t c = ((int64_t)blockIdx.x * 128 + threadIdx.x) * VEC;
@@ -968,6 +972,7 @@ __global__ void __launch_bounds__(128) norm_columns_kernel(const NormArgs a) {
             db[e] += fd[e];
         }
     }
+    pdl_launch_dependents();
 #pragma unroll
     for (int e = 0; e < VEC; e++) {
         a.ws[((int64_t)blockIdx.y * 2) * a.cols + c + e] = dw[e];
@@ -1094,8 +1099,7 @@ cudaError_t dx_only(const NormArgs& a, int64_t n, cudaStream_t st) {
     Shape s;
     cudaError_t e = shape(s, norm_dx_kernel<T, NV, EVEN>, a, lanes(n, NV, EVEN ? 4 : 16), [&](const Shape&) { return odd_bytes(a, NV, EVEN); }, 16, row_cta(a, EVEN));
     if (e != cudaSuccess) return e;
-    norm_dx_kernel<T, NV, EVEN><<<s.ctas, s.threads, s.smem, st>>>(a, s.tpr);
-    return cudaGetLastError();
+    return launch_k(a.dweight || a.dbias, norm_dx_kernel<T, NV, EVEN>, dim3(s.ctas), (unsigned)s.threads, s.smem, st, a, s.tpr);
 }
 
 template <typename T, int NV, int DEPTH, bool FULL>
