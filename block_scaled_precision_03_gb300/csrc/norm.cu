@@ -34,8 +34,8 @@
 // CTA of 1024 threads, copied in bulk and reduced together, took 49 us instead
 // of 45 on 8192 x 4096: its warps add, reduce and wait all at the same time.)
 //
-// Measured, BF16, of the copy rate: 8192 x 4096 forward 25.2 us (0.80), backward
-// 44.0 us (0.68); FP32 8192 x 2048 26.4 and 39.4 us; 8192 x 2047 24.7 and 50.9;
+// Measured, BF16, of the copy rate: 8192 x 4096 forward 24.7 us (0.81), backward
+// 43.1 us (0.70); FP32 8192 x 2048 26.4 and 39.4 us; 8192 x 2047 24.7 and 50.9;
 // 2048 x 14336 28.7 and 57.5; one row of 7168 4.1 us (a launch).
 #include <algorithm>
 #include "common.cuh"
@@ -513,7 +513,7 @@ __device__ __forceinline__ void pair_params(F2 (&f)[NV][VEC / 2], const void* p,
 // loop by itself).
 
 // Forward of EVEN rows where many stream through: weight and bias stay in
-// registers.  8192 x 4096 BF16: 25.2 us, 5.3 TB/s (0.80 of a copy's rate).
+// registers.  8192 x 4096 BF16: 24.7 us, 5.4 TB/s (0.81 of a copy's rate).
 template <typename T, int NV, int DEPTH, bool FULL>
 __global__ void __launch_bounds__(kMaxThreads) norm_stream_kernel(const NormArgs a, int tpr) {
     constexpr int VEC = kVec<T>, H = VEC / 2;
@@ -597,9 +597,9 @@ __global__ void __launch_bounds__(kMaxThreads) norm_stream_kernel(const NormArgs
 }
 
 // dx and the column sums of EVEN rows.  COLS: one partial row [2][cols] per CTA.
-// 8192 x 4096 BF16: 44.0 us with the sum of the partial rows (about 5 of them),
-// 4.6 TB/s (0.68).  The registers of the column sums allow 16 warps per SM, and
-// a row's instructions (339 per warp and 16 columns) take most of their time.
+// 8192 x 4096 BF16: 43.1 us with the sum of the partial rows (about 5 of them),
+// 4.7 TB/s (0.70).  The registers of the column sums allow 16 warps per SM, and
+// a row's instructions (some 330 per warp and 16 columns) take most of their time.
 // Two rows ahead: three left room for one CTA fewer per SM.
 template <typename T, int NV, int DEPTH, bool COLS, bool FULL>
 __global__ void __launch_bounds__(kMaxThreads) norm_backward_kernel(const NormArgs a, int tpr) {
