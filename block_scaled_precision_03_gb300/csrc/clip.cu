@@ -258,13 +258,13 @@ cudaError_t run(const ClipArgs& a, cudaStream_t st) {
     const bsq_grad* grads = static_cast<const bsq_grad*>(a.grads);
     const int most = std::min(a.num_sms * 8, kMaxCtas);
     Table<CAP> t;
-    const auto grid = [&] { return dim3((unsigned)std::max(1, std::min(t.first[t.count], most))); };
+    const auto grid = [most](const Table<CAP>& t) { return dim3((unsigned)std::max(1, std::min(t.first[t.count], most))); };
     int parts = 0, last = 0;
     cudaError_t e = cudaSuccess;
     for (int at = 0; at < a.count && e == cudaSuccess;) {
         last = at;
         at = fill(t, grads, at, a.count, a.scale);
-        const dim3 g = grid();
+        const dim3 g = grid(t);
         e = launch_k(false, square_sum_kernel<CAP>, g, kThreads, 0, st, t, a.ws + parts);
         parts += (int)g.x;
     }
@@ -277,7 +277,7 @@ cudaError_t run(const ClipArgs& a, cudaStream_t st) {
         if (last > 0) at = fill(t, grads, at, a.count, a.scale);
         else at = a.count;
         f.norm = first ? a.norm : nullptr;
-        e = launch_k(first, scale_kernel<CAP>, grid(), kThreads, 0, st, t, f);
+        e = launch_k(first, scale_kernel<CAP>, grid(t), kThreads, 0, st, t, f);
     }
     return e;
 }
