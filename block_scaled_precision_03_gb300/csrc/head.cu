@@ -31,8 +31,8 @@
 // (3e-6 -> 4e-7); the gradient's logits, whose g is rounded to BF16, keep one
 // accumulator for all of K.
 //
-// Measured, BF16: the loss of 8192 tokens, 65536 x 4096, in 2.49 ms (1770 TFLOP/s,
-// 0.99 of what a library product holds under the power cap, 0.91 of its burst),
+// Measured, BF16: the loss of 8192 tokens, 65536 x 4096, in 2.46 to 2.59 ms (up to 1790 TFLOP/s,
+// what a library product holds under the power cap, 0.92 of its burst; boxes differ),
 // its gradient in 7.8 ms (1690 TFLOP/s: bound by the power cap, and dh reads w
 // and dw h again); 7 tokens, 50021 x 4096, in 70 us (5.9 TB/s, 0.88 of a copy's
 // rate), the rest the start of the stream, the last tile and the join.  Calls
@@ -119,10 +119,23 @@ struct GemmParams {
     uint64_t timeout_ns;
 };
 
-__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+// Operand descriptors as two words: only the lower one, with the address, changes.
+struct Desc {
+    uint32_t lo, hi;
+    __device__ __forceinline__ explicit Desc(uint64_t d) : lo((uint32_t)d), hi((uint32_t)(d >> 32)) {}
+    __device__ __forceinline__ Desc(uint32_t l, uint32_t h) : lo(l), hi(h) {}
+    __device__ __forceinline__ Desc operator+(uint32_t n) const { return {lo + n, hi}; }
+};
+template <bool ACC>
+__device__ __forceinline__ void mma_bf16(uint32_t d, Desc a, Desc b, uint32_t idesc, uint32_t acc) {
+    if (ACC)
+        asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tmov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+                     "setp.eq.b32 p, 0, 0;\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n\t}"
+                     :: "r"(d), "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tmov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+                     "setp.ne.b32 p, %6, 0;\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n\t}"
+                     :: "r"(d), "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(acc) : "memory");
 }
 // tcgen05 instruction descriptor of kind::f16: bits 4-5 FP32 accumulator,
 // 7-9 and 10-12 BF16 operands, 15 and 16 MN-major A and B, 17-22 N>>3 (left
@@ -451,21 +464,22 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                             break;
                         }
                         tc::fence_after();
-                        const uint64_t ad = ad0 + (uint64_t)(stage * (kOpBytes >> 4));
-                        const uint64_t bd = bd0 + (uint64_t)(stage * (b_bytes >> 4));
+                        const Desc ad = Desc(ad0) + (uint32_t)(stage * (kOpBytes >> 4));
+                        const Desc bd = Desc(bd0) + (uint32_t)(stage * (b_bytes >> 4));
                         const int next = stage + 1 == S ? 0 : stage + 1;
                         const uint32_t next_phase = next == 0 ? phase ^ 1 : phase;
                         if (kb != p.k_stages - 1 || p.mma_last == kMmas) {
                             // the next stage's barrier is tested while this stage's MMAs run
+                            mma_bf16<false>(d, ad, bd, idesc, kb != c0);
 #pragma unroll
-                            for (int m = 0; m < kMmas; m++) {
+                            for (int m = 1; m < kMmas; m++) {
                                 if (m == kMmas - 1) ready = tc::mbar_test(full0 + 8 * next, next_phase);
-                                mma_bf16(d, ad + (m >> 2) * (kSubBytes >> 4) + (m & 3) * a_step,
-                                         bd + (m >> 2) * (sub_b >> 4) + (m & 3) * b_step, idesc, (kb != c0) | (m != 0));
+                                mma_bf16<true>(d, ad + (m >> 2) * (kSubBytes >> 4) + (m & 3) * a_step,
+                                               bd + (m >> 2) * (sub_b >> 4) + (m & 3) * b_step, idesc, 1);
                             }
                         } else {
                             for (int m = 0; m < p.mma_last; m++)
-                                mma_bf16(d, ad + (m >> 2) * (kSubBytes >> 4) + (m & 3) * a_step,
+                                mma_bf16<false>(d, ad + (m >> 2) * (kSubBytes >> 4) + (m & 3) * a_step,
                                          bd + (m >> 2) * (sub_b >> 4) + (m & 3) * b_step, idesc, (kb != c0) | (m != 0));
                             ready = false;
                         }
