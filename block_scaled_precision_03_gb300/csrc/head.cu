@@ -26,10 +26,11 @@
 //
 // The tensor cores' FP32 sums are not rounded to nearest: over K = 4096 the
 // logits came out up to 3e-6 to 6e-6 (relative) too small in magnitude, ten
-// times an FP32 product's error.  For the loss the accumulators are therefore
-// read out every kChunk of K and added up in registers, rounded to nearest
-// (3e-6 -> 4e-7); the gradient's logits, whose g is rounded to BF16, keep one
-// accumulator for all of K.
+// times an FP32 product's error.  For the loss and for the gradient's logits the
+// accumulators are therefore read out every kChunk of K and added up in
+// registers, rounded to nearest (3e-6 -> 4e-7).  The gradient needs it as much as
+// the loss: at the target g = exp(z - lse) - 1 cancels, so an error of 1e-4 in z
+// (a logit of 20) made the entry of a target with 1 - p = 1e-5 ten times too large.
 //
 // Measured, BF16: the loss of 8192 tokens, 65536 x 4096, in 2.46 to 2.59 ms (up to 1790 TFLOP/s,
 // what a library product holds under the power cap, 0.92 of its burst; boxes differ),
@@ -71,7 +72,7 @@ constexpr int kMaxStages = 6;                       // few tokens: as many as fi
 constexpr int kFewTokens = 128;
 constexpr int kFewTable = kFewTokens * 12;          // their lse, ratio and target
 constexpr int kFewOut = kFewTable + 8 * 2048;       // and 32 rows by 16 tokens for each warp of the epilogue
-// Stages (K = 512) that one accumulator sums for the loss.  Against 64 bits, 1024
+// Stages (K = 512) that one accumulator sums for the logits.  Against 64 bits, 1024
 // x 20000 x 4096: 3.2e-7 (2 stages 1.6e-7, 8 6.7e-7; a plain FP32 product
 // 6.8e-7); the batch takes 2.46 ms with 4 or 8, 2.59 with 2.
 constexpr int kChunk = 4;
@@ -332,7 +333,10 @@ __device__ __forceinline__ void few_tokens(const GemmParams& p, float* lse, floa
 // 151 to 161 us, tensor pipes 76 to 83% busy (few tokens: by reading w, 6.1 TB/s).
 // One thread issues all MMAs, about 88 cycles each; with 256 columns an MMA
 // takes longer than that.
-template <int MODE>
+// LONG: a tile's sum over K takes several accumulators, which the epilogue adds up in
+// registers.  Without it a thread keeps 32 columns at a time: a shorter program with
+// half the registers, which short calls run once.
+template <int MODE, bool LONG>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                  const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ GemmParams p) {
@@ -611,21 +615,56 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             }
             const bool live = row0 < p.M && (MODE == kStats || col0 < p.N);
             const uint32_t ta0 = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * 128);
-            if (MODE == kStats) {
-                float z[128] = {};
-                bool ok = true;
-                for (int c0 = ti.k0; c0 < ti.k1; c0 += p.chunk, ++iter) {
-                    ok = wait(tfull0 + 8 * (iter & 1), (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns);
-                    if (!ok) break;
-                    tc::fence_after();
+            // 32 columns of the product, from the tile's column c on, leave
+            const auto leave = [&](float (&v)[32], int c) {
+                const int col = (int)col0 + c;
+                if ((MODE == kDh || MODE == kDw) && !p.direct) {
+                    store_acc(v, stage_buf, &tmOut, col, (int)row0, ti.split, p.add != 0, n, lane);
+                    return;
+                }
+                if (MODE == kGrad) {
+                    // ratio 0 (a token that does not count) gives 0 whatever its logits
+#pragma unroll
+                    for (int j = 0; j < 32; j++) {
+                        const float g = exp2_fast((v[j] - lse) * kLog2e) - (target == c + j ? 1.0f : 0.0f);
+                        v[j] = ratio == 0.0f ? 0.0f : g;
+                    }
+                }
+                store_bf16(v, MODE == kGrad ? ratio : smax, stage_buf, &tmOut, col, (int)row0, n, lane);
+            };
+            if constexpr (!LONG) {
+                const int buf = iter & 1;
+                if (!wait(tfull0 + 8 * buf, (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns)) break;
+                tc::fence_after();
+                ++iter;
+                if (live)
+#pragma unroll 1
+                    for (int c = 0; c < 128; c += 32) {
+                        float v[32];
+                        load_acc(v, ta0 + (uint32_t)(buf * kTile + c));
+                        leave(v, c);
+                    }
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_cluster(tempty_c0 + 8 * buf);
+                continue;
+            }
+            float z[128] = {};
+            bool ok = true;
+            for (int c0 = ti.k0; c0 < ti.k1; c0 += p.chunk, ++iter) {
+                ok = wait(tfull0 + 8 * (iter & 1), (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns);
+                if (!ok) break;
+                tc::fence_after();
+                if (MODE == kStats || live)
 #pragma unroll
                     for (int c = 0; c < 128; c += 16) add_acc(z + c, ta0 + (uint32_t)((iter & 1) * kTile + c));
-                    tc::fence_before();
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive_cluster(tempty_c0 + 8 * (iter & 1));
-                }
-                if (!ok) break;
-                if (!live) continue;
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_cluster(tempty_c0 + 8 * (iter & 1));
+            }
+            if (!ok) break;
+            if (!live) continue;
+            if constexpr (MODE == kStats) {
                 const int cols = (int)min((int64_t)128, p.N - col0);       // 0 or less: an empty part
                 if (cols < 128)
 #pragma unroll
@@ -647,37 +686,15 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 #pragma unroll
                 for (int j = 0; j < 128; j++) s[j & 3] += exp2_fast((z[j] - m0) * kLog2e);
                 if (row < p.M) p.part[((int64_t)2 * ti.nt + half) * p.M + row] = make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
-                continue;
-            }
-            const int buf = iter & 1;
-            if (!wait(tfull0 + 8 * buf, (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns)) break;
-            tc::fence_after();
-            ++iter;
-            const uint32_t ta = ta0 + (uint32_t)(buf * kTile);
-            float v[32];
-            if (live) {
-                // ratio 0 (a token that does not count) gives 0 whatever its logits
-#pragma unroll 1
-                for (int c = 0; c < 128; c += 32) {
-                    load_acc(v, ta + c);
-                    const int col = (int)col0 + c;
-                    if ((MODE == kDh || MODE == kDw) && !p.direct) {
-                        store_acc(v, stage_buf, &tmOut, col, (int)row0, ti.split, p.add != 0, n, lane);
-                        continue;
-                    }
-                    if (MODE == kGrad) {
+            } else {
 #pragma unroll
-                        for (int j = 0; j < 32; j++) {
-                            const float g = exp2_fast((v[j] - lse) * kLog2e) - (target == c + j ? 1.0f : 0.0f);
-                            v[j] = ratio == 0.0f ? 0.0f : g;
-                        }
-                    }
-                    store_bf16(v, MODE == kGrad ? ratio : smax, stage_buf, &tmOut, col, (int)row0, n, lane);
+                for (int c = 0; c < 128; c += 32) {
+                    float v[32];
+#pragma unroll
+                    for (int j = 0; j < 32; j++) v[j] = z[c + j];
+                    leave(v, c);
                 }
             }
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive_cluster(tempty_c0 + 8 * buf);
         }
         if (lane == 0) tc::bulk_wait_all();
     }
@@ -779,6 +796,17 @@ int stream_rows(int64_t vocab, int num_sms) {
     }
     return best;
 }
+template <int MODE, bool LONG>
+cudaError_t launch_gemm(const GemmParams& p, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& out, int pairs,
+                        cudaStream_t st) {
+    static bool attr_done = false;
+    if (!attr_done) {
+        cudaError_t e = cudaFuncSetAttribute(head_gemm_kernel<MODE, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        attr_done = true;
+    }
+    return launch_k(p.wait != kWaitLaunch, head_gemm_kernel<MODE, LONG>, dim3(2 * pairs), kGemmThreads, kSmem, st, ta, tb, out, p);
+}
 template <int MODE>
 cudaError_t gemm(GemmParams p, const Operand& a, const Operand& b, const CUtensorMap* out, int64_t K, int splits,
                  int tile_m, int tile_n, int wait, const HeadArgs& args, cudaStream_t st) {
@@ -788,7 +816,7 @@ cudaError_t gemm(GemmParams p, const Operand& a, const Operand& b, const CUtenso
         return cudaErrorInvalidValue;
     p.tile_n = tile_n;
     p.k_stages = (int32_t)((K + kSub * kSubK - 1) / (kSub * kSubK));
-    p.chunk = MODE == kStats || MODE == kFewStats ? kChunk : p.k_stages;
+    p.chunk = MODE == kDh || MODE == kDw ? p.k_stages : kChunk;
     p.mma_last = (int32_t)((K - (int64_t)(p.k_stages - 1) * kSub * kSubK + 15) / 16);
     p.tile_m = tile_m;
     p.b_bytes = kSub * (tile_n / 2) * kSubK * 2;
@@ -804,15 +832,11 @@ cudaError_t gemm(GemmParams p, const Operand& a, const Operand& b, const CUtenso
     p.wait = wait;
     p.status = args.status;
     p.timeout_ns = args.timeout_ns;
-    static bool attr_done = false;
-    if (!attr_done) {
-        cudaError_t e = cudaFuncSetAttribute(head_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-        if (e != cudaSuccess) return e;
-        attr_done = true;
-    }
     const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(args.num_sms / 2, total));
     choose_raster(p, K, pairs);
-    return launch_k(wait != kWaitLaunch, head_gemm_kernel<MODE>, dim3(2 * pairs), kGemmThreads, kSmem, st, ta, tb, out ? *out : ta, p);
+    if constexpr (MODE == kGrad || MODE == kDh || MODE == kDw)
+        if (p.split_stages <= p.chunk) return launch_gemm<MODE, false>(p, ta, tb, out ? *out : ta, pairs, st);
+    return launch_gemm<MODE, true>(p, ta, tb, out ? *out : ta, pairs, st);
 }
 
 // ------------------------------------------------------- around the products

@@ -1,0 +1,66 @@
+"""How exact the linear cross entropy and its gradient are, with bounds near
+what their sums can hold: the K = 512 read-out of the tensor cores' sums in
+the loss and in the gradient's logits."""
+import pytest
+import torch
+
+from _ops_ref import U, UB, assert_close
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+# A tensor core's FP32 sum drops less than one unit in the last place at each of the 32 additions
+# (16 products each) of K = 512.  Over terms of one sign and like size the sum after j of them is
+# j / 32 of the whole, so what is lost is below sum_j 2^-23 j / 32 = 16.5 * 2^-23 of the whole:
+# 2.0e-6.  (One accumulator for K = 4096, 256 additions, loses up to eight times that.)
+CHUNK = 16.5 * 2.0 ** -23
+
+
+@pytest.fixture(scope="module")
+def bsq():
+    import block_scaled_precision_03_gb300 as b
+    b.lib()
+    return b
+
+
+@pytest.mark.parametrize("T", [40, 300])
+def test_loss_of_long_sums_of_one_sign(bsq, T):
+    # every logit is a sum of 4096 positive products: a bias of the sum is a bias of lse
+    V, D = 333, 4096
+    g = torch.Generator(device="cuda").manual_seed(T)
+    h = (torch.rand((T, D), generator=g, device="cuda") + 0.5).to(BF)
+    w = ((torch.rand((V, D), generator=g, device="cuda") + 0.5) / 64).to(BF)
+    targets = torch.randint(0, V, (T,), generator=g, device="cuda")
+    _, lse = bsq.linear_cross_entropy(h, w, targets)
+    z = h.double() @ w.double().T
+    want = torch.logsumexp(z, 1)
+    # the chunk's loss, 8 chunks added in FP32, the parts' exponentials and sums (64 U), the sum m + log s
+    tol = (CHUNK + 8 * U) * z.amax(1) + 64 * U + U * want.abs()
+    assert_close(lse, want, tol, "lse")
+
+
+@pytest.mark.parametrize("T", [40, 300])
+def test_gradient_of_confident_targets(bsq, T):
+    # 1 - p of the target from 1e-3 to 1e-6: p - 1 cancels, so an error of the logit of 1e-5 is an
+    # error of the gradient's largest entry of as much or more
+    V, D = 2000, 4096
+    g = torch.Generator(device="cuda").manual_seed(T)
+    w = (torch.randn((V, D), generator=g, device="cuda") * D ** -0.5).to(BF)
+    targets = torch.randperm(V, generator=g, device="cuda")[:T]
+    left = torch.logspace(-3, -6, T, device="cuda")                # 1 - p
+    h = ((V / left).log()[:, None] * w[targets].float()).to(BF)
+    _, lse = bsq.linear_cross_entropy(h, w, targets)
+    dh, dw = bsq.linear_cross_entropy_backward(h, w, targets, lse, torch.ones(T, device="cuda"))
+    hd, wd = h.double(), w.double()
+    z, mag = hd @ wd.T, hd.abs() @ wd.abs().T
+    far = z - lse.double()[:, None]
+    p = far.exp()
+    gr = p - torch.nn.functional.one_hot(targets, V)
+    # the logit (chunks, and 8 of them added), z - lse and the exponential (4 U of the argument, 8 U),
+    # the rounding of g to BF16
+    dg = p * ((CHUNK + 8 * U) * mag + 4 * U * far.abs() + 8 * U) + (UB + 4 * U) * gr.abs()
+    long = 1e-5                                                     # of dh's and dw's own sums, as in the other tests
+    want, tol = gr @ wd, dg @ wd.abs() + long * (gr.abs() @ wd.abs())
+    assert_close(dh, want, 1.01 * tol + 1.01 * UB * want.abs(), "dh")
+    want, tol = gr.T @ hd, dg.T @ hd.abs() + long * (gr.abs().T @ hd.abs())
+    assert_close(dw, want, 1.01 * tol + 1.01 * UB * want.abs(), "dw")
