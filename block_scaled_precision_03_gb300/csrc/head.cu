@@ -31,6 +31,7 @@
 // registers, rounded to nearest (3e-6 -> 4e-7).  The gradient needs it as much as
 // the loss: at the target g = exp(z - lse) - 1 cancels, so an error of 1e-4 in z
 // (a logit of 20) made the entry of a target with 1 - p = 1e-5 ten times too large.
+// dh and dw read theirs out every kSumChunk.
 //
 // Measured, BF16: the loss of 8192 tokens, 65536 x 4096, in 2.46 to 2.59 ms (up to 1790 TFLOP/s,
 // what a library product holds under the power cap, 0.92 of its burst; boxes differ),
@@ -76,6 +77,11 @@ constexpr int kFewOut = kFewTable + 8 * 2048;       // and 32 rows by 16 tokens 
 // x 20000 x 4096: 3.2e-7 (2 stages 1.6e-7, 8 6.7e-7; a plain FP32 product
 // 6.8e-7); the batch takes 2.46 ms with 4 or 8, 2.59 with 2.
 constexpr int kChunk = 4;
+// and for dh and dw (K = 4096), whose results are rounded to BF16: a sum loses some 6e-6,
+// whatever the number of tokens or columns.  (In one accumulator dw over 200003 tokens
+// came out 1.2e-3 too small, dh over 131072 columns 5.8e-4.)  The gradient of the batch
+// takes 7.6 to 7.7 ms with 16 or 32, 8.0 with 4.
+constexpr int kSumChunk = 32;
 constexpr int kSubBytes = 128 * kSubK * 2;          // one CTA's 128 rows of an operand, one sub-step
 constexpr int kOpBytes = kSub * kSubBytes;
 constexpr int kMmas = 4 * kSub;                     // per stage
@@ -816,7 +822,7 @@ cudaError_t gemm(GemmParams p, const Operand& a, const Operand& b, const CUtenso
         return cudaErrorInvalidValue;
     p.tile_n = tile_n;
     p.k_stages = (int32_t)((K + kSub * kSubK - 1) / (kSub * kSubK));
-    p.chunk = MODE == kDh || MODE == kDw ? p.k_stages : kChunk;
+    p.chunk = MODE == kDh || MODE == kDw ? kSumChunk : kChunk;
     p.mma_last = (int32_t)((K - (int64_t)(p.k_stages - 1) * kSub * kSubK + 15) / 16);
     p.tile_m = tile_m;
     p.b_bytes = kSub * (tile_n / 2) * kSubK * 2;

@@ -1,6 +1,8 @@
 """How exact the linear cross entropy and its gradient are, with bounds near
 what their sums can hold: the K = 512 read-out of the tensor cores' sums in
-the loss and in the gradient's logits."""
+the loss and in the gradient's logits, and long sums into dh and dw."""
+import math
+
 import pytest
 import torch
 
@@ -64,3 +66,58 @@ def test_gradient_of_confident_targets(bsq, T):
     assert_close(dh, want, 1.01 * tol + 1.01 * UB * want.abs(), "dh")
     want, tol = gr.T @ hd, dg.T @ hd.abs() + long * (gr.abs().T @ hd.abs())
     assert_close(dw, want, 1.01 * tol + 1.01 * UB * want.abs(), "dw")
+
+
+def mean_bias(got, want):
+    """Mean relative error, and five standard deviations of what BF16 outputs rounded to nearest leave
+    of it (each at most UB off, uniformly: UB / sqrt(3))."""
+    return float((got.double() / want - 1).mean()), 5 * UB / math.sqrt(3 * got.numel())
+
+
+def g_rounded(h, w, lse):
+    """exp(z - lse) as it enters the products: in BF16 (dloss is 1 here, so nothing is scaled)."""
+    return (h.double() @ w.double().T - lse.double()[:, None]).exp().to(BF).double()
+
+
+# dh and dw keep an accumulator for K = 4096 at most: 256 additions, sum_j 2^-23 j / 256
+LONG = 128.5 * 2.0 ** -23
+
+
+def test_dw_over_many_tokens_is_not_biased(bsq):
+    # dw[v] is a sum over 200003 tokens of terms of one sign (the target's column is left out)
+    T, V, D = 200003, 2100, 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    h = (torch.rand((T, D), generator=g, device="cuda") + 0.5).to(BF)
+    w = (torch.randn((V, D), generator=g, device="cuda") * 0.02).to(BF)
+    targets = torch.zeros(T, dtype=torch.int64, device="cuda")
+    _, lse = bsq.linear_cross_entropy(h, w, targets)
+    dw = torch.empty_like(w)
+    bsq.linear_cross_entropy_backward_into(h, w, targets, lse, torch.ones(T, device="cuda"), None, dw)
+    want = 0
+    for at in range(0, T, 32768):
+        want = want + g_rounded(h[at:at + 32768], w, lse[at:at + 32768]).T @ h[at:at + 32768].double()
+    bias, noise = mean_bias(dw[1:], want[1:])
+    # the logits (their |h w| sum to 1.3 here), the sum's own loss, its 49 chunks added in FP32
+    assert abs(bias) < noise + 1.3 * CHUNK + LONG + U * math.sqrt(49), bias
+
+
+def test_dh_over_a_large_vocabulary_is_not_biased(bsq):
+    # dh[t] is a sum over 131072 columns, of one sign (the target's row of w is 0); 76 tiles, so that
+    # the sum is not split.  128 of its rows are looked at.  w's columns differ in size, so that dh's
+    # elements do not lie within one rounding step of each other.
+    T, V, D = 1024, 131072, 4864
+    g = torch.Generator(device="cuda").manual_seed(2)
+    h = (torch.randn((T, D), generator=g, device="cuda") * 0.02).to(BF)
+    size = (1 + torch.rand(D, generator=g, device="cuda")) / 96
+    w = ((torch.rand((V, D), generator=g, device="cuda") + 0.5) * size).to(BF)
+    w[0] = 0
+    targets = torch.zeros(T, dtype=torch.int64, device="cuda")
+    _, lse = bsq.linear_cross_entropy(h, w, targets)
+    dh = torch.empty_like(h)
+    bsq.linear_cross_entropy_backward_into(h, w, targets, lse, torch.ones(T, device="cuda"), dh, None)
+    want = 0
+    for at in range(0, V, 8192):
+        want = want + g_rounded(h[:128], w[at:at + 8192], lse[:128]) @ w[at:at + 8192].double()
+    bias, noise = mean_bias(dh[:128], want)
+    # the logits (their |h w| sum to 1.3 here), the sum's own loss, its 32 chunks added in FP32
+    assert abs(bias) < noise + 1.3 * CHUNK + LONG + U * math.sqrt(32), bias
