@@ -6,8 +6,8 @@
 //   lse = M + log sum_i s_i exp(m_i - M),  M = max_i m_i,
 // and loss = lse - z[target].  Backward, a piece of the vocabulary at a time:
 // the logits' tile again, g = ratio (exp(z - lse) - [v = target]) in BF16 with
-// ratio = dloss / max |dloss|, then dh += g w (FP32 between pieces) and
-// dw = g^T h, both times max |dloss| in FP32.  With the usual dloss (one value
+// ratio = dloss / max |dloss| (of the finite ones), then dh += g w (FP32 between
+// pieces) and dw = g^T h, both times max |dloss| in FP32.  With the usual dloss (one value
 // for every token that counts) ratio is 1, so the one large entry of a row of
 // g, the target's, loses nothing to BF16.
 //
@@ -42,6 +42,7 @@
 // four launches in a chain, each with some 3000 cycles of set-up and first loads
 // and as many at the end.
 #include <algorithm>
+#include <cfloat>
 #include <cuda.h>
 #include "common.cuh"
 #include "epilogue.cuh"
@@ -301,7 +302,8 @@ __device__ __noinline__ void drain_loads(uint32_t full0, int stages, int n_own, 
     }
 }
 
-// max |dloss| over the tokens that count, of this warp's lanes' tokens lane, lane + step, ...
+// The largest finite |dloss| over the tokens that count, of this warp's lanes' tokens lane, lane + step, ...
+// (A NaN or an infinity must not scale the other tokens' rows: it stays in its own, as ratio.)
 __device__ __forceinline__ float largest_dloss(const float* dloss, const int64_t* targets, int64_t T, int64_t V, int64_t first,
                                                int step) {
     float m = 0.0f;
@@ -309,12 +311,15 @@ __device__ __forceinline__ float largest_dloss(const float* dloss, const int64_t
     for (int64_t t = first; t < T; t += step) {
         const int64_t id = targets[t];
         const float d = fabsf(dloss[t]);
-        if (id >= 0 && id < V) m = fmaxf(m, d);
+        if (id >= 0 && id < V && d <= FLT_MAX) m = fmaxf(m, d);
     }
 #pragma unroll
     for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     return m;
 }
+
+// what is taken out of dloss: 1 where there is nothing to take out, so that dloss / it is dloss
+__device__ __forceinline__ float dloss_scale(float largest) { return largest > 0.0f ? largest : 1.0f; }
 
 // The tokens' table of the few-token kernels, filled by the epilogue's warps
 template <int MODE>
@@ -322,7 +327,7 @@ __device__ __forceinline__ void few_tokens(const GemmParams& p, float* lse, floa
     const int t = threadIdx.x - 64;
     float smax = 0.0f;
     if (MODE == kFewGrad) {
-        smax = largest_dloss(p.dloss, p.targets, p.N, p.vocab, t & 31, 32);
+        smax = dloss_scale(largest_dloss(p.dloss, p.targets, p.N, p.vocab, t & 31, 32));
         if (p.put_smax && blockIdx.x == 0 && t == 0) *p.smax = smax;
     }
     if (t < kFewTokens) {
@@ -330,7 +335,7 @@ __device__ __forceinline__ void few_tokens(const GemmParams& p, float* lse, floa
         const bool counts = id >= 0 && id < p.vocab;
         target[t] = counts && id >= p.col0 && id - p.col0 < p.M ? (int)(id - p.col0) : -1;
         lse[t] = MODE == kFewGrad && counts ? p.lse[t] : 0.0f;
-        ratio[t] = MODE == kFewGrad && counts && smax > 0.0f ? p.dloss[t] / smax : 0.0f;
+        ratio[t] = MODE == kFewGrad && counts ? p.dloss[t] / smax : 0.0f;
     }
     asm volatile("bar.sync 1, %0;" :: "n"(32 * kEpiWarps) : "memory");
 }
@@ -611,7 +616,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             if ((MODE == kStats || MODE == kGrad) && row < p.M) {
                 const int64_t id = p.targets[row];
                 if (id >= 0 && id < p.vocab) {
-                    if (MODE == kGrad && smax > 0.0f) {
+                    if (MODE == kGrad) {
                         lse = p.lse[row];
                         ratio = p.dloss[row] / smax;
                     }
@@ -904,7 +909,7 @@ __global__ void __launch_bounds__(512) head_join_kernel(const float2* part, int6
     }
 }
 
-// max |dloss| over the tokens that count
+// What is taken out of dloss: its largest finite magnitude over the tokens that count
 __global__ void __launch_bounds__(1024) head_scale_kernel(const float* dloss, const int64_t* targets, int64_t T, int64_t V,
                                                           float* smax) {
     __shared__ float part[32];
@@ -914,7 +919,7 @@ __global__ void __launch_bounds__(1024) head_scale_kernel(const float* dloss, co
     __syncthreads();
     if (threadIdx.x == 0) {
         for (int w = 1; w < 32; w++) m = fmaxf(m, part[w]);
-        *smax = m;
+        *smax = dloss_scale(m);
     }
 }
 

@@ -390,7 +390,10 @@ bsq_status bsq_linear_cross_entropy(const void* h, int64_t ldh, const void* w, i
  * are computed again, a piece of the vocabulary at a time.  g enters the two
  * products in BF16, with the largest |dloss| taken out of it and put back in
  * FP32.  dh, dw on 16-byte boundaries, ld_dh and ld_dw multiples of 8;
- * dloss: DEVICE float[tokens], finite. */
+ * dloss: DEVICE float[tokens].  A NaN or infinite dloss[t] of a token that
+ * counts makes dh[t] and dw NaN or infinite, as the formula says, and leaves
+ * the other rows of dh as they are.  A token that does not count enters dw
+ * with g = 0, so its h has to be finite. */
 bsq_status bsq_linear_cross_entropy_backward(const void* h, int64_t ldh, const void* w, int64_t ldw,
                                              const int64_t* targets, int64_t tokens, int64_t vocab, int64_t cols,
                                              const float* lse, const float* dloss, void* dh, int64_t ld_dh, void* dw,

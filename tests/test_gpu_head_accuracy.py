@@ -1,6 +1,7 @@
 """How exact the linear cross entropy and its gradient are, with bounds near
 what their sums can hold: the K = 512 read-out of the tensor cores' sums in
-the loss and in the gradient's logits, and long sums into dh and dw."""
+the loss and in the gradient's logits, long sums into dh and dw; and values of
+dloss that are not finite."""
 import math
 
 import pytest
@@ -121,3 +122,32 @@ def test_dh_over_a_large_vocabulary_is_not_biased(bsq):
     bias, noise = mean_bias(dh[:128], want)
     # the logits (their |h w| sum to 1.3 here), the sum's own loss, its 32 chunks added in FP32
     assert abs(bias) < noise + 1.3 * CHUNK + LONG + U * math.sqrt(32), bias
+
+
+@pytest.mark.parametrize("T", [9, 300])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_dloss_that_is_not_finite(bsq, T, bad):
+    g = torch.Generator(device="cuda").manual_seed(T)
+    V, D = 500, 64
+    h = torch.randn((T, D), generator=g, device="cuda").to(BF)
+    w = (torch.randn((V, D), generator=g, device="cuda") / 8).to(BF)
+    targets = torch.randint(0, V, (T,), generator=g, device="cuda")
+    targets[2] = -100
+    _, lse = bsq.linear_cross_entropy(h, w, targets)
+    # every token's (one loss scale for all): the gradient says so
+    dh, dw = bsq.linear_cross_entropy_backward(h, w, targets, lse, torch.full((T,), bad, device="cuda"))
+    counts = torch.ones(T, dtype=torch.bool, device="cuda")
+    counts[2] = False
+    assert not torch.isfinite(dh[counts]).any() and (dh[2] == 0).all() and not torch.isfinite(dw).any()
+    # one token's: its row of dh and dw, not the other rows
+    dloss = torch.rand(T, generator=g, device="cuda")
+    dloss[4] = 0
+    clean = bsq.linear_cross_entropy_backward(h, w, targets, lse, dloss)
+    dloss[4] = bad
+    dh, dw = bsq.linear_cross_entropy_backward(h, w, targets, lse, dloss)
+    assert not torch.isfinite(dh[4]).any() and not torch.isfinite(dw).any()
+    dh[4] = clean[0][4]
+    assert torch.equal(dh, clean[0])
+    # that of a token that does not count is nobody's
+    dloss[4], dloss[2] = 0, bad
+    assert all(torch.equal(a, b) for a, b in zip(bsq.linear_cross_entropy_backward(h, w, targets, lse, dloss), clean))
