@@ -167,6 +167,9 @@ __device__ __forceinline__ float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// The maximum as it is taken out of the exponentials.  An infinite one is not: exp(-inf) is 0 and
+// exp(inf) is inf as they are, while inf - inf would be NaN.
+__device__ __forceinline__ float finite_or_zero(float m) { return fabsf(m) == INFINITY ? 0.0f : m; }
 // An element of g; ratio 0 (a token that does not count) gives 0 whatever its logits
 __device__ __forceinline__ float few_g(float z, float lse, float ratio, bool target) {
     const float g = exp2_fast((z - lse) * kLog2e) - (target ? 1.0f : 0.0f);
@@ -576,7 +579,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                         }
                         float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                        const float m0 = m == kNegInf ? 0.0f : m;
+                        const float m0 = finite_or_zero(m);
 #pragma unroll
                         for (int i = 0; i < 16; i++) s4[i & 3] += exp2_fast((x[i] - m0) * kLog2e);
                         float sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
@@ -692,7 +695,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 // z - m is formed first: a product with log2(e) before it would round away the
                 // difference of large logits
-                const float m0 = m == kNegInf ? 0.0f : m;
+                const float m0 = finite_or_zero(m);
                 float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int j = 0; j < 128; j++) s[j & 3] += exp2_fast((z[j] - m0) * kLog2e);
@@ -856,7 +859,6 @@ cudaError_t gemm(GemmParams p, const Operand& a, const Operand& b, const CUtenso
 struct Stat {
     float m, s;
 };
-__device__ __forceinline__ float finite_or_zero(float m) { return m == kNegInf ? 0.0f : m; }
 __device__ __forceinline__ Stat join(Stat a, Stat b) {
     const float m = fmaxf(a.m, b.m), m0 = finite_or_zero(m);
     return {m, a.s * exp2_fast((a.m - m0) * kLog2e) + b.s * exp2_fast((b.m - m0) * kLog2e)};

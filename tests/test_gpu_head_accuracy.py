@@ -1,7 +1,7 @@
 """How exact the linear cross entropy and its gradient are, with bounds near
 what their sums can hold: the K = 512 read-out of the tensor cores' sums in
 the loss and in the gradient's logits, long sums into dh and dw; and values of
-dloss that are not finite."""
+dloss and logits that are not finite."""
 import math
 
 import pytest
@@ -151,3 +151,26 @@ def test_dloss_that_is_not_finite(bsq, T, bad):
     # that of a token that does not count is nobody's
     dloss[4], dloss[2] = 0, bad
     assert all(torch.equal(a, b) for a, b in zip(bsq.linear_cross_entropy_backward(h, w, targets, lse, dloss), clean))
+
+
+@pytest.mark.parametrize("T", [5, 200])
+def test_infinite_logits(bsq, T):
+    # exp(inf) is inf: lse = inf, the loss of another target inf, that of the column itself inf - inf
+    V, D = 1000, 64
+    g = torch.Generator(device="cuda").manual_seed(T)
+    h = torch.randn((T, D), generator=g, device="cuda").to(BF)
+    w = torch.randn((V, D), generator=g, device="cuda").to(BF)
+    targets = torch.randint(0, V, (T,), generator=g, device="cuda")
+    h[:, 0] = 1
+    w[700, 0] = -float("inf")                       # a logit of -inf: exp is 0
+    targets[1], targets[2] = 700, 0
+    want = torch.logsumexp(h.double() @ w.double().T, 1)
+    loss, lse = bsq.linear_cross_entropy(h, w, targets)
+    assert torch.isfinite(lse).all() and (lse.double() - want).abs().max() < 1e-4
+    assert loss[1] == float("inf") and torch.isfinite(loss[targets != 700]).all()
+    w[300, 0] = float("inf")                        # and one of +inf
+    targets[targets == 300] = 301
+    targets[3] = 300
+    loss, lse = bsq.linear_cross_entropy(h, w, targets)
+    assert (lse == float("inf")).all()
+    assert torch.isnan(loss[3]) and (loss[targets != 300] == float("inf")).all()
