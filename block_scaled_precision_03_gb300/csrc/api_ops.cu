@@ -8,6 +8,8 @@
 namespace {
 
 constexpr int64_t kMaxRows = 0x7FFFFF00LL;
+// of expert rows: their kernels count a row's elements in 32 bits, up to 622592 past its end
+constexpr int64_t kMaxMoeCols = 1LL << 30;
 constexpr int32_t kMaxGrads = 1 << 20;
 constexpr int64_t kMaxElements = 1ll << 40;       // of all gradients of a call
 const uint64_t kWaitNs = 4000000000ull;            // 4 s per device-side wait, as the GEMMs
@@ -63,7 +65,7 @@ bsq_status check_rows(const void* src, int64_t ld_src, int32_t type, int64_t col
     bsq_status s = check_matrix(src, ld_src, type, cols);
     if (s != BSQ_OK) return s;
     if ((s = check_matrix(dst, ld_dst, type, cols)) != BSQ_OK) return s;
-    if (cols > kMaxRows) return BSQ_ERR_UNSUPPORTED;
+    if (cols > kMaxMoeCols) return BSQ_ERR_UNSUPPORTED;
     r.src = src;
     r.ld_src = ld_src;
     r.dst = dst;

@@ -292,7 +292,7 @@ typedef enum { BSQ_ID_I32 = 0, BSQ_ID_I64 = 1 } bsq_id_type;
  *   row_slot[r] = the slot in row r, -1 from row offsets[num_experts] on
  *                 (DEVICE int32[tokens * k])
  * All three arrays are the caller's.  1 <= k <= 256, 1 <= num_experts <=
- * 1024, tokens * k < 2^31 - 256. */
+ * 1024, tokens * k < 2^31 - 256; rows of up to 2^30 columns. */
 typedef struct {
     int64_t tokens;
     int32_t k;
