@@ -26,6 +26,7 @@
 #include <cuda.h>
 #include "common.cuh"
 #include "internal.h"
+#include "per_device.h"
 #include "tcgen05.cuh"
 #include "epilogue.cuh"
 #include "tmap.h"
@@ -394,13 +395,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 template <bool FP4>
 cudaError_t launch(const GemmArgs& a, const Params& p, const CUtensorMap& ta, const CUtensorMap& tb,
                    const CUtensorMap& tc_, int grid, cudaStream_t st) {
-    static bool attr_done = false;
-    cudaError_t e;
-    if (!attr_done) {
-        e = cudaFuncSetAttribute(gemm_kernel<FP4>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<FP4>::SMEM);
-        if (e != cudaSuccess) return e;
-        attr_done = true;
-    }
+    static SharedMemory smem;
+    const cudaError_t e = smem.allow(reinterpret_cast<const void*>(gemm_kernel<FP4>), Cfg<FP4>::SMEM);
+    if (e != cudaSuccess) return e;
     gemm_kernel<FP4><<<grid, kThreads, Cfg<FP4>::SMEM, st>>>(ta, tb, tc_, p);
     return cudaGetLastError();
 }

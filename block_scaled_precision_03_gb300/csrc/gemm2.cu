@@ -36,6 +36,7 @@
 #include <cuda.h>
 #include "common.cuh"
 #include "internal.h"
+#include "per_device.h"
 #include "tcgen05.cuh"
 #include "epilogue.cuh"
 #include "tmap.h"
@@ -572,12 +573,9 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
 template <int KIND>
 cudaError_t launch2(const Params2& p, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tsa,
                     const CUtensorMap& tsb, const CUtensorMap& tc_, int grid, cudaStream_t st) {
-    static bool attr_done = false;
-    if (!attr_done) {
-        cudaError_t e = cudaFuncSetAttribute(gemm2_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg2<KIND>::SMEM);
-        if (e != cudaSuccess) return e;
-        attr_done = true;
-    }
+    static SharedMemory smem;
+    const cudaError_t e = smem.allow(reinterpret_cast<const void*>(gemm2_kernel<KIND>), Cfg2<KIND>::SMEM);
+    if (e != cudaSuccess) return e;
     gemm2_kernel<KIND><<<grid, kThreads, Cfg2<KIND>::SMEM, st>>>(ta, tb, tsa, tsb, tc_, p);
     return cudaGetLastError();
 }

@@ -48,6 +48,7 @@
 #include "epilogue.cuh"
 #include "internal.h"
 #include "launch.cuh"
+#include "per_device.h"
 #include "tcgen05.cuh"
 #include "tmap.h"
 
@@ -813,12 +814,9 @@ int stream_rows(int64_t vocab, int num_sms) {
 template <int MODE, bool LONG>
 cudaError_t launch_gemm(const GemmParams& p, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& out, int pairs,
                         cudaStream_t st) {
-    static bool attr_done = false;
-    if (!attr_done) {
-        cudaError_t e = cudaFuncSetAttribute(head_gemm_kernel<MODE, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-        if (e != cudaSuccess) return e;
-        attr_done = true;
-    }
+    static SharedMemory smem;
+    const cudaError_t e = smem.allow(reinterpret_cast<const void*>(head_gemm_kernel<MODE, LONG>), kSmem);
+    if (e != cudaSuccess) return e;
     return launch_k(p.wait != kWaitLaunch, head_gemm_kernel<MODE, LONG>, dim3(2 * pairs), kGemmThreads, kSmem, st, ta, tb, out, p);
 }
 template <int MODE>
