@@ -13,6 +13,7 @@
 #include <cstdio>
 #include <cstring>
 #include <optional>
+#include <utility>
 #include "../../include/bsq.h"
 
 namespace {
@@ -54,10 +55,18 @@ void check(bsq_status status, const char* what) {
 
 bool none(PyObject* o) { return !o || o == Py_None; }
 
+// The device of a call's tensors: that of the first one it looks at (-1 before).  Set by guarded();
+// under Python's lock, like every call here.
+int call_device = -1;
+
 const at::Tensor& tensor(PyObject* o, const char* name) {
     if (!o || !THPVariable_Check(o)) refuse(BSQ_ERR_INVALID_ARG, "%s must be a CUDA tensor", name);
     const at::Tensor& t = THPVariable_Unpack(o);
     if (!t.is_cuda()) refuse(BSQ_ERR_INVALID_ARG, "%s must be a CUDA tensor", name);
+    if (call_device < 0) call_device = t.get_device();
+    if (t.get_device() != call_device)
+        refuse(BSQ_ERR_INVALID_ARG, "%s is on cuda:%d, other arguments of the call on cuda:%d", name, (int)t.get_device(),
+               call_device);
     return t;
 }
 
@@ -104,13 +113,15 @@ void* vector(PyObject* o, const char* name, int64_t n, at::ScalarType type) {
 
 // The stream to launch on (given, or the current one of the tensor's device)
 // and scratch that belongs to it: the allocator hands the scratch out again
-// only to work behind this call on that stream.
+// only to work behind this call on that stream.  That device is the current
+// one as long as this lives: the library launches on the current device.
 struct Launch {
+    c10::cuda::CUDAGuard device;
     cudaStream_t stream = nullptr;
     at::Tensor scratch;
     const at::Tensor& like;
     bool given;
-    Launch(PyObject* s, const at::Tensor& t) : like(t), given(!none(s)) {
+    Launch(PyObject* s, const at::Tensor& t) : device(t.get_device()), like(t), given(!none(s)) {
         if (!given) {
             stream = c10::cuda::getCurrentCUDAStream(t.get_device()).stream();
             return;
@@ -173,9 +184,13 @@ PyObject* returned(PyObject* a, PyObject* b, PyObject* c) {
     return PyTuple_Pack(3, a ? a : Py_None, b ? b : Py_None, c ? c : Py_None);
 }
 
-// Runs a call; C++ exceptions end here.
+// Runs a call; C++ exceptions end here.  (Reading a plan's attributes may run Python, and so another call.)
 template <typename F>
 PyObject* guarded(F f) {
+    struct Device {
+        int before = std::exchange(call_device, -1);
+        ~Device() { call_device = before; }
+    } own;
     try {
         return f();
     } catch (const Refused&) {

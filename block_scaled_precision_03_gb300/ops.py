@@ -293,6 +293,9 @@ class GradList:
         arr = (BsqGradC * len(grads))()
         for i, (g, o) in enumerate(zip(grads, outs)):
             t = _type(g, f"gradient {i}")
+            for name, x in (("gradient", g), ("output", o)):
+                if x.device != grads[0].device:
+                    _refuse(f"{name} {i} is on {x.device}, gradient 0 on {grads[0].device}")
             arr[i] = BsqGradC(_elements(g, f"gradient {i}", g.numel(), g.dtype),
                               _elements(o, f"output {i}", g.numel(), g.dtype), g.numel(), t, 0)
         self.grads, self.outs, self.array = grads, outs, arr
