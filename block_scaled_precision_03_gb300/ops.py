@@ -322,6 +322,11 @@ def _grad_list(grads) -> GradList:
     return grads if isinstance(grads, GradList) else GradList(grads)
 
 
+def _needs_bound(max_norm):
+    if max_norm is None:                               # the native call takes it for the norm only
+        _refuse("max_norm must be a number")
+
+
 def grad_norm(grads, stream=None):
     """The global 2-norm of a GradList or of tensors: float32 [1] on the device."""
     import torch
@@ -331,6 +336,7 @@ def grad_norm(grads, stream=None):
 
 
 def clip_grad_norm_into(grads, max_norm: float, norm, eps: float = 1e-6, stream=None):
+    _needs_bound(max_norm)
     g = _grad_list(grads)
     return _native().grads_into(g.address, g.count, max_norm, eps, norm, g.workspace(stream), stream)
 
@@ -339,5 +345,6 @@ def clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, stream=None):
     """Write every gradient times min(1, max_norm / (norm + eps)) to its
     output (a list of tensors: in place); returns the norm, float32 [1]."""
     import torch
+    _needs_bound(max_norm)
     g = _grad_list(grads)
     return clip_grad_norm_into(g, max_norm, _new(1, torch.float32, stream, g.grads[0]), eps, stream)

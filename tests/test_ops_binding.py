@@ -80,3 +80,12 @@ def test_gradient_lists_on_two_devices_are_refused(bsq):
     from block_scaled_precision_03_gb300 import ops
     with pytest.raises(bsq.BsqError, match="cuda:1"):
         ops._native().grads_into(0, 1, 1.0, 0.0, on(0, 1), on(1, 16, dtype=torch.uint8), None)
+
+
+def test_clipping_to_no_norm_is_refused(bsq):
+    # None would otherwise mean "the norm only" and leave the outputs as they are
+    grads = bsq.GradList([on(0, 8)], [on(0, 8)])
+    for call in (lambda: bsq.clip_grad_norm(grads, None), lambda: bsq.clip_grad_norm([on(0, 8)], None),
+                 lambda: bsq.clip_grad_norm_into(grads, None, on(0, 1))):
+        with pytest.raises(bsq.BsqError, match="max_norm"):
+            call()
