@@ -6,6 +6,7 @@
 #include <Python.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAException.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -440,9 +441,17 @@ ENTRY(grads_into) {
     });
 }
 
-// current_stream(tensor) -> handle of its device's current stream
-PyObject* current_stream(PyObject*, PyObject* o) {
-    return guarded([&] { return PyLong_FromVoidPtr(c10::cuda::getCurrentCUDAStream(tensor(o, "tensor").get_device()).stream()); });
+// stream_state(tensor, stream) -> (handle, whether it captures a graph) of the stream a call with it launches on
+ENTRY(stream_state) {
+    return guarded([&] {
+        static const char* const names[] = {"tensor", "stream"};
+        const Args a("stream_state", names, 1, args, n, kwnames);
+        const Launch l(a[1], tensor(a[0], "tensor"));
+        cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+        C10_CUDA_CHECK(cudaStreamIsCapturing(l.stream, &status));
+        return Py_BuildValue("NN", PyLong_FromVoidPtr(l.stream),
+                             PyBool_FromLong(status != cudaStreamCaptureStatusNone));
+    });
 }
 
 // bind(addresses by name, BsqError)
@@ -474,7 +483,7 @@ PyMethodDef methods[] = {
     METHOD(moe_sort_into), METHOD(moe_dispatch_into), METHOD(moe_gather_into), METHOD(moe_combine_into),
     METHOD(moe_combine_backward_into), METHOD(layer_norm_into), METHOD(layer_norm_backward_into),
     METHOD(linear_cross_entropy_into), METHOD(linear_cross_entropy_backward_into), METHOD(grads_into),
-    {"current_stream", current_stream, METH_O, nullptr},
+    METHOD(stream_state),
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(bind)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -308,10 +308,10 @@ class GradList:
         order, calls on two get one each.  A call captured in a graph gets its
         own: the graph may replay beside later calls."""
         import torch
-        if torch.cuda.is_current_stream_capturing():
+        raw, capturing = _native().stream_state(self.grads[0], stream)
+        if capturing:
             self._captured.append(_new(self.workspace_bytes, torch.uint8, stream, self.grads[0]))
             return self._captured[-1]
-        raw = stream.cuda_stream if stream is not None else _native().current_stream(self.grads[0])
         ws = self._workspaces.get(raw)
         if ws is None:
             ws = self._workspaces[raw] = _new(self.workspace_bytes, torch.uint8, stream, self.grads[0])
