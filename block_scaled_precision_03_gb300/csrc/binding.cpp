@@ -368,17 +368,24 @@ ENTRY(layer_norm_backward_into) {
     });
 }
 
+// A matrix of the head, whose pitches have to be whole vectors; that of a single row says nothing.
+Matrix head_matrix(PyObject* o, const char* name, int64_t rows = -1, int64_t cols = -1, const Matrix* like = nullptr) {
+    Matrix m = matrix(o, name, rows, cols, like);
+    if (m.rows == 1) m.ld = m.cols;
+    return m;
+}
+
 struct Head {
     Matrix h, w;
     const int64_t* targets;
     Head(PyObject* ph, PyObject* pw, PyObject* pt) {
-        h = matrix(ph, "h");
+        h = head_matrix(ph, "h");
         for (const char* name : {"h", "w"}) {
             const at::Tensor& t = tensor(name[0] == 'h' ? ph : pw, name);
             if (t.scalar_type() != at::kBFloat16)
                 refuse(BSQ_ERR_UNSUPPORTED, "%s: %s (BFloat16 is supported)", name, c10::toString(t.scalar_type()));
         }
-        w = matrix(pw, "w", -1, h.cols);
+        w = head_matrix(pw, "w", -1, h.cols);
         targets = static_cast<int64_t*>(vector(pt, "targets", h.rows, at::kLong));
     }
 };
@@ -405,8 +412,8 @@ ENTRY(linear_cross_entropy_backward_into) {
         const Args a("linear_cross_entropy_backward_into", names, 7, args, n, kwnames);
         const Head d(a[0], a[1], a[2]);
         Matrix dh, dw;
-        if (!none(a[5])) dh = matrix(a[5], "dh", d.h.rows, d.h.cols, &d.h);
-        if (!none(a[6])) dw = matrix(a[6], "dw", d.w.rows, d.w.cols, &d.w);
+        if (!none(a[5])) dh = head_matrix(a[5], "dh", d.h.rows, d.h.cols, &d.h);
+        if (!none(a[6])) dw = head_matrix(a[6], "dw", d.w.rows, d.w.cols, &d.w);
         const float* lse = static_cast<float*>(vector(a[3], "lse", d.h.rows, at::kFloat));
         const float* dloss = static_cast<float*>(vector(a[4], "dloss", d.h.rows, at::kFloat));
         Launch l(a[7], *d.h.t);

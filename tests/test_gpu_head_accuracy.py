@@ -174,3 +174,21 @@ def test_infinite_logits(bsq, T):
     loss, lse = bsq.linear_cross_entropy(h, w, targets)
     assert (lse == float("inf")).all()
     assert torch.isnan(loss[3]) and (loss[targets != 300] == float("inf")).all()
+
+
+def test_a_single_row_has_no_pitch(bsq):
+    # one token of a buffer whose rows are not whole vectors, and one column of such a head
+    g = torch.Generator(device="cuda").manual_seed(3)
+    h = torch.randn((5, 20), generator=g, device="cuda").to(BF)[:1, :16]
+    w = torch.randn((7, 16), generator=g, device="cuda").to(BF)
+    target, dloss = torch.tensor([2], device="cuda"), torch.ones(1, device="cuda")
+    want = bsq.linear_cross_entropy(h.contiguous(), w, target)
+    got = bsq.linear_cross_entropy(h, w, target)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    dh, dw = torch.empty((3, 20), dtype=BF, device="cuda")[:1, :16], torch.empty_like(w)
+    bsq.linear_cross_entropy_backward_into(h, w, target, want[1], dloss, dh, dw)
+    wh, ww = bsq.linear_cross_entropy_backward(h.contiguous(), w, target, want[1], dloss)
+    assert torch.equal(dh, wh) and torch.equal(dw, ww)
+    one = torch.randn((2, 20), generator=g, device="cuda").to(BF)[:1, :16]
+    assert torch.equal(bsq.linear_cross_entropy(h, one, target * 0)[1],
+                       bsq.linear_cross_entropy(h.contiguous(), one.contiguous(), target * 0)[1])
