@@ -461,10 +461,12 @@ ENTRY(stream_state) {
     });
 }
 
-// bind(addresses by name, BsqError)
+extern PyMethodDef methods[];
+
+// bind(addresses by name, BsqError, documentation by name)
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
-    if (n != 2 || !PyDict_Check(args[0])) {
-        PyErr_SetString(PyExc_TypeError, "bind(addresses, BsqError)");
+    if (n != 3 || !PyDict_Check(args[0]) || !PyDict_Check(args[2])) {
+        PyErr_SetString(PyExc_TypeError, "bind(addresses, BsqError, documentation)");
         return nullptr;
     }
 #define F(name)                                                                    \
@@ -480,6 +482,12 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
     }
     BSQ_FUNCTIONS(F)
 #undef F
+    for (PyMethodDef* m = methods; m->ml_name; m++)
+        if (PyObject* doc = PyDict_GetItemString(args[2], m->ml_name)) {
+            const char* text = PyUnicode_AsUTF8(doc);
+            if (!text) return nullptr;
+            m->ml_doc = strdup(text);              // kept, like the table
+        }
     Py_INCREF(args[1]);
     error_class = args[1];
     Py_RETURN_NONE;

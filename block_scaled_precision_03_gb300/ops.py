@@ -26,6 +26,7 @@ from __future__ import annotations
 import ctypes
 import importlib.machinery
 import importlib.util
+import inspect
 import os
 import sys
 from dataclasses import dataclass
@@ -75,7 +76,7 @@ def _signatures():
 # first of them and then stands in the place of the functions here; like the
 # library it has no fallback.
 _native_module = None
-_BOUND = []
+_BOUND = {}
 
 
 def _native():
@@ -89,7 +90,7 @@ def _native():
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_binding", loader))
         loader.exec_module(module)
         module.bind({name: ctypes.cast(getattr(library, name), ctypes.c_void_p).value for name in _signatures()},
-                    BsqError)
+                    BsqError, {name: _documentation(f) for name, f in _BOUND.items()})
         for name in _BOUND:
             native = getattr(module, name)
             setattr(sys.modules[__name__], name, native)
@@ -98,8 +99,15 @@ def _native():
     return _native_module
 
 
+def _documentation(f) -> str:
+    """A native function's documentation: its signature in the form inspect reads, then the text."""
+    signature = inspect.signature(f)
+    bare = [p.replace(annotation=p.empty) for p in signature.parameters.values()]
+    return f"{f.__name__}{inspect.Signature(bare)}\n--\n\n{inspect.getdoc(f)}"
+
+
 def _bound(f):
-    _BOUND.append(f.__name__)
+    _BOUND[f.__name__] = f
 
     def call(*args, **kwargs):
         return getattr(_native(), f.__name__)(*args, **kwargs)

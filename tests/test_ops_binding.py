@@ -89,3 +89,25 @@ def test_clipping_to_no_norm_is_refused(bsq):
                  lambda: bsq.clip_grad_norm_into(grads, None, on(0, 1))):
         with pytest.raises(bsq.BsqError, match="max_norm"):
             call()
+
+
+def test_the_calls_keep_their_documentation(bsq):
+    # the native functions take the places of the Python ones at the first call
+    import subprocess
+    import sys
+    code = """
+import inspect
+import block_scaled_precision_03_gb300 as bsq
+from block_scaled_precision_03_gb300 import ops
+before = {n: (inspect.getdoc(getattr(bsq, n)), list(inspect.signature(getattr(bsq, n)).parameters.values())) for n in ops._BOUND}
+ops._native()
+for name, (doc, parameters) in before.items():
+    f = getattr(bsq, name)
+    assert f is getattr(ops, name) and type(f).__name__ == "builtin_function_or_method"
+    assert doc and inspect.getdoc(f) == doc, (name, f.__doc__)
+    got = list(inspect.signature(f).parameters.values())
+    assert [(p.name, p.default) for p in got] == [(p.name, p.default) for p in parameters], (name, got)
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=root)
