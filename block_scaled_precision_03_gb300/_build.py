@@ -3,8 +3,9 @@ binding _binding.so with the host compiler.
 
 Each .cu file is compiled in parallel into _build/, then linked into
 block_scaled_precision_03_gb300/libbsq.so (CUDA runtime linked statically,
-driver entry points resolved at run time); binding.cpp is compiled against the
-installed PyTorch beside them.  Usage:
+driver entry points resolved at run time).  binding.cpp is compiled against the
+installed PyTorch beside them, and again when that is another one; the library
+does not wait for it, and stands where it cannot be built.  Usage:
 
     python -m block_scaled_precision_03_gb300._build [--force] [-v]
 """
@@ -40,9 +41,38 @@ def _deps():
     return max(os.path.getmtime(f) for f in files)
 
 
+def _made_for() -> str:
+    """What the binding is compiled against besides the sources: this Python and
+    the installed PyTorch, whose version file is read without importing it."""
+    import importlib.util
+    torch = importlib.util.find_spec("torch")
+    version = "none"
+    if torch is not None and torch.origin:
+        with open(os.path.join(os.path.dirname(torch.origin), "version.py")) as f:
+            version = f.read()
+    return f"{sys.version}\n{version}"
+
+
+def _lib_current() -> bool:
+    return os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps()
+
+
+def _binding_current() -> bool:
+    if not os.path.exists(BINDING) or os.path.getmtime(BINDING) < _deps():
+        return False
+    try:
+        with open(os.path.join(BUILD, "binding.for")) as f:
+            return f.read() == _made_for()
+    except FileNotFoundError:
+        return False
+
+
 def _compile_binding():
     import sysconfig
-    import torch
+    try:
+        import torch
+    except ImportError as e:
+        raise RuntimeError(f"the Python binding needs PyTorch: {e}") from e
     root = os.path.dirname(torch.__file__)
     tmp = BINDING + f".{os.getpid()}.tmp"
     abi = f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
@@ -52,16 +82,32 @@ def _compile_binding():
            "-I", os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"),
            os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", os.path.join(root, "lib"),
            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{os.path.join(root, 'lib')}"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        raise RuntimeError(f"g++ could not be run for binding.cpp: {e}") from e
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(os.path.join(BUILD, "binding.for"), "w") as f:
+        f.write(_made_for())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps() for f in (LIB, BINDING)):
-        return LIB
+    """Build what is out of date; returns the library's path.  Where the binding
+    cannot be built the library is built all the same, before the error."""
     os.makedirs(BUILD, exist_ok=True)
+    lib, binding = force or not _lib_current(), force or not _binding_current()
+    with ThreadPoolExecutor(1) as ex:
+        beside = ex.submit(_compile_binding) if binding else None
+        if lib:
+            _build_lib(verbose)
+        if beside:
+            beside.result()
+    return LIB
+
+
+def _build_lib(verbose: bool) -> None:
     flags = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE] + ARCH
     if verbose:
         flags += ["-Xptxas", "-v"]
@@ -76,17 +122,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
-    with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-        binding = ex.submit(_compile_binding)
+    with ThreadPoolExecutor(len(SOURCES)) as ex:
         objs = list(ex.map(compile_one, SOURCES))
-        binding.result()
     tmp = LIB + f".{os.getpid()}.tmp"
     r = subprocess.run([nvcc(), "-shared", *ARCH, "-o", tmp, *objs, "-cudart", "static"],
                        capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
