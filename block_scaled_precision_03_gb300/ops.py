@@ -299,13 +299,16 @@ class GradList:
         if not grads or len(outs) != len(grads):
             _refuse("a gradient list needs at least one gradient, and one output for each")
         arr = (BsqGradC * len(grads))()
+        where = grads[0].get_device()
         for i, (g, o) in enumerate(zip(grads, outs)):
+            n = g.numel()
             t = _type(g, f"gradient {i}")
-            for name, x in (("gradient", g), ("output", o)):
-                if x.device != grads[0].device:
-                    _refuse(f"{name} {i} is on {x.device}, gradient 0 on {grads[0].device}")
-            arr[i] = BsqGradC(_elements(g, f"gradient {i}", g.numel(), g.dtype),
-                              _elements(o, f"output {i}", g.numel(), g.dtype), g.numel(), t, 0)
+            if g.get_device() != where or o.get_device() != where:
+                name, x = (f"gradient {i}", g) if g.get_device() != where else (f"output {i}", o)
+                _refuse(f"{name} is on {x.device}, gradient 0 on {grads[0].device}")
+            at = _elements(g, f"gradient {i}", n, g.dtype)
+            to = at if o is g else _elements(o, f"output {i}", n, g.dtype)
+            arr[i] = BsqGradC(at, to, n, t, 0)
         self.grads, self.outs, self.array = grads, outs, arr
         self.address, self.count = ctypes.addressof(arr), len(grads)
         self.workspace_bytes = int(lib().bsq_grad_workspace_bytes(len(grads)))
