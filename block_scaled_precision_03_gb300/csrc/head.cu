@@ -7,9 +7,9 @@
 // and loss = lse - z[target].  Backward, a piece of the vocabulary at a time:
 // the logits' tile again, g = ratio (exp(z - lse) - [v = target]) in BF16 with
 // ratio = dloss / max |dloss| (of the finite ones), then dh += g w (FP32 between
-// pieces) and dw = g^T h, both times max |dloss| in FP32.  With the usual dloss (one value
-// for every token that counts) ratio is 1, so the one large entry of a row of
-// g, the target's, loses nothing to BF16.
+// pieces) and dw = g^T h, both times max |dloss| in FP32, so that no dloss, however
+// small, leaves BF16's range.  What g loses to BF16 is mostly the target's entry,
+// p - 1: 1.0e-3 of dh and dw, beside the 1.66e-3 of their own rounding.
 //
 // All four products run in one kernel on CTA pairs (tcgen05 cta_group::2,
 // M = N = 256, K = 16 per MMA): each CTA stages its own 128 rows of A and of
@@ -35,8 +35,8 @@
 //
 // Measured, BF16: the loss of 8192 tokens, 65536 x 4096, in 2.46 to 2.59 ms (up to 1790 TFLOP/s,
 // what a library product holds under the power cap, 0.92 of its burst; boxes differ),
-// its gradient in 7.8 ms (1690 TFLOP/s: bound by the power cap, and dh reads w
-// and dw h again); 7 tokens, 50021 x 4096, in 70 us (5.9 TB/s, 0.88 of a copy's
+// its gradient in 7.6 to 8.0 ms (1650 to 1740 TFLOP/s: bound by the power cap, and dh reads w
+// and dw h again); 64 tokens' gradient, 50021 x 4096, in 222 us (w read twice, dw written); 7 tokens, 50021 x 4096, in 70 us (5.9 TB/s, 0.88 of a copy's
 // rate), the rest the start of the stream, the last tile and the join.  Calls
 // below a few microseconds of work take 10 us (loss) to 16 us (gradient): two to
 // four launches in a chain, each with some 3000 cycles of set-up and first loads
@@ -345,7 +345,7 @@ __device__ __forceinline__ void few_tokens(const GemmParams& p, float* lse, floa
 }
 
 // Bound by the tensor cores: of 2048 tokens and 16384 x 4096 every product takes
-// 151 to 161 us, tensor pipes 76 to 83% busy (few tokens: by reading w, 6.1 TB/s).
+// 149 to 162 us, tensor pipes 75 to 81% busy (few tokens: by reading w, 6.1 TB/s).
 // One thread issues all MMAs, about 88 cycles each; with 256 columns an MMA
 // takes longer than that.
 // LONG: a tile's sum over K takes several accumulators, which the epilogue adds up in

@@ -290,8 +290,10 @@ def linear_cross_entropy_backward(h, w, targets, lse, dloss, stream=None):
 # ------------------------------------------------------ global norm and clipping
 class GradList:
     """The gradients of a step and where their clipped copies go (`outs`; in
-    place without it): contiguous CUDA tensors, bfloat16 or float32.  Built
-    once for buffers that stay; it keeps them alive."""
+    place without it): contiguous tensors of one GPU, bfloat16 or float32.
+    Built once for buffers that stay (some 2 us of host time a tensor); it
+    keeps them alive, and with them a workspace for each stream it is used on
+    and each call that a graph captured."""
 
     def __init__(self, grads, outs=None):
         grads = list(grads)
@@ -354,7 +356,8 @@ def clip_grad_norm_into(grads, max_norm: float, norm, eps: float = 1e-6, stream=
 
 def clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, stream=None):
     """Write every gradient times min(1, max_norm / (norm + eps)) to its
-    output (a list of tensors: in place); returns the norm, float32 [1]."""
+    output (a list of tensors: in place); returns the norm, float32 [1].  A
+    list of tensors costs what building its GradList costs, at every call."""
     import torch
     _needs_bound(max_norm)
     g = _grad_list(grads)
