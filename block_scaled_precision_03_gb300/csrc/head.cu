@@ -8,8 +8,11 @@
 // the logits' tile again, g = ratio (exp(z - lse) - [v = target]) in BF16 with
 // ratio = dloss / max |dloss| (of the finite ones), then dh += g w (FP32 between
 // pieces) and dw = g^T h, both times max |dloss| in FP32, so that no dloss, however
-// small, leaves BF16's range.  What g loses to BF16 is mostly the target's entry,
-// p - 1: 1.0e-3 of dh and dw, beside the 1.66e-3 of their own rounding.
+// small, leaves BF16's range.  The target's entry of g, p - 1, is by far the largest
+// of its row and shares its rounding with every token of that target (p = 1 / V rounds
+// to -1 for all of them), so it enters in full: what BF16 loses of it, lo, is added as
+// lo w[target] to dh and lo h to dw.  (Without that dh and dw were 1.0e-3 off before
+// their own rounding, 1.66e-3, and elements of a common target's row of dw up to 10%.)
 //
 // All four products run in one kernel on CTA pairs (tcgen05 cta_group::2,
 // M = N = 256, K = 16 per MMA): each CTA stages its own 128 rows of A and of
@@ -36,13 +39,14 @@
 // Measured, BF16: the loss of 8192 tokens, 65536 x 4096, in 2.46 to 2.59 ms (up to 1790 TFLOP/s,
 // what a library product holds under the power cap, 0.92 of its burst; boxes differ),
 // its gradient in 7.6 to 8.0 ms (1650 to 1740 TFLOP/s: bound by the power cap, and dh reads w
-// and dw h again); 64 tokens' gradient, 50021 x 4096, in 222 us (w read twice, dw written); 7 tokens, 50021 x 4096, in 70 us (5.9 TB/s, 0.88 of a copy's
+// and dw h again); 64 tokens' gradient, 50021 x 4096, in 226 us (w read twice, dw written); 7 tokens, 50021 x 4096, in 70 us (5.9 TB/s, 0.88 of a copy's
 // rate), the rest the start of the stream, the last tile and the join.  Calls
-// below a few microseconds of work take 10 us (loss) to 16 us (gradient): two to
-// four launches in a chain, each with some 3000 cycles of set-up and first loads
+// below a few microseconds of work take 10 us (loss) to 20 us (gradient): two to
+// five launches in a chain, each with some 3000 cycles of set-up and first loads
 // and as many at the end.
 #include <algorithm>
 #include <cfloat>
+#include <climits>
 #include <cuda.h>
 #include "common.cuh"
 #include "epilogue.cuh"
@@ -59,7 +63,7 @@ constexpr int64_t kPieceBytes = 256ll << 20;       // of g
 constexpr float kNegInf = -INFINITY;
 constexpr float kLog2e = 1.44269504088896340736f;
 
-enum { kStats, kGrad, kDh, kDw, kFewStats, kFewGrad };
+enum { kStats, kGrad, kDh, kDw, kFewStats, kFewGrad, kDwFull };
 // When a product waits for the kernel before it on the stream: that kernel is done
 // when it is launched; before it reads or writes anything (its set-up runs
 // earlier); before its epilogue (only the epilogue needs that kernel); at its end
@@ -97,8 +101,29 @@ __host__ __device__ constexpr bool is_few(int mode) { return mode == kFewStats |
 constexpr int64_t kL2Resident = 40ll << 20;         // operand bytes that stay in L2 while others stream past
 
 // MODE's operand layouts: K-major (false) or MN-major (true)
-__host__ __device__ constexpr bool a_mn(int mode) { return mode == kDw; }
-__host__ __device__ constexpr bool b_mn(int mode) { return mode == kDh || mode == kDw; }
+__host__ __device__ constexpr bool is_dw(int mode) { return mode == kDw || mode == kDwFull; }
+__host__ __device__ constexpr bool a_mn(int mode) { return is_dw(mode); }
+__host__ __device__ constexpr bool b_mn(int mode) { return mode == kDh || is_dw(mode); }
+// whose rows get what the targets' entries of g lost to BF16 in the epilogue
+__host__ __device__ constexpr bool takes_extra(int mode) { return mode == kDh || mode == kDw; }
+
+// The tokens with a vocabulary row as their target: the first of them, and their number
+struct Owner {
+    int32_t first, count;
+};
+// What the targets' entries of g lost to BF16, summed for the vocabulary rows that several tokens have as their
+// target: in fixed point, so that the sums do not depend on the order of the additions.  A sum of `count` terms
+// lo h, |lo| < 2^-8 and |h| at most hmax, is held in units of 2^unit, below 2^30 of them.
+struct Sums {
+    int32_t* rows;                 // [rows][cols], of a vocabulary row, or of its first token
+    int64_t cols;
+    int32_t by_row;
+    const float* hmax;             // [hmaxes]: partial maxima; *hmaxes: all of them
+    int32_t hmaxes;
+};
+__device__ __forceinline__ int sum_unit(float hmax, int count) {
+    return hmax > 0.0f ? ilogbf(hmax) + 1 - 8 + (32 - __clz(count)) - 30 : 0;
+}
 
 struct GemmParams {
     int64_t M, N;                  // output
@@ -116,12 +141,22 @@ struct GemmParams {
     int64_t col0;                  // first vocabulary column of the piece
     float2* part;                  // kStats: [part][M] (max, sum), a part per tile and 128 columns
     float* hit;                    // kStats: the target's logit
-    __nv_bfloat16* g;              // kFewGrad: g [tokens][ld_g]
+    __nv_bfloat16* g;              // kFewGrad: g [tokens][ld_g]; g_lo has the same pitch
     int64_t ld_g;
     const float* lse;
     const float* dloss;
     float* smax;
     int32_t put_smax;              // kFewGrad: leave max |dloss| there
+    float* lo;                     // [tokens] what the target's entry of g lost to BF16 (kGrad, kFewGrad leave it)
+    __nv_bfloat16* g_lo;           // kGrad, kFewGrad: the same as a matrix like g, for kDwFull
+    Owner* owner;                  // kGrad fills, kDw reads: [the piece's columns]
+    const __nv_bfloat16* w;        // kDh: the piece
+    int64_t ldw;
+    int64_t piece_cols;            // kDh: columns of the piece
+    Sums sums;                     // kDw
+    const __nv_bfloat16* h;        // kDw
+    int64_t ldh;
+    int32_t half_subs, sub_mmas;   // kDwFull: sub-steps of g (as many of g_lo follow), and the MMAs of each
     int32_t add;                   // kDh: add to what is there
     int32_t direct;                // kDh, kDw: the only piece and split, so dh or dw itself leaves
     unsigned* status;
@@ -175,6 +210,10 @@ __device__ __forceinline__ float finite_or_zero(float m) { return fabsf(m) == IN
 __device__ __forceinline__ float few_g(float z, float lse, float ratio, bool target) {
     const float g = exp2_fast((z - lse) * kLog2e) - (target ? 1.0f : 0.0f);
     return ratio == 0.0f ? 0.0f : g * ratio;
+}
+// What an entry of g loses to BF16 (nothing where it is not finite)
+__device__ __forceinline__ float left_over(float g) {
+    return fabsf(g) <= FLT_MAX ? g - __bfloat162float(__float2bfloat16_rn(g)) : 0.0f;
 }
 // Where lane l's i-th group of four rows starts: its 16 rows, begun at another
 // place for each of four neighbouring tokens
@@ -433,10 +472,14 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     if (leader) tc::mbar_expect_tx(full0 + 8 * stage, 2 * p.tx);
 #pragma unroll
                     for (int j = 0; j < kSub; j++) {
-                        const int k = (kb * kSub + j) * kSubK;
+                        const int sub = kb * kSub + j, half = MODE == kDwFull && sub >= p.half_subs ? 1 : 0;
+                        const int k = (sub - half * p.half_subs) * kSubK;
                         const uint32_t da = tc::smem_u32(smA + stage * kOpBytes + j * kSubBytes);
                         const uint32_t db = tc::smem_u32(smB + stage * b_bytes + j * sub_b);
-                        if (a_mn(MODE)) {
+                        if (MODE == kDwFull) {              // g, then g_lo, against the same rows of h
+                            tc::tma_load_3d_pair(da, &tmA, am, k, half, fb);
+                            tc::tma_load_3d_pair(da + 8192, &tmA, am + 64, k, half, fb);
+                        } else if (a_mn(MODE)) {
                             tc::tma_load_2d_pair(da, &tmA, am, k, fb);
                             tc::tma_load_2d_pair(da + 8192, &tmA, am + 64, k, fb);
                         } else {
@@ -487,7 +530,13 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                         const Desc bd = Desc(bd0) + (uint32_t)(stage * (b_bytes >> 4));
                         const int next = stage + 1 == S ? 0 : stage + 1;
                         const uint32_t next_phase = next == 0 ? phase ^ 1 : phase;
-                        if (kb != p.k_stages - 1 || p.mma_last == kMmas) {
+                        if (MODE == kDwFull && p.sub_mmas < 4) {
+                            for (int m = 0; m < kMmas; m++)
+                                if ((m & 3) < p.sub_mmas)
+                                    mma_bf16<false>(d, ad + (m >> 2) * (kSubBytes >> 4) + (m & 3) * a_step,
+                                                    bd + (m >> 2) * (sub_b >> 4) + (m & 3) * b_step, idesc, (kb != c0) | (m != 0));
+                            ready = false;
+                        } else if (kb != p.k_stages - 1 || p.mma_last == kMmas) {
                             // the next stage's barrier is tested while this stage's MMAs run
                             mma_bf16<false>(d, ad, bd, idesc, kb != c0);
 #pragma unroll
@@ -525,7 +574,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         const uint32_t tempty_c0 = tc::mapa(tempty0, 0);
         const uint32_t stage_buf = tc::smem_u32(smOut + (warp - 2) * kStage);
         if (p.wait == kWaitStart || p.wait == kWaitEpilogue) pdl_wait();
-        const float smax = MODE == kGrad || MODE == kDw || MODE == kDh ? __ldcg(p.smax) : 1.0f;
+        const float smax = MODE == kGrad || is_dw(MODE) || MODE == kDh ? __ldcg(p.smax) : 1.0f;
         int iter = 0, n = 0;
         if (FEW) {
             few_tokens<MODE>(p, few_lse, few_ratio, few_target);
@@ -600,16 +649,34 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                             const float4 x = *reinterpret_cast<const float4*>(mine + r);
                             const float v[4] = {few_g(x.x, lse, ratio, at == r), few_g(x.y, lse, ratio, at == r + 1),
                                                 few_g(x.z, lse, ratio, at == r + 2), few_g(x.w, lse, ratio, at == r + 3)};
-                            const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
-                            *reinterpret_cast<uint2*>(g + r) =
-                                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                            const auto put = [](__nv_bfloat16* to, float a, float b, float c, float d) {
+                                const __nv_bfloat162 lo = __floats2bfloat162_rn(a, b), hi = __floats2bfloat162_rn(c, d);
+                                *reinterpret_cast<uint2*>(to) =
+                                    make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                            };
+                            put(g + r, v[0], v[1], v[2], v[3]);
+                            float lost = 0.0f;
+                            if (at >= r && at < r + 4) {
+                                lost = left_over(at < r + 2 ? (at == r ? v[0] : v[1]) : (at == r + 2 ? v[2] : v[3]));
+                                p.lo[token] = lost;
+                            }
+                            if (p.g_lo)
+                                put(p.g_lo + (g - p.g) + r, at == r ? lost : 0.0f, at == r + 1 ? lost : 0.0f,
+                                    at == r + 2 ? lost : 0.0f, at == r + 3 ? lost : 0.0f);
                         }
                     }
 #pragma unroll
                     for (int j = 0; j < 48; j++) z[j] = z[j + 16];
                 }
             }
-        } else
+        } else {
+        // kDw: first and count of this thread's row of tile t, read a tile ahead
+        const auto owner_of = [&](int t) {
+            const TileAt at = tile_at(p, min(t, p.total - 1));
+            const int64_t r = (int64_t)at.mt * kTile + rank * 128 + q * 32 + lane;
+            return r < p.M && at.split == 0 ? *reinterpret_cast<const int2*>(p.owner + r) : make_int2(0, 0);
+        };
+        int2 next_owner = MODE == kDw ? owner_of(cid) : make_int2(0, 0);
         for (int t = cid; t < p.total; t += ncl) {
             const TileAt ti = tile_at(p, t);
             const int64_t row0 = (int64_t)ti.mt * kTile + rank * 128 + q * 32, row = row0 + lane;       // tile_m is 256
@@ -628,12 +695,68 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     if (at >= 0 && at < 128) target = (int)at;
                 }
             }
+            // what the targets' entries lost adds to this row: `factor` times a row, or a row of sums
+            const __nv_bfloat16* extra = nullptr;
+            const int32_t* sums = nullptr;
+            float factor = 1.0f, factor2 = 1.0f;
+            if (MODE == kDh && row < p.M && ti.split == 0) {
+                const int64_t id = p.targets[row] - p.col0;
+                if (id >= 0 && id < p.piece_cols) {
+                    factor = p.lo[row];
+                    if (factor != 0.0f) extra = p.w + id * p.ldw;
+                }
+            }
+            if (MODE == kDw) {
+                const int2 o = next_owner;
+                next_owner = owner_of(t + ncl);
+                if (o.y == 1) {
+                    extra = p.h + o.x * p.ldh;
+                    factor = p.lo[o.x];
+                } else if (o.y > 1) {
+                    sums = p.sums.rows + (p.sums.by_row ? p.col0 + row : o.x) * p.sums.cols;
+                    const int unit = sum_unit(p.sums.hmax[p.sums.hmaxes], o.y);
+                    factor = scalbnf(1.0f, unit / 2);      // (2^unit may not be a float)
+                    factor2 = scalbnf(1.0f, unit - unit / 2);
+                }
+            }
+            const int own_cols = (int)min((int64_t)128, p.N - col0);        // a multiple of 8 where it is used
+            const auto add_extra = [&](float* v, int u0) {         // to 32 columns, the tile's from 8 u0 on
+                if (extra) {
+                    Pack<__nv_bfloat16, 8> from[4];
+#pragma unroll
+                    for (int u = 0; u < 4; u++) {
+                        from[u].zero();
+                        if (8 * (u0 + u) < own_cols) from[u].load(extra + col0 + 8 * (u0 + u));
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4; u++) {
+                        float f[8];
+                        from[u].unpack(f);
+#pragma unroll
+                        for (int e = 0; e < 8; e++) v[8 * u + e] = fmaf(factor, f[e], v[8 * u + e]);
+                    }
+                } else if (MODE == kDw && sums) {
+                    int4 q[8];
+#pragma unroll
+                    for (int e = 0; e < 8; e++) {
+                        q[e] = make_int4(0, 0, 0, 0);
+                        if (8 * u0 + 4 * e < own_cols) q[e] = *reinterpret_cast<const int4*>(sums + col0 + 8 * u0 + 4 * e);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; e++) {
+                        v[4 * e] = fmaf((float)q[e].x * factor, factor2, v[4 * e]);
+                        v[4 * e + 1] = fmaf((float)q[e].y * factor, factor2, v[4 * e + 1]);
+                        v[4 * e + 2] = fmaf((float)q[e].z * factor, factor2, v[4 * e + 2]);
+                        v[4 * e + 3] = fmaf((float)q[e].w * factor, factor2, v[4 * e + 3]);
+                    }
+                }
+            };
             const bool live = row0 < p.M && (MODE == kStats || col0 < p.N);
             const uint32_t ta0 = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * 128);
             // 32 columns of the product, from the tile's column c on, leave
             const auto leave = [&](float (&v)[32], int c) {
                 const int col = (int)col0 + c;
-                if ((MODE == kDh || MODE == kDw) && !p.direct) {
+                if ((MODE == kDh || is_dw(MODE)) && !p.direct) {
                     store_acc(v, stage_buf, &tmOut, col, (int)row0, ti.split, p.add != 0, n, lane);
                     return;
                 }
@@ -644,11 +767,31 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                         const float g = exp2_fast((v[j] - lse) * kLog2e) - (target == c + j ? 1.0f : 0.0f);
                         v[j] = ratio == 0.0f ? 0.0f : g;
                     }
+                    const bool here = target >= c && target < c + 32;
+                    if (__any_sync(0xffffffffu, here)) {
+                        float at = 0.0f;
+#pragma unroll
+                        for (int j = 0; j < 32; j++) at = target == c + j ? v[j] : at;
+                        if (here) {
+                            const float lost = left_over(at * ratio);
+                            p.lo[row] = lost;
+                            if (p.g_lo) p.g_lo[row * p.ld_g + col0 + target] = __float2bfloat16_rn(lost);
+                            if (p.owner) {                 // the smallest and the number: in whatever order
+                                Owner* o = p.owner + col0 + target;
+                                atomicMin(&o->first, (int)row);
+                                atomicAdd(&o->count, 1);
+                            }
+                        }
+                    }
                 }
                 store_bf16(v, MODE == kGrad ? ratio : smax, stage_buf, &tmOut, col, (int)row0, n, lane);
             };
             if constexpr (!LONG) {
                 const int buf = iter & 1;
+                // on its way while the tile is computed (held in registers it cost 64 tokens' dh 8 of 148 us)
+                if (takes_extra(MODE) && extra)
+                    for (int u = 0; 8 * u < own_cols; u += 8)
+                        asm volatile("prefetch.global.L1 [%0];" :: "l"(extra + col0 + 8 * u));
                 if (!wait(tfull0 + 8 * buf, (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns)) break;
                 tc::fence_after();
                 ++iter;
@@ -657,6 +800,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     for (int c = 0; c < 128; c += 32) {
                         float v[32];
                         load_acc(v, ta0 + (uint32_t)(buf * kTile + c));
+                        if (takes_extra(MODE)) add_extra(v, c / 8);
                         leave(v, c);
                     }
                 tc::fence_before();
@@ -665,6 +809,9 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 continue;
             }
             float z[128] = {};
+            if (takes_extra(MODE))
+#pragma unroll
+                for (int u = 0; u < 16; u += 4) add_extra(z + 8 * u, u);
             bool ok = true;
             for (int c0 = ti.k0; c0 < ti.k1; c0 += p.chunk, ++iter) {
                 ok = wait(tfull0 + 8 * (iter & 1), (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns);
@@ -711,6 +858,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 }
             }
         }
+        }
         if (lane == 0) tc::bulk_wait_all();
     }
 
@@ -743,6 +891,18 @@ bool map_operand(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int6
     cuuint32_t box[2] = {64u, box_rows};
     cuuint32_t estr[2] = {1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// g and g_lo [2][tokens][ld], box 64 columns x 64 tokens x 1: tokens past the last read as zero
+bool map_halves(CUtensorMap* m, const void* p, int64_t tokens, int64_t cols, int64_t ld) {
+    tmap::EncodeTiledFn enc = tmap::encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)tokens, 2};
+    cuuint64_t strides[2] = {(cuuint64_t)(ld * 2), (cuuint64_t)(tokens * ld * 2)};
+    cuuint32_t box[3] = {64u, (cuuint32_t)kSubK, 1u};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -823,12 +983,13 @@ template <int MODE>
 cudaError_t gemm(GemmParams p, const Operand& a, const Operand& b, const CUtensorMap* out, int64_t K, int splits,
                  int tile_m, int tile_n, int wait, const HeadArgs& args, cudaStream_t st) {
     CUtensorMap ta, tb;
-    if (!map_operand(&ta, a.p, a.rows, a.cols, a.ld, a_mn(MODE) ? kSubK : tile_m / 2) ||
+    if (!(MODE == kDwFull ? map_halves(&ta, a.p, a.rows, a.cols, a.ld)
+                         : map_operand(&ta, a.p, a.rows, a.cols, a.ld, a_mn(MODE) ? kSubK : tile_m / 2)) ||
         !map_operand(&tb, b.p, b.rows, b.cols, b.ld, b_mn(MODE) ? kSubK : tile_n / 2))
         return cudaErrorInvalidValue;
     p.tile_n = tile_n;
     p.k_stages = (int32_t)((K + kSub * kSubK - 1) / (kSub * kSubK));
-    p.chunk = MODE == kDh || MODE == kDw ? kSumChunk : kChunk;
+    p.chunk = MODE == kDh || is_dw(MODE) ? kSumChunk : kChunk;
     p.mma_last = (int32_t)((K - (int64_t)(p.k_stages - 1) * kSub * kSubK + 15) / 16);
     p.tile_m = tile_m;
     p.b_bytes = kSub * (tile_n / 2) * kSubK * 2;
@@ -846,7 +1007,7 @@ cudaError_t gemm(GemmParams p, const Operand& a, const Operand& b, const CUtenso
     p.timeout_ns = args.timeout_ns;
     const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(args.num_sms / 2, total));
     choose_raster(p, K, pairs);
-    if constexpr (MODE == kGrad || MODE == kDh || MODE == kDw)
+    if constexpr (MODE == kGrad || MODE == kDh || is_dw(MODE))
         if (p.split_stages <= p.chunk) return launch_gemm<MODE, false>(p, ta, tb, out ? *out : ta, pairs, st);
     return launch_gemm<MODE, true>(p, ta, tb, out ? *out : ta, pairs, st);
 }
@@ -909,18 +1070,83 @@ __global__ void __launch_bounds__(512) head_join_kernel(const float2* part, int6
     }
 }
 
-// What is taken out of dloss: its largest finite magnitude over the tokens that count
+// What is taken out of dloss: its largest finite magnitude over the tokens that count (the first CTA).  And what
+// g's epilogue and head_target_kernel start from: g_lo or the sums are 0 (`zeros` 16-byte vectors at `zero`), and, with
+// `owner`, no token has any vocabulary row as its target, and each CTA's largest finite |h|.
 __global__ void __launch_bounds__(1024) head_scale_kernel(const float* dloss, const int64_t* targets, int64_t T, int64_t V,
-                                                          float* smax) {
+                                                          float* smax, uint4* zero, int64_t zeros, Owner* owner, float* hmax,
+                                                          const __nv_bfloat16* h, int64_t ldh, int64_t D) {
     __shared__ float part[32];
     pdl_launch_dependents();
-    float m = largest_dloss(dloss, targets, T, V, threadIdx.x, 1024);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < 32; w++) m = fmaxf(m, part[w]);
-        *smax = dloss_scale(m);
+    const int64_t at = (int64_t)blockIdx.x * 1024 + threadIdx.x, step = (int64_t)gridDim.x * 1024;
+    const auto largest = [&](float m) {            // of the CTA, known to the first thread
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+        __syncthreads();
+        if (threadIdx.x == 0)
+            for (int w = 1; w < 32; w++) m = fmaxf(m, part[w]);
+        return m;
+    };
+    if (blockIdx.x == 0) {
+        const float m = largest(largest_dloss(dloss, targets, T, V, threadIdx.x, 1024));
+        if (threadIdx.x == 0) *smax = dloss_scale(m);
     }
+    for (int64_t i = at; i < zeros; i += step) zero[i] = make_uint4(0, 0, 0, 0);
+    if (!owner) return;
+    for (int64_t v = at; v < V; v += step) owner[v] = {INT_MAX, 0};
+    float m = 0.0f;
+    const int64_t per = D / 8;
+#pragma unroll 4
+    for (int64_t i = at; i < T * per; i += step) {
+        const int64_t t = i / per;
+        Pack<__nv_bfloat16, 8> p;
+        float f[8];
+        p.load(h + t * ldh + (i - t * per) * 8);
+        p.unpack(f);
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+            if (fabsf(f[e]) <= FLT_MAX) m = fmaxf(m, fabsf(f[e]));
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    m = largest(m);
+    if (threadIdx.x == 0) hmax[blockIdx.x] = m;
+}
+
+// Adds lo[t] h[t, :] to its target's sums where several tokens have that target (kDw adds a single token's itself): a
+// warp a token, a column a lane.  Bound by the atomics: 200000 tokens of 257 x 256 in some 170 us (all of one target
+// 1.4 ms).
+// Right behind g (`after_g`), or beside dh, which leaves an SM 700 bytes of shared memory and 11000 registers.
+constexpr int kTargetThreads = 256;
+__global__ void __launch_bounds__(kTargetThreads, 5)
+head_target_kernel(const __nv_bfloat16* h, int64_t ldh, const int64_t* targets, const float* lo, int64_t T, int64_t v0,
+                   int64_t n, const Owner* owner, int after_g, Sums sums, float* all_hmax) {
+    if (after_g) pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * (kTargetThreads / 32) + (threadIdx.x >> 5), v = t < T ? targets[t] - v0 : -1;
+    Owner o = {0, 0};
+    if (v >= 0 && v < n) o = owner[v];
+    if (o.count > 1 || blockIdx.x == 0) {
+        float hmax = 0.0f;
+        for (int i = lane; i < sums.hmaxes; i += 32) hmax = fmaxf(hmax, sums.hmax[i]);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) hmax = fmaxf(hmax, __shfl_xor_sync(0xffffffffu, hmax, d));
+        if (blockIdx.x == 0 && threadIdx.x == 0) *all_hmax = hmax;
+        if (o.count > 1) {
+            const int unit = sum_unit(hmax, o.count);
+            const float f = lo[t], up = scalbnf(1.0f, -unit / 2), up2 = scalbnf(1.0f, -unit - (-unit / 2));
+            int32_t* row = sums.rows + (sums.by_row ? v0 + v : o.first) * sums.cols;
+            const __nv_bfloat16* from = h + t * ldh;
+#pragma unroll 8
+            for (int64_t c = lane; c < sums.cols; c += 32) {
+                const float x = __bfloat162float(from[c]);
+                if (fabsf(x) <= FLT_MAX) atomicAdd(row + c, __float2int_rn(f * x * up * up2));
+            }
+        }
+    }
+    // what was launched before this kernel is done when this kernel is
+    if (!after_g && blockIdx.x == 0) pdl_wait();
 }
 
 // dh (or dw) = smax * the sum of the splits' accumulators [splits][T][D], 8 columns a
@@ -976,9 +1202,23 @@ int splits_of(int64_t rows, int64_t cols, int64_t k, int num_sms) {
     const int64_t per = (stages + best - 1) / best;
     return (int)((stages + per - 1) / per);        // those that get any
 }
+// The targets' entries of g, which are by far its largest, enter dw in full.  Either what each lost to BF16 is a
+// second matrix g_lo, zero elsewhere, whose product with h is summed behind g's; or it is added by row, in kDw's
+// epilogue, from h or from the sums of head_target_kernel.  The matrix costs a third of the gradient's operations and
+// the bytes of g twice, the rows a launch beside dh and loads in the epilogue.  So the matrix is for few tokens, whose
+// dw is bound by its writes, for small products, and for vocabularies of whose rows each has several tokens.
+// (Matrix and rows: 64 tokens of 50021 x 4096 226 and 254 us, 129 of 300 x 64 23 and 27, 1909 of 409 x 1448 44 and 54,
+// 200 of 50021 x 4096 332 and 288.)
+bool full_matrix(int64_t tokens, int64_t vocab, int64_t cols, int64_t piece) {
+    const int64_t entries = tokens * piece;
+    return tokens <= kFewTokens || (piece >= vocab && (entries <= 1 << 20 || (tokens >= vocab && entries <= 1 << 24 &&
+                                                                              (double)tokens * vocab * cols <= 8e9)));
+}
+int half_subs(int64_t tokens) { return (int)((tokens + kSubK - 1) / kSubK); }
 // of dw: only where the vocabulary is one piece
 int dw_splits(int64_t tokens, int64_t vocab, int64_t cols, int64_t piece, int num_sms) {
-    return piece < vocab ? 1 : splits_of(vocab, cols, tokens, num_sms);
+    if (piece < vocab) return 1;
+    return splits_of(vocab, cols, full_matrix(tokens, vocab, cols, piece) ? (int64_t)half_subs(tokens) * kSub * kSubK : tokens, num_sms);
 }
 // dh comes out of one product as it is
 bool dh_direct(int splits, int64_t piece, int64_t vocab) { return splits == 1 && piece >= vocab; }
@@ -998,7 +1238,11 @@ size_t head_workspace(int64_t tokens, int64_t vocab, int64_t cols, bool backward
     if (!backward) return (size_t)(head_parts(tokens, vocab, num_sms) * tokens * 8 + round_up(tokens * 4, 16));
     const int64_t piece = piece_cols(tokens, vocab);
     const int splits = splits_of(tokens, cols, std::min(piece, vocab), num_sms), dw = dw_splits(tokens, vocab, cols, piece, num_sms);
-    return (size_t)(256 + (piece < vocab ? 2 : 1) * tokens * piece * 2 +
+    // g and g_lo; or g, the targets' owners, the sums of several tokens and the maxima of h
+    const bool full = full_matrix(tokens, vocab, cols, piece);
+    return (size_t)(256 + (piece < vocab ? 2 : 1) * (full ? 2 : 1) * tokens * piece * 2 + round_up(tokens * 4, 16) +
+                    (full ? 0 : round_up(vocab * (int64_t)sizeof(Owner), 16) + std::min(tokens, vocab) * cols * 4 +
+                                   round_up((num_sms + 1) * 4, 16)) +
                     (dh_direct(splits, piece, vocab) ? 0 : splits * tokens * cols * 4) + (dw > 1 ? dw * vocab * cols * 4 : 0));
 }
 
@@ -1027,7 +1271,7 @@ cudaError_t run_head(const HeadArgs& a, cudaStream_t st) {
                     a.loss, a.lse);
 }
 
-// Per piece: g, then dh and dw from it.  dw runs beside dh's last tiles, and
+// Per piece: g, then dh and dw from it.  dw (or the sums for its epilogue, and then dw) runs beside dh's last tiles, and
 // the next piece's g (in the other of two buffers) beside dw's: each kernel is
 // launched while the one before it drains, so that no SM waits for the end of
 // a wave.  dh waits until everything before it is done: it needs g, and its
@@ -1037,21 +1281,42 @@ cudaError_t run_head(const HeadArgs& a, cudaStream_t st) {
 cudaError_t run_head_backward(const HeadArgs& a, cudaStream_t st) {
     const int64_t T = a.tokens, V = a.vocab, D = a.cols, piece = piece_cols(T, V);
     const int splits = splits_of(T, D, std::min(piece, V), a.num_sms), dw_split = dw_splits(T, V, D, piece, a.num_sms);
-    const bool few = T <= kFewTokens, direct = dh_direct(splits, piece, V);
+    const bool few = T <= kFewTokens, full = full_matrix(T, V, D, piece), direct = dh_direct(splits, piece, V);
     uint8_t* ws = static_cast<uint8_t*>(a.ws);
     float* smax = reinterpret_cast<float*>(ws);
     uint8_t* g0 = ws + 256;
-    float* acc = reinterpret_cast<float*>(g0 + (piece < V ? 2 : 1) * T * piece * 2);
+    const int64_t g_bytes = (full ? 2 : 1) * T * piece * 2;
+    float* lo = reinterpret_cast<float*>(g0 + (piece < V ? 2 : 1) * g_bytes);
+    uint8_t* rest = reinterpret_cast<uint8_t*>(lo) + round_up(T * 4, 16);
+    Owner* owner = full || !a.dw ? nullptr : reinterpret_cast<Owner*>(rest);
+    // what head_scale_kernel clears: g_lo (one piece: behind the only g), or the sums
+    const int64_t zeros = !a.dw ? 0 : full ? T * piece / 8 : std::min(T, V) * D / 4;
+    const int ctas = (int)std::max<int64_t>(1, std::min<int64_t>(a.num_sms, owner ? std::max(V / 2048, T * D / 8192) : zeros / 2048));
+    Sums sums{};
+    float* hmax = nullptr;
+    if (!full) {
+        rest += round_up(V * (int64_t)sizeof(Owner), 16);
+        sums.rows = reinterpret_cast<int32_t*>(rest);
+        sums.cols = D;
+        sums.by_row = V <= T;
+        rest += std::min(T, V) * D * 4;
+        sums.hmax = hmax = reinterpret_cast<float*>(rest);
+        sums.hmaxes = ctas;
+        rest += round_up((a.num_sms + 1) * 4, 16);
+    }
+    float* acc = reinterpret_cast<float*>(rest);
     float* dw_acc = acc + (direct ? 0 : splits * T * D);
     cudaError_t e = cudaSuccess;
     if (!few) {
-        head_scale_kernel<<<1, 1024, 0, st>>>(a.dloss, a.targets, T, V, smax);
+        head_scale_kernel<<<ctas, 1024, 0, st>>>(a.dloss, a.targets, T, V, smax,
+                                                 reinterpret_cast<uint4*>(full ? g0 + T * piece * 2 : reinterpret_cast<uint8_t*>(sums.rows)),
+                                                 zeros, owner, hmax, static_cast<const __nv_bfloat16*>(a.h), a.ldh, D);
         e = cudaGetLastError();
     }
     for (int64_t v0 = 0, i = 0; v0 < V && e == cudaSuccess; v0 += piece, i++) {
         const int64_t n = std::min(piece, V - v0);
         const uint8_t* w = static_cast<const uint8_t*>(a.w) + v0 * a.ldw * 2;
-        uint8_t* g = g0 + (i & 1) * T * piece * 2;
+        uint8_t* g = g0 + (i & 1) * g_bytes;
         GemmParams p{};
         p.targets = a.targets;
         p.vocab = V;
@@ -1059,6 +1324,8 @@ cudaError_t run_head_backward(const HeadArgs& a, cudaStream_t st) {
         p.lse = a.lse;
         p.dloss = a.dloss;
         p.smax = smax;
+        p.lo = lo;
+        p.owner = owner ? owner + v0 : nullptr;
         p.put_smax = i == 0;
         p.M = T;
         p.N = n;
@@ -1066,11 +1333,12 @@ cudaError_t run_head_backward(const HeadArgs& a, cudaStream_t st) {
         const Operand h{a.h, T, D, a.ldh}, wp{w, n, D, a.ldw}, gp{g, T, n, piece};
         // without dw in between, the kernel before may be the dh of the piece that this buffer held
         const int wait = i == 0 ? (few ? kWaitLaunch : kWaitEpilogue) : a.dh && a.dw ? kWaitEnd : kWaitStart;
+        p.g = reinterpret_cast<__nv_bfloat16*>(g);
+        p.g_lo = full && a.dw ? p.g + T * piece : nullptr;
+        p.ld_g = piece;
         if (few) {
             p.M = n;
             p.N = T;
-            p.g = reinterpret_cast<__nv_bfloat16*>(g);
-            p.ld_g = piece;
             e = gemm<kFewGrad>(p, wp, h, nullptr, D, 1, stream_rows(n, a.num_sms), (int)round_up(T, 16), wait, a, st);
         } else {
             if (!tmap::out_2d(&out, g, T, n, piece, true)) return cudaErrorInvalidValue;
@@ -1081,6 +1349,9 @@ cudaError_t run_head_backward(const HeadArgs& a, cudaStream_t st) {
             p.N = D;
             p.add = v0 > 0;
             p.direct = direct;
+            p.w = reinterpret_cast<const __nv_bfloat16*>(w);
+            p.ldw = a.ldw;
+            p.piece_cols = n;
             if (!(direct ? tmap::out_2d(&out, a.dh, T, D, a.ld_dh, true) : map_acc(&out, acc, splits, T, D)))
                 return cudaErrorInvalidValue;
             e = gemm<kDh>(p, gp, wp, &out, n, splits, kTile, kTile, kWaitStart, a, st);
@@ -1093,7 +1364,20 @@ cudaError_t run_head_backward(const HeadArgs& a, cudaStream_t st) {
             if (!(p.direct ? tmap::out_2d(&out, static_cast<uint8_t*>(a.dw) + v0 * a.ld_dw * 2, n, D, a.ld_dw, true)
                            : map_acc(&out, dw_acc, dw_split, V, D)))
                 return cudaErrorInvalidValue;
-            e = gemm<kDw>(p, gp, h, &out, T, dw_split, kTile, kTile, a.dh ? kWaitEnd : kWaitStart, a, st);
+            if (full) {
+                p.half_subs = half_subs(T);
+                p.sub_mmas = (int32_t)((std::min<int64_t>(T, kSubK) + 15) / 16);
+                e = gemm<kDwFull>(p, gp, h, &out, (int64_t)p.half_subs * kSub * kSubK, dw_split, kTile, kTile,
+                                  a.dh ? kWaitEnd : kWaitStart, a, st);
+            } else {
+                constexpr int warps = kTargetThreads / 32;
+                p.h = static_cast<const __nv_bfloat16*>(a.h);
+                p.ldh = a.ldh;
+                p.sums = sums;
+                e = launch_k(true, head_target_kernel, dim3((unsigned)((T + warps - 1) / warps)), kTargetThreads, 0, st, p.h, a.ldh,
+                             a.targets, lo, T, v0, n, p.owner, a.dh ? 0 : 1, sums, hmax + ctas);
+                if (e == cudaSuccess) e = gemm<kDw>(p, gp, h, &out, T, dw_split, kTile, kTile, kWaitEpilogue, a, st);
+            }
         }
     }
     const auto sum = [&](const float* from, int n, int64_t rows, void* to, int64_t ld) {

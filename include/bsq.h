@@ -389,7 +389,8 @@ bsq_status bsq_linear_cross_entropy(const void* h, int64_t ldh, const void* w, i
  * Either of dh, dw may be NULL (a frozen head, or frozen states).  The logits
  * are computed again, a piece of the vocabulary at a time.  g enters the two
  * products in BF16, with the largest |dloss| taken out of it and put back in
- * FP32.  dh, dw on 16-byte boundaries, ld_dh and ld_dw multiples of 8;
+ * FP32; what the target's entry, by far the largest of its row, loses to BF16
+ * is added to dh and dw beside the products.  dh, dw on 16-byte boundaries, ld_dh and ld_dw multiples of 8;
  * dloss: DEVICE float[tokens].  A NaN or infinite dloss[t] of a token that
  * counts makes dh[t] and dw NaN or infinite, as the formula says, and leaves
  * the other rows of dh as they are.  A token that does not count enters dw

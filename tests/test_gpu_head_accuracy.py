@@ -1,7 +1,7 @@
 """How exact the linear cross entropy and its gradient are, with bounds near
 what their sums can hold: the K = 512 read-out of the tensor cores' sums in
-the loss and in the gradient's logits, long sums into dh and dw; and values of
-dloss and logits that are not finite."""
+the loss and in the gradient's logits, long sums into dh and dw, the target's entry
+of g; and values of dloss and logits that are not finite."""
 import math
 
 import pytest
@@ -192,3 +192,61 @@ def test_a_single_row_has_no_pitch(bsq):
     one = torch.randn((2, 20), generator=g, device="cuda").to(BF)[:1, :16]
     assert torch.equal(bsq.linear_cross_entropy(h, one, target * 0)[1],
                        bsq.linear_cross_entropy(h.contiguous(), one.contiguous(), target * 0)[1])
+
+
+@pytest.mark.parametrize("T,V,D", [(40, 20000, 256), (100, 20000, 256), (300, 20000, 256), (1200, 20000, 256),
+                                   (300, 700, 64), (2000, 257, 320), (1200, 1500, 2104), (17000, 1100, 64)])
+def test_gradient_keeps_the_targets_entry(bsq, T, V, D):
+    # p - 1 is the largest entry of a row of g by far, and enters dh and dw in full: what is left of the
+    # rounding of g are the other entries' errors, which are independent and small
+    g = torch.Generator(device="cuda").manual_seed(T + V)
+    w = (torch.randn((V, D), generator=g, device="cuda") * D ** -0.5).to(BF)
+    targets = torch.randint(0, V, (T,), generator=g, device="cuda")
+    targets[T // 2:T // 2 + 9] = targets[3]                       # tokens that share a target
+    h = (torch.randn((T, D), generator=g, device="cuda") + 10 * torch.rand((T, 1), generator=g, device="cuda")
+         * w[targets].float()).to(BF)
+    targets[1] = -100
+    _, lse = bsq.linear_cross_entropy(h, w, targets)
+    dloss = torch.rand(T, generator=g, device="cuda") + 0.5
+    hd, wd = h.double(), w.double()
+    p = (hd @ wd.T - lse.double()[:, None]).exp()
+    scale = torch.where(targets >= 0, dloss.double(), 0.0)[:, None]
+    others = p.scatter(1, targets.clamp(min=0)[:, None], 0.0) * scale
+    gr = scale * (p - torch.nn.functional.one_hot(targets.clamp(min=0), V))
+    both = bsq.linear_cross_entropy_backward(h, w, targets, lse, dloss)
+    for got, want, rest in ((both[0], gr @ wd, others.square() @ wd.square()),
+                            (both[1], gr.T @ hd, others.square().T @ hd.square())):
+        # before the outputs' rounding: each other entry rounded to BF16 (UB / sqrt(3) of it, independent),
+        # the target's logit and sums (4e-6).  Two values e apart are rounded to neighbours one unit (at most
+        # 2 UB) apart with a chance of e / unit: sqrt(e 2 UB) of mean square
+        norm = want.norm()
+        e = UB / math.sqrt(3) * float(rest.sum().sqrt() / norm) + 4e-6
+        apart = float((got.double() - want.to(BF).double()).norm() / norm)
+        assert apart <= 1.5 * math.sqrt(e * 2 * UB), (apart, e)
+    # each gradient alone: the same bits
+    one, two = torch.empty_like(both[0]), torch.empty_like(both[1])
+    bsq.linear_cross_entropy_backward_into(h, w, targets, lse, dloss, one, None)
+    bsq.linear_cross_entropy_backward_into(h, w, targets, lse, dloss, None, two)
+    assert torch.equal(one, both[0]) and torch.equal(two, both[1])
+
+
+@pytest.mark.parametrize("T,V,D", [(50, 3000, 136), (100, 3000, 136), (700, 3000, 136), (9000, 3000, 136),
+                                   (1025, 20000, 2104), (40000, 3000, 8)])
+def test_gradient_of_one_target_for_all(bsq, T, V, D):
+    # every token has the same target: dw's row of it is a sum over all of them, in a fixed order
+    g = torch.Generator(device="cuda").manual_seed(T)
+    h = torch.randn((T, D), generator=g, device="cuda").to(BF)
+    w = (torch.randn((V, D), generator=g, device="cuda") * 0.1).to(BF)
+    targets = torch.full((T,), 2999, device="cuda")
+    _, lse = bsq.linear_cross_entropy(h, w, targets)
+    dloss = torch.ones(T, device="cuda")
+    dh, dw = bsq.linear_cross_entropy_backward(h, w, targets, lse, dloss)
+    p = (h.double() @ w.double().T - lse.double()[:, None]).exp()
+    p[:, 2999] -= 1
+    want = p.T @ h.double()
+    # the row's own rounding, its entries (4e-6: logits and sums) and the rounding of the correction (UB^2)
+    tol = 1.01 * UB * want[2999].abs() + (4e-6 + UB * UB) * (p[:, 2999].abs() @ h.double().abs())
+    assert_close(dw[2999], want[2999], tol, "dw of the target")
+    for _ in range(3):
+        again = bsq.linear_cross_entropy_backward(h, w, targets, lse, dloss)
+        assert torch.equal(again[0], dh) and torch.equal(again[1], dw)
