@@ -1113,18 +1113,19 @@ __global__ void __launch_bounds__(1024) head_scale_kernel(const float* dloss, co
     if (threadIdx.x == 0) hmax[blockIdx.x] = m;
 }
 
-// Adds lo[t] h[t, :] to its target's sums where several tokens have that target (kDw adds a single token's itself): a
-// warp a token, a column a lane.  Bound by the atomics: 200000 tokens of 257 x 256 in some 170 us (all of one target
+// Adds lo[t] h[t, :] to its target's sums where several tokens have that target (kDw adds a single token's itself):
+// `wpt` warps a token, a column a lane.  Bound by the atomics: 200000 tokens of 257 x 256 in some 170 us (all of one target
 // 1.4 ms).
 // Right behind g (`after_g`), or beside dh, which leaves an SM 700 bytes of shared memory and 11000 registers.
 constexpr int kTargetThreads = 256;
 __global__ void __launch_bounds__(kTargetThreads, 5)
 head_target_kernel(const __nv_bfloat16* h, int64_t ldh, const int64_t* targets, const float* lo, int64_t T, int64_t v0,
-                   int64_t n, const Owner* owner, int after_g, Sums sums, float* all_hmax) {
+                   int64_t n, const Owner* owner, int after_g, Sums sums, float* all_hmax, int wpt) {
     if (after_g) pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int64_t t = (int64_t)blockIdx.x * (kTargetThreads / 32) + (threadIdx.x >> 5), v = t < T ? targets[t] - v0 : -1;
+    const int warp = threadIdx.x >> 5;
+    const int64_t t = (int64_t)blockIdx.x * (kTargetThreads / 32 / wpt) + warp / wpt, v = t < T ? targets[t] - v0 : -1;
     Owner o = {0, 0};
     if (v >= 0 && v < n) o = owner[v];
     if (o.count > 1 || blockIdx.x == 0) {
@@ -1139,7 +1140,7 @@ head_target_kernel(const __nv_bfloat16* h, int64_t ldh, const int64_t* targets, 
             int32_t* row = sums.rows + (sums.by_row ? v0 + v : o.first) * sums.cols;
             const __nv_bfloat16* from = h + t * ldh;
 #pragma unroll 8
-            for (int64_t c = lane; c < sums.cols; c += 32) {
+            for (int64_t c = warp % wpt * 32 + lane; c < sums.cols; c += 32 * wpt) {
                 const float x = __bfloat162float(from[c]);
                 if (fabsf(x) <= FLT_MAX) atomicAdd(row + c, __float2int_rn(f * x * up * up2));
             }
@@ -1370,12 +1371,14 @@ cudaError_t run_head_backward(const HeadArgs& a, cudaStream_t st) {
                 e = gemm<kDwFull>(p, gp, h, &out, (int64_t)p.half_subs * kSub * kSubK, dw_split, kTile, kTile,
                                   a.dh ? kWaitEnd : kWaitStart, a, st);
             } else {
-                constexpr int warps = kTargetThreads / 32;
+                int wpt = 1;                       // about 512 columns each
+                while (wpt < kTargetThreads / 32 && D > 512 * wpt) wpt *= 2;
+                const int tokens = kTargetThreads / 32 / wpt;
                 p.h = static_cast<const __nv_bfloat16*>(a.h);
                 p.ldh = a.ldh;
                 p.sums = sums;
-                e = launch_k(true, head_target_kernel, dim3((unsigned)((T + warps - 1) / warps)), kTargetThreads, 0, st, p.h, a.ldh,
-                             a.targets, lo, T, v0, n, p.owner, a.dh ? 0 : 1, sums, hmax + ctas);
+                e = launch_k(true, head_target_kernel, dim3((unsigned)((T + tokens - 1) / tokens)), kTargetThreads, 0, st, p.h, a.ldh,
+                             a.targets, lo, T, v0, n, p.owner, a.dh ? 0 : 1, sums, hmax + ctas, wpt);
                 if (e == cudaSuccess) e = gemm<kDw>(p, gp, h, &out, T, dw_split, kTile, kTile, kWaitEpilogue, a, st);
             }
         }
