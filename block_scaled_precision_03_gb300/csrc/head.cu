@@ -38,7 +38,7 @@
 //
 // Measured, BF16: the loss of 8192 tokens, 65536 x 4096, in 2.46 to 2.59 ms (up to 1790 TFLOP/s,
 // what a library product holds under the power cap, 0.92 of its burst; boxes differ),
-// its gradient in 7.6 to 8.0 ms (1650 to 1740 TFLOP/s: bound by the power cap, and dh reads w
+// its gradient in 7.7 to 8.0 ms (1650 to 1720 TFLOP/s: bound by the power cap, and dh reads w
 // and dw h again); 64 tokens' gradient, 50021 x 4096, in 226 us (w read twice, dw written); 7 tokens, 50021 x 4096, in 70 us (5.9 TB/s, 0.88 of a copy's
 // rate), the rest the start of the stream, the last tile and the join.  Calls
 // below a few microseconds of work take 10 us (loss) to 20 us (gradient): two to
@@ -86,7 +86,7 @@ constexpr int kChunk = 4;
 // and for dh and dw (K = 4096), whose results are rounded to BF16: a sum loses some 6e-6,
 // whatever the number of tokens or columns.  (In one accumulator dw over 200003 tokens
 // came out 1.2e-3 too small, dh over 131072 columns 5.8e-4.)  The gradient of the batch
-// takes 7.6 to 7.7 ms with 16 or 32, 8.0 with 4.
+// took 7.6 to 7.7 ms with 16 or 32, 8.0 with 4.
 constexpr int kSumChunk = 32;
 constexpr int kSubBytes = 128 * kSubK * 2;          // one CTA's 128 rows of an operand, one sub-step
 constexpr int kOpBytes = kSub * kSubBytes;
