@@ -14,7 +14,8 @@ Names follow the C ABI in ``include/bsq.h``:
     sync_status()                     -> raises BsqError on a recorded device fault
 
 The operators around the layer (expert sort, layer norm, linear cross
-entropy, gradient clipping) are bound in ``ops.py`` and exported here.
+entropy, linear layers with their epilogue, the gated feed-forward, gradient
+clipping, AdamW) are bound in ``ops.py`` and exported here.
 """
 from __future__ import annotations
 
@@ -356,9 +357,11 @@ def version() -> str:
     return lib().bsq_version().decode()
 
 
-from .ops import (GradList, MoePlan, _signatures, clip_grad_norm, clip_grad_norm_into, grad_norm,  # noqa: E402
-                  layer_norm, layer_norm_backward, layer_norm_backward_into, layer_norm_into, linear_cross_entropy,
-                  linear_cross_entropy_backward, linear_cross_entropy_backward_into, linear_cross_entropy_into,
-                  moe_combine, moe_combine_backward, moe_combine_backward_into, moe_combine_into, moe_dispatch,
-                  moe_dispatch_backward, moe_dispatch_into, moe_gather, moe_gather_into, moe_plan, moe_sort,
-                  moe_sort_into)
+from .ops import (ACTIVATIONS, AdamWList, GradList, MoePlan, _signatures, adamw_states, adamw_step,  # noqa: E402
+                  clip_grad_norm, clip_grad_norm_into, gated_linear, gated_linear_backward, gated_linear_backward_into,
+                  gated_linear_into, gemm_gated, gemm_gated_into, gemm_linear, gemm_linear_into, grad_norm, layer_norm,
+                  layer_norm_backward, layer_norm_backward_into, layer_norm_into, linear, linear_backward,
+                  linear_backward_into, linear_cross_entropy, linear_cross_entropy_backward,
+                  linear_cross_entropy_backward_into, linear_cross_entropy_into, linear_into, moe_combine,
+                  moe_combine_backward, moe_combine_backward_into, moe_combine_into, moe_dispatch, moe_dispatch_backward,
+                  moe_dispatch_into, moe_gather, moe_gather_into, moe_plan, moe_sort, moe_sort_into)

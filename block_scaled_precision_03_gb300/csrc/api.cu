@@ -37,6 +37,7 @@ unsigned* status_ptr() {
     return static_cast<unsigned*>(p);
 }
 
+bool out_type_ok(int32_t t) { return t == BSQ_OUT_F32 || t == BSQ_OUT_BF16; }
 bool valid_fmt(int32_t f) { return f >= BSQ_MXFP8_E4M3 && f <= BSQ_NVFP4_E2M1; }
 int blk(int32_t f) { return f == BSQ_NVFP4_E2M1 ? 16 : 32; }
 bool fp4(int32_t f) { return f == BSQ_MXFP4_E2M1 || f == BSQ_NVFP4_E2M1; }
@@ -199,20 +200,10 @@ static bsq_status check_gemm_pair(const bsq_tensor* A, const bsq_tensor* B) {
     return BSQ_ERR_UNSUPPORTED;
 }
 
-// bsq_gemm and bsq_debug_gemm_timeout: checks and launch with a given wait
-// limit; `force_single` selects the 1-CTA kernel.
-static bsq_status gemm_common(const bsq_tensor* A, const bsq_tensor* B, void* C, int32_t out_type, uint64_t timeout_ns,
-                              bool force_single, void* stream) {
-    bsq_status s = check_gemm_pair(A, B);
-    if (s != BSQ_OK) return s;
-    if (!C || (out_type != BSQ_OUT_F32 && out_type != BSQ_OUT_BF16)) return BSQ_ERR_INVALID_ARG;
-    if (A->rows > 0x7FFFFF00LL || B->rows > 0x7FFFFF00LL) return BSQ_ERR_UNSUPPORTED;
-    if (!al16(C)) return BSQ_ERR_ALIGNMENT;
-    // MXFP4 runs on the CTA-pair kernel only
-    if (force_single && A->fmt == BSQ_MXFP4_E2M1) return BSQ_ERR_UNSUPPORTED;
-    unsigned* st = status_ptr();
-    if (!st) return BSQ_ERR_CUDA;
-    bsq::GemmArgs a{};
+// the operands of a dense product
+static bsq_status dense_args(const bsq_tensor* A, const bsq_tensor* B, uint64_t timeout_ns, bsq::GemmArgs& a) {
+    a.status = status_ptr();
+    if (!a.status) return BSQ_ERR_CUDA;
     a.fmt_a = A->fmt;
     a.fmt_b = B->fmt;
     a.a_codes = static_cast<const uint8_t*>(A->codes);
@@ -224,18 +215,110 @@ static bsq_status gemm_common(const bsq_tensor* A, const bsq_tensor* B, void* C,
     a.M = A->rows;
     a.N = B->rows;
     a.K = A->cols;
+    a.num_sms = num_sms();
+    a.timeout_ns = timeout_ns;
+    return BSQ_OK;
+}
+
+// bsq_gemm and bsq_debug_gemm_timeout: checks and launch with a given wait
+// limit; `force_single` selects the 1-CTA kernel.
+static bsq_status gemm_common(const bsq_tensor* A, const bsq_tensor* B, void* C, int32_t out_type, uint64_t timeout_ns,
+                              bool force_single, void* stream) {
+    bsq_status s = check_gemm_pair(A, B);
+    if (s != BSQ_OK) return s;
+    if (!C || (out_type != BSQ_OUT_F32 && out_type != BSQ_OUT_BF16)) return BSQ_ERR_INVALID_ARG;
+    if (A->rows > 0x7FFFFF00LL || B->rows > 0x7FFFFF00LL) return BSQ_ERR_UNSUPPORTED;
+    if (!al16(C)) return BSQ_ERR_ALIGNMENT;
+    // MXFP4 runs on the CTA-pair kernel only
+    if (force_single && A->fmt == BSQ_MXFP4_E2M1) return BSQ_ERR_UNSUPPORTED;
+    bsq::GemmArgs a{};
+    if ((s = dense_args(A, B, timeout_ns, a)) != BSQ_OK) return s;
     a.C = C;
     a.out_bf16 = out_type == BSQ_OUT_BF16;
-    a.num_groups = 0;
     a.single_cta = force_single || env_single_cta();
-    a.num_sms = num_sms();
-    a.status = st;
-    a.timeout_ns = timeout_ns;
     return from_cuda(bsq::run_gemm(a, static_cast<cudaStream_t>(stream)));
 }
 
 bsq_status bsq_gemm(const bsq_tensor* A, const bsq_tensor* B, void* C, int32_t out_type, void* stream) {
     return gemm_common(A, B, C, out_type, kDefaultTimeoutNs, false, stream);
+}
+
+// ---- products with an epilogue
+// an output or a residual of the epilogue: any address and pitch of whole elements
+static bsq_status check_out(const void* p, int64_t ld, int32_t type, int64_t cols) {
+    if (ld < cols) return BSQ_ERR_INVALID_ARG;
+    return reinterpret_cast<uintptr_t>(p) % (type == BSQ_OUT_BF16 ? 2 : 4) ? BSQ_ERR_ALIGNMENT : BSQ_OK;
+}
+static size_t fused_bytes(int32_t fmt, int64_t tokens, int64_t out, int64_t cols, bool gated) {
+    if (!valid_fmt(fmt) || tokens < 1 || out < 1 || cols < 1 || tokens > 0x7FFFFF00LL || out > bsq::kLinearMaxOut) return 0;
+    return bsq::gemm_fused_workspace(fmt, tokens, out, cols, gated, num_sms());
+}
+
+size_t bsq_gemm_linear_workspace_bytes(int32_t fmt, int64_t tokens, int64_t out, int64_t cols) {
+    return fused_bytes(fmt, tokens, out, cols, false);
+}
+size_t bsq_gemm_gated_workspace_bytes(int32_t fmt, int64_t tokens, int64_t out, int64_t cols) {
+    return fused_bytes(fmt, tokens, out, cols, true);
+}
+
+static bsq_status fused_common(const bsq_tensor* A, const bsq_tensor* B, int32_t activation, void* y, int64_t ldy,
+                               int32_t type, void* workspace, size_t workspace_bytes, bool gated, bsq::GemmArgs& a,
+                               bsq::LinearArgs& l) {
+    bsq_status s = check_gemm_pair(A, B);
+    if (s != BSQ_OK) return s;
+    if (!y || !out_type_ok(type) || activation < BSQ_ACT_IDENTITY || activation > BSQ_ACT_GELU_TANH) return BSQ_ERR_INVALID_ARG;
+    if (A->rows > 0x7FFFFF00LL || B->rows > bsq::kLinearMaxOut) return BSQ_ERR_UNSUPPORTED;
+    if ((s = check_out(y, ldy, type, B->rows)) != BSQ_OK) return s;
+    const size_t need = fused_bytes(A->fmt, A->rows, B->rows, A->cols, gated);
+    if (need && (!workspace || workspace_bytes < need)) return BSQ_ERR_INVALID_ARG;
+    if (need && !al16(workspace)) return BSQ_ERR_ALIGNMENT;
+    if ((s = dense_args(A, B, kDefaultTimeoutNs, a)) != BSQ_OK) return s;
+    l.act = activation;
+    l.y = y;
+    l.ldy = ldy;
+    l.y_bf16 = type == BSQ_OUT_BF16;
+    l.ws = workspace;
+    return BSQ_OK;
+}
+
+bsq_status bsq_gemm_linear(const bsq_tensor* A, const bsq_tensor* B, const void* bias, int32_t bias_type,
+                           int32_t activation, const void* residual, int64_t ld_residual, void* y, int64_t ldy,
+                           int32_t type, void* z, int64_t ldz, void* workspace, size_t workspace_bytes, void* stream) {
+    bsq::GemmArgs a{};
+    bsq::LinearArgs l{};
+    if (bias && !out_type_ok(bias_type)) return BSQ_ERR_INVALID_ARG;
+    bsq_status s = fused_common(A, B, activation, y, ldy, type, workspace, workspace_bytes, false, a, l);
+    if (s != BSQ_OK) return s;
+    if (bias && (s = check_out(bias, B->rows, bias_type, B->rows)) != BSQ_OK) return s;
+    if (residual && (s = check_out(residual, ld_residual, type, B->rows)) != BSQ_OK) return s;
+    if (z && (s = check_out(z, ldz, BSQ_OUT_BF16, B->rows)) != BSQ_OK) return s;
+    l.bias = bias;
+    l.bias_bf16 = bias_type == BSQ_OUT_BF16;
+    l.residual = residual;
+    l.ld_res = ld_residual;
+    l.z = z;
+    l.ldz = ldz;
+    return from_cuda(bsq::run_gemm_linear(a, l, static_cast<cudaStream_t>(stream)));
+}
+
+bsq_status bsq_gemm_gated(const bsq_tensor* A, const bsq_tensor* B_gate, const bsq_tensor* B_up, int32_t activation,
+                          void* h, int64_t ldh, int32_t type, void* gate, int64_t ld_gate, void* up, int64_t ld_up,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+    bsq::GemmArgs a{}, b{};
+    bsq::LinearArgs l{};
+    bsq_status s = fused_common(A, B_gate, activation, h, ldh, type, workspace, workspace_bytes, true, a, l);
+    if (s != BSQ_OK) return s;
+    if ((s = check_gemm_pair(A, B_up)) != BSQ_OK) return s;
+    if (B_up->fmt != B_gate->fmt || B_up->rows != B_gate->rows || (gate == nullptr) != (up == nullptr)) return BSQ_ERR_INVALID_ARG;
+    if (gate && ((s = check_out(gate, ld_gate, BSQ_OUT_BF16, B_gate->rows)) != BSQ_OK ||
+                 (s = check_out(up, ld_up, BSQ_OUT_BF16, B_gate->rows)) != BSQ_OK))
+        return s;
+    if ((s = dense_args(A, B_up, kDefaultTimeoutNs, b)) != BSQ_OK) return s;
+    l.z = gate;
+    l.ldz = ld_gate;
+    l.u = up;
+    l.ldu = ld_up;
+    return from_cuda(bsq::run_gemm_gated(a, b, l, static_cast<cudaStream_t>(stream)));
 }
 
 bsq_status bsq_debug_gemm_timeout(const bsq_tensor* A, const bsq_tensor* B, void* C, int32_t out_type,

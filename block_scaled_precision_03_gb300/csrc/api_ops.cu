@@ -1,7 +1,8 @@
 // C ABI of the operators around the layer (expert sort, layer norm, linear
-// cross entropy, gradient clipping): argument checks on the host, then
-// dispatch to the kernels.  A rejected call launches nothing.
+// cross entropy, linear layers and the gated feed-forward, gradient clipping,
+// AdamW): argument checks on the host, then dispatch to the kernels.  A rejected call launches nothing.
 #include <cmath>
+#include <initializer_list>
 #include "../../include/bsq.h"
 #include "internal.h"
 
@@ -127,9 +128,55 @@ bsq_status clip_common(const bsq_grad* grads, int32_t count, bool scale, float m
     return from_cuda(bsq::run_clip(a, static_cast<cudaStream_t>(stream)));
 }
 
+// ---- linear layers
+bool valid_act(int32_t a) { return a >= BSQ_ACT_IDENTITY && a <= BSQ_ACT_GELU_TANH; }
+bool linear_sizes_ok(int64_t tokens, int64_t out, int64_t cols) { return tokens >= 1 && out >= 1 && cols >= 1; }
+bool linear_sizes_supported(int64_t tokens, int64_t out, int64_t cols) {
+    return tokens <= kMaxRows && out <= bsq::kLinearMaxOut && cols <= kMaxRows;
+}
+// a matrix that TMA reads or writes, or null
+bsq_status check_tiled(const void* p, int64_t ld, int64_t rows, int64_t cols) {
+    if (!p) return BSQ_OK;
+    if (ld < cols) return BSQ_ERR_INVALID_ARG;
+    return aligned(p, 16) && (rows == 1 || ld % 8 == 0) ? BSQ_OK : BSQ_ERR_ALIGNMENT;
+}
+bsq_status check_optional(const void* p, int64_t ld, int32_t type, int64_t cols) {
+    return p ? check_matrix(p, ld, type, cols) : BSQ_OK;
+}
+bsq_status first_bad(std::initializer_list<bsq_status> all) {
+    for (bsq_status s : all)
+        if (s == BSQ_ERR_INVALID_ARG) return s;
+    for (bsq_status s : all)
+        if (s != BSQ_OK) return s;
+    return BSQ_OK;
+}
+// a row's pitch where there is one row only: TMA wants a multiple of 16 bytes
+int64_t pitch(int64_t ld, int64_t rows, int64_t cols) { return rows == 1 ? cols : ld; }
+
+bsq_status linear_common(bsq::LinearArgs& a, int64_t tokens, int64_t out, int64_t cols, int32_t activation) {
+    if (!linear_sizes_ok(tokens, out, cols) || !valid_act(activation)) return BSQ_ERR_INVALID_ARG;
+    if (!linear_sizes_supported(tokens, out, cols)) return BSQ_ERR_UNSUPPORTED;
+    if (cols % 8) return BSQ_ERR_ALIGNMENT;
+    a.tokens = tokens;
+    a.out = out;
+    a.cols = cols;
+    a.act = activation;
+    a.num_sms = bsq::device_sms();
+    a.status = bsq::device_status();
+    a.timeout_ns = kWaitNs;
+    return a.status ? BSQ_OK : BSQ_ERR_CUDA;
+}
+size_t linear_bytes(int64_t tokens, int64_t out, int64_t cols, bool gated, bool backward) {
+    if (!linear_sizes_ok(tokens, out, cols) || !linear_sizes_supported(tokens, out, cols)) return 0;
+    return backward ? bsq::linear_backward_workspace(tokens, out, cols, gated, bsq::device_sms())
+                    : bsq::linear_workspace(tokens, out, cols, gated, bsq::device_sms());
+}
+bool finite_and_not_negative(double x) { return x >= 0.0 && !std::isinf(x); }
+
 }  // namespace
 
 extern "C" {
+
 
 size_t bsq_moe_workspace_bytes(int64_t tokens, int32_t k, int32_t num_experts) {
     if (!moe_sizes_ok(tokens, k, num_experts) || !moe_sizes_supported(tokens, k, num_experts)) return 0;
@@ -332,6 +379,184 @@ bsq_status bsq_clip_grad_norm(const bsq_grad* grads, int32_t count, float max_no
                               void* workspace, size_t workspace_bytes, void* stream) {
     if (!(max_norm >= 0.0f) || !(eps >= 0.0f)) return BSQ_ERR_INVALID_ARG;
     return clip_common(grads, count, true, max_norm, eps, norm, workspace, workspace_bytes, stream);
+}
+
+size_t bsq_linear_workspace_bytes(int64_t tokens, int64_t out, int64_t cols) {
+    return linear_bytes(tokens, out, cols, false, false);
+}
+size_t bsq_linear_backward_workspace_bytes(int64_t tokens, int64_t out, int64_t cols) {
+    return linear_bytes(tokens, out, cols, false, true);
+}
+size_t bsq_gated_linear_workspace_bytes(int64_t tokens, int64_t out, int64_t cols) {
+    return linear_bytes(tokens, out, cols, true, false);
+}
+size_t bsq_gated_linear_backward_workspace_bytes(int64_t tokens, int64_t out, int64_t cols) {
+    return linear_bytes(tokens, out, cols, true, true);
+}
+
+bsq_status bsq_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t tokens, int64_t out, int64_t cols,
+                      const void* bias, int32_t bias_type, int32_t activation, const void* residual,
+                      int64_t ld_residual, void* y, int64_t ldy, int32_t type, void* z, int64_t ldz, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+    bsq::LinearArgs a{};
+    if (!x || !w || !valid_type(type) || (bias && !valid_type(bias_type))) return BSQ_ERR_INVALID_ARG;
+    bsq_status s = linear_common(a, tokens, out, cols, activation);
+    if (s != BSQ_OK) return s;
+    s = first_bad({check_tiled(x, ldx, tokens, cols), check_tiled(w, ldw, out, cols), check_matrix(y, ldy, type, out),
+                   check_optional(residual, ld_residual, type, out), check_optional(z, ldz, BSQ_OUT_BF16, out),
+                   bias && !aligned(bias, elem(bias_type)) ? BSQ_ERR_ALIGNMENT : BSQ_OK});
+    if (s != BSQ_OK) return s;
+    s = check_workspace(workspace, workspace_bytes, linear_bytes(tokens, out, cols, false, false));
+    if (s != BSQ_OK) return s;
+    a.x = x;
+    a.ldx = pitch(ldx, tokens, cols);
+    a.w = w;
+    a.ldw = pitch(ldw, out, cols);
+    a.bias = bias;
+    a.bias_bf16 = bias_type == BSQ_OUT_BF16;
+    a.residual = residual;
+    a.ld_res = ld_residual;
+    a.y = y;
+    a.ldy = ldy;
+    a.y_bf16 = type == BSQ_OUT_BF16;
+    a.z = z;
+    a.ldz = ldz;
+    a.ws = workspace;
+    return from_cuda(bsq::run_linear(a, false, static_cast<cudaStream_t>(stream)));
+}
+
+bsq_status bsq_linear_backward(const void* dy, int64_t ld_dy, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                               int64_t tokens, int64_t out, int64_t cols, int32_t activation, const void* z, int64_t ldz,
+                               void* dx, int64_t ld_dx, void* dw, int64_t ld_dw, float* dbias, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+    bsq::LinearArgs a{};
+    if ((!dx && !dw && !dbias) || (dx && !w) || (dw && !x)) return BSQ_ERR_INVALID_ARG;
+    bsq_status s = linear_common(a, tokens, out, cols, activation);
+    if (s != BSQ_OK) return s;
+    const bool reads_z = activation != BSQ_ACT_IDENTITY;
+    if (reads_z && !z) return BSQ_ERR_INVALID_ARG;
+    s = first_bad({check_matrix(dy, ld_dy, BSQ_OUT_BF16, out), check_optional(reads_z ? z : nullptr, ldz, BSQ_OUT_BF16, out),
+                   check_tiled(dw ? x : nullptr, ldx, tokens, cols), check_tiled(dx ? w : nullptr, ldw, out, cols),
+                   check_tiled(dx, ld_dx, tokens, cols), check_tiled(dw, ld_dw, out, cols),
+                   aligned(dbias, 4) ? BSQ_OK : BSQ_ERR_ALIGNMENT});
+    if (s != BSQ_OK) return s;
+    s = check_workspace(workspace, workspace_bytes, linear_bytes(tokens, out, cols, false, true));
+    if (s != BSQ_OK) return s;
+    a.x = x;
+    a.ldx = pitch(ldx, tokens, cols);
+    a.w = w;
+    a.ldw = pitch(ldw, out, cols);
+    a.dy = dy;
+    a.ld_dy = ld_dy;
+    a.z = reads_z ? const_cast<void*>(z) : nullptr;
+    a.ldz = ldz;
+    a.dx = dx;
+    a.ld_dx = pitch(ld_dx, tokens, cols);
+    a.dw = dw;
+    a.ld_dw = pitch(ld_dw, out, cols);
+    a.dbias = dbias;
+    a.ws = workspace;
+    return from_cuda(bsq::run_linear_backward(a, false, static_cast<cudaStream_t>(stream)));
+}
+
+bsq_status bsq_gated_linear(const void* x, int64_t ldx, const void* w_gate, int64_t ld_gate_w, const void* w_up,
+                            int64_t ld_up_w, int64_t tokens, int64_t out, int64_t cols, int32_t activation, void* h,
+                            int64_t ldh, int32_t type, void* gate, int64_t ld_gate, void* up, int64_t ld_up,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+    bsq::LinearArgs a{};
+    if (!x || !w_gate || !w_up || !valid_type(type) || (gate == nullptr) != (up == nullptr)) return BSQ_ERR_INVALID_ARG;
+    bsq_status s = linear_common(a, tokens, out, cols, activation);
+    if (s != BSQ_OK) return s;
+    s = first_bad({check_tiled(x, ldx, tokens, cols), check_tiled(w_gate, ld_gate_w, out, cols),
+                   check_tiled(w_up, ld_up_w, out, cols), check_matrix(h, ldh, type, out),
+                   check_optional(gate, ld_gate, BSQ_OUT_BF16, out), check_optional(up, ld_up, BSQ_OUT_BF16, out)});
+    if (s != BSQ_OK) return s;
+    s = check_workspace(workspace, workspace_bytes, linear_bytes(tokens, out, cols, true, false));
+    if (s != BSQ_OK) return s;
+    a.x = x;
+    a.ldx = pitch(ldx, tokens, cols);
+    a.w = w_gate;
+    a.ldw = pitch(ld_gate_w, out, cols);
+    a.w2 = w_up;
+    a.ldw2 = pitch(ld_up_w, out, cols);
+    a.y = h;
+    a.ldy = ldh;
+    a.y_bf16 = type == BSQ_OUT_BF16;
+    a.z = gate;
+    a.ldz = ld_gate;
+    a.u = up;
+    a.ldu = ld_up;
+    a.ws = workspace;
+    return from_cuda(bsq::run_linear(a, true, static_cast<cudaStream_t>(stream)));
+}
+
+bsq_status bsq_gated_linear_backward(const void* dh, int64_t ld_dh, const void* x, int64_t ldx, const void* w_gate,
+                                     int64_t ld_gate_w, const void* w_up, int64_t ld_up_w, int64_t tokens, int64_t out,
+                                     int64_t cols, int32_t activation, const void* gate, int64_t ld_gate, const void* up,
+                                     int64_t ld_up, void* dx, int64_t ld_dx, void* dw_gate, int64_t ld_dw_gate,
+                                     void* dw_up, int64_t ld_dw_up, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+    bsq::LinearArgs a{};
+    if ((!dx && !dw_gate) || (dw_gate == nullptr) != (dw_up == nullptr) || (dx && (!w_gate || !w_up)) || (dw_gate && !x) ||
+        !gate || !up)
+        return BSQ_ERR_INVALID_ARG;
+    bsq_status s = linear_common(a, tokens, out, cols, activation);
+    if (s != BSQ_OK) return s;
+    s = first_bad({check_matrix(dh, ld_dh, BSQ_OUT_BF16, out), check_matrix(gate, ld_gate, BSQ_OUT_BF16, out),
+                   check_matrix(up, ld_up, BSQ_OUT_BF16, out), check_tiled(dw_gate ? x : nullptr, ldx, tokens, cols),
+                   check_tiled(dx ? w_gate : nullptr, ld_gate_w, out, cols), check_tiled(dx ? w_up : nullptr, ld_up_w, out, cols),
+                   check_tiled(dx, ld_dx, tokens, cols), check_tiled(dw_gate, ld_dw_gate, out, cols),
+                   check_tiled(dw_up, ld_dw_up, out, cols)});
+    if (s != BSQ_OK) return s;
+    s = check_workspace(workspace, workspace_bytes, linear_bytes(tokens, out, cols, true, true));
+    if (s != BSQ_OK) return s;
+    a.x = x;
+    a.ldx = pitch(ldx, tokens, cols);
+    a.w = w_gate;
+    a.ldw = pitch(ld_gate_w, out, cols);
+    a.w2 = w_up;
+    a.ldw2 = pitch(ld_up_w, out, cols);
+    a.dy = dh;
+    a.ld_dy = ld_dh;
+    a.z = const_cast<void*>(gate);
+    a.ldz = ld_gate;
+    a.u = const_cast<void*>(up);
+    a.ldu = ld_up;
+    a.dx = dx;
+    a.ld_dx = pitch(ld_dx, tokens, cols);
+    a.dw = dw_gate;
+    a.ld_dw = pitch(ld_dw_gate, out, cols);
+    a.dw2 = dw_up;
+    a.ld_dw2 = pitch(ld_dw_up, out, cols);
+    a.ws = workspace;
+    return from_cuda(bsq::run_linear_backward(a, true, static_cast<cudaStream_t>(stream)));
+}
+
+bsq_status bsq_adamw(const bsq_adamw_tensor* tensors, int32_t count, const bsq_adamw_options* options, void* stream) {
+    if (!tensors || count < 1 || !options || options->reserved != 0) return BSQ_ERR_INVALID_ARG;
+    const bsq_adamw_options& o = *options;
+    if (!finite_and_not_negative(o.lr) || !finite_and_not_negative(o.eps) || !finite_and_not_negative(o.weight_decay) ||
+        !(o.beta1 >= 0.0 && o.beta1 < 1.0) || !(o.beta2 >= 0.0 && o.beta2 < 1.0) || (!o.step_device && o.step < 1) ||
+        (o.norm && (!(o.max_norm >= 0.0) || !finite_and_not_negative(o.clip_eps))))
+        return BSQ_ERR_INVALID_ARG;
+    if (count > kMaxGrads) return BSQ_ERR_UNSUPPORTED;
+    if (!aligned(o.step_device, 8) || !aligned(o.lr_device, 4) || !aligned(o.norm, 4)) return BSQ_ERR_ALIGNMENT;
+    int64_t total = 0;
+    for (int32_t i = 0; i < count; i++) {
+        const bsq_adamw_tensor& t = tensors[i];
+        if (!valid_type(t.param_type) || !valid_type(t.grad_type) || t.reserved != 0 || t.n < 0 ||
+            (t.state != BSQ_MOMENTS_F32 && t.state != BSQ_MOMENTS_8BIT))
+            return BSQ_ERR_INVALID_ARG;
+        if (t.n > kMaxElements || (total += t.n) > kMaxElements) return BSQ_ERR_UNSUPPORTED;
+        if (t.n == 0) continue;
+        const bool codes = t.state == BSQ_MOMENTS_8BIT;
+        if (!t.param || !t.grad || !t.m || !t.v || (codes && (!t.m_scales || !t.v_scales))) return BSQ_ERR_INVALID_ARG;
+        if (!aligned(t.param, elem(t.param_type)) || !aligned(t.grad, elem(t.grad_type)) || !aligned(t.copy, 2) ||
+            (!codes && (!aligned(t.m, 4) || !aligned(t.v, 4))))
+            return BSQ_ERR_ALIGNMENT;
+    }
+    bsq::AdamwArgs a{tensors, count, options, bsq::device_sms()};
+    return from_cuda(bsq::run_adamw(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

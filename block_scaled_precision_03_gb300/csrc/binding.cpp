@@ -23,7 +23,12 @@ namespace {
     F(bsq_moe_workspace_bytes) F(bsq_moe_sort) F(bsq_moe_dispatch) F(bsq_moe_gather) F(bsq_moe_combine) \
     F(bsq_moe_combine_backward) F(bsq_layer_norm) F(bsq_layer_norm_workspace_bytes)                    \
     F(bsq_layer_norm_backward) F(bsq_linear_cross_entropy_workspace_bytes) F(bsq_linear_cross_entropy) \
-    F(bsq_linear_cross_entropy_backward) F(bsq_grad_norm) F(bsq_clip_grad_norm)
+    F(bsq_linear_cross_entropy_backward) F(bsq_grad_norm) F(bsq_clip_grad_norm)                        \
+    F(bsq_codes_bytes) F(bsq_scales_bytes) F(bsq_linear_workspace_bytes) F(bsq_linear)                 \
+    F(bsq_linear_backward_workspace_bytes) F(bsq_linear_backward) F(bsq_gated_linear_workspace_bytes)  \
+    F(bsq_gated_linear) F(bsq_gated_linear_backward_workspace_bytes) F(bsq_gated_linear_backward)      \
+    F(bsq_gemm_linear_workspace_bytes) F(bsq_gemm_linear) F(bsq_gemm_gated_workspace_bytes)            \
+    F(bsq_gemm_gated) F(bsq_adamw)
 
 struct Api {
 #define F(name) decltype(&::name) name;
@@ -33,6 +38,7 @@ struct Api {
 
 PyObject* error_class;             // BsqError
 PyObject *s_num_experts, *s_offsets, *s_slot_row, *s_row_slot, *s_cuda_stream;
+PyObject *s_fmt, *s_rows, *s_cols, *s_codes, *s_scales, *s_tensor_scale;
 
 // A refused call: the Python error is set.
 struct Refused {};
@@ -426,6 +432,225 @@ ENTRY(linear_cross_entropy_backward_into) {
     });
 }
 
+// ---- linear layers
+int32_t activation(PyObject* o, int32_t standard) {
+    if (none(o)) return standard;
+    static const char* const names[] = {"identity", "relu", "silu", "gelu", "gelu_tanh"};
+    if (PyUnicode_Check(o)) {
+        for (int32_t i = 0; i < 5; i++)
+            if (PyUnicode_CompareWithASCIIString(o, names[i]) == 0) return i;
+        refuse(BSQ_ERR_INVALID_ARG, "activation must be identity, relu, silu, gelu or gelu_tanh");
+    }
+    const long v = PyLong_AsLong(o);
+    if (v == -1 && PyErr_Occurred()) throw Refused{};
+    if (v < 0 || v > 4) refuse(BSQ_ERR_INVALID_ARG, "activation %ld", v);
+    return (int32_t)v;
+}
+// BF16 matrices, or none
+Matrix bf16_matrix(PyObject* o, const char* name, int64_t rows = -1, int64_t cols = -1) {
+    const Matrix m = head_matrix(o, name, rows, cols);
+    if (m.t->scalar_type() != at::kBFloat16)
+        refuse(BSQ_ERR_UNSUPPORTED, "%s: %s (BFloat16 is supported)", name, c10::toString(m.t->scalar_type()));
+    return m;
+}
+Matrix maybe_bf16(PyObject* o, const char* name, int64_t rows, int64_t cols) {
+    return none(o) ? Matrix{} : bf16_matrix(o, name, rows, cols);
+}
+// bias, of either type, or none
+const void* bias_of(PyObject* o, int64_t n, int32_t& type) {
+    type = BSQ_OUT_F32;
+    if (none(o)) return nullptr;
+    const at::Tensor& t = tensor(o, "bias");
+    type = type_of(t, "bias");
+    return vector(o, "bias", n, t.scalar_type());
+}
+
+ENTRY(linear_into) {
+    return guarded([&] {
+        static const char* const names[] = {"x", "w", "y", "bias", "residual", "activation", "z", "stream"};
+        const Args a("linear_into", names, 3, args, n, kwnames);
+        const Matrix x = bf16_matrix(a[0], "x"), w = bf16_matrix(a[1], "w", -1, x.cols), y = matrix(a[2], "y", x.rows, w.rows);
+        Matrix r;
+        if (!none(a[4])) r = matrix(a[4], "residual", x.rows, w.rows, &y);
+        const Matrix z = maybe_bf16(a[6], "z", x.rows, w.rows);
+        int32_t type;
+        const void* bias = bias_of(a[3], w.rows, type);
+        const int32_t act = activation(a[5], BSQ_ACT_IDENTITY);
+        Launch l(a[7], *x.t);
+        const size_t bytes = api.bsq_linear_workspace_bytes(x.rows, w.rows, x.cols);
+        check(api.bsq_linear(x.p, x.ld, w.p, w.ld, x.rows, w.rows, x.cols, bias, type, act, r.p, r.ld, y.p, y.ld,
+                             type_of(*y.t, "y"), z.p, z.ld, l.workspace(bytes), bytes, l.stream),
+              "bsq_linear");
+        return returned(a[2], a[6]);
+    });
+}
+
+ENTRY(linear_backward_into) {
+    return guarded([&] {
+        static const char* const names[] = {"dy", "x", "w", "dx", "dw", "dbias", "z", "activation", "stream"};
+        const Args a("linear_backward_into", names, 3, args, n, kwnames);
+        const Matrix dy = bf16_matrix(a[0], "dy");
+        const Matrix x = maybe_bf16(a[1], "x", dy.rows, -1), w = maybe_bf16(a[2], "w", dy.cols, x.t ? x.cols : -1);
+        const int64_t cols = x.t ? x.cols : w.t ? w.cols : 0;
+        if (!x.t && !w.t) refuse(BSQ_ERR_INVALID_ARG, "x or w must be given");
+        const Matrix dx = maybe_bf16(a[3], "dx", dy.rows, cols), dw = maybe_bf16(a[4], "dw", dy.cols, cols);
+        float* dbias = static_cast<float*>(vector(a[5], "dbias", dy.cols, at::kFloat));
+        const Matrix z = maybe_bf16(a[6], "z", dy.rows, dy.cols);
+        const int32_t act = activation(a[7], BSQ_ACT_IDENTITY);
+        Launch l(a[8], *dy.t);
+        const size_t bytes = api.bsq_linear_backward_workspace_bytes(dy.rows, dy.cols, cols);
+        check(api.bsq_linear_backward(dy.p, dy.ld, x.p, x.ld, w.p, w.ld, dy.rows, dy.cols, cols, act, z.p, z.ld, dx.p, dx.ld,
+                                      dw.p, dw.ld, dbias, l.workspace(bytes), bytes, l.stream),
+              "bsq_linear_backward");
+        return returned(a[3], a[4], a[5]);
+    });
+}
+
+ENTRY(gated_linear_into) {
+    return guarded([&] {
+        static const char* const names[] = {"x", "w_gate", "w_up", "h", "activation", "gate", "up", "stream"};
+        const Args a("gated_linear_into", names, 4, args, n, kwnames);
+        const Matrix x = bf16_matrix(a[0], "x"), g = bf16_matrix(a[1], "w_gate", -1, x.cols),
+                     u = bf16_matrix(a[2], "w_up", g.rows, x.cols), h = matrix(a[3], "h", x.rows, g.rows);
+        const Matrix gate = maybe_bf16(a[5], "gate", x.rows, g.rows), up = maybe_bf16(a[6], "up", x.rows, g.rows);
+        const int32_t act = activation(a[4], BSQ_ACT_SILU);
+        Launch l(a[7], *x.t);
+        const size_t bytes = api.bsq_gated_linear_workspace_bytes(x.rows, g.rows, x.cols);
+        check(api.bsq_gated_linear(x.p, x.ld, g.p, g.ld, u.p, u.ld, x.rows, g.rows, x.cols, act, h.p, h.ld,
+                                   type_of(*h.t, "h"), gate.p, gate.ld, up.p, up.ld, l.workspace(bytes), bytes, l.stream),
+              "bsq_gated_linear");
+        return returned(a[3], a[5], a[6]);
+    });
+}
+
+ENTRY(gated_linear_backward_into) {
+    return guarded([&] {
+        static const char* const names[] = {"dh", "x",  "w_gate",  "w_up",  "gate",       "up",
+                                            "dx", "dw_gate", "dw_up", "activation", "stream"};
+        const Args a("gated_linear_backward_into", names, 6, args, n, kwnames);
+        const Matrix dh = bf16_matrix(a[0], "dh");
+        const int64_t T = dh.rows, F = dh.cols;
+        const Matrix x = maybe_bf16(a[1], "x", T, -1), g = maybe_bf16(a[2], "w_gate", F, x.t ? x.cols : -1);
+        const int64_t cols = x.t ? x.cols : g.t ? g.cols : 0;
+        if (!x.t && !g.t) refuse(BSQ_ERR_INVALID_ARG, "x or w_gate must be given");
+        const Matrix u = maybe_bf16(a[3], "w_up", F, cols), gate = bf16_matrix(a[4], "gate", T, F), up = bf16_matrix(a[5], "up", T, F);
+        const Matrix dx = maybe_bf16(a[6], "dx", T, cols), dg = maybe_bf16(a[7], "dw_gate", F, cols),
+                     du = maybe_bf16(a[8], "dw_up", F, cols);
+        const int32_t act = activation(a[9], BSQ_ACT_SILU);
+        Launch l(a[10], *dh.t);
+        const size_t bytes = api.bsq_gated_linear_backward_workspace_bytes(T, F, cols);
+        check(api.bsq_gated_linear_backward(dh.p, dh.ld, x.p, x.ld, g.p, g.ld, u.p, u.ld, T, F, cols, act, gate.p, gate.ld, up.p,
+                                            up.ld, dx.p, dx.ld, dg.p, dg.ld, du.p, du.ld, l.workspace(bytes), bytes, l.stream),
+              "bsq_gated_linear_backward");
+        return returned(a[6], a[7], a[8]);
+    });
+}
+
+int64_t integer(PyObject* o) {
+    const long long v = PyLong_AsLongLong(o);
+    if (v == -1 && PyErr_Occurred()) throw Refused{};
+    return v;
+}
+
+// A quantized tensor (QTensor): its buffers have to be there in full
+struct Quantized {
+    bsq_tensor c{};
+    const at::Tensor* codes;
+    Quantized(PyObject* o, const char* name) {
+        const Ref fmt(o, s_fmt), rows(o, s_rows), cols(o, s_cols), pc(o, s_codes), ps(o, s_scales), pt(o, s_tensor_scale);
+        c.fmt = (int32_t)integer(fmt.o);
+        c.rows = integer(rows.o);
+        c.cols = integer(cols.o);
+        codes = &tensor(pc.o, name);
+        const at::Tensor& scales = tensor(ps.o, name);
+        for (const at::Tensor* t : {codes, &scales})
+            if (t->element_size() != 1 || !t->is_contiguous())
+                refuse(BSQ_ERR_INVALID_ARG, "%s: codes and scales must be contiguous bytes", name);
+        if (c.rows < 1 || c.cols < 1 || c.rows > INT32_MAX || c.cols > INT32_MAX ||
+            (size_t)codes->numel() < api.bsq_codes_bytes(c.fmt, c.rows, c.cols) ||
+            (size_t)scales.numel() < api.bsq_scales_bytes(c.fmt, c.rows, c.cols))
+            refuse(BSQ_ERR_INVALID_ARG, "%s: codes or scales are shorter than its shape", name);
+        c.codes = codes->data_ptr();
+        c.scales = static_cast<uint8_t*>(scales.data_ptr());
+        c.tensor_scale = static_cast<float*>(vector(pt.o, name, 1, at::kFloat));
+    }
+};
+
+ENTRY(gemm_linear_into) {
+    return guarded([&] {
+        static const char* const names[] = {"A", "B", "y", "bias", "residual", "activation", "z", "stream"};
+        const Args a("gemm_linear_into", names, 3, args, n, kwnames);
+        const Quantized qa(a[0], "A"), qb(a[1], "B");
+        const int64_t T = qa.c.rows, N = qb.c.rows;
+        const Matrix y = matrix(a[2], "y", T, N);
+        Matrix r;
+        if (!none(a[4])) r = matrix(a[4], "residual", T, N, &y);
+        const Matrix z = maybe_bf16(a[6], "z", T, N);
+        int32_t type;
+        const void* bias = bias_of(a[3], N, type);
+        const int32_t act = activation(a[5], BSQ_ACT_IDENTITY);
+        Launch l(a[7], *qa.codes);
+        const size_t bytes = api.bsq_gemm_linear_workspace_bytes(qa.c.fmt, T, N, qa.c.cols);
+        check(api.bsq_gemm_linear(&qa.c, &qb.c, bias, type, act, r.p, r.ld, y.p, y.ld, type_of(*y.t, "y"), z.p, z.ld,
+                                  l.workspace(bytes), bytes, l.stream),
+              "bsq_gemm_linear");
+        return returned(a[2], a[6]);
+    });
+}
+
+ENTRY(gemm_gated_into) {
+    return guarded([&] {
+        static const char* const names[] = {"A", "B_gate", "B_up", "h", "activation", "gate", "up", "stream"};
+        const Args a("gemm_gated_into", names, 4, args, n, kwnames);
+        const Quantized qa(a[0], "A"), qg(a[1], "B_gate"), qu(a[2], "B_up");
+        const int64_t T = qa.c.rows, F = qg.c.rows;
+        const Matrix h = matrix(a[3], "h", T, F), gate = maybe_bf16(a[5], "gate", T, F), up = maybe_bf16(a[6], "up", T, F);
+        const int32_t act = activation(a[4], BSQ_ACT_SILU);
+        Launch l(a[7], *qa.codes);
+        const size_t bytes = api.bsq_gemm_gated_workspace_bytes(qa.c.fmt, T, F, qa.c.cols);
+        check(api.bsq_gemm_gated(&qa.c, &qg.c, &qu.c, act, h.p, h.ld, type_of(*h.t, "h"), gate.p, gate.ld, up.p, up.ld,
+                                 l.workspace(bytes), bytes, l.stream),
+              "bsq_gemm_gated");
+        return returned(a[3], a[5], a[6]);
+    });
+}
+
+// The address of a bsq_adamw_tensor array and its length (an AdamWList keeps both); `like`: one of its tensors.
+// lr and step may be numbers, or tensors on the device; norm and seed may be None.
+ENTRY(adamw_into) {
+    return guarded([&] {
+        static const char* const names[] = {"array", "count", "like", "lr", "step", "beta1", "beta2", "eps", "weight_decay",
+                                            "norm", "max_norm", "clip_eps", "seed", "stream"};
+        const Args a("adamw_into", names, 13, args, n, kwnames);
+        const auto* tensors = static_cast<const bsq_adamw_tensor*>(PyLong_AsVoidPtr(a[0]));
+        const int32_t count = (int32_t)integer(a[1]);
+        if (PyErr_Occurred()) throw Refused{};
+        const at::Tensor& like = tensor(a[2], "like");
+        bsq_adamw_options o{};
+        if (THPVariable_Check(a[3])) o.lr_device = static_cast<float*>(vector(a[3], "lr", 1, at::kFloat));
+        else o.lr = number(a[3]);
+        if (THPVariable_Check(a[4])) o.step_device = static_cast<int64_t*>(vector(a[4], "step", 1, at::kLong));
+        else o.step = integer(a[4]);
+        o.beta1 = number(a[5]);
+        o.beta2 = number(a[6]);
+        o.eps = number(a[7]);
+        o.weight_decay = number(a[8]);
+        o.norm = static_cast<float*>(vector(a[9], "norm", 1, at::kFloat));
+        if (o.norm) {
+            o.max_norm = number(a[10]);
+            o.clip_eps = number(a[11]);
+        }
+        o.stochastic = !none(a[12]);
+        if (o.stochastic) {
+            o.seed = PyLong_AsUnsignedLongLongMask(a[12]);
+            if (PyErr_Occurred()) throw Refused{};
+        }
+        Launch l(a[13], like);
+        check(api.bsq_adamw(tensors, count, &o, l.stream), "bsq_adamw");
+        Py_RETURN_NONE;
+    });
+}
+
 // grads: the address of a bsq_grad array and its length (a GradList keeps both
 // and a workspace); max_norm None: the norm only.
 ENTRY(grads_into) {
@@ -498,7 +723,8 @@ PyMethodDef methods[] = {
     METHOD(moe_sort_into), METHOD(moe_dispatch_into), METHOD(moe_gather_into), METHOD(moe_combine_into),
     METHOD(moe_combine_backward_into), METHOD(layer_norm_into), METHOD(layer_norm_backward_into),
     METHOD(linear_cross_entropy_into), METHOD(linear_cross_entropy_backward_into), METHOD(grads_into),
-    METHOD(stream_state),
+    METHOD(stream_state), METHOD(linear_into), METHOD(linear_backward_into), METHOD(gated_linear_into),
+    METHOD(gated_linear_backward_into), METHOD(gemm_linear_into), METHOD(gemm_gated_into), METHOD(adamw_into),
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(bind)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
@@ -512,5 +738,11 @@ PyMODINIT_FUNC PyInit__binding() {
     s_slot_row = PyUnicode_InternFromString("slot_row");
     s_row_slot = PyUnicode_InternFromString("row_slot");
     s_cuda_stream = PyUnicode_InternFromString("cuda_stream");
+    s_fmt = PyUnicode_InternFromString("fmt");
+    s_rows = PyUnicode_InternFromString("rows");
+    s_cols = PyUnicode_InternFromString("cols");
+    s_codes = PyUnicode_InternFromString("codes");
+    s_scales = PyUnicode_InternFromString("scales");
+    s_tensor_scale = PyUnicode_InternFromString("tensor_scale");
     return PyModule_Create(&definition);
 }

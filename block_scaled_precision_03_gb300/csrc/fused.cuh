@@ -1,0 +1,263 @@
+// What the epilogue of a product does with its sums besides storing them:
+//   linear  z = sum + bias, y = act(z) + residual
+//   gated   h = act(gate) * up
+// for the BF16 products (linear.cu) and the block-scaled ones (gemm2.cu).
+// Everything is FP32 until the store, which rounds once.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+#include "launch.cuh"
+#include "pair_gemm.cuh"
+#include "tcgen05.cuh"
+
+namespace bsq {
+
+enum { kActIdentity, kActRelu, kActSilu, kActGelu, kActGeluTanh, kActs };
+
+// A TMA store does not cut a row inside 16 bytes: where a row ends there, the box with its end is written otherwise.
+enum { kNone, kPart, kWhole };
+
+struct Fused {
+    int32_t act;
+    int32_t y_bf16;                // y (and the residual): BF16 or FP32
+    int32_t bias_bf16;
+    int32_t y_tma, z_tma, u_tma;   // the output's rows suit TMA stores (kWhole, kPart), or not (0)
+    int32_t res_vec, bias_vec;     // 16-byte loads
+    const void* bias;              // [N] or nullptr
+    const void* residual;          // or nullptr
+    int64_t ld_res;
+    void* y;
+    int64_t ldy;
+    __nv_bfloat16* z;              // linear: the pre-activation; gated: the gate's; or nullptr
+    int64_t ldz;
+    __nv_bfloat16* u;              // gated: the other projection; or nullptr
+    int64_t ldu;
+};
+
+// ------------------------------------------------------------- activations
+// 1 / (1 + exp(-x)): ex2 and rcp are good to 2^-22 each; exp(-x) = inf gives 0
+__device__ __forceinline__ float sigmoid(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + pair::exp2_fast(-1.44269504088896340736f * x)));
+    return r;
+}
+constexpr float kSqrtHalf = 0.70710678118654752440f;
+constexpr float kGeluC = 0.79788456080286535588f;      // sqrt(2 / pi)
+constexpr float kGeluA = 0.044715f;
+// 0.5 (1 + tanh(t)) is the sigmoid of 2 t, without the cancellation at negative t
+__device__ __forceinline__ float gelu_gate(float z) { return sigmoid(2.0f * kGeluC * (z + kGeluA * z * z * z)); }
+__device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(-kSqrtHalf * z); }
+
+template <int ACT>
+__device__ __forceinline__ float act_one(float z) {
+    if (ACT == kActRelu) return z > 0.0f || z != z ? z : 0.0f;         // NaN stays NaN
+    if (ACT == kActSilu) return z * sigmoid(z);
+    if (ACT == kActGelu) return z * normal_cdf(z);
+    if (ACT == kActGeluTanh) return z * gelu_gate(z);
+    return z;
+}
+// act'(z), and act(z) beside it
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z, float& value) {
+    if (ACT == kActRelu) {
+        value = act_one<kActRelu>(z);
+        return z > 0.0f ? 1.0f : z != z ? z : 0.0f;
+    }
+    if (ACT == kActSilu) {
+        const float s = sigmoid(z);
+        value = z * s;
+        return s * fmaf(z, 1.0f - s, 1.0f);
+    }
+    if (ACT == kActGelu) {
+        const float c = normal_cdf(z);
+        value = z * c;
+        // z exp(-z^2 / 2) / sqrt(2 pi)
+        return fmaf(z * 0.39894228040143267794f, pair::exp2_fast(-0.72134752044448170368f * z * z), c);
+    }
+    if (ACT == kActGeluTanh) {
+        const float s = gelu_gate(z);
+        value = z * s;
+        return fmaf(2.0f * kGeluC * value * (1.0f - s), fmaf(3.0f * kGeluA, fminf(z * z, 1e30f), 1.0f), s);
+    }
+    value = z;
+    return 1.0f;
+}
+// f<ACT>() for the activation `act`
+#define BSQ_WITH_ACT(act, F)                                 \
+    switch (act) {                                           \
+        case kActRelu: F(kActRelu); break;                   \
+        case kActSilu: F(kActSilu); break;                   \
+        case kActGelu: F(kActGelu); break;                   \
+        case kActGeluTanh: F(kActGeluTanh); break;           \
+        default: F(kActIdentity); break;                     \
+    }
+
+template <int N>
+__device__ __forceinline__ void activate(int act, float (&v)[N]) {
+    if (act == kActIdentity) return;
+#define F(A)                                      \
+    _Pragma("unroll") for (int j = 0; j < N; j++) v[j] = act_one<A>(v[j])
+    BSQ_WITH_ACT(act, F)
+#undef F
+}
+
+__device__ __forceinline__ float load_as_float(const void* p, int64_t i, int bf16) {
+    return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
+}
+
+// ------------------------------------------------- chunks of 32 rows by 32 columns
+// v += p[0 .. 32), the first `n` of them (32 or more: all), 16 bytes at a time where `vec`
+__device__ __forceinline__ void add_row(float (&v)[32], const void* p, int64_t at, int bf16, int vec, int64_t n) {
+    if (vec && n >= 32) {
+        if (bf16) {
+            const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(p) + at;
+            Pack<__nv_bfloat16, 8> k[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) k[i].load(from + 8 * i);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                float f[8];
+                k[i].unpack(f);
+#pragma unroll
+                for (int e = 0; e < 8; e++) v[8 * i + e] += f[e];
+            }
+        } else {
+            const float* from = static_cast<const float*>(p) + at;
+            float4 k[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) k[i] = *reinterpret_cast<const float4*>(from + 4 * i);
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                v[4 * i] += k[i].x;
+                v[4 * i + 1] += k[i].y;
+                v[4 * i + 2] += k[i].z;
+                v[4 * i + 3] += k[i].w;
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 32; j++)
+        if (j < n) v[j] += load_as_float(p, at + j, bf16);
+}
+
+// A warp's staging: BUFS buffers of 2 KB, used in turn; `n` counts the chunks.
+template <int BUFS>
+struct Staging {
+    uint32_t base;
+    int n;
+    __device__ __forceinline__ uint32_t next(int lane) {
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" :: "n"(BUFS - 1) : "memory");
+        __syncwarp();
+        return base + (uint32_t)(n++ % BUFS) * 2048u;
+    }
+};
+
+// The warp's chunk (lane: row row0 + lane, its columns col ..) leaves as BF16 or FP32: through a staging
+// buffer and a TMA store, or (rows off 16-byte boundaries) from the buffer with neighbouring lanes on
+// neighbouring columns.  Rows from M and columns from N on are not written.
+template <int BUFS>
+__device__ __forceinline__ void store_chunk(const float (&v)[32], int bf16, int tma, const void* tmap, void* out, int64_t ld,
+                                            int64_t row0, int64_t col, int64_t M, int64_t N, Staging<BUFS>& st, int lane) {
+    if (bf16) {
+        uint32_t w[16];
+#pragma unroll
+        for (int j = 0; j < 16; j++) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+            w[j] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        const uint32_t buf = st.next(lane);
+        pair::stage_chunk(w, buf, lane);
+        if (tma == kWhole || (tma && col + 32 <= N)) {
+            if (lane == 0) {
+                tc::tma_store_2d(tmap, (int)col, (int)row0, buf);
+                tc::bulk_commit();
+            }
+            return;
+        }
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out) + row0 * ld + col;
+        const int rows = (int)min((int64_t)32, M - row0);
+        for (int r = 0; r < rows; r++) {
+            uint16_t x;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x)
+                         : "r"(buf + (uint32_t)r * 64u + ((((uint32_t)lane >> 3) ^ ((uint32_t)(r >> 1) & 3u)) << 4) + ((uint32_t)lane & 7u) * 2u)
+                         : "memory");
+            if (col + lane < N) o[r * ld + lane] = __ushort_as_bfloat16(x);
+        }
+        __syncwarp();
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < 32; c += 16) {
+        uint32_t w[16];
+#pragma unroll
+        for (int j = 0; j < 16; j++) w[j] = __float_as_uint(v[c + j]);
+        const uint32_t buf = st.next(lane);
+        pair::stage_chunk(w, buf, lane);
+        if (tma == kWhole || (tma && col + c + 16 <= N)) {
+            if (lane == 0) {
+                tc::tma_store_2d(tmap, (int)col + c, (int)row0, buf);
+                tc::bulk_commit();
+            }
+            continue;
+        }
+        float* o = static_cast<float*>(out) + row0 * ld + col + c;
+        const int rows = (int)min((int64_t)32, M - row0), k = lane & 15;
+        for (int r = lane >> 4; r < rows; r += 2) {
+            float x;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x)
+                         : "r"(buf + (uint32_t)r * 64u + ((((uint32_t)k >> 2) ^ ((uint32_t)(r >> 1) & 3u)) << 4) + ((uint32_t)k & 3u) * 4u)
+                         : "memory");
+            if (col + c + k < N) o[r * ld + k] = x;
+        }
+        __syncwarp();
+    }
+}
+
+// 32 columns of a linear layer's sums become z, y
+template <int BUFS>
+__device__ __forceinline__ void finish_linear(float (&v)[32], const Fused& f, const void* tm_y, const void* tm_z, int64_t row0,
+                                              int64_t col, int64_t M, int64_t N, Staging<BUFS>& st, int lane) {
+    if (f.bias) add_row(v, f.bias, col, f.bias_bf16, f.bias_vec, N - col);
+    if (f.z) store_chunk(v, 1, f.z_tma, tm_z, f.z, f.ldz, row0, col, M, N, st, lane);
+    activate(f.act, v);
+    if (f.residual && row0 + lane < M) add_row(v, f.residual, (row0 + lane) * f.ld_res + col, f.y_bf16, f.res_vec, N - col);
+    store_chunk(v, f.y_bf16, f.y_tma, tm_y, f.y, f.ldy, row0, col, M, N, st, lane);
+}
+// 32 columns of both projections become h
+template <int BUFS>
+__device__ __forceinline__ void finish_gated(float (&v)[32], const float (&u)[32], const Fused& f, const void* tm_y,
+                                             const void* tm_z, const void* tm_u, int64_t row0, int64_t col, int64_t M, int64_t N,
+                                             Staging<BUFS>& st, int lane) {
+    if (f.z) {
+        store_chunk(v, 1, f.z_tma, tm_z, f.z, f.ldz, row0, col, M, N, st, lane);
+        store_chunk(u, 1, f.u_tma, tm_u, f.u, f.ldu, row0, col, M, N, st, lane);
+    }
+    activate(f.act, v);
+#pragma unroll
+    for (int j = 0; j < 32; j++) v[j] *= u[j];
+    store_chunk(v, f.y_bf16, f.y_tma, tm_y, f.y, f.ldy, row0, col, M, N, st, lane);
+}
+
+struct LinearArgs;
+// the epilogue of a call (without the tensor maps' part)
+void fused_args(Fused& f, const LinearArgs& a);
+// Parts of a split sum over K are FP32 [part][row][fused_acc_cols]: gated, 128 columns of the gate's sums, then up's
+// of the same columns, and so on.
+int64_t fused_acc_cols(int64_t N, bool gated);
+// the parts that get any of `stages`, dealt to n
+int fused_parts(int64_t stages, int64_t n);
+// How many parts: more than one where there are fewer tiles than pairs, or few in the last wave.  The estimate: what
+// the busiest pair computes, and that each part's FP32 tile is written and read.
+int fused_splits(int64_t tiles, int64_t stages, double stage_us, double part_bytes, int pairs);
+// adds the parts in their order and does the epilogue; starts beside the kernel before it
+cudaError_t run_linear_join(const float* acc, int splits, int64_t M, int64_t N, bool gated, const LinearArgs& a, cudaStream_t st);
+
+// Tensor map of an output for 32 x 64-byte stores, if its rows suit them
+inline int fused_map(CUtensorMap* m, void* p, int64_t rows, int64_t cols, int64_t ld, bool bf16) {
+    const int64_t e = bf16 ? 2 : 4;
+    if (!p || reinterpret_cast<uintptr_t>(p) % 16 || ld * e % 16 || !tmap::out_2d(m, p, rows, cols, ld, bf16)) return kNone;
+    return cols * e % 16 ? kPart : kWhole;
+}
+
+}  // namespace bsq

@@ -30,11 +30,18 @@
 //               MMA thread: a scale copy costs the issuing thread about as
 //               long as an MMA, and from a second thread the copies overlap
 //               with the MMAs instead of queueing between them
+// With an epilogue (EPI) the sums become z = sum + bias, y = act(z) + residual, or
+// h = act(gate) * up.  Gated, the tile is 128 columns of both projections: the even
+// CTA's rows of B are the gate's, the odd one's up's, and both projections' scales of
+// those columns take the places of the tile's two B scale bands, so that a CTA's
+// accumulator holds gate and up of its rows, 128 columns apart.  Where there are few
+// tiles the sum over K is split; linear_join_kernel adds the parts.
 // Every wait is bounded; a CTA that gave up records the status, and before
 // the pair exits every MMA, scale copy and stage load it issued has landed.
 #include <algorithm>
 #include <cuda.h>
 #include "common.cuh"
+#include "fused.cuh"
 #include "internal.h"
 #include "per_device.h"
 #include "tcgen05.cuh"
@@ -120,6 +127,41 @@ struct Params2 {
     uint64_t timeout_ns;
 };
 
+// What the kernels with an epilogue take besides
+enum { kPlain, kLinear, kGated };
+struct Nothing {};
+struct More {
+    CUtensorMap b, sfb;            // gated: the other projection
+    CUtensorMap z, u;              // outputs
+    const float* ts_b;
+    int32_t splits, split_stages;  // parts of the sum over K, and stages of each
+    Fused f;
+};
+template <int EPI>
+struct MoreOf {
+    typedef More type;
+};
+template <>
+struct MoreOf<kPlain> {
+    typedef Nothing type;
+};
+// Tile t's place in the sum over K: its part, its stages, and t without the part
+struct Part {
+    int32_t split, k0, k1;
+};
+template <int EPI>
+__device__ __forceinline__ Part part_of(const Params2& p, const typename MoreOf<EPI>::type& more, int& t) {
+    Part a{0, 0, p.k_stages};
+    if constexpr (EPI != kPlain) {
+        const int per = p.m_tiles * p.n_tiles;
+        a.split = t / per;
+        t -= a.split * per;
+        a.k0 = a.split * more.split_stages;
+        a.k1 = min(p.k_stages, a.k0 + more.split_stages);
+    }
+    return a;
+}
+
 // Tile order: groups of `raster` tiles along one dimension, swept along the
 // other (raster_n: the groups run along n).  A group spanning the whole of
 // the smaller operand keeps that operand resident in L2 while the other one
@@ -171,6 +213,7 @@ struct Tile2 {
     int32_t row_lo, row_hi;    // rows of C this CTA may write
 };
 
+template <int EPI>
 __device__ __forceinline__ Tile2 tile2(const Params2& p, int t, const GroupTable2* gt, int& gcur, uint32_t rank) {
     Tile2 ti;
     if (p.num_groups == 0) {
@@ -179,8 +222,8 @@ __device__ __forceinline__ Tile2 tile2(const Params2& p, int t, const GroupTable
         ti.a_band = mt * 2 + (int)rank;
         ti.a_row = ti.a_band * 128;
         ti.nt = nt;
-        ti.b_row = nt * BN + (int)rank * 128;
-        ti.sfb_band = nt * 2;
+        ti.b_row = EPI == kGated ? nt * 128 : nt * BN + (int)rank * 128;
+        ti.sfb_band = EPI == kGated ? nt : nt * 2;
         ti.row_lo = ti.a_band * 128;
         ti.row_hi = min(p.M, ti.row_lo + 128);
     } else {
@@ -202,11 +245,12 @@ __device__ __forceinline__ Tile2 tile2(const Params2& p, int t, const GroupTable
     return ti;
 }
 
-template <int KIND>
+template <int KIND, int EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
              const __grid_constant__ CUtensorMap tmSFA, const __grid_constant__ CUtensorMap tmSFB,
-             const __grid_constant__ CUtensorMap tmC, const __grid_constant__ Params2 p) {
+             const __grid_constant__ CUtensorMap tmC, const __grid_constant__ Params2 p,
+             const __grid_constant__ typename MoreOf<EPI>::type more) {
     using CF = Cfg2<KIND>;
     constexpr int S = CF::STAGES;
     extern __shared__ uint8_t smem_raw[];
@@ -322,9 +366,14 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
             bool ok = true;
             int gcur = 0, issued = 0;
             for (int t = cid; t < total && ok; t += ncl) {
-                const Tile2 ti = tile2(p, t, gt, gcur, rank);
+                int tile = t;
+                const Part pt = part_of<EPI>(p, more, tile);
+                const Tile2 ti = tile2<EPI>(p, tile, gt, gcur, rank);
                 const int arow = ti.a_row, brow = ti.b_row;
-                for (int kb = 0; kb < p.k_stages; kb++) {
+                const CUtensorMap* mb = &tmB;
+                if constexpr (EPI == kGated)
+                    if (rank) mb = &more.b;
+                for (int kb = pt.k0; kb < pt.k1; kb++) {
                     if (!tc::mbar_wait(empty0 + 8 * stage, phase ^ 1, abort_flag, p.status, p.timeout_ns)) {
                         ok = false;
                         break;
@@ -335,7 +384,7 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
                     for (int j = 0; j < CF::KSUB; j++) {
                         const int kx = (kb * CF::KSUB + j) * BKB;
                         tc::tma_load_2d_pair(tc::smem_u32(smA + stage * CF::OP_BYTES + j * HALF), &tmA, kx, arow, fb);
-                        tc::tma_load_2d_pair(tc::smem_u32(smB + stage * CF::OP_BYTES + j * HALF), &tmB, kx, brow, fb);
+                        tc::tma_load_2d_pair(tc::smem_u32(smB + stage * CF::OP_BYTES + j * HALF), mb, kx, brow, fb);
                     }
                     ++issued;
                     if (++stage == S) { stage = 0; phase ^= 1; }
@@ -350,8 +399,10 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
             bool ok = true;
             int gcur = 0, issued = 0;
             for (int t = cid; t < total && ok; t += ncl) {
-                const Tile2 ti = tile2(p, t, gt, gcur, rank);
-                for (int kb = 0; kb < p.k_stages; kb++) {
+                int tile = t;
+                const Part pt = part_of<EPI>(p, more, tile);
+                const Tile2 ti = tile2<EPI>(p, tile, gt, gcur, rank);
+                for (int kb = pt.k0; kb < pt.k1; kb++) {
                     if (!tc::mbar_wait(sfree0 + 8 * stage, phase ^ 1, abort_flag, p.status, p.timeout_ns)) {
                         ok = false;
                         break;
@@ -360,7 +411,18 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
                     if (leader) tc::mbar_expect_tx(sfull0 + 8 * stage, 2 * CF::SF_TX);
                     uint8_t* sf = smSF + stage * CF::SF_STAGE;
                     tc::tma_load_3d_pair(tc::smem_u32(sf), &tmSFA, 0, kb * CF::SF_ATOMS, ti.a_band, sb);
-                    if (CF::SFB_QUARTERS)
+                    if constexpr (EPI == kGated) {
+                        // one band of each projection, up's behind the gate's
+                        constexpr int BAND = CF::SFB_BYTES / 2;
+                        const uint32_t db = tc::smem_u32(sf + CF::SFA_BYTES);
+                        if (CF::SFB_QUARTERS) {
+                            tc::tma_load_4d_pair(db, &tmSFB, 0, 0, ti.sfb_band, kb * CF::SF_ATOMS, sb);
+                            tc::tma_load_4d_pair(db + BAND, &more.sfb, 0, 0, ti.sfb_band, kb * CF::SF_ATOMS, sb);
+                        } else {
+                            tc::tma_load_3d_pair(db, &tmSFB, 0, kb * CF::SF_ATOMS, ti.sfb_band, sb);
+                            tc::tma_load_3d_pair(db + BAND, &more.sfb, 0, kb * CF::SF_ATOMS, ti.sfb_band, sb);
+                        }
+                    } else if (CF::SFB_QUARTERS)
                         tc::tma_load_4d_pair(tc::smem_u32(sf + CF::SFA_BYTES), &tmSFB, 0, 0, ti.sfb_band,
                                              kb * CF::SF_ATOMS, sb);
                     else
@@ -392,7 +454,9 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
                 // (tcgen05.wait::ld); a CTA-scope acquire suffices
                 if (!tc::mbar_wait(tempty, (iter & 1) ^ 1, abort_flag, p.status, p.timeout_ns)) { ok = false; break; }
                 tc::fence_after();
-                for (int kb = 0; kb < p.k_stages; kb++) {
+                int tile = t;
+                const Part pt = part_of<EPI>(p, more, tile);
+                for (int kb = pt.k0; kb < pt.k1; kb++) {
                     if (!tc::mbar_wait(full0 + 8 * stage, phase, abort_flag, p.status, p.timeout_ns) ||
                         !tc::mbar_wait(sfr0 + 8 * stage, phase, abort_flag, p.status, p.timeout_ns)) {
                         ok = false;
@@ -408,7 +472,7 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
                             const int sub = m >> 2, k = m & 3;
                             // +32 bytes along K inside a 128-byte swizzle row = +2 in the address field
                             const uint64_t adm = ad + sub * SUB_STEP + 2 * k, bdm = bd + sub * SUB_STEP + 2 * k;
-                            const uint32_t acc = (kb | m) != 0;
+                            const uint32_t acc = EPI == kPlain ? (kb | m) != 0 : ((kb - pt.k0) | m) != 0;
                             // FP8 takes scale byte k of the sub-step's atom (1X), NVFP4 one atom
                             // per MMA (4X), MXFP4 the byte pair 2 (m & 1) of atom m >> 1 (2X)
                             if (KIND == kKindNV) {
@@ -425,7 +489,7 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
                     }
                     any = true;
                     tc::commit<2>(empty0 + 8 * stage, 3);
-                    if (kb == p.k_stages - 1) tc::commit<2>(tfull, 3);
+                    if (kb == pt.k1 - 1) tc::commit<2>(tfull, 3);
                     if (++stage == S) { stage = 0; phase ^= 1; }
                 }
             }
@@ -450,23 +514,57 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
             alpha = *p.ts_a;
             beta = *p.ts_b;
         }
+        float beta2 = 1.0f;
+        if constexpr (KIND == kKindNV && EPI == kGated) beta2 = *more.ts_b;
+        Staging<1> stage_out{tc::smem_u32(smOut + (warp - 2) * 2048), 0};
         int iter = 0, gcur = 0;
         for (int t = cid; t < total; t += ncl, ++iter) {
-            const Tile2 ti = tile2(p, t, gt, gcur, rank);
+            int tile = t;
+            const Part pt = part_of<EPI>(p, more, tile);
+            const Tile2 ti = tile2<EPI>(p, tile, gt, gcur, rank);
             if (!tc::mbar_wait(tfull, iter & 1, abort_flag, p.status, p.timeout_ns)) break;
             tc::fence_after();
             uint32_t r[4][32];
-            const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * 128);
+            // gated: 64 columns of the gate's, and up's 64 of the same columns
+            constexpr int OWN = EPI == kGated ? 64 : 128, SECOND = EPI == kGated ? 128 : 64;
+            const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * OWN);
             BSQ_TMEM_LD32(r[0], ta);
             BSQ_TMEM_LD32(r[1], ta + 32);
-            BSQ_TMEM_LD32(r[2], ta + 64);
-            BSQ_TMEM_LD32(r[3], ta + 96);
+            BSQ_TMEM_LD32(r[2], ta + SECOND);
+            BSQ_TMEM_LD32(r[3], ta + SECOND + 32);
             tc::tmem_wait_ld();
             tc::fence_before();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive_cluster(tempty_c0);
             // this warp's 32 rows, clipped to the rows the CTA may write
             const int row0 = ti.a_row + q * 32;
+            if constexpr (EPI != kPlain) {
+                const int col0 = EPI == kGated ? ti.nt * 128 + h * 64 : ti.nt * BN + h * 128;
+                if (row0 >= p.M || col0 >= p.N) continue;
+#pragma unroll 1
+                for (int c = 0; c < OWN && col0 + c < p.N; c += 32) {
+                    // the loop stays one, and the sums move on
+                    float v[32], u[32];
+#pragma unroll
+                    for (int j = 0; j < 32; j++) {
+                        v[j] = __uint_as_float(r[0][j]) * alpha * beta;
+                        u[j] = __uint_as_float(r[2][j]) * alpha * beta2;
+                        r[0][j] = r[1][j];
+                        if (EPI == kLinear) r[1][j] = r[2][j];
+                        r[2][j] = r[3][j];
+                    }
+                    if (more.splits > 1) {
+                        const int at = ti.nt * BN + h * OWN + c;
+                        pair::store_part(v, stage_out, &tmC, at, row0, pt.split, lane);
+                        if (EPI == kGated) pair::store_part(u, stage_out, &tmC, at + 128, row0, pt.split, lane);
+                    } else if (EPI == kGated) {
+                        finish_gated(v, u, more.f, &tmC, &more.z, &more.u, row0, col0 + c, p.M, p.N, stage_out, lane);
+                    } else {
+                        finish_linear(v, more.f, &tmC, &more.z, row0, col0 + c, p.M, p.N, stage_out, lane);
+                    }
+                }
+                continue;
+            }
             const int col0 = ti.nt * BN + h * 128;
             const int lo = max(row0, ti.row_lo), hi = min(row0 + 32, ti.row_hi);
             if (lo >= hi || col0 >= p.N) continue;
@@ -497,7 +595,9 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
             uint32_t phase = 0;
             bool ok = true, any = false;
             for (int t = cid; t < total && ok; t += ncl) {
-                for (int kb = 0; kb < p.k_stages; kb++) {
+                int tile = t;
+                const Part pt = part_of<EPI>(p, more, tile);
+                for (int kb = pt.k0; kb < pt.k1; kb++) {
                     // the stage's scales have landed, and the MMAs that read the stage's
                     // tensor-memory slot last time have completed
                     if (!tc::mbar_wait(sfull0 + 8 * stage, phase, abort_flag, p.status, p.timeout_ns) ||
@@ -516,7 +616,9 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
 #pragma unroll
                         for (int a = 0; a < CF::SF_ATOMS; a++) {
                             tc::cp_sf<2>(sfa_t + 4 * a, sd + 32 * a);
-                            tc::cp_sf_128x256<2>(sfb_t + 8 * a, tc::desc_sf_ns(sfb_s + a * 4096, 2048, 128));
+                            // (gated: the bands one after the other, each with all of the stage's atoms)
+                            tc::cp_sf_128x256<2>(sfb_t + 8 * a, EPI == kGated ? tc::desc_sf_ns(sfb_s + a * 2048, CF::SF_ATOMS * 2048, 128)
+                                                                              : tc::desc_sf_ns(sfb_s + a * 4096, 2048, 128));
                         }
                     } else {
                         // copy c: atom c / 3, part c % 3 (A; B rows 0-127; B rows 128-255), each
@@ -570,14 +672,73 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
     }
 }
 
-template <int KIND>
+template <int KIND, int EPI>
 cudaError_t launch2(const Params2& p, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tsa,
-                    const CUtensorMap& tsb, const CUtensorMap& tc_, int grid, cudaStream_t st) {
+                    const CUtensorMap& tsb, const CUtensorMap& tc_, const typename MoreOf<EPI>::type& more, int grid,
+                    cudaStream_t st) {
     static SharedMemory smem;
-    const cudaError_t e = smem.allow(reinterpret_cast<const void*>(gemm2_kernel<KIND>), Cfg2<KIND>::SMEM);
+    const cudaError_t e = smem.allow(reinterpret_cast<const void*>(gemm2_kernel<KIND, EPI>), Cfg2<KIND>::SMEM);
     if (e != cudaSuccess) return e;
-    gemm2_kernel<KIND><<<grid, kThreads, Cfg2<KIND>::SMEM, st>>>(ta, tb, tsa, tsb, tc_, p);
+    gemm2_kernel<KIND, EPI><<<grid, kThreads, Cfg2<KIND>::SMEM, st>>>(ta, tb, tsa, tsb, tc_, p, more);
     return cudaGetLastError();
+}
+
+// The operands' part of a call: sizes, descriptors, tensor maps; `sfb_bands` 128-row bands of B's scales a load
+struct Setup {
+    Params2 p;
+    CUtensorMap ta, tb, tsa, tsb;
+    int kind, sf_atoms;
+    int64_t kbytes, n_atoms;
+};
+bool operand_b(const Setup& s, CUtensorMap& tb, CUtensorMap& tsb, const uint8_t* codes, const uint8_t* scales, int64_t rows,
+               uint32_t bands) {
+    return tmap::codes_2d(&tb, codes, rows, s.kbytes, 128) &&
+           (s.kind == kKindNV ? tmap::scales_4d_quarters(&tsb, scales, (rows + 127) / 128, s.n_atoms, s.sf_atoms, bands)
+                              : tmap::scales_3d(&tsb, scales, (rows + 127) / 128, s.n_atoms, s.sf_atoms, bands));
+}
+bool set_up(Setup& s, const GemmArgs& a, uint32_t sfb_bands) {
+    const int kind = s.kind = a.fmt_a == kNVFP4 ? kKindNV : (a.fmt_a == kMXFP4 ? kKindMX4 : kKindFP8);
+    const bool fp4 = kind != kKindFP8;
+    const int64_t kbytes = s.kbytes = fp4 ? a.K / 2 : a.K;
+    s.n_atoms = (a.K / (kind == kKindNV ? 16 : 32) + 3) / 4;
+    Params2& p = s.p;
+    p = Params2{};
+    p.M = (int32_t)a.M;
+    p.N = (int32_t)a.N;
+    const int64_t stage_kb = (int64_t)BKB * (fp4 ? Cfg2<kKindNV>::KSUB : Cfg2<kKindFP8>::KSUB);
+    p.k_stages = (int32_t)((kbytes + stage_kb - 1) / stage_kb);
+    p.mma_last = (int32_t)((kbytes - (int64_t)(p.k_stages - 1) * stage_kb + 31) / 32);
+    p.m_tiles = (int32_t)((a.M + 255) / 256);
+    // E2M1 operands are type 1 in the FP4 kinds; UE8M0 scales except NVFP4's UE4M3
+    p.idesc = fp4 ? make_idesc(1, 1, kind == kKindMX4, 256, BN)
+                  : make_idesc(a.fmt_a == kE5M2 ? 1 : 0, a.fmt_b == kE5M2 ? 1 : 0, true, 256, BN);
+    p.ts_a = a.ts_a;
+    p.ts_b = a.ts_b;
+    p.status = a.status;
+    p.timeout_ns = a.timeout_ns;
+    const bool grouped = a.num_groups > 0;
+    p.num_groups = a.num_groups;
+    p.gsf = grouped && a.a_grouped_sf;
+    p.offsets = a.offsets;
+    p.group_bands = (int32_t)(a.N / 128);
+    s.sf_atoms = kind == kKindNV ? Cfg2<kKindNV>::SF_ATOMS
+               : (kind == kKindMX4 ? Cfg2<kKindMX4>::SF_ATOMS : Cfg2<kKindFP8>::SF_ATOMS);
+    // the per-expert padded scale layout spans up to one extra 128-row tile per expert
+    const int64_t a_bands = (a.M + 127) / 128 + (p.gsf ? a.num_groups : 0);
+    return tmap::codes_2d(&s.ta, a.a_codes, a.M, kbytes, 128) &&
+           tmap::scales_3d(&s.tsa, a.a_scales, a_bands, s.n_atoms, s.sf_atoms, 1) &&
+           operand_b(s, s.tb, s.tsb, a.b_codes, grouped ? a.b_group_scales[0] : a.b_scales, grouped ? a.N * a.num_groups : a.N,
+                     sfb_bands);
+}
+// raster order: sweep the larger operand past the whole of the smaller one
+// when the smaller one fits in L2 with room to spare
+void order_tiles(Params2& p, int64_t a_bytes, int64_t b_bytes) {
+    p.raster = kRasterGroup;
+    p.raster_n = 0;
+    if (std::min(a_bytes, b_bytes) <= kL2Resident) {
+        p.raster_n = b_bytes < a_bytes;
+        p.raster = p.raster_n ? p.n_tiles : p.m_tiles;
+    }
 }
 
 }  // namespace
@@ -597,18 +758,9 @@ bool gemm_pair_grouped_ok(const GemmArgs& a) {
 // Block-scaled GEMM on CTA pairs: dense, or grouped over experts when
 // gemm_pair_grouped_ok() holds.
 cudaError_t run_gemm_pair(const GemmArgs& a, cudaStream_t st) {
-    const int kind = a.fmt_a == kNVFP4 ? kKindNV : (a.fmt_a == kMXFP4 ? kKindMX4 : kKindFP8);
-    const bool fp4 = kind != kKindFP8;
-    const int64_t kbytes = fp4 ? a.K / 2 : a.K;
-    const int64_t S = a.K / (kind == kKindNV ? 16 : 32);
-    const int64_t n_atoms = (S + 3) / 4;
-    Params2 p{};
-    p.M = (int32_t)a.M;
-    p.N = (int32_t)a.N;
-    const int64_t stage_kb = (int64_t)BKB * (fp4 ? Cfg2<kKindNV>::KSUB : Cfg2<kKindFP8>::KSUB);
-    p.k_stages = (int32_t)((kbytes + stage_kb - 1) / stage_kb);
-    p.mma_last = (int32_t)((kbytes - (int64_t)(p.k_stages - 1) * stage_kb + 31) / 32);
-    p.m_tiles = (int32_t)((a.M + 255) / 256);
+    Setup s;
+    if (!set_up(s, a, 2)) return cudaErrorInvalidValue;
+    Params2& p = s.p;
     p.n_tiles = (int32_t)((a.N + BN - 1) / BN);
     p.total_tiles = p.m_tiles * p.n_tiles;
     p.C = a.C;
@@ -616,56 +768,73 @@ cudaError_t run_gemm_pair(const GemmArgs& a, cudaStream_t st) {
     p.out_bf16 = a.out_bf16;
     const int esz = a.out_bf16 ? 2 : 4;
     p.vec_ok = ((reinterpret_cast<uintptr_t>(a.C) & 15) == 0) && ((a.N * esz) % 16 == 0);
-    p.ts_a = a.ts_a;
-    p.ts_b = a.ts_b;
-    // E2M1 operands are type 1 in the FP4 kinds; UE8M0 scales except NVFP4's UE4M3
-    p.idesc = fp4 ? make_idesc(1, 1, kind == kKindMX4, 256, BN)
-                  : make_idesc(a.fmt_a == kE5M2 ? 1 : 0, a.fmt_b == kE5M2 ? 1 : 0, true, 256, BN);
-    p.status = a.status;
-    p.timeout_ns = a.timeout_ns;
-    const bool grouped = a.num_groups > 0;
-    p.num_groups = a.num_groups;
-    p.gsf = grouped && a.a_grouped_sf;
-    p.offsets = a.offsets;
-    p.group_bands = (int32_t)(a.N / 128);
-    // raster order: sweep the larger operand past the whole of the smaller one
-    // when the smaller one fits in L2 with room to spare
-    {
-        const int64_t a_bytes = a.M * kbytes, b_bytes = a.N * kbytes;
-        p.raster = kRasterGroup;
-        p.raster_n = 0;
-        if (std::min(a_bytes, b_bytes) <= kL2Resident) {
-            p.raster_n = b_bytes < a_bytes;
-            p.raster = p.raster_n ? p.n_tiles : p.m_tiles;
-        }
-    }
-
-    const int sf_atoms = kind == kKindNV ? Cfg2<kKindNV>::SF_ATOMS
-                       : (kind == kKindMX4 ? Cfg2<kKindMX4>::SF_ATOMS : Cfg2<kKindFP8>::SF_ATOMS);
-    CUtensorMap ta, tb, tsa, tsb;
-    if (!tmap::codes_2d(&ta, a.a_codes, a.M, kbytes, 128)) return cudaErrorInvalidValue;
-    const int64_t b_rows = grouped ? a.N * a.num_groups : a.N;
-    const uint8_t* b_sf = grouped ? a.b_group_scales[0] : a.b_scales;
-    if (!tmap::codes_2d(&tb, a.b_codes, b_rows, kbytes, 128)) return cudaErrorInvalidValue;
-    // the per-expert padded scale layout spans up to one extra 128-row tile per expert
-    const int64_t a_bands = (a.M + 127) / 128 + (p.gsf ? a.num_groups : 0);
-    if (!tmap::scales_3d(&tsa, a.a_scales, a_bands, n_atoms, sf_atoms, 1)) return cudaErrorInvalidValue;
-    if (kind == kKindNV) {
-        if (!tmap::scales_4d_quarters(&tsb, b_sf, (b_rows + 127) / 128, n_atoms, sf_atoms, 2))
-            return cudaErrorInvalidValue;
-    } else if (!tmap::scales_3d(&tsb, b_sf, (b_rows + 127) / 128, n_atoms, sf_atoms, 2)) {
-        return cudaErrorInvalidValue;
-    }
+    order_tiles(p, a.M * s.kbytes, a.N * s.kbytes);
     // TMA stores of the output when its base and row pitch allow them
-    CUtensorMap tcm = ta;
+    CUtensorMap tcm = s.ta;
     p.tma_store = p.vec_ok && tmap::out_2d(&tcm, a.C, a.M, a.N, a.N, a.out_bf16 != 0);
-    if (!p.tma_store) tcm = ta;
+    if (!p.tma_store) tcm = s.ta;
     int pairs = a.num_sms / 2;
-    if (!grouped && p.total_tiles < pairs) pairs = p.total_tiles;
+    if (a.num_groups == 0 && p.total_tiles < pairs) pairs = p.total_tiles;
     if (pairs < 1) pairs = 1;
-    if (kind == kKindNV) return launch2<kKindNV>(p, ta, tb, tsa, tsb, tcm, 2 * pairs, st);
-    if (kind == kKindMX4) return launch2<kKindMX4>(p, ta, tb, tsa, tsb, tcm, 2 * pairs, st);
-    return launch2<kKindFP8>(p, ta, tb, tsa, tsb, tcm, 2 * pairs, st);
+    const Nothing none{};
+    if (s.kind == kKindNV) return launch2<kKindNV, kPlain>(p, s.ta, s.tb, s.tsa, s.tsb, tcm, none, 2 * pairs, st);
+    if (s.kind == kKindMX4) return launch2<kKindMX4, kPlain>(p, s.ta, s.tb, s.tsa, s.tsb, tcm, none, 2 * pairs, st);
+    return launch2<kKindFP8, kPlain>(p, s.ta, s.tb, s.tsa, s.tsb, tcm, none, 2 * pairs, st);
+}
+
+namespace {
+
+template <int EPI>
+cudaError_t fused(const GemmArgs& a, const GemmArgs& up, const LinearArgs& l, cudaStream_t st) {
+    constexpr bool GATED = EPI == kGated;
+    Setup s;
+    More more{};
+    if (!set_up(s, a, GATED ? 1 : 2)) return cudaErrorInvalidValue;
+    if (GATED && !operand_b(s, more.b, more.sfb, up.b_codes, up.b_scales, a.N, 1)) return cudaErrorInvalidValue;
+    Params2& p = s.p;
+    const int64_t n_tiles = GATED ? (a.N + 127) / 128 : (a.N + BN - 1) / BN, tiles = (a.M + 255) / 256 * n_tiles;
+    const int splits = gemm_fused_splits(a.fmt_a, a.M, a.N, a.K, GATED, a.num_sms);
+    if (tiles * splits > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    p.n_tiles = (int32_t)n_tiles;
+    p.total_tiles = (int32_t)(tiles * splits);
+    more.split_stages = (p.k_stages + splits - 1) / splits;
+    more.splits = splits;
+    more.ts_b = up.ts_b;
+    fused_args(more.f, l);
+    order_tiles(p, a.M * s.kbytes, (GATED ? 2 : 1) * a.N * s.kbytes);
+    CUtensorMap tcm = s.ta;
+    float* acc = static_cast<float*>(l.ws);
+    const int64_t ld = fused_acc_cols(a.N, GATED);
+    if (splits > 1) {
+        if (!pair::map_acc(&tcm, acc, splits, a.M, ld)) return cudaErrorInvalidValue;
+    } else {
+        more.f.y_tma = fused_map(&tcm, l.y, a.M, a.N, l.ldy, l.y_bf16);
+        more.f.z_tma = fused_map(&more.z, l.z, a.M, a.N, l.ldz, true);
+        more.f.u_tma = GATED ? fused_map(&more.u, l.u, a.M, a.N, l.ldu, true) : kNone;
+    }
+    const int pairs = std::max(1, std::min(a.num_sms / 2, p.total_tiles));
+    const cudaError_t e =
+        s.kind == kKindNV    ? launch2<kKindNV, EPI>(p, s.ta, s.tb, s.tsa, s.tsb, tcm, more, 2 * pairs, st)
+        : s.kind == kKindMX4 ? launch2<kKindMX4, EPI>(p, s.ta, s.tb, s.tsa, s.tsb, tcm, more, 2 * pairs, st)
+                             : launch2<kKindFP8, EPI>(p, s.ta, s.tb, s.tsa, s.tsb, tcm, more, 2 * pairs, st);
+    if (e != cudaSuccess || splits == 1) return e;
+    return run_linear_join(acc, splits, a.M, a.N, GATED, l, st);
+}
+
+}  // namespace
+
+// parts of the sum over K: a stage takes 0.4 us of MXFP8 (K = 256) or MXFP4, 0.45 of NVFP4 (K = 256)
+int gemm_fused_splits(int fmt, int64_t tokens, int64_t out, int64_t cols, bool gated, int num_sms) {
+    const int64_t tiles = (tokens + 255) / 256 * ((out + (gated ? 127 : 255)) / (gated ? 128 : 256)), stages = (cols + 255) / 256;
+    return fused_splits(tiles, stages, fmt == kNVFP4 ? 0.45 : 0.4, (double)tokens * fused_acc_cols(out, gated) * 8, num_sms / 2);
+}
+size_t gemm_fused_workspace(int fmt, int64_t tokens, int64_t out, int64_t cols, bool gated, int num_sms) {
+    const int n = gemm_fused_splits(fmt, tokens, out, cols, gated, num_sms);
+    return n > 1 ? (size_t)n * tokens * fused_acc_cols(out, gated) * 4 : 0;
+}
+cudaError_t run_gemm_linear(const GemmArgs& a, const LinearArgs& l, cudaStream_t st) { return fused<kLinear>(a, a, l, st); }
+cudaError_t run_gemm_gated(const GemmArgs& gate, const GemmArgs& up, const LinearArgs& l, cudaStream_t st) {
+    return fused<kGated>(gate, up, l, st);
 }
 
 }  // namespace bsq

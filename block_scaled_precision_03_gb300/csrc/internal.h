@@ -171,6 +171,62 @@ struct ClipArgs {
 size_t clip_workspace(int count, int num_sms);
 cudaError_t run_clip(const ClipArgs& a, cudaStream_t st);
 
+// ---- linear layers with their epilogue, and the gated half of a feed-forward block (linear.cu)
+struct LinearArgs {
+    const void* x;                 // BF16 [tokens, cols]
+    int64_t ldx;
+    const void* w;                 // BF16 [out, cols]; gated: the gate's
+    int64_t ldw;
+    const void* w2;                // gated: the other projection's
+    int64_t ldw2;
+    int64_t tokens, out, cols;
+    int act;
+    const void* bias;
+    int bias_bf16;
+    const void* residual;
+    int64_t ld_res;
+    void* y;                       // gated: h
+    int64_t ldy;
+    int y_bf16;
+    void* z;                       // linear: the pre-activation; gated: gate
+    int64_t ldz;
+    void* u;                       // gated: up
+    int64_t ldu;
+    const void* dy;                // backward
+    int64_t ld_dy;
+    void* dx;
+    int64_t ld_dx;
+    void* dw;
+    int64_t ld_dw;
+    void* dw2;
+    int64_t ld_dw2;
+    float* dbias;
+    void* ws;
+    int num_sms;
+    unsigned* status;
+    uint64_t timeout_ns;
+};
+constexpr int64_t kLinearMaxOut = 1ll << 24;       // the columns of a grid's second dimension
+size_t linear_workspace(int64_t tokens, int64_t out, int64_t cols, bool gated, int num_sms);
+size_t linear_backward_workspace(int64_t tokens, int64_t out, int64_t cols, bool gated, int num_sms);
+cudaError_t run_linear(const LinearArgs& a, bool gated, cudaStream_t st);
+cudaError_t run_linear_backward(const LinearArgs& a, bool gated, cudaStream_t st);
+
+// ---- the same on block-scaled operands (gemm2.cu); the LinearArgs say what the epilogue does
+int gemm_fused_splits(int fmt, int64_t tokens, int64_t out, int64_t cols, bool gated, int num_sms);
+size_t gemm_fused_workspace(int fmt, int64_t tokens, int64_t out, int64_t cols, bool gated, int num_sms);
+cudaError_t run_gemm_linear(const GemmArgs& a, const LinearArgs& l, cudaStream_t st);
+cudaError_t run_gemm_gated(const GemmArgs& gate, const GemmArgs& up, const LinearArgs& l, cudaStream_t st);
+
+// ---- AdamW over many tensors (adamw.cu)
+struct AdamwArgs {
+    const void* tensors;           // host array of bsq_adamw_tensor
+    int count;
+    const void* options;           // bsq_adamw_options
+    int num_sms;
+};
+cudaError_t run_adamw(const AdamwArgs& a, cudaStream_t st);
+
 // this device's SM count and status word (api.cu)
 int device_sms();
 unsigned* device_status();

@@ -1,0 +1,870 @@
+// Linear layers on BF16 operands with their epilogue, and the gated half of a
+// feed-forward block, forward and backward:
+//   linear   z = x w^T + bias, y = act(z) + residual
+//   gated    a = x wg^T, u = x wu^T, h = act(a) * u
+//   backward dz = dy act'(z); dx = dz w, dw = dz^T x, dbias = sum of dz's rows
+//            da = dh u act'(a), du = dh act(a); dx = da wg + du wu, dwg = da^T x,
+//            dwu = du^T x
+//
+// The products run on CTA pairs (tcgen05 cta_group::2, M = N = 256, K = 16 per
+// MMA): each CTA stages its own 128 rows of A and of B by TMA (128-byte
+// swizzle), the even CTA issues the MMAs, and two accumulators of 256
+// tensor-memory columns let the epilogue of one tile run under the MMAs of the
+// next.  An operand is read in the layout it has in memory, K-major or MN-major.
+//
+// Gated: a pair's tile is 128 columns of both projections.  The even CTA's 128
+// rows of B are wg's, the odd one's wu's, so that one MMA makes both, and each
+// CTA has gate and up of its own rows in its own tensor memory, 128 columns
+// apart: the activation and the product need nothing from anywhere else.
+//
+// Up to kFewTokens tokens a product is bound by streaming w and runs the other
+// way round, z^T = w x^T: w's rows are the tile's 256 rows and the tokens its 16
+// to 128 columns, so that a stage is nearly all w.  Gated, a stage is 64 of K of
+// 256 rows of wg and of wu, for two accumulators.
+//
+// dx of a gated layer is one product over K = 2 F: first da wg, then du wu.
+// Where there are too few tiles for the pairs the sum over K is split; a second
+// kernel adds the parts in their order and does the epilogue.
+//
+// The tensor cores' FP32 sums are not rounded to nearest: a sum over K = 4096
+// loses some 6e-6.  An accumulator is read out every kSumChunk stages (K =
+// 4096) where a BF16 result hides that, every kChunk (K = 512) for FP32 results,
+// and added up in registers.
+#include <algorithm>
+#include <cuda.h>
+#include "common.cuh"
+#include "fused.cuh"
+#include "internal.h"
+#include "launch.cuh"
+#include "pair_gemm.cuh"
+#include "per_device.h"
+#include "tcgen05.cuh"
+#include "tmap.h"
+
+namespace bsq {
+namespace {
+
+using namespace pair;
+
+enum { kFwd, kFew, kDx, kDw };
+enum { kWaitLaunch, kWaitStart, kWaitEnd };         // when a product waits for the kernel before it: see head.cu
+
+constexpr int kStages = 3;
+constexpr int kMaxStages = 6;                       // few tokens: as many as fit
+constexpr int kFewTokens = 128;
+constexpr int kChunk = 4, kSumChunk = 32;           // stages of K = 128 (few tokens, gated: twice as many of 64)
+constexpr int kSubBytes = 128 * kSubK * 2;          // one CTA's 128 rows of an operand, one sub-step
+constexpr int kOpBytes = kSub * kSubBytes;
+constexpr int kMmas = 4 * kSub;                     // per stage
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr uint32_t kTmemCols = 512;
+constexpr int kStageBytes = 4096;                   // a warp's staging: two chunks of 32 rows x 64 bytes
+constexpr int kSmem = 1024 + kStages * 2 * kOpBytes + kEpiWarps * kStageBytes + 256;
+static_assert(kSmem <= 232448, "shared memory per block");
+
+__host__ __device__ constexpr bool a_mn(int mode) { return mode == kDw; }
+__host__ __device__ constexpr bool b_mn(int mode) { return mode == kDx || mode == kDw; }
+
+struct Params {
+    int64_t M, N;                  // output; few tokens: M features, N tokens
+    int32_t k_stages, chunk;       // K stages in all; stages per accumulator
+    int32_t m_tiles, n_tiles, splits, split_stages, total;
+    int32_t raster, raster_n;
+    int32_t tile_m, tile_n;
+    int32_t stages, b_bytes;       // stages of the ring, one CTA's bytes of B per stage
+    int32_t half;                  // kDx gated: stages of the first pair of operands; kDw gated: its tiles along M
+    uint32_t tx;                   // bytes one CTA loads per stage
+    int32_t wait;
+    float* acc;                    // splits > 1: few tokens' partial sums [split][token][ld_acc]
+    int64_t ld_acc;
+    Fused f;
+    unsigned* status;
+    uint64_t timeout_ns;
+};
+struct Maps {
+    CUtensorMap a[2], b[2], out[3];
+};
+
+int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+int64_t div_up(int64_t v, int64_t m) { return (v + m - 1) / m; }
+
+// The column of column c of a gated layer's gate among its parts of a sum; up's is 128 further
+__device__ __forceinline__ int64_t gate_col(int64_t c) { return (c >> 7) * 256 + (c & 127); }
+
+// LONG: a tile's sum over K takes several accumulators.
+template <int MODE, bool GATED, bool LONG>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+linear_gemm_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // [stages] of A, [stages] of B, the epilogue's staging; the barriers come last
+    constexpr bool FEW = MODE == kFew;
+    constexpr int SUB_B = FEW && GATED ? 1 : kSub;             // sub-steps of B in a stage
+    const int S = FEW ? p.stages : kStages, b_bytes = FEW ? p.b_bytes : kOpBytes, sub_b = b_bytes / SUB_B;
+    uint8_t* smA = base;
+    uint8_t* smB = smA + S * kOpBytes;
+    uint8_t* smOut = base + kStages * 2 * kOpBytes;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(base + (kSmem - 1024 - 256));
+    // full[S], empty[S], tfull[2], tempty[2], drain
+    const uint32_t full0 = tc::smem_u32(bars), empty0 = tc::smem_u32(bars + kMaxStages);
+    const uint32_t tfull0 = tc::smem_u32(bars + 2 * kMaxStages), tempty0 = tc::smem_u32(bars + 2 * kMaxStages + 2);
+    const uint32_t drain = tc::smem_u32(bars + 2 * kMaxStages + 4);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 5);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* issued_slot = reinterpret_cast<volatile int*>(tmem_slot + 2);
+    volatile int* peer_abort = reinterpret_cast<volatile int*>(tmem_slot + 3);
+    static_assert(8 * (2 * kMaxStages + 5) + 16 <= 256, "barrier area");
+
+    if (p.wait != kWaitStart) pdl_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = tc::cluster_rank();
+    const bool leader = rank == 0;
+    const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < S; s++) {
+            tc::mbar_init(full0 + 8 * s, 1);
+            tc::mbar_init(empty0 + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; b++) {
+            tc::mbar_init(tfull0 + 8 * b, 1);
+            tc::mbar_init(tempty0 + 8 * b, 2 * kEpiWarps);
+        }
+        tc::mbar_init(drain, 1);
+        *abort_flag = 0;
+        *issued_slot = 0;
+        *peer_abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        tc::prefetch_tmap(&tm.a[0]);
+        tc::prefetch_tmap(&tm.b[0]);
+    }
+    if (warp == 1) tc::tmem_alloc<2>(tc::smem_u32(tmem_slot), kTmemCols);
+    tc::fence_before();
+    __syncthreads();
+    tc::cluster_sync();
+    tc::fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer (both CTAs)
+        if (lane == 0) {
+            const uint32_t full_c0 = tc::mapa(full0, 0);
+            int stage = 0, issued = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            if (p.wait == kWaitStart) {
+                pdl_wait();
+                pdl_launch_dependents();
+            }
+            for (int t = cid; t < p.total && ok; t += ncl) {
+                const TileAt ti = tile_at(p, t);
+                // which of the two operand pairs of a gated layer's dw
+                const int which = MODE == kDw && GATED && ti.mt >= p.half ? 1 : 0;
+                const int am = (ti.mt - which * p.half) * p.tile_m + (int)rank * (p.tile_m / 2);
+                // a gated layer's tile is 128 columns of either projection
+                const int bn = MODE == kFwd && GATED ? ti.nt * 128 : ti.nt * p.tile_n + (int)rank * (p.tile_n / 2);
+                const CUtensorMap* mb = MODE == kFwd && GATED ? &tm.b[rank] : &tm.b[0];
+                for (int kb = ti.k0; kb < ti.k1; kb++) {
+                    if (!wait(empty0 + 8 * stage, phase ^ 1, abort_flag, p.status, p.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb = full_c0 + 8 * stage;
+                    if (leader) tc::mbar_expect_tx(full0 + 8 * stage, 2 * p.tx);
+                    const int second = MODE == kDx && GATED && kb >= p.half ? 1 : 0;
+                    const CUtensorMap* ma = MODE == kDx && GATED ? &tm.a[second] : &tm.a[which];
+                    if (MODE == kDx && GATED) mb = &tm.b[second];
+#pragma unroll
+                    for (int j = 0; j < kSub; j++) {
+                        const int k = FEW && GATED ? kb * kSubK : ((kb - second * p.half) * kSub + j) * kSubK;
+                        const uint32_t da = tc::smem_u32(smA + stage * kOpBytes + j * kSubBytes);
+                        const uint32_t db = tc::smem_u32(smB + stage * b_bytes + j * sub_b);
+                        if (a_mn(MODE)) {
+                            tc::tma_load_2d_pair(da, ma, am, k, fb);
+                            tc::tma_load_2d_pair(da + 8192, ma, am + 64, k, fb);
+                        } else {
+                            tc::tma_load_2d_pair(da, FEW && GATED ? &tm.a[j] : ma, k, am, fb);
+                        }
+                        if (b_mn(MODE)) {
+                            tc::tma_load_2d_pair(db, mb, bn, k, fb);
+                            tc::tma_load_2d_pair(db + 8192, mb, bn + 64, k, fb);
+                        } else if (j < SUB_B) {
+                            tc::tma_load_2d_pair(db, mb, k, bn, fb);
+                        }
+                    }
+                    ++issued;
+                    if (++stage == S) { stage = 0; phase ^= 1; }
+                }
+            }
+            *issued_slot = issued;
+            if (!ok) *abort_flag = 1;
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer (even CTA)
+        if (lane == 0 && leader) {
+            const uint32_t idesc = idesc_bf16(a_mn(MODE), b_mn(MODE)) | ((uint32_t)(p.tile_n >> 3) << 17);
+            // 16 k further: 32 bytes of a K-major row, 16 rows of an MN-major tile
+            constexpr uint32_t a_step = a_mn(MODE) ? 2048 >> 4 : 2, b_step = b_mn(MODE) ? 2048 >> 4 : 2;
+            const uint64_t ad0 = a_mn(MODE) ? desc_mn_sw128(tc::smem_u32(smA)) : tc::desc_sw128(tc::smem_u32(smA));
+            const uint64_t bd0 = b_mn(MODE) ? desc_mn_sw128(tc::smem_u32(smB)) : tc::desc_sw128(tc::smem_u32(smB));
+            int stage = 0, iter = 0;
+            uint32_t phase = 0;
+            bool ok = true, any = false, ready = false;
+            if (p.wait == kWaitStart) pdl_wait();          // the limit of its waits counts from there
+            for (int t = cid; t < p.total && ok; t += ncl) {
+                const TileAt ti = tile_at(p, t);
+                for (int c0 = ti.k0; c0 < ti.k1 && ok; c0 += p.chunk, ++iter) {
+                    const int c1 = min(ti.k1, c0 + p.chunk), buf = iter & 1;
+                    if (!wait(tempty0 + 8 * buf, ((iter >> 1) & 1) ^ 1, abort_flag, p.status, p.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t d = tmem + (uint32_t)buf * kTile;
+                    for (int kb = c0; kb < c1; kb++) {
+                        if (!ready && !wait(full0 + 8 * stage, phase, abort_flag, p.status, p.timeout_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        tc::fence_after();
+                        const Desc ad = Desc(ad0) + (uint32_t)(stage * (kOpBytes >> 4));
+                        const Desc bd = Desc(bd0) + (uint32_t)(stage * (b_bytes >> 4));
+                        const int next = stage + 1 == S ? 0 : stage + 1;
+                        const uint32_t next_phase = next == 0 ? phase ^ 1 : phase;
+                        // the next stage's barrier is tested while this stage's MMAs run
+#pragma unroll
+                        for (int m = 0; m < kMmas; m++) {
+                            if (m == kMmas - 1) ready = tc::mbar_test(full0 + 8 * next, next_phase);
+                            const Desc am = ad + (m >> 2) * (kSubBytes >> 4) + (m & 3) * a_step;
+                            if (FEW && GATED) {            // wg into one accumulator, wu into the one beside it
+                                const Desc bm = bd + (m & 3) * b_step;
+                                if ((m & 3) == 0) mma_bf16<false>(d + (m >> 2) * 128, am, bm, idesc, kb != c0);
+                                else mma_bf16<true>(d + (m >> 2) * 128, am, bm, idesc, 1);
+                            } else {
+                                const Desc bm = bd + (m >> 2) * (sub_b >> 4) + (m & 3) * b_step;
+                                if (m == 0) mma_bf16<false>(d, am, bm, idesc, kb != c0);
+                                else mma_bf16<true>(d, am, bm, idesc, 1);
+                            }
+                        }
+                        any = true;
+                        tc::commit<2>(empty0 + 8 * stage, 3);
+                        if (kb == c1 - 1) tc::commit<2>(tfull0 + 8 * buf, 3);
+                        stage = next;
+                        phase = next_phase;
+                    }
+                }
+            }
+            if (!ok) *abort_flag = 1;
+            if (any) {
+                // every MMA issued finishes before tensor memory is released
+                tc::commit<2>(drain, 1);
+                volatile int no_abort = 0;
+                tc::mbar_wait(drain, 0, &no_abort, nullptr, 100000000ull);
+            }
+        }
+    } else {
+        // ------------------------------------------------ epilogue (both CTAs)
+        const int q = warp & 3, half = (warp - 2) >> 2;
+        const uint32_t tempty_c0 = tc::mapa(tempty0, 0);
+        Staging<2> st{tc::smem_u32(smOut + (warp - 2) * kStageBytes), 0};
+        if (p.wait == kWaitStart) pdl_wait();
+        int iter = 0;
+        if constexpr (FEW) {
+            // A thread owns one feature (rows past the tile's are whatever shared memory held: they stay
+            // in their rows) and half of the tokens, in sixteens; neighbouring lanes write neighbouring
+            // features.
+            const int share = ((int)p.N + 31) / 32 * 16, own = half * share;
+            const int tokens = min(share, (int)p.N - own);             // of this warp, at most 64; 0 or less: none
+            constexpr int P = GATED ? 2 : 1;
+            for (int t = cid; t < p.total; t += ncl) {
+                const TileAt ti = tile_at(p, t);
+                const int row = ti.mt * p.tile_m + (int)rank * (p.tile_m / 2) + q * 32 + lane;
+                const bool in = q * 32 + lane < p.tile_m / 2 && row < p.M;
+                float z[P][64] = {};
+                bool ok = true;
+                for (int c0 = ti.k0; c0 < ti.k1; c0 += p.chunk, ++iter) {
+                    const int buf = iter & 1;
+                    ok = wait(tfull0 + 8 * buf, (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns);
+                    if (!ok) break;
+                    tc::fence_after();
+                    const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kTile + own);
+#pragma unroll
+                    for (int c = 0; c < 64; c += 16)
+                        if (c < tokens)
+#pragma unroll
+                            for (int i = 0; i < P; i++) add_acc(z[i] + c, ta + 128 * i + c);
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive_cluster(tempty_c0 + 8 * buf);
+                }
+                if (!ok) break;
+                const float bias = !GATED && p.f.bias && in ? load_as_float(p.f.bias, row, p.f.bias_bf16) : 0.0f;
+#pragma unroll 1
+                for (int c = 0; c < tokens; c += 16) {
+                    float v[16];
+#pragma unroll
+                    for (int j = 0; j < 16; j++) v[j] = z[0][j] + bias;
+                    const int64_t token = own + c;
+                    const int n = in ? min(16, tokens - c) : 0;
+                    if (p.splits > 1) {
+                        float* a = p.acc + ((int64_t)ti.split * p.N + token) * p.ld_acc + (GATED ? gate_col(row) : row);
+#pragma unroll
+                        for (int j = 0; j < 16; j++)
+                            if (j < n) {
+                                a[j * p.ld_acc] = z[0][j];
+                                if (GATED) a[j * p.ld_acc + 128] = z[P - 1][j];
+                            }
+                    } else {
+                        if (p.f.z) {
+#pragma unroll
+                            for (int j = 0; j < 16; j++)
+                                if (j < n) {
+                                    p.f.z[(token + j) * p.f.ldz + row] = __float2bfloat16_rn(v[j]);
+                                    if (GATED) p.f.u[(token + j) * p.f.ldu + row] = __float2bfloat16_rn(z[P - 1][j]);
+                                }
+                        }
+                        activate(p.f.act, v);
+#pragma unroll
+                        for (int j = 0; j < 16; j++)
+                            if (j < n) {
+                                float y = GATED ? v[j] * z[P - 1][j] : v[j];
+                                if (!GATED && p.f.residual)
+                                    y += load_as_float(p.f.residual, (token + j) * p.f.ld_res + row, p.f.y_bf16);
+                                const int64_t at = (token + j) * p.f.ldy + row;
+                                if (p.f.y_bf16) static_cast<__nv_bfloat16*>(p.f.y)[at] = __float2bfloat16_rn(y);
+                                else static_cast<float*>(p.f.y)[at] = y;
+                            }
+                    }
+#pragma unroll
+                    for (int i = 0; i < P; i++)
+#pragma unroll
+                        for (int j = 0; j < 48; j++) z[i][j] = z[i][j + 16];
+                }
+            }
+        } else {
+            // A thread owns one row and 128 of the tile's columns (gated: 64 of each projection's)
+            constexpr bool PROJ = MODE == kFwd && GATED;
+            constexpr int OWN = PROJ ? 64 : 128;
+            for (int t = cid; t < p.total; t += ncl) {
+                const TileAt ti = tile_at(p, t);
+                const int which = MODE == kDw && GATED && ti.mt >= p.half ? 1 : 0;
+                const int64_t row0 = (int64_t)(ti.mt - which * p.half) * kTile + rank * 128 + q * 32;
+                const int64_t col0 = PROJ ? (int64_t)ti.nt * 128 + half * 64 : (int64_t)ti.nt * kTile + half * 128;
+                const bool live = row0 < p.M && col0 < p.N;
+                const uint32_t ta0 = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * OWN);
+                // 32 columns of the sums, from the thread's column c on, leave
+                const auto leave = [&](float (&v)[32], const float (&u)[32], int c) {
+                    if (p.splits > 1) {
+                        const int64_t at = (int64_t)ti.nt * kTile + half * OWN + c;
+                        const int64_t r = row0 + (int64_t)which * p.half * kTile;
+                        store_part(v, st, &tm.out[0], (int)at, (int)r, ti.split, lane);
+                        if (PROJ) store_part(u, st, &tm.out[0], (int)at + 128, (int)r, ti.split, lane);
+                    } else if (MODE != kFwd) {
+                        if (col0 + c < p.N) store_bf16(v, 1.0f, st.base, &tm.out[which], (int)col0 + c, (int)row0, st.n, lane);
+                    } else if (col0 + c < p.N) {
+                        if (PROJ) finish_gated(v, u, p.f, &tm.out[0], &tm.out[1], &tm.out[2], row0, col0 + c, p.M, p.N, st, lane);
+                        else finish_linear(v, p.f, &tm.out[0], &tm.out[1], row0, col0 + c, p.M, p.N, st, lane);
+                    }
+                };
+                if constexpr (!LONG) {
+                    const int buf = iter & 1;
+                    if (!wait(tfull0 + 8 * buf, (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns)) break;
+                    tc::fence_after();
+                    ++iter;
+                    if (live)
+#pragma unroll 1
+                        for (int c = 0; c < OWN; c += 32) {
+                            float v[32], u[32];
+                            load_acc(v, ta0 + (uint32_t)(buf * kTile + c));
+                            if (PROJ) load_acc(u, ta0 + (uint32_t)(buf * kTile + 128 + c));
+                            leave(v, u, c);
+                        }
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive_cluster(tempty_c0 + 8 * buf);
+                } else {
+                    float z[128] = {};
+                    bool ok = true;
+                    for (int c0 = ti.k0; c0 < ti.k1; c0 += p.chunk, ++iter) {
+                        ok = wait(tfull0 + 8 * (iter & 1), (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns);
+                        if (!ok) break;
+                        tc::fence_after();
+                        if (live)
+#pragma unroll
+                            for (int c = 0; c < 128; c += 16)
+                                add_acc(z + c, ta0 + (uint32_t)((iter & 1) * kTile + (PROJ && c >= 64 ? c + 64 : c)));
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive_cluster(tempty_c0 + 8 * (iter & 1));
+                    }
+                    if (!ok) break;
+                    if (!live) continue;
+                    // the loop stays one, and z moves on: the epilogue's code is long
+#pragma unroll 1
+                    for (int c = 0; c < OWN; c += 32) {
+                        float v[32], u[32];
+#pragma unroll
+                        for (int j = 0; j < 32; j++) {
+                            v[j] = z[j];
+                            if (PROJ) u[j] = z[64 + j];
+                        }
+                        leave(v, u, c);
+#pragma unroll
+                        for (int j = 0; j < 96; j++) z[j] = z[j + 32];
+                    }
+                }
+            }
+        }
+        if (lane == 0) tc::bulk_wait_all();
+    }
+
+    // what was launched before this kernel is done when this kernel is
+    if (p.wait == kWaitEnd) pdl_wait();
+    // Both CTAs have stopped issuing.  If either gave up, both know after the barrier, and the even CTA
+    // waits (bounded) for the loads still in flight before either may exit.
+    tc::fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && *abort_flag) st_cluster(tc::mapa(tc::smem_u32((const void*)peer_abort), rank ^ 1), 1);
+    tc::cluster_sync();
+    if (*abort_flag || *peer_abort) {
+        if (leader && warp == 0 && lane == 0)
+            drain_loads(full0, S, *issued_slot, tc::ld_cluster_s32(tc::mapa(tc::smem_u32((const void*)issued_slot), 1)), p.tx);
+        tc::cluster_sync();
+    }
+    if (warp == 1) {
+        tc::fence_after();
+        tc::tmem_dealloc<2>(tmem, kTmemCols);
+    }
+}
+
+// ------------------------------------------------------- around the products
+// The parts of a split sum [splits][M][ld], added in their order, and the forward epilogue: 4 columns a thread.
+template <bool GATED>
+__global__ void __launch_bounds__(256) linear_join_kernel(const float* acc, int splits, int64_t M, int64_t N, int64_t ld,
+                                                         const __grid_constant__ Fused f) {
+    const int64_t per = (N + 3) / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    pdl_wait();
+    if (i >= M * per) return;
+    const int64_t row = i / per, col = (i - row * per) * 4;
+    const int n = (int)min((int64_t)4, N - col);
+    const auto sum = [&](int64_t at) {
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int k = 0; k < splits; k++) {
+            const float4 x = *reinterpret_cast<const float4*>(acc + (k * M + row) * ld + at);
+            s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+        }
+        return s;
+    };
+    const float4 s = sum(GATED ? gate_col(col) : col), t = GATED ? sum(gate_col(col) + 128) : s;
+    float v[4] = {s.x, s.y, s.z, s.w};
+    const float u[4] = {t.x, t.y, t.z, t.w};
+    if (!GATED && f.bias)
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            if (j < n) v[j] += load_as_float(f.bias, col + j, f.bias_bf16);
+    if (f.z)
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            if (j < n) {
+                f.z[row * f.ldz + col + j] = __float2bfloat16_rn(v[j]);
+                if (GATED) f.u[row * f.ldu + col + j] = __float2bfloat16_rn(u[j]);
+            }
+    activate(f.act, v);
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+        if (j < n) {
+            float y = GATED ? v[j] * u[j] : v[j];
+            if (!GATED && f.residual) y += load_as_float(f.residual, row * f.ld_res + col + j, f.y_bf16);
+            const int64_t at = row * f.ldy + col + j;
+            if (f.y_bf16) static_cast<__nv_bfloat16*>(f.y)[at] = __float2bfloat16_rn(y);
+            else static_cast<float*>(f.y)[at] = y;
+        }
+}
+
+// out = the sum of the parts [splits][rows_all][D] from row `row0` on; 8 columns a thread
+__global__ void __launch_bounds__(256) linear_sum_kernel(const float* acc, int splits, int64_t rows_all, int64_t row0,
+                                                        int64_t rows, int64_t D, __nv_bfloat16* out, int64_t ld) {
+    const int64_t per = D / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    pdl_wait();
+    if (i >= rows * per) return;
+    const int64_t r = i / per, c = (i - r * per) * 8;
+    float v[8] = {};
+    for (int s = 0; s < splits; s++) {
+        const float4* a = reinterpret_cast<const float4*>(acc + (s * rows_all + row0 + r) * D + c);
+        const float4 x = a[0], y = a[1];
+        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+    }
+    Pack<__nv_bfloat16, 8> k;
+    k.pack(v);
+    k.store(out + r * ld + c);
+}
+
+// The epilogue's gradient, 8 columns of kRows rows a thread:
+//   linear  dz = dy act'(z) (z nullptr: dz = dy), and the column sums of a CTA's rows for dbias
+//   gated   da = dh u act'(a), du = dh act(a)
+// BF16 in, FP32 in between, BF16 out (nullptr: the sums only).  Bound by memory.
+constexpr int kGradRows = 64;                       // of a CTA: 8 threads' rows of 8
+struct SlopeArgs {
+    const __nv_bfloat16* dy;
+    int64_t ld_dy;
+    const __nv_bfloat16* z;        // gated: the gate's
+    int64_t ldz;
+    const __nv_bfloat16* u;
+    int64_t ldu;
+    __nv_bfloat16* dz;             // [rows][ld]; gated: da, and du behind it
+    __nv_bfloat16* du;
+    int64_t ld;
+    float* sums;                   // [row blocks][cols]
+    int64_t rows, cols;
+};
+template <int ACT, bool GATED, bool VEC>
+__global__ void __launch_bounds__(256) linear_slope_kernel(const SlopeArgs a) {
+    pdl_launch_dependents();
+    const int64_t col = ((int64_t)blockIdx.y * 32 + (threadIdx.x & 31)) * 8;
+    const int64_t row0 = (int64_t)blockIdx.x * kGradRows;
+    const int n = (int)max((int64_t)0, min((int64_t)8, a.cols - col));
+    float sum[8] = {};
+    if (n > 0)
+#pragma unroll 2
+        for (int k = threadIdx.x >> 5; k < kGradRows; k += 8) {
+            const int64_t row = row0 + k;
+            if (row >= a.rows) break;
+            const auto get = [&](const __nv_bfloat16* p, int64_t ld, float (&f)[8]) {
+                if (VEC) {
+                    Pack<__nv_bfloat16, 8> v;
+                    v.load(p + row * ld + col);
+                    v.unpack(f);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; j++) f[j] = j < n ? __bfloat162float(p[row * ld + col + j]) : 0.0f;
+                }
+            };
+            float d[8], z[8] = {}, u[8] = {};
+            get(a.dy, a.ld_dy, d);
+            if (ACT != kActIdentity || GATED) get(a.z, a.ldz, z);
+            if (GATED) get(a.u, a.ldu, u);
+            float o[8], w[8];
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                float value;
+                const float slope = act_slope<ACT>(z[j], value);
+                // (not contracted with the sum: dbias alone comes out as it does beside the products)
+                o[j] = GATED ? d[j] * u[j] * slope : ACT == kActIdentity ? d[j] : __fmul_rn(d[j], slope);
+                w[j] = d[j] * value;
+                if (!GATED) sum[j] += o[j];
+            }
+            // the workspace's rows hold whole vectors
+            if (a.dz) {
+                Pack<__nv_bfloat16, 8> v;
+                v.pack(o);
+                v.store(a.dz + row * a.ld + col);
+                if (GATED) {
+                    v.pack(w);
+                    v.store(a.du + row * a.ld + col);
+                }
+            }
+        }
+    if (GATED || !a.sums) return;
+    __shared__ float all[8][256 + 8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) all[threadIdx.x >> 5][(threadIdx.x & 31) * 8 + j] = sum[j];
+    __syncthreads();
+    const int64_t c = (int64_t)blockIdx.y * 256 + threadIdx.x;
+    if (c >= a.cols) return;
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; w++) s += all[w][threadIdx.x];
+    a.sums[(int64_t)blockIdx.x * a.cols + c] = s;
+}
+// dbias = the blocks' column sums in their order: 32 columns a CTA, eight threads each
+__global__ void __launch_bounds__(256) linear_bias_kernel(const float* sums, int64_t blocks, int64_t cols, float* out) {
+    __shared__ float all[8][32];
+    const int64_t c = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
+    pdl_launch_dependents();
+    pdl_wait();
+    float s = 0.0f;
+    if (c < cols)
+#pragma unroll 4
+        for (int64_t b = threadIdx.x >> 5; b < blocks; b += 8) s += sums[b * cols + c];
+    all[threadIdx.x >> 5][threadIdx.x & 31] = s;
+    __syncthreads();
+    if (threadIdx.x >= 32 || c >= cols) return;
+    s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; w++) s += all[w][threadIdx.x];
+    out[c] = s;
+}
+
+// How a product is cut: rows of a pair (few tokens), and parts of the sum over K.
+constexpr double kStageUs = 0.55;                   // a pair's stage of K = 128
+struct Cut {
+    bool few;
+    int tile_m, splits;
+};
+// Few tokens: what the busiest pair streams, in bytes of w, decides; parts cost a launch and their own bytes.
+Cut few_cut(int64_t N, int64_t K, int64_t T, bool gated, int num_sms) {
+    const int64_t pairs = std::max(1, num_sms / 2), stage_k = gated ? kSubK : kSub * kSubK, stages = div_up(K, stage_k);
+    Cut best{true, kTile, 1};
+    double least = 0.0;
+    for (int64_t n = 1; n == 1 || (n <= 16 && n * 4 <= stages); n++) {
+        const int64_t per = div_up(stages, n);
+        for (int t = kTile; t >= 96; t -= 16) {
+            const double load = (double)div_up(div_up(N, t) * fused_parts(stages, n), pairs) * t * per * stage_k * (gated ? 4 : 2);
+            // 80 GB/s for a pair; the join's launch and the parts, written and read
+            const double us = load / 80e3 + (n > 1 ? 2.5 + (double)n * T * N * (gated ? 16 : 8) / 5e6 : 0.0);
+            if (least == 0.0 || us < least) {
+                least = us;
+                best = {true, t, fused_parts(stages, n)};
+            }
+        }
+    }
+    return best;
+}
+Cut forward_cut(int64_t T, int64_t N, int64_t K, bool gated, int num_sms) {
+    if (T <= kFewTokens) return few_cut(N, K, T, gated, num_sms);
+    const int64_t tiles = div_up(T, kTile) * div_up(N, gated ? 128 : kTile);
+    return {false, kTile, fused_splits(tiles, div_up(K, kSub * kSubK), kStageUs, (double)T * fused_acc_cols(N, gated) * 8, num_sms / 2)};
+}
+
+struct Operand {
+    const void* p;
+    int64_t rows, cols, ld;
+};
+
+template <int MODE, bool GATED, bool LONG>
+cudaError_t launch_gemm(const Params& p, const Maps& tm, int pairs, cudaStream_t st) {
+    static SharedMemory smem;
+    const cudaError_t e = smem.allow(reinterpret_cast<const void*>(linear_gemm_kernel<MODE, GATED, LONG>), kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_k(p.wait != kWaitLaunch, linear_gemm_kernel<MODE, GATED, LONG>, dim3(2 * pairs), kThreads, kSmem, st, tm, p);
+}
+// K: the depth of each operand pair
+template <int MODE, bool GATED>
+cudaError_t gemm(Params p, const Operand (&a)[2], const Operand (&b)[2], Maps& tm, int64_t K, const Cut& cut, int wait,
+                 bool fine, const LinearArgs& args, cudaStream_t st) {
+    constexpr bool FEW = MODE == kFew;
+    const int tile_n = FEW ? (int)up(p.N, 16) : kTile;
+    for (int i = 0; i < 2; i++) {
+        const int j = GATED ? i : 0;
+        const int jb = GATED && (MODE == kFwd || MODE == kDx) ? i : 0;
+        if (!map_operand(&tm.a[i], a[j].p, a[j].rows, a[j].cols, a[j].ld, a_mn(MODE) ? kSubK : cut.tile_m / 2) ||
+            !map_operand(&tm.b[i], b[jb].p, b[jb].rows, b[jb].cols, b[jb].ld, b_mn(MODE) ? kSubK : tile_n / 2))
+            return cudaErrorInvalidValue;
+    }
+    const int64_t stage_k = FEW && GATED ? kSubK : kSub * kSubK;
+    const int64_t stages = div_up(K, stage_k);
+    p.half = MODE == kDx ? (int32_t)stages : (int32_t)div_up(p.M, cut.tile_m);
+    p.k_stages = (int32_t)(MODE == kDx && GATED ? 2 * stages : stages);
+    p.tile_m = cut.tile_m;
+    p.tile_n = tile_n;
+    p.b_bytes = (FEW && GATED ? 1 : kSub) * (tile_n / 2) * kSubK * 2;
+    p.stages = FEW ? std::min(kMaxStages, kStages * 2 * kOpBytes / (kOpBytes + p.b_bytes)) : kStages;
+    p.tx = (uint32_t)(kSub * (cut.tile_m / 2) * kSubK * 2 + p.b_bytes);
+    p.m_tiles = (int32_t)div_up(p.M, cut.tile_m) * (MODE == kDw && GATED ? 2 : 1);
+    p.n_tiles = (int32_t)div_up(p.N, MODE == kFwd && GATED ? 128 : tile_n);
+    p.split_stages = (int32_t)div_up(p.k_stages, cut.splits);
+    p.splits = (int32_t)div_up(p.k_stages, p.split_stages);
+    p.chunk = (fine ? kChunk : kSumChunk) * (FEW && GATED ? 2 : 1);
+    const int64_t total = (int64_t)p.m_tiles * p.n_tiles * p.splits;
+    if (total > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    p.total = (int32_t)total;
+    p.wait = wait;
+    p.status = args.status;
+    p.timeout_ns = args.timeout_ns;
+    const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(args.num_sms / 2, total));
+    choose_raster(p, K, pairs);
+    if constexpr (!FEW)
+        if (p.split_stages <= p.chunk) return launch_gemm<MODE, GATED, false>(p, tm, pairs, st);
+    return launch_gemm<MODE, GATED, true>(p, tm, pairs, st);
+}
+
+template <bool GATED>
+cudaError_t forward(const LinearArgs& a, cudaStream_t st) {
+    const int64_t T = a.tokens, N = a.out, K = a.cols;
+    const Cut cut = forward_cut(T, N, K, GATED, a.num_sms);
+    Params p{};
+    Maps tm{};
+    Fused& f = p.f;
+    fused_args(f, a);
+    p.acc = static_cast<float*>(a.ws);
+    p.ld_acc = fused_acc_cols(N, GATED);
+    const Operand x{a.x, T, K, a.ldx}, w0{a.w, N, K, a.ldw}, w1{GATED ? a.w2 : a.w, N, K, GATED ? a.ldw2 : a.ldw};
+    cudaError_t err;
+    if (cut.few) {
+        p.M = N;
+        p.N = T;
+        err = gemm<kFew, GATED>(p, {w0, w1}, {x, x}, tm, K, cut, kWaitLaunch, !a.y_bf16, a, st);
+    } else {
+        p.M = T;
+        p.N = N;
+        if (cut.splits > 1) {
+            if (!map_acc(&tm.out[0], p.acc, cut.splits, T, p.ld_acc)) return cudaErrorInvalidValue;
+        } else {
+            f.y_tma = fused_map(&tm.out[0], a.y, T, N, a.ldy, a.y_bf16);
+            f.z_tma = fused_map(&tm.out[1], a.z, T, N, a.ldz, true);
+            f.u_tma = GATED ? fused_map(&tm.out[2], a.u, T, N, a.ldu, true) : kNone;
+        }
+        err = gemm<kFwd, GATED>(p, {x, x}, {w0, w1}, tm, K, cut, kWaitLaunch, !a.y_bf16, a, st);
+    }
+    return err != cudaSuccess || cut.splits == 1 ? err : run_linear_join(p.acc, cut.splits, T, N, GATED, a, st);
+}
+
+// ------------------------------------------------------------- backward
+struct GradPlan {
+    int64_t ld, blocks;
+    Cut dx, dw;
+    size_t dz_bytes, sums_bytes, dx_bytes, dw_bytes;
+};
+GradPlan grad_plan(int64_t T, int64_t N, int64_t D, bool gated, int num_sms) {
+    GradPlan g{};
+    g.ld = up(N, 8);
+    g.blocks = div_up(T, kGradRows);
+    const int pairs = num_sms / 2;
+    const int64_t stages = div_up(N, kSub * kSubK) * (gated ? 2 : 1);
+    g.dx = {false, kTile, fused_splits(div_up(T, kTile) * div_up(D, kTile), stages, kStageUs, (double)T * D * 8, pairs)};
+    const int64_t rows = up(N, kTile) * (gated ? 2 : 1);
+    g.dw = {false, kTile, fused_splits(rows / kTile * div_up(D, kTile), div_up(T, kSub * kSubK), kStageUs, (double)rows * D * 8, pairs)};
+    g.dz_bytes = (size_t)(T * g.ld * 2 * (gated ? 2 : 1));
+    g.sums_bytes = gated ? 0 : (size_t)up(g.blocks * N * 4, 16);
+    g.dx_bytes = g.dx.splits > 1 ? (size_t)(g.dx.splits * T * D * 4) : 0;
+    g.dw_bytes = g.dw.splits > 1 ? (size_t)(g.dw.splits * rows * D * 4) : 0;
+    return g;
+}
+
+template <bool GATED>
+cudaError_t slope(const LinearArgs& a, const SlopeArgs& s, cudaStream_t st) {
+    const auto whole = [&](const void* p, int64_t ld) { return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0); };
+    const bool vec = s.cols % 8 == 0 && whole(s.dy, s.ld_dy) && whole(s.z, s.ldz) && whole(s.u, s.ldu);
+    const dim3 grid((unsigned)div_up(s.rows, kGradRows), (unsigned)div_up(s.cols, 256));
+    cudaError_t e = cudaErrorInvalidValue;
+#define F(A)                                                                                             \
+    e = vec ? launch_k(false, linear_slope_kernel<A, GATED, true>, grid, 256, 0, st, s)                  \
+            : launch_k(false, linear_slope_kernel<A, GATED, false>, grid, 256, 0, st, s)
+    BSQ_WITH_ACT(a.act, F)
+#undef F
+    return e;
+}
+
+template <bool GATED>
+cudaError_t backward(const LinearArgs& a, cudaStream_t st) {
+    const int64_t T = a.tokens, N = a.out, D = a.cols;
+    const GradPlan g = grad_plan(T, N, D, GATED, a.num_sms);
+    // dz is made in the workspace, or copied there for its address or pitch
+    const bool copy = GATED || a.act != kActIdentity || reinterpret_cast<uintptr_t>(a.dy) % 16 || (a.ld_dy % 8 && T > 1);
+    uint8_t* ws = static_cast<uint8_t*>(a.ws);
+    __nv_bfloat16* dz = reinterpret_cast<__nv_bfloat16*>(ws);
+    __nv_bfloat16* du = dz + T * g.ld;
+    float* sums = reinterpret_cast<float*>(ws + g.dz_bytes);
+    float* dx_acc = reinterpret_cast<float*>(ws + g.dz_bytes + g.sums_bytes);
+    float* dw_acc = reinterpret_cast<float*>(ws + g.dz_bytes + g.sums_bytes + g.dx_bytes);
+    cudaError_t e = cudaSuccess;
+    bool behind = false;                           // a kernel of this call runs before the next one
+    const bool products = a.dx || a.dw;
+    if ((copy && products) || a.dbias) {
+        SlopeArgs s{static_cast<const __nv_bfloat16*>(a.dy), a.ld_dy, static_cast<const __nv_bfloat16*>(a.z), a.ldz,
+                    static_cast<const __nv_bfloat16*>(a.u), a.ldu, copy && products ? dz : nullptr, du, g.ld,
+                    a.dbias ? sums : nullptr, T, N};
+        e = slope<GATED>(a, s, st);
+        behind = true;
+        if (e == cudaSuccess && a.dbias)
+            e = launch_k(true, linear_bias_kernel, dim3((unsigned)div_up(N, 32)), 256, 0, st, sums, g.blocks, N, a.dbias);
+    }
+    const Operand d0 = copy ? Operand{dz, T, N, g.ld} : Operand{a.dy, T, N, T > 1 ? a.ld_dy : up(N, 8)};
+    const Operand d1 = GATED ? Operand{du, T, N, g.ld} : d0;
+    const Operand w0{a.w, N, D, a.ldw}, w1{GATED ? a.w2 : a.w, N, D, GATED ? a.ldw2 : a.ldw}, x{a.x, T, D, a.ldx};
+    const auto sum = [&](const float* acc, int splits, int64_t all, int64_t row0, int64_t rows, void* to, int64_t ld) {
+        return launch_k(true, linear_sum_kernel, dim3((unsigned)div_up(rows * (D / 8), 256)), 256, 0, st, acc, splits, all, row0, rows,
+                        D, static_cast<__nv_bfloat16*>(to), ld);
+    };
+    if (e == cudaSuccess && a.dx) {
+        Params p{};
+        Maps tm{};
+        p.M = T;
+        p.N = D;
+        if (!(g.dx.splits > 1 ? map_acc(&tm.out[0], dx_acc, g.dx.splits, T, D) : tmap::out_2d(&tm.out[0], a.dx, T, D, a.ld_dx, true)))
+            return cudaErrorInvalidValue;
+        e = gemm<kDx, GATED>(p, {d0, d1}, {w0, w1}, tm, N, g.dx, behind ? kWaitStart : kWaitLaunch, false, a, st);
+        if (e == cudaSuccess && g.dx.splits > 1) e = sum(dx_acc, g.dx.splits, T, 0, T, a.dx, a.ld_dx);
+    }
+    if (e == cudaSuccess && a.dw) {
+        Params p{};
+        Maps tm{};
+        p.M = N;
+        p.N = D;
+        const int64_t half = up(N, kTile), all = GATED ? 2 * half : half;
+        if (g.dw.splits > 1) {
+            if (!map_acc(&tm.out[0], dw_acc, g.dw.splits, all, D)) return cudaErrorInvalidValue;
+        } else if (!tmap::out_2d(&tm.out[0], a.dw, N, D, a.ld_dw, true) ||
+                   (GATED && !tmap::out_2d(&tm.out[1], a.dw2, N, D, a.ld_dw2, true))) {
+            return cudaErrorInvalidValue;
+        }
+        // beside dx's last tiles, which waited for dz; the sum of dx's parts did not let anything start early
+        const int wait = !a.dx ? (behind ? kWaitStart : kWaitLaunch) : g.dx.splits > 1 ? kWaitLaunch : kWaitEnd;
+        e = gemm<kDw, GATED>(p, {d0, d1}, {x, x}, tm, T, g.dw, wait, false, a, st);
+        if (e == cudaSuccess && g.dw.splits > 1) e = sum(dw_acc, g.dw.splits, all, 0, N, a.dw, a.ld_dw);
+        if (e == cudaSuccess && g.dw.splits > 1 && GATED) e = sum(dw_acc, g.dw.splits, all, half, N, a.dw2, a.ld_dw2);
+    }
+    return e;
+}
+
+}  // namespace
+
+void fused_args(Fused& f, const LinearArgs& a) {
+    f.act = a.act;
+    f.y_bf16 = a.y_bf16;
+    f.bias = a.bias;
+    f.bias_bf16 = a.bias_bf16;
+    f.bias_vec = reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
+    f.residual = a.residual;
+    f.ld_res = a.ld_res;
+    f.res_vec = reinterpret_cast<uintptr_t>(a.residual) % 16 == 0 && a.ld_res * (a.y_bf16 ? 2 : 4) % 16 == 0;
+    f.y = a.y;
+    f.ldy = a.ldy;
+    f.z = static_cast<__nv_bfloat16*>(a.z);
+    f.ldz = a.ldz;
+    f.u = static_cast<__nv_bfloat16*>(a.u);
+    f.ldu = a.ldu;
+}
+int64_t fused_acc_cols(int64_t N, bool gated) { return gated ? div_up(N, 128) * 256 : up(N, 4); }
+int fused_parts(int64_t stages, int64_t n) {
+    const int64_t per = div_up(stages, n);
+    return (int)div_up(stages, per);
+}
+int fused_splits(int64_t tiles, int64_t stages, double stage_us, double part_bytes, int pairs) {
+    int64_t best = 1;
+    double least = 0.0;
+    pairs = std::max(1, pairs);
+    for (int64_t n = 1; n == 1 || (n * 4 <= stages && n * tiles <= 8 * pairs); n++) {
+        const double us = (double)div_up(tiles * n, pairs) * div_up(stages, n) * stage_us + (n > 1 ? 2.0 + n * part_bytes / 6.7e6 : 0.0);
+        if (n == 1 || us < least) {
+            least = us;
+            best = n;
+        }
+    }
+    return fused_parts(stages, best);
+}
+cudaError_t run_linear_join(const float* acc, int splits, int64_t M, int64_t N, bool gated, const LinearArgs& a, cudaStream_t st) {
+    Fused f{};
+    fused_args(f, a);
+    return launch_k(true, gated ? linear_join_kernel<true> : linear_join_kernel<false>, dim3((unsigned)div_up(M * div_up(N, 4), 256)),
+                    256, 0, st, acc, splits, M, N, fused_acc_cols(N, gated), f);
+}
+
+size_t linear_workspace(int64_t tokens, int64_t out, int64_t cols, bool gated, int num_sms) {
+    const Cut c = forward_cut(tokens, out, cols, gated, num_sms);
+    return c.splits > 1 ? (size_t)c.splits * tokens * fused_acc_cols(out, gated) * 4 : 0;
+}
+size_t linear_backward_workspace(int64_t tokens, int64_t out, int64_t cols, bool gated, int num_sms) {
+    const GradPlan g = grad_plan(tokens, out, cols, gated, num_sms);
+    return g.dz_bytes + g.sums_bytes + g.dx_bytes + g.dw_bytes;
+}
+cudaError_t run_linear(const LinearArgs& a, bool gated, cudaStream_t st) {
+    return gated ? forward<true>(a, st) : forward<false>(a, st);
+}
+cudaError_t run_linear_backward(const LinearArgs& a, bool gated, cudaStream_t st) {
+    return gated ? backward<true>(a, st) : backward<false>(a, st);
+}
+
+}  // namespace bsq

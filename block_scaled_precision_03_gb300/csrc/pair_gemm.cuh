@@ -119,6 +119,22 @@ __device__ __forceinline__ void store_acc(const float (&v)[32], uint32_t base, c
         }
     }
 }
+// store_acc through a staging area of its own (struct Staging)
+template <typename S>
+__device__ __forceinline__ void store_part(const float (&v)[32], S& st, const void* tmap, int col, int row, int split, int lane) {
+#pragma unroll
+    for (int c = 0; c < 2; c++) {
+        uint32_t w[16];
+#pragma unroll
+        for (int j = 0; j < 16; j++) w[j] = __float_as_uint(v[16 * c + j]);
+        const uint32_t buf = st.next(lane);
+        stage_chunk(w, buf, lane);
+        if (lane == 0) {
+            tma_store_3d<false>(tmap, col + 16 * c, row, split, buf);
+            tc::bulk_commit();
+        }
+    }
+}
 // 16 more columns of a chunk's accumulator onto a running sum
 __device__ __forceinline__ void add_acc(float* sum, uint32_t taddr) {
     uint32_t r[16];

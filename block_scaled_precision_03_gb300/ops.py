@@ -1,6 +1,7 @@
 """Binding of the operators around the layer: tokens sorted by expert and
-back, layer norm, the softmax cross entropy of a linear head, and the global
-gradient norm with clipping.  Like the rest of the binding it marshals
+back, layer norm, the softmax cross entropy of a linear head, linear layers with
+their epilogue and the gated feed-forward, the global gradient norm with
+clipping, and AdamW.  Like the rest of the binding it marshals
 arguments only, here mostly in a native module, since the smallest calls take
 no longer on the GPU than their marshalling in Python; include/bsq.h has the
 formulas, limits and errors.
@@ -15,7 +16,13 @@ formulas, limits and errors.
     layer_norm_backward(dy, x, weight, mean, rstd)  -> (dx, dweight, dbias)
     linear_cross_entropy(h, w, targets)           -> (loss, lse)
     linear_cross_entropy_backward(h, w, targets, lse, dloss) -> (dh, dw)
+    linear(x, w, bias, residual, activation)      -> y
+    linear_backward(dy, x, w, z, activation)      -> (dx, dw, dbias)
+    gated_linear(x, w_gate, w_up, activation)     -> h
+    gated_linear_backward(dh, x, w_gate, w_up, gate, up, activation) -> (dx, dw_gate, dw_up)
+    gemm_linear(A, B, ...), gemm_gated(A, B_gate, B_up, ...): the two forward calls on QTensors
     grad_norm(grads), clip_grad_norm(grads, max_norm) -> norm
+    adamw_step(AdamWList(params, grads), lr, step, ...)
 
 Matrices are CUDA tensors [rows, cols] with unit stride along cols and any
 row stride; each *_into form writes given tensors and allocates nothing but a
@@ -47,9 +54,25 @@ class BsqGradC(ctypes.Structure):
                 ("type", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class BsqAdamwTensorC(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p), ("copy", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("param_type", ctypes.c_int32), ("grad_type", ctypes.c_int32),
+                ("state", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class BsqAdamwOptionsC(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64), ("step_device", ctypes.c_void_p),
+                ("lr_device", ctypes.c_void_p), ("norm", ctypes.c_void_p), ("max_norm", ctypes.c_double),
+                ("clip_eps", ctypes.c_double), ("seed", ctypes.c_uint64), ("stochastic", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 def _signatures():
     i32, i64, vp, sz, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float
     PP, PG = ctypes.POINTER(BsqMoePlanC), ctypes.POINTER(BsqGradC)
+    PA, PO = ctypes.POINTER(BsqAdamwTensorC), ctypes.POINTER(BsqAdamwOptionsC)
     return {
         "bsq_moe_workspace_bytes": (sz, [i64, i32, i32]),
         "bsq_moe_sort": (i32, [vp, i32, PP, vp, sz, vp]),
@@ -65,6 +88,22 @@ def _signatures():
         "bsq_linear_cross_entropy": (i32, [vp, i64, vp, i64, vp, i64, i64, i64, vp, vp, vp, sz, vp]),
         "bsq_linear_cross_entropy_backward": (i32, [vp, i64, vp, i64, vp, i64, i64, i64, vp, vp, vp, i64, vp, i64, vp,
                                                     sz, vp]),
+        "bsq_linear_workspace_bytes": (sz, [i64, i64, i64]),
+        "bsq_linear": (i32, [vp, i64, vp, i64, i64, i64, i64, vp, i32, i32, vp, i64, vp, i64, i32, vp, i64, vp, sz, vp]),
+        "bsq_linear_backward_workspace_bytes": (sz, [i64, i64, i64]),
+        "bsq_linear_backward": (i32, [vp, i64, vp, i64, vp, i64, i64, i64, i64, i32, vp, i64, vp, i64, vp, i64, vp, vp, sz,
+                                      vp]),
+        "bsq_gated_linear_workspace_bytes": (sz, [i64, i64, i64]),
+        "bsq_gated_linear": (i32, [vp, i64, vp, i64, vp, i64, i64, i64, i64, i32, vp, i64, i32, vp, i64, vp, i64, vp, sz,
+                                   vp]),
+        "bsq_gated_linear_backward_workspace_bytes": (sz, [i64, i64, i64]),
+        "bsq_gated_linear_backward": (i32, [vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64, i32, vp, i64, vp, i64, vp,
+                                            i64, vp, i64, vp, i64, vp, sz, vp]),
+        "bsq_gemm_linear_workspace_bytes": (sz, [i32, i64, i64, i64]),
+        "bsq_gemm_linear": (i32, [vp, vp, vp, i32, i32, vp, i64, vp, i64, i32, vp, i64, vp, sz, vp]),
+        "bsq_gemm_gated_workspace_bytes": (sz, [i32, i64, i64, i64]),
+        "bsq_gemm_gated": (i32, [vp, vp, vp, i32, vp, i64, i32, vp, i64, vp, i64, vp, sz, vp]),
+        "bsq_adamw": (i32, [PA, i32, PO, vp]),
         "bsq_grad_workspace_bytes": (sz, [i32]),
         "bsq_grad_norm": (i32, [PG, i32, vp, vp, sz, vp]),
         "bsq_clip_grad_norm": (i32, [PG, i32, f32, f32, vp, vp, sz, vp]),
@@ -89,7 +128,8 @@ def _native():
         loader = importlib.machinery.ExtensionFileLoader("_binding", BINDING_PATH)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_binding", loader))
         loader.exec_module(module)
-        module.bind({name: ctypes.cast(getattr(library, name), ctypes.c_void_p).value for name in _signatures()},
+        names = [*_signatures(), "bsq_codes_bytes", "bsq_scales_bytes"]
+        module.bind({name: ctypes.cast(getattr(library, name), ctypes.c_void_p).value for name in names},
                     BsqError, {name: _documentation(f) for name, f in _BOUND.items()})
         for name in _BOUND:
             native = getattr(module, name)
@@ -287,6 +327,86 @@ def linear_cross_entropy_backward(h, w, targets, lse, dloss, stream=None):
     return linear_cross_entropy_backward_into(h, w, targets, lse, dloss, dh, dw, stream)
 
 
+# ------------------------------------- linear layers and the gated feed-forward
+ACTIVATIONS = ("identity", "relu", "silu", "gelu", "gelu_tanh")
+
+
+@_bound
+def linear_into(x, w, y, bias=None, residual=None, activation="identity", z=None, stream=None):
+    """y = act(z) + residual with z = x @ w.T + bias; bias, residual and z (the
+    pre-activation, for the backward pass) may each be None, and residual may be
+    y; returns (y, z)."""
+
+
+def linear(x, w, bias=None, residual=None, activation="identity", out_dtype=None, stream=None):
+    """act(x @ w.T + bias) + residual, of type `out_dtype` (x's)."""
+    y = _new((x.shape[0], w.shape[0]), out_dtype or x.dtype, stream, x)
+    return linear_into(x, w, y, bias, residual, activation, None, stream)[0]
+
+
+@_bound
+def linear_backward_into(dy, x, w, dx=None, dw=None, dbias=None, z=None, activation="identity", stream=None):
+    """Gradient of linear_into; dx, dw and dbias may each be None (x and w where dw and dx are),
+    z where the activation is the identity; returns (dx, dw, dbias)."""
+
+
+def linear_backward(dy, x, w, z=None, activation="identity", bias=True, stream=None):
+    """Gradient of linear: returns (dx, dw, dbias), dbias float32 (None without `bias`)."""
+    import torch
+    dx, dw = _new(tuple(x.shape), x.dtype, stream, x), _new(tuple(w.shape), w.dtype, stream, w)
+    dbias = _new(w.shape[0], torch.float32, stream, w) if bias else None
+    return linear_backward_into(dy, x, w, dx, dw, dbias, z, activation, stream)
+
+
+@_bound
+def gated_linear_into(x, w_gate, w_up, h, activation="silu", gate=None, up=None, stream=None):
+    """h = act(x @ w_gate.T) * (x @ w_up.T); gate and up, the two factors before the activation, are for
+    the backward pass and may both be None; returns (h, gate, up)."""
+
+
+def gated_linear(x, w_gate, w_up, activation="silu", out_dtype=None, stream=None):
+    """act(x @ w_gate.T) * (x @ w_up.T), of type `out_dtype` (x's)."""
+    h = _new((x.shape[0], w_gate.shape[0]), out_dtype or x.dtype, stream, x)
+    return gated_linear_into(x, w_gate, w_up, h, activation, None, None, stream)[0]
+
+
+@_bound
+def gated_linear_backward_into(dh, x, w_gate, w_up, gate, up, dx=None, dw_gate=None, dw_up=None, activation="silu",
+                               stream=None):
+    """Gradient of gated_linear_into; dx may be None (then the weights may be), and dw_gate and dw_up
+    together (then x may be); returns (dx, dw_gate, dw_up)."""
+
+
+def gated_linear_backward(dh, x, w_gate, w_up, gate, up, activation="silu", stream=None):
+    """Gradient of gated_linear: returns (dx, dw_gate, dw_up)."""
+    dx, dg, du = (_new(tuple(t.shape), t.dtype, stream, t) for t in (x, w_gate, w_up))
+    return gated_linear_backward_into(dh, x, w_gate, w_up, gate, up, dx, dg, du, activation, stream)
+
+
+@_bound
+def gemm_linear_into(A, B, y, bias=None, residual=None, activation="identity", z=None, stream=None):
+    """linear_into on the QTensors A and B; returns (y, z)."""
+
+
+def gemm_linear(A, B, bias=None, residual=None, activation="identity", out_dtype=None, stream=None):
+    """act(A @ B.T + bias) + residual of QTensors, bfloat16 or `out_dtype`."""
+    import torch
+    y = _new((A.rows, B.rows), out_dtype or torch.bfloat16, stream, A.codes)
+    return gemm_linear_into(A, B, y, bias, residual, activation, None, stream)[0]
+
+
+@_bound
+def gemm_gated_into(A, B_gate, B_up, h, activation="silu", gate=None, up=None, stream=None):
+    """gated_linear_into on the QTensors A, B_gate and B_up; returns (h, gate, up)."""
+
+
+def gemm_gated(A, B_gate, B_up, activation="silu", out_dtype=None, stream=None):
+    """act(A @ B_gate.T) * (A @ B_up.T) of QTensors, bfloat16 or `out_dtype`."""
+    import torch
+    h = _new((A.rows, B_gate.rows), out_dtype or torch.bfloat16, stream, A.codes)
+    return gemm_gated_into(A, B_gate, B_up, h, activation, None, None, stream)[0]
+
+
 # ------------------------------------------------------ global norm and clipping
 class GradList:
     """The gradients of a step and where their clipped copies go (`outs`; in
@@ -362,3 +482,75 @@ def clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, stream=None):
     _needs_bound(max_norm)
     g = _grad_list(grads)
     return clip_grad_norm_into(g, max_norm, _new(1, torch.float32, stream, g.grads[0]), eps, stream)
+
+
+# -------------------------------------------------------------------- AdamW
+MOMENTS_F32, MOMENTS_8BIT = 0, 1
+
+
+def adamw_states(params, bits: int = 32):
+    """Moments to start with, zeros: for each parameter (m, v) float32, or with
+    bits = 8 (m, m_scales, v, v_scales) uint8, E4M3 codes and an E8M0 byte for 32."""
+    import torch
+    if bits not in (8, 32):
+        _refuse(f"moments of {bits} bits (8 and 32 are supported)")
+
+    def zeros(n, dtype, p):
+        return torch.zeros(n, dtype=dtype, device=p.device)
+
+    if bits == 32:
+        return [(zeros(p.numel(), torch.float32, p), zeros(p.numel(), torch.float32, p)) for p in params]
+    return [tuple(zeros(n, torch.uint8, p) for n in (p.numel(), -(-p.numel() // 32)) * 2) for p in params]
+
+
+class AdamWList:
+    """The parameters of a step, their gradients and moments: contiguous tensors
+    of one GPU.  params, grads: bfloat16 or float32 each; states: 32 or 8 (bits of
+    moments that start at 0), or what adamw_states returns; copies: None, or for
+    each parameter a bfloat16 tensor for its rounded copy (or None).  Built once
+    for buffers that stay; keeps them alive."""
+
+    def __init__(self, params, grads, states=32, copies=None):
+        import torch
+        params, grads = list(params), list(grads)
+        states = adamw_states(params, states) if isinstance(states, int) else [tuple(s) for s in states]
+        copies = [None] * len(params) if copies is None else list(copies)
+        if not params or not len(params) == len(grads) == len(states) == len(copies):
+            _refuse("an AdamW list needs at least one parameter, and a gradient and moments for each")
+        where = params[0].device
+        arr = (BsqAdamwTensorC * len(params))()
+        for i, (p, g, state, c) in enumerate(zip(params, grads, states, copies)):
+            n, blocks = p.numel(), -(-p.numel() // 32)
+            if len(state) not in (2, 4):
+                _refuse(f"moments {i} must be (m, v) or (m, m_scales, v, v_scales)")
+            for t in (p, g, *state, *(() if c is None else (c,))):
+                if t.device != where:
+                    _refuse(f"a tensor of parameter {i} is on {t.device}, parameter 0 on {where}")
+            a = arr[i]
+            a.param_type, a.grad_type = _type(p, f"parameter {i}"), _type(g, f"gradient {i}")
+            a.param, a.grad = _elements(p, f"parameter {i}", n, p.dtype), _elements(g, f"gradient {i}", n, g.dtype)
+            if len(state) == 2:
+                a.state = MOMENTS_F32
+                a.m, a.v = (_elements(t, f"moments {i}", n, torch.float32) for t in state)
+            else:
+                a.state = MOMENTS_8BIT
+                a.m, a.m_scales, a.v, a.v_scales = (
+                    _elements(t, f"moments {i}", k, torch.uint8) for t, k in zip(state, (n, blocks, n, blocks)))
+            a.copy = None if c is None else _elements(c, f"copy {i}", n, torch.bfloat16)
+            a.n = n
+        self.params, self.grads, self.states, self.copies, self.array = params, grads, states, copies, arr
+        self.address, self.count = ctypes.addressof(arr), len(params)
+
+
+def adamw_step(tensors: AdamWList, lr, step, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01, norm=None,
+               max_norm=None, clip_eps: float = 1e-6, seed=None, stream=None):
+    """One AdamW step of an AdamWList, in place.  step: its number, from 1 on; lr
+    and step may be float32 and int64 tensors [1] on the device, which a captured
+    step reads at each replay.  norm (of grad_norm) and max_norm clip the gradients in
+    the same pass, as clip_grad_norm would, without writing them.  seed: codes of
+    8-bit moments and bfloat16 parameters are rounded stochastically (None: to
+    nearest); it may stay the same from step to step."""
+    if (norm is None) != (max_norm is None):
+        _refuse("norm and max_norm go together")
+    _native().adamw_into(tensors.address, tensors.count, tensors.params[0], lr, step, betas[0], betas[1], eps, weight_decay,
+                         norm, max_norm, clip_eps, seed, stream)

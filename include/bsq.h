@@ -24,6 +24,10 @@
  *  - What a mixture-of-experts step runs next to it: tokens sorted by expert
  *    and back, layer norm, the softmax cross entropy of a linear head and
  *    the global gradient norm with clipping, each with its gradient.
+ *  - The dense feed-forward block and its update: linear layers with bias,
+ *    activation and residual in the product's epilogue, the gated half with
+ *    both projections in one kernel (BF16 with gradients, and on block-scaled
+ *    operands), and AdamW over many tensors with moments in 32 or 8 bits.
  *
  * Conventions shared by every entry point
  *  - Matrices are row-major.  A GEMM computes C[M,N] = A[M,K] * B[N,K]^T:
@@ -400,6 +404,97 @@ bsq_status bsq_linear_cross_entropy_backward(const void* h, int64_t ldh, const v
                                              const float* lse, const float* dloss, void* dh, int64_t ld_dh, void* dw,
                                              int64_t ld_dw, void* workspace, size_t workspace_bytes, void* stream);
 
+/* -- linear layers with their epilogue, and the gated feed-forward -------- */
+
+/* act(z), and act'(z) in the gradients:
+ *   IDENTITY z;  RELU max(z, 0);  SILU z / (1 + exp(-z));
+ *   GELU z (1 + erf(z / sqrt(2))) / 2;
+ *   GELU_TANH z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+typedef enum {
+    BSQ_ACT_IDENTITY = 0,
+    BSQ_ACT_RELU = 1,
+    BSQ_ACT_SILU = 2,
+    BSQ_ACT_GELU = 3,
+    BSQ_ACT_GELU_TANH = 4
+} bsq_activation;
+
+/* Workspaces of the four BF16 calls below (0 on bad sizes too).  `out` is w's
+ * rows, for a gated layer its width. */
+size_t bsq_linear_workspace_bytes(int64_t tokens, int64_t out, int64_t cols);
+size_t bsq_linear_backward_workspace_bytes(int64_t tokens, int64_t out, int64_t cols);
+size_t bsq_gated_linear_workspace_bytes(int64_t tokens, int64_t out, int64_t cols);
+size_t bsq_gated_linear_backward_workspace_bytes(int64_t tokens, int64_t out, int64_t cols);
+
+/* z = x w^T + bias, y = act(z) + residual, in the product's epilogue.
+ * x: BF16 [tokens, cols], w: BF16 [out, cols], both on 16-byte boundaries
+ * with cols, ldx and ldw multiples of 8 (BSQ_ERR_ALIGNMENT otherwise; the
+ * pitch of a single row says nothing); any tokens and out up to 2^31 - 256 and
+ * 2^24.  bias: DEVICE [out] of `bias_type` (bsq_out) or NULL.  residual:
+ * [tokens, out] of y's type or NULL; y may be residual itself (same pointer and
+ * pitch).  y: [tokens, out] of `type` (bsq_out).  z: BF16 [tokens, out] for the
+ * backward pass, or NULL.  FP32 sums on the tensor cores; z, act and the
+ * residual in FP32, each output rounded once. */
+bsq_status bsq_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t tokens, int64_t out, int64_t cols,
+                      const void* bias, int32_t bias_type, int32_t activation, const void* residual,
+                      int64_t ld_residual, void* y, int64_t ldy, int32_t type, void* z, int64_t ldz, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* Gradient of bsq_linear for dy: BF16 [tokens, out] (the residual's gradient is
+ * dy itself), with z as the forward call left it (BF16; not read, and may be
+ * NULL, with BSQ_ACT_IDENTITY):
+ *   dz = dy act'(z), rounded to BF16 for the two products
+ *   dx = dz w      BF16 [tokens, cols]
+ *   dw = dz^T x    BF16 [out, cols]
+ *   dbias = the sum of dz's rows, before that rounding   DEVICE float[out]
+ * Each of dx, dw, dbias may be NULL, but not all; w is read for dx only and x
+ * for dw only (else each may be NULL).  dx, dw on 16-byte boundaries with
+ * pitches that are multiples of 8; dy and z of any address and pitch. */
+bsq_status bsq_linear_backward(const void* dy, int64_t ld_dy, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                               int64_t tokens, int64_t out, int64_t cols, int32_t activation, const void* z, int64_t ldz,
+                               void* dx, int64_t ld_dx, void* dw, int64_t ld_dw, float* dbias, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* The gated half of a feed-forward block, both projections in one kernel:
+ *   gate = x w_gate^T, up = x w_up^T, h = act(gate) * up
+ * x, w_gate, w_up: BF16 as x and w of bsq_linear, w_gate and w_up [out, cols].
+ * h: [tokens, out] of `type` (bsq_out).  gate, up: BF16 [tokens, out] for the
+ * backward pass, both or neither. */
+bsq_status bsq_gated_linear(const void* x, int64_t ldx, const void* w_gate, int64_t ld_gate_w, const void* w_up,
+                            int64_t ld_up_w, int64_t tokens, int64_t out, int64_t cols, int32_t activation, void* h,
+                            int64_t ldh, int32_t type, void* gate, int64_t ld_gate, void* up, int64_t ld_up,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of bsq_gated_linear for dh: BF16 [tokens, out], with gate and up as
+ * the forward call left them:
+ *   dgate = dh up act'(gate), dup = dh act(gate), rounded to BF16 for the products
+ *   dx = dgate w_gate + dup w_up, dw_gate = dgate^T x, dw_up = dup^T x (BF16)
+ * dx may be NULL (then w_gate and w_up may be), and so may dw_gate and dw_up
+ * together (then x may be); alignments as for bsq_linear_backward. */
+bsq_status bsq_gated_linear_backward(const void* dh, int64_t ld_dh, const void* x, int64_t ldx, const void* w_gate,
+                                     int64_t ld_gate_w, const void* w_up, int64_t ld_up_w, int64_t tokens, int64_t out,
+                                     int64_t cols, int32_t activation, const void* gate, int64_t ld_gate, const void* up,
+                                     int64_t ld_up, void* dx, int64_t ld_dx, void* dw_gate, int64_t ld_dw_gate,
+                                     void* dw_up, int64_t ld_dw_up, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
+/* Workspaces of the two calls below for operands of A's format (0 on bad sizes too). */
+size_t bsq_gemm_linear_workspace_bytes(int32_t fmt, int64_t tokens, int64_t out, int64_t cols);
+size_t bsq_gemm_gated_workspace_bytes(int32_t fmt, int64_t tokens, int64_t out, int64_t cols);
+
+/* bsq_gemm with the epilogue of bsq_linear: z = A B^T + bias, y = act(z) +
+ * residual.  Operands, formats and limits as for bsq_gemm; bias, residual, y
+ * and z as for bsq_linear (A.rows tokens, B.rows out). */
+bsq_status bsq_gemm_linear(const bsq_tensor* A, const bsq_tensor* B, const void* bias, int32_t bias_type,
+                           int32_t activation, const void* residual, int64_t ld_residual, void* y, int64_t ldy,
+                           int32_t type, void* z, int64_t ldz, void* workspace, size_t workspace_bytes, void* stream);
+
+/* bsq_gated_linear on block-scaled operands: gate = A B_gate^T, up = A B_up^T,
+ * h = act(gate) * up.  B_gate and B_up have one format and one shape; operands
+ * and limits as for bsq_gemm. */
+bsq_status bsq_gemm_gated(const bsq_tensor* A, const bsq_tensor* B_gate, const bsq_tensor* B_up, int32_t activation,
+                          void* h, int64_t ldh, int32_t type, void* gate, int64_t ld_gate, void* up, int64_t ld_up,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
 /* -- global norm and clipping ------------------------------------------- */
 
 /* One gradient: n contiguous elements (0 is valid) of `type` (bsq_out) at
@@ -429,6 +524,78 @@ bsq_status bsq_grad_norm(const bsq_grad* grads, int32_t count, float* norm, void
  * max_norm >= 0, eps >= 0. */
 bsq_status bsq_clip_grad_norm(const bsq_grad* grads, int32_t count, float max_norm, float eps, float* norm,
                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* -- AdamW ---------------------------------------------------------------- */
+
+typedef enum { BSQ_MOMENTS_F32 = 0, BSQ_MOMENTS_8BIT = 1 } bsq_moments;
+
+/* One parameter tensor of n contiguous elements (0 is valid) and its moments.
+ *   BSQ_MOMENTS_F32   m, v: float[n]; m_scales, v_scales unused
+ *   BSQ_MOMENTS_8BIT  m, v: n E4M3 codes, m_scales, v_scales: ceil(n / 32) E8M0
+ *                     bytes, one for 32 elements; v's codes hold its square root
+ * A tensor of zeros is the start of either (codes and scales).  `copy`: BF16[n],
+ * the new parameters rounded to nearest, or NULL.  No two tensors overlap.
+ * Elements of any address that is a multiple of their size; 16-byte boundaries
+ * (codes: 8) are faster. */
+typedef struct {
+    void* param;
+    const void* grad;
+    void* m;
+    void* v;
+    uint8_t* m_scales;
+    uint8_t* v_scales;
+    void* copy;
+    int64_t n;
+    int32_t param_type;        /* bsq_out */
+    int32_t grad_type;         /* bsq_out */
+    int32_t state;             /* bsq_moments */
+    int32_t reserved;          /* must be 0 */
+} bsq_adamw_tensor;
+
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay;
+    int64_t step;              /* of this update, from 1 on */
+    const int64_t* step_device;/* DEVICE int64[1] instead of `step`, or NULL */
+    const float* lr_device;    /* DEVICE float[1] instead of `lr`, or NULL */
+    const float* norm;         /* DEVICE float[1], or NULL: gradients as they are */
+    double max_norm, clip_eps; /* with norm */
+    uint64_t seed;             /* with stochastic */
+    int32_t stochastic;
+    int32_t reserved;          /* must be 0 */
+} bsq_adamw_options;
+
+/* One AdamW step of every tensor, in FP32, each operation rounded to nearest in
+ * this order:
+ *   g = grad * min(1, max_norm / (norm + clip_eps))      (norm: of bsq_grad_norm)
+ *   m = beta1 m + (1 - beta1) g
+ *   v = beta2 v + ((1 - beta2) g) g
+ *   param = (1 - lr weight_decay) param
+ *           - lr / (1 - beta1^step) * (m / (sqrt(v) / sqrt(1 - beta2^step) + eps))
+ * where the factors of lr, the betas and the step are computed in FP64 and
+ * rounded (with step_device or lr_device in FP32 on the device, so that a
+ * captured call takes the step's number and learning rate of each replay).
+ *
+ * Moments in 8 bits: with x a block's largest magnitude, its scale is 2^e with e =
+ * floor(log2(x * 8/7)) - 8 (the product in FP32; e >= -127), which keeps |x| 2^-e at
+ * 448 or below; a code is x 2^-e rounded to E4M3; a v that is not 0 keeps a code that
+ * is not; a block with a NaN or an infinity gets scale 0xFF and NaN codes.  The update
+ * takes the moments before that rounding.
+ *
+ * stochastic = 0: codes and BF16 parameters are rounded to nearest.  Else they
+ * are rounded up in magnitude with the probability of what is cut off, from 16
+ * random bits each.  With mix(x) = lowbias32 (xor x >> 16, times 0x7FEB352D, xor
+ * x >> 15, times 0x846CA68B, xor x >> 16; 32 bits), element j of tensor i has
+ *   key  = mix(mix(mix(i ^ low(seed)) ^ high(seed)) ^ low(step))
+ *          + high(j) * 0x9E3779B9
+ *   bits = mix(low(j) ^ key)
+ * (low and high: 32 bits); its lower half rounds m's code, its upper half v's,
+ * and bits 16 .. 31 of bits * 0x9E3779B1 the parameter.  A seed may stay the same
+ * from step to step.
+ *
+ * `tensors` is a HOST array, read before the call returns, and so are the
+ * options; count <= 2^20, at most 2^40 elements.  lr, eps, weight_decay,
+ * max_norm, clip_eps >= 0 and finite (max_norm may be infinite), 0 <= beta < 1, step >= 1. */
+bsq_status bsq_adamw(const bsq_adamw_tensor* tensors, int32_t count, const bsq_adamw_options* options, void* stream);
 
 /* Take and clear the device status word (one atomic exchange on the
  * device, ordered after the work already on `stream`), synchronize
