@@ -18,7 +18,7 @@
 // cut off, and move as they should on average.
 //
 // The list travels in the kernel's parameters; tensors are cut into chunks of
-// 2048 elements, 8 neighbours a thread: a block of 32 is four lanes.
+// 1024 elements, 8 neighbours a thread: a block of 32 is four lanes.
 #include <algorithm>
 #include <cmath>
 #include "../../include/bsq.h"
@@ -29,8 +29,9 @@
 namespace bsq {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kPer = 8;                             // elements of a thread
+constexpr int kCtas = 32;                           // at most, of an SM
 constexpr int64_t kChunk = (int64_t)kThreads * kPer;
 
 struct Entry {
@@ -40,8 +41,8 @@ struct Entry {
     uint8_t *m_scales, *v_scales;
     __nv_bfloat16* copy;
     int64_t n;
-    int32_t index;                 // in the caller's list
-    int8_t p_bf16, g_bf16, bits8, vec;
+    uint32_t key;                  // of its random bits, before the step's number
+    int8_t p_bf16, g_bf16, vec;
 };
 template <int CAP>
 struct Table {
@@ -49,7 +50,7 @@ struct Table {
     int32_t first[CAP + 1];        // chunks before each tensor
     int32_t count;
 };
-constexpr int kSmall = 16, kLarge = 384;
+constexpr int kSmall = 16, kMiddle = 96, kLarge = 384;   // the smallest that holds the list travels
 struct Options {
     float beta1, beta2, c1, c2;    // c: 1 - beta
     float decay, size, root, eps;
@@ -65,31 +66,58 @@ static_assert(sizeof(Table<kLarge>) + sizeof(Options) <= 32764, "kernel paramete
 
 // A permutation of the 32-bit integers that leaves no visible order (multiply and
 // xor-shift; the constants are those of C. Wellons' lowbias32)
-__device__ __forceinline__ uint32_t mix(uint32_t x) {
+__host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
     x ^= x >> 16;
     x *= 0x7FEB352Du;
     x ^= x >> 15;
     x *= 0x846CA68Bu;
     return x ^ (x >> 16);
 }
+// mix((at + i) ^ key) for the 8 elements from `at` on, a multiple of 8: i stays in the lowest bits
+__device__ __forceinline__ void random_bits(uint32_t at, uint32_t key, uint32_t (&bits)[kPer]) {
+    uint32_t x = at ^ key;
+    x ^= x >> 16;
+#pragma unroll
+    for (int i = 0; i < kPer; i++) {
+        uint32_t b = (x ^ (uint32_t)i) * 0x7FEB352Du;
+        b = (b ^ (b >> 15)) * 0x846CA68Bu;
+        bits[i] = b ^ (b >> 16);
+    }
+}
+// the largest and smallest of 8 (their magnitudes where ABS), NaN if one is
+template <bool ABS>
+__device__ __forceinline__ float largest(const float (&x)[kPer]) {
+    const auto most = [](float a, float b, float c) {
+        float m;
+        if (ABS) asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+        else asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+        return m;
+    };
+    return most(most(x[0], x[1], x[2]), most(x[3], x[4], x[5]), most(x[6], x[7], x[7]));
+}
+template <bool ABS>
+__device__ __forceinline__ float smallest(const float (&x)[kPer]) {
+    const auto least = [](float a, float b, float c) {
+        float m;
+        if (ABS) asm("min.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+        else asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+        return m;
+    };
+    return least(least(x[0], x[1], x[2]), least(x[3], x[4], x[5]), least(x[6], x[7], x[7]));
+}
 // 2^(byte - 127)
 __device__ __forceinline__ float power(uint32_t byte) { return __uint_as_float(byte == 0 ? 1u << 22 : byte << 23); }
 
-// 8 magnitudes, already scaled to at most 448 (a little more is cut), to the E4M3 grid: 16 random bits each.
-// Below 2^-6 the grid's steps are 2^-9: with 2^-6 added they are those of the next binade.
-__device__ __forceinline__ float stochastic_e4m3(float y, uint32_t bits16) {
-    const float low = y < 0.015625f ? 0.015625f : 0.0f;
-    const uint32_t w = __float_as_uint(__fadd_rn(y, low)) + (bits16 << 4);
-    return __fsub_rn(__uint_as_float(w & ~0xFFFFFu), low);
-}
-
-// The 8 moments x of a thread (their block: four neighbouring lanes) as codes and a scale byte
+// The 8 moments x of a thread (their block: four neighbouring lanes) as codes and a scale byte.
+//
+// Stochastically a value, already scaled, goes to the E4M3 grid by 16 random bits added below the three bits of
+// mantissa that stay, sign and magnitude apart by themselves.  Below 2^-6 the grid's steps are 2^-9: with 2^-6 added
+// they are those of the next binade.  A thread with such a value (one in some 10000 moments) takes the longer way,
+// on which a second moment that is not 0 is kept from becoming so.
 template <bool RANDOM, bool ROOT>
 __device__ __forceinline__ uint2 encode(const float (&x)[kPer], const uint32_t (&bits)[kPer], uint32_t& byte) {
-    // bits of the largest magnitude: NaN and infinity above all others
-    uint32_t most = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; i++) most = max(most, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+    // bits of the largest magnitude: those of NaN and infinity are above all others
+    uint32_t most = __float_as_uint(largest<!ROOT>(x));
 #pragma unroll
     for (int d = 1; d < 4; d <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
     if (most >= 0x7F800000u) {
@@ -98,20 +126,46 @@ __device__ __forceinline__ uint2 encode(const float (&x)[kPer], const uint32_t (
     }
     const int e = (int)(__float_as_uint(__fmul_rn(__uint_as_float(most), 8.0f / 7.0f)) >> 23) - 8;
     byte = (uint32_t)max(e, 0);
-    const float up = power(254 - byte);
+    const F2 up(power(254 - byte));
     float y[kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; i++) {
-        const float a = __fmul_rn(fabsf(x[i]), up);
-        const float s = fminf(RANDOM ? stochastic_e4m3(a, ROOT ? bits[i] >> 16 : bits[i] & 0xFFFFu) : a, 448.0f);
-        // a second moment that is not 0 stays so (2^-9 is the smallest code)
-        if (ROOT) y[i] = x[i] != 0.0f ? fmaxf(s, 0.001953125f) : 0.0f;
-        else y[i] = x[i] < 0.0f ? -s : s;
+    for (int i = 0; i < kPer; i += 2) {
+        const float2 a = (F2(x[i], x[i + 1]) * up).get();
+        y[i] = a.x;
+        y[i + 1] = a.y;
     }
-    return pack8_fp8<kE4M3>(y);
+    // (16 random bits four places up, the high ones by the high word of a product)
+    const auto cut = [&](float a, int i) {
+        uint32_t c = __float_as_uint(a);
+        if (ROOT) asm("mad.hi.u32 %0, %1, %2, %0;" : "+r"(c) : "r"(bits[i] & 0xFFFF0000u), "r"(1u << 20));
+        else c += (bits[i] & 0xFFFFu) * 16u;
+        return __uint_as_float(c & 0xFFF00000u);
+    };
+    if (smallest<!ROOT>(y) >= 0.015625f) {
+        if (RANDOM)
+#pragma unroll
+            for (int i = 0; i < kPer; i++) y[i] = cut(y[i], i);
+        return pack8_fp8<kE4M3>(y);
+    }
+    uint2 c;
+    if (RANDOM) {
+#pragma unroll
+        for (int i = 0; i < kPer; i++) {
+            const float a = fabsf(y[i]), low = a < 0.015625f ? 0.015625f : 0.0f;
+            y[i] = copysignf(__fsub_rn(cut(__fadd_rn(a, low), i), low), x[i]);
+        }
+    }
+    c = pack8_fp8<kE4M3>(y);
+    if (ROOT)
+#pragma unroll
+        for (int i = 0; i < kPer; i++) {
+            uint32_t& w = i < 4 ? c.x : c.y;
+            if (x[i] != 0.0f && (w >> (8 * (i & 3)) & 0xFF) == 0) w |= 1u << (8 * (i & 3));
+        }
+    return c;
 }
-__device__ __forceinline__ void decode(uint2 codes, uint32_t byte, float (&x)[kPer]) {
-    const float s = power(byte);
+__device__ __forceinline__ void decode(uint2 codes, uint32_t byte, F2 (&x)[kPer / 2]) {
+    const F2 s(power(byte));
     const uint32_t w[2] = {codes.x, codes.y};
 #pragma unroll
     for (int i = 0; i < 4; i++) {
@@ -119,35 +173,11 @@ __device__ __forceinline__ void decode(uint2 codes, uint32_t byte, float (&x)[kP
         const uint16_t in = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
         asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(in));
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-        x[2 * i] = __fmul_rn(f.x, s);
-        x[2 * i + 1] = __fmul_rn(f.y, s);
+        x[i] = F2(f.x, f.y) * s;
     }
 }
 
 // 8 elements at p[at ..), the first n of them; 16-byte (codes: 8-byte) accesses where `vec`
-__device__ __forceinline__ void get(const void* p, int64_t at, int bf16, bool vec, int n, float (&x)[kPer]) {
-    if (bf16) {
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p) + at;
-        if (vec) {
-            Pack<__nv_bfloat16, 8> k;
-            k.load(q);
-            k.unpack(x);
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < kPer; i++) x[i] = i < n ? __bfloat162float(q[i]) : 0.0f;
-        return;
-    }
-    const float* q = static_cast<const float*>(p) + at;
-    if (vec) {
-        const float4 a = reinterpret_cast<const float4*>(q)[0], b = reinterpret_cast<const float4*>(q)[1];
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; i++) x[i] = i < n ? q[i] : 0.0f;
-}
 __device__ __forceinline__ void put(void* p, int64_t at, int bf16, bool vec, int n, const float (&x)[kPer]) {
     if (bf16) {
         __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p) + at;
@@ -213,7 +243,187 @@ __device__ __forceinline__ void step_scalars(Options& o) {
     o.step = step;
 }
 
-template <int CAP, bool RANDOM>
+// The moments and parameters of 8 elements; r: the root of v.
+//
+// The root and the quotient are correctly rounded by Newton steps with a fused
+// multiply-add (P. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990): from y = 1 / sqrt(v) to some 23 bits, g = v y and h = y
+// / 2 are brought to full precision by one step, and the exact remainder v - g^2 rounds
+// g; for m / d the remainder m - d q does.  In packed instructions that is 4.5 and 3.5
+// of them an element, a third of the library's IEEE functions, which all of the 8-bit
+// step's time went to.  The remainders are exact while nothing underflows: v from 2^-90 to 2^90;
+// elsewhere (a v of 0 among them) the library's functions.  A quotient whose m is below
+// 2^-90 may be off in its last bit.
+//
+// A packed product and the addition behind it came out as one fused instruction, in
+// spite of their .rn, so a product that is added is two single ones.
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    const float2 x = a.get(), y = b.get();
+    return F2(__fmul_rn(x.x, y.x), __fmul_rn(x.y, y.y));
+}
+__device__ __forceinline__ void update(float (&p)[kPer], const float (&g)[kPer], float (&m)[kPer], float (&v)[kPer],
+                                       float (&r)[kPer], const Options& o, float factor) {
+    const F2 b1(o.beta1), b2(o.beta2), c1(o.c1), c2(o.c2), f(factor);
+#pragma unroll
+    for (int i = 0; i < kPer; i += 2) {
+        const F2 x = F2(g[i], g[i + 1]) * f;                // (times 1 without clipping)
+        const float2 ms = (mul2(b1, F2(m[i], m[i + 1])) + mul2(c1, x)).get();
+        const float2 vs = (mul2(b2, F2(v[i], v[i + 1])) + mul2(c2 * x, x)).get();
+        m[i] = ms.x; m[i + 1] = ms.y;
+        v[i] = vs.x; v[i + 1] = vs.y;
+    }
+    if (smallest<false>(v) >= 0x1p-90f && largest<false>(v) <= 0x1p90f) {
+        const F2 minus(-1.0f);
+#pragma unroll
+        for (int i = 0; i < kPer; i += 2) {
+            const F2 vv(v[i], v[i + 1]);
+            float y0, y1;
+            asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y0) : "f"(v[i]));
+            asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y1) : "f"(v[i + 1]));
+            const F2 y(y0, y1);
+            F2 q = vv * y, h = y * F2(-0.5f);              // h: -1 / (2 sqrt(v))
+            const F2 e = fma2(q, h, F2(0.5f));
+            q = fma2(q, e, q);
+            h = fma2(h, e, h);
+            q = fma2(fma2(q, q, vv * minus), h, q);
+            const float2 root = q.get();
+            r[i] = root.x; r[i + 1] = root.y;
+            const F2 d = mul2(q, F2(o.root)) + F2(o.eps), nd = d * minus, mm(m[i], m[i + 1]);
+            const float2 ds = d.get();
+            float i0, i1;
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(i0) : "f"(ds.x));
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(i1) : "f"(ds.y));
+            F2 k(i0, i1);
+            k = fma2(k, fma2(nd, k, F2(1.0f)), k);
+            F2 t = mm * k;
+            t = fma2(fma2(nd, t, mm), k, t);
+            const float2 n = (mul2(F2(o.decay), F2(p[i], p[i + 1])) + mul2(F2(-o.size), t)).get();
+            p[i] = n.x; p[i + 1] = n.y;
+        }
+        return;
+    }
+#pragma unroll 1
+    for (int k = 0; k < kPer; k++) {
+        // one at a time, and the arrays move on: this is rare, and long
+        r[0] = __fsqrt_rn(v[0]);
+        const float d = __fadd_rn(__fmul_rn(r[0], o.root), o.eps);
+        p[0] = __fsub_rn(__fmul_rn(o.decay, p[0]), __fmul_rn(o.size, __fdiv_rn(m[0], d)));
+        const float r0 = r[0], v0 = v[0], p0 = p[0], m0 = m[0];
+#pragma unroll
+        for (int i = 0; i + 1 < kPer; i++) {
+            r[i] = r[i + 1];
+            v[i] = v[i + 1];
+            p[i] = p[i + 1];
+            m[i] = m[i + 1];
+        }
+        r[kPer - 1] = r0;
+        v[kPer - 1] = v0;
+        p[kPer - 1] = p0;
+        m[kPer - 1] = m0;
+    }
+}
+
+// Chunk c of the list: its tensor, and where this thread's elements start
+template <int CAP>
+struct Place {
+    const Entry* e;
+    int64_t at;
+    int n;                         // of the 8 elements
+    bool vec;
+    __device__ __forceinline__ Place(const Table<CAP>& t, int c) {
+        int lo = 0, hi = t.count - 1;               // the last tensor whose first chunk is <= c
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (t.first[mid] <= c) lo = mid; else hi = mid - 1;
+        }
+        e = &t.e[lo];
+        at = (int64_t)(c - t.first[lo]) * kChunk + threadIdx.x * kPer;
+        n = (int)max((int64_t)0, min((int64_t)kPer, e->n - at));
+        vec = e->vec && n == kPer;
+    }
+};
+// What a chunk reads, as it lies in memory (the elements of a tensor whose rows do not suit vectors put together)
+struct Words {
+    uint4 v[2];
+    __device__ __forceinline__ void load(const void* p, int64_t at, int bf16, bool vec, int n) {
+        v[0] = v[1] = make_uint4(0, 0, 0, 0);
+        if (bf16) {
+            const uint16_t* q = static_cast<const uint16_t*>(p) + at;
+            if (vec) {
+                v[0] = *reinterpret_cast<const uint4*>(q);
+                return;
+            }
+            uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < kPer; i++)
+                if (i < n) w[i >> 1] |= (uint32_t)q[i] << (16 * (i & 1));
+            v[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            return;
+        }
+        const uint32_t* q = static_cast<const uint32_t*>(p) + at;
+        if (vec) {
+            v[0] = reinterpret_cast<const uint4*>(q)[0];
+            v[1] = reinterpret_cast<const uint4*>(q)[1];
+            return;
+        }
+        uint32_t w[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; i++) w[i] = i < n ? q[i] : 0u;
+        v[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        v[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+    __device__ __forceinline__ void get(int bf16, float (&x)[kPer]) const {
+        if (bf16) {
+            Pack<__nv_bfloat16, 8> k;
+            k.v = v[0];
+            k.unpack(x);
+            return;
+        }
+        const uint32_t w[kPer] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+#pragma unroll
+        for (int i = 0; i < kPer; i++) x[i] = __uint_as_float(w[i]);
+    }
+};
+template <bool BITS8>
+struct Moments;
+template <>
+struct Moments<false> {
+    Words m, v;
+    __device__ __forceinline__ void load(const Entry& e, int64_t at, bool vec, int n) {
+        m.load(e.m, at, 0, vec, n);
+        v.load(e.v, at, 0, vec, n);
+    }
+    __device__ __forceinline__ void get(float (&a)[kPer], float (&b)[kPer]) const {
+        m.get(0, a);
+        v.get(0, b);
+    }
+};
+template <>
+struct Moments<true> {
+    uint2 m, v;
+    uint32_t mb, vb;
+    __device__ __forceinline__ void load(const Entry& e, int64_t at, bool vec, int n) {
+        m = get_codes(e.m, at, vec, n);
+        v = get_codes(e.v, at, vec, n);
+        mb = n > 0 ? e.m_scales[at >> 5] : 0;
+        vb = n > 0 ? e.v_scales[at >> 5] : 0;
+    }
+    __device__ __forceinline__ void get(float (&a)[kPer], float (&b)[kPer]) const {
+        F2 x[kPer / 2], y[kPer / 2];
+        decode(m, mb, x);
+        decode(v, vb, y);
+#pragma unroll
+        for (int i = 0; i < kPer / 2; i++) {
+            const float2 f = x[i].get(), r = (y[i] * y[i]).get();
+            a[2 * i] = f.x;
+            a[2 * i + 1] = f.y;
+            b[2 * i] = r.x;
+            b[2 * i + 1] = r.y;
+        }
+    }
+};
+
+template <int CAP, bool RANDOM, bool BITS8>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table<CAP> t, Options o) {
     if (o.step_at || o.lr_at) step_scalars(o);
     float factor = 1.0f;
@@ -221,86 +431,82 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         const float f = __fdiv_rn(o.max_norm, __fadd_rn(*o.norm, o.clip_eps));
         factor = f > 1.0f ? 1.0f : f;               // NaN stays NaN
     }
-    for (int c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
-        int lo = 0, hi = t.count - 1;               // the last tensor whose first chunk is <= c
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (t.first[mid] <= c) lo = mid; else hi = mid - 1;
-        }
-        const Entry& e = t.e[lo];
-        const int64_t at = (int64_t)(c - t.first[lo]) * kChunk + threadIdx.x * kPer;
-        const int n = (int)max((int64_t)0, min((int64_t)kPer, e.n - at));
-        const bool vec = e.vec && n == kPer;
-        float p[kPer], g[kPer], m[kPer] = {}, v[kPer] = {};
-        uint2 mc = make_uint2(0, 0), vc = mc;
-        uint32_t mb = 0, vb = 0;
-        get(e.p, at, e.p_bf16, vec, n, p);
-        get(e.g, at, e.g_bf16, vec, n, g);
-        if (e.bits8) {
-            mc = get_codes(e.m, at, vec, n);
-            vc = get_codes(e.v, at, vec, n);
-            if (n > 0) {
-                mb = e.m_scales[at >> 5];
-                vb = e.v_scales[at >> 5];
-            }
-            decode(mc, mb, m);
-            decode(vc, vb, v);
-#pragma unroll
-            for (int i = 0; i < kPer; i++) v[i] = __fmul_rn(v[i], v[i]);
-        } else {
-            get(e.m, at, 0, vec, n, m);
-            get(e.v, at, 0, vec, n, v);
+    const int chunks = t.first[t.count];
+    // a chunk's loads run while the one before it is computed
+    struct Chunk {
+        Words p, g;
+        Moments<BITS8> s;
+    };
+    const auto load = [&](const Place<CAP>& a, Chunk& c) {
+        c.p.load(a.e->p, a.at, a.e->p_bf16, a.vec, a.n);
+        c.g.load(a.e->g, a.at, a.e->g_bf16, a.vec, a.n);
+        c.s.load(*a.e, a.at, a.vec, a.n);
+    };
+    int next = blockIdx.x;
+    Place<CAP> ahead(t, next);
+    Chunk words;
+    load(ahead, words);
+    while (next < chunks) {
+        const Place<CAP> at = ahead;
+        const Entry& e = *at.e;
+        float p[kPer], g[kPer], m[kPer], v[kPer], r[kPer];
+        words.p.get(e.p_bf16, p);
+        words.g.get(e.g_bf16, g);
+        words.s.get(m, v);
+        next += gridDim.x;
+        if (next < chunks) {
+            ahead = Place<CAP>(t, next);
+            load(ahead, words);
         }
         uint32_t bits[kPer] = {};
         if (RANDOM) {
-            uint32_t key = mix((uint32_t)e.index ^ o.seed_lo);
-            key = mix(key ^ o.seed_hi);
-            key = mix(key ^ (uint32_t)o.step) + (uint32_t)(at >> 32) * 0x9E3779B9u;
-#pragma unroll
-            for (int i = 0; i < kPer; i++) bits[i] = mix((uint32_t)(at + i) ^ key);
+            const uint32_t key = mix(e.key ^ (uint32_t)o.step) + (uint32_t)(at.at >> 32) * 0x9E3779B9u;
+            random_bits((uint32_t)at.at, key, bits);
         }
-        float r[kPer];
+        update(p, g, m, v, r, o, factor);
+        if (BITS8) {
+            if (at.n < kPer)
+                // elements past the end are 0 and change no scale; every lane takes part in the block's maximum
 #pragma unroll
-        for (int i = 0; i < kPer; i++) {
-            const float x = o.norm ? __fmul_rn(g[i], factor) : g[i];
-            m[i] = __fadd_rn(__fmul_rn(o.beta1, m[i]), __fmul_rn(o.c1, x));
-            v[i] = __fadd_rn(__fmul_rn(o.beta2, v[i]), __fmul_rn(__fmul_rn(o.c2, x), x));
-            r[i] = __fsqrt_rn(v[i]);
-            const float d = __fadd_rn(__fmul_rn(r[i], o.root), o.eps);
-            p[i] = __fsub_rn(__fmul_rn(o.decay, p[i]), __fmul_rn(o.size, __fdiv_rn(m[i], d)));
-        }
-        if (e.bits8) {
-            // elements past the end are 0 and change no scale; every lane takes part in the block's maximum
-#pragma unroll
-            for (int i = 0; i < kPer; i++)
-                if (i >= n) m[i] = r[i] = 0.0f;
-            mc = encode<RANDOM, false>(m, bits, mb);
-            vc = encode<RANDOM, true>(r, bits, vb);
-            put_codes(e.m, at, vec, n, mc);
-            put_codes(e.v, at, vec, n, vc);
-            if (n > 0 && (threadIdx.x & 3) == 0) {
-                e.m_scales[at >> 5] = (uint8_t)mb;
-                e.v_scales[at >> 5] = (uint8_t)vb;
+                for (int i = 0; i < kPer; i++)
+                    if (i >= at.n) m[i] = r[i] = 0.0f;
+            uint32_t mb, vb;
+            const uint2 mc = encode<RANDOM, false>(m, bits, mb), vc = encode<RANDOM, true>(r, bits, vb);
+            put_codes(e.m, at.at, at.vec, at.n, mc);
+            put_codes(e.v, at.at, at.vec, at.n, vc);
+            if (at.n > 0 && (threadIdx.x & 3) == 0) {
+                e.m_scales[at.at >> 5] = (uint8_t)mb;
+                e.v_scales[at.at >> 5] = (uint8_t)vb;
             }
         } else {
-            put(e.m, at, 0, vec, n, m);
-            put(e.v, at, 0, vec, n, v);
+            put(e.m, at.at, 0, at.vec, at.n, m);
+            put(e.v, at.at, 0, at.vec, at.n, v);
         }
-        if (e.copy) put(e.copy, at, 1, vec, n, p);
-        if (RANDOM && e.p_bf16) {
+        if (e.copy) put(e.copy, at.at, 1, at.vec, at.n, p);
+        if (RANDOM && e.p_bf16 && __float_as_uint(largest<true>(p)) < 0x7F800000u) {       // (else to nearest: it stays as it is)
+            uint32_t w[kPer];
 #pragma unroll
             for (int i = 0; i < kPer; i++) {
-                const uint32_t w = __float_as_uint(p[i]);
-                if ((w & 0x7F800000u) != 0x7F800000u)       // not infinite, not NaN
-                    p[i] = __uint_as_float((w + (bits[i] * 0x9E3779B1u >> 16)) & 0xFFFF0000u);
+                w[i] = __float_as_uint(p[i]);
+                asm("mad.hi.u32 %0, %1, %2, %0;" : "+r"(w[i]) : "r"(bits[i] * 0x9E3779B1u), "r"(1u << 16));
             }
+            if (at.vec) {
+                // the upper halves are the results
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(e.p) + at.at) =
+                    make_uint4(__byte_perm(w[0], w[1], 0x7632), __byte_perm(w[2], w[3], 0x7632), __byte_perm(w[4], w[5], 0x7632),
+                               __byte_perm(w[6], w[7], 0x7632));
+                continue;
+            }
+#pragma unroll
+            for (int i = 0; i < kPer; i++) p[i] = __uint_as_float(w[i] & 0xFFFF0000u);
         }
-        put(e.p, at, e.p_bf16, vec, n, p);
+        put(e.p, at.at, e.p_bf16, at.vec, at.n, p);
     }
 }
 
-template <int CAP>
-cudaError_t run(const AdamwArgs& a, const Options& o, bool random, cudaStream_t st) {
+// The tensors with 8-bit moments or the others: a launch for every CAP of them
+template <int CAP, bool RANDOM, bool BITS8>
+cudaError_t run(const AdamwArgs& a, const Options& o, cudaStream_t st) {
     const bsq_adamw_tensor* list = static_cast<const bsq_adamw_tensor*>(a.tensors);
     cudaError_t e = cudaSuccess;
     for (int at = 0; at < a.count && e == cudaSuccess;) {
@@ -309,22 +515,27 @@ cudaError_t run(const AdamwArgs& a, const Options& o, bool random, cudaStream_t 
         t.first[0] = 0;
         for (; at < a.count && t.count < CAP; at++) {
             const bsq_adamw_tensor& x = list[at];
-            if (x.n == 0) continue;
+            if (x.n == 0 || (x.state == BSQ_MOMENTS_8BIT) != BITS8) continue;
             const int i = t.count++;
             const auto on = [](const void* p, uintptr_t k) { return reinterpret_cast<uintptr_t>(p) % k == 0; };
-            const bool bits8 = x.state == BSQ_MOMENTS_8BIT;
-            t.e[i] = {x.param, x.grad, x.m, x.v, x.m_scales, x.v_scales, static_cast<__nv_bfloat16*>(x.copy), x.n, at,
-                      (int8_t)(x.param_type == BSQ_OUT_BF16), (int8_t)(x.grad_type == BSQ_OUT_BF16), (int8_t)bits8,
-                      (int8_t)(on(x.param, 16) && on(x.grad, 16) && on(x.copy, 16) && on(x.m, bits8 ? 8 : 16) &&
-                               on(x.v, bits8 ? 8 : 16))};
+            constexpr uintptr_t state = BITS8 ? 8 : 16;
+            t.e[i] = {x.param, x.grad, x.m, x.v, x.m_scales, x.v_scales, static_cast<__nv_bfloat16*>(x.copy), x.n,
+                      mix(mix((uint32_t)at ^ o.seed_lo) ^ o.seed_hi),
+                      (int8_t)(x.param_type == BSQ_OUT_BF16), (int8_t)(x.grad_type == BSQ_OUT_BF16),
+                      (int8_t)(on(x.param, 16) && on(x.grad, 16) && on(x.copy, 16) && on(x.m, state) && on(x.v, state))};
             t.first[i + 1] = t.first[i] + (int32_t)((x.n + kChunk - 1) / kChunk);
         }
         if (t.count == 0) break;
-        const unsigned grid = (unsigned)std::min(t.first[t.count], a.num_sms * 16);
-        e = random ? launch_k(false, adamw_kernel<CAP, true>, dim3(grid), kThreads, 0, st, t, o)
-                   : launch_k(false, adamw_kernel<CAP, false>, dim3(grid), kThreads, 0, st, t, o);
+        const unsigned grid = (unsigned)std::min(t.first[t.count], a.num_sms * kCtas);
+        e = launch_k(false, adamw_kernel<CAP, RANDOM, BITS8>, dim3(grid), kThreads, 0, st, t, o);
     }
     return e;
+}
+template <int CAP>
+cudaError_t run(const AdamwArgs& a, const Options& o, bool random, cudaStream_t st) {
+    const cudaError_t e = random ? run<CAP, true, false>(a, o, st) : run<CAP, false, false>(a, o, st);
+    if (e != cudaSuccess) return e;
+    return random ? run<CAP, true, true>(a, o, st) : run<CAP, false, true>(a, o, st);
 }
 
 }  // namespace
@@ -352,7 +563,8 @@ cudaError_t run_adamw(const AdamwArgs& a, cudaStream_t st) {
     o.weight_decay = (float)x.weight_decay;
     o.log_beta1 = (float)std::log(x.beta1);
     o.log_beta2 = (float)std::log(x.beta2);
-    return a.count <= kSmall ? run<kSmall>(a, o, x.stochastic != 0, st) : run<kLarge>(a, o, x.stochastic != 0, st);
+    if (a.count <= kSmall) return run<kSmall>(a, o, x.stochastic != 0, st);
+    return a.count <= kMiddle ? run<kMiddle>(a, o, x.stochastic != 0, st) : run<kLarge>(a, o, x.stochastic != 0, st);
 }
 
 }  // namespace bsq

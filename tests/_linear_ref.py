@@ -179,7 +179,7 @@ def encode(x, bits, root):
     if root:
         code = np.where((x != 0) & (code == 0), 1, code)
     else:
-        code = np.where(x < 0, code | 0x80, code)
+        code = np.where(np.signbit(x), code | 0x80, code)
     code = np.where(np.repeat(bad, 32)[:n], 0x7F, code)
     return code.astype(np.uint8), np.where(bad, 255, e + 127).astype(np.uint8)
 

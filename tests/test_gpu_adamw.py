@@ -11,7 +11,7 @@ import torch
 from _linear_ref import E4M3, adamw_ref, decode
 
 pytestmark = pytest.mark.gpu
-BF, F32 = torch.bfloat16, torch.float32
+BF, F32, F32N = torch.bfloat16, torch.float32, np.float32
 HYPER = dict(lr=3e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.1)
 
 
@@ -244,6 +244,26 @@ def test_stochastic_rounding_moves_as_it_should_on_average(bsq):
     # a step's rounding has a deviation of at most half a step, 2^-4 of the value; 200 of them and 65536 elements
     assert abs(ratio[1] - want) <= 6 * 2.0 ** -4 * math.sqrt(steps / n)
     assert E4M3[0x7E] == 448
+
+
+def test_root_and_quotient_are_correctly_rounded(bsq):
+    # with beta1 = 0 and beta2 = 1/2 far from the first step, weight decay and eps 0 and lr 1, p' = -(g / sqrt(v / 2 + g^2 / 2)):
+    # every mantissa of v under two exponents with a g that does not reach it, then random quotients
+    grid = (np.arange(1 << 23, dtype=np.uint32) | (np.uint32(127) << np.uint32(23))).view(F32N)
+    rng = np.random.default_rng(0)
+    for k, (v, g) in enumerate([(grid, np.full(1 << 23, 2.0 ** -40, F32N)), (grid * F32N(2), np.full(1 << 23, 2.0 ** -40, F32N)),
+                                (grid, (1 + rng.random(1 << 23)).astype(F32N) * F32N(2.0 ** -30)),
+                                (rng.random(1 << 23).astype(F32N) * F32N(1e-10), rng.standard_normal(1 << 23).astype(F32N) * F32N(1e-5)),
+                                (np.ldexp(grid, rng.integers(-140, 120, 1 << 23)).astype(F32N), np.full(1 << 23, 0.75, F32N))]):
+        p = torch.zeros(1 << 23, device="cuda")
+        m, vt = torch.zeros(1 << 23, device="cuda"), torch.from_numpy(v.copy()).cuda()
+        bsq.adamw_step(bsq.AdamWList([p], [torch.from_numpy(g).cuda()], [(m, vt)]), 1.0, 100, betas=(0.0, 0.5), eps=0.0, weight_decay=0.0)
+        with np.errstate(over="ignore"):
+            want = F32N(0.5) * v + (F32N(0.5) * g) * g
+            q = F32N(0) - F32N(1) * (g / np.sqrt(want))
+        assert np.array_equal(host(vt), want) and np.array_equal(host(m), g)
+        got = host(p)
+        assert np.array_equal(got, q), (k, int((got != q).sum()))
 
 
 def test_refusals(bsq):
