@@ -177,12 +177,13 @@ __device__ __forceinline__ void store_chunk(const float (&v)[32], int bf16, int 
         }
         __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out) + row0 * ld + col;
         const int rows = (int)min((int64_t)32, M - row0);
-        for (int r = 0; r < rows; r++) {
+#pragma unroll 8
+        for (int r = 0; r < 32; r++) {
             uint16_t x;
             asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x)
                          : "r"(buf + (uint32_t)r * 64u + ((((uint32_t)lane >> 3) ^ ((uint32_t)(r >> 1) & 3u)) << 4) + ((uint32_t)lane & 7u) * 2u)
                          : "memory");
-            if (col + lane < N) o[r * ld + lane] = __ushort_as_bfloat16(x);
+            if (r < rows && col + lane < N) o[r * ld + lane] = __ushort_as_bfloat16(x);
         }
         __syncwarp();
         return;
@@ -203,12 +204,14 @@ __device__ __forceinline__ void store_chunk(const float (&v)[32], int bf16, int 
         }
         float* o = static_cast<float*>(out) + row0 * ld + col + c;
         const int rows = (int)min((int64_t)32, M - row0), k = lane & 15;
-        for (int r = lane >> 4; r < rows; r += 2) {
+#pragma unroll 8
+        for (int i = 0; i < 16; i++) {
+            const int r = 2 * i + (lane >> 4);
             float x;
             asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x)
                          : "r"(buf + (uint32_t)r * 64u + ((((uint32_t)k >> 2) ^ ((uint32_t)(r >> 1) & 3u)) << 4) + ((uint32_t)k & 3u) * 4u)
                          : "memory");
-            if (col + c + k < N) o[r * ld + k] = x;
+            if (r < rows && col + c + k < N) o[r * ld + k] = x;
         }
         __syncwarp();
     }

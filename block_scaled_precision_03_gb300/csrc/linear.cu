@@ -437,6 +437,115 @@ linear_gemm_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Para
     }
 }
 
+// ------------------------------------------------------- up to four tokens
+// Rows of w by up to TOK tokens on the CUDA cores: a warp takes kRows rows of w (gated: of both, for half as many
+// features), 16 bytes a lane and row at a time, and the tokens' same columns from L1; `parts` warps of a CTA share a
+// row's columns.  Bound by streaming w: there is no set-up before its first loads, where the tensor cores' kernel has
+// barriers, tensor memory and descriptors to prepare, and enough of them are in flight (16 warps per SM with 4 KB
+// each).  More tokens cost more than the stream: 13 instructions an element of w for eight of them.
+constexpr int kGemvTokens = 4;
+constexpr int kGemvThreads = 256;
+constexpr int kRows = 4, kAhead = 2;               // a warp's rows, and their loads in flight
+struct Gemv {
+    const __nv_bfloat16* x;
+    int64_t ldx;
+    const __nv_bfloat16* w[2];
+    int64_t ldw[2];
+    int64_t N;
+    int64_t vectors, part;         // 8 columns each: of a row, and of one of its parts
+    int32_t T, parts;
+    Fused f;
+};
+__device__ __forceinline__ uint4 stream16(const __nv_bfloat16* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+template <int TOK, bool GATED>
+__global__ void __launch_bounds__(kGemvThreads) linear_gemv_kernel(const __grid_constant__ Gemv p) {
+    constexpr int WARPS = kGemvThreads / 32, FEATURES = GATED ? kRows / 2 : kRows;
+    __shared__ float sums[WARPS][kRows * TOK];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int group = warp / p.parts, part = warp - group * p.parts, groups = WARPS / p.parts;
+    const int64_t feature0 = (int64_t)blockIdx.x * groups * FEATURES;
+    const __nv_bfloat16* row[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; r++) {
+        // features past the last read the last one's row and are not written
+        const int64_t f = min(p.N - 1, feature0 + group * FEATURES + (GATED ? r >> 1 : r));
+        const int which = GATED ? r & 1 : 0;
+        row[r] = p.w[which] + f * p.ldw[which];
+    }
+    float acc[kRows][TOK] = {};
+    const int64_t end = min(p.vectors, (part + 1) * p.part);
+    for (int64_t k = part * p.part + lane; k < end; k += 32 * kAhead) {
+        Pack<__nv_bfloat16, 8> w[kAhead][kRows], x[kAhead][TOK];
+#pragma unroll
+        for (int a = 0; a < kAhead; a++) {
+            const bool in = k + 32 * a < end;
+#pragma unroll
+            for (int r = 0; r < kRows; r++) {
+                w[a][r].zero();
+                if (in) w[a][r].v = stream16(row[r] + (k + 32 * a) * 8);
+            }
+#pragma unroll
+            for (int t = 0; t < TOK; t++) {
+                x[a][t].zero();
+                if (in && t < p.T) x[a][t].load(p.x + t * p.ldx + (k + 32 * a) * 8);
+            }
+        }
+#pragma unroll
+        for (int a = 0; a < kAhead; a++) {
+            float v[TOK][8];
+#pragma unroll
+            for (int t = 0; t < TOK; t++) x[a][t].unpack(v[t]);
+#pragma unroll
+            for (int r = 0; r < kRows; r++) {
+                float u[8];
+                w[a][r].unpack(u);
+#pragma unroll
+                for (int t = 0; t < TOK; t++)
+#pragma unroll
+                    for (int e = 0; e < 8; e++) acc[r][t] = fmaf(u[e], v[t][e], acc[r][t]);
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; r++)
+#pragma unroll
+        for (int t = 0; t < TOK; t++) {
+            float s = acc[r][t];
+#pragma unroll
+            for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+            if (lane == 0) sums[warp][r * TOK + t] = s;
+        }
+    __syncthreads();
+    // one output a thread, the parts of a row in their order
+    const int i = threadIdx.x;
+    if (i >= groups * FEATURES * TOK) return;
+    const int t = i / (groups * FEATURES), g = i - t * groups * FEATURES, mine = g / FEATURES, at = g - mine * FEATURES;
+    const int64_t feature = feature0 + g;
+    if (t >= p.T || feature >= p.N) return;
+    const auto sum = [&](int r) {
+        float s = 0.0f;
+        for (int k = 0; k < p.parts; k++) s += sums[mine * p.parts + k][r * TOK + t];
+        return s;
+    };
+    float z = sum(GATED ? 2 * at : at);
+    const float u = GATED ? sum(2 * at + 1) : 1.0f;
+    if (!GATED && p.f.bias) z += load_as_float(p.f.bias, feature, p.f.bias_bf16);
+    if (p.f.z) {
+        p.f.z[t * p.f.ldz + feature] = __float2bfloat16_rn(z);
+        if (GATED) p.f.u[t * p.f.ldu + feature] = __float2bfloat16_rn(u);
+    }
+    float v[1] = {z};
+    activate(p.f.act, v);
+    float y = GATED ? v[0] * u : v[0];
+    if (!GATED && p.f.residual) y += load_as_float(p.f.residual, t * p.f.ld_res + feature, p.f.y_bf16);
+    if (p.f.y_bf16) static_cast<__nv_bfloat16*>(p.f.y)[t * p.f.ldy + feature] = __float2bfloat16_rn(y);
+    else static_cast<float*>(p.f.y)[t * p.f.ldy + feature] = y;
+}
+
 // ------------------------------------------------------- around the products
 // The parts of a split sum [splits][M][ld], added in their order, and the forward epilogue: 4 columns a thread.
 template <bool GATED>
@@ -681,8 +790,34 @@ cudaError_t gemm(Params p, const Operand (&a)[2], const Operand (&b)[2], Maps& t
 }
 
 template <bool GATED>
+cudaError_t gemv(const LinearArgs& a, cudaStream_t st) {
+    Gemv p{};
+    p.x = static_cast<const __nv_bfloat16*>(a.x);
+    p.ldx = a.ldx;
+    p.w[0] = static_cast<const __nv_bfloat16*>(a.w);
+    p.ldw[0] = a.ldw;
+    p.w[1] = static_cast<const __nv_bfloat16*>(a.w2);
+    p.ldw[1] = a.ldw2;
+    p.N = a.out;
+    p.T = (int32_t)a.tokens;
+    p.vectors = a.cols / 8;
+    fused_args(p.f, a);
+    // a row's columns are shared by several warps where the rows alone would not fill the SMs twice over
+    constexpr int WARPS = kGemvThreads / 32;
+    const int64_t tasks = div_up(a.out, GATED ? kRows / 2 : kRows);
+    p.parts = 1;
+    while (p.parts < WARPS && tasks * p.parts < (int64_t)a.num_sms * 32) p.parts *= 2;
+    p.part = up(div_up(p.vectors, p.parts), 32);
+    const dim3 grid((unsigned)div_up(tasks, WARPS / p.parts));
+    if (p.T == 1) return launch_k(false, linear_gemv_kernel<1, GATED>, grid, kGemvThreads, 0, st, p);
+    if (p.T == 2) return launch_k(false, linear_gemv_kernel<2, GATED>, grid, kGemvThreads, 0, st, p);
+    return launch_k(false, linear_gemv_kernel<4, GATED>, grid, kGemvThreads, 0, st, p);
+}
+
+template <bool GATED>
 cudaError_t forward(const LinearArgs& a, cudaStream_t st) {
     const int64_t T = a.tokens, N = a.out, K = a.cols;
+    if (T <= kGemvTokens) return gemv<GATED>(a, st);
     const Cut cut = forward_cut(T, N, K, GATED, a.num_sms);
     Params p{};
     Maps tm{};
@@ -853,6 +988,7 @@ cudaError_t run_linear_join(const float* acc, int splits, int64_t M, int64_t N, 
 }
 
 size_t linear_workspace(int64_t tokens, int64_t out, int64_t cols, bool gated, int num_sms) {
+    if (tokens <= kGemvTokens) return 0;
     const Cut c = forward_cut(tokens, out, cols, gated, num_sms);
     return c.splits > 1 ? (size_t)c.splits * tokens * fused_acc_cols(out, gated) * 4 : 0;
 }
