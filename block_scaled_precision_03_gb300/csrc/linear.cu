@@ -101,7 +101,7 @@ linear_gemm_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Para
     // [stages] of A, [stages] of B, the epilogue's staging; the barriers come last
     constexpr bool FEW = MODE == kFew;
     constexpr int SUB_B = FEW && GATED ? 1 : kSub;             // sub-steps of B in a stage
-    const int S = FEW ? p.stages : kStages, b_bytes = FEW ? p.b_bytes : kOpBytes, sub_b = b_bytes / SUB_B;
+    const int S = FEW ? p.stages : kStages, b_bytes = FEW ? p.b_bytes : kOpBytes, sub_b = b_bytes / SUB_B;    // (places, not sizes)
     uint8_t* smA = base;
     uint8_t* smB = smA + S * kOpBytes;
     uint8_t* smOut = base + kStages * 2 * kOpBytes;
@@ -162,8 +162,8 @@ linear_gemm_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Para
                 // which of the two operand pairs of a gated layer's dw
                 const int which = MODE == kDw && GATED && ti.mt >= p.half ? 1 : 0;
                 const int am = (ti.mt - which * p.half) * p.tile_m + (int)rank * (p.tile_m / 2);
-                // a gated layer's tile is 128 columns of either projection
-                const int bn = MODE == kFwd && GATED ? ti.nt * 128 : ti.nt * p.tile_n + (int)rank * (p.tile_n / 2);
+                // a gated layer's tile is half as many columns of either projection
+                const int bn = MODE == kFwd && GATED ? ti.nt * (p.tile_n / 2) : ti.nt * p.tile_n + (int)rank * (p.tile_n / 2);
                 const CUtensorMap* mb = MODE == kFwd && GATED ? &tm.b[rank] : &tm.b[0];
                 for (int kb = ti.k0; kb < ti.k1; kb++) {
                     if (!wait(empty0 + 8 * stage, phase ^ 1, abort_flag, p.status, p.timeout_ns)) {
@@ -344,18 +344,20 @@ linear_gemm_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Para
         } else {
             // A thread owns one row and 128 of the tile's columns (gated: 64 of each projection's)
             constexpr bool PROJ = MODE == kFwd && GATED;
-            constexpr int OWN = PROJ ? 64 : 128;
+            // (forward, narrower tiles: 64 or 32; gated: 32)
+            const int own = MODE != kFwd ? 128 : PROJ ? p.tile_n / 4 : p.tile_n / 2;
+            const uint32_t second = PROJ ? (uint32_t)p.tile_n / 2 : 0;
             for (int t = cid; t < p.total; t += ncl) {
                 const TileAt ti = tile_at(p, t);
                 const int which = MODE == kDw && GATED && ti.mt >= p.half ? 1 : 0;
                 const int64_t row0 = (int64_t)(ti.mt - which * p.half) * kTile + rank * 128 + q * 32;
-                const int64_t col0 = PROJ ? (int64_t)ti.nt * 128 + half * 64 : (int64_t)ti.nt * kTile + half * 128;
+                const int64_t col0 = (int64_t)ti.nt * (PROJ ? p.tile_n / 2 : MODE == kFwd ? p.tile_n : kTile) + half * own;
                 const bool live = row0 < p.M && col0 < p.N;
-                const uint32_t ta0 = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * OWN);
+                const uint32_t ta0 = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * own);
                 // 32 columns of the sums, from the thread's column c on, leave
                 const auto leave = [&](float (&v)[32], const float (&u)[32], int c) {
                     if (p.splits > 1) {
-                        const int64_t at = (int64_t)ti.nt * kTile + half * OWN + c;
+                        const int64_t at = PROJ ? gate_col(col0 + c) : col0 + c;
                         const int64_t r = row0 + (int64_t)which * p.half * kTile;
                         store_part(v, st, &tm.out[0], (int)at, (int)r, ti.split, lane);
                         if (PROJ) store_part(u, st, &tm.out[0], (int)at + 128, (int)r, ti.split, lane);
@@ -373,10 +375,10 @@ linear_gemm_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Para
                     ++iter;
                     if (live)
 #pragma unroll 1
-                        for (int c = 0; c < OWN; c += 32) {
+                        for (int c = 0; c < own; c += 32) {
                             float v[32], u[32];
                             load_acc(v, ta0 + (uint32_t)(buf * kTile + c));
-                            if (PROJ) load_acc(u, ta0 + (uint32_t)(buf * kTile + 128 + c));
+                            if (PROJ) load_acc(u, ta0 + second + (uint32_t)(buf * kTile + c));
                             leave(v, u, c);
                         }
                     tc::fence_before();
@@ -392,7 +394,8 @@ linear_gemm_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Para
                         if (live)
 #pragma unroll
                             for (int c = 0; c < 128; c += 16)
-                                add_acc(z + c, ta0 + (uint32_t)((iter & 1) * kTile + (PROJ && c >= 64 ? c + 64 : c)));
+                                if ((PROJ ? c & 63 : c) < own)
+                                    add_acc(z + c, ta0 + (PROJ && c >= 64 ? second : 0u) + (uint32_t)((iter & 1) * kTile + (PROJ ? c & 63 : c)));
                         tc::fence_before();
                         __syncwarp();
                         if (lane == 0) tc::mbar_arrive_cluster(tempty_c0 + 8 * (iter & 1));
@@ -401,7 +404,7 @@ linear_gemm_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Para
                     if (!live) continue;
                     // the loop stays one, and z moves on: the epilogue's code is long
 #pragma unroll 1
-                    for (int c = 0; c < OWN; c += 32) {
+                    for (int c = 0; c < own; c += 32) {
                         float v[32], u[32];
 #pragma unroll
                         for (int j = 0; j < 32; j++) {
@@ -710,12 +713,13 @@ __global__ void __launch_bounds__(256) linear_bias_kernel(const float* sums, int
 constexpr double kStageUs = 0.55;                   // a pair's stage of K = 128
 struct Cut {
     bool few;
-    int tile_m, splits;
+    int tile_m, tile_n, splits;
 };
 // Few tokens: what the busiest pair streams, in bytes of w, decides; parts cost a launch and their own bytes.
 Cut few_cut(int64_t N, int64_t K, int64_t T, bool gated, int num_sms) {
     const int64_t pairs = std::max(1, num_sms / 2), stage_k = gated ? kSubK : kSub * kSubK, stages = div_up(K, stage_k);
-    Cut best{true, kTile, 1};
+    const int tile_n = (int)up(T, 16);
+    Cut best{true, kTile, tile_n, 1};
     double least = 0.0;
     for (int64_t n = 1; n == 1 || (n <= 16 && n * 4 <= stages); n++) {
         const int64_t per = div_up(stages, n);
@@ -725,7 +729,7 @@ Cut few_cut(int64_t N, int64_t K, int64_t T, bool gated, int num_sms) {
             const double us = load / 80e3 + (n > 1 ? 2.5 + (double)n * T * N * (gated ? 16 : 8) / 5e6 : 0.0);
             if (least == 0.0 || us < least) {
                 least = us;
-                best = {true, t, fused_parts(stages, n)};
+                best = {true, t, tile_n, fused_parts(stages, n)};
             }
         }
     }
@@ -733,8 +737,26 @@ Cut few_cut(int64_t N, int64_t K, int64_t T, bool gated, int num_sms) {
 }
 Cut forward_cut(int64_t T, int64_t N, int64_t K, bool gated, int num_sms) {
     if (T <= kFewTokens) return few_cut(N, K, T, gated, num_sms);
-    const int64_t tiles = div_up(T, kTile) * div_up(N, gated ? 128 : kTile);
-    return {false, kTile, fused_splits(tiles, div_up(K, kSub * kSubK), kStageUs, (double)T * fused_acc_cols(N, gated) * 8, num_sms / 2)};
+    // Narrower tiles where there are few: a stage of 128 or 64 columns takes 0.40 or 0.35 us instead of 0.55 (its MMAs
+    // cost the issuing thread the same), but there are more of them, and the last tile's epilogue is shorter.
+    static constexpr struct { int n; double stage_us, end_us; } kWidths[] = {{256, kStageUs, 4.0}, {128, 0.40, 2.0}, {64, 0.35, 1.0}};
+    const int64_t stages = div_up(K, kSub * kSubK), m_tiles = div_up(T, kTile);
+    const int pairs = std::max(1, num_sms / 2);
+    Cut best{};
+    double least = 0.0;
+    for (const auto& w : kWidths) {
+        if (gated && w.n < 128) break;             // a chunk of the epilogue is 32 columns of either projection
+        const int64_t tiles = m_tiles * div_up(N, gated ? w.n / 2 : w.n);
+        const double part_bytes = (double)T * fused_acc_cols(N, gated) * 8;
+        const int splits = fused_splits(tiles, stages, w.stage_us, part_bytes, pairs);
+        const double us = (double)div_up(tiles * splits, pairs) * div_up(stages, splits) * w.stage_us + w.end_us +
+                          (splits > 1 ? 2.0 + splits * part_bytes / 6.7e6 : 0.0);
+        if (least == 0.0 || us < least) {
+            least = us;
+            best = {false, kTile, w.n, splits};
+        }
+    }
+    return best;
 }
 
 struct Operand {
@@ -754,7 +776,7 @@ template <int MODE, bool GATED>
 cudaError_t gemm(Params p, const Operand (&a)[2], const Operand (&b)[2], Maps& tm, int64_t K, const Cut& cut, int wait,
                  bool fine, const LinearArgs& args, cudaStream_t st) {
     constexpr bool FEW = MODE == kFew;
-    const int tile_n = FEW ? (int)up(p.N, 16) : kTile;
+    const int tile_n = cut.tile_n;
     for (int i = 0; i < 2; i++) {
         const int j = GATED ? i : 0;
         const int jb = GATED && (MODE == kFwd || MODE == kDx) ? i : 0;
@@ -772,7 +794,7 @@ cudaError_t gemm(Params p, const Operand (&a)[2], const Operand (&b)[2], Maps& t
     p.stages = FEW ? std::min(kMaxStages, kStages * 2 * kOpBytes / (kOpBytes + p.b_bytes)) : kStages;
     p.tx = (uint32_t)(kSub * (cut.tile_m / 2) * kSubK * 2 + p.b_bytes);
     p.m_tiles = (int32_t)div_up(p.M, cut.tile_m) * (MODE == kDw && GATED ? 2 : 1);
-    p.n_tiles = (int32_t)div_up(p.N, MODE == kFwd && GATED ? 128 : tile_n);
+    p.n_tiles = (int32_t)div_up(p.N, MODE == kFwd && GATED ? tile_n / 2 : tile_n);
     p.split_stages = (int32_t)div_up(p.k_stages, cut.splits);
     p.splits = (int32_t)div_up(p.k_stages, p.split_stages);
     p.chunk = (fine ? kChunk : kSumChunk) * (FEW && GATED ? 2 : 1);
@@ -858,9 +880,9 @@ GradPlan grad_plan(int64_t T, int64_t N, int64_t D, bool gated, int num_sms) {
     g.blocks = div_up(T, kGradRows);
     const int pairs = num_sms / 2;
     const int64_t stages = div_up(N, kSub * kSubK) * (gated ? 2 : 1);
-    g.dx = {false, kTile, fused_splits(div_up(T, kTile) * div_up(D, kTile), stages, kStageUs, (double)T * D * 8, pairs)};
+    g.dx = {false, kTile, kTile, fused_splits(div_up(T, kTile) * div_up(D, kTile), stages, kStageUs, (double)T * D * 8, pairs)};
     const int64_t rows = up(N, kTile) * (gated ? 2 : 1);
-    g.dw = {false, kTile, fused_splits(rows / kTile * div_up(D, kTile), div_up(T, kSub * kSubK), kStageUs, (double)rows * D * 8, pairs)};
+    g.dw = {false, kTile, kTile, fused_splits(rows / kTile * div_up(D, kTile), div_up(T, kSub * kSubK), kStageUs, (double)rows * D * 8, pairs)};
     g.dz_bytes = (size_t)(T * g.ld * 2 * (gated ? 2 : 1));
     g.sums_bytes = gated ? 0 : (size_t)up(g.blocks * N * 4, 16);
     g.dx_bytes = g.dx.splits > 1 ? (size_t)(g.dx.splits * T * D * 4) : 0;
