@@ -35,52 +35,92 @@ struct Fused {
 };
 
 // ------------------------------------------------------------- activations
-// 1 / (1 + exp(-x)): ex2 and rcp are good to 2^-22 each; exp(-x) = inf gives 0
-__device__ __forceinline__ float sigmoid(float x) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + pair::exp2_fast(-1.44269504088896340736f * x)));
-    return r;
-}
-constexpr float kSqrtHalf = 0.70710678118654752440f;
+// Two values at a time, in packed instructions: the epilogue's instructions compete with those of the thread that
+// issues the MMAs.  ex2 and rcp are good to 2^-22 each; exp(-x) = inf gives 0.
+constexpr float kLog2eF = 1.44269504088896340736f;
 constexpr float kGeluC = 0.79788456080286535588f;      // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
-// 0.5 (1 + tanh(t)) is the sigmoid of 2 t, without the cancellation at negative t
-__device__ __forceinline__ float gelu_gate(float z) { return sigmoid(2.0f * kGeluC * (z + kGeluA * z * z * z)); }
-__device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(-kSqrtHalf * z); }
+__device__ __forceinline__ F2 exp2_two(F2 x) {
+    const float2 v = x.get();
+    return F2(pair::exp2_fast(v.x), pair::exp2_fast(v.y));
+}
+__device__ __forceinline__ F2 rcp_two(F2 x) {
+    const float2 v = x.get();
+    float a, b;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(v.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(v.y));
+    return F2(a, b);
+}
+__device__ __forceinline__ F2 sigmoid(F2 x) { return rcp_two(F2(1.0f) + exp2_two(x * F2(-kLog2eF))); }
+// 0.5 (1 + tanh(t)) is the sigmoid of 2 t, without the cancellation at negative t; 2 t = z (2 c + 2 c a z^2)
+__device__ __forceinline__ F2 gelu_gate(F2 z) {
+    const F2 t = z * fma2(z * z, F2(-2.0f * kGeluC * kGeluA * kLog2eF), F2(-2.0f * kGeluC * kLog2eF));
+    return rcp_two(F2(1.0f) + exp2_two(t));
+}
+// The normal distribution's value at z, and e = exp(-z^2 / 2).  With x = |z| / sqrt(2) and t = 1 / (1 + 0.45 x) the
+// tail beyond |z| is e / 2 times t P(t), a polynomial fitted to exp(x^2) erfc(x) for the least relative error (2.8e-7);
+// no part of it cancels, so it keeps its relative error as far as e does.  A third of erfcf's instructions, which
+// were most of a gelu epilogue.
+__device__ __forceinline__ F2 normal_cdf(F2 z, F2& e) {
+    const float2 v = z.get();
+    const F2 a(fabsf(v.x), fabsf(v.y));
+    e = exp2_two(z * z * F2(-0.72134752044448170368f));
+    const F2 t = rcp_two(fma2(F2(0.31819805153394638598f), a, F2(1.0f)));
+    F2 q(0.5f * 0.06687701493501663f);
+    q = fma2(q, t, F2(0.5f * -0.2403355836868286f));
+    q = fma2(q, t, F2(0.5f * 0.20899593830108643f));
+    q = fma2(q, t, F2(0.5f * 0.040100302547216415f));
+    q = fma2(q, t, F2(0.5f * 0.18878303468227386f));
+    q = fma2(q, t, F2(0.5f * 0.22802451252937317f));
+    q = fma2(q, t, F2(0.5f * 0.25364693999290466f));
+    q = fma2(q, t, F2(0.5f * 0.2539081275463104f));
+    const F2 tail = q * t * e;
+    const float2 lo = tail.get(), hi = fma2(tail, F2(-1.0f), F2(1.0f)).get();
+    return F2(v.x < 0.0f ? lo.x : hi.x, v.y < 0.0f ? lo.y : hi.y);
+}
 
 template <int ACT>
-__device__ __forceinline__ float act_one(float z) {
-    if (ACT == kActRelu) return z > 0.0f || z != z ? z : 0.0f;         // NaN stays NaN
+__device__ __forceinline__ F2 act_two(F2 z) {
+    if (ACT == kActRelu) {
+        const float2 v = z.get();                                      // NaN stays NaN
+        return F2(v.x > 0.0f || v.x != v.x ? v.x : 0.0f, v.y > 0.0f || v.y != v.y ? v.y : 0.0f);
+    }
     if (ACT == kActSilu) return z * sigmoid(z);
-    if (ACT == kActGelu) return z * normal_cdf(z);
+    if (ACT == kActGelu) {
+        F2 e;
+        return z * normal_cdf(z, e);
+    }
     if (ACT == kActGeluTanh) return z * gelu_gate(z);
     return z;
 }
 // act'(z), and act(z) beside it
 template <int ACT>
-__device__ __forceinline__ float act_slope(float z, float& value) {
+__device__ __forceinline__ F2 act_slope(F2 z, F2& value) {
+    value = z;
     if (ACT == kActRelu) {
-        value = act_one<kActRelu>(z);
-        return z > 0.0f ? 1.0f : z != z ? z : 0.0f;
+        value = act_two<kActRelu>(z);
+        const float2 v = z.get();
+        return F2(v.x > 0.0f ? 1.0f : v.x != v.x ? v.x : 0.0f, v.y > 0.0f ? 1.0f : v.y != v.y ? v.y : 0.0f);
     }
     if (ACT == kActSilu) {
-        const float s = sigmoid(z);
+        const F2 s = sigmoid(z);
         value = z * s;
-        return s * fmaf(z, 1.0f - s, 1.0f);
+        return s * fma2(z, fma2(s, F2(-1.0f), F2(1.0f)), F2(1.0f));
     }
     if (ACT == kActGelu) {
-        const float c = normal_cdf(z);
+        F2 e;
+        const F2 c = normal_cdf(z, e);
         value = z * c;
-        // z exp(-z^2 / 2) / sqrt(2 pi)
-        return fmaf(z * 0.39894228040143267794f, pair::exp2_fast(-0.72134752044448170368f * z * z), c);
+        return fma2(z * F2(0.39894228040143267794f), e, c);            // + z exp(-z^2 / 2) / sqrt(2 pi)
     }
     if (ACT == kActGeluTanh) {
-        const float s = gelu_gate(z);
+        const F2 s = gelu_gate(z);
         value = z * s;
-        return fmaf(2.0f * kGeluC * value * (1.0f - s), fmaf(3.0f * kGeluA, fminf(z * z, 1e30f), 1.0f), s);
+        const float2 q = (z * z).get();                                // (finite: 0 times it is 0)
+        const F2 p = fma2(F2(3.0f * kGeluA), F2(fminf(q.x, 1e30f), fminf(q.y, 1e30f)), F2(1.0f));
+        return fma2(value * F2(2.0f * kGeluC) * fma2(s, F2(-1.0f), F2(1.0f)), p, s);
     }
-    value = z;
-    return 1.0f;
+    return F2(1.0f);
 }
 // f<ACT>() for the activation `act`
 #define BSQ_WITH_ACT(act, F)                                 \
@@ -95,8 +135,12 @@ __device__ __forceinline__ float act_slope(float z, float& value) {
 template <int N>
 __device__ __forceinline__ void activate(int act, float (&v)[N]) {
     if (act == kActIdentity) return;
-#define F(A)                                      \
-    _Pragma("unroll") for (int j = 0; j < N; j++) v[j] = act_one<A>(v[j])
+#define F(A)                                                                  \
+    _Pragma("unroll") for (int j = 0; j < N; j += 2) {                        \
+        const float2 y = act_two<A>(F2(v[j], v[j + 1 < N ? j + 1 : j])).get(); \
+        v[j] = y.x;                                                           \
+        if (j + 1 < N) v[j + 1 < N ? j + 1 : j] = y.y;                        \
+    }
     BSQ_WITH_ACT(act, F)
 #undef F
 }
@@ -106,6 +150,11 @@ __device__ __forceinline__ float load_as_float(const void* p, int64_t i, int bf1
 }
 
 // ------------------------------------------------- chunks of 32 rows by 32 columns
+__device__ __forceinline__ void add_two(float* v, F2 x) {
+    const float2 s = (F2(v[0], v[1]) + x).get();
+    v[0] = s.x;
+    v[1] = s.y;
+}
 // v += p[0 .. 32), the first `n` of them (32 or more: all), 16 bytes at a time where `vec`
 __device__ __forceinline__ void add_row(float (&v)[32], const void* p, int64_t at, int bf16, int vec, int64_t n) {
     if (vec && n >= 32) {
@@ -116,10 +165,10 @@ __device__ __forceinline__ void add_row(float (&v)[32], const void* p, int64_t a
             for (int i = 0; i < 4; i++) k[i].load(from + 8 * i);
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-                float f[8];
-                k[i].unpack(f);
+                F2 f[4];
+                unpack2(k[i], f);
 #pragma unroll
-                for (int e = 0; e < 8; e++) v[8 * i + e] += f[e];
+                for (int e = 0; e < 4; e++) add_two(v + 8 * i + 2 * e, f[e]);
             }
         } else {
             const float* from = static_cast<const float*>(p) + at;
@@ -128,10 +177,8 @@ __device__ __forceinline__ void add_row(float (&v)[32], const void* p, int64_t a
             for (int i = 0; i < 8; i++) k[i] = *reinterpret_cast<const float4*>(from + 4 * i);
 #pragma unroll
             for (int i = 0; i < 8; i++) {
-                v[4 * i] += k[i].x;
-                v[4 * i + 1] += k[i].y;
-                v[4 * i + 2] += k[i].z;
-                v[4 * i + 3] += k[i].w;
+                add_two(v + 4 * i, F2(k[i].x, k[i].y));
+                add_two(v + 4 * i + 2, F2(k[i].z, k[i].w));
             }
         }
         return;
@@ -238,9 +285,16 @@ __device__ __forceinline__ void finish_gated(float (&v)[32], const float (&u)[32
     }
     activate(f.act, v);
 #pragma unroll
-    for (int j = 0; j < 32; j++) v[j] *= u[j];
+    for (int j = 0; j < 32; j += 2) {
+        const float2 h = (F2(v[j], v[j + 1]) * F2(u[j], u[j + 1])).get();
+        v[j] = h.x;
+        v[j + 1] = h.y;
+    }
     store_chunk(v, f.y_bf16, f.y_tma, tm_y, f.y, f.ldy, row0, col, M, N, st, lane);
 }
+
+// The column of column c of a gated layer's gate among its parts of a sum; up's is 128 further
+__device__ __forceinline__ int64_t gate_col(int64_t c) { return (c >> 7) * 256 + (c & 127); }
 
 struct LinearArgs;
 // the epilogue of a call (without the tensor maps' part)

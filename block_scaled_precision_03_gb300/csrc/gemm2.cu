@@ -35,7 +35,11 @@
 // CTA's rows of B are the gate's, the odd one's up's, and both projections' scales of
 // those columns take the places of the tile's two B scale bands, so that a CTA's
 // accumulator holds gate and up of its rows, 128 columns apart.  Where there are few
-// tiles the sum over K is split; linear_join_kernel adds the parts.
+// tiles the sum over K is split; linear_join_kernel adds the parts.  Up to kFewTokens
+// tokens the time goes to streaming the weights, and the product runs the other way
+// round: they are the tile's 256 rows, both CTAs' A, and the tokens its columns (one
+// q8 layer of 14336 -> 4096: 16 tiles, 76 pairs, so parts of K); the gate's and up's rows
+// are then tiles of their own, which the join brings together.
 // Every wait is bounded; a CTA that gave up records the status, and before
 // the pair exits every MMA, scale copy and stage load it issued has landed.
 #include <algorithm>
@@ -128,13 +132,17 @@ struct Params2 {
 };
 
 // What the kernels with an epilogue take besides
-enum { kPlain, kLinear, kGated };
+enum { kPlain, kLinear, kGated, kFewLinear, kFewGated };
+constexpr int64_t kFewTokens = 128;
 struct Nothing {};
 struct More {
-    CUtensorMap b, sfb;            // gated: the other projection
+    CUtensorMap b, sfb;            // gated: the other projection (few tokens: its rows as A)
     CUtensorMap z, u;              // outputs
     const float* ts_b;
     int32_t splits, split_stages;  // parts of the sum over K, and stages of each
+    int32_t half;                  // few tokens, gated: tiles of the gate's rows
+    float* acc;                    // few tokens: the parts [split][token][ld_acc]
+    int64_t ld_acc;
     Fused f;
 };
 template <int EPI>
@@ -160,6 +168,12 @@ __device__ __forceinline__ Part part_of(const Params2& p, const typename MoreOf<
         a.k1 = min(p.k_stages, a.k0 + more.split_stages);
     }
     return a;
+}
+
+template <int EPI>
+__device__ __forceinline__ int half_of(const typename MoreOf<EPI>::type& more) {
+    if constexpr (EPI != kPlain) return more.half;
+    else return 0;
 }
 
 // Tile order: groups of `raster` tiles along one dimension, swept along the
@@ -205,6 +219,7 @@ __device__ __noinline__ void drain_pair_loads(uint32_t full0, int S, int n_own, 
 // mixes experts and at most half a tile is idle when an expert covers an odd
 // number of bands.
 struct Tile2 {
+    int32_t which;         // few tokens, gated: 0 the gate's rows, 1 up's
     int32_t a_row;         // this CTA's first row of A (and of C)
     int32_t a_band;        // its 128-row band of A's scale tiles
     int32_t nt;            // 256-column tile of C
@@ -214,11 +229,16 @@ struct Tile2 {
 };
 
 template <int EPI>
-__device__ __forceinline__ Tile2 tile2(const Params2& p, int t, const GroupTable2* gt, int& gcur, uint32_t rank) {
+__device__ __forceinline__ Tile2 tile2(const Params2& p, int t, const GroupTable2* gt, int& gcur, uint32_t rank, int half = 0) {
     Tile2 ti;
+    ti.which = 0;
     if (p.num_groups == 0) {
         int mt, nt;
         tile_mn(p, t, mt, nt);
+        if (EPI == kFewGated && mt >= half) {
+            ti.which = 1;
+            mt -= half;
+        }
         ti.a_band = mt * 2 + (int)rank;
         ti.a_row = ti.a_band * 128;
         ti.nt = nt;
@@ -368,11 +388,14 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
             for (int t = cid; t < total && ok; t += ncl) {
                 int tile = t;
                 const Part pt = part_of<EPI>(p, more, tile);
-                const Tile2 ti = tile2<EPI>(p, tile, gt, gcur, rank);
+                const Tile2 ti = tile2<EPI>(p, tile, gt, gcur, rank, half_of<EPI>(more));
                 const int arow = ti.a_row, brow = ti.b_row;
                 const CUtensorMap* mb = &tmB;
+                const CUtensorMap* ma = &tmA;
                 if constexpr (EPI == kGated)
                     if (rank) mb = &more.b;
+                if constexpr (EPI == kFewGated)
+                    if (ti.which) ma = &more.b;
                 for (int kb = pt.k0; kb < pt.k1; kb++) {
                     if (!tc::mbar_wait(empty0 + 8 * stage, phase ^ 1, abort_flag, p.status, p.timeout_ns)) {
                         ok = false;
@@ -383,7 +406,7 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
 #pragma unroll
                     for (int j = 0; j < CF::KSUB; j++) {
                         const int kx = (kb * CF::KSUB + j) * BKB;
-                        tc::tma_load_2d_pair(tc::smem_u32(smA + stage * CF::OP_BYTES + j * HALF), &tmA, kx, arow, fb);
+                        tc::tma_load_2d_pair(tc::smem_u32(smA + stage * CF::OP_BYTES + j * HALF), ma, kx, arow, fb);
                         tc::tma_load_2d_pair(tc::smem_u32(smB + stage * CF::OP_BYTES + j * HALF), mb, kx, brow, fb);
                     }
                     ++issued;
@@ -401,7 +424,7 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
             for (int t = cid; t < total && ok; t += ncl) {
                 int tile = t;
                 const Part pt = part_of<EPI>(p, more, tile);
-                const Tile2 ti = tile2<EPI>(p, tile, gt, gcur, rank);
+                const Tile2 ti = tile2<EPI>(p, tile, gt, gcur, rank, half_of<EPI>(more));
                 for (int kb = pt.k0; kb < pt.k1; kb++) {
                     if (!tc::mbar_wait(sfree0 + 8 * stage, phase ^ 1, abort_flag, p.status, p.timeout_ns)) {
                         ok = false;
@@ -410,7 +433,10 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
                     const uint32_t sb = sfull_c0 + 8 * stage;
                     if (leader) tc::mbar_expect_tx(sfull0 + 8 * stage, 2 * CF::SF_TX);
                     uint8_t* sf = smSF + stage * CF::SF_STAGE;
-                    tc::tma_load_3d_pair(tc::smem_u32(sf), &tmSFA, 0, kb * CF::SF_ATOMS, ti.a_band, sb);
+                    const CUtensorMap* msf = &tmSFA;
+                    if constexpr (EPI == kFewGated)
+                        if (ti.which) msf = &more.sfb;
+                    tc::tma_load_3d_pair(tc::smem_u32(sf), msf, 0, kb * CF::SF_ATOMS, ti.a_band, sb);
                     if constexpr (EPI == kGated) {
                         // one band of each projection, up's behind the gate's
                         constexpr int BAND = CF::SFB_BYTES / 2;
@@ -515,13 +541,13 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
             beta = *p.ts_b;
         }
         float beta2 = 1.0f;
-        if constexpr (KIND == kKindNV && EPI == kGated) beta2 = *more.ts_b;
+        if constexpr (KIND == kKindNV && (EPI == kGated || EPI == kFewGated)) beta2 = *more.ts_b;
         Staging<1> stage_out{tc::smem_u32(smOut + (warp - 2) * 2048), 0};
         int iter = 0, gcur = 0;
         for (int t = cid; t < total; t += ncl, ++iter) {
             int tile = t;
             const Part pt = part_of<EPI>(p, more, tile);
-            const Tile2 ti = tile2<EPI>(p, tile, gt, gcur, rank);
+            const Tile2 ti = tile2<EPI>(p, tile, gt, gcur, rank, half_of<EPI>(more));
             if (!tc::mbar_wait(tfull, iter & 1, abort_flag, p.status, p.timeout_ns)) break;
             tc::fence_after();
             uint32_t r[4][32];
@@ -538,20 +564,59 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
             if (lane == 0) tc::mbar_arrive_cluster(tempty_c0);
             // this warp's 32 rows, clipped to the rows the CTA may write
             const int row0 = ti.a_row + q * 32;
-            if constexpr (EPI != kPlain) {
+            if constexpr (EPI == kFewLinear || EPI == kFewGated) {
+                // a thread owns one feature; neighbouring lanes write neighbouring features of a token
+                const int feature = row0 + lane;
+                if (h != 0 || feature >= p.M) continue;
+                const float a2 = EPI == kFewGated && ti.which ? beta2 : alpha;
+                const bool whole = EPI == kFewLinear && more.splits == 1;
+                const Fused& f = more.f;
+                const float bias = whole && f.bias ? load_as_float(f.bias, feature, f.bias_bf16) : 0.0f;
+#pragma unroll 1
+                for (int c = 0; c < p.N; c += 32) {
+                    float v[32];
+#pragma unroll
+                    for (int j = 0; j < 32; j++) {
+                        v[j] = __uint_as_float(r[0][j]) * a2 * beta + bias;
+                        r[0][j] = r[1][j];
+                        r[1][j] = r[2][j];
+                        r[2][j] = r[3][j];
+                    }
+                    const int n = min(32, p.N - c);
+                    if (!whole) {
+                        float* to = more.acc + ((int64_t)pt.split * p.N + c) * more.ld_acc +
+                                    (EPI == kFewGated ? gate_col(feature) + 128 * ti.which : feature);
+#pragma unroll
+                        for (int j = 0; j < 32; j++)
+                            if (j < n) to[j * more.ld_acc] = v[j];
+                        continue;
+                    }
+                    if (f.z) {
+#pragma unroll
+                        for (int j = 0; j < 32; j++)
+                            if (j < n) f.z[(c + j) * f.ldz + feature] = __float2bfloat16_rn(v[j]);
+                    }
+                    activate(f.act, v);
+#pragma unroll
+                    for (int j = 0; j < 32; j++)
+                        if (j < n) {
+                            const float y = f.residual ? v[j] + load_as_float(f.residual, (c + j) * f.ld_res + feature, f.y_bf16) : v[j];
+                            if (f.y_bf16) static_cast<__nv_bfloat16*>(f.y)[(c + j) * f.ldy + feature] = __float2bfloat16_rn(y);
+                            else static_cast<float*>(f.y)[(c + j) * f.ldy + feature] = y;
+                        }
+                }
+                continue;
+            } else if constexpr (EPI != kPlain) {
                 const int col0 = EPI == kGated ? ti.nt * 128 + h * 64 : ti.nt * BN + h * 128;
                 if (row0 >= p.M || col0 >= p.N) continue;
-#pragma unroll 1
-                for (int c = 0; c < OWN && col0 + c < p.N; c += 32) {
-                    // the loop stays one, and the sums move on
+#pragma unroll
+                for (int c = 0; c < OWN; c += 32) {
+                    if (col0 + c >= p.N) break;
                     float v[32], u[32];
 #pragma unroll
                     for (int j = 0; j < 32; j++) {
-                        v[j] = __uint_as_float(r[0][j]) * alpha * beta;
-                        u[j] = __uint_as_float(r[2][j]) * alpha * beta2;
-                        r[0][j] = r[1][j];
-                        if (EPI == kLinear) r[1][j] = r[2][j];
-                        r[2][j] = r[3][j];
+                        v[j] = __uint_as_float(r[c / 32][j]) * alpha * beta;
+                        u[j] = EPI == kGated ? __uint_as_float(r[2 + (c / 32 & 1)][j]) * alpha * beta2 : 0.0f;
                     }
                     if (more.splits > 1) {
                         const int at = ti.nt * BN + h * OWN + c;
@@ -785,56 +850,87 @@ cudaError_t run_gemm_pair(const GemmArgs& a, cudaStream_t st) {
 namespace {
 
 template <int EPI>
+cudaError_t launch_kind(const Setup& s, const CUtensorMap& tc_, const More& more, int pairs, cudaStream_t st) {
+    if (s.kind == kKindNV) return launch2<kKindNV, EPI>(s.p, s.ta, s.tb, s.tsa, s.tsb, tc_, more, 2 * pairs, st);
+    if (s.kind == kKindMX4) return launch2<kKindMX4, EPI>(s.p, s.ta, s.tb, s.tsa, s.tsb, tc_, more, 2 * pairs, st);
+    return launch2<kKindFP8, EPI>(s.p, s.ta, s.tb, s.tsa, s.tsb, tc_, more, 2 * pairs, st);
+}
+// a: the tokens and w, or the gate's weights; up: the tokens and up's weights
+template <bool GATED>
 cudaError_t fused(const GemmArgs& a, const GemmArgs& up, const LinearArgs& l, cudaStream_t st) {
-    constexpr bool GATED = EPI == kGated;
+    const bool few = a.M <= kFewTokens;
+    GemmArgs q = a;
+    if (few) {
+        // the weights are A, the tokens B; their tensor scales change places with them
+        q.fmt_a = a.fmt_b;
+        q.fmt_b = a.fmt_a;
+        q.a_codes = a.b_codes;
+        q.a_scales = a.b_scales;
+        q.b_codes = a.a_codes;
+        q.b_scales = a.a_scales;
+        q.ts_a = a.ts_b;
+        q.ts_b = a.ts_a;
+        q.M = a.N;
+        q.N = a.M;
+    }
     Setup s;
     More more{};
-    if (!set_up(s, a, GATED ? 1 : 2)) return cudaErrorInvalidValue;
-    if (GATED && !operand_b(s, more.b, more.sfb, up.b_codes, up.b_scales, a.N, 1)) return cudaErrorInvalidValue;
+    if (!set_up(s, q, GATED && !few ? 1 : 2)) return cudaErrorInvalidValue;
+    if (GATED && few) {
+        if (!tmap::codes_2d(&more.b, up.b_codes, a.N, s.kbytes, 128) ||
+            !tmap::scales_3d(&more.sfb, up.b_scales, (a.N + 127) / 128, s.n_atoms, s.sf_atoms, 1))
+            return cudaErrorInvalidValue;
+    } else if (GATED && !operand_b(s, more.b, more.sfb, up.b_codes, up.b_scales, a.N, 1)) {
+        return cudaErrorInvalidValue;
+    }
     Params2& p = s.p;
-    const int64_t n_tiles = GATED ? (a.N + 127) / 128 : (a.N + BN - 1) / BN, tiles = (a.M + 255) / 256 * n_tiles;
     const int splits = gemm_fused_splits(a.fmt_a, a.M, a.N, a.K, GATED, a.num_sms);
-    if (tiles * splits > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    const int64_t n_tiles = few ? 1 : GATED ? (a.N + 127) / 128 : (a.N + BN - 1) / BN;
+    more.half = p.m_tiles;
+    if (GATED && few) p.m_tiles *= 2;
+    if (p.m_tiles * n_tiles * splits > 0x7FFFFFFF) return cudaErrorInvalidValue;
     p.n_tiles = (int32_t)n_tiles;
-    p.total_tiles = (int32_t)(tiles * splits);
+    p.total_tiles = (int32_t)(p.m_tiles * n_tiles * splits);
     more.split_stages = (p.k_stages + splits - 1) / splits;
     more.splits = splits;
     more.ts_b = up.ts_b;
+    more.acc = static_cast<float*>(l.ws);
+    more.ld_acc = fused_acc_cols(a.N, GATED);
     fused_args(more.f, l);
     order_tiles(p, a.M * s.kbytes, (GATED ? 2 : 1) * a.N * s.kbytes);
     CUtensorMap tcm = s.ta;
-    float* acc = static_cast<float*>(l.ws);
-    const int64_t ld = fused_acc_cols(a.N, GATED);
-    if (splits > 1) {
-        if (!pair::map_acc(&tcm, acc, splits, a.M, ld)) return cudaErrorInvalidValue;
-    } else {
+    const bool parts = splits > 1 || (GATED && few);
+    if (!few && parts) {
+        if (!pair::map_acc(&tcm, more.acc, splits, a.M, more.ld_acc)) return cudaErrorInvalidValue;
+    } else if (!few) {
         more.f.y_tma = fused_map(&tcm, l.y, a.M, a.N, l.ldy, l.y_bf16);
         more.f.z_tma = fused_map(&more.z, l.z, a.M, a.N, l.ldz, true);
         more.f.u_tma = GATED ? fused_map(&more.u, l.u, a.M, a.N, l.ldu, true) : kNone;
     }
     const int pairs = std::max(1, std::min(a.num_sms / 2, p.total_tiles));
-    const cudaError_t e =
-        s.kind == kKindNV    ? launch2<kKindNV, EPI>(p, s.ta, s.tb, s.tsa, s.tsb, tcm, more, 2 * pairs, st)
-        : s.kind == kKindMX4 ? launch2<kKindMX4, EPI>(p, s.ta, s.tb, s.tsa, s.tsb, tcm, more, 2 * pairs, st)
-                             : launch2<kKindFP8, EPI>(p, s.ta, s.tb, s.tsa, s.tsb, tcm, more, 2 * pairs, st);
-    if (e != cudaSuccess || splits == 1) return e;
-    return run_linear_join(acc, splits, a.M, a.N, GATED, l, st);
+    const cudaError_t e = few ? launch_kind<GATED ? kFewGated : kFewLinear>(s, tcm, more, pairs, st)
+                              : launch_kind<GATED ? kGated : kLinear>(s, tcm, more, pairs, st);
+    return e != cudaSuccess || !parts ? e : run_linear_join(more.acc, splits, a.M, a.N, GATED, l, st);
 }
 
 }  // namespace
 
-// parts of the sum over K: a stage takes 0.4 us of MXFP8 (K = 256) or MXFP4, 0.45 of NVFP4 (K = 256)
+// parts of the sum over K: a stage (K = 256) takes 0.4 us of MXFP8 or MXFP4, 0.45 of NVFP4; with few tokens it is
+// the pair's share of the weights' stream
 int gemm_fused_splits(int fmt, int64_t tokens, int64_t out, int64_t cols, bool gated, int num_sms) {
-    const int64_t tiles = (tokens + 255) / 256 * ((out + (gated ? 127 : 255)) / (gated ? 128 : 256)), stages = (cols + 255) / 256;
-    return fused_splits(tiles, stages, fmt == kNVFP4 ? 0.45 : 0.4, (double)tokens * fused_acc_cols(out, gated) * 8, num_sms / 2);
+    const bool few = tokens <= kFewTokens, fp4 = fmt >= kMXFP4;
+    const int64_t tiles = few ? (out + 255) / 256 * (gated ? 2 : 1)
+                              : (tokens + 255) / 256 * ((out + (gated ? 127 : 255)) / (gated ? 128 : 256));
+    const double us = few ? (fp4 ? 0.45 : 0.82) : fmt == kNVFP4 ? 0.45 : 0.4;
+    return fused_splits(tiles, (cols + 255) / 256, us, (double)tokens * fused_acc_cols(out, gated) * 8, num_sms / 2);
 }
 size_t gemm_fused_workspace(int fmt, int64_t tokens, int64_t out, int64_t cols, bool gated, int num_sms) {
     const int n = gemm_fused_splits(fmt, tokens, out, cols, gated, num_sms);
-    return n > 1 ? (size_t)n * tokens * fused_acc_cols(out, gated) * 4 : 0;
+    return n > 1 || (gated && tokens <= kFewTokens) ? (size_t)n * tokens * fused_acc_cols(out, gated) * 4 : 0;
 }
-cudaError_t run_gemm_linear(const GemmArgs& a, const LinearArgs& l, cudaStream_t st) { return fused<kLinear>(a, a, l, st); }
+cudaError_t run_gemm_linear(const GemmArgs& a, const LinearArgs& l, cudaStream_t st) { return fused<false>(a, a, l, st); }
 cudaError_t run_gemm_gated(const GemmArgs& gate, const GemmArgs& up, const LinearArgs& l, cudaStream_t st) {
-    return fused<kGated>(gate, up, l, st);
+    return fused<true>(gate, up, l, st);
 }
 
 }  // namespace bsq

@@ -89,9 +89,6 @@ struct Maps {
 int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 int64_t div_up(int64_t v, int64_t m) { return (v + m - 1) / m; }
 
-// The column of column c of a gated layer's gate among its parts of a sum; up's is 128 further
-__device__ __forceinline__ int64_t gate_col(int64_t c) { return (c >> 7) * 256 + (c & 127); }
-
 // LONG: a tile's sum over K takes several accumulators.
 template <int MODE, bool GATED, bool LONG>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -659,13 +656,20 @@ __global__ void __launch_bounds__(256) linear_slope_kernel(const SlopeArgs a) {
             if (GATED) get(a.u, a.ldu, u);
             float o[8], w[8];
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-                float value;
-                const float slope = act_slope<ACT>(z[j], value);
-                // (not contracted with the sum: dbias alone comes out as it does beside the products)
-                o[j] = GATED ? d[j] * u[j] * slope : ACT == kActIdentity ? d[j] : __fmul_rn(d[j], slope);
-                w[j] = d[j] * value;
-                if (!GATED) sum[j] += o[j];
+            for (int j = 0; j < 8; j += 2) {
+                F2 value;
+                const F2 dd(d[j], d[j + 1]), slope = act_slope<ACT>(F2(z[j], z[j + 1]), value);
+                const float2 a2 = (GATED ? dd * F2(u[j], u[j + 1]) * slope : ACT == kActIdentity ? dd : dd * slope).get();
+                const float2 b2 = (dd * value).get();
+                o[j] = a2.x;
+                o[j + 1] = a2.y;
+                w[j] = b2.x;
+                w[j + 1] = b2.y;
+                // (single additions: not contracted with the product, dbias alone comes out as it does beside the products)
+                if (!GATED) {
+                    sum[j] = __fadd_rn(sum[j], a2.x);
+                    sum[j + 1] = __fadd_rn(sum[j + 1], a2.y);
+                }
             }
             // the workspace's rows hold whole vectors
             if (a.dz) {
