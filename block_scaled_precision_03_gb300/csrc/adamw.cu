@@ -84,26 +84,23 @@ __device__ __forceinline__ void random_bits(uint32_t at, uint32_t key, uint32_t 
         bits[i] = b ^ (b >> 16);
     }
 }
-// the largest and smallest of 8 (their magnitudes where ABS), NaN if one is
-template <bool ABS>
-__device__ __forceinline__ float largest(const float (&x)[kPer]) {
-    const auto most = [](float a, float b, float c) {
-        float m;
-        if (ABS) asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
-        else asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
-        return m;
-    };
-    return most(most(x[0], x[1], x[2]), most(x[3], x[4], x[5]), most(x[6], x[7], x[7]));
+// The largest and smallest of 8 floats that are not negative, by their bits, which are in the same order: NaN is above
+// infinity, and a NaN with its sign set is below 0.
+__device__ __forceinline__ int32_t bits_of(float x) { return __float_as_int(x); }
+__device__ __forceinline__ int32_t largest(const float (&x)[kPer]) {
+    const int32_t a = __vimax3_s32(bits_of(x[0]), bits_of(x[1]), bits_of(x[2])), b = __vimax3_s32(bits_of(x[3]), bits_of(x[4]), bits_of(x[5]));
+    return max(__vimax3_s32(a, b, bits_of(x[6])), bits_of(x[7]));
 }
-template <bool ABS>
-__device__ __forceinline__ float smallest(const float (&x)[kPer]) {
-    const auto least = [](float a, float b, float c) {
-        float m;
-        if (ABS) asm("min.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
-        else asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
-        return m;
-    };
-    return least(least(x[0], x[1], x[2]), least(x[3], x[4], x[5]), least(x[6], x[7], x[7]));
+__device__ __forceinline__ int32_t smallest(const float (&x)[kPer]) {
+    const int32_t a = __vimin3_s32(bits_of(x[0]), bits_of(x[1]), bits_of(x[2])), b = __vimin3_s32(bits_of(x[3]), bits_of(x[4]), bits_of(x[5]));
+    return min(__vimin3_s32(a, b, bits_of(x[6])), bits_of(x[7]));
+}
+// The bits of the largest magnitude of 8: of the positive ones the largest signed, of the others the largest unsigned
+__device__ __forceinline__ uint32_t largest_magnitude(const float (&x)[kPer]) {
+    const auto u = [](float f) { return __float_as_uint(f); };
+    const uint32_t a = __vimax3_u32(u(x[0]), u(x[1]), u(x[2])), b = __vimax3_u32(u(x[3]), u(x[4]), u(x[5]));
+    const uint32_t n = max(__vimax3_u32(a, b, u(x[6])), u(x[7]));
+    return max(n & 0x7FFFFFFFu, (uint32_t)max(largest(x), 0));
 }
 // 2^(byte - 127)
 __device__ __forceinline__ float power(uint32_t byte) { return __uint_as_float(byte == 0 ? 1u << 22 : byte << 23); }
@@ -117,7 +114,7 @@ __device__ __forceinline__ float power(uint32_t byte) { return __uint_as_float(b
 template <bool RANDOM, bool ROOT>
 __device__ __forceinline__ uint2 encode(const float (&x)[kPer], const uint32_t (&bits)[kPer], uint32_t& byte) {
     // bits of the largest magnitude: those of NaN and infinity are above all others
-    uint32_t most = __float_as_uint(largest<!ROOT>(x));
+    uint32_t most = ROOT ? (uint32_t)largest(x) : largest_magnitude(x);
 #pragma unroll
     for (int d = 1; d < 4; d <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
     if (most >= 0x7F800000u) {
@@ -141,7 +138,10 @@ __device__ __forceinline__ uint2 encode(const float (&x)[kPer], const uint32_t (
         else c += (bits[i] & 0xFFFFu) * 16u;
         return __uint_as_float(c & 0xFFF00000u);
     };
-    if (smallest<!ROOT>(y) >= 0.015625f) {
+    float least = fabsf(y[0]);
+#pragma unroll
+    for (int i = 1; i < kPer; i++) least = fminf(least, fabsf(y[i]));
+    if (least >= 0.015625f) {
         if (RANDOM)
 #pragma unroll
             for (int i = 0; i < kPer; i++) y[i] = cut(y[i], i);
@@ -243,26 +243,13 @@ __device__ __forceinline__ void step_scalars(Options& o) {
     o.step = step;
 }
 
-// The moments and parameters of 8 elements; r: the root of v.
-//
-// The root and the quotient are correctly rounded by Newton steps with a fused
-// multiply-add (P. Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", 1990): from y = 1 / sqrt(v) to some 23 bits, g = v y and h = y
-// / 2 are brought to full precision by one step, and the exact remainder v - g^2 rounds
-// g; for m / d the remainder m - d q does.  In packed instructions that is 4.5 and 3.5
-// of them an element, a third of the library's IEEE functions, which all of the 8-bit
-// step's time went to.  The remainders are exact while nothing underflows: v from 2^-90 to 2^90;
-// elsewhere (a v of 0 among them) the library's functions.  A quotient whose m is below
-// 2^-90 may be off in its last bit.
-//
-// A packed product and the addition behind it came out as one fused instruction, in
-// spite of their .rn, so a product that is added is two single ones.
+// The moments of 8 elements.  A packed product and the addition behind it came out as one fused instruction, in spite
+// of their .rn, so a product that is added is two single ones.
 __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
     const float2 x = a.get(), y = b.get();
     return F2(__fmul_rn(x.x, y.x), __fmul_rn(x.y, y.y));
 }
-__device__ __forceinline__ void update(float (&p)[kPer], const float (&g)[kPer], float (&m)[kPer], float (&v)[kPer],
-                                       float (&r)[kPer], const Options& o, float factor) {
+__device__ __forceinline__ void moments(const float (&g)[kPer], float (&m)[kPer], float (&v)[kPer], const Options& o, float factor) {
     const F2 b1(o.beta1), b2(o.beta2), c1(o.c1), c2(o.c2), f(factor);
 #pragma unroll
     for (int i = 0; i < kPer; i += 2) {
@@ -272,54 +259,58 @@ __device__ __forceinline__ void update(float (&p)[kPer], const float (&g)[kPer],
         m[i] = ms.x; m[i + 1] = ms.y;
         v[i] = vs.x; v[i + 1] = vs.y;
     }
-    if (smallest<false>(v) >= 0x1p-90f && largest<false>(v) <= 0x1p90f) {
-        const F2 minus(-1.0f);
+}
+// Their parameters; r: the root of v.
+//
+// The root and the quotient are correctly rounded by Newton steps with a fused
+// multiply-add (P. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990): from y = 1 / sqrt(v) to some 23 bits, g = v y and h = y
+// / 2 are brought to full precision by one step, and the exact remainder v - g^2 rounds
+// g; for m / d the remainder m - d q does.  In packed instructions that is 4.5 and 3.5
+// of them an element, a third of the library's IEEE functions.  The remainders are exact
+// while nothing underflows: v from 2^-90 to 2^90 (in_range); elsewhere, a v of 0 among
+// them, the library's functions.  A quotient whose m is below 2^-90 may be off in its last bit.
+__device__ __forceinline__ bool in_range(const float (&v)[kPer]) {
+    constexpr int32_t least = (127 - 90) << 23, most = (127 + 90) << 23;
+    return smallest(v) >= least && largest(v) <= most;
+}
+__device__ __forceinline__ void update(float (&p)[kPer], const float (&m)[kPer], const float (&v)[kPer], float (&r)[kPer],
+                                       const Options& o) {
+    const F2 minus(-1.0f);
 #pragma unroll
-        for (int i = 0; i < kPer; i += 2) {
-            const F2 vv(v[i], v[i + 1]);
-            float y0, y1;
-            asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y0) : "f"(v[i]));
-            asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y1) : "f"(v[i + 1]));
-            const F2 y(y0, y1);
-            F2 q = vv * y, h = y * F2(-0.5f);              // h: -1 / (2 sqrt(v))
-            const F2 e = fma2(q, h, F2(0.5f));
-            q = fma2(q, e, q);
-            h = fma2(h, e, h);
-            q = fma2(fma2(q, q, vv * minus), h, q);
-            const float2 root = q.get();
-            r[i] = root.x; r[i + 1] = root.y;
-            const F2 d = mul2(q, F2(o.root)) + F2(o.eps), nd = d * minus, mm(m[i], m[i + 1]);
-            const float2 ds = d.get();
-            float i0, i1;
-            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(i0) : "f"(ds.x));
-            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(i1) : "f"(ds.y));
-            F2 k(i0, i1);
-            k = fma2(k, fma2(nd, k, F2(1.0f)), k);
-            F2 t = mm * k;
-            t = fma2(fma2(nd, t, mm), k, t);
-            const float2 n = (mul2(F2(o.decay), F2(p[i], p[i + 1])) + mul2(F2(-o.size), t)).get();
-            p[i] = n.x; p[i + 1] = n.y;
-        }
-        return;
+    for (int i = 0; i < kPer; i += 2) {
+        const F2 vv(v[i], v[i + 1]);
+        float y0, y1;
+        asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y0) : "f"(v[i]));
+        asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y1) : "f"(v[i + 1]));
+        const F2 y(y0, y1);
+        F2 q = vv * y, h = y * F2(-0.5f);                  // h: -1 / (2 sqrt(v))
+        const F2 e = fma2(q, h, F2(0.5f));
+        q = fma2(q, e, q);
+        h = fma2(h, e, h);
+        q = fma2(fma2(q, q, vv * minus), h, q);
+        const float2 root = q.get();
+        r[i] = root.x; r[i + 1] = root.y;
+        const F2 d = mul2(q, F2(o.root)) + F2(o.eps), nd = d * minus, mm(m[i], m[i + 1]);
+        const float2 ds = d.get();
+        float i0, i1;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(i0) : "f"(ds.x));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(i1) : "f"(ds.y));
+        F2 k(i0, i1);
+        k = fma2(k, fma2(nd, k, F2(1.0f)), k);
+        F2 t = mm * k;
+        t = fma2(fma2(nd, t, mm), k, t);
+        const float2 n = (mul2(F2(o.decay), F2(p[i], p[i + 1])) + mul2(F2(-o.size), t)).get();
+        p[i] = n.x; p[i + 1] = n.y;
     }
-#pragma unroll 1
-    for (int k = 0; k < kPer; k++) {
-        // one at a time, and the arrays move on: this is rare, and long
-        r[0] = __fsqrt_rn(v[0]);
-        const float d = __fadd_rn(__fmul_rn(r[0], o.root), o.eps);
-        p[0] = __fsub_rn(__fmul_rn(o.decay, p[0]), __fmul_rn(o.size, __fdiv_rn(m[0], d)));
-        const float r0 = r[0], v0 = v[0], p0 = p[0], m0 = m[0];
+}
+__device__ __forceinline__ void update_any(float (&p)[kPer], const float (&m)[kPer], const float (&v)[kPer], float (&r)[kPer],
+                                           const Options& o) {
 #pragma unroll
-        for (int i = 0; i + 1 < kPer; i++) {
-            r[i] = r[i + 1];
-            v[i] = v[i + 1];
-            p[i] = p[i + 1];
-            m[i] = m[i + 1];
-        }
-        r[kPer - 1] = r0;
-        v[kPer - 1] = v0;
-        p[kPer - 1] = p0;
-        m[kPer - 1] = m0;
+    for (int i = 0; i < kPer; i++) {
+        r[i] = __fsqrt_rn(v[i]);
+        const float d = __fadd_rn(__fmul_rn(r[i], o.root), o.eps);
+        p[i] = __fsub_rn(__fmul_rn(o.decay, p[i]), __fmul_rn(o.size, __fdiv_rn(m[i], d)));
     }
 }
 
@@ -329,7 +320,7 @@ struct Place {
     const Entry* e;
     int64_t at;
     int n;                         // of the 8 elements
-    bool vec;
+    bool whole;                    // the warp's elements are all there, and lie on 16-byte boundaries
     __device__ __forceinline__ Place(const Table<CAP>& t, int c) {
         int lo = 0, hi = t.count - 1;               // the last tensor whose first chunk is <= c
         while (lo < hi) {
@@ -337,12 +328,14 @@ struct Place {
             if (t.first[mid] <= c) lo = mid; else hi = mid - 1;
         }
         e = &t.e[lo];
-        at = (int64_t)(c - t.first[lo]) * kChunk + threadIdx.x * kPer;
-        n = (int)max((int64_t)0, min((int64_t)kPer, e->n - at));
-        vec = e->vec && n == kPer;
+        const int64_t start = (int64_t)(c - t.first[lo]) * kChunk;
+        const int own = threadIdx.x * kPer, rest = (int)min(kChunk, e->n - start);
+        at = start + own;
+        n = max(0, min(kPer, rest - own));
+        whole = e->vec && rest >= (int)(threadIdx.x & ~31u) * kPer + 32 * kPer;
     }
 };
-// What a chunk reads, as it lies in memory (the elements of a tensor whose rows do not suit vectors put together)
+// What a chunk reads, as it lies in memory (elements off 16-byte boundaries put together)
 struct Words {
     uint4 v[2];
     __device__ __forceinline__ void load(const void* p, int64_t at, int bf16, bool vec, int n) {
@@ -423,84 +416,134 @@ struct Moments<true> {
     }
 };
 
+// What a thread holds of a chunk becomes its new state
+template <bool RANDOM, bool BITS8>
+__device__ __forceinline__ void leave(const Entry& e, int64_t at, int n, bool vec, const Options& o, const float (&m)[kPer],
+                                      const float (&v)[kPer], const float (&r)[kPer], float (&p)[kPer]) {
+    uint32_t bits[kPer] = {};
+    if (RANDOM) {
+        const uint32_t key = mix(e.key ^ (uint32_t)o.step) + (uint32_t)(at >> 32) * 0x9E3779B9u;
+        random_bits((uint32_t)at, key, bits);
+    }
+    if (BITS8) {
+        uint32_t mb, vb;
+        const uint2 mc = encode<RANDOM, false>(m, bits, mb), vc = encode<RANDOM, true>(r, bits, vb);
+        put_codes(e.m, at, vec, n, mc);
+        put_codes(e.v, at, vec, n, vc);
+        if (n > 0 && (threadIdx.x & 3) == 0) {
+            e.m_scales[at >> 5] = (uint8_t)mb;
+            e.v_scales[at >> 5] = (uint8_t)vb;
+        }
+    } else {
+        put(e.m, at, 0, vec, n, m);
+        put(e.v, at, 0, vec, n, v);
+    }
+    if (e.copy) put(e.copy, at, 1, vec, n, p);
+    if (RANDOM && e.p_bf16) {
+        uint32_t w[kPer];
+        float all = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kPer; i++) {
+            all += p[i];
+            w[i] = __float_as_uint(p[i]);
+            asm("mad.hi.u32 %0, %1, %2, %0;" : "+r"(w[i]) : "r"(bits[i] * 0x9E3779B1u), "r"(1u << 16));
+        }
+        if (vec && fabsf(all) < INFINITY) {
+            // the upper halves are the results
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(e.p) + at) =
+                make_uint4(__byte_perm(w[0], w[1], 0x7632), __byte_perm(w[2], w[3], 0x7632), __byte_perm(w[4], w[5], 0x7632),
+                           __byte_perm(w[6], w[7], 0x7632));
+            return;
+        }
+        // (NaN and infinity stay as they are: the random bits would carry a NaN over into the sign)
+#pragma unroll
+        for (int i = 0; i < kPer; i++)
+            if (fabsf(p[i]) < INFINITY) p[i] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+    put(e.p, at, e.p_bf16, vec, n, p);
+}
+
+// A warp's part of a chunk, 256 elements, is a unit of its own.  The first loop takes those that are whole, on 16-byte
+// boundaries and in the range of update(), with the next one's loads under way; what it leaves, the second loop takes.
+// (One loop with both ways in it held its values twice over: 92 instructions an element of 8-bit moments, not 78.)
+constexpr int kMost = 2048;                         // chunks of a CTA
 template <int CAP, bool RANDOM, bool BITS8>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table<CAP> t, Options o) {
+    __shared__ uint32_t left[kThreads / 32][kMost / 32];
+    uint32_t* mine = left[threadIdx.x >> 5];
+    const int lane = threadIdx.x & 31, chunks = t.first[t.count];
     if (o.step_at || o.lr_at) step_scalars(o);
     float factor = 1.0f;
     if (o.norm) {
         const float f = __fdiv_rn(o.max_norm, __fadd_rn(*o.norm, o.clip_eps));
         factor = f > 1.0f ? 1.0f : f;               // NaN stays NaN
     }
-    const int chunks = t.first[t.count];
-    // a chunk's loads run while the one before it is computed
     struct Chunk {
         Words p, g;
         Moments<BITS8> s;
+        __device__ __forceinline__ void load(const Place<CAP>& a, bool vec) {
+            p.load(a.e->p, a.at, a.e->p_bf16, vec, a.n);
+            g.load(a.e->g, a.at, a.e->g_bf16, vec, a.n);
+            s.load(*a.e, a.at, vec, a.n);
+        }
     };
-    const auto load = [&](const Place<CAP>& a, Chunk& c) {
-        c.p.load(a.e->p, a.at, a.e->p_bf16, a.vec, a.n);
-        c.g.load(a.e->g, a.at, a.e->g_bf16, a.vec, a.n);
-        c.s.load(*a.e, a.at, a.vec, a.n);
-    };
-    int next = blockIdx.x;
-    Place<CAP> ahead(t, next);
-    Chunk words;
-    load(ahead, words);
-    while (next < chunks) {
-        const Place<CAP> at = ahead;
+    {
+        Place<CAP> ahead(t, blockIdx.x);
+        Chunk words;
+        if (ahead.whole) words.load(ahead, true);
+        uint32_t some = 0;
+        int k = 0;
+        for (int c = blockIdx.x; c < chunks; k++) {
+            const Place<CAP> at = ahead;
+            const Entry& e = *at.e;
+            float p[kPer], g[kPer], m[kPer], v[kPer], r[kPer];
+            words.p.get(e.p_bf16, p);
+            words.g.get(e.g_bf16, g);
+            words.s.get(m, v);
+            c += gridDim.x;
+            if (c < chunks) {
+                ahead = Place<CAP>(t, c);
+                if (ahead.whole) words.load(ahead, true);
+            }
+            if (k > 0 && (k & 31) == 0) {
+                if (lane == 0) mine[(k >> 5) - 1] = some;
+                some = 0;
+            }
+            moments(g, m, v, o, factor);
+            if (!at.whole || !__all_sync(0xffffffffu, in_range(v))) {
+                some |= 1u << (k & 31);
+                continue;
+            }
+            update(p, m, v, r, o);
+            leave<RANDOM, BITS8>(e, at.at, kPer, true, o, m, v, r, p);
+        }
+        if (k > 0 && lane == 0) mine[(k - 1) >> 5] = some;
+        __syncwarp();
+    }
+    for (int k = 0, c = blockIdx.x; c < chunks; k++, c += gridDim.x) {
+        if (!(mine[k >> 5] >> (k & 31) & 1)) continue;
+        const Place<CAP> at(t, c);
         const Entry& e = *at.e;
+        Chunk words;
+        words.load(at, at.whole);
         float p[kPer], g[kPer], m[kPer], v[kPer], r[kPer];
         words.p.get(e.p_bf16, p);
         words.g.get(e.g_bf16, g);
         words.s.get(m, v);
-        next += gridDim.x;
-        if (next < chunks) {
-            ahead = Place<CAP>(t, next);
-            load(ahead, words);
-        }
-        uint32_t bits[kPer] = {};
-        if (RANDOM) {
-            const uint32_t key = mix(e.key ^ (uint32_t)o.step) + (uint32_t)(at.at >> 32) * 0x9E3779B9u;
-            random_bits((uint32_t)at.at, key, bits);
-        }
-        update(p, g, m, v, r, o, factor);
-        if (BITS8) {
-            if (at.n < kPer)
-                // elements past the end are 0 and change no scale; every lane takes part in the block's maximum
+        moments(g, m, v, o, factor);
+        // elements past the end change no scale; every lane takes part in the block's maximum
 #pragma unroll
-                for (int i = 0; i < kPer; i++)
-                    if (i >= at.n) m[i] = r[i] = 0.0f;
-            uint32_t mb, vb;
-            const uint2 mc = encode<RANDOM, false>(m, bits, mb), vc = encode<RANDOM, true>(r, bits, vb);
-            put_codes(e.m, at.at, at.vec, at.n, mc);
-            put_codes(e.v, at.at, at.vec, at.n, vc);
-            if (at.n > 0 && (threadIdx.x & 3) == 0) {
-                e.m_scales[at.at >> 5] = (uint8_t)mb;
-                e.v_scales[at.at >> 5] = (uint8_t)vb;
+        for (int i = 0; i < kPer; i++)
+            if (i >= at.n) {
+                m[i] = 0.0f;
+                v[i] = 1.0f;
             }
-        } else {
-            put(e.m, at.at, 0, at.vec, at.n, m);
-            put(e.v, at.at, 0, at.vec, at.n, v);
-        }
-        if (e.copy) put(e.copy, at.at, 1, at.vec, at.n, p);
-        if (RANDOM && e.p_bf16 && __float_as_uint(largest<true>(p)) < 0x7F800000u) {       // (else to nearest: it stays as it is)
-            uint32_t w[kPer];
+        if (in_range(v)) update(p, m, v, r, o);
+        else update_any(p, m, v, r, o);
 #pragma unroll
-            for (int i = 0; i < kPer; i++) {
-                w[i] = __float_as_uint(p[i]);
-                asm("mad.hi.u32 %0, %1, %2, %0;" : "+r"(w[i]) : "r"(bits[i] * 0x9E3779B1u), "r"(1u << 16));
-            }
-            if (at.vec) {
-                // the upper halves are the results
-                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(e.p) + at.at) =
-                    make_uint4(__byte_perm(w[0], w[1], 0x7632), __byte_perm(w[2], w[3], 0x7632), __byte_perm(w[4], w[5], 0x7632),
-                               __byte_perm(w[6], w[7], 0x7632));
-                continue;
-            }
-#pragma unroll
-            for (int i = 0; i < kPer; i++) p[i] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-        put(e.p, at.at, e.p_bf16, at.vec, at.n, p);
+        for (int i = 0; i < kPer; i++)
+            if (i >= at.n) r[i] = 0.0f;
+        leave<RANDOM, BITS8>(e, at.at, at.n, at.whole, o, m, v, r, p);
     }
 }
 
@@ -526,7 +569,8 @@ cudaError_t run(const AdamwArgs& a, const Options& o, cudaStream_t st) {
             t.first[i + 1] = t.first[i] + (int32_t)((x.n + kChunk - 1) / kChunk);
         }
         if (t.count == 0) break;
-        const unsigned grid = (unsigned)std::min(t.first[t.count], a.num_sms * kCtas);
+        const int n = t.first[t.count];
+        const unsigned grid = (unsigned)std::max(std::min(n, a.num_sms * kCtas), (n + kMost - 1) / kMost);
         e = launch_k(false, adamw_kernel<CAP, RANDOM, BITS8>, dim3(grid), kThreads, 0, st, t, o);
     }
     return e;

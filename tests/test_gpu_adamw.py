@@ -179,6 +179,10 @@ def test_a_captured_step_counts_on(bsq):
 
 @pytest.mark.parametrize("bits", [32, 8])
 def test_values_that_are_not_finite(bsq, bits):
+    for p_type in (F32, BF):
+        params, grads, states = make(bsq, [200], p_type, F32, bits, 0, 8)
+        grads[0][40], grads[0][100], params[0][150], params[0][160] = float("nan"), float("inf"), float("inf"), float("nan")
+        check(bsq, params, grads, states, seed=2)
     params, grads, states = make(bsq, [200], F32, F32, bits, 0, 8)
     grads[0][40] = float("nan")
     grads[0][100] = float("inf")
