@@ -472,6 +472,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     __shared__ uint32_t left[kThreads / 32][kMost / 32];
     uint32_t* mine = left[threadIdx.x >> 5];
     const int lane = threadIdx.x & 31, chunks = t.first[t.count];
+    pdl_launch_dependents();
+    pdl_wait();
     if (o.step_at || o.lr_at) step_scalars(o);
     float factor = 1.0f;
     if (o.norm) {
@@ -571,7 +573,7 @@ cudaError_t run(const AdamwArgs& a, const Options& o, cudaStream_t st) {
         if (t.count == 0) break;
         const int n = t.first[t.count];
         const unsigned grid = (unsigned)std::max(std::min(n, a.num_sms * kCtas), (n + kMost - 1) / kMost);
-        e = launch_k(false, adamw_kernel<CAP, RANDOM, BITS8>, dim3(grid), kThreads, 0, st, t, o);
+        e = launch_k(true, adamw_kernel<CAP, RANDOM, BITS8>, dim3(grid), kThreads, 0, st, t, o);
     }
     return e;
 }

@@ -27,9 +27,10 @@
 // kernel adds the parts in their order and does the epilogue.
 //
 // The tensor cores' FP32 sums are not rounded to nearest: a sum over K = 4096
-// loses some 6e-6.  An accumulator is read out every kSumChunk stages (K =
-// 4096) where a BF16 result hides that, every kChunk (K = 512) for FP32 results,
-// and added up in registers.
+// loses some 6e-6, over K = 16384 some 1e-4.  An accumulator is read out every
+// kSumChunk stages (K = 16384) where a BF16 result hides that, every kChunk (K =
+// 512) for FP32 results, and added up in registers.  (Read out every K = 4096 the
+// batch of 8192 x 14336 -> 4096 took 3% longer.)
 #include <algorithm>
 #include <cuda.h>
 #include "common.cuh"
@@ -47,12 +48,14 @@ namespace {
 using namespace pair;
 
 enum { kFwd, kFew, kDx, kDw };
-enum { kWaitLaunch, kWaitStart, kWaitEnd };         // when a product waits for the kernel before it: see head.cu
+// When a product waits for the kernel before it on the stream, whose dependent it is: before it reads or writes anything
+// (its set-up runs earlier), or at its end (it needs nothing of that kernel, and runs beside it).
+enum { kWaitStart, kWaitEnd };
 
 constexpr int kStages = 3;
 constexpr int kMaxStages = 6;                       // few tokens: as many as fit
 constexpr int kFewTokens = 128;
-constexpr int kChunk = 4, kSumChunk = 32;           // stages of K = 128 (few tokens, gated: twice as many of 64)
+constexpr int kChunk = 4, kSumChunk = 128;          // stages of K = 128 (few tokens, gated: twice as many of 64)
 constexpr int kSubBytes = 128 * kSubK * 2;          // one CTA's 128 rows of an operand, one sub-step
 constexpr int kOpBytes = kSub * kSubBytes;
 constexpr int kMmas = 4 * kSub;                     // per stage
@@ -477,6 +480,8 @@ __global__ void __launch_bounds__(kGemvThreads) linear_gemv_kernel(const __grid_
         row[r] = p.w[which] + f * p.ldw[which];
     }
     float acc[kRows][TOK] = {};
+    pdl_launch_dependents();
+    pdl_wait();
     const int64_t end = min(p.vectors, (part + 1) * p.part);
     for (int64_t k = part * p.part + lane; k < end; k += 32 * kAhead) {
         Pack<__nv_bfloat16, 8> w[kAhead][kRows], x[kAhead][TOK];
@@ -605,6 +610,7 @@ __global__ void __launch_bounds__(kFewThreads) linear_few_grad_kernel(const __gr
     const int64_t n0 = (int64_t)blockIdx.x * p.rows;
     const int rows = (int)min((int64_t)p.rows, p.N - n0), T = (int)p.T;
     pdl_launch_dependents();
+    pdl_wait();
     for (int i = threadIdx.x; i < rows * T; i += kFewThreads) {
         const int t = i / rows, r = i - t * rows;
         float2 d;
@@ -685,6 +691,7 @@ __global__ void __launch_bounds__(kFewThreads) linear_small_grad_kernel(const __
     const int64_t n0 = dw ? (int64_t)blockIdx.x * kEight : (int64_t)(b / groups) * kDxRows;
     const int rows = (int)min((int64_t)(dw ? kEight : kDxRows), p.N - n0);
     pdl_launch_dependents();
+    pdl_wait();
     // [part][token][8 rows], or [part][row][8 tokens]: the eight next to each other, 0 where there are fewer
     for (int i = threadIdx.x; i < (dw ? tokens : rows) * kEight; i += kFewThreads) {
         const int k = i / kEight, j = i - k * kEight, r = dw ? j : k, t = dw ? k : j;
@@ -870,6 +877,7 @@ struct SlopeArgs {
 template <int ACT, bool GATED, bool VEC>
 __global__ void __launch_bounds__(256) linear_slope_kernel(const SlopeArgs a) {
     pdl_launch_dependents();
+    pdl_wait();
     const int64_t col = ((int64_t)blockIdx.y * 32 + (threadIdx.x & 31)) * 8;
     const int64_t row0 = (int64_t)blockIdx.x * kGradRows;
     const int n = (int)max((int64_t)0, min((int64_t)8, a.cols - col));
@@ -953,6 +961,7 @@ __global__ void __launch_bounds__(256) linear_bias_kernel(const float* sums, int
 }
 
 // How a product is cut: rows of a pair (few tokens), and parts of the sum over K.
+constexpr int64_t kResident = 60ll << 20;          // (see choose_raster: 40 MB took 1% longer for 8192 x 14336 -> 4096, 80 MB 2%)
 constexpr double kStageUs = 0.55;                   // a pair's stage of K = 128
 struct Cut {
     bool few;
@@ -1012,7 +1021,7 @@ cudaError_t launch_gemm(const Params& p, const Maps& tm, int pairs, cudaStream_t
     static SharedMemory smem;
     const cudaError_t e = smem.allow(reinterpret_cast<const void*>(linear_gemm_kernel<MODE, GATED, LONG>), kSmem);
     if (e != cudaSuccess) return e;
-    return launch_k(p.wait != kWaitLaunch, linear_gemm_kernel<MODE, GATED, LONG>, dim3(2 * pairs), kThreads, kSmem, st, tm, p);
+    return launch_k(true, linear_gemm_kernel<MODE, GATED, LONG>, dim3(2 * pairs), kThreads, kSmem, st, tm, p);
 }
 // K: the depth of each operand pair
 template <int MODE, bool GATED>
@@ -1048,7 +1057,7 @@ cudaError_t gemm(Params p, const Operand (&a)[2], const Operand (&b)[2], Maps& t
     p.status = args.status;
     p.timeout_ns = args.timeout_ns;
     const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(args.num_sms / 2, total));
-    choose_raster(p, K, pairs);
+    choose_raster(p, K, pairs, kResident);
     if constexpr (!FEW)
         if (p.split_stages <= p.chunk) return launch_gemm<MODE, GATED, false>(p, tm, pairs, st);
     return launch_gemm<MODE, GATED, true>(p, tm, pairs, st);
@@ -1074,9 +1083,9 @@ cudaError_t gemv(const LinearArgs& a, cudaStream_t st) {
     while (p.parts < WARPS && tasks * p.parts < (int64_t)a.num_sms * 32) p.parts *= 2;
     p.part = up(div_up(p.vectors, p.parts), 32);
     const dim3 grid((unsigned)div_up(tasks, WARPS / p.parts));
-    if (p.T == 1) return launch_k(false, linear_gemv_kernel<1, GATED>, grid, kGemvThreads, 0, st, p);
-    if (p.T == 2) return launch_k(false, linear_gemv_kernel<2, GATED>, grid, kGemvThreads, 0, st, p);
-    return launch_k(false, linear_gemv_kernel<4, GATED>, grid, kGemvThreads, 0, st, p);
+    if (p.T == 1) return launch_k(true, linear_gemv_kernel<1, GATED>, grid, kGemvThreads, 0, st, p);
+    if (p.T == 2) return launch_k(true, linear_gemv_kernel<2, GATED>, grid, kGemvThreads, 0, st, p);
+    return launch_k(true, linear_gemv_kernel<4, GATED>, grid, kGemvThreads, 0, st, p);
 }
 
 template <bool GATED>
@@ -1095,7 +1104,7 @@ cudaError_t forward(const LinearArgs& a, cudaStream_t st) {
     if (cut.few) {
         p.M = N;
         p.N = T;
-        err = gemm<kFew, GATED>(p, {w0, w1}, {x, x}, tm, K, cut, kWaitLaunch, !a.y_bf16, a, st);
+        err = gemm<kFew, GATED>(p, {w0, w1}, {x, x}, tm, K, cut, kWaitStart, !a.y_bf16, a, st);
     } else {
         p.M = T;
         p.N = N;
@@ -1106,7 +1115,7 @@ cudaError_t forward(const LinearArgs& a, cudaStream_t st) {
             f.z_tma = fused_map(&tm.out[1], a.z, T, N, a.ldz, true);
             f.u_tma = GATED ? fused_map(&tm.out[2], a.u, T, N, a.ldu, true) : kNone;
         }
-        err = gemm<kFwd, GATED>(p, {x, x}, {w0, w1}, tm, K, cut, kWaitLaunch, !a.y_bf16, a, st);
+        err = gemm<kFwd, GATED>(p, {x, x}, {w0, w1}, tm, K, cut, kWaitStart, !a.y_bf16, a, st);
     }
     return err != cudaSuccess || cut.splits == 1 ? err : run_linear_join(p.acc, cut.splits, T, N, GATED, a, st);
 }
@@ -1140,8 +1149,8 @@ cudaError_t slope(const LinearArgs& a, const SlopeArgs& s, cudaStream_t st) {
     const dim3 grid((unsigned)div_up(s.rows, kGradRows), (unsigned)div_up(s.cols, 256));
     cudaError_t e = cudaErrorInvalidValue;
 #define F(A)                                                                                             \
-    e = vec ? launch_k(false, linear_slope_kernel<A, GATED, true>, grid, 256, 0, st, s)                  \
-            : launch_k(false, linear_slope_kernel<A, GATED, false>, grid, 256, 0, st, s)
+    e = vec ? launch_k(true, linear_slope_kernel<A, GATED, true>, grid, 256, 0, st, s)                  \
+            : launch_k(true, linear_slope_kernel<A, GATED, false>, grid, 256, 0, st, s)
     BSQ_WITH_ACT(a.act, F)
 #undef F
     return e;
@@ -1176,10 +1185,10 @@ cudaError_t backward_few(const LinearArgs& a, cudaStream_t st) {
     cudaError_t e;
     if (T <= kGemvTokens) {
         const auto k = T == 1 ? linear_few_grad_kernel<GATED, 1> : T == 2 ? linear_few_grad_kernel<GATED, 2> : linear_few_grad_kernel<GATED, 4>;
-        e = launch_k(false, k, dim3((unsigned)parts, wide), kFewThreads, (size_t)rows * (GATED ? 2 : 1) * T * 4, st, p);
+        e = launch_k(true, k, dim3((unsigned)parts, wide), kFewThreads, (size_t)rows * (GATED ? 2 : 1) * T * 4, st, p);
     } else {
         const int dw_ctas = a.dw || a.dbias ? (int)div_up(N, kEight) : 0, dx_ctas = a.dx ? (int)(parts * div_up(T, kEight)) : 0;
-        e = launch_k(false, linear_small_grad_kernel<GATED>, dim3((unsigned)(dw_ctas + dx_ctas), wide), kFewThreads, 0, st, p, dw_ctas);
+        e = launch_k(true, linear_small_grad_kernel<GATED>, dim3((unsigned)(dw_ctas + dx_ctas), wide), kFewThreads, 0, st, p, dw_ctas);
     }
     if (e == cudaSuccess && p.acc)
         e = launch_k(true, linear_few_sum_kernel, dim3((unsigned)div_up(T * (D / 4), 16)), 256, 0, st, p.acc, parts, T, D, to(a.dx), a.ld_dx);
@@ -1200,14 +1209,12 @@ cudaError_t backward(const LinearArgs& a, cudaStream_t st) {
     float* dx_acc = reinterpret_cast<float*>(ws + g.dz_bytes + g.sums_bytes);
     float* dw_acc = reinterpret_cast<float*>(ws + g.dz_bytes + g.sums_bytes + g.dx_bytes);
     cudaError_t e = cudaSuccess;
-    bool behind = false;                           // a kernel of this call runs before the next one
     const bool products = a.dx || a.dw;
     if ((copy && products) || a.dbias) {
         SlopeArgs s{static_cast<const __nv_bfloat16*>(a.dy), a.ld_dy, static_cast<const __nv_bfloat16*>(a.z), a.ldz,
                     static_cast<const __nv_bfloat16*>(a.u), a.ldu, copy && products ? dz : nullptr, du, g.ld,
                     a.dbias ? sums : nullptr, T, N};
         e = slope<GATED>(a, s, st);
-        behind = true;
         if (e == cudaSuccess && a.dbias)
             e = launch_k(true, linear_bias_kernel, dim3((unsigned)div_up(N, 32)), 256, 0, st, sums, g.blocks, N, a.dbias);
     }
@@ -1225,7 +1232,7 @@ cudaError_t backward(const LinearArgs& a, cudaStream_t st) {
         p.N = D;
         if (!(g.dx.splits > 1 ? map_acc(&tm.out[0], dx_acc, g.dx.splits, T, D) : tmap::out_2d(&tm.out[0], a.dx, T, D, a.ld_dx, true)))
             return cudaErrorInvalidValue;
-        e = gemm<kDx, GATED>(p, {d0, d1}, {w0, w1}, tm, N, g.dx, behind ? kWaitStart : kWaitLaunch, false, a, st);
+        e = gemm<kDx, GATED>(p, {d0, d1}, {w0, w1}, tm, N, g.dx, kWaitStart, false, a, st);
         if (e == cudaSuccess && g.dx.splits > 1) e = sum(dx_acc, g.dx.splits, T, 0, T, a.dx, a.ld_dx);
     }
     if (e == cudaSuccess && a.dw) {
@@ -1241,7 +1248,7 @@ cudaError_t backward(const LinearArgs& a, cudaStream_t st) {
             return cudaErrorInvalidValue;
         }
         // beside dx's last tiles, which waited for dz; the sum of dx's parts did not let anything start early
-        const int wait = !a.dx ? (behind ? kWaitStart : kWaitLaunch) : g.dx.splits > 1 ? kWaitLaunch : kWaitEnd;
+        const int wait = a.dx && g.dx.splits == 1 ? kWaitEnd : kWaitStart;
         e = gemm<kDw, GATED>(p, {d0, d1}, {x, x}, tm, T, g.dw, wait, false, a, st);
         if (e == cudaSuccess && g.dw.splits > 1) e = sum(dw_acc, g.dw.splits, all, 0, N, a.dw, a.ld_dw);
         if (e == cudaSuccess && g.dw.splits > 1 && GATED) e = sum(dw_acc, g.dw.splits, all, half, N, a.dw2, a.ld_dw2);
