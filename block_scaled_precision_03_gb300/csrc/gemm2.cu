@@ -385,6 +385,11 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
             uint32_t phase = 0;
             bool ok = true;
             int gcur = 0, issued = 0;
+            if constexpr (EPI != kPlain) {
+                // its set-up runs beside the kernel before it on the stream
+                pdl_wait();
+                pdl_launch_dependents();
+            }
             for (int t = cid; t < total && ok; t += ncl) {
                 int tile = t;
                 const Part pt = part_of<EPI>(p, more, tile);
@@ -421,6 +426,7 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
             uint32_t phase = 0;
             bool ok = true;
             int gcur = 0, issued = 0;
+            if constexpr (EPI != kPlain) pdl_wait();
             for (int t = cid; t < total && ok; t += ncl) {
                 int tile = t;
                 const Part pt = part_of<EPI>(p, more, tile);
@@ -475,6 +481,7 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
             uint32_t phase = 0;
             int iter = 0;
             bool ok = true, any = false;
+            if constexpr (EPI != kPlain) pdl_wait();          // the limits of the waits count from there
             for (int t = cid; t < total && ok; t += ncl, ++iter) {
                 // both CTAs' epilogue warps arrive here after their TMEM loads completed
                 // (tcgen05.wait::ld); a CTA-scope acquire suffices
@@ -536,6 +543,7 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
         // NVFP4: the two tensor scales are applied one after the other, so that
         // their product is never formed on its own (it can underflow FP32)
         float alpha = 1.0f, beta = 1.0f;
+        if constexpr (EPI != kPlain) pdl_wait();
         if (KIND == kKindNV) {
             alpha = *p.ts_a;
             beta = *p.ts_b;
@@ -659,6 +667,7 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true, any = false;
+            if constexpr (EPI != kPlain) pdl_wait();
             for (int t = cid; t < total && ok; t += ncl) {
                 int tile = t;
                 const Part pt = part_of<EPI>(p, more, tile);
@@ -744,8 +753,8 @@ cudaError_t launch2(const Params2& p, const CUtensorMap& ta, const CUtensorMap& 
     static SharedMemory smem;
     const cudaError_t e = smem.allow(reinterpret_cast<const void*>(gemm2_kernel<KIND, EPI>), Cfg2<KIND>::SMEM);
     if (e != cudaSuccess) return e;
-    gemm2_kernel<KIND, EPI><<<grid, kThreads, Cfg2<KIND>::SMEM, st>>>(ta, tb, tsa, tsb, tc_, p, more);
-    return cudaGetLastError();
+    return launch_k(EPI != kPlain, gemm2_kernel<KIND, EPI>, dim3((unsigned)grid), kThreads, Cfg2<KIND>::SMEM, st, ta, tb, tsa, tsb, tc_, p,
+                    more);
 }
 
 // The operands' part of a call: sizes, descriptors, tensor maps; `sfb_bands` 128-row bands of B's scales a load

@@ -1029,11 +1029,12 @@ cudaError_t gemm(Params p, const Operand (&a)[2], const Operand (&b)[2], Maps& t
                  bool fine, const LinearArgs& args, cudaStream_t st) {
     constexpr bool FEW = MODE == kFew;
     const int tile_n = cut.tile_n;
+    // the second operands where there are any
+    constexpr bool TWO_A = GATED && MODE != kFwd, TWO_B = GATED && (MODE == kFwd || MODE == kDx);
     for (int i = 0; i < 2; i++) {
-        const int j = GATED ? i : 0;
-        const int jb = GATED && (MODE == kFwd || MODE == kDx) ? i : 0;
-        if (!map_operand(&tm.a[i], a[j].p, a[j].rows, a[j].cols, a[j].ld, a_mn(MODE) ? kSubK : cut.tile_m / 2) ||
-            !map_operand(&tm.b[i], b[jb].p, b[jb].rows, b[jb].cols, b[jb].ld, b_mn(MODE) ? kSubK : tile_n / 2))
+        if ((i == 0 || TWO_A) && !map_operand(&tm.a[i], a[i].p, a[i].rows, a[i].cols, a[i].ld, a_mn(MODE) ? kSubK : cut.tile_m / 2))
+            return cudaErrorInvalidValue;
+        if ((i == 0 || TWO_B) && !map_operand(&tm.b[i], b[i].p, b[i].rows, b[i].cols, b[i].ld, b_mn(MODE) ? kSubK : tile_n / 2))
             return cudaErrorInvalidValue;
     }
     const int64_t stage_k = FEW && GATED ? kSubK : kSub * kSubK;
