@@ -188,7 +188,7 @@ linear_gemm_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Para
                         }
                         if (b_mn(MODE)) {
                             tc::tma_load_2d_pair(db, mb, bn, k, fb);
-                            tc::tma_load_2d_pair(db + 8192, mb, bn + 64, k, fb);
+                            if (p.tile_n == kTile) tc::tma_load_2d_pair(db + 8192, mb, bn + 64, k, fb);
                         } else if (j < SUB_B) {
                             tc::tma_load_2d_pair(db, mb, k, bn, fb);
                         }
@@ -344,14 +344,14 @@ linear_gemm_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Para
         } else {
             // A thread owns one row and 128 of the tile's columns (gated: 64 of each projection's)
             constexpr bool PROJ = MODE == kFwd && GATED;
-            // (forward, narrower tiles: 64 or 32; gated: 32)
-            const int own = MODE != kFwd ? 128 : PROJ ? p.tile_n / 4 : p.tile_n / 2;
+            // (narrower tiles: 64 or 32; gated: 32)
+            const int own = PROJ ? p.tile_n / 4 : p.tile_n / 2;
             const uint32_t second = PROJ ? (uint32_t)p.tile_n / 2 : 0;
             for (int t = cid; t < p.total; t += ncl) {
                 const TileAt ti = tile_at(p, t);
                 const int which = MODE == kDw && GATED && ti.mt >= p.half ? 1 : 0;
                 const int64_t row0 = (int64_t)(ti.mt - which * p.half) * kTile + rank * 128 + q * 32;
-                const int64_t col0 = (int64_t)ti.nt * (PROJ ? p.tile_n / 2 : MODE == kFwd ? p.tile_n : kTile) + half * own;
+                const int64_t col0 = (int64_t)ti.nt * (PROJ ? p.tile_n / 2 : p.tile_n) + half * own;
                 const bool live = row0 < p.M && col0 < p.N;
                 const uint32_t ta0 = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * own);
                 // 32 columns of the sums, from the thread's column c on, leave
@@ -987,28 +987,32 @@ Cut few_cut(int64_t N, int64_t K, int64_t T, bool gated, int num_sms) {
     }
     return best;
 }
-Cut forward_cut(int64_t T, int64_t N, int64_t K, bool gated, int num_sms) {
-    if (T <= kFewTokens) return few_cut(N, K, T, gated, num_sms);
-    // Narrower tiles where there are few: a stage of 128 or 64 columns takes 0.40 or 0.35 us instead of 0.55 (its MMAs
-    // cost the issuing thread the same), but there are more of them, and the last tile's epilogue is shorter.
+// Tiles of `least` to 256 columns.  Narrower ones where there are few: a stage of 128 or 64 columns takes 0.40 or 0.35
+// us instead of 0.55 (its MMAs cost the issuing thread the same), but there are more of them, and the last tile's
+// epilogue is shorter.  `per`: columns of the result for a column of a tile; part_bytes: a part's, written and read.
+Cut wide_cut(int64_t m_tiles, int64_t cols, double per, int64_t stages, double part_bytes, int least, int num_sms) {
     static constexpr struct { int n; double stage_us, end_us; } kWidths[] = {{256, kStageUs, 4.0}, {128, 0.40, 2.0}, {64, 0.35, 1.0}};
-    const int64_t stages = div_up(K, kSub * kSubK), m_tiles = div_up(T, kTile);
     const int pairs = std::max(1, num_sms / 2);
     Cut best{};
-    double least = 0.0;
+    double fewest = 0.0;
     for (const auto& w : kWidths) {
-        if (gated && w.n < 128) break;             // a chunk of the epilogue is 32 columns of either projection
-        const int64_t tiles = m_tiles * div_up(N, gated ? w.n / 2 : w.n);
-        const double part_bytes = (double)T * fused_acc_cols(N, gated) * 8;
+        if (w.n < least) break;
+        const int64_t tiles = m_tiles * div_up(cols, (int64_t)(w.n * per));
         const int splits = fused_splits(tiles, stages, w.stage_us, part_bytes, pairs);
         const double us = (double)div_up(tiles * splits, pairs) * div_up(stages, splits) * w.stage_us + w.end_us +
                           (splits > 1 ? 2.0 + splits * part_bytes / 6.7e6 : 0.0);
-        if (least == 0.0 || us < least) {
-            least = us;
+        if (fewest == 0.0 || us < fewest) {
+            fewest = us;
             best = {false, kTile, w.n, splits};
         }
     }
     return best;
+}
+Cut forward_cut(int64_t T, int64_t N, int64_t K, bool gated, int num_sms) {
+    if (T <= kFewTokens) return few_cut(N, K, T, gated, num_sms);
+    // (gated: a chunk of the epilogue is 32 columns of either projection)
+    return wide_cut(div_up(T, kTile), N, gated ? 0.5 : 1.0, div_up(K, kSub * kSubK), (double)T * fused_acc_cols(N, gated) * 8,
+                    gated ? 128 : 64, num_sms);
 }
 
 struct Operand {
@@ -1131,11 +1135,10 @@ GradPlan grad_plan(int64_t T, int64_t N, int64_t D, bool gated, int num_sms) {
     GradPlan g{};
     g.ld = up(N, 8);
     g.blocks = div_up(T, kGradRows);
-    const int pairs = num_sms / 2;
-    const int64_t stages = div_up(N, kSub * kSubK) * (gated ? 2 : 1);
-    g.dx = {false, kTile, kTile, fused_splits(div_up(T, kTile) * div_up(D, kTile), stages, kStageUs, (double)T * D * 8, pairs)};
+    // (an MN-major operand is read in boxes of 64 columns for either CTA)
+    g.dx = wide_cut(div_up(T, kTile), D, 1.0, div_up(N, kSub * kSubK) * (gated ? 2 : 1), (double)T * D * 8, 128, num_sms);
     const int64_t rows = up(N, kTile) * (gated ? 2 : 1);
-    g.dw = {false, kTile, kTile, fused_splits(rows / kTile * div_up(D, kTile), div_up(T, kSub * kSubK), kStageUs, (double)rows * D * 8, pairs)};
+    g.dw = wide_cut(rows / kTile, D, 1.0, div_up(T, kSub * kSubK), (double)rows * D * 8, 128, num_sms);
     g.dz_bytes = (size_t)(T * g.ld * 2 * (gated ? 2 : 1));
     g.sums_bytes = gated ? 0 : (size_t)up(g.blocks * N * 4, 16);
     g.dx_bytes = g.dx.splits > 1 ? (size_t)(g.dx.splits * T * D * 4) : 0;
