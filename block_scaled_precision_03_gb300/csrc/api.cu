@@ -249,8 +249,11 @@ static bsq_status check_out(const void* p, int64_t ld, int32_t type, int64_t col
     if (ld < cols) return BSQ_ERR_INVALID_ARG;
     return reinterpret_cast<uintptr_t>(p) % (type == BSQ_OUT_BF16 ? 2 : 4) ? BSQ_ERR_ALIGNMENT : BSQ_OK;
 }
+static bool fused_supported(int64_t tokens, int64_t out) {
+    return tokens <= 0x7FFFFF00LL && out <= bsq::kLinearMax && tokens * out <= bsq::kLinearMaxElements;
+}
 static size_t fused_bytes(int32_t fmt, int64_t tokens, int64_t out, int64_t cols, bool gated) {
-    if (!valid_fmt(fmt) || tokens < 1 || out < 1 || cols < 1 || tokens > 0x7FFFFF00LL || out > bsq::kLinearMaxOut) return 0;
+    if (!valid_fmt(fmt) || tokens < 1 || out < 1 || cols < 1 || !fused_supported(tokens, out)) return 0;
     return bsq::gemm_fused_workspace(fmt, tokens, out, cols, gated, num_sms());
 }
 
@@ -262,17 +265,15 @@ size_t bsq_gemm_gated_workspace_bytes(int32_t fmt, int64_t tokens, int64_t out, 
 }
 
 static bsq_status fused_common(const bsq_tensor* A, const bsq_tensor* B, int32_t activation, void* y, int64_t ldy,
-                               int32_t type, void* workspace, size_t workspace_bytes, bool gated, bsq::GemmArgs& a,
-                               bsq::LinearArgs& l) {
+                               int32_t type, void* workspace, size_t workspace_bytes, bool gated, bsq::LinearArgs& l) {
     bsq_status s = check_gemm_pair(A, B);
     if (s != BSQ_OK) return s;
     if (!y || !out_type_ok(type) || activation < BSQ_ACT_IDENTITY || activation > BSQ_ACT_GELU_TANH) return BSQ_ERR_INVALID_ARG;
-    if (A->rows > 0x7FFFFF00LL || B->rows > bsq::kLinearMaxOut) return BSQ_ERR_UNSUPPORTED;
+    if (!fused_supported(A->rows, B->rows)) return BSQ_ERR_UNSUPPORTED;
     if ((s = check_out(y, ldy, type, B->rows)) != BSQ_OK) return s;
     const size_t need = fused_bytes(A->fmt, A->rows, B->rows, A->cols, gated);
     if (need && (!workspace || workspace_bytes < need)) return BSQ_ERR_INVALID_ARG;
     if (need && !al16(workspace)) return BSQ_ERR_ALIGNMENT;
-    if ((s = dense_args(A, B, kDefaultTimeoutNs, a)) != BSQ_OK) return s;
     l.act = activation;
     l.y = y;
     l.ldy = ldy;
@@ -287,11 +288,12 @@ bsq_status bsq_gemm_linear(const bsq_tensor* A, const bsq_tensor* B, const void*
     bsq::GemmArgs a{};
     bsq::LinearArgs l{};
     if (bias && !out_type_ok(bias_type)) return BSQ_ERR_INVALID_ARG;
-    bsq_status s = fused_common(A, B, activation, y, ldy, type, workspace, workspace_bytes, false, a, l);
+    bsq_status s = fused_common(A, B, activation, y, ldy, type, workspace, workspace_bytes, false, l);
     if (s != BSQ_OK) return s;
     if (bias && (s = check_out(bias, B->rows, bias_type, B->rows)) != BSQ_OK) return s;
     if (residual && (s = check_out(residual, ld_residual, type, B->rows)) != BSQ_OK) return s;
     if (z && (s = check_out(z, ldz, BSQ_OUT_BF16, B->rows)) != BSQ_OK) return s;
+    if ((s = dense_args(A, B, kDefaultTimeoutNs, a)) != BSQ_OK) return s;
     l.bias = bias;
     l.bias_bf16 = bias_type == BSQ_OUT_BF16;
     l.residual = residual;
@@ -306,14 +308,14 @@ bsq_status bsq_gemm_gated(const bsq_tensor* A, const bsq_tensor* B_gate, const b
                           void* workspace, size_t workspace_bytes, void* stream) {
     bsq::GemmArgs a{}, b{};
     bsq::LinearArgs l{};
-    bsq_status s = fused_common(A, B_gate, activation, h, ldh, type, workspace, workspace_bytes, true, a, l);
+    bsq_status s = fused_common(A, B_gate, activation, h, ldh, type, workspace, workspace_bytes, true, l);
     if (s != BSQ_OK) return s;
     if ((s = check_gemm_pair(A, B_up)) != BSQ_OK) return s;
     if (B_up->fmt != B_gate->fmt || B_up->rows != B_gate->rows || (gate == nullptr) != (up == nullptr)) return BSQ_ERR_INVALID_ARG;
     if (gate && ((s = check_out(gate, ld_gate, BSQ_OUT_BF16, B_gate->rows)) != BSQ_OK ||
                  (s = check_out(up, ld_up, BSQ_OUT_BF16, B_gate->rows)) != BSQ_OK))
         return s;
-    if ((s = dense_args(A, B_up, kDefaultTimeoutNs, b)) != BSQ_OK) return s;
+    if ((s = dense_args(A, B_gate, kDefaultTimeoutNs, a)) != BSQ_OK || (s = dense_args(A, B_up, kDefaultTimeoutNs, b)) != BSQ_OK) return s;
     l.z = gate;
     l.ldz = ld_gate;
     l.u = up;

@@ -132,7 +132,8 @@ bsq_status clip_common(const bsq_grad* grads, int32_t count, bool scale, float m
 bool valid_act(int32_t a) { return a >= BSQ_ACT_IDENTITY && a <= BSQ_ACT_GELU_TANH; }
 bool linear_sizes_ok(int64_t tokens, int64_t out, int64_t cols) { return tokens >= 1 && out >= 1 && cols >= 1; }
 bool linear_sizes_supported(int64_t tokens, int64_t out, int64_t cols) {
-    return tokens <= kMaxRows && out <= bsq::kLinearMaxOut && cols <= kMaxRows;
+    return tokens <= kMaxRows && out <= bsq::kLinearMax && cols <= bsq::kLinearMax && tokens * out <= bsq::kLinearMaxElements &&
+           tokens * cols <= bsq::kLinearMaxElements && out * cols <= bsq::kLinearMaxElements;
 }
 // a matrix that TMA reads or writes, or null
 bsq_status check_tiled(const void* p, int64_t ld, int64_t rows, int64_t cols) {
@@ -161,6 +162,13 @@ bsq_status linear_common(bsq::LinearArgs& a, int64_t tokens, int64_t out, int64_
     a.out = out;
     a.cols = cols;
     a.act = activation;
+    return BSQ_OK;
+}
+// the last check: of the workspace; and what a launch needs of the device
+bsq_status linear_ready(bsq::LinearArgs& a, void* ws, size_t have, size_t need) {
+    const bsq_status s = check_workspace(ws, have, need);
+    if (s != BSQ_OK) return s;
+    a.ws = ws;
     a.num_sms = bsq::device_sms();
     a.status = bsq::device_status();
     a.timeout_ns = kWaitNs;
@@ -406,7 +414,7 @@ bsq_status bsq_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, in
                    check_optional(residual, ld_residual, type, out), check_optional(z, ldz, BSQ_OUT_BF16, out),
                    bias && !aligned(bias, elem(bias_type)) ? BSQ_ERR_ALIGNMENT : BSQ_OK});
     if (s != BSQ_OK) return s;
-    s = check_workspace(workspace, workspace_bytes, linear_bytes(tokens, out, cols, false, false));
+    s = linear_ready(a, workspace, workspace_bytes, linear_bytes(tokens, out, cols, false, false));
     if (s != BSQ_OK) return s;
     a.x = x;
     a.ldx = pitch(ldx, tokens, cols);
@@ -421,7 +429,6 @@ bsq_status bsq_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, in
     a.y_bf16 = type == BSQ_OUT_BF16;
     a.z = z;
     a.ldz = ldz;
-    a.ws = workspace;
     return from_cuda(bsq::run_linear(a, false, static_cast<cudaStream_t>(stream)));
 }
 
@@ -440,7 +447,7 @@ bsq_status bsq_linear_backward(const void* dy, int64_t ld_dy, const void* x, int
                    check_tiled(dx, ld_dx, tokens, cols), check_tiled(dw, ld_dw, out, cols),
                    aligned(dbias, 4) ? BSQ_OK : BSQ_ERR_ALIGNMENT});
     if (s != BSQ_OK) return s;
-    s = check_workspace(workspace, workspace_bytes, linear_bytes(tokens, out, cols, false, true));
+    s = linear_ready(a, workspace, workspace_bytes, linear_bytes(tokens, out, cols, false, true));
     if (s != BSQ_OK) return s;
     a.x = x;
     a.ldx = pitch(ldx, tokens, cols);
@@ -455,7 +462,6 @@ bsq_status bsq_linear_backward(const void* dy, int64_t ld_dy, const void* x, int
     a.dw = dw;
     a.ld_dw = pitch(ld_dw, out, cols);
     a.dbias = dbias;
-    a.ws = workspace;
     return from_cuda(bsq::run_linear_backward(a, false, static_cast<cudaStream_t>(stream)));
 }
 
@@ -471,7 +477,7 @@ bsq_status bsq_gated_linear(const void* x, int64_t ldx, const void* w_gate, int6
                    check_tiled(w_up, ld_up_w, out, cols), check_matrix(h, ldh, type, out),
                    check_optional(gate, ld_gate, BSQ_OUT_BF16, out), check_optional(up, ld_up, BSQ_OUT_BF16, out)});
     if (s != BSQ_OK) return s;
-    s = check_workspace(workspace, workspace_bytes, linear_bytes(tokens, out, cols, true, false));
+    s = linear_ready(a, workspace, workspace_bytes, linear_bytes(tokens, out, cols, true, false));
     if (s != BSQ_OK) return s;
     a.x = x;
     a.ldx = pitch(ldx, tokens, cols);
@@ -486,7 +492,6 @@ bsq_status bsq_gated_linear(const void* x, int64_t ldx, const void* w_gate, int6
     a.ldz = ld_gate;
     a.u = up;
     a.ldu = ld_up;
-    a.ws = workspace;
     return from_cuda(bsq::run_linear(a, true, static_cast<cudaStream_t>(stream)));
 }
 
@@ -508,7 +513,7 @@ bsq_status bsq_gated_linear_backward(const void* dh, int64_t ld_dh, const void* 
                    check_tiled(dx, ld_dx, tokens, cols), check_tiled(dw_gate, ld_dw_gate, out, cols),
                    check_tiled(dw_up, ld_dw_up, out, cols)});
     if (s != BSQ_OK) return s;
-    s = check_workspace(workspace, workspace_bytes, linear_bytes(tokens, out, cols, true, true));
+    s = linear_ready(a, workspace, workspace_bytes, linear_bytes(tokens, out, cols, true, true));
     if (s != BSQ_OK) return s;
     a.x = x;
     a.ldx = pitch(ldx, tokens, cols);
@@ -528,7 +533,6 @@ bsq_status bsq_gated_linear_backward(const void* dh, int64_t ld_dh, const void* 
     a.ld_dw = pitch(ld_dw_gate, out, cols);
     a.dw2 = dw_up;
     a.ld_dw2 = pitch(ld_dw_up, out, cols);
-    a.ws = workspace;
     return from_cuda(bsq::run_linear_backward(a, true, static_cast<cudaStream_t>(stream)));
 }
 

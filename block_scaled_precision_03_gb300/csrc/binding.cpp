@@ -475,11 +475,11 @@ ENTRY(linear_into) {
         const Matrix z = maybe_bf16(a[6], "z", x.rows, w.rows);
         int32_t type;
         const void* bias = bias_of(a[3], w.rows, type);
-        const int32_t act = activation(a[5], BSQ_ACT_IDENTITY);
+        const int32_t act = activation(a[5], BSQ_ACT_IDENTITY), out = type_of(*y.t, "y");
         Launch l(a[7], *x.t);
         const size_t bytes = api.bsq_linear_workspace_bytes(x.rows, w.rows, x.cols);
         check(api.bsq_linear(x.p, x.ld, w.p, w.ld, x.rows, w.rows, x.cols, bias, type, act, r.p, r.ld, y.p, y.ld,
-                             type_of(*y.t, "y"), z.p, z.ld, l.workspace(bytes), bytes, l.stream),
+                             out, z.p, z.ld, l.workspace(bytes), bytes, l.stream),
               "bsq_linear");
         return returned(a[2], a[6]);
     });
@@ -513,11 +513,11 @@ ENTRY(gated_linear_into) {
         const Matrix x = bf16_matrix(a[0], "x"), g = bf16_matrix(a[1], "w_gate", -1, x.cols),
                      u = bf16_matrix(a[2], "w_up", g.rows, x.cols), h = matrix(a[3], "h", x.rows, g.rows);
         const Matrix gate = maybe_bf16(a[5], "gate", x.rows, g.rows), up = maybe_bf16(a[6], "up", x.rows, g.rows);
-        const int32_t act = activation(a[4], BSQ_ACT_SILU);
+        const int32_t act = activation(a[4], BSQ_ACT_SILU), out = type_of(*h.t, "h");
         Launch l(a[7], *x.t);
         const size_t bytes = api.bsq_gated_linear_workspace_bytes(x.rows, g.rows, x.cols);
         check(api.bsq_gated_linear(x.p, x.ld, g.p, g.ld, u.p, u.ld, x.rows, g.rows, x.cols, act, h.p, h.ld,
-                                   type_of(*h.t, "h"), gate.p, gate.ld, up.p, up.ld, l.workspace(bytes), bytes, l.stream),
+                                   out, gate.p, gate.ld, up.p, up.ld, l.workspace(bytes), bytes, l.stream),
               "bsq_gated_linear");
         return returned(a[3], a[5], a[6]);
     });
@@ -588,10 +588,10 @@ ENTRY(gemm_linear_into) {
         const Matrix z = maybe_bf16(a[6], "z", T, N);
         int32_t type;
         const void* bias = bias_of(a[3], N, type);
-        const int32_t act = activation(a[5], BSQ_ACT_IDENTITY);
+        const int32_t act = activation(a[5], BSQ_ACT_IDENTITY), out = type_of(*y.t, "y");
         Launch l(a[7], *qa.codes);
         const size_t bytes = api.bsq_gemm_linear_workspace_bytes(qa.c.fmt, T, N, qa.c.cols);
-        check(api.bsq_gemm_linear(&qa.c, &qb.c, bias, type, act, r.p, r.ld, y.p, y.ld, type_of(*y.t, "y"), z.p, z.ld,
+        check(api.bsq_gemm_linear(&qa.c, &qb.c, bias, type, act, r.p, r.ld, y.p, y.ld, out, z.p, z.ld,
                                   l.workspace(bytes), bytes, l.stream),
               "bsq_gemm_linear");
         return returned(a[2], a[6]);
@@ -605,10 +605,10 @@ ENTRY(gemm_gated_into) {
         const Quantized qa(a[0], "A"), qg(a[1], "B_gate"), qu(a[2], "B_up");
         const int64_t T = qa.c.rows, F = qg.c.rows;
         const Matrix h = matrix(a[3], "h", T, F), gate = maybe_bf16(a[5], "gate", T, F), up = maybe_bf16(a[6], "up", T, F);
-        const int32_t act = activation(a[4], BSQ_ACT_SILU);
+        const int32_t act = activation(a[4], BSQ_ACT_SILU), out = type_of(*h.t, "h");
         Launch l(a[7], *qa.codes);
         const size_t bytes = api.bsq_gemm_gated_workspace_bytes(qa.c.fmt, T, F, qa.c.cols);
-        check(api.bsq_gemm_gated(&qa.c, &qg.c, &qu.c, act, h.p, h.ld, type_of(*h.t, "h"), gate.p, gate.ld, up.p, up.ld,
+        check(api.bsq_gemm_gated(&qa.c, &qg.c, &qu.c, act, h.p, h.ld, out, gate.p, gate.ld, up.p, up.ld,
                                  l.workspace(bytes), bytes, l.stream),
               "bsq_gemm_gated");
         return returned(a[3], a[5], a[6]);

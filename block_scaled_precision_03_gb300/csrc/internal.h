@@ -206,7 +206,8 @@ struct LinearArgs {
     unsigned* status;
     uint64_t timeout_ns;
 };
-constexpr int64_t kLinearMaxOut = 1ll << 24;       // the columns of a grid's second dimension
+constexpr int64_t kLinearMax = 1ll << 23;          // out and cols (a grid's second dimension counts 256 columns)
+constexpr int64_t kLinearMaxElements = 1ll << 44;  // of any matrix: fewer than 2^31 tiles
 size_t linear_workspace(int64_t tokens, int64_t out, int64_t cols, bool gated, int num_sms);
 size_t linear_backward_workspace(int64_t tokens, int64_t out, int64_t cols, bool gated, int num_sms);
 cudaError_t run_linear(const LinearArgs& a, bool gated, cudaStream_t st);

@@ -428,8 +428,8 @@ size_t bsq_gated_linear_backward_workspace_bytes(int64_t tokens, int64_t out, in
 /* z = x w^T + bias, y = act(z) + residual, in the product's epilogue.
  * x: BF16 [tokens, cols], w: BF16 [out, cols], both on 16-byte boundaries
  * with cols, ldx and ldw multiples of 8 (BSQ_ERR_ALIGNMENT otherwise; the
- * pitch of a single row says nothing); any tokens and out up to 2^31 - 256 and
- * 2^24.  bias: DEVICE [out] of `bias_type` (bsq_out) or NULL.  residual:
+ * pitch of a single row says nothing); tokens up to 2^31 - 256, out and cols up to
+ * 2^23, no matrix of more than 2^44 elements.  bias: DEVICE [out] of `bias_type` (bsq_out) or NULL.  residual:
  * [tokens, out] of y's type or NULL; y may be residual itself (same pointer and
  * pitch).  y: [tokens, out] of `type` (bsq_out).  z: BF16 [tokens, out] for the
  * backward pass, or NULL.  FP32 sums on the tensor cores; z, act and the
@@ -442,7 +442,8 @@ bsq_status bsq_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, in
 /* Gradient of bsq_linear for dy: BF16 [tokens, out] (the residual's gradient is
  * dy itself), with z as the forward call left it (BF16; not read, and may be
  * NULL, with BSQ_ACT_IDENTITY):
- *   dz = dy act'(z), rounded to BF16 for the two products
+ *   dz = dy act'(z), rounded to BF16 for the two products (not where there are
+ *        up to 4 tokens, or little to sum)
  *   dx = dz w      BF16 [tokens, cols]
  *   dw = dz^T x    BF16 [out, cols]
  *   dbias = the sum of dz's rows, before that rounding   DEVICE float[out]
@@ -466,7 +467,7 @@ bsq_status bsq_gated_linear(const void* x, int64_t ldx, const void* w_gate, int6
 
 /* Gradient of bsq_gated_linear for dh: BF16 [tokens, out], with gate and up as
  * the forward call left them:
- *   dgate = dh up act'(gate), dup = dh act(gate), rounded to BF16 for the products
+ *   dgate = dh up act'(gate), dup = dh act(gate), rounded as dz there
  *   dx = dgate w_gate + dup w_up, dw_gate = dgate^T x, dw_up = dup^T x (BF16)
  * dx may be NULL (then w_gate and w_up may be), and so may dw_gate and dw_up
  * together (then x may be); alignments as for bsq_linear_backward. */
@@ -482,7 +483,7 @@ size_t bsq_gemm_linear_workspace_bytes(int32_t fmt, int64_t tokens, int64_t out,
 size_t bsq_gemm_gated_workspace_bytes(int32_t fmt, int64_t tokens, int64_t out, int64_t cols);
 
 /* bsq_gemm with the epilogue of bsq_linear: z = A B^T + bias, y = act(z) +
- * residual.  Operands, formats and limits as for bsq_gemm; bias, residual, y
+ * residual.  Operands and formats as for bsq_gemm, B.rows up to 2^23; bias, residual, y
  * and z as for bsq_linear (A.rows tokens, B.rows out). */
 bsq_status bsq_gemm_linear(const bsq_tensor* A, const bsq_tensor* B, const void* bias, int32_t bias_type,
                            int32_t activation, const void* residual, int64_t ld_residual, void* y, int64_t ldy,
@@ -490,7 +491,7 @@ bsq_status bsq_gemm_linear(const bsq_tensor* A, const bsq_tensor* B, const void*
 
 /* bsq_gated_linear on block-scaled operands: gate = A B_gate^T, up = A B_up^T,
  * h = act(gate) * up.  B_gate and B_up have one format and one shape; operands
- * and limits as for bsq_gemm. */
+ * and limits as for bsq_gemm_linear. */
 bsq_status bsq_gemm_gated(const bsq_tensor* A, const bsq_tensor* B_gate, const bsq_tensor* B_up, int32_t activation,
                           void* h, int64_t ldh, int32_t type, void* gate, int64_t ld_gate, void* up, int64_t ld_up,
                           void* workspace, size_t workspace_bytes, void* stream);
