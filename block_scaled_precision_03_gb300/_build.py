@@ -23,7 +23,7 @@ LIB = os.path.join(HERE, "libbsq.so")
 BINDING = os.path.join(HERE, "_binding.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["api.cu", "quantize.cu", "convert.cu", "gemm.cu", "gemm2.cu", "api_ops.cu", "moe.cu",
-           "norm.cu", "head.cu", "linear.cu", "clip.cu", "adamw.cu"]
+           "norm.cu", "head.cu", "linear.cu", "gemv.cu", "clip.cu", "adamw.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -264,6 +264,22 @@ __device__ __forceinline__ void store_chunk(const float (&v)[32], int bf16, int 
     }
 }
 
+// One element, of one token: sum (and of a gated layer up's) becomes z and y, or gate, up and h
+template <bool GATED>
+__device__ __forceinline__ void finish_one(float z, float u, const Fused& f, int64_t t, int64_t feature) {
+    if (!GATED && f.bias) z += load_as_float(f.bias, feature, f.bias_bf16);
+    if (f.z) {
+        f.z[t * f.ldz + feature] = __float2bfloat16_rn(z);
+        if (GATED) f.u[t * f.ldu + feature] = __float2bfloat16_rn(u);
+    }
+    float v[1] = {z};
+    activate(f.act, v);
+    float y = GATED ? v[0] * u : v[0];
+    if (!GATED && f.residual) y += load_as_float(f.residual, t * f.ld_res + feature, f.y_bf16);
+    if (f.y_bf16) static_cast<__nv_bfloat16*>(f.y)[t * f.ldy + feature] = __float2bfloat16_rn(y);
+    else static_cast<float*>(f.y)[t * f.ldy + feature] = y;
+}
+
 // 32 columns of a linear layer's sums become z, y
 template <int BUFS>
 __device__ __forceinline__ void finish_linear(float (&v)[32], const Fused& f, const void* tm_y, const void* tm_z, int64_t row0,

@@ -867,6 +867,7 @@ cudaError_t launch_kind(const Setup& s, const CUtensorMap& tc_, const More& more
 // a: the tokens and w, or the gate's weights; up: the tokens and up's weights
 template <bool GATED>
 cudaError_t fused(const GemmArgs& a, const GemmArgs& up, const LinearArgs& l, cudaStream_t st) {
+    if (a.M <= kScaledGemvTokens) return run_scaled_gemv(a, up, l, GATED, st);
     const bool few = a.M <= kFewTokens;
     GemmArgs q = a;
     if (few) {
@@ -934,6 +935,7 @@ int gemm_fused_splits(int fmt, int64_t tokens, int64_t out, int64_t cols, bool g
     return fused_splits(tiles, (cols + 255) / 256, us, (double)tokens * fused_acc_cols(out, gated) * 8, num_sms / 2);
 }
 size_t gemm_fused_workspace(int fmt, int64_t tokens, int64_t out, int64_t cols, bool gated, int num_sms) {
+    if (tokens <= kScaledGemvTokens) return 0;
     const int n = gemm_fused_splits(fmt, tokens, out, cols, gated, num_sms);
     return n > 1 || (gated && tokens <= kFewTokens) ? (size_t)n * tokens * fused_acc_cols(out, gated) * 4 : 0;
 }

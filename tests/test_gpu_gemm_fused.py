@@ -11,7 +11,7 @@ from _ops_ref import Guard, assert_close, strided
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
 FORMATS = [("mxfp8_e4m3", "mxfp8_e4m3"), ("mxfp8_e5m2", "mxfp8_e4m3"), ("mxfp4", "mxfp4"), ("nvfp4", "nvfp4")]
-SIZES = [(1, 5, 32), (3, 130, 96), (1, 4096, 8192), (130, 257, 544), (257, 384, 1024), (300, 1000, 4128), (700, 264, 256)]
+SIZES = [(1, 5, 32), (3, 130, 96), (2, 70, 1056), (1, 4096, 8192), (4, 300, 4128), (5, 40, 64), (100, 700, 2080), (130, 257, 544), (257, 384, 1024), (300, 1000, 4128), (700, 264, 256)]
 
 
 @pytest.fixture(scope="module")
@@ -74,6 +74,23 @@ def test_gemm_gated(bsq, T, N, K, fa, fb):
             assert_close(u, uw, ut, "up")
             Guard(a, abuf).check()
             Guard(u, ubuf).check()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8_e4m3", "mxfp8_e5m2", "mxfp4"])
+@pytest.mark.parametrize("T", [1, 4, 9, 200])
+def test_scales_far_from_one(bsq, fmt, T):
+    # one operand's scales near 2^100, the other's near 2^-100, and a row whose scales are NaN
+    g = torch.Generator(device="cuda").manual_seed(5)
+    A, x = quantized(bsq, g, T, 96, fmt, 2.0 ** 100)
+    v = torch.randn((140, 96), generator=g, device="cuda") * 2.0 ** -100
+    v[7, 40] = float("nan")
+    B, _ = bsq.quantize(v.to(BF), fmt)
+    w = bsq.dequantize(B)
+    got = bsq.gemm_linear(A, B, out_dtype=F32)
+    assert torch.isnan(got[:, 7]).all()
+    rows = [i for i in range(140) if i != 7]
+    want, tol, _, _ = linear_ref(x.double(), w[rows].double(), None, None, "identity", F32)
+    assert_close(got[:, rows], want, tol)
 
 
 @pytest.mark.parametrize("fmt", ["mxfp8_e4m3", "mxfp4", "nvfp4"])
