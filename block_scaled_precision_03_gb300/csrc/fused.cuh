@@ -118,7 +118,7 @@ __device__ __forceinline__ F2 act_slope(F2 z, F2& value) {
         value = z * s;
         const float2 q = (z * z).get();                                // (finite: 0 times it is 0)
         const F2 p = fma2(F2(3.0f * kGeluA), F2(fminf(q.x, 1e30f), fminf(q.y, 1e30f)), F2(1.0f));
-        return fma2(value * F2(2.0f * kGeluC) * fma2(s, F2(-1.0f), F2(1.0f)), p, s);
+        return fma2(value * fma2(s, F2(-1.0f), F2(1.0f)) * F2(2.0f * kGeluC), p, s);
     }
     return F2(1.0f);
 }
@@ -321,8 +321,9 @@ int64_t fused_acc_cols(int64_t N, bool gated);
 // the parts that get any of `stages`, dealt to n
 int fused_parts(int64_t stages, int64_t n);
 // How many parts: more than one where there are fewer tiles than pairs, or few in the last wave.  The estimate: what
-// the busiest pair computes, and that each part's FP32 tile is written and read.
-int fused_splits(int64_t tiles, int64_t stages, double stage_us, double part_bytes, int pairs);
+// the busiest pair computes (tile_us: what a tile costs besides its stages), and that each part's FP32 tile is written
+// and read.
+int fused_splits(int64_t tiles, int64_t stages, double stage_us, double tile_us, double part_bytes, int pairs);
 // adds the parts in their order and does the epilogue; starts beside the kernel before it
 cudaError_t run_linear_join(const float* acc, int splits, int64_t M, int64_t N, bool gated, const LinearArgs& a, cudaStream_t st);
 

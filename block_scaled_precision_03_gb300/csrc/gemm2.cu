@@ -926,13 +926,13 @@ cudaError_t fused(const GemmArgs& a, const GemmArgs& up, const LinearArgs& l, cu
 }  // namespace
 
 // parts of the sum over K: a stage (K = 256) takes 0.4 us of MXFP8 or MXFP4, 0.45 of NVFP4; with few tokens it is
-// the pair's share of the weights' stream
+// the pair's share of the weights' stream; between two tiles the one accumulator is read out
 int gemm_fused_splits(int fmt, int64_t tokens, int64_t out, int64_t cols, bool gated, int num_sms) {
     const bool few = tokens <= kFewTokens, fp4 = fmt >= kMXFP4;
     const int64_t tiles = few ? (out + 255) / 256 * (gated ? 2 : 1)
                               : (tokens + 255) / 256 * ((out + (gated ? 127 : 255)) / (gated ? 128 : 256));
     const double us = few ? (fp4 ? 0.45 : 0.82) : fmt == kNVFP4 ? 0.45 : 0.4;
-    return fused_splits(tiles, (cols + 255) / 256, us, (double)tokens * fused_acc_cols(out, gated) * 8, num_sms / 2);
+    return fused_splits(tiles, (cols + 255) / 256, us, 1.5, (double)tokens * fused_acc_cols(out, gated) * 8, num_sms / 2);
 }
 size_t gemm_fused_workspace(int fmt, int64_t tokens, int64_t out, int64_t cols, bool gated, int num_sms) {
     if (tokens <= kScaledGemvTokens) return 0;

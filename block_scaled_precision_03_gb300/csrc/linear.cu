@@ -985,7 +985,7 @@ Cut wide_cut(int64_t m_tiles, int64_t cols, double per, int64_t stages, double p
     for (const auto& w : kWidths) {
         if (w.n < least) break;
         const int64_t tiles = m_tiles * div_up(cols, (int64_t)(w.n * per));
-        const int splits = fused_splits(tiles, stages, w.stage_us, part_bytes, pairs);
+        const int splits = fused_splits(tiles, stages, w.stage_us, 0.0, part_bytes, pairs);
         const double us = (double)div_up(tiles * splits, pairs) * div_up(stages, splits) * w.stage_us + w.end_us +
                           (splits > 1 ? 2.0 + splits * part_bytes / 6.7e6 : 0.0);
         if (fewest == 0.0 || us < fewest) {
@@ -1271,12 +1271,12 @@ int fused_parts(int64_t stages, int64_t n) {
     const int64_t per = div_up(stages, n);
     return (int)div_up(stages, per);
 }
-int fused_splits(int64_t tiles, int64_t stages, double stage_us, double part_bytes, int pairs) {
+int fused_splits(int64_t tiles, int64_t stages, double stage_us, double tile_us, double part_bytes, int pairs) {
     int64_t best = 1;
     double least = 0.0;
     pairs = std::max(1, pairs);
     for (int64_t n = 1; n == 1 || (n * 4 <= stages && n * tiles <= 8 * pairs); n++) {
-        const double us = (double)div_up(tiles * n, pairs) * div_up(stages, n) * stage_us + (n > 1 ? 2.0 + n * part_bytes / 6.7e6 : 0.0);
+        const double us = (double)div_up(tiles * n, pairs) * (div_up(stages, n) * stage_us + tile_us) + (n > 1 ? 2.0 + n * part_bytes / 6.7e6 : 0.0);
         if (n == 1 || us < least) {
             least = us;
             best = n;

@@ -192,6 +192,49 @@ def test_calls_in_any_order_without_waiting(bsq, streams):
             assert same(got[i], want[i]), i
 
 
+@pytest.mark.parametrize("T,D", [(1, 2048), (2, 1024), (4, 1024), (20, 1024), (60, 64), (200, 512), (600, 512)])
+def test_every_call_reads_what_the_one_before_wrote(bsq, T, D):
+    # calls that start beside the one before them, each on its results, over two buffers that are written again and
+    # again: the same as with a wait after each of them
+    g = torch.Generator(device="cuda").manual_seed(T)
+    w = [(torch.randn((D, D), generator=g, device="cuda") * D ** -0.5).to(BF) for _ in range(3)]
+    start = torch.randn((T, D), generator=g, device="cuda").to(BF)
+
+    def chain(wait):
+        a, b, c, dw = start.clone(), torch.empty_like(start), torch.empty_like(start), torch.empty_like(w[0])
+        weights = [t.clone() for t in w]
+        lists = bsq.AdamWList(weights, [dw] * 3, 8)
+        q = bsq.empty("mxfp8_e4m3", T, D)
+        qw = bsq.empty("mxfp8_e4m3", D, D)
+        for k in range(1, 16):
+            bsq.linear_into(a, weights[0], b, None, a, "gelu")
+            wait()
+            bsq.gated_linear_into(b, weights[1], weights[2], a)
+            wait()
+            bsq.linear_backward_into(a, b, weights[0], c, dw)
+            wait()
+            bsq.adamw_step(lists, 1e-2, k, weight_decay=0.1, seed=1)
+            wait()
+            bsq.layer_norm_into(c, None, None, 1e-5, b)
+            wait()
+            bsq.quantize_into(b, "mxfp8_e4m3", "row", q, None)
+            bsq.quantize_into(weights[k % 3], "mxfp8_e4m3", "row", qw, None)
+            wait()
+            bsq.gemm_linear_into(q, qw, a)
+            wait()
+            bsq.gemm_gated_into(q, qw, qw, b)
+            wait()
+            bsq.layer_norm_into(b, None, None, 1e-5, a)
+            wait()
+        torch.cuda.synchronize()
+        return [a, b, c, dw, *weights]
+
+    want = chain(torch.cuda.synchronize)
+    assert all(torch.isfinite(t).all() for t in want)
+    for _ in range(4):
+        assert same(chain(lambda: None), want)
+
+
 def test_forward_and_backward_are_those_of_autograd(bsq):
     # the formulas once more, as torch differentiates them
     i = inputs(130, 64, 72)

@@ -195,6 +195,44 @@ def test_large_values(bsq, name):
     assert_close(bsq.linear_backward(dy, x, eye, x, name)[0], xr, xt, name)
 
 
+@pytest.mark.parametrize("name", ACTS)
+def test_the_types_lowest_and_highest_values(bsq, name):
+    # pre-activations at BF16's ends: the activation is 0 or the value itself, its slope 0 or 1
+    top = torch.finfo(BF).max
+    v = torch.tensor([-top, -1e30, 1e30, top], dtype=BF, device="cuda").repeat(20)
+    n = v.numel()
+    x = torch.zeros((n, n), dtype=BF, device="cuda")
+    x.diagonal().copy_(v)
+    eye = torch.eye(n, dtype=BF, device="cuda")
+    want = v.float() if name == "identity" else v.float().clamp(min=0)
+    for T in (1, 3, n):
+        got = bsq.linear(x[:T], eye, None, None, name, F32)
+        assert torch.equal(got.diagonal(), want[:T]) and int((got != 0).sum()) == int((want[:T] != 0).sum())
+        dx = bsq.linear_backward(torch.ones((T, n), dtype=BF, device="cuda"), x[:T], eye, x[:T].contiguous(), name)[0]
+        slope = torch.ones(n, device="cuda") if name == "identity" else (v > 0).float()
+        assert torch.equal(dx.float().diagonal(), slope[:T])
+
+
+# what the choice of a kernel goes by: 4 and 5, 16 and 17, 128 and 129 tokens, products of 4096 and 16384 elements
+@pytest.mark.parametrize("T,N,K", [(4, 5, 8), (5, 1, 8), (5, 3276, 64), (5, 3277, 64), (16, 1024, 200), (17, 240, 72), (17, 241, 72),
+                                   (128, 1, 16), (128, 32, 1000), (128, 33, 32), (129, 1, 8), (129, 32, 32), (300, 3, 8), (4, 8000, 1032)])
+def test_sizes_at_the_borders(bsq, T, N, K):
+    g = gen(T, N, K, 77)
+    x, w, v = operands(g, T, N, K, 2)
+    bias = randn(g, N, dtype=F32)
+    want, tol, _, _ = linear_ref(x, w, bias, None, "gelu_tanh", BF)
+    assert_close(bsq.linear(x, w, bias, None, "gelu_tanh"), want, tol, "y")
+    want, tol, *_ = gated_ref(x, w, v, "silu", BF)
+    assert_close(bsq.gated_linear(x, w, v), want, tol, "h")
+    dy, a, b = (randn(g, T, N) for _ in range(3))
+    want = linear_grad_ref(dy, x, w, a, "gelu")
+    for got, r, t, what in zip(bsq.linear_backward(dy, x, w, a, "gelu"), want[::2], want[1::2], ("dx", "dw", "dbias")):
+        assert_close(got, r, t, what)
+    want = gated_grad_ref(dy, x, w, v, a, b, "silu")
+    for got, r, t, what in zip(bsq.gated_linear_backward(dy, x, w, v, a, b), want[::2], want[1::2], ("dx", "dw_gate", "dw_up")):
+        assert_close(got, r, t, what)
+
+
 def test_gradients_against_differences(bsq):
     # the loss sum(c * f) of the forward calls in FP64, moved along a direction
     from _linear_ref import act
