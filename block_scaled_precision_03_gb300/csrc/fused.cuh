@@ -214,23 +214,35 @@ __device__ __forceinline__ void store_chunk(const float (&v)[32], int bf16, int 
             w[j] = *reinterpret_cast<const uint32_t*>(&h);
         }
         const uint32_t buf = st.next(lane);
-        pair::stage_chunk(w, buf, lane);
         if (tma == kWhole || (tma && col + 32 <= N)) {
+            pair::stage_chunk(w, buf, lane);
             if (lane == 0) {
                 tc::tma_store_2d(tmap, (int)col, (int)row0, buf);
                 tc::bulk_commit();
             }
             return;
         }
-        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out) + row0 * ld + col;
+        // (not through the asynchronous proxy, whose fence would wait for the stores of the chunk before)
+        pair::put_chunk(w, buf, lane);
+        __syncwarp();
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out) + row0 * ld + col + lane;
         const int rows = (int)min((int64_t)32, M - row0);
-#pragma unroll 8
-        for (int r = 0; r < 32; r++) {
-            uint16_t x;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x)
-                         : "r"(buf + (uint32_t)r * 64u + ((((uint32_t)lane >> 3) ^ ((uint32_t)(r >> 1) & 3u)) << 4) + ((uint32_t)lane & 7u) * 2u)
-                         : "memory");
-            if (r < rows && col + lane < N) o[r * ld + lane] = __ushort_as_bfloat16(x);
+        const bool in = col + lane < N;
+        // where the lane's column is in rows 0 and 1, 2 and 3, 4 and 5, 6 and 7 of every eight
+        uint32_t at[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++) at[k] = buf + ((((uint32_t)lane >> 3) ^ k) << 4) + ((uint32_t)lane & 7u) * 2u;
+#pragma unroll 1
+        for (int r = 0; r < rows; r += 8) {
+            uint16_t x[8];
+#pragma unroll
+            for (int k = 0; k < 8; k++)
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x[k]) : "r"(at[k >> 1] + (uint32_t)(r + k) * 64u) : "memory");
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                if (in && r + k < rows) *o = __ushort_as_bfloat16(x[k]);
+                o += ld;
+            }
         }
         __syncwarp();
         return;
@@ -241,24 +253,34 @@ __device__ __forceinline__ void store_chunk(const float (&v)[32], int bf16, int 
 #pragma unroll
         for (int j = 0; j < 16; j++) w[j] = __float_as_uint(v[c + j]);
         const uint32_t buf = st.next(lane);
-        pair::stage_chunk(w, buf, lane);
         if (tma == kWhole || (tma && col + c + 16 <= N)) {
+            pair::stage_chunk(w, buf, lane);
             if (lane == 0) {
                 tc::tma_store_2d(tmap, (int)col + c, (int)row0, buf);
                 tc::bulk_commit();
             }
             continue;
         }
-        float* o = static_cast<float*>(out) + row0 * ld + col + c;
-        const int rows = (int)min((int64_t)32, M - row0), k = lane & 15;
-#pragma unroll 8
-        for (int i = 0; i < 16; i++) {
-            const int r = 2 * i + (lane >> 4);
-            float x;
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x)
-                         : "r"(buf + (uint32_t)r * 64u + ((((uint32_t)k >> 2) ^ ((uint32_t)(r >> 1) & 3u)) << 4) + ((uint32_t)k & 3u) * 4u)
-                         : "memory");
-            if (r < rows && col + c + k < N) o[r * ld + k] = x;
+        pair::put_chunk(w, buf, lane);
+        __syncwarp();
+        const int k0 = lane & 15, r0 = lane >> 4;
+        float* o = static_cast<float*>(out) + (row0 + r0) * ld + col + c + k0;
+        const int rows = (int)min((int64_t)32, M - row0);
+        const bool in = col + c + k0 < N;
+        uint32_t at[4];                            // rows 2 k and 2 k + 1 of every eight
+#pragma unroll
+        for (int k = 0; k < 4; k++) at[k] = buf + (uint32_t)r0 * 64u + ((((uint32_t)k0 >> 2) ^ k) << 4) + ((uint32_t)k0 & 3u) * 4u;
+#pragma unroll 1
+        for (int r = 0; r < rows; r += 8) {
+            float x[4];
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x[k]) : "r"(at[k] + (uint32_t)(r + 2 * k) * 64u) : "memory");
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                if (in && r + 2 * k + r0 < rows) *o = x[k];
+                o += 2 * ld;
+            }
         }
         __syncwarp();
     }

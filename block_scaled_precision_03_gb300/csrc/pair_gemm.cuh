@@ -72,13 +72,16 @@ __device__ __forceinline__ void tma_store_3d(const void* tmap, int32_t x, int32_
 // BF16 or 16 FP32 columns) through two 2 KB staging buffers laid out with the
 // 64-byte swizzle (16-byte unit u of row r at unit u ^ ((r >> 1) & 3)), one
 // TMA tile store each; `n` counts the warp's chunks.
-__device__ __forceinline__ void stage_chunk(const uint32_t (&w)[16], uint32_t buf, int lane) {
+__device__ __forceinline__ void put_chunk(const uint32_t (&w)[16], uint32_t buf, int lane) {
     const uint32_t row = buf + (uint32_t)lane * 64u, sw = (uint32_t)((lane >> 1) & 3);
 #pragma unroll
     for (int u = 0; u < 4; u++)
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
                      :: "r"(row + ((u ^ sw) << 4)), "r"(w[4 * u]), "r"(w[4 * u + 1]), "r"(w[4 * u + 2]), "r"(w[4 * u + 3])
                      : "memory");
+}
+__device__ __forceinline__ void stage_chunk(const uint32_t (&w)[16], uint32_t buf, int lane) {
+    put_chunk(w, buf, lane);
     tc::fence_async_smem();
     __syncwarp();
 }
