@@ -53,7 +53,7 @@ enum { kFwd, kFew, kDx, kDw };
 enum { kWaitStart, kWaitEnd };
 
 constexpr int kStages = 3;
-constexpr int kMaxStages = 6;                       // few tokens: as many as fit
+constexpr int kMaxStages = 6;                       // of narrower tiles: as many as fit
 constexpr int kFewTokens = 128;
 constexpr int kChunk = 4, kSumChunk = 128;          // stages of K = 128 (few tokens, gated: twice as many of 64)
 constexpr int kSubBytes = 128 * kSubK * 2;          // one CTA's 128 rows of an operand, one sub-step
@@ -101,7 +101,7 @@ linear_gemm_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Para
     // [stages] of A, [stages] of B, the epilogue's staging; the barriers come last
     constexpr bool FEW = MODE == kFew;
     constexpr int SUB_B = FEW && GATED ? 1 : kSub;             // sub-steps of B in a stage
-    const int S = FEW ? p.stages : kStages, b_bytes = FEW ? p.b_bytes : kOpBytes, sub_b = b_bytes / SUB_B;    // (places, not sizes)
+    const int S = p.stages, b_bytes = p.b_bytes, sub_b = b_bytes / SUB_B;
     uint8_t* smA = base;
     uint8_t* smB = smA + S * kOpBytes;
     uint8_t* smOut = base + kStages * 2 * kOpBytes;
@@ -948,7 +948,6 @@ __global__ void __launch_bounds__(256) linear_bias_kernel(const float* sums, int
 }
 
 // How a product is cut: rows of a pair (few tokens), and parts of the sum over K.
-constexpr int64_t kResident = 60ll << 20;          // (see choose_raster: 40 MB took 1% longer for 8192 x 14336 -> 4096, 80 MB 2%)
 constexpr double kStageUs = 0.55;                   // a pair's stage of K = 128
 struct Cut {
     bool few;
@@ -1035,7 +1034,7 @@ cudaError_t gemm(Params p, const Operand (&a)[2], const Operand (&b)[2], Maps& t
     p.tile_m = cut.tile_m;
     p.tile_n = tile_n;
     p.b_bytes = (FEW && GATED ? 1 : kSub) * (tile_n / 2) * kSubK * 2;
-    p.stages = FEW ? std::min(kMaxStages, kStages * 2 * kOpBytes / (kOpBytes + p.b_bytes)) : kStages;
+    p.stages = std::min(kMaxStages, kStages * 2 * kOpBytes / (kOpBytes + p.b_bytes));
     p.tx = (uint32_t)(kSub * (cut.tile_m / 2) * kSubK * 2 + p.b_bytes);
     p.m_tiles = (int32_t)div_up(p.M, cut.tile_m) * (MODE == kDw && GATED ? 2 : 1);
     p.n_tiles = (int32_t)div_up(p.N, MODE == kFwd && GATED ? tile_n / 2 : tile_n);
@@ -1049,7 +1048,7 @@ cudaError_t gemm(Params p, const Operand (&a)[2], const Operand (&b)[2], Maps& t
     p.status = args.status;
     p.timeout_ns = args.timeout_ns;
     const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(args.num_sms / 2, total));
-    choose_raster(p, K, pairs, kResident);
+    choose_raster(p, K, pairs);
     if constexpr (!FEW)
         if (p.split_stages <= p.chunk) return launch_gemm<MODE, GATED, false>(p, tm, pairs, st);
     return launch_gemm<MODE, GATED, true>(p, tm, pairs, st);

@@ -239,7 +239,7 @@ inline bool map_acc(CUtensorMap* m, float* p, int64_t splits, int64_t rows, int6
 // 16 row tiles 2.451 ms, 12 2.481, 24 2.458, and 8 or 32 (67 MB, which do not
 // stay) 4 to 6% slower.
 template <typename P>
-void choose_raster(P& p, int64_t K, int pairs, int64_t resident = kL2Resident) {
+void choose_raster(P& p, int64_t K, int pairs) {
     const double strip_a = 512.0 * K, strip_b = 2.0 * p.tile_n * K;
     const double a_bytes = strip_a * p.m_tiles, b_bytes = strip_b * p.n_tiles;
     const double waves = (double)p.m_tiles * p.n_tiles / pairs;
@@ -250,7 +250,7 @@ void choose_raster(P& p, int64_t K, int pairs, int64_t resident = kL2Resident) {
         for (int most = 1; most <= std::min(tiles, 2 * pairs); most++) {
             const int groups = (tiles + most - 1) / most, g = (tiles + groups - 1) / groups;
             const double across = std::min<double>(others, std::max(1.0, (double)pairs / g));
-            const double bytes = g * own <= (double)resident
+            const double bytes = g * own <= (double)kL2Resident
                                      ? (along_n ? b_bytes : a_bytes) + groups * (along_n ? a_bytes : b_bytes)
                                      : waves * (std::min(g, pairs) * own + across * other);
             if (best == 0.0 || bytes < best) {
