@@ -188,7 +188,8 @@ __device__ __forceinline__ void add_row(float (&v)[32], const void* p, int64_t a
         if (j < n) v[j] += load_as_float(p, at + j, bf16);
 }
 
-// A warp's staging: BUFS buffers of 2 KB, used in turn; `n` counts the chunks.
+// A warp's staging: BUFS buffers of 2 KB, used in turn; `n` counts the chunks.  Every chunk is a bulk group, an empty one
+// where no TMA store reads it, so that the groups before the last BUFS - 1 are the buffer's own store too.
 template <int BUFS>
 struct Staging {
     uint32_t base;
@@ -244,6 +245,7 @@ __device__ __forceinline__ void store_chunk(const float (&v)[32], int bf16, int 
                 o += ld;
             }
         }
+        if (lane == 0) tc::bulk_commit();
         __syncwarp();
         return;
     }
@@ -282,6 +284,7 @@ __device__ __forceinline__ void store_chunk(const float (&v)[32], int bf16, int 
                 o += 2 * ld;
             }
         }
+        if (lane == 0) tc::bulk_commit();
         __syncwarp();
     }
 }

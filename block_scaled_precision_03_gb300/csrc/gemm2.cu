@@ -575,13 +575,13 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
             if constexpr (EPI == kFewLinear || EPI == kFewGated) {
                 // a thread owns one feature; neighbouring lanes write neighbouring features of a token
                 const int feature = row0 + lane;
-                if (h != 0 || feature >= p.M) continue;
+                const bool in = feature < p.M;         // (the warp stays together: it reads tensor memory next)
                 const float a2 = EPI == kFewGated && ti.which ? beta2 : alpha;
                 const bool whole = EPI == kFewLinear && more.splits == 1;
                 const Fused& f = more.f;
-                const float bias = whole && f.bias ? load_as_float(f.bias, feature, f.bias_bf16) : 0.0f;
+                const float bias = whole && f.bias && in ? load_as_float(f.bias, feature, f.bias_bf16) : 0.0f;
 #pragma unroll 1
-                for (int c = 0; c < p.N; c += 32) {
+                for (int c = 0; c < (h == 0 ? p.N : 0); c += 32) {
                     float v[32];
 #pragma unroll
                     for (int j = 0; j < 32; j++) {
@@ -590,7 +590,7 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
                         r[1][j] = r[2][j];
                         r[2][j] = r[3][j];
                     }
-                    const int n = min(32, p.N - c);
+                    const int n = in ? min(32, p.N - c) : 0;
                     if (!whole) {
                         float* to = more.acc + ((int64_t)pt.split * p.N + c) * more.ld_acc +
                                     (EPI == kFewGated ? gate_col(feature) + 128 * ti.which : feature);
@@ -613,6 +613,7 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
                             else static_cast<float*>(f.y)[(c + j) * f.ldy + feature] = y;
                         }
                 }
+                __syncwarp();
                 continue;
             } else if constexpr (EPI != kPlain) {
                 const int col0 = EPI == kGated ? ti.nt * 128 + h * 64 : ti.nt * BN + h * 128;

@@ -340,6 +340,7 @@ linear_gemm_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Para
 #pragma unroll
                         for (int j = 0; j < 48; j++) z[i][j] = z[i][j + 16];
                 }
+                __syncwarp();
             }
         } else {
             // A thread owns one row and 128 of the tile's columns (gated: 64 of each projection's)

@@ -269,7 +269,8 @@ bsq_status bsq_mxfp4_to_fp8_1x128(const bsq_tensor* in_mxfp4, void* out_codes, v
  *    BF16), its shape and `ld`, the distance between two rows in ELEMENTS
  *    (ld >= cols; the last axis is contiguous).  Any ld and any address that
  *    is a multiple of the element size is valid; rows that start on 16-byte
- *    boundaries are faster.  The linear cross entropy asks for 16-byte rows.
+ *    boundaries are faster.  The linear cross entropy and the operands of the
+ *    linear layers ask for 16-byte rows.
  *  - Inputs and outputs may not overlap unless a call says so.
  *  - Sums, statistics and softmax terms are held in FP32 (the global norm in
  *    FP64); a BF16 result is rounded once, at its store.  No result depends
@@ -535,7 +536,8 @@ typedef enum { BSQ_MOMENTS_F32 = 0, BSQ_MOMENTS_8BIT = 1 } bsq_moments;
  *   BSQ_MOMENTS_8BIT  m, v: n E4M3 codes, m_scales, v_scales: ceil(n / 32) E8M0
  *                     bytes, one for 32 elements; v's codes hold its square root
  * A tensor of zeros is the start of either (codes and scales).  `copy`: BF16[n],
- * the new parameters rounded to nearest, or NULL.  No two tensors overlap.
+ * the new parameters, before their own rounding, rounded to nearest, or NULL.  No two
+ * tensors overlap.
  * Elements of any address that is a multiple of their size; 16-byte boundaries
  * (codes: 8) are faster. */
 typedef struct {

@@ -162,6 +162,32 @@ def test_sums_of_whole_numbers(bsq, T, N, K):
     assert torch.equal(du, (d.double().T @ x.double()).float().to(BF))
 
 
+# which of the outputs are on 16-byte rows (bit 0: y or h, 1: z or gate, 2: up): a warp's stores go two ways in turn
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows16", range(8))
+@pytest.mark.parametrize("N", [520, 515])
+def test_outputs_on_rows_of_different_alignment(bsq, N, rows16, dtype):
+    # small whole numbers, exact in BF16: sums up to 16, products up to 256
+    T, K = 2500, 16
+    g = gen(N, rows16, 50)
+    x, w, v = (torch.randint(-1, 2, s, generator=g, device="cuda").to(BF) for s in ((T, K), (N, K), (N, K)))
+    a, u = x.double() @ w.double().T, x.double() @ v.double().T
+
+    def out(bit, t):
+        whole = rows16 >> bit & 1
+        return strided((T, N), t, pad=(-N) % 8 if whole else 3, offset=0 if whole else 1, fill=float("nan"))
+
+    (y, yb), (z, zb), (s, sb) = out(0, dtype), out(1, BF), out(2, BF)
+    bsq.linear_into(x, w, y, None, None, "relu", z)
+    assert torch.equal(z.double(), a) and torch.equal(y.double(), a.clamp(min=0))
+    y.fill_(float("nan"))
+    z.fill_(float("nan"))
+    bsq.gated_linear_into(x, w, v, y, "relu", z, s)
+    assert torch.equal(z.double(), a) and torch.equal(s.double(), u) and torch.equal(y.double(), a.clamp(min=0) * u)
+    for m, b in ((y, yb), (z, zb), (s, sb)):
+        Guard(m, b).check()
+
+
 @pytest.mark.parametrize("T", [3, 200])
 def test_values_that_are_not_finite_stay_in_their_rows(bsq, T):
     g = gen(T)
