@@ -121,11 +121,14 @@ def mix(x):
         return x ^ (x >> np.uint32(16))
 
 
-def random_bits(seed, step, tensor, n):
+def random_bits(seed, step, tensor, n, start=0):
+    """of the elements from `start` on, which do not pass a multiple of 2^32"""
     key = mix(np.array([tensor ^ (seed & 0xFFFFFFFF)]))
     key = mix(key ^ np.uint32(seed >> 32))
     key = mix(key ^ np.uint32(step & 0xFFFFFFFF))
-    return mix(np.arange(n, dtype=np.uint32) ^ key)
+    with np.errstate(over="ignore"):
+        key = key + np.uint32(start >> 32) * np.uint32(0x9E3779B9)
+    return mix(np.arange(start & 0xFFFFFFFF, (start & 0xFFFFFFFF) + n, dtype=np.uint64).astype(np.uint32) ^ key)
 
 
 def e4m3_values():
@@ -184,7 +187,7 @@ def encode(x, bits, root):
     return code.astype(np.uint8), np.where(bad, 255, e + 127).astype(np.uint8)
 
 
-def adamw_ref(p, g, state, lr, step, betas, eps, wd, factor=None, seed=None, tensor=0, p_bf16=False):
+def adamw_ref(p, g, state, lr, step, betas, eps, wd, factor=None, seed=None, tensor=0, p_bf16=False, start=0):
     """One step in FP32, each operation rounded, as numpy does it; returns (p, copy, state), p before its rounding to
     nearest (BF16 with a seed: rounded)."""
     b1, b2 = betas
@@ -204,7 +207,7 @@ def adamw_ref(p, g, state, lr, step, betas, eps, wd, factor=None, seed=None, ten
         q = F(1 - lr * wd) * p.astype(F) - F(lr / (1 - b1 ** step)) * (m / d)
     assert m.dtype == v.dtype == q.dtype == F
     copy = q
-    bits = None if seed is None else random_bits(seed, step, tensor, len(p))
+    bits = None if seed is None else random_bits(seed, step, tensor, len(p), start)
     if len(state) == 2:
         out = (m, v)
     else:

@@ -125,6 +125,28 @@ def test_copies_and_clipping(bsq, bits):
     check(bsq, params, grads, states, norm=torch.zeros(1, device="cuda"), max_norm=0.0)
 
 
+@pytest.mark.parametrize("seed", [None, 77])
+def test_a_tensor_of_more_than_2_32_elements(bsq, seed):
+    n, tail, step = (1 << 32) + 5003, 5003, 3
+    param, grad = (torch.zeros(n, dtype=BF, device="cuda") for _ in range(2))
+    m, v = (torch.zeros(n, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ms, vs = (torch.zeros(-(-n // 32), dtype=torch.uint8, device="cuda") for _ in range(2))
+    (p,), (g,), (st,) = make(bsq, [tail], BF, BF, 8, 0, 5)
+    first = 1 << 32
+    for whole, part in ((param, p), (grad, g), (m, st[0]), (v, st[2])):
+        whole[first:] = part
+    ms[first // 32:], vs[first // 32:] = st[1], st[3]
+    bsq.adamw_step(bsq.AdamWList([param], [grad], [(m, ms, v, vs)]), HYPER["lr"], step, HYPER["betas"], HYPER["eps"],
+                   HYPER["weight_decay"], seed=seed)
+    q, _, state = adamw_ref(host(p), host(g), tuple(host(s) for s in st), HYPER["lr"], step, HYPER["betas"], HYPER["eps"],
+                            HYPER["weight_decay"], None, seed, 0, True, first)
+    assert equal(host(param[first:]), to(q, BF))
+    for got, want in zip((m[first:], ms[first // 32:], v[first:], vs[first // 32:]), state):
+        assert equal(host(got), want)
+    # everything before is 0 and stays so
+    assert not param[:4096].any() and not param[first - 4096:first].any() and not m[:first].any() and not v[:first].any()
+
+
 def test_many_tensors(bsq):
     sizes = [1 + i % 40 for i in range(1000)]
     params, grads, states = make(bsq, sizes, F32, F32, 8, 0, 2)

@@ -206,6 +206,29 @@ def test_values_that_are_not_finite_stay_in_their_rows(bsq, T):
     assert torch.equal(z[rows, 7].float(), torch.where(x[rows, 3] > 0, float("inf"), -float("inf")))
 
 
+@pytest.mark.parametrize("pad", [0, 3])
+def test_results_of_more_than_2_31_elements(bsq, pad):
+    # whole numbers; the last rows and columns lie past 2^31 elements
+    T, N, K = 70001, 32776, 8
+    g = gen(pad, 60)
+    x, w, v = (torch.randint(-1, 2, s, generator=g, device="cuda").to(BF) for s in ((T, K), (N, K), (N, K)))
+    y, z, u = (torch.full((T, N + pad), 77.0, dtype=BF, device="cuda")[:, :N] for _ in range(3))
+    tail = slice(T - 300, T)
+    a, b = x[tail].double() @ w.double().T, x[tail].double() @ v.double().T
+    bsq.linear_into(x, w, y, None, None, "relu", z)
+    assert torch.equal(z[tail].double(), a) and torch.equal(y[tail].double(), a.clamp(min=0))
+    bsq.gated_linear_into(x, w, v, y, "relu", z, u)
+    assert torch.equal(z[tail].double(), a) and torch.equal(u[tail].double(), b) and torch.equal(y[tail].double(), a.clamp(min=0) * b)
+    # gradients: dy is 1 in the last row and 0 elsewhere
+    y.zero_()
+    y[-1] = 1.0
+    z[tail] = a.to(BF)
+    dx, dw, db = bsq.linear_backward(y, x, w, z, "relu")
+    s = (a[-1] > 0).double()
+    assert torch.equal(dx[-1], (s @ w.double()).float().to(BF)) and not dx[:-1].any()
+    assert torch.equal(dw, (s[:, None] * x[-1].double()).to(BF)) and torch.equal(db, s.float())
+
+
 @pytest.mark.parametrize("name", ACTS)
 def test_large_values(bsq, name):
     # pre-activations from -1e4 to 1e4 through a product with the unit matrix
