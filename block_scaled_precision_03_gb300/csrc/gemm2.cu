@@ -35,11 +35,13 @@
 // CTA's rows of B are the gate's, the odd one's up's, and both projections' scales of
 // those columns take the places of the tile's two B scale bands, so that a CTA's
 // accumulator holds gate and up of its rows, 128 columns apart.  Where there are few
-// tiles the sum over K is split; linear_join_kernel adds the parts.  Up to kFewTokens
-// tokens the time goes to streaming the weights, and the product runs the other way
-// round: they are the tile's 256 rows, both CTAs' A, and the tokens its columns (one
-// q8 layer of 14336 -> 4096: 16 tiles, 76 pairs, so parts of K); the gate's and up's rows
-// are then tiles of their own, which the join brings together.
+// tiles the sum over K is split; linear_join_kernel adds the parts.  Of up to 128 tokens only their rows of the
+// operand are loaded: a 128-row box with 8 of them inside costs the copy engine more than its bytes (4096 -> 14336 of 8
+// tokens, MXFP8 gated: 36.9 us, 39.9 with it); what is left in shared memory stays in rows that are not written.  Linear,
+// up to kFewTokens of them, the product runs the other way round: the weights are the tile's 256 rows, both CTAs' A, and
+// the tokens its columns, for an epilogue of one column block (NVFP4 512 -> 512 of 8 tokens 12.3 us, 16.4 the other way;
+// 32 tokens of 14336 -> 4096 23.5 and 23.6; 64 of 512 -> 512 14.3 and 16.4, but 128 18.4 and 16.4; MXFP8 64 of 512 ->
+// 512 16.3 and 14.3).
 // Every wait is bounded; a CTA that gave up records the status, and before
 // the pair exits every MMA, scale copy and stage load it issued has landed.
 #include <algorithm>
@@ -132,15 +134,15 @@ struct Params2 {
 };
 
 // What the kernels with an epilogue take besides
-enum { kPlain, kLinear, kGated, kFewLinear, kFewGated };
-constexpr int64_t kFewTokens = 128;
+enum { kPlain, kLinear, kGated, kFewLinear };
+constexpr int64_t kFewTokens = 32;
 struct Nothing {};
 struct More {
-    CUtensorMap b, sfb;            // gated: the other projection (few tokens: its rows as A)
+    CUtensorMap b, sfb;            // gated: the other projection
     CUtensorMap z, u;              // outputs
     const float* ts_b;
     int32_t splits, split_stages;  // parts of the sum over K, and stages of each
-    int32_t half;                  // few tokens, gated: tiles of the gate's rows
+    uint32_t op_tx;                // operand bytes one CTA loads per stage
     float* acc;                    // few tokens: the parts [split][token][ld_acc]
     int64_t ld_acc;
     Fused f;
@@ -170,10 +172,10 @@ __device__ __forceinline__ Part part_of(const Params2& p, const typename MoreOf<
     return a;
 }
 
-template <int EPI>
-__device__ __forceinline__ int half_of(const typename MoreOf<EPI>::type& more) {
-    if constexpr (EPI != kPlain) return more.half;
-    else return 0;
+template <int KIND, int EPI>
+__device__ __forceinline__ uint32_t op_tx_of(const typename MoreOf<EPI>::type& more) {
+    if constexpr (EPI != kPlain) return more.op_tx;
+    else return Cfg2<KIND>::OP_TX;
 }
 
 // Tile order: groups of `raster` tiles along one dimension, swept along the
@@ -219,7 +221,6 @@ __device__ __noinline__ void drain_pair_loads(uint32_t full0, int S, int n_own, 
 // mixes experts and at most half a tile is idle when an expert covers an odd
 // number of bands.
 struct Tile2 {
-    int32_t which;         // few tokens, gated: 0 the gate's rows, 1 up's
     int32_t a_row;         // this CTA's first row of A (and of C)
     int32_t a_band;        // its 128-row band of A's scale tiles
     int32_t nt;            // 256-column tile of C
@@ -229,16 +230,11 @@ struct Tile2 {
 };
 
 template <int EPI>
-__device__ __forceinline__ Tile2 tile2(const Params2& p, int t, const GroupTable2* gt, int& gcur, uint32_t rank, int half = 0) {
+__device__ __forceinline__ Tile2 tile2(const Params2& p, int t, const GroupTable2* gt, int& gcur, uint32_t rank) {
     Tile2 ti;
-    ti.which = 0;
     if (p.num_groups == 0) {
         int mt, nt;
         tile_mn(p, t, mt, nt);
-        if (EPI == kFewGated && mt >= half) {
-            ti.which = 1;
-            mt -= half;
-        }
         ti.a_band = mt * 2 + (int)rank;
         ti.a_row = ti.a_band * 128;
         ti.nt = nt;
@@ -393,25 +389,22 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
             for (int t = cid; t < total && ok; t += ncl) {
                 int tile = t;
                 const Part pt = part_of<EPI>(p, more, tile);
-                const Tile2 ti = tile2<EPI>(p, tile, gt, gcur, rank, half_of<EPI>(more));
+                const Tile2 ti = tile2<EPI>(p, tile, gt, gcur, rank);
                 const int arow = ti.a_row, brow = ti.b_row;
                 const CUtensorMap* mb = &tmB;
-                const CUtensorMap* ma = &tmA;
                 if constexpr (EPI == kGated)
                     if (rank) mb = &more.b;
-                if constexpr (EPI == kFewGated)
-                    if (ti.which) ma = &more.b;
                 for (int kb = pt.k0; kb < pt.k1; kb++) {
                     if (!tc::mbar_wait(empty0 + 8 * stage, phase ^ 1, abort_flag, p.status, p.timeout_ns)) {
                         ok = false;
                         break;
                     }
                     const uint32_t fb = full_c0 + 8 * stage;
-                    if (leader) tc::mbar_expect_tx(full0 + 8 * stage, 2 * CF::OP_TX);
+                    if (leader) tc::mbar_expect_tx(full0 + 8 * stage, 2 * op_tx_of<KIND, EPI>(more));
 #pragma unroll
                     for (int j = 0; j < CF::KSUB; j++) {
                         const int kx = (kb * CF::KSUB + j) * BKB;
-                        tc::tma_load_2d_pair(tc::smem_u32(smA + stage * CF::OP_BYTES + j * HALF), ma, kx, arow, fb);
+                        tc::tma_load_2d_pair(tc::smem_u32(smA + stage * CF::OP_BYTES + j * HALF), &tmA, kx, arow, fb);
                         tc::tma_load_2d_pair(tc::smem_u32(smB + stage * CF::OP_BYTES + j * HALF), mb, kx, brow, fb);
                     }
                     ++issued;
@@ -430,7 +423,7 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
             for (int t = cid; t < total && ok; t += ncl) {
                 int tile = t;
                 const Part pt = part_of<EPI>(p, more, tile);
-                const Tile2 ti = tile2<EPI>(p, tile, gt, gcur, rank, half_of<EPI>(more));
+                const Tile2 ti = tile2<EPI>(p, tile, gt, gcur, rank);
                 for (int kb = pt.k0; kb < pt.k1; kb++) {
                     if (!tc::mbar_wait(sfree0 + 8 * stage, phase ^ 1, abort_flag, p.status, p.timeout_ns)) {
                         ok = false;
@@ -439,10 +432,7 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
                     const uint32_t sb = sfull_c0 + 8 * stage;
                     if (leader) tc::mbar_expect_tx(sfull0 + 8 * stage, 2 * CF::SF_TX);
                     uint8_t* sf = smSF + stage * CF::SF_STAGE;
-                    const CUtensorMap* msf = &tmSFA;
-                    if constexpr (EPI == kFewGated)
-                        if (ti.which) msf = &more.sfb;
-                    tc::tma_load_3d_pair(tc::smem_u32(sf), msf, 0, kb * CF::SF_ATOMS, ti.a_band, sb);
+                    tc::tma_load_3d_pair(tc::smem_u32(sf), &tmSFA, 0, kb * CF::SF_ATOMS, ti.a_band, sb);
                     if constexpr (EPI == kGated) {
                         // one band of each projection, up's behind the gate's
                         constexpr int BAND = CF::SFB_BYTES / 2;
@@ -549,13 +539,13 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
             beta = *p.ts_b;
         }
         float beta2 = 1.0f;
-        if constexpr (KIND == kKindNV && (EPI == kGated || EPI == kFewGated)) beta2 = *more.ts_b;
+        if constexpr (KIND == kKindNV && EPI == kGated) beta2 = *more.ts_b;
         Staging<1> stage_out{tc::smem_u32(smOut + (warp - 2) * 2048), 0};
         int iter = 0, gcur = 0;
         for (int t = cid; t < total; t += ncl, ++iter) {
             int tile = t;
             const Part pt = part_of<EPI>(p, more, tile);
-            const Tile2 ti = tile2<EPI>(p, tile, gt, gcur, rank, half_of<EPI>(more));
+            const Tile2 ti = tile2<EPI>(p, tile, gt, gcur, rank);
             if (!tc::mbar_wait(tfull, iter & 1, abort_flag, p.status, p.timeout_ns)) break;
             tc::fence_after();
             uint32_t r[4][32];
@@ -572,45 +562,34 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
             if (lane == 0) tc::mbar_arrive_cluster(tempty_c0);
             // this warp's 32 rows, clipped to the rows the CTA may write
             const int row0 = ti.a_row + q * 32;
-            if constexpr (EPI == kFewLinear || EPI == kFewGated) {
+            if constexpr (EPI == kFewLinear) {
                 // a thread owns one feature; neighbouring lanes write neighbouring features of a token
-                const int feature = row0 + lane;
-                const bool in = feature < p.M;         // (the warp stays together: it reads tensor memory next)
-                const float a2 = EPI == kFewGated && ti.which ? beta2 : alpha;
-                const bool whole = EPI == kFewLinear && more.splits == 1;
+                if (h != 0) continue;
                 const Fused& f = more.f;
-                const float bias = whole && f.bias && in ? load_as_float(f.bias, feature, f.bias_bf16) : 0.0f;
-#pragma unroll 1
-                for (int c = 0; c < (h == 0 ? p.N : 0); c += 32) {
-                    float v[32];
+                const int feature = row0 + lane;
+                const int n = feature < p.M ? p.N : 0; // (the warp stays together: it reads tensor memory next)
+                const float bias = more.splits == 1 && f.bias && n ? load_as_float(f.bias, feature, f.bias_bf16) : 0.0f;
+                float v[32];
 #pragma unroll
-                    for (int j = 0; j < 32; j++) {
-                        v[j] = __uint_as_float(r[0][j]) * a2 * beta + bias;
-                        r[0][j] = r[1][j];
-                        r[1][j] = r[2][j];
-                        r[2][j] = r[3][j];
-                    }
-                    const int n = in ? min(32, p.N - c) : 0;
-                    if (!whole) {
-                        float* to = more.acc + ((int64_t)pt.split * p.N + c) * more.ld_acc +
-                                    (EPI == kFewGated ? gate_col(feature) + 128 * ti.which : feature);
+                for (int j = 0; j < 32; j++) v[j] = __uint_as_float(r[0][j]) * alpha * beta + bias;
+                if (more.splits > 1) {
+                    float* to = more.acc + (int64_t)pt.split * p.N * more.ld_acc + feature;
 #pragma unroll
-                        for (int j = 0; j < 32; j++)
-                            if (j < n) to[j * more.ld_acc] = v[j];
-                        continue;
-                    }
+                    for (int j = 0; j < 32; j++)
+                        if (j < n) to[j * more.ld_acc] = v[j];
+                } else {
                     if (f.z) {
 #pragma unroll
                         for (int j = 0; j < 32; j++)
-                            if (j < n) f.z[(c + j) * f.ldz + feature] = __float2bfloat16_rn(v[j]);
+                            if (j < n) f.z[j * f.ldz + feature] = __float2bfloat16_rn(v[j]);
                     }
                     activate(f.act, v);
 #pragma unroll
                     for (int j = 0; j < 32; j++)
                         if (j < n) {
-                            const float y = f.residual ? v[j] + load_as_float(f.residual, (c + j) * f.ld_res + feature, f.y_bf16) : v[j];
-                            if (f.y_bf16) static_cast<__nv_bfloat16*>(f.y)[(c + j) * f.ldy + feature] = __float2bfloat16_rn(y);
-                            else static_cast<float*>(f.y)[(c + j) * f.ldy + feature] = y;
+                            const float y = f.residual ? v[j] + load_as_float(f.residual, j * f.ld_res + feature, f.y_bf16) : v[j];
+                            if (f.y_bf16) static_cast<__nv_bfloat16*>(f.y)[j * f.ldy + feature] = __float2bfloat16_rn(y);
+                            else static_cast<float*>(f.y)[j * f.ldy + feature] = y;
                         }
                 }
                 __syncwarp();
@@ -737,7 +716,7 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
             const int sf_own = *sf_issued_slot;
             const int sf_peer = tc::ld_cluster_s32(tc::mapa(tc::smem_u32((const void*)sf_issued_slot), 1));
             drain_pair_loads(sfull0, S, sf_own, sf_peer, CF::SF_TX);
-            drain_pair_loads(full0, S, n_own, n_peer, CF::OP_TX);
+            drain_pair_loads(full0, S, n_own, n_peer, op_tx_of<KIND, EPI>(more));
         }
     }
     tc::cluster_sync();
@@ -766,12 +745,12 @@ struct Setup {
     int64_t kbytes, n_atoms;
 };
 bool operand_b(const Setup& s, CUtensorMap& tb, CUtensorMap& tsb, const uint8_t* codes, const uint8_t* scales, int64_t rows,
-               uint32_t bands) {
-    return tmap::codes_2d(&tb, codes, rows, s.kbytes, 128) &&
+               uint32_t bands, uint32_t box_rows = 128) {
+    return tmap::codes_2d(&tb, codes, rows, s.kbytes, box_rows) &&
            (s.kind == kKindNV ? tmap::scales_4d_quarters(&tsb, scales, (rows + 127) / 128, s.n_atoms, s.sf_atoms, bands)
                               : tmap::scales_3d(&tsb, scales, (rows + 127) / 128, s.n_atoms, s.sf_atoms, bands));
 }
-bool set_up(Setup& s, const GemmArgs& a, uint32_t sfb_bands) {
+bool set_up(Setup& s, const GemmArgs& a, uint32_t sfb_bands, uint32_t a_rows = 128, uint32_t b_rows = 128) {
     const int kind = s.kind = a.fmt_a == kNVFP4 ? kKindNV : (a.fmt_a == kMXFP4 ? kKindMX4 : kKindFP8);
     const bool fp4 = kind != kKindFP8;
     const int64_t kbytes = s.kbytes = fp4 ? a.K / 2 : a.K;
@@ -800,10 +779,10 @@ bool set_up(Setup& s, const GemmArgs& a, uint32_t sfb_bands) {
                : (kind == kKindMX4 ? Cfg2<kKindMX4>::SF_ATOMS : Cfg2<kKindFP8>::SF_ATOMS);
     // the per-expert padded scale layout spans up to one extra 128-row tile per expert
     const int64_t a_bands = (a.M + 127) / 128 + (p.gsf ? a.num_groups : 0);
-    return tmap::codes_2d(&s.ta, a.a_codes, a.M, kbytes, 128) &&
+    return tmap::codes_2d(&s.ta, a.a_codes, a.M, kbytes, a_rows) &&
            tmap::scales_3d(&s.tsa, a.a_scales, a_bands, s.n_atoms, s.sf_atoms, 1) &&
            operand_b(s, s.tb, s.tsb, a.b_codes, grouped ? a.b_group_scales[0] : a.b_scales, grouped ? a.N * a.num_groups : a.N,
-                     sfb_bands);
+                     sfb_bands, b_rows);
 }
 // raster order: sweep the larger operand past the whole of the smaller one
 // when the smaller one fits in L2 with room to spare
@@ -869,7 +848,7 @@ cudaError_t launch_kind(const Setup& s, const CUtensorMap& tc_, const More& more
 template <bool GATED>
 cudaError_t fused(const GemmArgs& a, const GemmArgs& up, const LinearArgs& l, cudaStream_t st) {
     if (a.M <= kScaledGemvTokens) return run_scaled_gemv(a, up, l, GATED, st);
-    const bool few = a.M <= kFewTokens;
+    const bool few = !GATED && a.M <= kFewTokens;
     GemmArgs q = a;
     if (few) {
         // the weights are A, the tokens B; their tensor scales change places with them
@@ -886,19 +865,13 @@ cudaError_t fused(const GemmArgs& a, const GemmArgs& up, const LinearArgs& l, cu
     }
     Setup s;
     More more{};
-    if (!set_up(s, q, GATED && !few ? 1 : 2)) return cudaErrorInvalidValue;
-    if (GATED && few) {
-        if (!tmap::codes_2d(&more.b, up.b_codes, a.N, s.kbytes, 128) ||
-            !tmap::scales_3d(&more.sfb, up.b_scales, (a.N + 127) / 128, s.n_atoms, s.sf_atoms, 1))
-            return cudaErrorInvalidValue;
-    } else if (GATED && !operand_b(s, more.b, more.sfb, up.b_codes, up.b_scales, a.N, 1)) {
-        return cudaErrorInvalidValue;
-    }
+    const uint32_t x_rows = (uint32_t)std::min<int64_t>(128, (a.M + 7) / 8 * 8);
+    if (!set_up(s, q, GATED ? 1 : 2, few ? 128 : x_rows, few ? x_rows : 128)) return cudaErrorInvalidValue;
+    more.op_tx = (128 + x_rows) * BKB * (s.kind == kKindFP8 ? Cfg2<kKindFP8>::KSUB : Cfg2<kKindNV>::KSUB);
+    if (GATED && !operand_b(s, more.b, more.sfb, up.b_codes, up.b_scales, a.N, 1)) return cudaErrorInvalidValue;
     Params2& p = s.p;
     const int splits = gemm_fused_splits(a.fmt_a, a.M, a.N, a.K, GATED, a.num_sms);
     const int64_t n_tiles = few ? 1 : GATED ? (a.N + 127) / 128 : (a.N + BN - 1) / BN;
-    more.half = p.m_tiles;
-    if (GATED && few) p.m_tiles *= 2;
     if (p.m_tiles * n_tiles * splits > 0x7FFFFFFF) return cudaErrorInvalidValue;
     p.n_tiles = (int32_t)n_tiles;
     p.total_tiles = (int32_t)(p.m_tiles * n_tiles * splits);
@@ -910,8 +883,7 @@ cudaError_t fused(const GemmArgs& a, const GemmArgs& up, const LinearArgs& l, cu
     fused_args(more.f, l);
     order_tiles(p, a.M * s.kbytes, (GATED ? 2 : 1) * a.N * s.kbytes);
     CUtensorMap tcm = s.ta;
-    const bool parts = splits > 1 || (GATED && few);
-    if (!few && parts) {
+    if (!few && splits > 1) {
         if (!pair::map_acc(&tcm, more.acc, splits, a.M, more.ld_acc)) return cudaErrorInvalidValue;
     } else if (!few) {
         more.f.y_tma = fused_map(&tcm, l.y, a.M, a.N, l.ldy, l.y_bf16);
@@ -919,9 +891,9 @@ cudaError_t fused(const GemmArgs& a, const GemmArgs& up, const LinearArgs& l, cu
         more.f.u_tma = GATED ? fused_map(&more.u, l.u, a.M, a.N, l.ldu, true) : kNone;
     }
     const int pairs = std::max(1, std::min(a.num_sms / 2, p.total_tiles));
-    const cudaError_t e = few ? launch_kind<GATED ? kFewGated : kFewLinear>(s, tcm, more, pairs, st)
+    const cudaError_t e = few ? launch_kind<kFewLinear>(s, tcm, more, pairs, st)
                               : launch_kind<GATED ? kGated : kLinear>(s, tcm, more, pairs, st);
-    return e != cudaSuccess || !parts ? e : run_linear_join(more.acc, splits, a.M, a.N, GATED, l, st);
+    return e != cudaSuccess || splits == 1 ? e : run_linear_join(more.acc, splits, a.M, a.N, GATED, l, st);
 }
 
 }  // namespace
@@ -929,16 +901,16 @@ cudaError_t fused(const GemmArgs& a, const GemmArgs& up, const LinearArgs& l, cu
 // parts of the sum over K: a stage (K = 256) takes 0.4 us of MXFP8 or MXFP4, 0.45 of NVFP4; with few tokens it is
 // the pair's share of the weights' stream; between two tiles the one accumulator is read out
 int gemm_fused_splits(int fmt, int64_t tokens, int64_t out, int64_t cols, bool gated, int num_sms) {
-    const bool few = tokens <= kFewTokens, fp4 = fmt >= kMXFP4;
-    const int64_t tiles = few ? (out + 255) / 256 * (gated ? 2 : 1)
+    const bool few = !gated && tokens <= kFewTokens, fp4 = fmt >= kMXFP4;
+    const int64_t tiles = few ? (out + 255) / 256
                               : (tokens + 255) / 256 * ((out + (gated ? 127 : 255)) / (gated ? 128 : 256));
     const double us = few ? (fp4 ? 0.45 : 0.82) : fmt == kNVFP4 ? 0.45 : 0.4;
-    return fused_splits(tiles, (cols + 255) / 256, us, 1.5, (double)tokens * fused_acc_cols(out, gated) * 8, num_sms / 2);
+    return fused_splits(tiles, (cols + 255) / 256, us, 1.5, 0.0, (double)tokens * fused_acc_cols(out, gated) * 8, num_sms / 2);
 }
 size_t gemm_fused_workspace(int fmt, int64_t tokens, int64_t out, int64_t cols, bool gated, int num_sms) {
     if (tokens <= kScaledGemvTokens) return 0;
     const int n = gemm_fused_splits(fmt, tokens, out, cols, gated, num_sms);
-    return n > 1 || (gated && tokens <= kFewTokens) ? (size_t)n * tokens * fused_acc_cols(out, gated) * 4 : 0;
+    return n > 1 ? (size_t)n * tokens * fused_acc_cols(out, gated) * 4 : 0;
 }
 cudaError_t run_gemm_linear(const GemmArgs& a, const LinearArgs& l, cudaStream_t st) { return fused<false>(a, a, l, st); }
 cudaError_t run_gemm_gated(const GemmArgs& gate, const GemmArgs& up, const LinearArgs& l, cudaStream_t st) {

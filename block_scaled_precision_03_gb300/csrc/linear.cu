@@ -17,10 +17,11 @@
 // CTA has gate and up of its own rows in its own tensor memory, 128 columns
 // apart: the activation and the product need nothing from anywhere else.
 //
-// Up to kFewTokens tokens a product is bound by streaming w and runs the other
-// way round, z^T = w x^T: w's rows are the tile's 256 rows and the tokens its 16
-// to 128 columns, so that a stage is nearly all w.  Gated, a stage is 64 of K of
-// 256 rows of wg and of wu, for two accumulators.
+// Of up to 192 tokens a tile has 64, 128 or 192 rows, half of them in either CTA: the MMA is the same, but the operand
+// takes less of a stage, more stages are in flight, and a box mostly outside the matrix costs the copy engine more than
+// its bytes (4096 -> 14336 of 8 tokens, gated, 41 us; 74 with boxes of 128 rows).  (The other way round, z^T = w x^T with
+// w's rows as the tile's and the tokens its columns, was as fast at 8 tokens and slower from 32 on: 128 tokens of 4096 ->
+// 4096 29 us, 21 now.)
 //
 // dx of a gated layer is one product over K = 2 F: first da wg, then du wu.
 // Where there are too few tiles for the pairs the sum over K is split; a second
@@ -47,15 +48,14 @@ namespace {
 
 using namespace pair;
 
-enum { kFwd, kFew, kDx, kDw };
+enum { kFwd, kDx, kDw };
 // When a product waits for the kernel before it on the stream, whose dependent it is: before it reads or writes anything
 // (its set-up runs earlier), or at its end (it needs nothing of that kernel, and runs beside it).
 enum { kWaitStart, kWaitEnd };
 
 constexpr int kStages = 3;
-constexpr int kMaxStages = 6;                       // of narrower tiles: as many as fit
-constexpr int kFewTokens = 128;
-constexpr int kChunk = 4, kSumChunk = 128;          // stages of K = 128 (few tokens, gated: twice as many of 64)
+constexpr int kMaxStages = 12;                      // of smaller tiles: as many as fit
+constexpr int kChunk = 4, kSumChunk = 128;          // stages of K = 128
 constexpr int kSubBytes = 128 * kSubK * 2;          // one CTA's 128 rows of an operand, one sub-step
 constexpr int kOpBytes = kSub * kSubBytes;
 constexpr int kMmas = 4 * kSub;                     // per stage
@@ -70,17 +70,15 @@ __host__ __device__ constexpr bool a_mn(int mode) { return mode == kDw; }
 __host__ __device__ constexpr bool b_mn(int mode) { return mode == kDx || mode == kDw; }
 
 struct Params {
-    int64_t M, N;                  // output; few tokens: M features, N tokens
+    int64_t M, N;                  // output
     int32_t k_stages, chunk;       // K stages in all; stages per accumulator
     int32_t m_tiles, n_tiles, splits, split_stages, total;
     int32_t raster, raster_n;
     int32_t tile_m, tile_n;
-    int32_t stages, b_bytes;       // stages of the ring, one CTA's bytes of B per stage
+    int32_t stages, a_bytes, b_bytes;  // stages of the ring, one CTA's bytes of A and B per stage
     int32_t half;                  // kDx gated: stages of the first pair of operands; kDw gated: its tiles along M
     uint32_t tx;                   // bytes one CTA loads per stage
     int32_t wait;
-    float* acc;                    // splits > 1: few tokens' partial sums [split][token][ld_acc]
-    int64_t ld_acc;
     Fused f;
     unsigned* status;
     uint64_t timeout_ns;
@@ -99,11 +97,9 @@ linear_gemm_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Para
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     // [stages] of A, [stages] of B, the epilogue's staging; the barriers come last
-    constexpr bool FEW = MODE == kFew;
-    constexpr int SUB_B = FEW && GATED ? 1 : kSub;             // sub-steps of B in a stage
-    const int S = p.stages, b_bytes = p.b_bytes, sub_b = b_bytes / SUB_B;
+    const int S = p.stages, a_bytes = p.a_bytes, b_bytes = p.b_bytes, sub_a = a_bytes / kSub, sub_b = b_bytes / kSub;
     uint8_t* smA = base;
-    uint8_t* smB = smA + S * kOpBytes;
+    uint8_t* smB = smA + S * a_bytes;
     uint8_t* smOut = base + kStages * 2 * kOpBytes;
     uint64_t* bars = reinterpret_cast<uint64_t*>(base + (kSmem - 1024 - 256));
     // full[S], empty[S], tfull[2], tempty[2], drain
@@ -177,19 +173,19 @@ linear_gemm_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Para
                     if (MODE == kDx && GATED) mb = &tm.b[second];
 #pragma unroll
                     for (int j = 0; j < kSub; j++) {
-                        const int k = FEW && GATED ? kb * kSubK : ((kb - second * p.half) * kSub + j) * kSubK;
-                        const uint32_t da = tc::smem_u32(smA + stage * kOpBytes + j * kSubBytes);
+                        const int k = ((kb - second * p.half) * kSub + j) * kSubK;
+                        const uint32_t da = tc::smem_u32(smA + stage * a_bytes + j * sub_a);
                         const uint32_t db = tc::smem_u32(smB + stage * b_bytes + j * sub_b);
                         if (a_mn(MODE)) {
                             tc::tma_load_2d_pair(da, ma, am, k, fb);
                             tc::tma_load_2d_pair(da + 8192, ma, am + 64, k, fb);
                         } else {
-                            tc::tma_load_2d_pair(da, FEW && GATED ? &tm.a[j] : ma, k, am, fb);
+                            tc::tma_load_2d_pair(da, ma, k, am, fb);
                         }
                         if (b_mn(MODE)) {
                             tc::tma_load_2d_pair(db, mb, bn, k, fb);
-                            if (p.tile_n == kTile) tc::tma_load_2d_pair(db + 8192, mb, bn + 64, k, fb);
-                        } else if (j < SUB_B) {
+                            if (p.tile_n > 128) tc::tma_load_2d_pair(db + 8192, mb, bn + 64, k, fb);
+                        } else {
                             tc::tma_load_2d_pair(db, mb, k, bn, fb);
                         }
                     }
@@ -227,7 +223,7 @@ linear_gemm_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Para
                             break;
                         }
                         tc::fence_after();
-                        const Desc ad = Desc(ad0) + (uint32_t)(stage * (kOpBytes >> 4));
+                        const Desc ad = Desc(ad0) + (uint32_t)(stage * (a_bytes >> 4));
                         const Desc bd = Desc(bd0) + (uint32_t)(stage * (b_bytes >> 4));
                         const int next = stage + 1 == S ? 0 : stage + 1;
                         const uint32_t next_phase = next == 0 ? phase ^ 1 : phase;
@@ -235,16 +231,10 @@ linear_gemm_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Para
 #pragma unroll
                         for (int m = 0; m < kMmas; m++) {
                             if (m == kMmas - 1) ready = tc::mbar_test(full0 + 8 * next, next_phase);
-                            const Desc am = ad + (m >> 2) * (kSubBytes >> 4) + (m & 3) * a_step;
-                            if (FEW && GATED) {            // wg into one accumulator, wu into the one beside it
-                                const Desc bm = bd + (m & 3) * b_step;
-                                if ((m & 3) == 0) mma_bf16<false>(d + (m >> 2) * 128, am, bm, idesc, kb != c0);
-                                else mma_bf16<true>(d + (m >> 2) * 128, am, bm, idesc, 1);
-                            } else {
-                                const Desc bm = bd + (m >> 2) * (sub_b >> 4) + (m & 3) * b_step;
-                                if (m == 0) mma_bf16<false>(d, am, bm, idesc, kb != c0);
-                                else mma_bf16<true>(d, am, bm, idesc, 1);
-                            }
+                            const Desc am = ad + (m >> 2) * (sub_a >> 4) + (m & 3) * a_step;
+                            const Desc bm = bd + (m >> 2) * (sub_b >> 4) + (m & 3) * b_step;
+                            if (m == 0) mma_bf16<false>(d, am, bm, idesc, kb != c0);
+                            else mma_bf16<true>(d, am, bm, idesc, 1);
                         }
                         any = true;
                         tc::commit<2>(empty0 + 8 * stage, 3);
@@ -269,153 +259,79 @@ linear_gemm_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Para
         Staging<2> st{tc::smem_u32(smOut + (warp - 2) * kStageBytes), 0};
         if (p.wait == kWaitStart) pdl_wait();
         int iter = 0;
-        if constexpr (FEW) {
-            // A thread owns one feature (rows past the tile's are whatever shared memory held: they stay
-            // in their rows) and half of the tokens, in sixteens; neighbouring lanes write neighbouring
-            // features.
-            const int share = ((int)p.N + 31) / 32 * 16, own = half * share;
-            const int tokens = min(share, (int)p.N - own);             // of this warp, at most 64; 0 or less: none
-            constexpr int P = GATED ? 2 : 1;
-            for (int t = cid; t < p.total; t += ncl) {
-                const TileAt ti = tile_at(p, t);
-                const int row = ti.mt * p.tile_m + (int)rank * (p.tile_m / 2) + q * 32 + lane;
-                const bool in = q * 32 + lane < p.tile_m / 2 && row < p.M;
-                float z[P][64] = {};
-                bool ok = true;
-                for (int c0 = ti.k0; c0 < ti.k1; c0 += p.chunk, ++iter) {
-                    const int buf = iter & 1;
-                    ok = wait(tfull0 + 8 * buf, (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns);
-                    if (!ok) break;
-                    tc::fence_after();
-                    const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kTile + own);
-#pragma unroll
-                    for (int c = 0; c < 64; c += 16)
-                        if (c < tokens)
-#pragma unroll
-                            for (int i = 0; i < P; i++) add_acc(z[i] + c, ta + 128 * i + c);
-                    tc::fence_before();
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive_cluster(tempty_c0 + 8 * buf);
+        // A thread owns one row and half of the tile's columns in chunks of 32, at most 128 (gated: of each
+        // projection's, at most 64); of an odd number of chunks the first half has one more
+        constexpr bool PROJ = MODE == kFwd && GATED;
+        const int cols = PROJ ? p.tile_n / 2 : p.tile_n, first = (cols / 32 + 1) / 2 * 32;
+        const int own = half == 0 ? first : cols - first;
+        const uint32_t second = PROJ ? (uint32_t)cols : 0;
+        for (int t = cid; t < p.total; t += ncl) {
+            const TileAt ti = tile_at(p, t);
+            const int which = MODE == kDw && GATED && ti.mt >= p.half ? 1 : 0;
+            const int64_t row0 = (int64_t)(ti.mt - which * p.half) * p.tile_m + rank * (p.tile_m / 2) + q * 32;
+            const int64_t col0 = (int64_t)ti.nt * cols + half * first;
+            const bool live = q * 32 < p.tile_m / 2 && row0 < p.M && col0 < p.N;
+            const uint32_t ta0 = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * first);
+            // 32 columns of the sums, from the thread's column c on, leave
+            const auto leave = [&](float (&v)[32], const float (&u)[32], int c) {
+                if (p.splits > 1) {
+                    const int64_t at = PROJ ? gate_col(col0 + c) : col0 + c;
+                    const int64_t r = row0 + (int64_t)which * p.half * kTile;
+                    store_part(v, st, &tm.out[0], (int)at, (int)r, ti.split, lane);
+                    if (PROJ) store_part(u, st, &tm.out[0], (int)at + 128, (int)r, ti.split, lane);
+                } else if (MODE != kFwd) {
+                    if (col0 + c < p.N) store_bf16(v, 1.0f, st.base, &tm.out[which], (int)col0 + c, (int)row0, st.n, lane);
+                } else if (col0 + c < p.N) {
+                    if (PROJ) finish_gated(v, u, p.f, &tm.out[0], &tm.out[1], &tm.out[2], row0, col0 + c, p.M, p.N, st, lane);
+                    else finish_linear(v, p.f, &tm.out[0], &tm.out[1], row0, col0 + c, p.M, p.N, st, lane);
                 }
-                if (!ok) break;
-                const float bias = !GATED && p.f.bias && in ? load_as_float(p.f.bias, row, p.f.bias_bf16) : 0.0f;
-#pragma unroll 1
-                for (int c = 0; c < tokens; c += 16) {
-                    float v[16];
-#pragma unroll
-                    for (int j = 0; j < 16; j++) v[j] = z[0][j] + bias;
-                    const int64_t token = own + c;
-                    const int n = in ? min(16, tokens - c) : 0;
-                    if (p.splits > 1) {
-                        float* a = p.acc + ((int64_t)ti.split * p.N + token) * p.ld_acc + (GATED ? gate_col(row) : row);
-#pragma unroll
-                        for (int j = 0; j < 16; j++)
-                            if (j < n) {
-                                a[j * p.ld_acc] = z[0][j];
-                                if (GATED) a[j * p.ld_acc + 128] = z[P - 1][j];
-                            }
-                    } else {
-                        if (p.f.z) {
-#pragma unroll
-                            for (int j = 0; j < 16; j++)
-                                if (j < n) {
-                                    p.f.z[(token + j) * p.f.ldz + row] = __float2bfloat16_rn(v[j]);
-                                    if (GATED) p.f.u[(token + j) * p.f.ldu + row] = __float2bfloat16_rn(z[P - 1][j]);
-                                }
-                        }
-                        activate(p.f.act, v);
-#pragma unroll
-                        for (int j = 0; j < 16; j++)
-                            if (j < n) {
-                                float y = GATED ? v[j] * z[P - 1][j] : v[j];
-                                if (!GATED && p.f.residual)
-                                    y += load_as_float(p.f.residual, (token + j) * p.f.ld_res + row, p.f.y_bf16);
-                                const int64_t at = (token + j) * p.f.ldy + row;
-                                if (p.f.y_bf16) static_cast<__nv_bfloat16*>(p.f.y)[at] = __float2bfloat16_rn(y);
-                                else static_cast<float*>(p.f.y)[at] = y;
-                            }
-                    }
-#pragma unroll
-                    for (int i = 0; i < P; i++)
-#pragma unroll
-                        for (int j = 0; j < 48; j++) z[i][j] = z[i][j + 16];
-                }
-                __syncwarp();
-            }
-        } else {
-            // A thread owns one row and 128 of the tile's columns (gated: 64 of each projection's)
-            constexpr bool PROJ = MODE == kFwd && GATED;
-            // (narrower tiles: 64 or 32; gated: 32)
-            const int own = PROJ ? p.tile_n / 4 : p.tile_n / 2;
-            const uint32_t second = PROJ ? (uint32_t)p.tile_n / 2 : 0;
-            for (int t = cid; t < p.total; t += ncl) {
-                const TileAt ti = tile_at(p, t);
-                const int which = MODE == kDw && GATED && ti.mt >= p.half ? 1 : 0;
-                const int64_t row0 = (int64_t)(ti.mt - which * p.half) * kTile + rank * 128 + q * 32;
-                const int64_t col0 = (int64_t)ti.nt * (PROJ ? p.tile_n / 2 : p.tile_n) + half * own;
-                const bool live = row0 < p.M && col0 < p.N;
-                const uint32_t ta0 = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * own);
-                // 32 columns of the sums, from the thread's column c on, leave
-                const auto leave = [&](float (&v)[32], const float (&u)[32], int c) {
-                    if (p.splits > 1) {
-                        const int64_t at = PROJ ? gate_col(col0 + c) : col0 + c;
-                        const int64_t r = row0 + (int64_t)which * p.half * kTile;
-                        store_part(v, st, &tm.out[0], (int)at, (int)r, ti.split, lane);
-                        if (PROJ) store_part(u, st, &tm.out[0], (int)at + 128, (int)r, ti.split, lane);
-                    } else if (MODE != kFwd) {
-                        if (col0 + c < p.N) store_bf16(v, 1.0f, st.base, &tm.out[which], (int)col0 + c, (int)row0, st.n, lane);
-                    } else if (col0 + c < p.N) {
-                        if (PROJ) finish_gated(v, u, p.f, &tm.out[0], &tm.out[1], &tm.out[2], row0, col0 + c, p.M, p.N, st, lane);
-                        else finish_linear(v, p.f, &tm.out[0], &tm.out[1], row0, col0 + c, p.M, p.N, st, lane);
-                    }
-                };
-                if constexpr (!LONG) {
-                    const int buf = iter & 1;
-                    if (!wait(tfull0 + 8 * buf, (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns)) break;
-                    tc::fence_after();
-                    ++iter;
-                    if (live)
-#pragma unroll 1
-                        for (int c = 0; c < own; c += 32) {
-                            float v[32], u[32];
-                            load_acc(v, ta0 + (uint32_t)(buf * kTile + c));
-                            if (PROJ) load_acc(u, ta0 + second + (uint32_t)(buf * kTile + c));
-                            leave(v, u, c);
-                        }
-                    tc::fence_before();
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive_cluster(tempty_c0 + 8 * buf);
-                } else {
-                    float z[128] = {};
-                    bool ok = true;
-                    for (int c0 = ti.k0; c0 < ti.k1; c0 += p.chunk, ++iter) {
-                        ok = wait(tfull0 + 8 * (iter & 1), (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns);
-                        if (!ok) break;
-                        tc::fence_after();
-                        if (live)
-#pragma unroll
-                            for (int c = 0; c < 128; c += 16)
-                                if ((PROJ ? c & 63 : c) < own)
-                                    add_acc(z + c, ta0 + (PROJ && c >= 64 ? second : 0u) + (uint32_t)((iter & 1) * kTile + (PROJ ? c & 63 : c)));
-                        tc::fence_before();
-                        __syncwarp();
-                        if (lane == 0) tc::mbar_arrive_cluster(tempty_c0 + 8 * (iter & 1));
-                    }
-                    if (!ok) break;
-                    if (!live) continue;
-                    // the loop stays one, and z moves on: the epilogue's code is long
+            };
+            if constexpr (!LONG) {
+                const int buf = iter & 1;
+                if (!wait(tfull0 + 8 * buf, (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns)) break;
+                tc::fence_after();
+                ++iter;
+                if (live)
 #pragma unroll 1
                     for (int c = 0; c < own; c += 32) {
                         float v[32], u[32];
-#pragma unroll
-                        for (int j = 0; j < 32; j++) {
-                            v[j] = z[j];
-                            if (PROJ) u[j] = z[64 + j];
-                        }
+                        load_acc(v, ta0 + (uint32_t)(buf * kTile + c));
+                        if (PROJ) load_acc(u, ta0 + second + (uint32_t)(buf * kTile + c));
                         leave(v, u, c);
-#pragma unroll
-                        for (int j = 0; j < 96; j++) z[j] = z[j + 32];
                     }
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_cluster(tempty_c0 + 8 * buf);
+            } else {
+                float z[128] = {};
+                bool ok = true;
+                for (int c0 = ti.k0; c0 < ti.k1; c0 += p.chunk, ++iter) {
+                    ok = wait(tfull0 + 8 * (iter & 1), (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns);
+                    if (!ok) break;
+                    tc::fence_after();
+                    if (live)
+#pragma unroll
+                        for (int c = 0; c < 128; c += 16)
+                            if ((PROJ ? c & 63 : c) < own)
+                                add_acc(z + c, ta0 + (PROJ && c >= 64 ? second : 0u) + (uint32_t)((iter & 1) * kTile + (PROJ ? c & 63 : c)));
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive_cluster(tempty_c0 + 8 * (iter & 1));
+                }
+                if (!ok) break;
+                if (!live) continue;
+                // the loop stays one, and z moves on: the epilogue's code is long
+#pragma unroll 1
+                for (int c = 0; c < own; c += 32) {
+                    float v[32], u[32];
+#pragma unroll
+                    for (int j = 0; j < 32; j++) {
+                        v[j] = z[j];
+                        if (PROJ) u[j] = z[64 + j];
+                    }
+                    leave(v, u, c);
+#pragma unroll
+                    for (int j = 0; j < 96; j++) z[j] = z[j + 32];
                 }
             }
         }
@@ -948,58 +864,46 @@ __global__ void __launch_bounds__(256) linear_bias_kernel(const float* sums, int
     out[c] = s;
 }
 
-// How a product is cut: rows of a pair (few tokens), and parts of the sum over K.
-constexpr double kStageUs = 0.55;                   // a pair's stage of K = 128
+constexpr double kPartUs = 4.0;                     // the epilogue of a part's tile, behind which the next tile's stages may hide
 struct Cut {
-    bool few;
     int tile_m, tile_n, splits;
 };
-// Few tokens: what the busiest pair streams, in bytes of w, decides; parts cost a launch and their own bytes.
-Cut few_cut(int64_t N, int64_t K, int64_t T, bool gated, int num_sms) {
-    const int64_t pairs = std::max(1, num_sms / 2), stage_k = gated ? kSubK : kSub * kSubK, stages = div_up(K, stage_k);
-    const int tile_n = (int)up(T, 16);
-    Cut best{true, kTile, tile_n, 1};
-    double least = 0.0;
-    for (int64_t n = 1; n == 1 || (n <= 16 && n * 4 <= stages); n++) {
-        const int64_t per = div_up(stages, n);
-        for (int t = kTile; t >= 96; t -= 16) {
-            const double load = (double)div_up(div_up(N, t) * fused_parts(stages, n), pairs) * t * per * stage_k * (gated ? 4 : 2);
-            // 80 GB/s for a pair; the join's launch and the parts, written and read
-            const double us = load / 80e3 + (n > 1 ? 2.5 + (double)n * T * N * (gated ? 16 : 8) / 5e6 : 0.0);
-            if (least == 0.0 || us < least) {
-                least = us;
-                best = {true, t, tile_n, fused_parts(stages, n)};
-            }
-        }
-    }
-    return best;
+// the busiest pair's time, and the join's: its launch, and the parts written and read
+double split_us(int64_t tiles, int64_t stages, int64_t n, double stage_us, double tile_us, double part_us, double part_bytes, int pairs) {
+    const double tile = div_up(stages, n) * stage_us + tile_us;
+    if (n == 1) return div_up(tiles, pairs) * tile;
+    return tile + (div_up(tiles * n, pairs) - 1) * std::max(tile, part_us) + 2.0 + n * part_bytes / 6.7e6;
 }
-// Tiles of `least` to 256 columns.  Narrower ones where there are few: a stage of 128 or 64 columns takes 0.40 or 0.35
-// us instead of 0.55 (its MMAs cost the issuing thread the same), but there are more of them, and the last tile's
-// epilogue is shorter.  `per`: columns of the result for a column of a tile; part_bytes: a part's, written and read.
-Cut wide_cut(int64_t m_tiles, int64_t cols, double per, int64_t stages, double part_bytes, int least, int num_sms) {
-    static constexpr struct { int n; double stage_us, end_us; } kWidths[] = {{256, kStageUs, 4.0}, {128, 0.40, 2.0}, {64, 0.35, 1.0}};
-    const int pairs = std::max(1, num_sms / 2);
+// How a product is cut: rows and columns of a pair's tile, and parts of the sum over K.  The estimate: what the
+// busiest pair computes, and the last tile's epilogue.  A narrower tile's stage is not shorter in proportion (the MMAs
+// of few columns wait for A's rows, and cost the issuing thread the same), but the tiles fill the pairs better: 4096 x
+// 4096 -> 4096 in 84 us with 224 columns, 88 with 256, 96 with 192; 512 x 4096 -> 14336 in 53 with 192, 58 with 256.
+// With one row of tiles a stage takes as long as its share of the memory's rate for w.  `per`: columns of the result
+// for a column of a tile; `step`: widths that the kernel takes (32 columns are a chunk of the epilogue; gated, of either
+// projection; an MN-major operand is read in boxes of 64 columns for either CTA); part_bytes: a part's, written and read.
+Cut wide_cut(int64_t rows, int64_t cols, double per, int64_t stages, double part_bytes, int step, int num_sms) {
+    static constexpr struct { int n; double stage_us, end_us; } kWidths[] = {
+        {256, 0.60, 4.0}, {224, 0.57, 4.0}, {192, 0.54, 3.5}, {160, 0.50, 3.0}, {128, 0.435, 2.0}, {96, 0.43, 1.5}, {64, 0.42, 1.0}};
+    const int pairs = std::max(1, num_sms / 2), tile_m = rows > kTile - 64 ? kTile : (int)up(rows, 64);
+    const int64_t m_tiles = div_up(rows, kTile);
     Cut best{};
     double fewest = 0.0;
     for (const auto& w : kWidths) {
-        if (w.n < least) break;
+        if (w.n % step) continue;
         const int64_t tiles = m_tiles * div_up(cols, (int64_t)(w.n * per));
-        const int splits = fused_splits(tiles, stages, w.stage_us, 0.0, part_bytes, pairs);
-        const double us = (double)div_up(tiles * splits, pairs) * div_up(stages, splits) * w.stage_us + w.end_us +
-                          (splits > 1 ? 2.0 + splits * part_bytes / 6.7e6 : 0.0);
+        const double stage_us = m_tiles == 1 ? std::max(w.stage_us, w.n * 256 / 88e3) : w.stage_us;
+        const int splits = fused_splits(tiles, stages, stage_us, 0.0, kPartUs, part_bytes, pairs);
+        const double us = split_us(tiles, stages, splits, stage_us, 0.0, kPartUs, part_bytes, pairs) + w.end_us;
         if (fewest == 0.0 || us < fewest) {
             fewest = us;
-            best = {false, kTile, w.n, splits};
+            best = {tile_m, w.n, splits};
         }
     }
     return best;
 }
 Cut forward_cut(int64_t T, int64_t N, int64_t K, bool gated, int num_sms) {
-    if (T <= kFewTokens) return few_cut(N, K, T, gated, num_sms);
-    // (gated: a chunk of the epilogue is 32 columns of either projection)
-    return wide_cut(div_up(T, kTile), N, gated ? 0.5 : 1.0, div_up(K, kSub * kSubK), (double)T * fused_acc_cols(N, gated) * 8,
-                    gated ? 128 : 64, num_sms);
+    return wide_cut(T, N, gated ? 0.5 : 1.0, div_up(K, kSub * kSubK), (double)T * fused_acc_cols(N, gated) * 8,
+                    gated ? 64 : 32, num_sms);
 }
 
 struct Operand {
@@ -1018,7 +922,6 @@ cudaError_t launch_gemm(const Params& p, const Maps& tm, int pairs, cudaStream_t
 template <int MODE, bool GATED>
 cudaError_t gemm(Params p, const Operand (&a)[2], const Operand (&b)[2], Maps& tm, int64_t K, const Cut& cut, int wait,
                  bool fine, const LinearArgs& args, cudaStream_t st) {
-    constexpr bool FEW = MODE == kFew;
     const int tile_n = cut.tile_n;
     // the second operands where there are any
     constexpr bool TWO_A = GATED && MODE != kFwd, TWO_B = GATED && (MODE == kFwd || MODE == kDx);
@@ -1028,20 +931,21 @@ cudaError_t gemm(Params p, const Operand (&a)[2], const Operand (&b)[2], Maps& t
         if ((i == 0 || TWO_B) && !map_operand(&tm.b[i], b[i].p, b[i].rows, b[i].cols, b[i].ld, b_mn(MODE) ? kSubK : tile_n / 2))
             return cudaErrorInvalidValue;
     }
-    const int64_t stage_k = FEW && GATED ? kSubK : kSub * kSubK;
-    const int64_t stages = div_up(K, stage_k);
+    const int64_t stages = div_up(K, kSub * kSubK);
     p.half = MODE == kDx ? (int32_t)stages : (int32_t)div_up(p.M, cut.tile_m);
     p.k_stages = (int32_t)(MODE == kDx && GATED ? 2 * stages : stages);
     p.tile_m = cut.tile_m;
     p.tile_n = tile_n;
-    p.b_bytes = (FEW && GATED ? 1 : kSub) * (tile_n / 2) * kSubK * 2;
-    p.stages = std::min(kMaxStages, kStages * 2 * kOpBytes / (kOpBytes + p.b_bytes));
-    p.tx = (uint32_t)(kSub * (cut.tile_m / 2) * kSubK * 2 + p.b_bytes);
+    // (of an MN-major operand whole boxes of 64 columns)
+    p.b_bytes = kSub * (int)(b_mn(MODE) ? up(tile_n / 2, 64) : tile_n / 2) * kSubK * 2;
+    p.a_bytes = kSub * (cut.tile_m / 2) * kSubK * 2;
+    p.stages = std::min(kMaxStages, kStages * 2 * kOpBytes / (p.a_bytes + p.b_bytes));
+    p.tx = (uint32_t)(p.a_bytes + p.b_bytes);
     p.m_tiles = (int32_t)div_up(p.M, cut.tile_m) * (MODE == kDw && GATED ? 2 : 1);
     p.n_tiles = (int32_t)div_up(p.N, MODE == kFwd && GATED ? tile_n / 2 : tile_n);
     p.split_stages = (int32_t)div_up(p.k_stages, cut.splits);
     p.splits = (int32_t)div_up(p.k_stages, p.split_stages);
-    p.chunk = (fine ? kChunk : kSumChunk) * (FEW && GATED ? 2 : 1);
+    p.chunk = fine ? kChunk : kSumChunk;
     const int64_t total = (int64_t)p.m_tiles * p.n_tiles * p.splits;
     if (total > 0x7FFFFFFF) return cudaErrorInvalidValue;
     p.total = (int32_t)total;
@@ -1050,8 +954,7 @@ cudaError_t gemm(Params p, const Operand (&a)[2], const Operand (&b)[2], Maps& t
     p.timeout_ns = args.timeout_ns;
     const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(args.num_sms / 2, total));
     choose_raster(p, K, pairs);
-    if constexpr (!FEW)
-        if (p.split_stages <= p.chunk) return launch_gemm<MODE, GATED, false>(p, tm, pairs, st);
+    if (p.split_stages <= p.chunk) return launch_gemm<MODE, GATED, false>(p, tm, pairs, st);
     return launch_gemm<MODE, GATED, true>(p, tm, pairs, st);
 }
 
@@ -1090,27 +993,19 @@ cudaError_t forward(const LinearArgs& a, cudaStream_t st) {
     Maps tm{};
     Fused& f = p.f;
     fused_args(f, a);
-    p.acc = static_cast<float*>(a.ws);
-    p.ld_acc = fused_acc_cols(N, GATED);
+    float* acc = static_cast<float*>(a.ws);
     const Operand x{a.x, T, K, a.ldx}, w0{a.w, N, K, a.ldw}, w1{GATED ? a.w2 : a.w, N, K, GATED ? a.ldw2 : a.ldw};
-    cudaError_t err;
-    if (cut.few) {
-        p.M = N;
-        p.N = T;
-        err = gemm<kFew, GATED>(p, {w0, w1}, {x, x}, tm, K, cut, kWaitStart, !a.y_bf16, a, st);
+    p.M = T;
+    p.N = N;
+    if (cut.splits > 1) {
+        if (!map_acc(&tm.out[0], acc, cut.splits, T, fused_acc_cols(N, GATED))) return cudaErrorInvalidValue;
     } else {
-        p.M = T;
-        p.N = N;
-        if (cut.splits > 1) {
-            if (!map_acc(&tm.out[0], p.acc, cut.splits, T, p.ld_acc)) return cudaErrorInvalidValue;
-        } else {
-            f.y_tma = fused_map(&tm.out[0], a.y, T, N, a.ldy, a.y_bf16);
-            f.z_tma = fused_map(&tm.out[1], a.z, T, N, a.ldz, true);
-            f.u_tma = GATED ? fused_map(&tm.out[2], a.u, T, N, a.ldu, true) : kNone;
-        }
-        err = gemm<kFwd, GATED>(p, {x, x}, {w0, w1}, tm, K, cut, kWaitStart, !a.y_bf16, a, st);
+        f.y_tma = fused_map(&tm.out[0], a.y, T, N, a.ldy, a.y_bf16);
+        f.z_tma = fused_map(&tm.out[1], a.z, T, N, a.ldz, true);
+        f.u_tma = GATED ? fused_map(&tm.out[2], a.u, T, N, a.ldu, true) : kNone;
     }
-    return err != cudaSuccess || cut.splits == 1 ? err : run_linear_join(p.acc, cut.splits, T, N, GATED, a, st);
+    const cudaError_t err = gemm<kFwd, GATED>(p, {x, x}, {w0, w1}, tm, K, cut, kWaitStart, !a.y_bf16, a, st);
+    return err != cudaSuccess || cut.splits == 1 ? err : run_linear_join(acc, cut.splits, T, N, GATED, a, st);
 }
 
 // ------------------------------------------------------------- backward
@@ -1123,10 +1018,9 @@ GradPlan grad_plan(int64_t T, int64_t N, int64_t D, bool gated, int num_sms) {
     GradPlan g{};
     g.ld = up(N, 8);
     g.blocks = div_up(T, kGradRows);
-    // (an MN-major operand is read in boxes of 64 columns for either CTA)
-    g.dx = wide_cut(div_up(T, kTile), D, 1.0, div_up(N, kSub * kSubK) * (gated ? 2 : 1), (double)T * D * 8, 128, num_sms);
+    g.dx = wide_cut(T, D, 1.0, div_up(N, kSub * kSubK) * (gated ? 2 : 1), (double)T * D * 8, 128, num_sms);
     const int64_t rows = up(N, kTile) * (gated ? 2 : 1);
-    g.dw = wide_cut(rows / kTile, D, 1.0, div_up(T, kSub * kSubK), (double)rows * D * 8, 128, num_sms);
+    g.dw = wide_cut(rows, D, 1.0, div_up(T, kSub * kSubK), (double)rows * D * 8, 128, num_sms);
     g.dz_bytes = (size_t)(T * g.ld * 2 * (gated ? 2 : 1));
     g.sums_bytes = gated ? 0 : (size_t)up(g.blocks * N * 4, 16);
     g.dx_bytes = g.dx.splits > 1 ? (size_t)(g.dx.splits * T * D * 4) : 0;
@@ -1271,12 +1165,12 @@ int fused_parts(int64_t stages, int64_t n) {
     const int64_t per = div_up(stages, n);
     return (int)div_up(stages, per);
 }
-int fused_splits(int64_t tiles, int64_t stages, double stage_us, double tile_us, double part_bytes, int pairs) {
+int fused_splits(int64_t tiles, int64_t stages, double stage_us, double tile_us, double part_us, double part_bytes, int pairs) {
     int64_t best = 1;
     double least = 0.0;
     pairs = std::max(1, pairs);
     for (int64_t n = 1; n == 1 || (n * 4 <= stages && n * tiles <= 8 * pairs); n++) {
-        const double us = (double)div_up(tiles * n, pairs) * (div_up(stages, n) * stage_us + tile_us) + (n > 1 ? 2.0 + n * part_bytes / 6.7e6 : 0.0);
+        const double us = split_us(tiles, stages, n, stage_us, tile_us, part_us, part_bytes, pairs);
         if (n == 1 || us < least) {
             least = us;
             best = n;
