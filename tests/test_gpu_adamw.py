@@ -104,6 +104,19 @@ def test_step(bsq, p_type, g_type, bits, seed, offset):
         check(bsq, params, grads, states, step=1 + 3 * i, seed=seed)
 
 
+# only the moments on 16-byte boundaries: parameters, gradients and copies each somewhere else
+@pytest.mark.parametrize("seed", [None, 99])
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("p_type,g_type", [(BF, BF), (F32, F32), (F32, BF), (BF, F32)])
+def test_parameters_off_16_byte_boundaries(bsq, p_type, g_type, bits, seed):
+    for sizes in ([70000, 255, 4096], [1025, 2048]):
+        for at, (p_off, g_off, c_off) in enumerate([(1, 0, 2), (2, 1, 0), (0, 2, 1), (3, 3, 3), (0, 0, 1)]):
+            params, grads, states = make(bsq, sizes, p_type, g_type, bits, 0, at)
+            params, grads = pieces(sizes, p_type, p_off, params), pieces(sizes, g_type, g_off, grads)
+            copies = pieces(sizes, BF, c_off, [torch.zeros(n, device="cuda") for n in sizes]) if at % 2 == 0 else None
+            check(bsq, params, grads, states, seed=seed, copies=copies)
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_several_steps_from_nothing(bsq, bits):
     g = torch.Generator(device="cuda").manual_seed(1)
