@@ -178,6 +178,14 @@ __device__ __forceinline__ uint32_t op_tx_of(const typename MoreOf<EPI>::type& m
     else return Cfg2<KIND>::OP_TX;
 }
 
+// With few tokens the waits poll for a while before they suspend the thread (see pair::wait): NVFP4 512 -> 512 of 8 tokens
+// 10.2 us, was 12.3.  (Not elsewhere: gated MXFP8 2048 -> 512 of 64 tokens 11.3 us, 12.0 with it.)
+template <int EPI>
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* status, uint64_t limit_ns) {
+    if constexpr (EPI == kFewLinear) return pair::wait(bar, parity, abort_flag, status, limit_ns);
+    else return tc::mbar_wait(bar, parity, abort_flag, status, limit_ns);
+}
+
 // Tile order: groups of `raster` tiles along one dimension, swept along the
 // other (raster_n: the groups run along n).  A group spanning the whole of
 // the smaller operand keeps that operand resident in L2 while the other one
@@ -395,7 +403,7 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
                 if constexpr (EPI == kGated)
                     if (rank) mb = &more.b;
                 for (int kb = pt.k0; kb < pt.k1; kb++) {
-                    if (!tc::mbar_wait(empty0 + 8 * stage, phase ^ 1, abort_flag, p.status, p.timeout_ns)) {
+                    if (!wait_for<EPI>(empty0 + 8 * stage, phase ^ 1, abort_flag, p.status, p.timeout_ns)) {
                         ok = false;
                         break;
                     }
@@ -425,7 +433,7 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
                 const Part pt = part_of<EPI>(p, more, tile);
                 const Tile2 ti = tile2<EPI>(p, tile, gt, gcur, rank);
                 for (int kb = pt.k0; kb < pt.k1; kb++) {
-                    if (!tc::mbar_wait(sfree0 + 8 * stage, phase ^ 1, abort_flag, p.status, p.timeout_ns)) {
+                    if (!wait_for<EPI>(sfree0 + 8 * stage, phase ^ 1, abort_flag, p.status, p.timeout_ns)) {
                         ok = false;
                         break;
                     }
@@ -475,13 +483,13 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
             for (int t = cid; t < total && ok; t += ncl, ++iter) {
                 // both CTAs' epilogue warps arrive here after their TMEM loads completed
                 // (tcgen05.wait::ld); a CTA-scope acquire suffices
-                if (!tc::mbar_wait(tempty, (iter & 1) ^ 1, abort_flag, p.status, p.timeout_ns)) { ok = false; break; }
+                if (!wait_for<EPI>(tempty, (iter & 1) ^ 1, abort_flag, p.status, p.timeout_ns)) { ok = false; break; }
                 tc::fence_after();
                 int tile = t;
                 const Part pt = part_of<EPI>(p, more, tile);
                 for (int kb = pt.k0; kb < pt.k1; kb++) {
-                    if (!tc::mbar_wait(full0 + 8 * stage, phase, abort_flag, p.status, p.timeout_ns) ||
-                        !tc::mbar_wait(sfr0 + 8 * stage, phase, abort_flag, p.status, p.timeout_ns)) {
+                    if (!wait_for<EPI>(full0 + 8 * stage, phase, abort_flag, p.status, p.timeout_ns) ||
+                        !wait_for<EPI>(sfr0 + 8 * stage, phase, abort_flag, p.status, p.timeout_ns)) {
                         ok = false;
                         break;
                     }
@@ -546,7 +554,7 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
             int tile = t;
             const Part pt = part_of<EPI>(p, more, tile);
             const Tile2 ti = tile2<EPI>(p, tile, gt, gcur, rank);
-            if (!tc::mbar_wait(tfull, iter & 1, abort_flag, p.status, p.timeout_ns)) break;
+            if (!wait_for<EPI>(tfull, iter & 1, abort_flag, p.status, p.timeout_ns)) break;
             tc::fence_after();
             uint32_t r[4][32];
             // gated: 64 columns of the gate's, and up's 64 of the same columns
@@ -584,12 +592,16 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
                             if (j < n) f.z[j * f.ldz + feature] = __float2bfloat16_rn(v[j]);
                     }
                     activate(f.act, v);
+                    // (all of the residual before the first store, which may be to its place)
+                    if (f.residual)
+#pragma unroll
+                        for (int j = 0; j < 32; j++)
+                            if (j < n) v[j] += load_as_float(f.residual, j * f.ld_res + feature, f.y_bf16);
 #pragma unroll
                     for (int j = 0; j < 32; j++)
                         if (j < n) {
-                            const float y = f.residual ? v[j] + load_as_float(f.residual, j * f.ld_res + feature, f.y_bf16) : v[j];
-                            if (f.y_bf16) static_cast<__nv_bfloat16*>(f.y)[j * f.ldy + feature] = __float2bfloat16_rn(y);
-                            else static_cast<float*>(f.y)[j * f.ldy + feature] = y;
+                            if (f.y_bf16) static_cast<__nv_bfloat16*>(f.y)[j * f.ldy + feature] = __float2bfloat16_rn(v[j]);
+                            else static_cast<float*>(f.y)[j * f.ldy + feature] = v[j];
                         }
                 }
                 __syncwarp();
@@ -597,24 +609,37 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
             } else if constexpr (EPI != kPlain) {
                 const int col0 = EPI == kGated ? ti.nt * 128 + h * 64 : ti.nt * BN + h * 128;
                 if (row0 >= p.M || col0 >= p.N) continue;
+                // Two chunks of code, and r moves on: the epilogue is long.  (A copy of it for each of the four, fetched
+                // from memory the first time, made 512 -> 512 of 128 tokens 19.5 us, not 14.7; one copy in all is as
+                // fast there, and moves more: gated NVFP4 8192 x 4096 -> 14336 403 us, 383 with two.)
+#pragma unroll 1
+                for (int b = 0; b < OWN && col0 + b < p.N; b += 64) {
 #pragma unroll
-                for (int c = 0; c < OWN; c += 32) {
-                    if (col0 + c >= p.N) break;
-                    float v[32], u[32];
+                    for (int c = 0; c < 64; c += 32) {
+                        const int col = col0 + b + c;
+                        if (col >= p.N) break;
+                        float v[32], u[32];
 #pragma unroll
-                    for (int j = 0; j < 32; j++) {
-                        v[j] = __uint_as_float(r[c / 32][j]) * alpha * beta;
-                        u[j] = EPI == kGated ? __uint_as_float(r[2 + (c / 32 & 1)][j]) * alpha * beta2 : 0.0f;
+                        for (int j = 0; j < 32; j++) {
+                            v[j] = __uint_as_float(r[c / 32][j]) * alpha * beta;
+                            u[j] = EPI == kGated ? __uint_as_float(r[2 + c / 32][j]) * alpha * beta2 : 0.0f;
+                        }
+                        if (more.splits > 1) {
+                            const int at = ti.nt * BN + h * OWN + b + c;
+                            pair::store_part(v, stage_out, &tmC, at, row0, pt.split, lane);
+                            if (EPI == kGated) pair::store_part(u, stage_out, &tmC, at + 128, row0, pt.split, lane);
+                        } else if (EPI == kGated) {
+                            finish_gated(v, u, more.f, &tmC, &more.z, &more.u, row0, col, p.M, p.N, stage_out, lane);
+                        } else {
+                            finish_linear(v, more.f, &tmC, &more.z, row0, col, p.M, p.N, stage_out, lane);
+                        }
                     }
-                    if (more.splits > 1) {
-                        const int at = ti.nt * BN + h * OWN + c;
-                        pair::store_part(v, stage_out, &tmC, at, row0, pt.split, lane);
-                        if (EPI == kGated) pair::store_part(u, stage_out, &tmC, at + 128, row0, pt.split, lane);
-                    } else if (EPI == kGated) {
-                        finish_gated(v, u, more.f, &tmC, &more.z, &more.u, row0, col0 + c, p.M, p.N, stage_out, lane);
-                    } else {
-                        finish_linear(v, more.f, &tmC, &more.z, row0, col0 + c, p.M, p.N, stage_out, lane);
-                    }
+                    if (EPI != kGated)
+#pragma unroll
+                        for (int j = 0; j < 32; j++) {
+                            r[0][j] = r[2][j];
+                            r[1][j] = r[3][j];
+                        }
                 }
                 continue;
             }
@@ -654,8 +679,8 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
                 for (int kb = pt.k0; kb < pt.k1; kb++) {
                     // the stage's scales have landed, and the MMAs that read the stage's
                     // tensor-memory slot last time have completed
-                    if (!tc::mbar_wait(sfull0 + 8 * stage, phase, abort_flag, p.status, p.timeout_ns) ||
-                        !tc::mbar_wait(empty0 + 8 * stage, phase ^ 1, abort_flag, p.status, p.timeout_ns)) {
+                    if (!wait_for<EPI>(sfull0 + 8 * stage, phase, abort_flag, p.status, p.timeout_ns) ||
+                        !wait_for<EPI>(empty0 + 8 * stage, phase ^ 1, abort_flag, p.status, p.timeout_ns)) {
                         ok = false;
                         break;
                     }

@@ -702,14 +702,18 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const float* acc, int 
                 if (GATED) f.u[row * f.ldu + col + j] = __float2bfloat16_rn(u[j]);
             }
     activate(f.act, v);
+    // (all of the residual before the first store, which may be to its place)
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        if (GATED) v[j] *= u[j];
+        else if (f.residual && j < n) v[j] += load_as_float(f.residual, row * f.ld_res + col + j, f.y_bf16);
+    }
 #pragma unroll
     for (int j = 0; j < 4; j++)
         if (j < n) {
-            float y = GATED ? v[j] * u[j] : v[j];
-            if (!GATED && f.residual) y += load_as_float(f.residual, row * f.ld_res + col + j, f.y_bf16);
             const int64_t at = row * f.ldy + col + j;
-            if (f.y_bf16) static_cast<__nv_bfloat16*>(f.y)[at] = __float2bfloat16_rn(y);
-            else static_cast<float*>(f.y)[at] = y;
+            if (f.y_bf16) static_cast<__nv_bfloat16*>(f.y)[at] = __float2bfloat16_rn(v[j]);
+            else static_cast<float*>(f.y)[at] = v[j];
         }
 }
 
@@ -1042,13 +1046,13 @@ cudaError_t slope(const LinearArgs& a, const SlopeArgs& s, cudaStream_t st) {
     return e;
 }
 
-// In FP32 and unrounded: up to kGemvTokens tokens, and small products, where the rounding of few elements of dz to
-// BF16, or of few results, does not average out.  Measured against the tensor cores' way: 5 tokens of 4096 -> 1000 in
-// 12.8 us (23.0), 16 of them 17.1 (23), gated 20.5 and 30 (27); 60 of 512 -> 64 12.4 (16.5); but 100 of 4096 -> 160 26 (18).
-bool few_grad(int64_t tokens, int64_t out, int64_t cols) {
-    if (tokens <= kGemvTokens) return true;
-    const int64_t most = tokens <= 16 ? 16384 : 4096;
-    return tokens <= kSmallTokens && (tokens * out <= most || tokens * cols <= 4096) && (double)tokens * out * cols <= 0x1p28;
+// In FP32 and with dz unrounded: up to kGemvTokens tokens, and, where dz is not dy itself, small products, where the
+// rounding of few elements of dz to BF16, or of few results, does not average out.  Measured against the tensor cores' way
+// (silu): 5 tokens of 4096 -> 1000 19.2 us (19.5), 60 of 512 -> 64 16.4 (19.3), 100 of 4096 -> 40 29 (20); 16 of 4096 ->
+// 1000 would take 22.5 (20.4).
+bool few_grad(int64_t tokens, int64_t out, int64_t cols, bool exact) {
+    if (tokens <= kGemvTokens || exact) return tokens <= kGemvTokens;
+    return tokens <= kSmallTokens && (tokens * out <= 4096 || tokens * cols <= 4096) && (double)tokens * out * cols <= 0x1p28;
 }
 // Rows of w for a part of dx.  Up to kGemvTokens tokens: some four CTAs for every SM.
 int few_rows(int64_t tokens, int64_t out, int64_t cols, int num_sms) {
@@ -1084,7 +1088,8 @@ cudaError_t backward_few(const LinearArgs& a, cudaStream_t st) {
 template <bool GATED>
 cudaError_t backward(const LinearArgs& a, cudaStream_t st) {
     const int64_t T = a.tokens, N = a.out, D = a.cols;
-    if (few_grad(T, N, D)) return backward_few<GATED>(a, st);
+    // (the identity's dz is dy)
+    if (few_grad(T, N, D, !GATED && a.act == kActIdentity)) return backward_few<GATED>(a, st);
     const GradPlan g = grad_plan(T, N, D, GATED, a.num_sms);
     // dz is made in the workspace, or copied there for its address or pitch
     const bool copy = GATED || a.act != kActIdentity || reinterpret_cast<uintptr_t>(a.dy) % 16 || (a.ld_dy % 8 && T > 1);
@@ -1191,12 +1196,15 @@ size_t linear_workspace(int64_t tokens, int64_t out, int64_t cols, bool gated, i
     return c.splits > 1 ? (size_t)c.splits * tokens * fused_acc_cols(out, gated) * 4 : 0;
 }
 size_t linear_backward_workspace(int64_t tokens, int64_t out, int64_t cols, bool gated, int num_sms) {
-    if (few_grad(tokens, out, cols)) {
+    // whichever way the activation takes
+    size_t most = 0;
+    if (few_grad(tokens, out, cols, false)) {
         const int64_t parts = div_up(out, few_rows(tokens, out, cols, num_sms));
-        return parts > 1 ? (size_t)(parts * tokens * cols * 4) : 0;
+        most = parts > 1 ? (size_t)(parts * tokens * cols * 4) : 0;
+        if (gated || tokens <= kGemvTokens) return most;
     }
     const GradPlan g = grad_plan(tokens, out, cols, gated, num_sms);
-    return g.dz_bytes + g.sums_bytes + g.dx_bytes + g.dw_bytes;
+    return std::max(most, g.dz_bytes + g.sums_bytes + g.dx_bytes + g.dw_bytes);
 }
 cudaError_t run_linear(const LinearArgs& a, bool gated, cudaStream_t st) {
     return gated ? forward<true>(a, st) : forward<false>(a, st);

@@ -80,6 +80,14 @@ __device__ __forceinline__ void put_chunk(const uint32_t (&w)[16], uint32_t buf,
                      :: "r"(row + ((u ^ sw) << 4)), "r"(w[4 * u]), "r"(w[4 * u + 1]), "r"(w[4 * u + 2]), "r"(w[4 * u + 3])
                      : "memory");
 }
+__device__ __forceinline__ void get_chunk(uint32_t (&w)[16], uint32_t buf, int lane) {
+    const uint32_t row = buf + (uint32_t)lane * 64u, sw = (uint32_t)((lane >> 1) & 3);
+#pragma unroll
+    for (int u = 0; u < 4; u++)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[4 * u]), "=r"(w[4 * u + 1]), "=r"(w[4 * u + 2]), "=r"(w[4 * u + 3])
+                     : "r"(row + ((u ^ sw) << 4)) : "memory");
+}
 __device__ __forceinline__ void stage_chunk(const uint32_t (&w)[16], uint32_t buf, int lane) {
     put_chunk(w, buf, lane);
     tc::fence_async_smem();
