@@ -415,9 +415,10 @@ void fused_args(Fused& f, const LinearArgs& a);
 int64_t fused_acc_cols(int64_t N, bool gated);
 // the parts that get any of `stages`, dealt to n
 int fused_parts(int64_t stages, int64_t n);
-// How many parts: more than one where there are fewer tiles than pairs, or few in the last wave.  The estimate: what
-// the busiest pair computes (tile_us: what a tile costs besides its stages; part_us: the least for a part's), and that each part's FP32 tile is written
-// and read.
+// What `n` parts of each tile's sum cost: the busiest pair's time, and the join's, its launch and the parts written and
+// read (tile_us: what a tile costs besides its stages; part_us: the least for a part's)
+double split_us(int64_t tiles, int64_t stages, int64_t n, double stage_us, double tile_us, double part_us, double part_bytes, int pairs);
+// How many parts: more than one where there are fewer tiles than pairs, or few in the last wave
 int fused_splits(int64_t tiles, int64_t stages, double stage_us, double tile_us, double part_us, double part_bytes, int pairs);
 // adds the parts in their order and does the epilogue; starts beside the kernel before it
 cudaError_t run_linear_join(const float* acc, int splits, int64_t M, int64_t N, bool gated, const LinearArgs& a, cudaStream_t st);

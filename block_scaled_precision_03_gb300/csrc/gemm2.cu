@@ -142,6 +142,7 @@ struct More {
     CUtensorMap z, u;              // outputs
     const float* ts_b;
     int32_t splits, split_stages;  // parts of the sum over K, and stages of each
+    int32_t tile_n;                // kLinear: columns of a pair's tile
     uint32_t op_tx;                // operand bytes one CTA loads per stage
     float* acc;                    // few tokens: the parts [split][token][ld_acc]
     int64_t ld_acc;
@@ -238,7 +239,8 @@ struct Tile2 {
 };
 
 template <int EPI>
-__device__ __forceinline__ Tile2 tile2(const Params2& p, int t, const GroupTable2* gt, int& gcur, uint32_t rank) {
+__device__ __forceinline__ Tile2 tile2(const Params2& p, int t, const GroupTable2* gt, int& gcur, uint32_t rank,
+                                       const typename MoreOf<EPI>::type& more) {
     Tile2 ti;
     if (p.num_groups == 0) {
         int mt, nt;
@@ -248,6 +250,10 @@ __device__ __forceinline__ Tile2 tile2(const Params2& p, int t, const GroupTable
         ti.nt = nt;
         ti.b_row = EPI == kGated ? nt * 128 : nt * BN + (int)rank * 128;
         ti.sfb_band = EPI == kGated ? nt : nt * 2;
+        if constexpr (EPI == kLinear) {
+            ti.b_row = nt * more.tile_n + (int)rank * (more.tile_n / 2);
+            ti.sfb_band = nt * (more.tile_n / 128);
+        }
         ti.row_lo = ti.a_band * 128;
         ti.row_hi = min(p.M, ti.row_lo + 128);
     } else {
@@ -397,7 +403,7 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
             for (int t = cid; t < total && ok; t += ncl) {
                 int tile = t;
                 const Part pt = part_of<EPI>(p, more, tile);
-                const Tile2 ti = tile2<EPI>(p, tile, gt, gcur, rank);
+                const Tile2 ti = tile2<EPI>(p, tile, gt, gcur, rank, more);
                 const int arow = ti.a_row, brow = ti.b_row;
                 const CUtensorMap* mb = &tmB;
                 if constexpr (EPI == kGated)
@@ -431,7 +437,7 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
             for (int t = cid; t < total && ok; t += ncl) {
                 int tile = t;
                 const Part pt = part_of<EPI>(p, more, tile);
-                const Tile2 ti = tile2<EPI>(p, tile, gt, gcur, rank);
+                const Tile2 ti = tile2<EPI>(p, tile, gt, gcur, rank, more);
                 for (int kb = pt.k0; kb < pt.k1; kb++) {
                     if (!wait_for<EPI>(sfree0 + 8 * stage, phase ^ 1, abort_flag, p.status, p.timeout_ns)) {
                         ok = false;
@@ -553,13 +559,15 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
         for (int t = cid; t < total; t += ncl, ++iter) {
             int tile = t;
             const Part pt = part_of<EPI>(p, more, tile);
-            const Tile2 ti = tile2<EPI>(p, tile, gt, gcur, rank);
+            const Tile2 ti = tile2<EPI>(p, tile, gt, gcur, rank, more);
             if (!wait_for<EPI>(tfull, iter & 1, abort_flag, p.status, p.timeout_ns)) break;
             tc::fence_after();
             uint32_t r[4][32];
-            // gated: 64 columns of the gate's, and up's 64 of the same columns
-            constexpr int OWN = EPI == kGated ? 64 : 128, SECOND = EPI == kGated ? 128 : 64;
-            const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * OWN);
+            // gated: 64 columns of the gate's, and up's 64 of the same columns; a tile of 128 columns: 64 (and 64 that say nothing)
+            constexpr int SECOND = EPI == kGated ? 128 : 64;
+            int own = EPI == kGated ? 64 : 128;
+            if constexpr (EPI == kLinear) own = more.tile_n / 2;
+            const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * own);
             BSQ_TMEM_LD32(r[0], ta);
             BSQ_TMEM_LD32(r[1], ta + 32);
             BSQ_TMEM_LD32(r[2], ta + SECOND);
@@ -607,13 +615,13 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
                 __syncwarp();
                 continue;
             } else if constexpr (EPI != kPlain) {
-                const int col0 = EPI == kGated ? ti.nt * 128 + h * 64 : ti.nt * BN + h * 128;
+                const int col0 = EPI == kGated ? ti.nt * 128 + h * 64 : ti.nt * more.tile_n + h * own;
                 if (row0 >= p.M || col0 >= p.N) continue;
                 // Two chunks of code, and r moves on: the epilogue is long.  (A copy of it for each of the four, fetched
                 // from memory the first time, made 512 -> 512 of 128 tokens 19.5 us, not 14.7; one copy in all is as
                 // fast there, and moves more: gated NVFP4 8192 x 4096 -> 14336 403 us, 383 with two.)
 #pragma unroll 1
-                for (int b = 0; b < OWN && col0 + b < p.N; b += 64) {
+                for (int b = 0; b < own && col0 + b < p.N; b += 64) {
 #pragma unroll
                     for (int c = 0; c < 64; c += 32) {
                         const int col = col0 + b + c;
@@ -625,7 +633,7 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
                             u[j] = EPI == kGated ? __uint_as_float(r[2 + c / 32][j]) * alpha * beta2 : 0.0f;
                         }
                         if (more.splits > 1) {
-                            const int at = ti.nt * BN + h * OWN + b + c;
+                            const int at = EPI == kGated ? ti.nt * BN + h * 64 + c : col;
                             pair::store_part(v, stage_out, &tmC, at, row0, pt.split, lane);
                             if (EPI == kGated) pair::store_part(u, stage_out, &tmC, at + 128, row0, pt.split, lane);
                         } else if (EPI == kGated) {
@@ -869,6 +877,35 @@ cudaError_t launch_kind(const Setup& s, const CUtensorMap& tc_, const More& more
     if (s.kind == kKindMX4) return launch2<kKindMX4, EPI>(s.p, s.ta, s.tb, s.tsa, s.tsb, tc_, more, 2 * pairs, st);
     return launch2<kKindFP8, EPI>(s.p, s.ta, s.tb, s.tsa, s.tsb, tc_, more, 2 * pairs, st);
 }
+// A tile's columns, and the parts of the sum over K.  A stage (K = 256) takes 0.72 us of MXFP8, 0.6 of MXFP4 or NVFP4, and
+// of 128 columns three quarters of it; with few tokens it is the pair's share of the weights' stream.  Between two tiles the
+// one accumulator is read out, and the last tile's epilogue is waited for.  (MXFP8, 256 and 128 columns: 660 x 160 -> 481
+// with residual 18 and 11 us, 1024 x 1024 -> 1024 10.5 and 8.9; 512 x 4096 -> 14336 31 and 36.)
+struct Cut {
+    int tile_n, splits;
+};
+Cut fused_cut(int fmt, int64_t tokens, int64_t out, int64_t cols, bool gated, int num_sms) {
+    const bool few = !gated && tokens <= kFewTokens, fp4 = fmt >= kMXFP4;
+    const int64_t stages = (cols + 255) / 256;
+    const double part_bytes = (double)tokens * fused_acc_cols(out, gated) * 8;
+    const int pairs = std::max(1, num_sms / 2);
+    if (few) return {BN, fused_splits((out + 255) / 256, stages, fp4 ? 0.45 : 0.82, 1.5, 0.0, part_bytes, pairs)};
+    static constexpr struct { int n; double stage_us, tile_us, end_us; } kWidths[] = {{256, 1.0, 1.5, 5.0}, {128, 0.76, 1.5, 2.5}};
+    Cut best{};
+    double least = 0.0;
+    for (const auto& w : kWidths) {
+        if (gated && w.n != 256) break;
+        const int64_t tiles = (tokens + 255) / 256 * ((out + (gated ? 127 : w.n - 1)) / (gated ? 128 : w.n));
+        const double stage_us = w.stage_us * (fp4 ? 0.6 : 0.72);
+        const int splits = fused_splits(tiles, stages, stage_us, w.tile_us, 0.0, part_bytes, pairs);
+        const double us = split_us(tiles, stages, splits, stage_us, w.tile_us, 0.0, part_bytes, pairs) + w.end_us;
+        if (least == 0.0 || us < least) {
+            least = us;
+            best = {w.n, splits};
+        }
+    }
+    return best;
+}
 // a: the tokens and w, or the gate's weights; up: the tokens and up's weights
 template <bool GATED>
 cudaError_t fused(const GemmArgs& a, const GemmArgs& up, const LinearArgs& l, cudaStream_t st) {
@@ -891,12 +928,16 @@ cudaError_t fused(const GemmArgs& a, const GemmArgs& up, const LinearArgs& l, cu
     Setup s;
     More more{};
     const uint32_t x_rows = (uint32_t)std::min<int64_t>(128, (a.M + 7) / 8 * 8);
-    if (!set_up(s, q, GATED ? 1 : 2, few ? 128 : x_rows, few ? x_rows : 128)) return cudaErrorInvalidValue;
-    more.op_tx = (128 + x_rows) * BKB * (s.kind == kKindFP8 ? Cfg2<kKindFP8>::KSUB : Cfg2<kKindNV>::KSUB);
+    const Cut cut = fused_cut(a.fmt_a, a.M, a.N, a.K, GATED, a.num_sms);
+    const uint32_t w_rows = few || GATED ? 128u : (uint32_t)cut.tile_n / 2;
+    if (!set_up(s, q, GATED ? 1 : 2, few ? w_rows : x_rows, few ? x_rows : w_rows)) return cudaErrorInvalidValue;
+    more.op_tx = (w_rows + x_rows) * BKB * (s.kind == kKindFP8 ? Cfg2<kKindFP8>::KSUB : Cfg2<kKindNV>::KSUB);
     if (GATED && !operand_b(s, more.b, more.sfb, up.b_codes, up.b_scales, a.N, 1)) return cudaErrorInvalidValue;
     Params2& p = s.p;
-    const int splits = gemm_fused_splits(a.fmt_a, a.M, a.N, a.K, GATED, a.num_sms);
-    const int64_t n_tiles = few ? 1 : GATED ? (a.N + 127) / 128 : (a.N + BN - 1) / BN;
+    const int splits = cut.splits;
+    const int64_t n_tiles = few ? 1 : GATED ? (a.N + 127) / 128 : (a.N + cut.tile_n - 1) / cut.tile_n;
+    more.tile_n = cut.tile_n;
+    if (!GATED && !few) p.idesc = (p.idesc & ~(0x3Fu << 17)) | ((uint32_t)(cut.tile_n >> 3) << 17);
     if (p.m_tiles * n_tiles * splits > 0x7FFFFFFF) return cudaErrorInvalidValue;
     p.n_tiles = (int32_t)n_tiles;
     p.total_tiles = (int32_t)(p.m_tiles * n_tiles * splits);
@@ -923,18 +964,9 @@ cudaError_t fused(const GemmArgs& a, const GemmArgs& up, const LinearArgs& l, cu
 
 }  // namespace
 
-// parts of the sum over K: a stage (K = 256) takes 0.4 us of MXFP8 or MXFP4, 0.45 of NVFP4; with few tokens it is
-// the pair's share of the weights' stream; between two tiles the one accumulator is read out
-int gemm_fused_splits(int fmt, int64_t tokens, int64_t out, int64_t cols, bool gated, int num_sms) {
-    const bool few = !gated && tokens <= kFewTokens, fp4 = fmt >= kMXFP4;
-    const int64_t tiles = few ? (out + 255) / 256
-                              : (tokens + 255) / 256 * ((out + (gated ? 127 : 255)) / (gated ? 128 : 256));
-    const double us = few ? (fp4 ? 0.45 : 0.82) : fmt == kNVFP4 ? 0.45 : 0.4;
-    return fused_splits(tiles, (cols + 255) / 256, us, 1.5, 0.0, (double)tokens * fused_acc_cols(out, gated) * 8, num_sms / 2);
-}
 size_t gemm_fused_workspace(int fmt, int64_t tokens, int64_t out, int64_t cols, bool gated, int num_sms) {
     if (tokens <= kScaledGemvTokens) return 0;
-    const int n = gemm_fused_splits(fmt, tokens, out, cols, gated, num_sms);
+    const int n = fused_cut(fmt, tokens, out, cols, gated, num_sms).splits;
     return n > 1 ? (size_t)n * tokens * fused_acc_cols(out, gated) * 4 : 0;
 }
 cudaError_t run_gemm_linear(const GemmArgs& a, const LinearArgs& l, cudaStream_t st) { return fused<false>(a, a, l, st); }

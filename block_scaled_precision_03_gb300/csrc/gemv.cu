@@ -224,7 +224,7 @@ cudaError_t run_scaled_gemv(const GemmArgs& a, const GemmArgs& up, const LinearA
     fused_args(p.f, l);
     const int64_t tasks = (a.N + 127) / 128 * 32;
     p.parts = 1;
-    while (p.parts < kWarps && tasks * p.parts * p.T < (int64_t)a.num_sms * 64) p.parts *= 2;
+    while (p.parts < kWarps && tasks * p.parts * p.T < (int64_t)a.num_sms * 64 && p.vectors > 32 * p.parts) p.parts *= 2;
     p.part = ((p.vectors + p.parts - 1) / p.parts + 31) / 32 * 32;
     const dim3 grid((unsigned)((tasks * p.parts + kWarps - 1) / kWarps));
     if (kind == kNV) return gated ? launch<kNV, true>(p, grid, st) : launch<kNV, false>(p, grid, st);

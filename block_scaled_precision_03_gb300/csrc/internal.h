@@ -216,7 +216,6 @@ cudaError_t run_linear_backward(const LinearArgs& a, bool gated, cudaStream_t st
 constexpr int kGemvTokens = 4, kScaledGemvTokens = 2;      // up to so many go to the CUDA cores
 
 // ---- the same on block-scaled operands (gemm2.cu, gemv.cu); the LinearArgs say what the epilogue does
-int gemm_fused_splits(int fmt, int64_t tokens, int64_t out, int64_t cols, bool gated, int num_sms);
 size_t gemm_fused_workspace(int fmt, int64_t tokens, int64_t out, int64_t cols, bool gated, int num_sms);
 cudaError_t run_scaled_gemv(const GemmArgs& a, const GemmArgs& up, const LinearArgs& l, bool gated, cudaStream_t st);
 cudaError_t run_gemm_linear(const GemmArgs& a, const LinearArgs& l, cudaStream_t st);

@@ -872,12 +872,6 @@ constexpr double kPartUs = 4.0;                     // the epilogue of a part's 
 struct Cut {
     int tile_m, tile_n, splits;
 };
-// the busiest pair's time, and the join's: its launch, and the parts written and read
-double split_us(int64_t tiles, int64_t stages, int64_t n, double stage_us, double tile_us, double part_us, double part_bytes, int pairs) {
-    const double tile = div_up(stages, n) * stage_us + tile_us;
-    if (n == 1) return div_up(tiles, pairs) * tile;
-    return tile + (div_up(tiles * n, pairs) - 1) * std::max(tile, part_us) + 2.0 + n * part_bytes / 6.7e6;
-}
 // How a product is cut: rows and columns of a pair's tile, and parts of the sum over K.  The estimate: what the
 // busiest pair computes, and the last tile's epilogue.  A narrower tile's stage is not shorter in proportion (the MMAs
 // of few columns wait for A's rows, and cost the issuing thread the same), but the tiles fill the pairs better: 4096 x
@@ -975,12 +969,13 @@ cudaError_t gemv(const LinearArgs& a, cudaStream_t st) {
     p.T = (int32_t)a.tokens;
     p.vectors = a.cols / 8;
     fused_args(p.f, a);
-    // a row's columns are shared by several warps where the rows alone would not fill the SMs a few times over
+    // a row's columns are shared by several warps where the rows alone would not fill the SMs a few times over, and every
+    // lane has some (288 -> 8625 with each of eight warps on 36 vectors 6.2 us, 3.0 with one)
     // (gated, 1 token of 4096 -> 14336: 36.3 us with two, 38.0 with one; 4 tokens 45.8 with one, 49.8 with two)
     constexpr int WARPS = kGemvThreads / 32;
     const int64_t tasks = div_up(a.out, GATED ? kRows / 2 : kRows);
     p.parts = 1;
-    while (p.parts < WARPS && tasks * p.parts * p.T < (int64_t)a.num_sms * 64) p.parts *= 2;
+    while (p.parts < WARPS && tasks * p.parts * p.T < (int64_t)a.num_sms * 64 && p.vectors > 32 * p.parts) p.parts *= 2;
     p.part = up(div_up(p.vectors, p.parts), 32);
     const dim3 grid((unsigned)div_up(tasks, WARPS / p.parts));
     if (p.T == 1) return launch_k(true, linear_gemv_kernel<1, GATED>, grid, kGemvThreads, 0, st, p);
@@ -1169,6 +1164,11 @@ int64_t fused_acc_cols(int64_t N, bool gated) { return gated ? div_up(N, 128) * 
 int fused_parts(int64_t stages, int64_t n) {
     const int64_t per = div_up(stages, n);
     return (int)div_up(stages, per);
+}
+double split_us(int64_t tiles, int64_t stages, int64_t n, double stage_us, double tile_us, double part_us, double part_bytes, int pairs) {
+    const double tile = div_up(stages, n) * stage_us + tile_us;
+    if (n == 1) return div_up(tiles, pairs) * tile;
+    return tile + (div_up(tiles * n, pairs) - 1) * std::max(tile, part_us) + 2.0 + n * part_bytes / 6.7e6;
 }
 int fused_splits(int64_t tiles, int64_t stages, double stage_us, double tile_us, double part_us, double part_bytes, int pairs) {
     int64_t best = 1;
