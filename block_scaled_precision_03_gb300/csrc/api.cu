@@ -50,6 +50,10 @@ size_t scales_bytes(int32_t f, int64_t r, int64_t c) {
 }
 bool scales_padded(int32_t f, int64_t r, int64_t c) { return (r % 128) != 0 || ((c / blk(f)) % 4) != 0; }
 
+// sizes of a product with an epilogue
+bool fused_supported(int64_t tokens, int64_t out) {
+    return tokens <= 0x7FFFFF00LL && out <= bsq::kLinearMax && tokens * out <= bsq::kLinearMaxElements;
+}
 // a tensor descriptor is usable as a quantized operand
 bsq_status check_tensor(const bsq_tensor* t, bool need_ts) {
     if (!t || !valid_fmt(t->fmt) || t->reserved != 0) return BSQ_ERR_INVALID_ARG;
@@ -248,9 +252,6 @@ bsq_status bsq_gemm(const bsq_tensor* A, const bsq_tensor* B, void* C, int32_t o
 static bsq_status check_out(const void* p, int64_t ld, int32_t type, int64_t cols) {
     if (ld < cols) return BSQ_ERR_INVALID_ARG;
     return reinterpret_cast<uintptr_t>(p) % (type == BSQ_OUT_BF16 ? 2 : 4) ? BSQ_ERR_ALIGNMENT : BSQ_OK;
-}
-static bool fused_supported(int64_t tokens, int64_t out) {
-    return tokens <= 0x7FFFFF00LL && out <= bsq::kLinearMax && tokens * out <= bsq::kLinearMaxElements;
 }
 static size_t fused_bytes(int32_t fmt, int64_t tokens, int64_t out, int64_t cols, bool gated) {
     if (!valid_fmt(fmt) || tokens < 1 || out < 1 || cols < 1 || !fused_supported(tokens, out)) return 0;
