@@ -48,10 +48,7 @@ namespace {
 
 using namespace pair;
 
-enum { kFwd, kDx, kDw };
-// When a product waits for the kernel before it on the stream, whose dependent it is: before it reads or writes anything
-// (its set-up runs earlier), or at its end (it needs nothing of that kernel, and runs beside it).
-enum { kWaitStart, kWaitEnd };
+enum { kFwd, kGrad };
 
 constexpr int kStages = 3;
 constexpr int kMaxStages = 12;                      // of smaller tiles: as many as fit
@@ -62,12 +59,10 @@ constexpr int kMmas = 4 * kSub;                     // per stage
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr uint32_t kTmemCols = 512;
+constexpr int kBarBytes = 320;
 constexpr int kStageBytes = 4096;                   // a warp's staging: two chunks of 32 rows x 64 bytes
-constexpr int kSmem = 1024 + kStages * 2 * kOpBytes + kEpiWarps * kStageBytes + 256;
+constexpr int kSmem = 1024 + kStages * 2 * kOpBytes + kEpiWarps * kStageBytes + kBarBytes;
 static_assert(kSmem <= 232448, "shared memory per block");
-
-__host__ __device__ constexpr bool a_mn(int mode) { return mode == kDw; }
-__host__ __device__ constexpr bool b_mn(int mode) { return mode == kDx || mode == kDw; }
 
 struct Params {
     int64_t M, N;                  // output
@@ -75,34 +70,90 @@ struct Params {
     int32_t m_tiles, n_tiles, splits, split_stages, total;
     int32_t raster, raster_n;
     int32_t tile_m, tile_n;
-    int32_t stages, a_bytes, b_bytes;  // stages of the ring, one CTA's bytes of A and B per stage
-    int32_t half;                  // kDx gated: stages of the first pair of operands; kDw gated: its tiles along M
-    uint32_t tx;                   // bytes one CTA loads per stage
-    int32_t wait;
+    int32_t sub_a, sub_b;          // one CTA's bytes of A and B per sub-step
+    int32_t half;                  // gated: dx's stages of the first pair of operands; dw's tiles along M
     Fused f;
+};
+struct Job {
+    CUtensorMap a[2], b[2], out[3];
+    Params p;
+};
+// A forward product, or a gradient's two: dx and dw in one launch, whose tiles follow one another (no tiles: not wanted).
+// Small gradients gain by it (294 x 80 -> 576 5.8 us, two launches 8.3; 2048 x 4096 -> 4096 100, 112); of many tiles each
+// has a launch (8192 x 4096 -> 14336 1.03 ms, 1.06 in one: the two then share L2 for longer).
+template <int MODE>
+struct Jobs {
+    Job job[MODE == kFwd ? 1 : 2];
+    int32_t stages, a_bytes, b_bytes;  // stages of the ring, and its room for one CTA's A and B per stage
+    int32_t extra;                 // dw's tiles that a pair with one of dx's fewer takes in its place
+    // When it waits for the kernel before it on the stream, whose dependent it is: before it reads or writes anything (its
+    // set-up runs earlier), or at its end (it needs nothing of that kernel, and runs beside it).
+    int32_t wait_end;
     unsigned* status;
     uint64_t timeout_ns;
 };
-struct Maps {
-    CUtensorMap a[2], b[2], out[3];
-};
+// A pair's i-th tile, dx's first, each dealt in turn.  Where dx's last round does not reach every pair, the others take
+// `extra` tiles of dw in its place, and the rest goes round from the first of them.
+template <int MODE>
+__device__ __forceinline__ bool nth_tile(const Jobs<MODE>& j, int cid, int ncl, int i, bool& dw, int& t) {
+    const int n = j.job[0].p.total;
+    t = cid + i * ncl;
+    dw = false;
+    if (MODE == kFwd || t < n) return t < n;
+    dw = true;
+    const int all = j.job[MODE].p.total, rest = n % ncl, light = ncl - rest;
+    int k = i - (cid < n ? (n - cid + ncl - 1) / ncl : 0);
+    if (cid >= rest) {
+        t = cid - rest + k * light;
+        if (k < j.extra) return t < all;
+        k -= j.extra;
+    }
+    t = j.extra * light + (cid >= rest ? cid - rest : cid - rest + ncl) + k * ncl;
+    return t < all;
+}
+// After an abort, as pair::drain_loads: loads of a stage, of the same size or of sizes that the CTA which issued them noted
+// per slot
+__device__ __noinline__ void drain_ring(uint32_t full0, int stages, int n_own, int n_peer, const volatile uint32_t* tx, uint32_t peer_tx,
+                                        uint32_t same) {
+    const int n = max(n_own, n_peer);
+    for (int k = max(0, n - stages); k < n; k++) {
+        const int s = k % stages;
+        const uint32_t bar = full0 + 8 * (uint32_t)s;
+        const uint32_t bytes = same ? same : k < n_own ? tx[s] : (uint32_t)tc::ld_cluster_s32(peer_tx + 4 * (uint32_t)s);
+        if (k < n_own && k >= n_peer) tc::mbar_complete_tx(bar, bytes);
+        if (k < n_peer && k >= n_own) tc::mbar_expect_tx(bar, bytes);
+        volatile int no_abort = 0;
+        tc::mbar_wait(bar, (uint32_t)((k / stages) & 1), &no_abort, nullptr, 100000000ull);
+    }
+}
 
 int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 int64_t div_up(int64_t v, int64_t m) { return (v + m - 1) / m; }
 
+// Reads a line of each part of a job, so that its parameters are there when the wait for the kernel before is over
+__device__ __forceinline__ void read_ahead(const Params& p) {
+    asm volatile("" :: "l"(p.M), "r"(p.k_stages), "r"(p.raster), "r"(p.tile_n), "r"(p.sub_b), "r"(p.f.act), "l"(p.f.bias), "l"(p.f.y),
+                 "l"(p.f.u));
+}
+template <uint32_t V>
+struct Constant {
+    static constexpr uint32_t value = V;
+};
+
 // LONG: a tile's sum over K takes several accumulators.
 template <int MODE, bool GATED, bool LONG>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-linear_gemm_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Params p) {
+linear_gemm_kernel(const __grid_constant__ Jobs<MODE> j) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     // [stages] of A, [stages] of B, the epilogue's staging; the barriers come last
-    const int S = p.stages, a_bytes = p.a_bytes, b_bytes = p.b_bytes, sub_a = a_bytes / kSub, sub_b = b_bytes / kSub;
+    constexpr bool GRAD = MODE == kGrad;
+    const int S = j.stages, a_bytes = j.a_bytes, b_bytes = j.b_bytes;
     uint8_t* smA = base;
     uint8_t* smB = smA + S * a_bytes;
     uint8_t* smOut = base + kStages * 2 * kOpBytes;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(base + (kSmem - 1024 - 256));
-    // full[S], empty[S], tfull[2], tempty[2], drain
+    uint64_t* bars = reinterpret_cast<uint64_t*>(base + (kSmem - 1024 - kBarBytes));
+    // full[S], empty[S], tfull[2], tempty[2], drain, and the bytes of a load per stage
     const uint32_t full0 = tc::smem_u32(bars), empty0 = tc::smem_u32(bars + kMaxStages);
     const uint32_t tfull0 = tc::smem_u32(bars + 2 * kMaxStages), tempty0 = tc::smem_u32(bars + 2 * kMaxStages + 2);
     const uint32_t drain = tc::smem_u32(bars + 2 * kMaxStages + 4);
@@ -110,14 +161,16 @@ linear_gemm_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Para
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     volatile int* issued_slot = reinterpret_cast<volatile int*>(tmem_slot + 2);
     volatile int* peer_abort = reinterpret_cast<volatile int*>(tmem_slot + 3);
-    static_assert(8 * (2 * kMaxStages + 5) + 16 <= 256, "barrier area");
+    volatile uint32_t* load_tx = tmem_slot + 4;
+    static_assert(8 * (2 * kMaxStages + 5) + 16 + 4 * kMaxStages <= kBarBytes, "barrier area");
 
-    if (p.wait != kWaitStart) pdl_launch_dependents();
+    if (j.wait_end) pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_rank();
     const bool leader = rank == 0;
     const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
-
+    const Job& ahead = j.job[GRAD && cid >= j.job[0].p.total];
+    read_ahead(ahead.p);
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < S; s++) {
             tc::mbar_init(full0 + 8 * s, 1);
@@ -132,8 +185,8 @@ linear_gemm_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Para
         *issued_slot = 0;
         *peer_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        tc::prefetch_tmap(&tm.a[0]);
-        tc::prefetch_tmap(&tm.b[0]);
+        tc::prefetch_tmap(&ahead.a[0]);
+        tc::prefetch_tmap(&ahead.b[0]);
     }
     if (warp == 1) tc::tmem_alloc<2>(tc::smem_u32(tmem_slot), kTmemCols);
     tc::fence_before();
@@ -149,42 +202,48 @@ linear_gemm_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Para
             int stage = 0, issued = 0;
             uint32_t phase = 0;
             bool ok = true;
-            if (p.wait == kWaitStart) {
+            if (!j.wait_end) {
                 pdl_wait();
                 pdl_launch_dependents();
             }
-            for (int t = cid; t < p.total && ok; t += ncl) {
+            bool dw;
+            for (int i = 0, t; ok && nth_tile(j, cid, ncl, i, dw, t); i++) {
+                const Job& job = j.job[dw];
+                const Params& p = job.p;
                 const TileAt ti = tile_at(p, t);
                 // which of the two operand pairs of a gated layer's dw
-                const int which = MODE == kDw && GATED && ti.mt >= p.half ? 1 : 0;
+                const int which = GATED && dw && ti.mt >= p.half ? 1 : 0;
                 const int am = (ti.mt - which * p.half) * p.tile_m + (int)rank * (p.tile_m / 2);
                 // a gated layer's tile is half as many columns of either projection
-                const int bn = MODE == kFwd && GATED ? ti.nt * (p.tile_n / 2) : ti.nt * p.tile_n + (int)rank * (p.tile_n / 2);
-                const CUtensorMap* mb = MODE == kFwd && GATED ? &tm.b[rank] : &tm.b[0];
+                const int bn = !GRAD && GATED ? ti.nt * (p.tile_n / 2) : ti.nt * p.tile_n + (int)rank * (p.tile_n / 2);
+                const int half = GATED && GRAD && !dw ? p.half : ti.k1, sub_a = p.sub_a, sub_b = p.sub_b;
+                const uint32_t tx = (uint32_t)(kSub * (sub_a + sub_b));
+                const bool wide = p.tile_n > 128;
                 for (int kb = ti.k0; kb < ti.k1; kb++) {
-                    if (!wait(empty0 + 8 * stage, phase ^ 1, abort_flag, p.status, p.timeout_ns)) {
+                    if (!wait(empty0 + 8 * stage, phase ^ 1, abort_flag, j.status, j.timeout_ns)) {
                         ok = false;
                         break;
                     }
                     const uint32_t fb = full_c0 + 8 * stage;
-                    if (leader) tc::mbar_expect_tx(full0 + 8 * stage, 2 * p.tx);
-                    const int second = MODE == kDx && GATED && kb >= p.half ? 1 : 0;
-                    const CUtensorMap* ma = MODE == kDx && GATED ? &tm.a[second] : &tm.a[which];
-                    if (MODE == kDx && GATED) mb = &tm.b[second];
+                    if (GRAD) load_tx[stage] = tx;
+                    if (leader) tc::mbar_expect_tx(full0 + 8 * stage, 2 * tx);
+                    const int second = GRAD && GATED && kb >= half ? 1 : 0;        // dx of a gated layer
+                    const CUtensorMap* ma = &job.a[GRAD ? (dw ? which : second) : 0];
+                    const CUtensorMap* mb = &job.b[GRAD ? second : GATED ? (int)rank : 0];
 #pragma unroll
-                    for (int j = 0; j < kSub; j++) {
-                        const int k = ((kb - second * p.half) * kSub + j) * kSubK;
-                        const uint32_t da = tc::smem_u32(smA + stage * a_bytes + j * sub_a);
-                        const uint32_t db = tc::smem_u32(smB + stage * b_bytes + j * sub_b);
-                        if (a_mn(MODE)) {
+                    for (int u = 0; u < kSub; u++) {
+                        const int k = ((kb - second * half) * kSub + u) * kSubK;
+                        const uint32_t da = tc::smem_u32(smA + stage * a_bytes + u * sub_a);
+                        const uint32_t db = tc::smem_u32(smB + stage * b_bytes + u * sub_b);
+                        if (dw) {
                             tc::tma_load_2d_pair(da, ma, am, k, fb);
                             tc::tma_load_2d_pair(da + 8192, ma, am + 64, k, fb);
                         } else {
                             tc::tma_load_2d_pair(da, ma, k, am, fb);
                         }
-                        if (b_mn(MODE)) {
+                        if (GRAD) {
                             tc::tma_load_2d_pair(db, mb, bn, k, fb);
-                            if (p.tile_n > 128) tc::tma_load_2d_pair(db + 8192, mb, bn + 64, k, fb);
+                            if (wide) tc::tma_load_2d_pair(db + 8192, mb, bn + 64, k, fb);
                         } else {
                             tc::tma_load_2d_pair(db, mb, k, bn, fb);
                         }
@@ -199,50 +258,58 @@ linear_gemm_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Para
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer (even CTA)
         if (lane == 0 && leader) {
-            const uint32_t idesc = idesc_bf16(a_mn(MODE), b_mn(MODE)) | ((uint32_t)(p.tile_n >> 3) << 17);
-            // 16 k further: 32 bytes of a K-major row, 16 rows of an MN-major tile
-            constexpr uint32_t a_step = a_mn(MODE) ? 2048 >> 4 : 2, b_step = b_mn(MODE) ? 2048 >> 4 : 2;
-            const uint64_t ad0 = a_mn(MODE) ? desc_mn_sw128(tc::smem_u32(smA)) : tc::desc_sw128(tc::smem_u32(smA));
-            const uint64_t bd0 = b_mn(MODE) ? desc_mn_sw128(tc::smem_u32(smB)) : tc::desc_sw128(tc::smem_u32(smB));
+            // K-major and MN-major operands; 16 k further: 32 bytes of a K-major row, 16 rows of an MN-major tile
+            constexpr uint32_t k_step = 2, mn_step = 2048 >> 4, b_step = GRAD ? mn_step : k_step;
+            const uint64_t bd0 = GRAD ? desc_mn_sw128(tc::smem_u32(smB)) : tc::desc_sw128(tc::smem_u32(smB));
             int stage = 0, iter = 0;
             uint32_t phase = 0;
             bool ok = true, any = false, ready = false;
-            if (p.wait == kWaitStart) pdl_wait();          // the limit of its waits counts from there
-            for (int t = cid; t < p.total && ok; t += ncl) {
+            if (!j.wait_end) pdl_wait();                   // the limit of its waits counts from there
+            bool dw;
+            for (int i = 0, t; ok && nth_tile(j, cid, ncl, i, dw, t); i++) {
+                const Params& p = j.job[dw].p;
                 const TileAt ti = tile_at(p, t);
-                for (int c0 = ti.k0; c0 < ti.k1 && ok; c0 += p.chunk, ++iter) {
-                    const int c1 = min(ti.k1, c0 + p.chunk), buf = iter & 1;
-                    if (!wait(tempty0 + 8 * buf, ((iter >> 1) & 1) ^ 1, abort_flag, p.status, p.timeout_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t d = tmem + (uint32_t)buf * kTile;
-                    for (int kb = c0; kb < c1; kb++) {
-                        if (!ready && !wait(full0 + 8 * stage, phase, abort_flag, p.status, p.timeout_ns)) {
+                const uint32_t idesc = idesc_bf16(dw, GRAD) | ((uint32_t)(p.tile_n >> 3) << 17);
+                const uint64_t ad0 = dw ? desc_mn_sw128(tc::smem_u32(smA)) : tc::desc_sw128(tc::smem_u32(smA));
+                const uint32_t sub_a = (uint32_t)p.sub_a >> 4, sub_b = (uint32_t)p.sub_b >> 4;
+                const int chunk = p.chunk;
+                const auto run = [&](auto a_step) {
+                    for (int c0 = ti.k0; c0 < ti.k1 && ok; c0 += chunk, ++iter) {
+                        const int c1 = min(ti.k1, c0 + chunk), buf = iter & 1;
+                        if (!wait(tempty0 + 8 * buf, ((iter >> 1) & 1) ^ 1, abort_flag, j.status, j.timeout_ns)) {
                             ok = false;
                             break;
                         }
-                        tc::fence_after();
-                        const Desc ad = Desc(ad0) + (uint32_t)(stage * (a_bytes >> 4));
-                        const Desc bd = Desc(bd0) + (uint32_t)(stage * (b_bytes >> 4));
-                        const int next = stage + 1 == S ? 0 : stage + 1;
-                        const uint32_t next_phase = next == 0 ? phase ^ 1 : phase;
-                        // the next stage's barrier is tested while this stage's MMAs run
+                        const uint32_t d = tmem + (uint32_t)buf * kTile;
+                        for (int kb = c0; kb < c1; kb++) {
+                            if (!ready && !wait(full0 + 8 * stage, phase, abort_flag, j.status, j.timeout_ns)) {
+                                ok = false;
+                                break;
+                            }
+                            tc::fence_after();
+                            const Desc ad = Desc(ad0) + (uint32_t)(stage * (a_bytes >> 4));
+                            const Desc bd = Desc(bd0) + (uint32_t)(stage * (b_bytes >> 4));
+                            const int next = stage + 1 == S ? 0 : stage + 1;
+                            const uint32_t next_phase = next == 0 ? phase ^ 1 : phase;
+                            // the next stage's barrier is tested while this stage's MMAs run
 #pragma unroll
-                        for (int m = 0; m < kMmas; m++) {
-                            if (m == kMmas - 1) ready = tc::mbar_test(full0 + 8 * next, next_phase);
-                            const Desc am = ad + (m >> 2) * (sub_a >> 4) + (m & 3) * a_step;
-                            const Desc bm = bd + (m >> 2) * (sub_b >> 4) + (m & 3) * b_step;
-                            if (m == 0) mma_bf16<false>(d, am, bm, idesc, kb != c0);
-                            else mma_bf16<true>(d, am, bm, idesc, 1);
+                            for (int m = 0; m < kMmas; m++) {
+                                if (m == kMmas - 1) ready = tc::mbar_test(full0 + 8 * next, next_phase);
+                                const Desc am = ad + (m >> 2) * sub_a + (m & 3) * a_step.value;
+                                const Desc bm = bd + (m >> 2) * sub_b + (m & 3) * b_step;
+                                if (m == 0) mma_bf16<false>(d, am, bm, idesc, kb != c0);
+                                else mma_bf16<true>(d, am, bm, idesc, 1);
+                            }
+                            any = true;
+                            tc::commit<2>(empty0 + 8 * stage, 3);
+                            if (kb == c1 - 1) tc::commit<2>(tfull0 + 8 * buf, 3);
+                            stage = next;
+                            phase = next_phase;
                         }
-                        any = true;
-                        tc::commit<2>(empty0 + 8 * stage, 3);
-                        if (kb == c1 - 1) tc::commit<2>(tfull0 + 8 * buf, 3);
-                        stage = next;
-                        phase = next_phase;
                     }
-                }
+                };
+                if (dw) run(Constant<mn_step>());
+                else run(Constant<k_step>());
             }
             if (!ok) *abort_flag = 1;
             if (any) {
@@ -257,17 +324,20 @@ linear_gemm_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Para
         const int q = warp & 3, half = (warp - 2) >> 2;
         const uint32_t tempty_c0 = tc::mapa(tempty0, 0);
         Staging<2> st{tc::smem_u32(smOut + (warp - 2) * kStageBytes), 0};
-        if (p.wait == kWaitStart) pdl_wait();
+        if (!j.wait_end) pdl_wait();
         int iter = 0;
         // A thread owns one row and half of the tile's columns in chunks of 32, at most 128 (gated: of each
         // projection's, at most 64); of an odd number of chunks the first half has one more
-        constexpr bool PROJ = MODE == kFwd && GATED;
-        const int cols = PROJ ? p.tile_n / 2 : p.tile_n, first = (cols / 32 + 1) / 2 * 32;
-        const int own = half == 0 ? first : cols - first;
-        const uint32_t second = PROJ ? (uint32_t)cols : 0;
-        for (int t = cid; t < p.total; t += ncl) {
+        constexpr bool PROJ = !GRAD && GATED;
+        bool dw;
+        for (int i = 0, t; nth_tile(j, cid, ncl, i, dw, t); i++) {
+            const Job& job = j.job[dw];
+            const Params& p = job.p;
             const TileAt ti = tile_at(p, t);
-            const int which = MODE == kDw && GATED && ti.mt >= p.half ? 1 : 0;
+            const int cols = PROJ ? p.tile_n / 2 : p.tile_n, first = (cols / 32 + 1) / 2 * 32;
+            const int own = half == 0 ? first : cols - first;
+            const uint32_t second = PROJ ? (uint32_t)cols : 0;
+            const int which = GATED && dw && ti.mt >= p.half ? 1 : 0;
             const int64_t row0 = (int64_t)(ti.mt - which * p.half) * p.tile_m + rank * (p.tile_m / 2) + q * 32;
             const int64_t col0 = (int64_t)ti.nt * cols + half * first;
             const bool live = q * 32 < p.tile_m / 2 && row0 < p.M && col0 < p.N;
@@ -277,18 +347,18 @@ linear_gemm_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Para
                 if (p.splits > 1) {
                     const int64_t at = PROJ ? gate_col(col0 + c) : col0 + c;
                     const int64_t r = row0 + (int64_t)which * p.half * kTile;
-                    store_part(v, st, &tm.out[0], (int)at, (int)r, ti.split, lane);
-                    if (PROJ) store_part(u, st, &tm.out[0], (int)at + 128, (int)r, ti.split, lane);
-                } else if (MODE != kFwd) {
-                    if (col0 + c < p.N) store_bf16(v, 1.0f, st.base, &tm.out[which], (int)col0 + c, (int)row0, st.n, lane);
+                    store_part(v, st, &job.out[0], (int)at, (int)r, ti.split, lane);
+                    if (PROJ) store_part(u, st, &job.out[0], (int)at + 128, (int)r, ti.split, lane);
+                } else if (GRAD) {
+                    if (col0 + c < p.N) store_bf16(v, 1.0f, st.base, &job.out[which], (int)col0 + c, (int)row0, st.n, lane);
                 } else if (col0 + c < p.N) {
-                    if (PROJ) finish_gated(v, u, p.f, &tm.out[0], &tm.out[1], &tm.out[2], row0, col0 + c, p.M, p.N, st, lane);
-                    else finish_linear(v, p.f, &tm.out[0], &tm.out[1], row0, col0 + c, p.M, p.N, st, lane);
+                    if (PROJ) finish_gated(v, u, p.f, &job.out[0], &job.out[1], &job.out[2], row0, col0 + c, p.M, p.N, st, lane);
+                    else finish_linear(v, p.f, &job.out[0], &job.out[1], row0, col0 + c, p.M, p.N, st, lane);
                 }
             };
             if constexpr (!LONG) {
                 const int buf = iter & 1;
-                if (!wait(tfull0 + 8 * buf, (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns)) break;
+                if (!wait(tfull0 + 8 * buf, (iter >> 1) & 1, abort_flag, j.status, j.timeout_ns)) break;
                 tc::fence_after();
                 ++iter;
                 if (live)
@@ -306,7 +376,7 @@ linear_gemm_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Para
                 float z[128] = {};
                 bool ok = true;
                 for (int c0 = ti.k0; c0 < ti.k1; c0 += p.chunk, ++iter) {
-                    ok = wait(tfull0 + 8 * (iter & 1), (iter >> 1) & 1, abort_flag, p.status, p.timeout_ns);
+                    ok = wait(tfull0 + 8 * (iter & 1), (iter >> 1) & 1, abort_flag, j.status, j.timeout_ns);
                     if (!ok) break;
                     tc::fence_after();
                     if (live)
@@ -339,7 +409,7 @@ linear_gemm_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Para
     }
 
     // what was launched before this kernel is done when this kernel is
-    if (p.wait == kWaitEnd) pdl_wait();
+    if (j.wait_end) pdl_wait();
     // Both CTAs have stopped issuing.  If either gave up, both know after the barrier, and the even CTA
     // waits (bounded) for the loads still in flight before either may exit.
     tc::fence_before();
@@ -348,7 +418,8 @@ linear_gemm_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Para
     tc::cluster_sync();
     if (*abort_flag || *peer_abort) {
         if (leader && warp == 0 && lane == 0)
-            drain_loads(full0, S, *issued_slot, tc::ld_cluster_s32(tc::mapa(tc::smem_u32((const void*)issued_slot), 1)), p.tx);
+            drain_ring(full0, S, *issued_slot, tc::ld_cluster_s32(tc::mapa(tc::smem_u32((const void*)issued_slot), 1)), load_tx,
+                       tc::mapa(tc::smem_u32((const void*)load_tx), 1), GRAD ? 0 : (uint32_t)(kSub * (j.job[0].p.sub_a + j.job[0].p.sub_b)));
         tc::cluster_sync();
     }
     if (warp == 1) {
@@ -850,22 +921,25 @@ __global__ void __launch_bounds__(256) linear_slope_kernel(const SlopeArgs a) {
     a.sums[(int64_t)blockIdx.x * a.cols + c] = s;
 }
 // dbias = the blocks' column sums in their order: 32 columns a CTA, eight threads each
-__global__ void __launch_bounds__(256) linear_bias_kernel(const float* sums, int64_t blocks, int64_t cols, float* out) {
+// (wait_end: beside the products, which waited for the sums)
+__global__ void __launch_bounds__(256) linear_bias_kernel(const float* sums, int64_t blocks, int64_t cols, float* out, int wait_end) {
     __shared__ float all[8][32];
     const int64_t c = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
     pdl_launch_dependents();
-    pdl_wait();
+    if (!wait_end) pdl_wait();
     float s = 0.0f;
     if (c < cols)
 #pragma unroll 4
         for (int64_t b = threadIdx.x >> 5; b < blocks; b += 8) s += sums[b * cols + c];
     all[threadIdx.x >> 5][threadIdx.x & 31] = s;
     __syncthreads();
-    if (threadIdx.x >= 32 || c >= cols) return;
-    s = 0.0f;
+    if (threadIdx.x < 32 && c < cols) {
+        s = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 8; w++) s += all[w][threadIdx.x];
-    out[c] = s;
+        for (int w = 0; w < 8; w++) s += all[w][threadIdx.x];
+        out[c] = s;
+    }
+    if (wait_end) pdl_wait();
 }
 
 constexpr double kPartUs = 4.0;                     // the epilogue of a part's tile, behind which the next tile's stages may hide
@@ -910,50 +984,69 @@ struct Operand {
 };
 
 template <int MODE, bool GATED, bool LONG>
-cudaError_t launch_gemm(const Params& p, const Maps& tm, int pairs, cudaStream_t st) {
+cudaError_t launch_gemm(const Jobs<MODE>& j, int pairs, cudaStream_t st) {
     static SharedMemory smem;
     const cudaError_t e = smem.allow(reinterpret_cast<const void*>(linear_gemm_kernel<MODE, GATED, LONG>), kSmem);
     if (e != cudaSuccess) return e;
-    return launch_k(true, linear_gemm_kernel<MODE, GATED, LONG>, dim3(2 * pairs), kThreads, kSmem, st, tm, p);
+    return launch_k(true, linear_gemm_kernel<MODE, GATED, LONG>, dim3(2 * pairs), kThreads, kSmem, st, j);
 }
-// K: the depth of each operand pair
-template <int MODE, bool GATED>
-cudaError_t gemm(Params p, const Operand (&a)[2], const Operand (&b)[2], Maps& tm, int64_t K, const Cut& cut, int wait,
-                 bool fine, const LinearArgs& args, cudaStream_t st) {
+enum { kProduct, kDx, kDw };
+// A job but for its outputs; K: the depth of each operand pair
+template <int KIND, bool GATED>
+bool set_up(Job& job, const Operand (&a)[2], const Operand (&b)[2], int64_t M, int64_t N, int64_t K, const Cut& cut, bool fine, int num_sms) {
+    constexpr bool A_MN = KIND == kDw, B_MN = KIND != kProduct;
     const int tile_n = cut.tile_n;
     // the second operands where there are any
-    constexpr bool TWO_A = GATED && MODE != kFwd, TWO_B = GATED && (MODE == kFwd || MODE == kDx);
+    constexpr bool TWO_A = GATED && KIND != kProduct, TWO_B = GATED && KIND != kDw;
     for (int i = 0; i < 2; i++) {
-        if ((i == 0 || TWO_A) && !map_operand(&tm.a[i], a[i].p, a[i].rows, a[i].cols, a[i].ld, a_mn(MODE) ? kSubK : cut.tile_m / 2))
-            return cudaErrorInvalidValue;
-        if ((i == 0 || TWO_B) && !map_operand(&tm.b[i], b[i].p, b[i].rows, b[i].cols, b[i].ld, b_mn(MODE) ? kSubK : tile_n / 2))
-            return cudaErrorInvalidValue;
+        if ((i == 0 || TWO_A) && !map_operand(&job.a[i], a[i].p, a[i].rows, a[i].cols, a[i].ld, A_MN ? kSubK : cut.tile_m / 2)) return false;
+        if ((i == 0 || TWO_B) && !map_operand(&job.b[i], b[i].p, b[i].rows, b[i].cols, b[i].ld, B_MN ? kSubK : tile_n / 2)) return false;
     }
+    Params& p = job.p;
+    p.M = M;
+    p.N = N;
     const int64_t stages = div_up(K, kSub * kSubK);
-    p.half = MODE == kDx ? (int32_t)stages : (int32_t)div_up(p.M, cut.tile_m);
-    p.k_stages = (int32_t)(MODE == kDx && GATED ? 2 * stages : stages);
+    p.half = KIND == kDx ? (int32_t)stages : (int32_t)div_up(M, cut.tile_m);
+    p.k_stages = (int32_t)(KIND == kDx && GATED ? 2 * stages : stages);
     p.tile_m = cut.tile_m;
     p.tile_n = tile_n;
     // (of an MN-major operand whole boxes of 64 columns)
-    p.b_bytes = kSub * (int)(b_mn(MODE) ? up(tile_n / 2, 64) : tile_n / 2) * kSubK * 2;
-    p.a_bytes = kSub * (cut.tile_m / 2) * kSubK * 2;
-    p.stages = std::min(kMaxStages, kStages * 2 * kOpBytes / (p.a_bytes + p.b_bytes));
-    p.tx = (uint32_t)(p.a_bytes + p.b_bytes);
-    p.m_tiles = (int32_t)div_up(p.M, cut.tile_m) * (MODE == kDw && GATED ? 2 : 1);
-    p.n_tiles = (int32_t)div_up(p.N, MODE == kFwd && GATED ? tile_n / 2 : tile_n);
+    p.sub_a = cut.tile_m / 2 * kSubK * 2;
+    p.sub_b = (int)(B_MN ? up(tile_n / 2, 64) : tile_n / 2) * kSubK * 2;
+    p.m_tiles = (int32_t)div_up(M, cut.tile_m) * (KIND == kDw && GATED ? 2 : 1);
+    p.n_tiles = (int32_t)div_up(N, KIND == kProduct && GATED ? tile_n / 2 : tile_n);
     p.split_stages = (int32_t)div_up(p.k_stages, cut.splits);
     p.splits = (int32_t)div_up(p.k_stages, p.split_stages);
     p.chunk = fine ? kChunk : kSumChunk;
     const int64_t total = (int64_t)p.m_tiles * p.n_tiles * p.splits;
-    if (total > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    if (total > 0x3FFFFFFF) return false;
     p.total = (int32_t)total;
-    p.wait = wait;
-    p.status = args.status;
-    p.timeout_ns = args.timeout_ns;
-    const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(args.num_sms / 2, total));
-    choose_raster(p, K, pairs);
-    if (p.split_stages <= p.chunk) return launch_gemm<MODE, GATED, false>(p, tm, pairs, st);
-    return launch_gemm<MODE, GATED, true>(p, tm, pairs, st);
+    choose_raster(p, K, (int)std::max<int64_t>(1, std::min<int64_t>(num_sms / 2, total)));
+    return true;
+}
+template <int MODE, bool GATED>
+cudaError_t gemm(Jobs<MODE>& j, const LinearArgs& args, cudaStream_t st) {
+    int total = 0;
+    bool is_long = false;
+    for (const Job& job : j.job) {
+        const Params& p = job.p;
+        total += p.total;
+        if (!p.total) continue;
+        is_long |= p.split_stages > p.chunk;
+        j.a_bytes = std::max(j.a_bytes, kSub * p.sub_a);
+        j.b_bytes = std::max(j.b_bytes, kSub * p.sub_b);
+    }
+    j.stages = std::min(kMaxStages, kStages * 2 * kOpBytes / (j.a_bytes + j.b_bytes));
+    j.status = args.status;
+    j.timeout_ns = args.timeout_ns;
+    const int pairs = std::max(1, std::min(args.num_sms / 2, total));
+    if (MODE == kGrad) {
+        const Params &dx = j.job[0].p, &dw = j.job[MODE].p;
+        // (of few stages the epilogue is what a tile takes)
+        const auto us = [](const Params& p) { return std::max(p.split_stages * 0.6, 4.0); };
+        j.extra = dx.total % pairs && dw.total ? (int)(us(dx) / us(dw)) : 0;
+    }
+    return is_long ? launch_gemm<MODE, GATED, true>(j, pairs, st) : launch_gemm<MODE, GATED, false>(j, pairs, st);
 }
 
 template <bool GATED>
@@ -988,22 +1081,21 @@ cudaError_t forward(const LinearArgs& a, cudaStream_t st) {
     const int64_t T = a.tokens, N = a.out, K = a.cols;
     if (T <= kGemvTokens) return gemv<GATED>(a, st);
     const Cut cut = forward_cut(T, N, K, GATED, a.num_sms);
-    Params p{};
-    Maps tm{};
-    Fused& f = p.f;
+    Jobs<kFwd> j{};
+    Job& job = j.job[0];
+    Fused& f = job.p.f;
     fused_args(f, a);
     float* acc = static_cast<float*>(a.ws);
     const Operand x{a.x, T, K, a.ldx}, w0{a.w, N, K, a.ldw}, w1{GATED ? a.w2 : a.w, N, K, GATED ? a.ldw2 : a.ldw};
-    p.M = T;
-    p.N = N;
+    if (!set_up<kProduct, GATED>(job, {x, x}, {w0, w1}, T, N, K, cut, !a.y_bf16, a.num_sms)) return cudaErrorInvalidValue;
     if (cut.splits > 1) {
-        if (!map_acc(&tm.out[0], acc, cut.splits, T, fused_acc_cols(N, GATED))) return cudaErrorInvalidValue;
+        if (!map_acc(&job.out[0], acc, cut.splits, T, fused_acc_cols(N, GATED))) return cudaErrorInvalidValue;
     } else {
-        f.y_tma = fused_map(&tm.out[0], a.y, T, N, a.ldy, a.y_bf16);
-        f.z_tma = fused_map(&tm.out[1], a.z, T, N, a.ldz, true);
-        f.u_tma = GATED ? fused_map(&tm.out[2], a.u, T, N, a.ldu, true) : kNone;
+        f.y_tma = fused_map(&job.out[0], a.y, T, N, a.ldy, a.y_bf16);
+        f.z_tma = fused_map(&job.out[1], a.z, T, N, a.ldz, true);
+        f.u_tma = GATED ? fused_map(&job.out[2], a.u, T, N, a.ldu, true) : kNone;
     }
-    const cudaError_t err = gemm<kFwd, GATED>(p, {x, x}, {w0, w1}, tm, K, cut, kWaitStart, !a.y_bf16, a, st);
+    const cudaError_t err = gemm<kFwd, GATED>(j, a, st);
     return err != cudaSuccess || cut.splits == 1 ? err : run_linear_join(acc, cut.splits, T, N, GATED, a, st);
 }
 
@@ -1101,8 +1193,6 @@ cudaError_t backward(const LinearArgs& a, cudaStream_t st) {
                     static_cast<const __nv_bfloat16*>(a.u), a.ldu, copy && products ? dz : nullptr, du, g.ld,
                     a.dbias ? sums : nullptr, T, N};
         e = slope<GATED>(a, s, st);
-        if (e == cudaSuccess && a.dbias)
-            e = launch_k(true, linear_bias_kernel, dim3((unsigned)div_up(N, 32)), 256, 0, st, sums, g.blocks, N, a.dbias);
     }
     const Operand d0 = copy ? Operand{dz, T, N, g.ld} : Operand{a.dy, T, N, T > 1 ? a.ld_dy : up(N, 8)};
     const Operand d1 = GATED ? Operand{du, T, N, g.ld} : d0;
@@ -1111,33 +1201,35 @@ cudaError_t backward(const LinearArgs& a, cudaStream_t st) {
         return launch_k(true, linear_sum_kernel, dim3((unsigned)div_up(rows * (D / 8), 256)), 256, 0, st, acc, splits, all, row0, rows,
                         D, static_cast<__nv_bfloat16*>(to), ld);
     };
-    if (e == cudaSuccess && a.dx) {
-        Params p{};
-        Maps tm{};
-        p.M = T;
-        p.N = D;
-        if (!(g.dx.splits > 1 ? map_acc(&tm.out[0], dx_acc, g.dx.splits, T, D) : tmap::out_2d(&tm.out[0], a.dx, T, D, a.ld_dx, true)))
-            return cudaErrorInvalidValue;
-        e = gemm<kDx, GATED>(p, {d0, d1}, {w0, w1}, tm, N, g.dx, kWaitStart, false, a, st);
-        if (e == cudaSuccess && g.dx.splits > 1) e = sum(dx_acc, g.dx.splits, T, 0, T, a.dx, a.ld_dx);
-    }
-    if (e == cudaSuccess && a.dw) {
-        Params p{};
-        Maps tm{};
-        p.M = N;
-        p.N = D;
+    if (e == cudaSuccess && products) {
+        Jobs<kGrad> j{};
+        Job &dx = j.job[0], &dw = j.job[1];
         const int64_t half = up(N, kTile), all = GATED ? 2 * half : half;
-        if (g.dw.splits > 1) {
-            if (!map_acc(&tm.out[0], dw_acc, g.dw.splits, all, D)) return cudaErrorInvalidValue;
-        } else if (!tmap::out_2d(&tm.out[0], a.dw, N, D, a.ld_dw, true) ||
-                   (GATED && !tmap::out_2d(&tm.out[1], a.dw2, N, D, a.ld_dw2, true))) {
+        if (a.dx && (!set_up<kDx, GATED>(dx, {d0, d1}, {w0, w1}, T, D, N, g.dx, false, a.num_sms) ||
+                     !(g.dx.splits > 1 ? map_acc(&dx.out[0], dx_acc, g.dx.splits, T, D) : tmap::out_2d(&dx.out[0], a.dx, T, D, a.ld_dx, true))))
             return cudaErrorInvalidValue;
+        if (a.dw && (!set_up<kDw, GATED>(dw, {d0, d1}, {x, x}, N, D, T, g.dw, false, a.num_sms) ||
+                     !(g.dw.splits > 1 ? map_acc(&dw.out[0], dw_acc, g.dw.splits, all, D)
+                                       : tmap::out_2d(&dw.out[0], a.dw, N, D, a.ld_dw, true) &&
+                                             (!GATED || tmap::out_2d(&dw.out[1], a.dw2, N, D, a.ld_dw2, true)))))
+            return cudaErrorInvalidValue;
+        if (a.dx && a.dw && dx.p.total + dw.p.total > 8 * (a.num_sms / 2)) {
+            Jobs<kGrad> one{};
+            one.job[0] = dx;
+            dx.p.total = 0;
+            e = gemm<kGrad, GATED>(one, a, st);
+            // beside dx's last tiles, which waited for dz
+            j.wait_end = 1;
         }
-        // beside dx's last tiles, which waited for dz; the sum of dx's parts did not let anything start early
-        const int wait = a.dx && g.dx.splits == 1 ? kWaitEnd : kWaitStart;
-        e = gemm<kDw, GATED>(p, {d0, d1}, {x, x}, tm, T, g.dw, wait, false, a, st);
-        if (e == cudaSuccess && g.dw.splits > 1) e = sum(dw_acc, g.dw.splits, all, 0, N, a.dw, a.ld_dw);
-        if (e == cudaSuccess && g.dw.splits > 1 && GATED) e = sum(dw_acc, g.dw.splits, all, half, N, a.dw2, a.ld_dw2);
+        if (e == cudaSuccess) e = gemm<kGrad, GATED>(j, a, st);
+    }
+    if (e == cudaSuccess && a.dbias)
+        e = launch_k(true, linear_bias_kernel, dim3((unsigned)div_up(N, 32)), 256, 0, st, sums, g.blocks, N, a.dbias, products ? 1 : 0);
+    if (e == cudaSuccess && a.dx && g.dx.splits > 1) e = sum(dx_acc, g.dx.splits, T, 0, T, a.dx, a.ld_dx);
+    if (a.dw && g.dw.splits > 1) {
+        const int64_t half = up(N, kTile), all = GATED ? 2 * half : half;
+        if (e == cudaSuccess) e = sum(dw_acc, g.dw.splits, all, 0, N, a.dw, a.ld_dw);
+        if (e == cudaSuccess && GATED) e = sum(dw_acc, g.dw.splits, all, half, N, a.dw2, a.ld_dw2);
     }
     return e;
 }
