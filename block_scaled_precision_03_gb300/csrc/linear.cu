@@ -48,7 +48,7 @@ namespace {
 
 using namespace pair;
 
-enum { kFwd, kGrad };
+enum { kFwd, kDx, kDw, kGrad };                     // kGrad: dx and dw
 
 constexpr int kStages = 3;
 constexpr int kMaxStages = 12;                      // of smaller tiles: as many as fit
@@ -78,12 +78,12 @@ struct Job {
     CUtensorMap a[2], b[2], out[3];
     Params p;
 };
-// A forward product, or a gradient's two: dx and dw in one launch, whose tiles follow one another (no tiles: not wanted).
-// Small gradients gain by it (294 x 80 -> 576 5.8 us, two launches 8.3; 2048 x 4096 -> 4096 100, 112); of many tiles each
-// has a launch (8192 x 4096 -> 14336 1.03 ms, 1.06 in one: the two then share L2 for longer).
+// A product, or dx and dw in one launch, whose tiles follow one another: small gradients gain by it (294 x 80 -> 576
+// 5.8 us, two launches 8.3; 2048 x 4096 -> 4096 97, 109); of many tiles each has its own launch and program (8192 x 4096 ->
+// 14336 1.02 ms, 1.05 in one).
 template <int MODE>
 struct Jobs {
-    Job job[MODE == kFwd ? 1 : 2];
+    Job job[MODE == kGrad ? 2 : 1];
     int32_t stages, a_bytes, b_bytes;  // stages of the ring, and its room for one CTA's A and B per stage
     int32_t extra;                 // dw's tiles that a pair with one of dx's fewer takes in its place
     // When it waits for the kernel before it on the stream, whose dependent it is: before it reads or writes anything (its
@@ -98,10 +98,10 @@ template <int MODE>
 __device__ __forceinline__ bool nth_tile(const Jobs<MODE>& j, int cid, int ncl, int i, bool& dw, int& t) {
     const int n = j.job[0].p.total;
     t = cid + i * ncl;
-    dw = false;
-    if (MODE == kFwd || t < n) return t < n;
+    dw = MODE == kDw;
+    if (MODE != kGrad || t < n) return t < n;
     dw = true;
-    const int all = j.job[MODE].p.total, rest = n % ncl, light = ncl - rest;
+    const int all = j.job[MODE == kGrad].p.total, rest = n % ncl, light = ncl - rest;
     int k = i - (cid < n ? (n - cid + ncl - 1) / ncl : 0);
     if (cid >= rest) {
         t = cid - rest + k * light;
@@ -147,7 +147,7 @@ linear_gemm_kernel(const __grid_constant__ Jobs<MODE> j) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     // [stages] of A, [stages] of B, the epilogue's staging; the barriers come last
-    constexpr bool GRAD = MODE == kGrad;
+    constexpr bool GRAD = MODE != kFwd, BOTH = MODE == kGrad;
     const int S = j.stages, a_bytes = j.a_bytes, b_bytes = j.b_bytes;
     uint8_t* smA = base;
     uint8_t* smB = smA + S * a_bytes;
@@ -169,7 +169,7 @@ linear_gemm_kernel(const __grid_constant__ Jobs<MODE> j) {
     const uint32_t rank = tc::cluster_rank();
     const bool leader = rank == 0;
     const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
-    const Job& ahead = j.job[GRAD && cid >= j.job[0].p.total];
+    const Job& ahead = j.job[BOTH && cid >= j.job[0].p.total];
     read_ahead(ahead.p);
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < S; s++) {
@@ -208,7 +208,7 @@ linear_gemm_kernel(const __grid_constant__ Jobs<MODE> j) {
             }
             bool dw;
             for (int i = 0, t; ok && nth_tile(j, cid, ncl, i, dw, t); i++) {
-                const Job& job = j.job[dw];
+                const Job& job = j.job[BOTH && dw];
                 const Params& p = job.p;
                 const TileAt ti = tile_at(p, t);
                 // which of the two operand pairs of a gated layer's dw
@@ -225,7 +225,7 @@ linear_gemm_kernel(const __grid_constant__ Jobs<MODE> j) {
                         break;
                     }
                     const uint32_t fb = full_c0 + 8 * stage;
-                    if (GRAD) load_tx[stage] = tx;
+                    if (BOTH) load_tx[stage] = tx;
                     if (leader) tc::mbar_expect_tx(full0 + 8 * stage, 2 * tx);
                     const int second = GRAD && GATED && kb >= half ? 1 : 0;        // dx of a gated layer
                     const CUtensorMap* ma = &job.a[GRAD ? (dw ? which : second) : 0];
@@ -267,7 +267,7 @@ linear_gemm_kernel(const __grid_constant__ Jobs<MODE> j) {
             if (!j.wait_end) pdl_wait();                   // the limit of its waits counts from there
             bool dw;
             for (int i = 0, t; ok && nth_tile(j, cid, ncl, i, dw, t); i++) {
-                const Params& p = j.job[dw].p;
+                const Params& p = j.job[BOTH && dw].p;
                 const TileAt ti = tile_at(p, t);
                 const uint32_t idesc = idesc_bf16(dw, GRAD) | ((uint32_t)(p.tile_n >> 3) << 17);
                 const uint64_t ad0 = dw ? desc_mn_sw128(tc::smem_u32(smA)) : tc::desc_sw128(tc::smem_u32(smA));
@@ -331,7 +331,7 @@ linear_gemm_kernel(const __grid_constant__ Jobs<MODE> j) {
         constexpr bool PROJ = !GRAD && GATED;
         bool dw;
         for (int i = 0, t; nth_tile(j, cid, ncl, i, dw, t); i++) {
-            const Job& job = j.job[dw];
+            const Job& job = j.job[BOTH && dw];
             const Params& p = job.p;
             const TileAt ti = tile_at(p, t);
             const int cols = PROJ ? p.tile_n / 2 : p.tile_n, first = (cols / 32 + 1) / 2 * 32;
@@ -419,7 +419,7 @@ linear_gemm_kernel(const __grid_constant__ Jobs<MODE> j) {
     if (*abort_flag || *peer_abort) {
         if (leader && warp == 0 && lane == 0)
             drain_ring(full0, S, *issued_slot, tc::ld_cluster_s32(tc::mapa(tc::smem_u32((const void*)issued_slot), 1)), load_tx,
-                       tc::mapa(tc::smem_u32((const void*)load_tx), 1), GRAD ? 0 : (uint32_t)(kSub * (j.job[0].p.sub_a + j.job[0].p.sub_b)));
+                       tc::mapa(tc::smem_u32((const void*)load_tx), 1), BOTH ? 0 : (uint32_t)(kSub * (j.job[0].p.sub_a + j.job[0].p.sub_b)));
         tc::cluster_sync();
     }
     if (warp == 1) {
@@ -990,14 +990,13 @@ cudaError_t launch_gemm(const Jobs<MODE>& j, int pairs, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     return launch_k(true, linear_gemm_kernel<MODE, GATED, LONG>, dim3(2 * pairs), kThreads, kSmem, st, j);
 }
-enum { kProduct, kDx, kDw };
 // A job but for its outputs; K: the depth of each operand pair
 template <int KIND, bool GATED>
 bool set_up(Job& job, const Operand (&a)[2], const Operand (&b)[2], int64_t M, int64_t N, int64_t K, const Cut& cut, bool fine, int num_sms) {
-    constexpr bool A_MN = KIND == kDw, B_MN = KIND != kProduct;
+    constexpr bool A_MN = KIND == kDw, B_MN = KIND != kFwd;
     const int tile_n = cut.tile_n;
     // the second operands where there are any
-    constexpr bool TWO_A = GATED && KIND != kProduct, TWO_B = GATED && KIND != kDw;
+    constexpr bool TWO_A = GATED && KIND != kFwd, TWO_B = GATED && KIND != kDw;
     for (int i = 0; i < 2; i++) {
         if ((i == 0 || TWO_A) && !map_operand(&job.a[i], a[i].p, a[i].rows, a[i].cols, a[i].ld, A_MN ? kSubK : cut.tile_m / 2)) return false;
         if ((i == 0 || TWO_B) && !map_operand(&job.b[i], b[i].p, b[i].rows, b[i].cols, b[i].ld, B_MN ? kSubK : tile_n / 2)) return false;
@@ -1014,7 +1013,7 @@ bool set_up(Job& job, const Operand (&a)[2], const Operand (&b)[2], int64_t M, i
     p.sub_a = cut.tile_m / 2 * kSubK * 2;
     p.sub_b = (int)(B_MN ? up(tile_n / 2, 64) : tile_n / 2) * kSubK * 2;
     p.m_tiles = (int32_t)div_up(M, cut.tile_m) * (KIND == kDw && GATED ? 2 : 1);
-    p.n_tiles = (int32_t)div_up(N, KIND == kProduct && GATED ? tile_n / 2 : tile_n);
+    p.n_tiles = (int32_t)div_up(N, KIND == kFwd && GATED ? tile_n / 2 : tile_n);
     p.split_stages = (int32_t)div_up(p.k_stages, cut.splits);
     p.splits = (int32_t)div_up(p.k_stages, p.split_stages);
     p.chunk = fine ? kChunk : kSumChunk;
@@ -1041,7 +1040,7 @@ cudaError_t gemm(Jobs<MODE>& j, const LinearArgs& args, cudaStream_t st) {
     j.timeout_ns = args.timeout_ns;
     const int pairs = std::max(1, std::min(args.num_sms / 2, total));
     if (MODE == kGrad) {
-        const Params &dx = j.job[0].p, &dw = j.job[MODE].p;
+        const Params &dx = j.job[0].p, &dw = j.job[MODE == kGrad].p;
         // (of few stages the epilogue is what a tile takes)
         const auto us = [](const Params& p) { return std::max(p.split_stages * 0.6, 4.0); };
         j.extra = dx.total % pairs && dw.total ? (int)(us(dx) / us(dw)) : 0;
@@ -1087,7 +1086,7 @@ cudaError_t forward(const LinearArgs& a, cudaStream_t st) {
     fused_args(f, a);
     float* acc = static_cast<float*>(a.ws);
     const Operand x{a.x, T, K, a.ldx}, w0{a.w, N, K, a.ldw}, w1{GATED ? a.w2 : a.w, N, K, GATED ? a.ldw2 : a.ldw};
-    if (!set_up<kProduct, GATED>(job, {x, x}, {w0, w1}, T, N, K, cut, !a.y_bf16, a.num_sms)) return cudaErrorInvalidValue;
+    if (!set_up<kFwd, GATED>(job, {x, x}, {w0, w1}, T, N, K, cut, !a.y_bf16, a.num_sms)) return cudaErrorInvalidValue;
     if (cut.splits > 1) {
         if (!map_acc(&job.out[0], acc, cut.splits, T, fused_acc_cols(N, GATED))) return cudaErrorInvalidValue;
     } else {
@@ -1213,15 +1212,21 @@ cudaError_t backward(const LinearArgs& a, cudaStream_t st) {
                                        : tmap::out_2d(&dw.out[0], a.dw, N, D, a.ld_dw, true) &&
                                              (!GATED || tmap::out_2d(&dw.out[1], a.dw2, N, D, a.ld_dw2, true)))))
             return cudaErrorInvalidValue;
-        if (a.dx && a.dw && dx.p.total + dw.p.total > 8 * (a.num_sms / 2)) {
-            Jobs<kGrad> one{};
-            one.job[0] = dx;
-            dx.p.total = 0;
-            e = gemm<kGrad, GATED>(one, a, st);
-            // beside dx's last tiles, which waited for dz
-            j.wait_end = 1;
+        if (a.dx && a.dw && dx.p.total + dw.p.total <= 8 * (a.num_sms / 2)) {
+            e = gemm<kGrad, GATED>(j, a, st);
+        } else {
+            if (a.dx) {
+                Jobs<kDx> one{};
+                one.job[0] = dx;
+                e = gemm<kDx, GATED>(one, a, st);
+            }
+            if (a.dw && e == cudaSuccess) {
+                Jobs<kDw> one{};
+                one.job[0] = dw;
+                one.wait_end = a.dx ? 1 : 0;               // beside dx's last tiles, which waited for dz
+                e = gemm<kDw, GATED>(one, a, st);
+            }
         }
-        if (e == cudaSuccess) e = gemm<kGrad, GATED>(j, a, st);
     }
     if (e == cudaSuccess && a.dbias)
         e = launch_k(true, linear_bias_kernel, dim3((unsigned)div_up(N, 32)), 256, 0, st, sums, g.blocks, N, a.dbias, products ? 1 : 0);

@@ -206,6 +206,21 @@ def test_values_that_are_not_finite_stay_in_their_rows(bsq, T):
     assert torch.equal(z[rows, 7].float(), torch.where(x[rows, 3] > 0, float("inf"), -float("inf")))
 
 
+@pytest.mark.parametrize("T,N,K", [(2600, 2600, 8200), (9000, 72, 264), (40, 9000, 1032)])
+def test_gradients_of_many_tiles(bsq, T, N, K):
+    # dx and dw in one launch, or in two; -1, 0, 1, so that every sum is exact
+    g = gen(T, N, K, 90)
+    x, w, v, d = (torch.randint(-1, 2, s, generator=g, device="cuda").to(BF) for s in ((T, K), (N, K), (N, K), (T, N)))
+    dx, dw, db = bsq.linear_backward(d, x, w)
+    xf, wf, vf, df = (t.double() for t in (x, w, v, d))
+    assert torch.equal(dx, (df @ wf).float().to(BF)) and torch.equal(dw, (df.T @ xf).float().to(BF))
+    assert torch.equal(db, df.sum(0).float())
+    one = torch.ones((T, N), dtype=BF, device="cuda")
+    dx, dg, du = bsq.gated_linear_backward(d, x, w, v, one, -one, "identity")
+    assert torch.equal(dx, (df @ vf - df @ wf).float().to(BF))
+    assert torch.equal(dg, -(df.T @ xf).float().to(BF)) and torch.equal(du, (df.T @ xf).float().to(BF))
+
+
 @pytest.mark.parametrize("pad", [0, 3])
 def test_results_of_more_than_2_31_elements(bsq, pad):
     # whole numbers; the last rows and columns lie past 2^31 elements
