@@ -132,11 +132,9 @@ __device__ __forceinline__ uint2 encode(const float (&x)[kPer], const uint32_t (
         y[i] = a.x;
         y[i + 1] = a.y;
     }
-    // (16 random bits four places up, the high ones by the high word of a product)
+    // (16 random bits four places up: their half of the word times 16, by a product of halves and bytes)
     const auto cut = [&](float a, int i) {
-        uint32_t c = __float_as_uint(a);
-        if (ROOT) asm("mad.hi.u32 %0, %1, %2, %0;" : "+r"(c) : "r"(bits[i] & 0xFFFF0000u), "r"(1u << 20));
-        else c += (bits[i] & 0xFFFFu) * 16u;
+        const uint32_t c = __dp2a_lo(bits[i], ROOT ? 0x1000u : 0x0010u, __float_as_uint(a));
         return __uint_as_float(c & 0xFFF00000u);
     };
     float least = fabsf(y[0]);
@@ -479,8 +477,7 @@ __device__ __forceinline__ void leave(const Entry& e, int64_t at, int n, bool ve
 #pragma unroll
         for (int i = 0; i < kPer; i++) {
             all += p[i];
-            w[i] = __float_as_uint(p[i]);
-            asm("mad.hi.u32 %0, %1, %2, %0;" : "+r"(w[i]) : "r"(bits[i] * 0x9E3779B1u), "r"(1u << 16));
+            w[i] = __dp2a_lo(bits[i] * 0x9E3779B1u, 0x0100u, __float_as_uint(p[i]));
         }
         if (n == kPer && fabsf(all) < INFINITY) {
             // the upper halves are the results
