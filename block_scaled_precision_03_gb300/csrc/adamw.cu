@@ -343,6 +343,9 @@ __device__ __forceinline__ void update_any(float (&p)[kPer], const float (&m)[kP
     }
 }
 
+struct Last {
+    int tensor, first, next;       // and its chunks
+};
 // Chunk c of the list: its tensor, and where this thread's elements start
 template <int CAP>
 struct Place {
@@ -350,14 +353,18 @@ struct Place {
     int64_t at;
     int n;                         // of the 8 elements
     bool whole;                    // the warp's elements are all there, and their moments lie on 16-byte boundaries
-    __device__ __forceinline__ Place(const Table<CAP>& t, int c) {
-        int lo = 0, hi = t.count - 1;               // the last tensor whose first chunk is <= c
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (t.first[mid] <= c) lo = mid; else hi = mid - 1;
+    // (`last`: where the chunk before was; mostly it is the same tensor)
+    __device__ __forceinline__ Place(const Table<CAP>& t, int c, Last& last) {
+        if (c >= last.next) {
+            int lo = last.tensor, hi = t.count - 1;  // the last tensor whose first chunk is <= c
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (t.first[mid] <= c) lo = mid; else hi = mid - 1;
+            }
+            last = {lo, t.first[lo], t.first[lo + 1]};
         }
-        e = &t.e[lo];
-        const int64_t start = (int64_t)(c - t.first[lo]) * kChunk;
+        e = &t.e[last.tensor];
+        const int64_t start = (int64_t)(c - last.first) * kChunk;
         const int own = threadIdx.x * kPer, rest = (int)min(kChunk, e->n - start);
         at = start + own;
         n = max(0, min(kPer, rest - own));
@@ -524,7 +531,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         }
     };
     {
-        Place<CAP> ahead(t, blockIdx.x);
+        Last last{0, 0, 0};
+        Place<CAP> ahead(t, blockIdx.x, last);
         Chunk words;
         if (ahead.whole) words.load(ahead, true);
         uint32_t some = 0;
@@ -538,7 +546,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
             words.s.get(m, v);
             c += gridDim.x;
             if (c < chunks) {
-                ahead = Place<CAP>(t, c);
+                ahead = Place<CAP>(t, c, last);
                 if (ahead.whole) words.load(ahead, true);
             }
             if (k > 0 && (k & 31) == 0) {
@@ -556,9 +564,10 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         if (k > 0 && lane == 0) mine[(k - 1) >> 5] = some;
         __syncwarp();
     }
+    Last last{0, 0, 0};
     for (int k = 0, c = blockIdx.x; c < chunks; k++, c += gridDim.x) {
         if (!(mine[k >> 5] >> (k & 31) & 1)) continue;
-        const Place<CAP> at(t, c);
+        const Place<CAP> at(t, c, last);
         const Entry& e = *at.e;
         Chunk words;
         words.load(at, at.whole);
