@@ -96,12 +96,22 @@ __device__ __forceinline__ int32_t smallest(const float (&x)[kPer]) {
     const int32_t a = __vimin3_s32(bits_of(x[0]), bits_of(x[1]), bits_of(x[2])), b = __vimin3_s32(bits_of(x[3]), bits_of(x[4]), bits_of(x[5]));
     return min(__vimin3_s32(a, b, bits_of(x[6])), bits_of(x[7]));
 }
-// The bits of the largest magnitude of 8: of the positive ones the largest signed, of the others the largest unsigned
-__device__ __forceinline__ uint32_t largest_magnitude(const float (&x)[kPer]) {
-    const auto u = [](float f) { return __float_as_uint(f); };
-    const uint32_t a = __vimax3_u32(u(x[0]), u(x[1]), u(x[2])), b = __vimax3_u32(u(x[3]), u(x[4]), u(x[5]));
-    const uint32_t n = max(__vimax3_u32(a, b, u(x[6])), u(x[7]));
-    return max(n & 0x7FFFFFFFu, (uint32_t)max(largest(x), 0));
+// Of 8 magnitudes the largest (NaN if one is) and the smallest
+__device__ __forceinline__ float largest_magnitude(const float (&x)[kPer]) {
+    float a, b;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(a) : "f"(x[0]), "f"(x[1]), "f"(x[2]));
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(b) : "f"(x[3]), "f"(x[4]), "f"(x[5]));
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(a) : "f"(a), "f"(b), "f"(x[6]));
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(a) : "f"(a), "f"(x[7]), "f"(x[7]));
+    return a;
+}
+__device__ __forceinline__ float smallest_magnitude(const float (&x)[kPer]) {
+    float a, b;
+    asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(a) : "f"(x[0]), "f"(x[1]), "f"(x[2]));
+    asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(b) : "f"(x[3]), "f"(x[4]), "f"(x[5]));
+    asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(a) : "f"(a), "f"(b), "f"(x[6]));
+    asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(a) : "f"(a), "f"(x[7]), "f"(x[7]));
+    return a;
 }
 // 2^(byte - 127)
 __device__ __forceinline__ float power(uint32_t byte) { return __uint_as_float(byte == 0 ? 1u << 22 : byte << 23); }
@@ -115,7 +125,7 @@ __device__ __forceinline__ float power(uint32_t byte) { return __uint_as_float(b
 template <bool RANDOM, bool ROOT>
 __device__ __forceinline__ uint2 encode(const float (&x)[kPer], const uint32_t (&bits)[kPer], uint32_t& byte) {
     // bits of the largest magnitude: those of NaN and infinity are above all others
-    uint32_t most = ROOT ? (uint32_t)largest(x) : largest_magnitude(x);
+    uint32_t most = ROOT ? (uint32_t)largest(x) : __float_as_uint(largest_magnitude(x));
 #pragma unroll
     for (int d = 1; d < 4; d <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
     if (most >= 0x7F800000u) {
@@ -137,10 +147,7 @@ __device__ __forceinline__ uint2 encode(const float (&x)[kPer], const uint32_t (
         const uint32_t c = __dp2a_lo(bits[i], ROOT ? 0x1000u : 0x0010u, __float_as_uint(a));
         return __uint_as_float(c & 0xFFF00000u);
     };
-    float least = fabsf(y[0]);
-#pragma unroll
-    for (int i = 1; i < kPer; i++) least = fminf(least, fabsf(y[i]));
-    if (least >= 0.015625f) {
+    if (smallest_magnitude(y) >= 0.015625f) {
         if (RANDOM)
 #pragma unroll
             for (int i = 0; i < kPer; i++) y[i] = cut(y[i], i);
@@ -480,13 +487,10 @@ __device__ __forceinline__ void leave(const Entry& e, int64_t at, int n, bool ve
     if (e.copy) put(e.copy, at, 1, copy_vec, n, p);
     if (RANDOM && e.p_bf16) {
         uint32_t w[kPer];
-        float all = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kPer; i++) {
-            all += p[i];
+        for (int i = 0; i < kPer; i++)
             w[i] = __dp2a_lo(bits[i] * 0x9E3779B1u, 0x0100u, __float_as_uint(p[i]));
-        }
-        if (n == kPer && fabsf(all) < INFINITY) {
+        if (n == kPer && largest_magnitude(p) < INFINITY) {
             // the upper halves are the results
             const uint32_t h[4] = {__byte_perm(w[0], w[1], 0x7632), __byte_perm(w[2], w[3], 0x7632), __byte_perm(w[4], w[5], 0x7632),
                                    __byte_perm(w[6], w[7], 0x7632)};
