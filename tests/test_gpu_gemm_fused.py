@@ -76,6 +76,14 @@ def test_gemm_gated(bsq, T, N, K, fa, fb):
             Guard(u, ubuf).check()
 
 
+# the smaller sizes above have tiles of 128 columns; these of 256, whole and in parts
+@pytest.mark.parametrize("fa,fb", [FORMATS[0], FORMATS[3]])
+@pytest.mark.parametrize("T,N,K", [(2050, 2500, 2080), (100, 4096, 14336), (60, 2051, 8192)])
+def test_wide_tiles_and_long_sums(bsq, T, N, K, fa, fb):
+    test_gemm_linear(bsq, T, N, K, fa, fb)
+    test_gemm_gated(bsq, T, N, K, fa, fb)
+
+
 @pytest.mark.parametrize("fmt", ["mxfp8_e4m3", "mxfp8_e5m2", "mxfp4"])
 @pytest.mark.parametrize("T", [1, 4, 9, 200])
 def test_scales_far_from_one(bsq, fmt, T):
