@@ -206,6 +206,26 @@ def test_values_that_are_not_finite_stay_in_their_rows(bsq, T):
     assert torch.equal(z[rows, 7].float(), torch.where(x[rows, 3] > 0, float("inf"), -float("inf")))
 
 
+# tiles of 64 to 256 columns and 64 to 256 rows, whole and in parts
+@pytest.mark.parametrize("T,N,K", [(40, 6000, 264), (40, 1000, 4104), (257, 4100, 264), (40, 1537, 4104), (257, 6000, 1000), (40, 6000, 4104),
+                                   (520, 4100, 1000), (40, 2500, 8200), (1030, 3001, 1000), (40, 4100, 8200), (520, 6000, 1000),
+                                   (40, 2500, 20000), (100, 513, 4104), (150, 2050, 8200), (190, 1000, 20000), (70, 2500, 264)])
+def test_tiles_of_every_size(bsq, T, N, K):
+    # -1, 0, 1: every sum is exact in FP32, and a result is rounded once
+    g = gen(T, N, K, 91)
+    x, w, v = (torch.randint(-1, 2, s, generator=g, device="cuda").to(BF) for s in ((T, K), (N, K), (N, K)))
+    a, u = x.double() @ w.double().T, x.double() @ v.double().T
+    for dtype in (BF, F32):
+        res = torch.randint(-99, 100, (T, N), generator=g, device="cuda").to(dtype)
+        z = torch.empty((T, N), dtype=BF, device="cuda")
+        y = torch.empty((T, N), dtype=dtype, device="cuda")
+        bsq.linear_into(x, w, y, None, res, "relu", z)
+        assert torch.equal(y, (a.clamp(min=0) + res.double()).to(dtype)) and torch.equal(z, a.to(BF))
+        h, gate, up = torch.empty_like(y), torch.empty_like(z), torch.empty_like(z)
+        bsq.gated_linear_into(x, w, v, h, "relu", gate, up)
+        assert torch.equal(h, (a.clamp(min=0) * u).to(dtype)) and torch.equal(gate, z) and torch.equal(up, u.to(BF))
+
+
 @pytest.mark.parametrize("T,N,K", [(2600, 2600, 8200), (9000, 72, 264), (40, 9000, 1032)])
 def test_gradients_of_many_tiles(bsq, T, N, K):
     # dx and dw in one launch, or in two; -1, 0, 1, so that every sum is exact
