@@ -10,7 +10,13 @@ namespace bsq {
 // A kernel launched with launch_k(true, ...) may start while the kernel before
 // it on the stream still runs.  Such a kernel calls pdl_wait() before its
 // first access to global memory; the kernel before it may let it start early
-// with pdl_launch_dependents().
+// with pdl_launch_dependents().  Only pdl_wait() makes visible what kernels
+// before it wrote, so whoever may follow any kernel waits first, always.  A few
+// kernels behind another one of the same call (the head's dw, norm_dx_kernel,
+// moe_gather_kernel) read before it what that kernel does not write, and say so:
+// the call's first kernel is launched without this attribute, so that all the
+// stream's work before the call is done, and what the call itself wrote two
+// kernels before is read from L2 (TMA, __ldcg).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -78,17 +78,42 @@ struct Job {
     CUtensorMap a[2], b[2], out[3];
     Params p;
 };
+// dbias from the column sums of the row blocks [blocks][cols], added in their order: 32 columns a round of a CTA, eight
+// warps that take every eighth block each.  `all`: their sums in shared memory; sync: of the eight.
+constexpr int kSumWarps = 8;
+struct BlockSums {
+    const float* from;
+    int64_t blocks, cols;
+    float* out;                    // or nullptr
+};
+template <typename SYNC>
+__device__ __forceinline__ void add_blocks(const BlockSums& b, int warp, int lane, float (*all)[32], SYNC sync) {
+    for (int64_t c0 = (int64_t)blockIdx.x * 32; c0 < b.cols; c0 += (int64_t)gridDim.x * 32) {
+        const int64_t c = c0 + lane;
+        float s = 0.0f;
+        if (c < b.cols)
+#pragma unroll 4
+            for (int64_t i = warp; i < b.blocks; i += kSumWarps) s += b.from[i * b.cols + c];
+        all[warp][lane] = s;
+        sync();
+        if (warp == 0 && c < b.cols) {
+            s = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kSumWarps; w++) s += all[w][lane];
+            b.out[c] = s;
+        }
+        sync();
+    }
+}
 // A product, or dx and dw in one launch, whose tiles follow one another: small gradients gain by it (294 x 80 -> 576
 // 5.8 us, two launches 8.3; 2048 x 4096 -> 4096 97, 109); of many tiles each has its own launch and program (8192 x 4096 ->
-// 14336 1.02 ms, 1.05 in one).
+// 14336 with gelu_tanh 1.16 ms, 1.18 in one).  The first launch's epilogue warps add up dbias while they would wait for their first tile.
 template <int MODE>
 struct Jobs {
     Job job[MODE == kGrad ? 2 : 1];
     int32_t stages, a_bytes, b_bytes;  // stages of the ring, and its room for one CTA's A and B per stage
     int32_t extra;                 // dw's tiles that a pair with one of dx's fewer takes in its place
-    // When it waits for the kernel before it on the stream, whose dependent it is: before it reads or writes anything (its
-    // set-up runs earlier), or at its end (it needs nothing of that kernel, and runs beside it).
-    int32_t wait_end;
+    BlockSums dbias;
     unsigned* status;
     uint64_t timeout_ns;
 };
@@ -164,7 +189,6 @@ linear_gemm_kernel(const __grid_constant__ Jobs<MODE> j) {
     volatile uint32_t* load_tx = tmem_slot + 4;
     static_assert(8 * (2 * kMaxStages + 5) + 16 + 4 * kMaxStages <= kBarBytes, "barrier area");
 
-    if (j.wait_end) pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_rank();
     const bool leader = rank == 0;
@@ -202,10 +226,8 @@ linear_gemm_kernel(const __grid_constant__ Jobs<MODE> j) {
             int stage = 0, issued = 0;
             uint32_t phase = 0;
             bool ok = true;
-            if (!j.wait_end) {
-                pdl_wait();
-                pdl_launch_dependents();
-            }
+            // (its set-up runs beside the kernel before it on the stream)
+            pdl_wait();
             bool dw;
             for (int i = 0, t; ok && nth_tile(j, cid, ncl, i, dw, t); i++) {
                 const Job& job = j.job[BOTH && dw];
@@ -252,6 +274,9 @@ linear_gemm_kernel(const __grid_constant__ Jobs<MODE> j) {
                     if (++stage == S) { stage = 0; phase ^= 1; }
                 }
             }
+            // What comes next on the stream starts when every CTA has its last loads under way.  (From the wait on, its CTAs
+            // crowded into the first SMs that were free: the gradient of 1021 x 2040 -> 1531 with gelu 34.3 us in a row, 30.4 now.)
+            pdl_launch_dependents();
             *issued_slot = issued;
             if (!ok) *abort_flag = 1;
         }
@@ -264,7 +289,7 @@ linear_gemm_kernel(const __grid_constant__ Jobs<MODE> j) {
             int stage = 0, iter = 0;
             uint32_t phase = 0;
             bool ok = true, any = false, ready = false;
-            if (!j.wait_end) pdl_wait();                   // the limit of its waits counts from there
+            pdl_wait();                                    // the limit of its waits counts from there
             bool dw;
             for (int i = 0, t; ok && nth_tile(j, cid, ncl, i, dw, t); i++) {
                 const Params& p = j.job[BOTH && dw].p;
@@ -324,7 +349,10 @@ linear_gemm_kernel(const __grid_constant__ Jobs<MODE> j) {
         const int q = warp & 3, half = (warp - 2) >> 2;
         const uint32_t tempty_c0 = tc::mapa(tempty0, 0);
         Staging<2> st{tc::smem_u32(smOut + (warp - 2) * kStageBytes), 0};
-        if (!j.wait_end) pdl_wait();
+        pdl_wait();
+        if (GRAD && j.dbias.out)
+            add_blocks(j.dbias, warp - 2, lane, reinterpret_cast<float (*)[32]>(smOut),
+                       [] { asm volatile("bar.sync 1, %0;" :: "n"(32 * kEpiWarps) : "memory"); });
         int iter = 0;
         // A thread owns one row and half of the tile's columns in chunks of 32, at most 128 (gated: of each
         // projection's, at most 64); of an odd number of chunks the first half has one more
@@ -408,8 +436,6 @@ linear_gemm_kernel(const __grid_constant__ Jobs<MODE> j) {
         if (lane == 0) tc::bulk_wait_all();
     }
 
-    // what was launched before this kernel is done when this kernel is
-    if (j.wait_end) pdl_wait();
     // Both CTAs have stopped issuing.  If either gave up, both know after the barrier, and the even CTA
     // waits (bounded) for the loads still in flight before either may exit.
     tc::fence_before();
@@ -746,6 +772,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const float* acc, int 
                                                          const __grid_constant__ Fused f) {
     const int64_t per = (N + 3) / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     pdl_wait();
+    pdl_launch_dependents();
     if (i >= M * per) return;
     const int64_t row = i / per, col = (i - row * per) * 4;
     const int n = (int)min((int64_t)4, N - col);
@@ -793,6 +820,7 @@ __global__ void __launch_bounds__(256) linear_sum_kernel(const float* acc, int s
                                                         int64_t rows, int64_t D, __nv_bfloat16* out, int64_t ld) {
     const int64_t per = D / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     pdl_wait();
+    pdl_launch_dependents();
     if (i >= rows * per) return;
     const int64_t r = i / per, c = (i - r * per) * 8;
     float v[8] = {};
@@ -920,26 +948,12 @@ __global__ void __launch_bounds__(256) linear_slope_kernel(const SlopeArgs a) {
     for (int w = 0; w < 8; w++) s += all[w][threadIdx.x];
     a.sums[(int64_t)blockIdx.x * a.cols + c] = s;
 }
-// dbias = the blocks' column sums in their order: 32 columns a CTA, eight threads each
-// (wait_end: beside the products, which waited for the sums)
-__global__ void __launch_bounds__(256) linear_bias_kernel(const float* sums, int64_t blocks, int64_t cols, float* out, int wait_end) {
-    __shared__ float all[8][32];
-    const int64_t c = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
+// dbias without a product behind it
+__global__ void __launch_bounds__(32 * kSumWarps) linear_bias_kernel(const BlockSums b) {
+    __shared__ float all[kSumWarps][32];
     pdl_launch_dependents();
-    if (!wait_end) pdl_wait();
-    float s = 0.0f;
-    if (c < cols)
-#pragma unroll 4
-        for (int64_t b = threadIdx.x >> 5; b < blocks; b += 8) s += sums[b * cols + c];
-    all[threadIdx.x >> 5][threadIdx.x & 31] = s;
-    __syncthreads();
-    if (threadIdx.x < 32 && c < cols) {
-        s = 0.0f;
-#pragma unroll
-        for (int w = 0; w < 8; w++) s += all[w][threadIdx.x];
-        out[c] = s;
-    }
-    if (wait_end) pdl_wait();
+    pdl_wait();
+    add_blocks(b, threadIdx.x >> 5, threadIdx.x & 31, all, [] { __syncthreads(); });
 }
 
 constexpr double kPartUs = 4.0;                     // the epilogue of a part's tile, behind which the next tile's stages may hide
@@ -1038,7 +1052,9 @@ cudaError_t gemm(Jobs<MODE>& j, const LinearArgs& args, cudaStream_t st) {
     j.stages = std::min(kMaxStages, kStages * 2 * kOpBytes / (j.a_bytes + j.b_bytes));
     j.status = args.status;
     j.timeout_ns = args.timeout_ns;
-    const int pairs = std::max(1, std::min(args.num_sms / 2, total));
+    // (a pair without a tile may still have columns of dbias)
+    const int64_t work = std::max<int64_t>(total, j.dbias.out ? div_up(j.dbias.cols, 64) : 0);
+    const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(args.num_sms / 2, work));
     if (MODE == kGrad) {
         const Params &dx = j.job[0].p, &dw = j.job[MODE == kGrad].p;
         // (of few stages the epilogue is what a tile takes)
@@ -1193,6 +1209,7 @@ cudaError_t backward(const LinearArgs& a, cudaStream_t st) {
                     a.dbias ? sums : nullptr, T, N};
         e = slope<GATED>(a, s, st);
     }
+    const BlockSums dbias{sums, g.blocks, N, a.dbias};
     const Operand d0 = copy ? Operand{dz, T, N, g.ld} : Operand{a.dy, T, N, T > 1 ? a.ld_dy : up(N, 8)};
     const Operand d1 = GATED ? Operand{du, T, N, g.ld} : d0;
     const Operand w0{a.w, N, D, a.ldw}, w1{GATED ? a.w2 : a.w, N, D, GATED ? a.ldw2 : a.ldw}, x{a.x, T, D, a.ldx};
@@ -1213,23 +1230,25 @@ cudaError_t backward(const LinearArgs& a, cudaStream_t st) {
                                              (!GATED || tmap::out_2d(&dw.out[1], a.dw2, N, D, a.ld_dw2, true)))))
             return cudaErrorInvalidValue;
         if (a.dx && a.dw && dx.p.total + dw.p.total <= 8 * (a.num_sms / 2)) {
+            j.dbias = dbias;
             e = gemm<kGrad, GATED>(j, a, st);
         } else {
             if (a.dx) {
                 Jobs<kDx> one{};
                 one.job[0] = dx;
+                one.dbias = dbias;
                 e = gemm<kDx, GATED>(one, a, st);
             }
             if (a.dw && e == cudaSuccess) {
                 Jobs<kDw> one{};
                 one.job[0] = dw;
-                one.wait_end = a.dx ? 1 : 0;               // beside dx's last tiles, which waited for dz
+                if (!a.dx) one.dbias = dbias;
                 e = gemm<kDw, GATED>(one, a, st);
             }
         }
     }
-    if (e == cudaSuccess && a.dbias)
-        e = launch_k(true, linear_bias_kernel, dim3((unsigned)div_up(N, 32)), 256, 0, st, sums, g.blocks, N, a.dbias, products ? 1 : 0);
+    if (e == cudaSuccess && a.dbias && !products)
+        e = launch_k(true, linear_bias_kernel, dim3((unsigned)div_up(N, 32)), 32 * kSumWarps, 0, st, dbias);
     if (e == cudaSuccess && a.dx && g.dx.splits > 1) e = sum(dx_acc, g.dx.splits, T, 0, T, a.dx, a.ld_dx);
     if (a.dw && g.dw.splits > 1) {
         const int64_t half = up(N, kTile), all = GATED ? 2 * half : half;
