@@ -472,9 +472,10 @@ struct Gemv {
     int32_t T, parts;
     Fused f;
 };
+// (not .nc, for data that does not change while the kernel runs: it runs already while the kernel before it writes w)
 __device__ __forceinline__ uint4 stream16(const __nv_bfloat16* p) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
 template <int TOK, bool GATED>

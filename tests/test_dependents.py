@@ -48,3 +48,9 @@ def test_every_kernel_waits_whatever_its_arguments(name):
 def test_no_launch_says_when_its_kernel_waits():
     # a parameter that says when is a kernel that may not wait first
     assert not re.search(r"\bwait_(end|start|at)\b", text("linear.cu"))
+
+
+@pytest.mark.parametrize("name", FILES + ["fused.cuh", "pair_gemm.cuh", "launch.cuh"])
+def test_no_load_takes_its_data_for_constant(name):
+    # the kernel before may write it while this one runs already
+    assert not re.search(r"ld\.global[\w.:]*\.nc\b|__ldg\s*\(|__restrict__", text(name))
