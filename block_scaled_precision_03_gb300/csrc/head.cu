@@ -887,16 +887,20 @@ head_target_kernel(const __nv_bfloat16* h, int64_t ldh, const int64_t* targets, 
     const int warp = threadIdx.x >> 5;
     const int64_t t = (int64_t)blockIdx.x * (kTargetThreads / 32 / wpt) + warp / wpt, v = t < T ? targets[t] - v0 : -1;
     Owner o = {0, 0};
-    if (v >= 0 && v < n) o = owner[v];
+    // (beside dh, which waited for g: what g's kernel left is read from L2)
+    if (v >= 0 && v < n) {
+        const int2 k = __ldcg(reinterpret_cast<const int2*>(owner + v));
+        o = {k.x, k.y};
+    }
     if (o.count > 1 || blockIdx.x == 0) {
         float hmax = 0.0f;
-        for (int i = lane; i < sums.hmaxes; i += 32) hmax = fmaxf(hmax, sums.hmax[i]);
+        for (int i = lane; i < sums.hmaxes; i += 32) hmax = fmaxf(hmax, __ldcg(sums.hmax + i));
 #pragma unroll
         for (int d = 16; d; d >>= 1) hmax = fmaxf(hmax, __shfl_xor_sync(0xffffffffu, hmax, d));
         if (blockIdx.x == 0 && threadIdx.x == 0) *all_hmax = hmax;
         if (o.count > 1) {
             const int unit = sum_unit(hmax, o.count);
-            const float f = lo[t], up = scalbnf(1.0f, -unit / 2), up2 = scalbnf(1.0f, -unit - (-unit / 2));
+            const float f = __ldcg(lo + t), up = scalbnf(1.0f, -unit / 2), up2 = scalbnf(1.0f, -unit - (-unit / 2));
             int32_t* row = sums.rows + (sums.by_row ? v0 + v : o.first) * sums.cols;
             const __nv_bfloat16* from = h + t * ldh;
 #pragma unroll 8

@@ -54,3 +54,11 @@ def test_no_launch_says_when_its_kernel_waits():
 def test_no_load_takes_its_data_for_constant(name):
     # the kernel before may write it while this one runs already
     assert not re.search(r"ld\.global[\w.:]*\.nc\b|__ldg\s*\(|__restrict__", text(name))
+
+
+def test_the_head_reads_what_an_earlier_kernel_of_the_call_left_from_l2():
+    # head_target_kernel beside dh: g's kernel wrote lo, owner and hmax, dh's waited for it, this one only at its end
+    body = kernels(text("head.cu"))["head_target_kernel"]
+    for what in (r"\bowner\[", r"\blo\[", r"\bhmax\["):
+        assert not re.search(what, body)
+    assert body.count("__ldcg(") == 3
