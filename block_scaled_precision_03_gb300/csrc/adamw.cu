@@ -123,9 +123,8 @@ __device__ __forceinline__ float power(uint32_t byte) { return __uint_as_float(b
 // they are those of the next binade.  A thread with such a value (one in some 10000 moments) takes the longer way,
 // on which a second moment that is not 0 is kept from becoming so.
 template <bool RANDOM, bool ROOT>
-__device__ __forceinline__ uint2 encode(const float (&x)[kPer], const uint32_t (&bits)[kPer], uint32_t& byte) {
-    // bits of the largest magnitude: those of NaN and infinity are above all others
-    uint32_t most = ROOT ? (uint32_t)largest(x) : __float_as_uint(largest_magnitude(x));
+__device__ __forceinline__ uint2 encode(const float (&x)[kPer], uint32_t most, const uint32_t (&bits)[kPer], uint32_t& byte) {
+    // `most`: bits of the largest magnitude; those of NaN and infinity are above all others
 #pragma unroll
     for (int d = 1; d < 4; d <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
     if (most >= 0x7F800000u) {
@@ -304,12 +303,29 @@ __device__ __forceinline__ void moments(const float (&g)[kPer], float (&m)[kPer]
 // / 2 are brought to full precision by one step, and the exact remainder v - g^2 rounds
 // g; for m / d the remainder m - d q does.  In packed instructions that is 4.5 and 3.5
 // of them an element, a third of the library's IEEE functions.  The remainders are exact
-// while nothing underflows: v from 2^-90 to 2^90 (in_range); elsewhere, a v of 0 among
-// them, the library's functions.  A quotient whose m is below 2^-90 may be off in its last bit.
-__device__ __forceinline__ bool in_range(const float (&v)[kPer]) {
-    constexpr int32_t least = (127 - 90) << 23, most = (127 + 90) << 23;
-    return smallest(v) >= least && largest(v) <= most;
+// and the quotient is neither infinite nor below 2^-126 while r lies in 2^-45 .. 2^25, |m|
+// in 2^-90 .. 2^80 or is 0, 1 / sqrt(1 - beta2^step) is at most 2^10 and eps at most 2^34:
+// d lies in 2^-45 .. 2^36, m / d is at most 2^125, and its remainder a multiple of 2^-149
+// (in_range, usual; a v of 0, an infinite one and NaN leave an r that is not in range).
+// Elsewhere the library's functions.  (The ranges are looked at behind the update, where
+// the largest r and |m| are what the 8-bit codes' scales take too; before it, those of v
+// and m, 243 M weights in 12 tensors took 513 us to nearest, 487 now.)
+struct Largest {
+    uint32_t m, r;                 // bits of the largest magnitudes
+};
+__device__ __forceinline__ Largest largest_of(const float (&m)[kPer], const float (&r)[kPer]) {
+    return {__float_as_uint(largest_magnitude(m)), (uint32_t)largest(r)};
 }
+__device__ __forceinline__ bool in_range(const float (&m)[kPer], const float (&r)[kPer], const Largest& most) {
+    constexpr int32_t least = (127 - 45) << 23;
+    bool in = smallest(r) >= least && most.r <= (127u + 25) << 23 && most.m <= (127u + 80) << 23;
+    if (smallest_magnitude(m) < 0x1p-90f) {        // 0, or too small
+#pragma unroll
+        for (int i = 0; i < kPer; i++) in = in && (fabsf(m[i]) >= 0x1p-90f || m[i] == 0.0f);
+    }
+    return in;
+}
+__device__ __forceinline__ bool usual(const Options& o) { return o.root <= 1024.0f && o.eps <= 0x1p34f; }
 __device__ __forceinline__ void update(float (&p)[kPer], const float (&m)[kPer], const float (&v)[kPer], float (&r)[kPer],
                                        const Options& o) {
     const F2 minus(-1.0f);
@@ -327,17 +343,18 @@ __device__ __forceinline__ void update(float (&p)[kPer], const float (&m)[kPer],
         q = fma2(fma2(q, q, vv * minus), h, q);
         const float2 root = q.get();
         r[i] = root.x; r[i + 1] = root.y;
-        const F2 d = mul2(q, F2(o.root)) + F2(o.eps), nd = d * minus, mm(m[i], m[i + 1]);
+        // (k: -1 / d and n: -m, so that a quotient of 0 has m's sign)
+        const F2 d = mul2(q, F2(o.root)) + F2(o.eps), n = F2(m[i], m[i + 1]) * minus;
         const float2 ds = d.get();
         float i0, i1;
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(i0) : "f"(ds.x));
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(i1) : "f"(ds.y));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(i0) : "f"(-ds.x));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(i1) : "f"(-ds.y));
         F2 k(i0, i1);
-        k = fma2(k, fma2(nd, k, F2(1.0f)), k);
-        F2 t = mm * k;
-        t = fma2(fma2(nd, t, mm), k, t);
-        const float2 n = (mul2(F2(o.decay), F2(p[i], p[i + 1])) + mul2(F2(-o.size), t)).get();
-        p[i] = n.x; p[i + 1] = n.y;
+        k = fma2(k, fma2(d, k, F2(1.0f)), k);
+        F2 t = n * k;
+        t = fma2(fma2(d, t, n), k, t);
+        const float2 x = (mul2(F2(o.decay), F2(p[i], p[i + 1])) + mul2(F2(-o.size), t)).get();
+        p[i] = x.x; p[i + 1] = x.y;
     }
 }
 __device__ __forceinline__ void update_any(float (&p)[kPer], const float (&m)[kPer], const float (&v)[kPer], float (&r)[kPer],
@@ -464,7 +481,7 @@ struct Moments<true> {
 // What a thread holds of a chunk becomes its new state
 template <bool RANDOM, bool BITS8, bool ANY>
 __device__ __forceinline__ void leave(const Entry& e, int64_t at, int n, bool vec, const Options& o, const float (&m)[kPer],
-                                      const float (&v)[kPer], const float (&r)[kPer], float (&p)[kPer]) {
+                                      const float (&v)[kPer], const float (&r)[kPer], const Largest& most, float (&p)[kPer]) {
     const bool p_vec = vec && (!ANY || e.p_vec), copy_vec = vec && (!ANY || e.copy_vec);
     uint32_t bits[kPer] = {};
     if (RANDOM) {
@@ -473,7 +490,7 @@ __device__ __forceinline__ void leave(const Entry& e, int64_t at, int n, bool ve
     }
     if (BITS8) {
         uint32_t mb, vb;
-        const uint2 mc = encode<RANDOM, false>(m, bits, mb), vc = encode<RANDOM, true>(r, bits, vb);
+        const uint2 mc = encode<RANDOM, false>(m, most.m, bits, mb), vc = encode<RANDOM, true>(r, most.r, bits, vb);
         put_codes(e.m, at, vec, n, mc);
         put_codes(e.v, at, vec, n, vc);
         if (n > 0 && (threadIdx.x & 3) == 0) {
@@ -525,6 +542,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         const float f = __fdiv_rn(o.max_norm, __fadd_rn(*o.norm, o.clip_eps));
         factor = f > 1.0f ? 1.0f : f;               // NaN stays NaN
     }
+    const bool fast = usual(o);
     struct Chunk {
         Words p, g;
         Moments<BITS8> s;
@@ -557,13 +575,16 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
                 if (lane == 0) mine[(k >> 5) - 1] = some;
                 some = 0;
             }
-            moments(g, m, v, o, factor);
-            if (!at.whole || !__all_sync(0xffffffffu, in_range(v))) {
-                some |= 1u << (k & 31);
-                continue;
+            if (at.whole && fast) {
+                moments(g, m, v, o, factor);
+                update(p, m, v, r, o);
+                const Largest most = largest_of(m, r);
+                if (__all_sync(0xffffffffu, in_range(m, r, most))) {
+                    leave<RANDOM, BITS8, ANY>(e, at.at, kPer, true, o, m, v, r, most, p);
+                    continue;
+                }
             }
-            update(p, m, v, r, o);
-            leave<RANDOM, BITS8, ANY>(e, at.at, kPer, true, o, m, v, r, p);
+            some |= 1u << (k & 31);
         }
         if (k > 0 && lane == 0) mine[(k - 1) >> 5] = some;
         __syncwarp();
@@ -587,12 +608,18 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
                 m[i] = 0.0f;
                 v[i] = 1.0f;
             }
-        if (in_range(v)) update(p, m, v, r, o);
-        else update_any(p, m, v, r, o);
+        float q[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; i++) q[i] = p[i];
+        update(q, m, v, r, o);
+        if (!fast || !in_range(m, r, largest_of(m, r))) update_any(p, m, v, r, o);
+        else
+#pragma unroll
+            for (int i = 0; i < kPer; i++) p[i] = q[i];
 #pragma unroll
         for (int i = 0; i < kPer; i++)
             if (i >= at.n) r[i] = 0.0f;
-        leave<RANDOM, BITS8, ANY>(e, at.at, at.n, at.whole, o, m, v, r, p);
+        leave<RANDOM, BITS8, ANY>(e, at.at, at.n, at.whole, o, m, v, r, largest_of(m, r), p);
     }
 }
 
