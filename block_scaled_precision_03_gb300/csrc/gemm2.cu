@@ -142,6 +142,7 @@ struct More {
     CUtensorMap z, u;              // outputs
     const float* ts_b;
     int32_t splits, split_stages;  // parts of the sum over K, and stages of each
+    int32_t chunk;                 // stages of one accumulator
     int32_t tile_n;                // kLinear: columns of a pair's tile
     uint32_t op_tx;                // operand bytes one CTA loads per stage
     float* acc;                    // few tokens: the parts [split][token][ld_acc]
@@ -171,6 +172,19 @@ __device__ __forceinline__ Part part_of(const Params2& p, const typename MoreOf<
         a.k1 = min(p.k_stages, a.k0 + more.split_stages);
     }
     return a;
+}
+
+// Where the accumulator ends that begins at stage c0.  The tensor cores' sums are truncated: of operands of one sign an
+// MXFP8 sum over K = 4096 loses 9e-7 of itself, over 16384 7e-6, over 65536 4e-5, an NVFP4 sum 2e-7, 4e-6 and 2e-5 (MXFP4
+// none: its products are whole quarters).  FP32 results take a new accumulator every K = 4096 (FP4 8192) and add them in
+// registers, which keeps them at 1e-6 whatever K; BF16 results every K = 65536, far below their own rounding.
+constexpr int kFineChunk8 = 16, kFineChunk4 = 32, kChunk = 256;      // stages of K = 256
+// LONG: a tile's sum takes several accumulators.  (One program for both has more to fetch: 660 x 160 -> 481 of MXFP8 13.4 us,
+// 12.6 with two.)
+template <bool LONG, typename MORE>
+__device__ __forceinline__ int chunk_end(const Part& pt, const MORE& more, int c0) {
+    if constexpr (LONG) return min(pt.k1, c0 + more.chunk);
+    else return pt.k1;
 }
 
 template <int KIND, int EPI>
@@ -275,7 +289,7 @@ __device__ __forceinline__ Tile2 tile2(const Params2& p, int t, const GroupTable
     return ti;
 }
 
-template <int KIND, int EPI>
+template <int KIND, int EPI, bool LONG>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
              const __grid_constant__ CUtensorMap tmSFA, const __grid_constant__ CUtensorMap tmSFB,
@@ -486,48 +500,51 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
             int iter = 0;
             bool ok = true, any = false;
             if constexpr (EPI != kPlain) pdl_wait();          // the limits of the waits count from there
-            for (int t = cid; t < total && ok; t += ncl, ++iter) {
-                // both CTAs' epilogue warps arrive here after their TMEM loads completed
-                // (tcgen05.wait::ld); a CTA-scope acquire suffices
-                if (!wait_for<EPI>(tempty, (iter & 1) ^ 1, abort_flag, p.status, p.timeout_ns)) { ok = false; break; }
-                tc::fence_after();
+            for (int t = cid; t < total && ok; t += ncl) {
                 int tile = t;
                 const Part pt = part_of<EPI>(p, more, tile);
-                for (int kb = pt.k0; kb < pt.k1; kb++) {
-                    if (!wait_for<EPI>(full0 + 8 * stage, phase, abort_flag, p.status, p.timeout_ns) ||
-                        !wait_for<EPI>(sfr0 + 8 * stage, phase, abort_flag, p.status, p.timeout_ns)) {
-                        ok = false;
-                        break;
-                    }
+                for (int c0 = pt.k0, c1; c0 < pt.k1 && ok; c0 = c1, ++iter) {
+                    c1 = chunk_end<LONG>(pt, more, c0);
+                    // both CTAs' epilogue warps arrive here after their TMEM loads completed
+                    // (tcgen05.wait::ld); a CTA-scope acquire suffices
+                    if (!wait_for<EPI>(tempty, (iter & 1) ^ 1, abort_flag, p.status, p.timeout_ns)) { ok = false; break; }
                     tc::fence_after();
-                    const uint32_t sfa_t = sf_t0 + stage * CF::SF_COLS, sfb_t = sfa_t + CF::SFA_COLS;
-                    const uint64_t ad = ad_base + (uint64_t)(stage * OP_STEP), bd = bd_base + (uint64_t)(stage * OP_STEP);
-                    const int nk = kb == p.k_stages - 1 ? p.mma_last : MPS;
+                    for (int kb = c0; kb < c1; kb++) {
+                        if (!wait_for<EPI>(full0 + 8 * stage, phase, abort_flag, p.status, p.timeout_ns) ||
+                            !wait_for<EPI>(sfr0 + 8 * stage, phase, abort_flag, p.status, p.timeout_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        tc::fence_after();
+                        const uint32_t sfa_t = sf_t0 + stage * CF::SF_COLS, sfb_t = sfa_t + CF::SFA_COLS;
+                        const uint64_t ad = ad_base + (uint64_t)(stage * OP_STEP), bd = bd_base + (uint64_t)(stage * OP_STEP);
+                        const int nk = kb == p.k_stages - 1 ? p.mma_last : MPS;
 #pragma unroll
-                    for (int m = 0; m < MPS; m++) {
-                        if (m < nk) {
-                            const int sub = m >> 2, k = m & 3;
-                            // +32 bytes along K inside a 128-byte swizzle row = +2 in the address field
-                            const uint64_t adm = ad + sub * SUB_STEP + 2 * k, bdm = bd + sub * SUB_STEP + 2 * k;
-                            const uint32_t acc = EPI == kPlain ? (kb | m) != 0 : ((kb - pt.k0) | m) != 0;
-                            // FP8 takes scale byte k of the sub-step's atom (1X), NVFP4 one atom
-                            // per MMA (4X), MXFP4 the byte pair 2 (m & 1) of atom m >> 1 (2X)
-                            if (KIND == kKindNV) {
-                                tc::mma<2, tc::kMmaNV>(tmem, adm, bdm, p.idesc, sfa_t + 4 * m, sfb_t + 8 * m, acc);
-                            } else if (KIND == kKindMX4) {
-                                const uint32_t id = (uint32_t)(m & 1) * 2u;
-                                tc::mma<2, tc::kMmaMX4>(tmem, adm, bdm, p.idesc | (id << 4) | (id << 29),
-                                                        sfa_t + 4 * (m >> 1), sfb_t + 8 * (m >> 1), acc);
-                            } else {
-                                tc::mma<2, tc::kMmaFP8>(tmem, adm, bdm, p.idesc | ((uint32_t)k << 4) | ((uint32_t)k << 29),
-                                                        sfa_t + 4 * sub, sfb_t + 8 * sub, acc);
+                        for (int m = 0; m < MPS; m++) {
+                            if (m < nk) {
+                                const int sub = m >> 2, k = m & 3;
+                                // +32 bytes along K inside a 128-byte swizzle row = +2 in the address field
+                                const uint64_t adm = ad + sub * SUB_STEP + 2 * k, bdm = bd + sub * SUB_STEP + 2 * k;
+                                const uint32_t acc = EPI == kPlain ? (kb | m) != 0 : ((kb - c0) | m) != 0;
+                                // FP8 takes scale byte k of the sub-step's atom (1X), NVFP4 one atom
+                                // per MMA (4X), MXFP4 the byte pair 2 (m & 1) of atom m >> 1 (2X)
+                                if (KIND == kKindNV) {
+                                    tc::mma<2, tc::kMmaNV>(tmem, adm, bdm, p.idesc, sfa_t + 4 * m, sfb_t + 8 * m, acc);
+                                } else if (KIND == kKindMX4) {
+                                    const uint32_t id = (uint32_t)(m & 1) * 2u;
+                                    tc::mma<2, tc::kMmaMX4>(tmem, adm, bdm, p.idesc | (id << 4) | (id << 29),
+                                                            sfa_t + 4 * (m >> 1), sfb_t + 8 * (m >> 1), acc);
+                                } else {
+                                    tc::mma<2, tc::kMmaFP8>(tmem, adm, bdm, p.idesc | ((uint32_t)k << 4) | ((uint32_t)k << 29),
+                                                            sfa_t + 4 * sub, sfb_t + 8 * sub, acc);
+                                }
                             }
                         }
+                        any = true;
+                        tc::commit<2>(empty0 + 8 * stage, 3);
+                        if (kb == c1 - 1) tc::commit<2>(tfull, 3);
+                        if (++stage == S) { stage = 0; phase ^= 1; }
                     }
-                    any = true;
-                    tc::commit<2>(empty0 + 8 * stage, 3);
-                    if (kb == pt.k1 - 1) tc::commit<2>(tfull, 3);
-                    if (++stage == S) { stage = 0; phase ^= 1; }
                 }
             }
             if (!ok) *abort_flag = 1;
@@ -576,6 +593,29 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
             tc::fence_before();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive_cluster(tempty_c0);
+            if constexpr (LONG) {
+                // the sum's further accumulators
+                bool ok = true;
+                for (int c = chunk_end<LONG>(pt, more, pt.k0); c < pt.k1; c = chunk_end<LONG>(pt, more, c)) {
+                    ++iter;
+                    ok = wait_for<EPI>(tfull, iter & 1, abort_flag, p.status, p.timeout_ns);
+                    if (!ok) break;
+                    tc::fence_after();
+#pragma unroll
+                    for (int k = 0; k < (EPI == kFewLinear ? 2 : 8); k++) {
+                        float v[16];
+#pragma unroll
+                        for (int j = 0; j < 16; j++) v[j] = __uint_as_float(r[k >> 1][(k & 1) * 16 + j]);
+                        pair::add_acc(v, ta + (k < 4 ? 16 * k : SECOND + 16 * (k - 4)));
+#pragma unroll
+                        for (int j = 0; j < 16; j++) r[k >> 1][(k & 1) * 16 + j] = __float_as_uint(v[j]);
+                    }
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive_cluster(tempty_c0);
+                }
+                if (!ok) break;
+            }
             // this warp's 32 rows, clipped to the rows the CTA may write
             const int row0 = ti.a_row + q * 32;
             if constexpr (EPI == kFewLinear) {
@@ -759,14 +799,14 @@ gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
     }
 }
 
-template <int KIND, int EPI>
+template <int KIND, int EPI, bool LONG>
 cudaError_t launch2(const Params2& p, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tsa,
                     const CUtensorMap& tsb, const CUtensorMap& tc_, const typename MoreOf<EPI>::type& more, int grid,
                     cudaStream_t st) {
     static SharedMemory smem;
-    const cudaError_t e = smem.allow(reinterpret_cast<const void*>(gemm2_kernel<KIND, EPI>), Cfg2<KIND>::SMEM);
+    const cudaError_t e = smem.allow(reinterpret_cast<const void*>(gemm2_kernel<KIND, EPI, LONG>), Cfg2<KIND>::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_k(EPI != kPlain, gemm2_kernel<KIND, EPI>, dim3((unsigned)grid), kThreads, Cfg2<KIND>::SMEM, st, ta, tb, tsa, tsb, tc_, p,
+    return launch_k(EPI != kPlain, gemm2_kernel<KIND, EPI, LONG>, dim3((unsigned)grid), kThreads, Cfg2<KIND>::SMEM, st, ta, tb, tsa, tsb, tc_, p,
                     more);
 }
 
@@ -864,18 +904,23 @@ cudaError_t run_gemm_pair(const GemmArgs& a, cudaStream_t st) {
     if (a.num_groups == 0 && p.total_tiles < pairs) pairs = p.total_tiles;
     if (pairs < 1) pairs = 1;
     const Nothing none{};
-    if (s.kind == kKindNV) return launch2<kKindNV, kPlain>(p, s.ta, s.tb, s.tsa, s.tsb, tcm, none, 2 * pairs, st);
-    if (s.kind == kKindMX4) return launch2<kKindMX4, kPlain>(p, s.ta, s.tb, s.tsa, s.tsb, tcm, none, 2 * pairs, st);
-    return launch2<kKindFP8, kPlain>(p, s.ta, s.tb, s.tsa, s.tsb, tcm, none, 2 * pairs, st);
+    if (s.kind == kKindNV) return launch2<kKindNV, kPlain, false>(p, s.ta, s.tb, s.tsa, s.tsb, tcm, none, 2 * pairs, st);
+    if (s.kind == kKindMX4) return launch2<kKindMX4, kPlain, false>(p, s.ta, s.tb, s.tsa, s.tsb, tcm, none, 2 * pairs, st);
+    return launch2<kKindFP8, kPlain, false>(p, s.ta, s.tb, s.tsa, s.tsb, tcm, none, 2 * pairs, st);
 }
 
 namespace {
 
+template <int KIND, int EPI>
+cudaError_t launch_long(const Setup& s, const CUtensorMap& tc_, const More& more, int pairs, cudaStream_t st) {
+    return more.split_stages > more.chunk ? launch2<KIND, EPI, true>(s.p, s.ta, s.tb, s.tsa, s.tsb, tc_, more, 2 * pairs, st)
+                                          : launch2<KIND, EPI, false>(s.p, s.ta, s.tb, s.tsa, s.tsb, tc_, more, 2 * pairs, st);
+}
 template <int EPI>
 cudaError_t launch_kind(const Setup& s, const CUtensorMap& tc_, const More& more, int pairs, cudaStream_t st) {
-    if (s.kind == kKindNV) return launch2<kKindNV, EPI>(s.p, s.ta, s.tb, s.tsa, s.tsb, tc_, more, 2 * pairs, st);
-    if (s.kind == kKindMX4) return launch2<kKindMX4, EPI>(s.p, s.ta, s.tb, s.tsa, s.tsb, tc_, more, 2 * pairs, st);
-    return launch2<kKindFP8, EPI>(s.p, s.ta, s.tb, s.tsa, s.tsb, tc_, more, 2 * pairs, st);
+    if (s.kind == kKindNV) return launch_long<kKindNV, EPI>(s, tc_, more, pairs, st);
+    if (s.kind == kKindMX4) return launch_long<kKindMX4, EPI>(s, tc_, more, pairs, st);
+    return launch_long<kKindFP8, EPI>(s, tc_, more, pairs, st);
 }
 // A tile's columns, and the parts of the sum over K.  A stage (K = 256) takes 0.72 us of MXFP8, 0.6 of MXFP4 or NVFP4, and
 // of 128 columns three quarters of it; with few tokens it is the pair's share of the weights' stream.  Between two tiles the
@@ -943,6 +988,7 @@ cudaError_t fused(const GemmArgs& a, const GemmArgs& up, const LinearArgs& l, cu
     p.total_tiles = (int32_t)(p.m_tiles * n_tiles * splits);
     more.split_stages = (p.k_stages + splits - 1) / splits;
     more.splits = splits;
+    more.chunk = l.y_bf16 ? kChunk : s.kind == kKindFP8 ? kFineChunk8 : kFineChunk4;
     more.ts_b = up.ts_b;
     more.acc = static_cast<float*>(l.ws);
     more.ld_acc = fused_acc_cols(a.N, GATED);

@@ -433,8 +433,10 @@ size_t bsq_gated_linear_backward_workspace_bytes(int64_t tokens, int64_t out, in
  * 2^23, no matrix of more than 2^44 elements.  bias: DEVICE [out] of `bias_type` (bsq_out) or NULL.  residual:
  * [tokens, out] of y's type or NULL; y may be residual itself (same pointer and
  * pitch).  y: [tokens, out] of `type` (bsq_out).  z: BF16 [tokens, out] for the
- * backward pass, or NULL.  FP32 sums on the tensor cores; z, act and the
- * residual in FP32, each output rounded once. */
+ * backward pass, or NULL.  FP32 sums on the tensor cores, whose additions are
+ * truncated: a sum is read out every K = 16384 where y is BF16 (off by some 1e-4
+ * of the sum of its magnitudes at most), every K = 512 where it is FP32 (1e-6);
+ * z, act and the residual in FP32, each output rounded once. */
 bsq_status bsq_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t tokens, int64_t out, int64_t cols,
                       const void* bias, int32_t bias_type, int32_t activation, const void* residual,
                       int64_t ld_residual, void* y, int64_t ldy, int32_t type, void* z, int64_t ldz, void* workspace,
@@ -485,7 +487,9 @@ size_t bsq_gemm_gated_workspace_bytes(int32_t fmt, int64_t tokens, int64_t out, 
 
 /* bsq_gemm with the epilogue of bsq_linear: z = A B^T + bias, y = act(z) +
  * residual.  Operands and formats as for bsq_gemm, B.rows up to 2^23; bias, residual, y
- * and z as for bsq_linear (A.rows tokens, B.rows out). */
+ * and z as for bsq_linear (A.rows tokens, B.rows out).  A sum is read out every K =
+ * 65536 where y is BF16 (off by 5e-5 of its magnitudes at most), every K = 4096 of
+ * MXFP8 and 8192 of MXFP4 and NVFP4 where it is FP32 (1e-6); bsq_gemm takes any K in one. */
 bsq_status bsq_gemm_linear(const bsq_tensor* A, const bsq_tensor* B, const void* bias, int32_t bias_type,
                            int32_t activation, const void* residual, int64_t ld_residual, void* y, int64_t ldy,
                            int32_t type, void* z, int64_t ldz, void* workspace, size_t workspace_bytes, void* stream);
