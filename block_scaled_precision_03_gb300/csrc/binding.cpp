@@ -552,12 +552,13 @@ int64_t integer(PyObject* o) {
     return v;
 }
 
-// A quantized tensor (QTensor): its buffers have to be there in full
+// A quantized tensor (QTensor): its buffers have to be there in full, and live as long as this, whatever made them
 struct Quantized {
+    const Ref pc, ps, pt;
     bsq_tensor c{};
     const at::Tensor* codes;
-    Quantized(PyObject* o, const char* name) {
-        const Ref fmt(o, s_fmt), rows(o, s_rows), cols(o, s_cols), pc(o, s_codes), ps(o, s_scales), pt(o, s_tensor_scale);
+    Quantized(PyObject* o, const char* name) : pc(o, s_codes), ps(o, s_scales), pt(o, s_tensor_scale) {
+        const Ref fmt(o, s_fmt), rows(o, s_rows), cols(o, s_cols);
         c.fmt = (int32_t)integer(fmt.o);
         c.rows = integer(rows.o);
         c.cols = integer(cols.o);
