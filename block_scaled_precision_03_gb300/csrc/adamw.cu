@@ -524,10 +524,11 @@ __device__ __forceinline__ void leave(const Entry& e, int64_t at, int n, bool ve
 }
 
 // A warp's part of a chunk, 256 elements, is a unit of its own.  The first loop takes those that are whole, with moments
-// on 16-byte boundaries and in the range of update(), with the next one's loads under way; what it leaves, the second loop
-// takes.  ANY: parameters, gradients or copies off those boundaries, a few elements at a time (118 M weights in BF16,
-// 8-bit moments, stochastic: 470 us, 944 in the second loop, 312 where all are on them).
-// (One loop with both ways in it held its values twice over: 92 instructions an element of 8-bit moments, not 78.)
+// on 16-byte boundaries, with the next one's loads under way, and stores what was in the range of update(); the rest the
+// second loop takes.  ANY: parameters, gradients or copies off those boundaries, a few elements at a time (118 M weights
+// in BF16, 8-bit moments, stochastic: 441 us, 944 in the second loop, 292 where all are on them).
+// (One loop with both ways in it held its values twice over: 92 instructions an element of 8-bit moments, 78 with two then;
+// 81 now, with the ranges of m.)
 constexpr int kMost = 2048;                         // chunks of a CTA
 template <int CAP, bool RANDOM, bool BITS8, bool ANY>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table<CAP> t, Options o) {

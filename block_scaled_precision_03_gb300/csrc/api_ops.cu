@@ -185,7 +185,6 @@ bool finite_and_not_negative(double x) { return x >= 0.0 && !std::isinf(x); }
 
 extern "C" {
 
-
 size_t bsq_moe_workspace_bytes(int64_t tokens, int32_t k, int32_t num_experts) {
     if (!moe_sizes_ok(tokens, k, num_experts) || !moe_sizes_supported(tokens, k, num_experts)) return 0;
     return bsq::moe_sort_workspace(tokens, k, num_experts);

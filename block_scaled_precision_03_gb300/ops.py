@@ -507,8 +507,9 @@ class AdamWList:
     """The parameters of a step, their gradients and moments: contiguous tensors
     of one GPU.  params, grads: bfloat16 or float32 each; states: 32 or 8 (bits of
     moments that start at 0), or what adamw_states returns; copies: None, or for
-    each parameter a bfloat16 tensor for its rounded copy (or None).  Built once
-    for buffers that stay; keeps them alive."""
+    each parameter a bfloat16 tensor for its rounded copy (or None).  No two of all
+    these overlap.  Built once for buffers that stay, at 3 to 5 us of host time a
+    parameter, which new gradient tensors cost at every step; keeps them alive."""
 
     def __init__(self, params, grads, states=32, copies=None):
         import torch

@@ -585,8 +585,10 @@ typedef struct {
  * Moments in 8 bits: with x a block's largest magnitude, its scale is 2^e with e =
  * floor(log2(x * 8/7)) - 8 (the product in FP32; e >= -127), which keeps |x| 2^-e at
  * 448 or below; a code is x 2^-e rounded to E4M3; a v that is not 0 keeps a code that
- * is not; a block with a NaN or an infinity gets scale 0xFF and NaN codes.  The update
- * takes the moments before that rounding.
+ * is not; a block with a NaN or an infinity gets scale 0xFF and NaN codes, and its 32
+ * parameters are NaN from the next step on: a gradient that may not be finite is to
+ * be looked at (its norm is enough) before it comes here.  The update takes the moments
+ * before that rounding.
  *
  * stochastic = 0: codes and BF16 parameters are rounded to nearest.  Else they
  * are rounded up in magnitude with the probability of what is cut off, from 16
