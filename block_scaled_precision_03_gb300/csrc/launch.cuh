@@ -12,11 +12,13 @@ namespace bsq {
 // first access to global memory; the kernel before it may let it start early
 // with pdl_launch_dependents().  Only pdl_wait() makes visible what kernels
 // before it wrote, so whoever may follow any kernel waits first, always.  A few
-// kernels behind another one of the same call (the head's dw, norm_dx_kernel,
-// moe_gather_kernel) read before it what that kernel does not write, and say so:
-// the call's first kernel is launched without this attribute, so that all the
-// stream's work before the call is done, and what the call itself wrote two
-// kernels before is read from L2 (TMA, __ldcg).
+// kernels behind another one of the same call (norm_dx_kernel, moe_place_kernel,
+// moe_gather_kernel, scale_kernel, the head's) read before it what that kernel does
+// not write, and say so: inputs, as the call's first kernel is launched without this
+// attribute, when all the stream's work before the call is done; and, in the head's
+// gradient, what a kernel wrote for which the one in between has waited, from L2
+// (TMA, __ldcg).  (Waits there cost it 1 to 8%: 2048 tokens of 16384 x 1024 171 us, 159
+// without; 8192 of 65536 x 4096 7.9 ms either way.)
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
